@@ -259,6 +259,109 @@ int pkv_append_attention_fp8(const void *k_new, const void *v_new, const int64_t
                              cudaStream_t stream);
 
 /*
+ * A step's block tables and slot map, built on the device from request
+ * lengths: new blocks are popped from a free list, so that a serving loop's
+ * next step needs no host round trip and can be captured in a CUDA graph.
+ *   prev_lens       [num_reqs] int32: tokens of request r cached before the
+ *                   step; row r of block_tables holds ceil(prev / 16) blocks
+ *   new_tokens      [num_reqs] int32: tokens it brings (0: it sits the step out)
+ *   free_list       [num_blocks] int32: the first *num_free_in entries are
+ *                   free block ids, taken from the end
+ *   block_tables    [num_reqs, max_blocks_per_req]: the entries of the new
+ *                   blocks are written, the others left as they are
+ *   seq_lens        [num_reqs] out: prev + new (prev for a refused request; 0
+ *                   for one whose numbers are invalid)
+ *   query_start_loc [num_reqs + 1] out
+ *   slot_mapping    [num_q_tokens] int64 out: block * 16 + offset of each new
+ *                   token in request order, -1 in the rows past the last
+ *   num_free_out    [1] out: free blocks left
+ *   num_refused     [1] out, or NULL: requests refused
+ * Requests are served in index order until the first whose blocks or token
+ * rows no longer fit; from there on every request that brings tokens is
+ * refused: it gets no query row and no block, and its table row and length
+ * stay as they were, so that a later step can offer it again.  An invalid
+ * request (negative numbers, prev + new > 16 * max_blocks_per_req) is refused
+ * by itself and recorded as PKV_ERR_DEVICE_BOUNDS, as is a number of free
+ * blocks outside [0, num_blocks] (taken as the nearest bound) or a block id
+ * outside the pool where a token would be stored (its slot is -1).
+ * seq_lens may be prev_lens and num_free_out may be num_free_in (in place);
+ * no other arrays may overlap.  free_list is not written.  Only
+ * dims->num_reqs, num_q_tokens, block_size, num_blocks and max_blocks_per_req
+ * are read.  The call never lets the next kernel start before it is done, so
+ * any call of this library may follow it.
+ * Source: The Serving Playbook, "CUDA graphs and the CPU you forgot about"
+ * (block tables and slot mappings among the step buffers); LLM 7 - Efficient
+ * LLM Serving, sec. 3 "Paging the Cache" (blocks allocated on demand).
+ */
+int pkv_build_step(const int32_t *prev_lens, const int32_t *new_tokens, const int32_t *free_list,
+                   const int32_t *num_free_in, int32_t *block_tables, int32_t *seq_lens,
+                   int32_t *query_start_loc, int64_t *slot_mapping, int32_t *num_free_out,
+                   int32_t *num_refused, const pkv_dims *dims, cudaStream_t stream);
+
+/*
+ * Gives blocks back: request r, seq_lens[r] tokens long, keeps its first
+ * keep_lens[r] tokens (0: it has finished), and the blocks of table columns
+ * ceil(keep / 16) .. ceil(len / 16) - 1 are appended to the free list in
+ * request, then column order, from entry *num_free_in on.  num_free_out gets
+ * the new number of free blocks (it may be num_free_in).  The tables are not
+ * written: entries past a request's blocks are never read.
+ * A request with keep < 0, keep > len or len > 16 * max_blocks_per_req gives
+ * nothing back, and block ids outside the pool are dropped; both, and more
+ * blocks than the list can hold (the rest is dropped: some block was given
+ * back twice), are recorded as PKV_ERR_DEVICE_BOUNDS.  free_list:
+ * [num_blocks].  Blocks shared by several requests are the caller's to count.
+ * Only dims->num_reqs, block_size, num_blocks and max_blocks_per_req are read.
+ * Source: LLM 7 - Efficient LLM Serving, sec. 3 "Paging the Cache" (freed
+ * blocks return to the pool); "Sharing and Preemption".
+ */
+int pkv_release_blocks(const int32_t *block_tables, const int32_t *seq_lens,
+                       const int32_t *keep_lens, int32_t *free_list, const int32_t *num_free_in,
+                       int32_t *num_free_out, const pkv_dims *dims, cudaStream_t stream);
+
+/*
+ * KV append into e4m3 pools that hold one scale per (block, KV head):
+ * k_scales / v_scales [num_blocks, num_kv_heads] fp32, the value of a code
+ * being decode(code) * scale.  The new tokens of request r are rows
+ * query_start_loc[r] .. of k_new / v_new [num_q_tokens, num_kv_heads, 128]
+ * and sit at positions L_r - q_r .. L_r - 1, found through block_tables.  For
+ * every block they touch, KV head and tensor, with A the largest finite
+ * magnitude among the block's new rows and need the smallest power of two s
+ * >= 2^-126 with A / s <= 448: the scale becomes need where the block holds no
+ * earlier token of the request (whatever the scale was: blocks need no
+ * initialisation), else max(scale, need); new rows are stored as the codes
+ * nearest to x / scale (ties to even, magnitudes beyond 448 -- infinities --
+ * saturated, NaN kept); and where a scale grew, the earlier rows' codes are
+ * rewritten for it (exact but for codes that fall below the normal range).
+ * Rows past L_r and other blocks are untouched.  A block written by two
+ * requests of one call is a caller's error.  Padded steps as in
+ * pkv_attention.  dims->num_q_heads is not read.
+ * Source: The Serving Playbook, "Quantized serving" (an fp8 KV cache halves
+ * the bytes decode reads); LLM 7 - Efficient LLM Serving, sec. 3 "What the
+ * Cache Stores".
+ */
+int pkv_append_fp8_block(const void *k_new, const void *v_new, const int32_t *block_tables,
+                         const int32_t *seq_lens, const int32_t *query_start_loc, void *k_pool,
+                         void *v_pool, float *k_scales, float *v_scales, const pkv_dims *dims,
+                         cudaStream_t stream);
+
+/*
+ * pkv_attention over such pools: the key of position j, KV head kh, in block b
+ * is decode(code) * k_scales[b, kh], the value decode(code) * v_scales[b, kh];
+ * scales are finite and >= 0 (any, not only powers of two).  Everything else
+ * (q, out, lengths, tables, workspace, errors, launch overlap) as in
+ * pkv_attention.  Both products take the codes themselves (e4m3 tensor-core
+ * operands); q and the probabilities enter them as pairs of e4m3 numbers with
+ * eight significant bits.  num_blocks * num_kv_heads * 16 must be below 2^31.
+ * Source: as pkv_attention_fp8kv.
+ */
+int pkv_attention_fp8_block(const void *q, const void *k_pool, const void *v_pool,
+                            const float *k_scales, const float *v_scales,
+                            const int32_t *block_tables, const int32_t *seq_lens,
+                            const int32_t *query_start_loc, float scale, void *out,
+                            const pkv_dims *dims, void *workspace, size_t workspace_bytes,
+                            cudaStream_t stream);
+
+/*
  * Bytes of workspace pkv_attention_cascade needs for these dims: the
  * pkv_attention workspace (same head, initialised the same way with
  * pkv_workspace_init), plus partial states for up to 8 chunks of each shared

@@ -31,7 +31,8 @@ EXPORTED = ("pkv_append", "pkv_attention", "pkv_attention_workspace_size",
             "pkv_attention_noalloc", "pkv_copy_blocks", "pkv_append_fp8",
             "pkv_attention_fp8kv", "pkv_cascade_workspace_size", "pkv_attention_cascade",
             "pkv_append_attention", "pkv_append_attention_fp8", "pkv_get_options",
-            "pkv_set_options")
+            "pkv_set_options", "pkv_build_step", "pkv_release_blocks", "pkv_append_fp8_block",
+            "pkv_attention_fp8_block")
 
 # Fields of pkv_options, in declaration order (int32 each).
 OPTION_FIELDS = ("pdl", "early_plan", "early_kv", "early_trigger", "plan_cache", "decode_tc",
@@ -106,6 +107,14 @@ def load_library(path: str = LIB_PATH):
         lib.pkv_append_attention_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                                  ctypes.c_float, vp, dp, vp, sz, vp]
         lib.pkv_append_attention_fp8.restype = ctypes.c_int
+        lib.pkv_build_step.argtypes = [vp] * 10 + [dp, vp]
+        lib.pkv_build_step.restype = ctypes.c_int
+        lib.pkv_release_blocks.argtypes = [vp] * 6 + [dp, vp]
+        lib.pkv_release_blocks.restype = ctypes.c_int
+        lib.pkv_append_fp8_block.argtypes = [vp] * 9 + [dp, vp]
+        lib.pkv_append_fp8_block.restype = ctypes.c_int
+        lib.pkv_attention_fp8_block.argtypes = [vp] * 8 + [ctypes.c_float, vp, dp, vp, sz, vp]
+        lib.pkv_attention_fp8_block.restype = ctypes.c_int
         lib.pkv_get_options.argtypes = [ctypes.POINTER(Options)]
         lib.pkv_get_options.restype = None
         lib.pkv_set_options.argtypes = [ctypes.POINTER(Options)]
@@ -424,6 +433,170 @@ def pkv_append_attention_fp8(k_new, v_new, slot_mapping, k_pool, v_pool, k_scale
         ctypes.c_void_p(out.data_ptr()), ctypes.byref(dims), ctypes.c_void_p(ws_ptr), ws_bytes,
         ctypes.c_void_p(_stream(stream, q.device))))
     return out
+
+
+def _need_all(*args):
+    """_need for (tensor, name, dtype, ndim) tuples that have to lie on one
+    device; returns it.  One pass with the common case first: these checks
+    are most of a small call's host time."""
+    dev = None
+    for t, name, dtype, ndim in args:
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype
+                and t.dim() == ndim and t.is_contiguous()):
+            _need(t, name, dtype, ndim)
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, {args[0][1]} on {dev}")
+    return dev
+
+
+@contextlib.contextmanager
+def _other_device(dev):
+    with torch.cuda.device(dev):
+        yield
+
+
+def _on(dev):
+    """A context in which ``dev`` is current (the library launches on the
+    current device)."""
+    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() \
+        else _other_device(dev)
+
+
+def _block_pool_checks(k_pool, v_pool, k_scales, v_scales):
+    nb, Hkv = k_pool.shape[:2]
+    if v_pool.shape != k_pool.shape:
+        raise ValueError("v_pool must have k_pool's shape")
+    if tuple(k_scales.shape) != (nb, Hkv) or tuple(v_scales.shape) != (nb, Hkv):
+        raise ValueError(f"k_scales and v_scales must be [num_blocks, num_kv_heads] = {(nb, Hkv)}")
+
+
+def pkv_append_fp8_block(k_new, v_new, block_tables, seq_lens, query_start_loc, k_pool, v_pool,
+                         k_scales, v_scales, stream=None):
+    """Quantise this step's k_new/v_new [Tq, Hkv, D] bf16 into e4m3 pools
+    (uint8 [blocks, Hkv, 16, D]) with a scale per (block, KV head)
+    (k_scales / v_scales [blocks, Hkv] fp32, updated); token i of request r
+    goes to position seq_lens[r] - q_r + i through block_tables."""
+    bf, i32, u8, f32 = torch.bfloat16, torch.int32, torch.uint8, torch.float32
+    dev = _need_all((k_new, "k_new", bf, 3), (v_new, "v_new", bf, 3),
+                    (block_tables, "block_tables", i32, 2), (seq_lens, "seq_lens", i32, 1),
+                    (query_start_loc, "query_start_loc", i32, 1), (k_pool, "k_pool", u8, 4),
+                    (v_pool, "v_pool", u8, 4), (k_scales, "k_scales", f32, 2),
+                    (v_scales, "v_scales", f32, 2))
+    T, Hkv, D = k_new.shape
+    R = seq_lens.shape[0]
+    nb, hkv, bs, d = k_pool.shape
+    if v_new.shape != k_new.shape:
+        raise ValueError("v_new must have k_new's shape")
+    if query_start_loc.shape[0] != R + 1 or block_tables.shape[0] != R:
+        raise ValueError("seq_lens, query_start_loc and block_tables disagree on num_reqs")
+    if hkv != Hkv or d != D:
+        raise ValueError("pool shape does not match the new rows")
+    _block_pool_checks(k_pool, v_pool, k_scales, v_scales)
+    dims = Dims(R, T, Hkv, Hkv, D, bs, nb, block_tables.shape[1])
+    with _on(dev):
+        _check(load_library().pkv_append_fp8_block(
+            k_new.data_ptr(), v_new.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+            query_start_loc.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+            k_scales.data_ptr(), v_scales.data_ptr(), ctypes.byref(dims), _stream(stream, dev)))
+
+
+def pkv_attention_fp8_block(q, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens,
+                            query_start_loc, scale, out=None,
+                            workspace: Workspace | None = None, stream=None):
+    """pkv_attention over e4m3 pools (uint8) with a scale per (block, KV head)
+    (k_scales / v_scales [blocks, Hkv] fp32); returns out [Tq, Hq, D] bf16."""
+    bf, i32, u8, f32 = torch.bfloat16, torch.int32, torch.uint8, torch.float32
+    if out is None:
+        out = torch.empty_like(q)
+    dev = _need_all((q, "q", bf, 3), (k_pool, "k_pool", u8, 4), (v_pool, "v_pool", u8, 4),
+                    (k_scales, "k_scales", f32, 2), (v_scales, "v_scales", f32, 2),
+                    (block_tables, "block_tables", i32, 2), (seq_lens, "seq_lens", i32, 1),
+                    (query_start_loc, "query_start_loc", i32, 1), (out, "out", bf, 3))
+    R = check_attention_shapes(q, k_pool, v_pool, block_tables, seq_lens, query_start_loc, out)
+    _block_pool_checks(k_pool, v_pool, k_scales, v_scales)
+    dims = make_dims(q.shape, k_pool.shape, R, block_tables.shape[1])
+    with _on(dev):
+        ws_ptr, ws_bytes = None, 0
+        if workspace is not None:
+            if workspace.buf.device != dev:
+                raise ValueError(f"workspace is on {workspace.buf.device}, q on {dev}")
+            if workspace.counter_dims != (dims.num_q_tokens, dims.num_kv_heads):
+                pkv_workspace_init(workspace, dims, stream)
+            ws_ptr, ws_bytes = workspace.ptr, workspace.nbytes
+        _check(load_library().pkv_attention_fp8_block(
+            q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), k_scales.data_ptr(),
+            v_scales.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+            query_start_loc.data_ptr(), scale, out.data_ptr(), ctypes.byref(dims), ws_ptr,
+            ws_bytes, _stream(stream, dev)))
+    return out
+
+
+def pkv_build_step(prev_lens, new_tokens, free_list, num_free, block_tables, seq_lens,
+                   query_start_loc, slot_mapping, num_free_out=None, num_refused=None,
+                   stream=None):
+    """Build a step's buffers on the GPU: request r, prev_lens[r] tokens long,
+    brings new_tokens[r]; the blocks it needs beyond ceil(prev / 16) are taken
+    from the end of free_list[:num_free] and entered in block_tables, and
+    seq_lens, query_start_loc and slot_mapping (one row per token, -1 past the
+    last) are written.  num_free_out defaults to num_free (in place); seq_lens
+    may be prev_lens.  Requests from the first that does not fit on are
+    refused (counted in num_refused, if given).  All int32 but slot_mapping
+    (int64); num_free, num_free_out and num_refused hold one element."""
+    i32 = torch.int32
+    if num_free_out is None:
+        num_free_out = num_free
+    args = [(prev_lens, "prev_lens", i32, 1), (new_tokens, "new_tokens", i32, 1),
+            (free_list, "free_list", i32, 1), (num_free, "num_free", i32, 1),
+            (block_tables, "block_tables", i32, 2), (seq_lens, "seq_lens", i32, 1),
+            (query_start_loc, "query_start_loc", i32, 1),
+            (slot_mapping, "slot_mapping", torch.int64, 1),
+            (num_free_out, "num_free_out", i32, 1)]
+    if num_refused is not None:
+        args.append((num_refused, "num_refused", i32, 1))
+    dev = _need_all(*args)
+    R = prev_lens.shape[0]
+    if new_tokens.shape[0] != R or seq_lens.shape[0] != R or block_tables.shape[0] != R \
+            or query_start_loc.shape[0] != R + 1:
+        raise ValueError("prev_lens, new_tokens, seq_lens, query_start_loc and block_tables "
+                         "disagree on num_reqs")
+    if num_free.shape[0] != 1 or num_free_out.shape[0] != 1 or \
+            (num_refused is not None and num_refused.shape[0] != 1):
+        raise ValueError("num_free, num_free_out and num_refused hold one element each")
+    dims = Dims(R, slot_mapping.shape[0], 1, 1, 128, 16, free_list.shape[0], block_tables.shape[1])
+    with _on(dev):
+        _check(load_library().pkv_build_step(
+            prev_lens.data_ptr(), new_tokens.data_ptr(), free_list.data_ptr(),
+            num_free.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+            query_start_loc.data_ptr(), slot_mapping.data_ptr(), num_free_out.data_ptr(),
+            None if num_refused is None else num_refused.data_ptr(), ctypes.byref(dims),
+            _stream(stream, dev)))
+
+
+def pkv_release_blocks(block_tables, seq_lens, keep_lens, free_list, num_free,
+                       num_free_out=None, stream=None):
+    """Give back the blocks that request r, seq_lens[r] tokens long, no longer
+    needs once it keeps keep_lens[r] tokens (0: finished): they are appended to
+    free_list[:num_free] in request, then column order.  num_free_out defaults
+    to num_free (in place).  All int32."""
+    i32 = torch.int32
+    if num_free_out is None:
+        num_free_out = num_free
+    dev = _need_all((block_tables, "block_tables", i32, 2), (seq_lens, "seq_lens", i32, 1),
+                    (keep_lens, "keep_lens", i32, 1), (free_list, "free_list", i32, 1),
+                    (num_free, "num_free", i32, 1), (num_free_out, "num_free_out", i32, 1))
+    R = seq_lens.shape[0]
+    if keep_lens.shape[0] != R or block_tables.shape[0] != R:
+        raise ValueError("seq_lens, keep_lens and block_tables disagree on num_reqs")
+    if num_free.shape[0] != 1 or num_free_out.shape[0] != 1:
+        raise ValueError("num_free and num_free_out hold one element each")
+    dims = Dims(R, 0, 1, 1, 128, 16, free_list.shape[0], block_tables.shape[1])
+    with _on(dev):
+        _check(load_library().pkv_release_blocks(
+            block_tables.data_ptr(), seq_lens.data_ptr(), keep_lens.data_ptr(),
+            free_list.data_ptr(), num_free.data_ptr(), num_free_out.data_ptr(),
+            ctypes.byref(dims), _stream(stream, dev)))
 
 
 class CascadeWorkspace(Workspace):

@@ -108,6 +108,21 @@ int check_dims(const pkv_dims* d, bool for_attention) {
   return PKV_OK;
 }
 
+// The sizes that a step's tables and lengths are read with (the calls that
+// take them without a group size).
+int check_step_dims(const pkv_dims* d) {
+  if (d == nullptr) return fail(PKV_ERR_INVALID, "dims is NULL");
+  if (d->block_size != pkv::kBlockSize)
+    return fail(PKV_ERR_UNSUPPORTED, "block_size %d unsupported (only 16)", d->block_size);
+  if (d->num_reqs < 0 || d->num_q_tokens < 0 || d->num_blocks < 0 || d->max_blocks_per_req < 0)
+    return fail(PKV_ERR_INVALID, "negative dims");
+  if (d->num_reqs > pkv::kMaxReqs)
+    return fail(PKV_ERR_UNSUPPORTED, "num_reqs %d beyond %d", d->num_reqs, pkv::kMaxReqs);
+  if ((long long)d->max_blocks_per_req * pkv::kBlockSize > (1ll << 30))
+    return fail(PKV_ERR_UNSUPPORTED, "max_blocks_per_req too large");
+  return PKV_OK;
+}
+
 pkv::WorkspaceLayout layout_for(const pkv_dims* d, int sm_count) {
   return pkv::decode_workspace_layout(d->num_q_tokens, d->num_kv_heads,
                                       d->num_q_heads / d->num_kv_heads, sm_count);
@@ -420,14 +435,15 @@ CascadeLayout cascade_layout(const pkv::WorkspaceLayout& w, const pkv_dims* d) {
   return c;
 }
 
-// The attention entry points: bf16 pools (k_scale == nullptr) or e4m3 pools,
+// The attention entry points: bf16 pools (k_scale == nullptr) or e4m3 pools
+// (scales per KV head, or with block_scales per block and KV head),
 // optionally with shared-prefix groups.
 int attention_impl(const void* q, const void* k_pool, const void* v_pool, const float* k_scale,
                    const float* v_scale, const int32_t* block_tables, const int32_t* seq_lens,
                    const int32_t* query_start_loc, float scale, void* out, const pkv_dims* dims,
                    void* workspace, size_t workspace_bytes, cudaStream_t stream,
                    const CascadeArgs* cas = nullptr, bool after_append = false,
-                   bool append_triggered_early = false) {
+                   bool append_triggered_early = false, bool block_scales = false) {
   g_last_error[0] = '\0';
   const bool fp8 = k_scale != nullptr;
   int rc = check_dims(dims, true);
@@ -600,7 +616,29 @@ int attention_impl(const void* q, const void* k_pool, const void* v_pool, const 
   p.early_kv = after_append && !cascade && p.pdl;
   p.early_q = !append_triggered_early;
   const bool do_prefill = run_prefill && !cascade;
-  if (use_tc) {
+  // Long steps run two decode CTAs per SM; steps with at most 8 tiles (64
+  // blocks) per SM run on one, so that the next launch's CTAs can prepare
+  // beside them.  When the dims alone bound the work that low (every decode
+  // row reads at most max_blocks_per_req blocks per KV head) the grid is one
+  // CTA per SM; otherwise the plan makes the choice on the device from the
+  // lengths.
+  constexpr long long kHalfGridBlocks = 64;
+  const long long bound = (long long)dims->num_q_tokens * dims->max_blocks_per_req * dims->num_kv_heads;
+  const bool small = bound <= kHalfGridBlocks * st->sm_count;
+  const int tc_grid = small ? st->sm_count : 2 * st->sm_count;
+  // tuning override, bounded by the workspace's slots
+  const bool grid_forced = opt.decode_grid > 0 && 2 * opt.decode_grid <= w.num_slots;
+  const int half_grid_blocks = small || grid_forced ? 0 : (int)kHalfGridBlocks;
+  if (block_scales) {
+    pkv::DecodeBlockLaunch B{};
+    rc = encode_pool_map_e4m3(&B.kmap, k_pool, dims);
+    if (rc == PKV_OK) rc = encode_pool_map_e4m3(&B.vmap, v_pool, dims);
+    if (rc != PKV_OK) return rc;
+    B.p = p;
+    B.grid = grid_forced ? opt.decode_grid : tc_grid;
+    B.p.half_grid_blocks = half_grid_blocks;
+    e = pkv::launch_decode_block(B, group, stream);
+  } else if (use_tc) {
     pkv::DecodeTcLaunch T{};
     rc = encode_q_map(&T.qmap, q, dims, group, 1);
     if (rc == PKV_OK) rc = fp8 ? encode_pool_map_e4m3(&T.kmap, k_pool, dims)
@@ -609,21 +647,8 @@ int attention_impl(const void* q, const void* k_pool, const void* v_pool, const 
                                : encode_pool_map(&T.vmap, v_pool, dims);
     if (rc != PKV_OK) return rc;
     T.p = p;
-    // Two CTAs per SM; steps with at most 8 tiles (64 blocks) per SM run on
-    // one CTA per SM, so that the next launch's CTAs can prepare beside them.
-    // When the dims alone bound the work that low (every decode row reads at
-    // most max_blocks_per_req blocks per KV head) the grid is one CTA per SM;
-    // otherwise the plan makes the choice on the device from the lengths.
-    constexpr long long kHalfGridBlocks = 64;
-    const long long bound = (long long)dims->num_q_tokens * dims->max_blocks_per_req * dims->num_kv_heads;
-    const bool small = bound <= kHalfGridBlocks * st->sm_count;
-    T.grid = small ? st->sm_count : 2 * st->sm_count;
-    T.p.half_grid_blocks = small ? 0 : (int)kHalfGridBlocks;
-    // tuning override, bounded by the workspace's slots
-    if (opt.decode_grid > 0 && 2 * opt.decode_grid <= w.num_slots) {
-      T.grid = opt.decode_grid;
-      T.p.half_grid_blocks = 0;
-    }
+    T.grid = grid_forced ? opt.decode_grid : tc_grid;
+    T.p.half_grid_blocks = half_grid_blocks;
     e = pkv::launch_decode_tc(T, group, stream);
   } else {
     e = pkv::launch_decode(p, group, grid, stream);
@@ -749,6 +774,127 @@ int pkv_attention_fp8kv(const void* q, const void* k_pool, const void* v_pool,
   }
   return attention_impl(q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens,
                         query_start_loc, scale, out, dims, workspace, workspace_bytes, stream);
+}
+
+int pkv_append_fp8_block(const void* k_new, const void* v_new, const int32_t* block_tables,
+                         const int32_t* seq_lens, const int32_t* query_start_loc, void* k_pool,
+                         void* v_pool, float* k_scales, float* v_scales, const pkv_dims* dims,
+                         cudaStream_t stream) {
+  g_last_error[0] = '\0';
+  int rc = check_dims(dims, false);
+  if (rc == PKV_OK) rc = check_step_dims(dims);
+  if (rc != PKV_OK) return rc;
+  if (dims->num_reqs == 0 || dims->num_q_tokens == 0) return PKV_OK;
+  if (!k_new || !v_new || !block_tables || !seq_lens || !query_start_loc || !k_pool || !v_pool ||
+      !k_scales || !v_scales)
+    return fail(PKV_ERR_INVALID, "NULL pointer argument");
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pool) || !aligned16(v_pool))
+    return fail(PKV_ERR_INVALID, "k/v buffers and pools must be 16-byte aligned");
+  DeviceState* st = device_state();
+  if (!st) return PKV_ERR_CUDA;
+  pkv::AppendBlockParams p{};
+  p.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  p.v_new = static_cast<const __nv_bfloat16*>(v_new);
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.query_start_loc = query_start_loc;
+  p.k_pool = static_cast<uint8_t*>(k_pool);
+  p.v_pool = static_cast<uint8_t*>(v_pool);
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.err = st->err;
+  p.num_reqs = dims->num_reqs;
+  p.num_tokens = dims->num_q_tokens;
+  p.num_kv_heads = dims->num_kv_heads;
+  p.num_blocks = dims->num_blocks;
+  p.max_blocks = dims->max_blocks_per_req;
+  p.pdl = current_options().pdl != 0;
+  const cudaError_t e = pkv::launch_append_fp8_block(p, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "append_fp8_block launch");
+  return PKV_OK;
+}
+
+int pkv_attention_fp8_block(const void* q, const void* k_pool, const void* v_pool,
+                            const float* k_scales, const float* v_scales,
+                            const int32_t* block_tables, const int32_t* seq_lens,
+                            const int32_t* query_start_loc, float scale, void* out,
+                            const pkv_dims* dims, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream) {
+  g_last_error[0] = '\0';
+  if (!k_scales || !v_scales) return fail(PKV_ERR_INVALID, "k_scales / v_scales is NULL");
+  const int rc = check_dims(dims, true);
+  if (rc != PKV_OK) return rc;
+  // (tensor-map rows are addressed with 32-bit coordinates)
+  if ((long long)dims->num_blocks * dims->num_kv_heads * pkv::kBlockSize > 0x7fffffffll)
+    return fail(PKV_ERR_UNSUPPORTED, "pool beyond 2^31 - 1 rows");
+  return attention_impl(q, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens,
+                        query_start_loc, scale, out, dims, workspace, workspace_bytes, stream,
+                        nullptr, false, false, true);
+}
+
+int pkv_build_step(const int32_t* prev_lens, const int32_t* new_tokens, const int32_t* free_list,
+                   const int32_t* num_free_in, int32_t* block_tables, int32_t* seq_lens,
+                   int32_t* query_start_loc, int64_t* slot_mapping, int32_t* num_free_out,
+                   int32_t* num_refused, const pkv_dims* dims, cudaStream_t stream) {
+  g_last_error[0] = '\0';
+  const int rc = check_step_dims(dims);
+  if (rc != PKV_OK) return rc;
+  // (arrays without an element may be NULL)
+  if (!num_free_in || !query_start_loc || !num_free_out ||
+      (!slot_mapping && dims->num_q_tokens > 0) || (!free_list && dims->num_blocks > 0) ||
+      (dims->num_reqs > 0 && (!prev_lens || !new_tokens || !seq_lens)) ||
+      (dims->num_reqs > 0 && dims->max_blocks_per_req > 0 && !block_tables))
+    return fail(PKV_ERR_INVALID, "NULL pointer argument");
+  DeviceState* st = device_state();
+  if (!st) return PKV_ERR_CUDA;
+  pkv::StepParams p{};
+  p.prev_lens = prev_lens;
+  p.new_tokens = new_tokens;
+  p.free_list = free_list;
+  p.num_free_in = num_free_in;
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.query_start_loc = query_start_loc;
+  p.slot_mapping = slot_mapping;
+  p.num_free_out = num_free_out;
+  p.num_refused = num_refused;
+  p.err = st->err;
+  p.num_reqs = dims->num_reqs;
+  p.num_q_tokens = dims->num_q_tokens;
+  p.num_blocks = dims->num_blocks;
+  p.max_blocks = dims->max_blocks_per_req;
+  const cudaError_t e = pkv::launch_build_step(p, current_options().pdl != 0, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "build_step launch");
+  return PKV_OK;
+}
+
+int pkv_release_blocks(const int32_t* block_tables, const int32_t* seq_lens,
+                       const int32_t* keep_lens, int32_t* free_list, const int32_t* num_free_in,
+                       int32_t* num_free_out, const pkv_dims* dims, cudaStream_t stream) {
+  g_last_error[0] = '\0';
+  const int rc = check_step_dims(dims);
+  if (rc != PKV_OK) return rc;
+  // (arrays without an element may be NULL)
+  if (!num_free_in || !num_free_out || (!free_list && dims->num_blocks > 0) ||
+      (dims->num_reqs > 0 && (!seq_lens || !keep_lens)) ||
+      (dims->num_reqs > 0 && dims->max_blocks_per_req > 0 && !block_tables))
+    return fail(PKV_ERR_INVALID, "NULL pointer argument");
+  DeviceState* st = device_state();
+  if (!st) return PKV_ERR_CUDA;
+  pkv::ReleaseParams p{};
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.keep_lens = keep_lens;
+  p.free_list = free_list;
+  p.num_free_in = num_free_in;
+  p.num_free_out = num_free_out;
+  p.err = st->err;
+  p.num_reqs = dims->num_reqs;
+  p.num_blocks = dims->num_blocks;
+  p.max_blocks = dims->max_blocks_per_req;
+  const cudaError_t e = pkv::launch_release_blocks(p, current_options().pdl != 0, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "release_blocks launch");
+  return PKV_OK;
 }
 
 void pkv_get_options(pkv_options* opts) {

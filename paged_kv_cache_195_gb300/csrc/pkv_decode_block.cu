@@ -1,0 +1,706 @@
+// pkv_decode_block.cu -- paged decode attention over e4m3 pools with a scale
+// per (16-token block, KV head), the codes fed to the tensor core as they lie
+// in the pool.
+//
+// For a query row and KV head, with ks, vs the scales of key j's block:
+//     s_j = scale * <q, decode(K_j)> * ks,   p_j = exp(s_j - max s),
+//     out = sum_j p_j * vs * decode(V_j) / sum_j p_j.
+//
+// No widening.  Both products run as e4m3 x e4m3 (tcgen05 kind::f8f6f4) on
+// the pool's own bytes; what is split instead is the small operand.  A head's
+// q is scaled by a power of two so that its largest element lies in
+// [224, 448) and written as two e4m3 rows, q = hi + lo / 16 with lo =
+// e4m3(16 (q - hi)): e4m3 keeps four significant bits, so hi leaves at most
+// 2^-4 of an element and the pair at most 2^-9 -- half a bf16 step; for q,
+// which is bf16, the pair is exact except below 2^-19 of the row's largest
+// element.  The probabilities are split the same way.  The eight (at most)
+// heads' hi rows and lo rows are the sixteen columns the smallest N of an
+// M = 128 MMA has anyway:
+//     S^T[128 keys x (8 hi | 8 lo)] = K[128 x 128 d] . Qhl^T         (A, B K-major)
+//     O^T[128 d x (8 hi | 8 lo)]   += V^T[128 d x 128 keys] . Phl^T  (A MN-major)
+// so the split costs no tensor time.  A kernel that widens the codes to 16
+// bits in shared memory or TMEM first is bound by that widening's latency.
+//
+// Scales.  ks multiplies the scores after the MMA (a tile's 128 keys are 8
+// blocks; TMEM lane = key).  vs joins the probabilities before they are
+// rounded: with vs = r 2^lv, r in [1, 2), the value fed to the MMA is
+//     P = exp2(s + lv - mo) * r * 2^4,
+// where mo is a running maximum of s + lv, next to the running maximum m of s
+// that the normaliser uses.  A second maximum because a block that holds most
+// of the probability may have a V scale far below its neighbours': P is then
+// still of order one where it matters.  The two are raised, and O^T rescaled,
+// when a value exceeds its maximum by more than 2^3 (a CTA-wide vote), so P
+// stays below 2^8 and an error of half of lo's last subnormal step is 2^-18
+// of the largest probability.
+//
+// Plan, pieces, workspace and the log-sum-exp merge are those of the other
+// decode kernels (pkv_plan.cuh); rows of every request the caller leaves to
+// this kernel, any group size 1..8.
+//
+// Roles (224 threads, two CTAs per SM): warps 0-3 softmax and epilogue, one
+// key (TMEM lane) per thread; warp 4 plans and issues the copies -- K and V
+// tiles by TMA into a ring of six 16 KiB slots, the sixteen scales of a tile
+// by 4-byte asynchronous copies -- warp 5 issues the MMAs, warp 6 converts
+// each piece's q, a piece ahead.
+#include <climits>
+
+#include "pkv_internal.h"
+#include "pkv_plan.cuh"
+#include "pkv_tc.cuh"
+
+namespace pkv {
+namespace {
+
+using plan::Piece;
+using plan::kEndRow;
+
+constexpr int kWarpProd = 4, kWarpMma = 5, kWarpQ = 6;
+constexpr int kThreads = 32 * 7;
+constexpr int kTile = 128;                   // keys per tile
+constexpr int kBlkPerTile = kTile / kBlockSize;
+constexpr int kTileCodes = kTile * kHeadDim; // one K or V tile, bytes
+constexpr int kSlots = 6;                    // ring: K of tile t, V of tile t, K of t + 1, ...
+constexpr int kScales = 4;                   // tiles whose scales are held (see the producer)
+constexpr int kN = 16;                       // MMA N: 8 hi columns, 8 lo columns
+constexpr int kAtom = 8 * 128;               // 8 operand rows of 128 bytes
+constexpr uint32_t kTmemCols = 64;           // S0 0..15, S1 16..31, O0 32..47, O1 48..63
+constexpr uint32_t kColO = 32;
+constexpr float kNegBig = -1.0e30f;
+constexpr float kMargin = 3.f;               // log2 of the largest exp2(s - m) allowed
+constexpr float kTop = 4.f;                  // P carries 2^kTop: P < 2^(kMargin + 1 + kTop) = 2^8
+constexpr float kLo = 16.f;                  // weight of the lo rows' reciprocal
+constexpr int kBarSoftmax = 1;
+constexpr int kSoftThreads = 128;
+constexpr int kPastPiece = INT_MIN;
+constexpr int kWindow = 32;                  // block-table entries loaded at a time (4 tiles)
+
+struct __align__(1024) BkSmem {
+  uint8_t slot[kSlots][kTileCodes];  // occupant n: K (n even) or V (n odd) of tile n / 2
+  uint8_t q[2][2][kAtom];            // [piece buffer][hi | lo][8 heads x 128 d], 128-byte swizzle
+  uint8_t pt[2][2][kAtom];           // [tile & 1][hi | lo][8 heads x 128 keys]
+  float sc[kScales][2][kBlkPerTile]; // [tile % kScales][K | V][block of the tile]
+  float qf[2][8];                    // [piece buffer]: factor of a head's raw scores (log2 units)
+  float red[2][4][8];                // per-warp partial maxima (of s, of s + lv)
+  float st_l[4][8];
+  Piece pinfo[2];
+  uint64_t pc_full[2];               // piece published by the producer
+  uint64_t q_full[2], q_empty[2];    // q converted / read by the piece's last MMA
+  uint64_t full[kSlots], empty[kSlots];
+  uint64_t sc_full[kScales];
+  uint64_t s_full[2], s_free[2];
+  uint64_t p_full[2], p_free[2];
+  uint64_t o_full[2], o_empty[2];
+  uint64_t mma_done;
+  uint32_t tmem_base;
+  WaitCtl wait;
+  int is_last;
+  int idle;
+};
+
+__device__ __forceinline__ float warp_max(float v) {
+  #pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+  #pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Two fp32 to two e4m3 codes (the first in the low byte): nearest even,
+// saturating, NaN kept.
+__device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
+  unsigned short r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// hi = e4m3(x) and lo = e4m3(16 (x - hi)) of a pair, low byte first.
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = to_e4m3x2(a, b);
+  const float2 h = e4m3x2_to_float2(hi);
+  lo = to_e4m3x2((a - h.x) * kLo, (b - h.y) * kLo);
+}
+
+// 4 bytes global -> shared, asynchronously; `bytes` 0 writes zero instead.
+__device__ __forceinline__ void copy4_async(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(bytes)
+               : "memory");
+}
+
+// Arrive on `bar` once this thread's asynchronous copies so far have landed.
+__device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+
+// Key row `row` of a staged V tile set to zero.
+static __device__ __noinline__ void zero_row(uint8_t* tile, int row) {
+  uint4* v = reinterpret_cast<uint4*>(tile + row * 128);
+  #pragma unroll
+  for (int c = 0; c < 8; ++c) v[c] = make_uint4(0, 0, 0, 0);
+}
+
+// The last piece of a split row-group to arrive merges the pieces' partial
+// states of output dim d (normalised outputs and (max, normaliser) pairs in
+// workspace slots 2 (c0 + s), + 1 for piece 0 when odd0) by log-sum-exp.
+template <int G>
+static __device__ __noinline__ void merge_row(const float* ws_ml, const float* ws_o,
+                                              __nv_bfloat16* out, int c0, int S, int odd0, int d) {
+  float M[G], num[G], den[G];
+  #pragma unroll
+  for (int h = 0; h < G; ++h) {
+    M[h] = kNegBig;
+    num[h] = den[h] = 0.f;
+  }
+  #pragma unroll 1
+  for (int s = 0; s < S; ++s) {
+    const int slot = 2 * (c0 + s) + ((s == 0 && odd0) ? 1 : 0);
+    float2 ml[G];
+    float o[G];
+    #pragma unroll
+    for (int h = 0; h < G; ++h) {
+      const long long x = (long long)slot * G + h;
+      ml[h] = __ldcg(reinterpret_cast<const float2*>(ws_ml + x * 2));
+      o[h] = __ldcg(ws_o + x * kHeadDim + d);
+    }
+    #pragma unroll
+    for (int h = 0; h < G; ++h) {
+      const float Mn = fmaxf(M[h], ml[h].x);
+      const float a = fast_exp2(M[h] - Mn), w = fast_exp2(ml[h].x - Mn) * ml[h].y;
+      num[h] = num[h] * a + w * o[h];
+      den[h] = den[h] * a + w;
+      M[h] = Mn;
+    }
+  }
+  #pragma unroll
+  for (int h = 0; h < G; ++h)
+    out[h * kHeadDim] = __float2bfloat16_rn(den[h] == 0.f ? 0.f : num[h] / den[h]);
+}
+
+template <int G>
+__global__ void __launch_bounds__(kThreads, 2)
+    decode_block_kernel(const __grid_constant__ CUtensorMap kmap,
+                        const __grid_constant__ CUtensorMap vmap, const DecodeParams p) {
+  static_assert(G >= 1 && G <= 8, "group size");
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  BkSmem& sm = *reinterpret_cast<BkSmem*>(smem_raw + (((raw + 1023u) & ~1023u) - raw));
+  WaitCtl* abort_flag = &sm.wait;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int Hkv = p.num_kv_heads;
+  plan::Range rg;
+  plan::Walker wk;
+  Piece pc, pn;
+  bool have = false, have_n = false;
+  // Block-table entries, one window of 32 blocks per load: the current
+  // piece's first two and the next piece's, loaded a piece ahead.
+  int ent_w0 = kPastPiece, ent_w1 = kPastPiece, ent_n0 = kPastPiece, ent_n1 = kPastPiece;
+  auto raw_entries = [&](const Piece& q, int x0) {
+    const int x = x0 + lane;
+    return x < q.nblk ? __ldg(p.block_tables + (long long)q.r * p.max_blocks + q.b0 + x)
+                      : kPastPiece;
+  };
+  auto advance = [&]() {
+    pc = pn;
+    have = have_n;
+    ent_w0 = ent_n0;
+    ent_w1 = ent_n1;
+    have_n = have && wk.next(p, pn);
+    ent_n0 = have_n ? raw_entries(pn, 0) : kPastPiece;
+    ent_n1 = have_n && pn.nblk > kWindow ? raw_entries(pn, kWindow) : kPastPiece;
+  };
+  if (warp == kWarpProd) {
+    if (!p.early_plan) {
+      grid_dependency_wait();
+      allow_dependent_launch();
+    }
+    plan::plan_cta(p, lane, rg, wk);
+    have_n = true;
+    #pragma unroll 1
+    for (int i = 0; i < 2; ++i) advance();
+    asm volatile("" ::"r"(ent_w0), "r"(ent_w1), "r"(ent_n0), "r"(ent_n1));
+    if (lane == 0) sm.idle = !have;
+  }
+  __syncthreads();
+  if (sm.idle) {  // no work: leave, but not before the kernel ahead
+    grid_dependency_wait();
+    allow_dependent_launch();
+    return;
+  }
+
+  if (tid == 0) {
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sm.pc_full[b], 1);
+      mbar_init(&sm.q_full[b], 1);
+      mbar_init(&sm.q_empty[b], 1);
+      mbar_init(&sm.s_full[b], 1);
+      mbar_init(&sm.s_free[b], 4);
+      mbar_init(&sm.p_full[b], 4);
+      mbar_init(&sm.p_free[b], 1);
+      mbar_init(&sm.o_full[b], 1);
+      mbar_init(&sm.o_empty[b], 4);
+    }
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int s = 0; s < kScales; ++s) mbar_init(&sm.sc_full[s], 2 * kBlkPerTile);
+    mbar_init(&sm.mma_done, 1);
+    sm.wait.abort = 0;
+    sm.wait.limit_ns = p.wait_limit_ns;
+    fence_barrier_init();
+  }
+  // Operand rows of padding heads stay zero for the whole kernel.
+  for (int i = tid; i < (int)(sizeof(sm.q) + sizeof(sm.pt)) / 16; i += kThreads)
+    reinterpret_cast<uint4*>(&sm.q[0][0][0])[i] = make_uint4(0, 0, 0, 0);
+  static_assert(offsetof(BkSmem, pt) == offsetof(BkSmem, q) + sizeof(sm.q), "q and pt are adjacent");
+  fence_proxy_async_smem();
+  if (warp == kWarpProd && lane == 0) {
+    prefetch_tensormap(&kmap);
+    prefetch_tensormap(&vmap);
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(&sm.tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  if (warp != kWarpProd || p.early_plan) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+  }
+
+  if (warp == kWarpProd) {
+    // ========================= plan + copies ===============================
+    const int oob_row = p.num_blocks * Hkv * kBlockSize;  // zero-filled by TMA
+    const uint64_t pol = l2_policy_evict_first();
+    int j = 0, t = 0, n_occ = 0;
+    bool ok = true;
+    while (ok && have && !abort_flag->abort) {
+      const int k = pc.k;
+      const int ntile = plan::cdiv(pc.nblk, kBlkPerTile);
+      int ent_cur = ent_w0, ent_nxt = ent_w1;
+      int ent_nn = ntile > 8 ? raw_entries(pc, 2 * kWindow) : kPastPiece;
+      // The piece's buffers are free once the MMAs of piece j - 2 are done.
+      const int ub = j & 1;
+      if (j >= 2 && !mbar_wait(&sm.q_empty[ub], ((j >> 1) - 1) & 1, p.err, abort_flag)) break;
+      if (lane == 0) {
+        sm.pinfo[ub] = pc;
+        mbar_arrive(&sm.pc_full[ub]);
+      }
+      __syncwarp();
+      for (int tt = 0; tt < ntile; ++tt, ++t) {
+        if (tt > 0 && (tt & 3) == 0) {
+          ent_cur = ent_nxt;
+          ent_nxt = ent_nn;
+          ent_nn = tt + 8 < ntile ? raw_entries(pc, (tt + 8) * kBlkPerTile) : kPastPiece;
+        }
+        const int phys = __shfl_sync(0xffffffffu, ent_cur, (tt & 3) * kBlkPerTile + (lane & 7));
+        const bool good = (unsigned)phys < (unsigned)p.num_blocks;
+        if (!good && phys != kPastPiece && lane < 8) record_error(p.err, kErrBounds);
+        const int row = good ? (phys * Hkv + k) * kBlockSize : oob_row;
+        #pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+          const int n = 2 * t + kv, s = n % kSlots;
+          if (n >= kSlots &&
+              !mbar_wait(&sm.empty[s], ((n / kSlots) - 1) & 1, p.err, abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&sm.full[s], (uint32_t)kTileCodes);
+          __syncwarp();
+          if (lane < 8)
+            tma_load_2d(sm.slot[s] + lane * 2048, kv ? &vmap : &kmap, 0, row, &sm.full[s], pol);
+          if (kv == 0 && lane < 2 * kBlkPerTile) {
+            // The tile's scales, K's from lanes 0-7 and V's from lanes 8-15;
+            // blocks that are not read get 0.  Their buffer last held tile t
+            // - kScales, whose PV is done (its V slot has been refilled), so
+            // the softmax has read it.
+            static_assert(2 * kScales > kSlots + 1, "scales outlive the tile's ring slots");
+            const float* src = (lane < 8 ? p.k_scale : p.v_scale) +
+                               (good ? (long long)phys * Hkv + k : 0);
+            copy4_async(&sm.sc[t % kScales][lane >> 3][lane & 7], src, good ? 4u : 0u);
+            arrive_after_copies(&sm.sc_full[t % kScales]);
+          }
+          __syncwarp();
+          n_occ = n + 1;
+        }
+        if (!ok) break;
+      }
+      if (!ok) break;
+      ++j;
+      advance();
+    }
+    if (!abort_flag->abort) {
+      const int ub = j & 1;  // end marker
+      if (j < 2 || mbar_wait(&sm.q_empty[ub], ((j >> 1) - 1) & 1, p.err, abort_flag)) {
+        if (lane == 0) {
+          sm.pinfo[ub].row = kEndRow;
+          mbar_arrive(&sm.pc_full[ub]);
+        }
+      }
+    }
+    if (abort_flag->abort) {
+      // Copies in flight land before the CTA's shared memory is released.
+      for (int m = max(0, n_occ - kSlots); m < n_occ; ++m)
+        mbar_wait_drain(&sm.full[m % kSlots], (m / kSlots) & 1, p.err, abort_flag);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == kWarpMma) {
+    // ============================ MMA issuer ==============================
+    if (lane == 0) {
+      constexpr uint32_t kIdescS = idesc_e4m3_f32(kTile, kN, 0, 0);
+      constexpr uint32_t kIdescO = idesc_e4m3_f32(kHeadDim, kN, 1, 0);
+      int t = 0;
+      bool ok = true;
+      auto pv = [&](int tt, bool first, int j) {
+        const int n = 2 * tt + 1, s = n % kSlots, ob = j & 1, b = tt & 1;
+        const uint32_t tO = tmem + kColO + ob * kN;
+        ok = ok && mbar_wait(&sm.p_full[b], (tt >> 1) & 1, p.err, abort_flag);
+        ok = ok && mbar_wait(&sm.full[s], (n / kSlots) & 1, p.err, abort_flag);
+        if (first && j >= 2)
+          ok = ok && mbar_wait(&sm.o_empty[ob], ((j >> 1) - 1) & 1, p.err, abort_flag);
+        if (!ok) return;
+        tc_fence_after();
+        #pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          // V^T is MN-major: one 128-byte atom holds all 128 dims, 8-key
+          // groups 1024 bytes apart; 32 keys per MMA.
+          const uint64_t da = smem_desc_sw128(smem_u32(sm.slot[s]) + kk * 4096, 1024, 1024);
+          const uint64_t db = smem_desc_sw128(smem_u32(sm.pt[b][0]) + kk * 32, 16, kAtom);
+          tc_mma_f8_ss(tO, da, db, kIdescO, !first || kk > 0);
+        }
+        tc_commit(&sm.empty[s]);
+        tc_commit(&sm.p_free[b]);
+      };
+      for (int j = 0; ok; ++j) {
+        const int ub = j & 1;
+        if (!mbar_wait(&sm.q_full[ub], (j >> 1) & 1, p.err, abort_flag)) break;
+        const int row = sm.pinfo[ub].row;
+        if (row == kEndRow) break;
+        const int ntile = plan::cdiv(sm.pinfo[ub].nblk, kBlkPerTile);
+        tc_fence_after();
+        for (int tt = 0; tt < ntile && ok; ++tt, ++t) {
+          const int b = t & 1, n = 2 * t, s = n % kSlots;
+          ok = ok && mbar_wait(&sm.full[s], (n / kSlots) & 1, p.err, abort_flag);
+          if (t >= 2) ok = ok && mbar_wait(&sm.s_free[b], ((t >> 1) - 1) & 1, p.err, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t tS = tmem + b * kN;
+          #pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t da = smem_desc_sw128(smem_u32(sm.slot[s]) + kk * 32, 16, 1024);
+            const uint64_t db = smem_desc_sw128(smem_u32(sm.q[ub][0]) + kk * 32, 16, kAtom);
+            tc_mma_f8_ss(tS, da, db, kIdescS, kk > 0);
+          }
+          tc_commit(&sm.empty[s]);
+          tc_commit(&sm.s_full[b]);
+          if (tt >= 1) pv(t - 1, tt == 1, j);
+        }
+        if (ok) pv(t - 1, ntile == 1, j);
+        tc_commit(&sm.o_full[ub]);
+        tc_commit(&sm.q_empty[ub]);
+      }
+      if (abort_flag->abort) {
+        // The MMAs already issued must finish before TMEM is freed.
+        tc_commit(&sm.mma_done);
+        mbar_wait_drain(&sm.mma_done, 0, p.err, abort_flag);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kWarpQ) {
+    // ============================ q, a piece ahead ========================
+    for (int j = 0;; ++j) {
+      const int ub = j & 1;
+      if (!mbar_wait(&sm.pc_full[ub], (j >> 1) & 1, p.err, abort_flag)) break;
+      const int row = sm.pinfo[ub].row, k = sm.pinfo[ub].k;
+      if (row == kEndRow) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.q_full[ub]);
+        break;
+      }
+      // Testing only: the first piece's q never comes, so the waits on it run out.
+      if (p.debug_withhold_q && j == 0) continue;
+      // Four dims of every head per lane.
+      const uint2* src = reinterpret_cast<const uint2*>(
+                             p.q + ((long long)row * p.num_q_heads + (long long)k * G) * kHeadDim) +
+                         lane;
+      uint2 x[G];
+      #pragma unroll
+      for (int h = 0; h < G; ++h) x[h] = __ldg(src + h * (kHeadDim / 4));
+      #pragma unroll
+      for (int h = 0; h < G; ++h) {
+        const uint32_t a = x[h].x & 0x7fff7fffu, c = x[h].y & 0x7fff7fffu;
+        uint32_t top = max(max(a & 0xffffu, a >> 16), max(c & 0xffffu, c >> 16));
+        top = __reduce_max_sync(0xffffffffu, top);
+        // sigma = 2^(7 - e) of the largest |q| = 1.f 2^e puts it in [128, 256);
+        // a zero or subnormal row is scaled like the smallest normal one.
+        // A row with an infinity or a NaN becomes NaN throughout (its scores
+        // are undefined).
+        const int e = max((int)(top >> 7), 1);  // biased
+        const bool finite = e < 255;
+        // 2^(134 - e biased): within fp32 for e <= 253 as 2^-119 .. 2^133, so
+        // in two factors.
+        const float s1 = finite ? __uint_as_float((uint32_t)(127 + (134 - e) / 2) << 23)
+                                : __int_as_float(0x7fc00000);
+        const float s2 = __uint_as_float((uint32_t)(127 + (134 - e) - (134 - e) / 2) << 23);
+        const float2 u = bf16x2_to_float2(x[h].x), v = bf16x2_to_float2(x[h].y);
+        uint32_t h0, l0, h1, l1;
+        split_pair(u.x * s1 * s2, u.y * s1 * s2, h0, l0);
+        split_pair(v.x * s1 * s2, v.y * s1 * s2, h1, l1);
+        const int at = h * 128 + (((lane >> 2) ^ h) * 16) + (lane & 3) * 4;
+        *reinterpret_cast<uint32_t*>(sm.q[ub][0] + at) = h0 | h1 << 16;
+        *reinterpret_cast<uint32_t*>(sm.q[ub][1] + at) = l0 | l1 << 16;
+        if (lane == 0) sm.qf[ub][h] = p.scale_log2 / s1 / s2;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.q_full[ub]);
+    }
+  } else {
+    // ================ softmax + epilogue (warps 0-3) ======================
+    const int row = tid, d = tid;  // key `row` of a tile, dim `d` of O^T
+    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    int t = 0;
+    for (int j = 0;; ++j) {
+      const int ub = j & 1;
+      const bool got = mbar_wait(&sm.q_full[ub], (j >> 1) & 1, p.err, abort_flag);
+      const Piece pc = sm.pinfo[ub];
+      // Agree before any barrier: a wait that gave up (abort) stops everyone.
+      if (barrier_or(kBarSoftmax, kSoftThreads, !got || pc.row == kEndRow)) break;
+      bool ok = true;
+      const uint32_t tO = tmem + lane_off + kColO + ub * kN;
+      const int ntile = plan::cdiv(pc.nblk, kBlkPerTile);
+      float m[G], mo[G], l[G], qf[G];
+      #pragma unroll
+      for (int h = 0; h < G; ++h) {
+        m[h] = mo[h] = kNegBig;
+        l[h] = 0.f;
+        qf[h] = sm.qf[ub][h];
+      }
+      for (int tt = 0; tt < ntile; ++tt, ++t) {
+        const int b = t & 1;
+        ok = ok && mbar_wait(&sm.sc_full[t % kScales], (t / kScales) & 1, p.err, abort_flag);
+        const float ks = sm.sc[t % kScales][0][row >> 4];
+        const float vs = sm.sc[t % kScales][1][row >> 4];
+        ok = ok && mbar_wait(&sm.s_full[b], (t >> 1) & 1, p.err, abort_flag);
+        tc_fence_after();
+        float v[16];
+        tmem_ld16(tmem + lane_off + b * kN, v);
+        tc_wait_ld();
+        const int x = tt * kBlkPerTile + (row >> 4);
+        const int pos = (pc.b0 + x) * kBlockSize + (row & 15);
+        const bool valid = ok && x < pc.nblk && pos < pc.limit;
+        // vs = r 2^lv (a scale that is not finite becomes NaN)
+        const int ve = min(max((int)((__float_as_uint(vs) >> 23) & 255u), 1), 253);
+        const float lv = (float)(ve - 127);
+        const float r = vs - vs == 0.f ? vs * __uint_as_float((uint32_t)(254 - ve) << 23)
+                                       : __int_as_float(0x7fc00000);
+        bool over = false;
+        float s[G];
+        #pragma unroll
+        for (int h = 0; h < G; ++h) {
+          s[h] = valid ? fmaf(v[8 + h], 1.f / kLo, v[h]) * (qf[h] * ks) : -INFINITY;
+          over |= s[h] > m[h] + kMargin || s[h] + lv > mo[h] + kMargin;
+        }
+        // S buffer b has been read: the MMA may overwrite it (tile t + 2).
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.s_free[b]);
+        if (barrier_or(kBarSoftmax, kSoftThreads, over)) {
+          // Raise the running maxima to this tile's; O^T and l move along.
+          #pragma unroll
+          for (int h = 0; h < G; ++h) {
+            const float a = warp_max(s[h]), c = warp_max(s[h] + lv);
+            if (lane == 0) {
+              sm.red[0][warp][h] = a;
+              sm.red[1][warp][h] = c;
+            }
+          }
+          // O^T must hold the PV of tile t - 1 before it is rescaled.
+          if (tt > 0) ok = ok && mbar_wait(&sm.p_free[(t - 1) & 1], ((t - 1) >> 1) & 1, p.err, abort_flag);
+          named_barrier(kBarSoftmax, kSoftThreads);
+          float alpha[G];
+          bool grow = false;
+          #pragma unroll
+          for (int h = 0; h < G; ++h) {
+            const float mn = fmaxf(m[h], fmaxf(fmaxf(sm.red[0][0][h], sm.red[0][1][h]),
+                                               fmaxf(sm.red[0][2][h], sm.red[0][3][h])));
+            const float mon = fmaxf(mo[h], fmaxf(fmaxf(sm.red[1][0][h], sm.red[1][1][h]),
+                                                 fmaxf(sm.red[1][2][h], sm.red[1][3][h])));
+            l[h] *= fast_exp2(m[h] - mn);
+            alpha[h] = fast_exp2(mo[h] - mon);
+            grow |= mon != mo[h];
+            m[h] = mn;
+            mo[h] = mon;
+          }
+          if (tt > 0 && grow) {
+            tc_fence_after();
+            float o[16];
+            tmem_ld16(tO, o);
+            tc_wait_ld();
+            #pragma unroll
+            for (int h = 0; h < G; ++h) {
+              o[h] *= alpha[h];
+              o[8 + h] *= alpha[h];
+            }
+            tmem_st16(tO, reinterpret_cast<const uint32_t(&)[16]>(o));
+            tc_wait_st();
+          }
+          named_barrier(kBarSoftmax, kSoftThreads);  // sm.red is free again
+        }
+        // P buffer b was last read by the PV of tile t - 2.
+        if (t >= 2) ok = ok && mbar_wait(&sm.p_free[b], ((t >> 1) - 1) & 1, p.err, abort_flag);
+        uint8_t* const hi_row = sm.pt[b][0] + (row & 15);
+        uint8_t* const lo_row = sm.pt[b][1] + (row & 15);
+        const float lt = lv + kTop;
+        #pragma unroll
+        for (int h = 0; h < G; h += 2) {
+          const bool two = h + 1 < G;
+          const float p0 = fast_exp2(s[h] + lt - mo[h]) * r;
+          const float p1 = two ? fast_exp2(s[two ? h + 1 : h] + lt - mo[two ? h + 1 : h]) * r : 0.f;
+          l[h] += fast_exp2(s[h] - m[h]);
+          if (two) l[two ? h + 1 : h] += fast_exp2(s[two ? h + 1 : h] - m[two ? h + 1 : h]);
+          uint32_t hi, lo;
+          split_pair(p0, p1, hi, lo);
+          const int at = h * 128 + (((row >> 4) ^ h) * 16);
+          hi_row[at] = (uint8_t)hi;
+          lo_row[at] = (uint8_t)lo;
+          if (two) {
+            const int at1 = (h + 1) * 128 + (((row >> 4) ^ (h + 1)) * 16);
+            hi_row[at1] = (uint8_t)(hi >> 8);
+            lo_row[at1] = (uint8_t)(lo >> 8);
+          }
+        }
+        // Keys past the request's end inside its last block may hold anything
+        // (NaN codes too): their V rows become zero, so that 0 * V stays 0.
+        if (x < pc.nblk && pos >= pc.L) {
+          const int n = 2 * t + 1, sv = n % kSlots;
+          ok = ok && mbar_wait(&sm.full[sv], (n / kSlots) & 1, p.err, abort_flag);
+          zero_row(sm.slot[sv], row);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[b]);
+      }
+      // ============ epilogue of the piece (same four warps) ================
+      #pragma unroll
+      for (int h = 0; h < G; ++h) {
+        const float sw = warp_sum(l[h]);
+        if (lane == 0) sm.st_l[warp][h] = sw;
+      }
+      named_barrier(kBarSoftmax, kSoftThreads);
+      const bool okO = ok && mbar_wait(&sm.o_full[ub], (j >> 1) & 1, p.err, abort_flag);
+      tc_fence_after();
+      float v[16];
+      tmem_ld16(tO, v);
+      tc_wait_ld();
+      float o[G], lt[G];
+      #pragma unroll
+      for (int h = 0; h < G; ++h) {
+        lt[h] = (sm.st_l[0][h] + sm.st_l[1][h]) + (sm.st_l[2][h] + sm.st_l[3][h]);
+        // O carries 2^(kTop - mo), the normaliser 2^-m
+        const float num = fmaf(v[8 + h], 1.f / kLo, v[h]) * exp2f(mo[h] - m[h] - kTop);
+        o[h] = lt[h] == 0.f ? 0.f : __fdividef(num, lt[h]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.o_empty[ub]);
+      const bool in_range = pc.row >= 0 && pc.row < p.num_q_tokens && pc.k >= 0 &&
+                            pc.k < Hkv && pc.nblk >= 1 && pc.S >= 1 && pc.c0 >= 0 &&
+                            2 * (pc.c0 + pc.S) <= p.num_slots && pc.slot >= 0 &&
+                            pc.slot < p.num_slots;
+      __nv_bfloat16* const out =
+          p.out + ((long long)pc.row * p.num_q_heads + (long long)pc.k * G) * kHeadDim + d;
+      if (in_range && pc.S == 1) {
+        if (okO) {
+          #pragma unroll
+          for (int h = 0; h < G; ++h) out[h * kHeadDim] = __float2bfloat16_rn(o[h]);
+        }
+      } else if (in_range) {
+        if (okO) {
+          #pragma unroll
+          for (int h = 0; h < G; ++h) {
+            const long long slot = (long long)pc.slot * G + h;
+            p.ws_o[slot * kHeadDim + d] = o[h];
+            if (d == 0) *reinterpret_cast<float2*>(p.ws_ml + slot * 2) = make_float2(m[h], lt[h]);
+          }
+        }
+        named_barrier(kBarSoftmax, kSoftThreads);
+        if (d == 0) {
+          int* cnt = p.ws_cnt + (long long)pc.row * Hkv + pc.k;
+          const int old = atom_add_acq_rel_gpu(cnt, 1);
+          const int last = (old == pc.S - 1);
+          if (last) *cnt = 0;
+          sm.is_last = last;
+        }
+        named_barrier(kBarSoftmax, kSoftThreads);
+        if (sm.is_last) merge_row<G>(p.ws_ml, p.ws_o, out, pc.c0, pc.S, pc.odd0, d);
+      }
+      named_barrier(kBarSoftmax, kSoftThreads);  // sm.st_l and sm.is_last are free again
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) tmem_dealloc(tmem, kTmemCols);
+}
+
+static_assert(sizeof(BkSmem) + 1024 <= (228 * 1024) / 2 - 1024, "two CTAs per SM");
+
+template <int G>
+cudaError_t launch_g(const DecodeBlockLaunch& L, cudaStream_t stream) {
+  const size_t smem = sizeof(BkSmem) + 1024;  // + alignment slack
+  static unsigned long long configured = 0;   // bit per device ordinal
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & bit)) {
+    e = cudaFuncSetAttribute(decode_block_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)smem);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(decode_block_kernel<G>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             100);
+    if (e != cudaSuccess) return e;
+    __atomic_fetch_or(&configured, bit, __ATOMIC_RELEASE);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(L.grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = L.p.pdl ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, decode_block_kernel<G>, L.kmap, L.vmap, L.p);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_decode_block(const DecodeBlockLaunch& L, int group, cudaStream_t stream) {
+  switch (group) {
+    case 1: return launch_g<1>(L, stream);
+    case 2: return launch_g<2>(L, stream);
+    case 3: return launch_g<3>(L, stream);
+    case 4: return launch_g<4>(L, stream);
+    case 5: return launch_g<5>(L, stream);
+    case 6: return launch_g<6>(L, stream);
+    case 7: return launch_g<7>(L, stream);
+    case 8: return launch_g<8>(L, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace pkv

@@ -144,6 +144,17 @@ struct DecodeTcLaunch {
 
 cudaError_t launch_decode_tc(const DecodeTcLaunch& L, int group, cudaStream_t stream);
 
+// Decode over e4m3 pools with a scale per (block, KV head); kmap / vmap view
+// the pools as [blocks*Hkv*16][128] bytes, box (128, 16), 128-byte swizzle.
+struct DecodeBlockLaunch {
+  CUtensorMap kmap;
+  CUtensorMap vmap;
+  DecodeParams p;         // k_scale / v_scale: [num_blocks, Hkv]
+  int grid;
+};
+
+cudaError_t launch_decode_block(const DecodeBlockLaunch& L, int group, cudaStream_t stream);
+
 // Quantising KV append into e4m3 pools.
 struct AppendFp8Params {
   const __nv_bfloat16* k_new;
@@ -162,6 +173,66 @@ struct AppendFp8Params {
 };
 
 cudaError_t launch_append_fp8(const AppendFp8Params& p, cudaStream_t stream);
+
+// Quantising KV append into e4m3 pools with a scale per (block, KV head).
+struct AppendBlockParams {
+  const __nv_bfloat16* k_new;
+  const __nv_bfloat16* v_new;
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* query_start_loc;
+  uint8_t* k_pool;
+  uint8_t* v_pool;
+  float* k_scales;  // [num_blocks, Hkv]
+  float* v_scales;
+  int* err;
+  int num_reqs;
+  int num_tokens;
+  int num_kv_heads;
+  int num_blocks;
+  int max_blocks;
+  int pdl;
+};
+
+cudaError_t launch_append_fp8_block(const AppendBlockParams& p, cudaStream_t stream);
+
+// A step's tables and slots from request lengths, and blocks given back.
+struct StepParams {
+  const int32_t* prev_lens;
+  const int32_t* new_tokens;
+  const int32_t* free_list;
+  const int32_t* num_free_in;
+  int32_t* block_tables;
+  int32_t* seq_lens;
+  int32_t* query_start_loc;
+  int64_t* slot_mapping;
+  int32_t* num_free_out;
+  int32_t* num_refused;  // or null
+  int* err;
+  int num_reqs;
+  int num_q_tokens;
+  int num_blocks;
+  int max_blocks;
+  int per_cta;  // requests per CTA (set by the launcher)
+};
+
+cudaError_t launch_build_step(const StepParams& p, bool pdl, cudaStream_t stream);
+
+struct ReleaseParams {
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* keep_lens;
+  int32_t* free_list;
+  const int32_t* num_free_in;
+  int32_t* num_free_out;
+  int* err;
+  int num_reqs;
+  int num_blocks;
+  int max_blocks;
+  int per_cta;
+};
+
+cudaError_t launch_release_blocks(const ReleaseParams& p, bool pdl, cudaStream_t stream);
 
 // Chunked-prefill attention on tcgen05 tensor cores (requests with
 // q_r >= prefill_min_q).

@@ -529,9 +529,9 @@ int attention_impl(const void* q, const void* k_pool, const void* v_pool, const 
   // Launch it only when the step can hold such a request next to one query
   // for every other request; otherwise the decode kernel serves every row
   // (it is correct for any q_r, the prefill kernel is only faster).
-  // e4m3 pools: every row runs in the decode kernel.
+  // e4m3 pools with scales per head: every row runs in the decode kernel.
   const bool run_prefill =
-      !fp8 && (long long)dims->num_q_tokens - dims->num_reqs + 1 >= (long long)prefill_min_q;
+      (!fp8 || block_scales) && (long long)dims->num_q_tokens - dims->num_reqs + 1 >= (long long)prefill_min_q;
   p.prefill_min_q = run_prefill ? prefill_min_q : 0x7fffffff;
   p.num_slots = w.num_slots;
   p.pdl = opt.pdl != 0;
@@ -654,7 +654,35 @@ int attention_impl(const void* q, const void* k_pool, const void* v_pool, const 
     e = pkv::launch_decode(p, group, grid, stream);
   }
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
-  if (do_prefill) {
+  if (do_prefill && block_scales) {
+    pkv::PrefillBlockLaunch L{};
+    rc = encode_pool_map_e4m3(&L.kmap, k_pool, dims);
+    if (rc == PKV_OK) rc = encode_pool_map_e4m3(&L.vmap, v_pool, dims);
+    if (rc != PKV_OK) return rc;
+    L.p.q = p.q;
+    L.p.k_scales = k_scale;
+    L.p.v_scales = v_scale;
+    pkv::PrefillParams& f = L.p.p;
+    f.block_tables = block_tables;
+    f.seq_lens = seq_lens;
+    f.qsl = query_start_loc;
+    f.out = p.out;
+    f.err = st->err;
+    f.num_reqs = dims->num_reqs;
+    f.num_q_tokens = dims->num_q_tokens;
+    f.num_q_heads = dims->num_q_heads;
+    f.num_kv_heads = dims->num_kv_heads;
+    f.num_blocks = dims->num_blocks;
+    f.max_blocks = dims->max_blocks_per_req;
+    f.scale_log2 = p.scale_log2;
+    f.prefill_min_q = prefill_min_q;
+    f.pdl = p.pdl;
+    f.sched = reinterpret_cast<unsigned long long*>(ws + w.sched_off);
+    f.wait_limit_ns = p.wait_limit_ns;
+    L.grid = st->sm_count;
+    e = pkv::launch_prefill_block(L, group, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
+  } else if (do_prefill) {
     pkv::PrefillLaunch L{};
     rc = encode_q_map(&L.qmap, q, dims, group, pkv::prefill_tokens_per_tile(group));
     if (rc == PKV_OK) rc = encode_pool_map(&L.kmap, k_pool, dims);

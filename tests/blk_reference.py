@@ -70,10 +70,11 @@ def append(k_new, v_new, table, lens, qsl, pools, scales):
     return pools, scales
 
 
-def attention(q, pools, scales, table, lens, qsl, scale):
+def attention(q, pools, scales, table, lens, qsl, scale, min_q=16):
     """q float64 [T, Hq, 128].  Returns (out, bound): the outputs and, element
     by element, how far a computation may be off that rounds what the kernels
-    round (see bound's terms below)."""
+    round (see bound's terms below).  Requests with at least min_q query rows
+    are taken by the prefill kernel, which rounds more."""
     out, bound = np.zeros(q.shape), np.zeros(q.shape)
     hq, hkv = q.shape[1], pools[0].shape[1]
     g = hq // hkv
@@ -99,16 +100,25 @@ def attention(q, pools, scales, table, lens, qsl, scale):
                 # argument of size |s| carries |s| 2^-23.
                 mag = np.where(sees, abs(scale) * (np.abs(x) @ np.abs(K).T), 0).max(1, keepdims=True)
                 ds = 2 * mag * (2.0 ** -20 + 2.0 ** -22)
-                # A weight is rounded to eight significant bits (2^-9; bf16,
-                # 2^-8, where a weight enters as one 16-bit number), or by at
-                # most 2^-18 of the largest weight times value scale.
+                # q, scaled so that its largest element lies in [128, 256), is
+                # a pair of e4m3 numbers: exact where the lowest of its eight
+                # bits is at least e4m3's smallest, 2^-9 (elements from 2^-2
+                # on, scaled), and off by at most half of that below.
+                top = np.abs(x).max(1, keepdims=True)
+                unit = 2.0 ** (np.floor(np.log2(np.where(top > 0, top, 1))) - 7)
+                small = (np.abs(x) < unit / 4) * (x != 0) * unit * 2.0 ** -10
+                ds = ds + 2 * np.where(sees, abs(scale) * (small @ np.abs(K).T), 0).max(1, keepdims=True)
+                # A weight is a pair of e4m3 numbers: rounded by at most 2^-9,
+                # or by at most 2^-18 of the largest weight times value scale.
+                # The prefill kernel rounds weight and value to bf16: 2^-8 each.
+                rounded = 2.0 ** -7 if m >= min_q else 2.0 ** -9
                 floor = 2.0 ** -18 * (w * sc[1][None]).max(1, keepdims=True) * \
                     (np.where(sees, 1.0, 0.0) @ np.abs(codes[1]))
                 mean = w @ np.abs(V)
                 out[qsl[r]:qsl[r + 1], h] = o
                 # and the output is bf16, half a step 2^-8
                 bound[qsl[r]:qsl[r + 1], h] = 2.0 ** -8 * np.abs(o) + \
-                    (2.0 ** -9 + ds + 2.0 ** -16) * (1 + 2.0 ** -8) * mean + floor + 1e-37
+                    (rounded + ds + 2.0 ** -16) * (1 + 2.0 ** -7) * mean + floor + 1e-37
     return out, bound
 
 

@@ -5,9 +5,9 @@ plain 64-bit implementation, and a run of them together.
 Append and the integer operators are compared exactly.  Attention is compared
 element by element with the bound that blk_reference.attention derives beside
 its formula (half a bf16 step of the output, 2^-9 of the probability-weighted
-mean of |V| for the rounded probabilities, the fp32 sums), and, on random
-inputs, as a whole: independent roundings of 2^-8 (output) and 2^-9 (weights)
-give at most 2^-8 + 2^-9 of the outputs' norm."""
+mean of |V| for the rounded probabilities -- 2^-7 for prefill chunks -- and the
+fp32 sums), and, on random inputs, as a whole: independent roundings of the
+output (2^-8) and of the weights give at most their sum of the outputs' norm."""
 import numpy as np
 import pytest
 import torch
@@ -299,12 +299,13 @@ def _attend(c, q, rows, scale, workspace=None, out=None, **kw):
                                        scale, workspace=workspace, out=out, **kw)
 
 
-def _check(c, q, rows, scale=0.09, norm=True, **kw):
+def _check(c, q, rows, scale=0.09, norm=True, min_q=16, **kw):
     got = _attend(c, q, rows, scale, **kw)
     torch.cuda.synchronize()
     assert pkv.pkv_get_device_error() == 0, pkv.pkv_last_error()
     T = sum(q)
-    want, bound = ref.attention(rows[:T].double().numpy(), c.pools, c.scales, c.table, c.lens, _qsl(q), scale)
+    want, bound = ref.attention(rows[:T].double().numpy(), c.pools, c.scales, c.table, c.lens, _qsl(q), scale,
+                               min_q)
     g = got[:T].double().cpu().numpy()
     assert np.isfinite(g).all()
     off = np.abs(g - want)
@@ -312,7 +313,7 @@ def _check(c, q, rows, scale=0.09, norm=True, **kw):
     assert worst <= 1, (worst, np.unravel_index((off / bound).argmax(), off.shape))
     if norm:
         rel = np.linalg.norm(g - want) / np.linalg.norm(want)
-        assert rel <= 2.0 ** -8 + 2.0 ** -9, rel
+        assert rel <= 2.0 ** -8 + (2.0 ** -7 if max(q) >= min_q else 2.0 ** -9), rel
     return got
 
 
@@ -379,6 +380,16 @@ def test_attention_weight_on_a_block_of_small_values(q):
     c.pools[0][ids[3]] = ref.encode(np.full((1, 16, 128), -440.0))
     got = _check(c, [q], rows, scale=2.0)
     assert got.abs().max() < 1
+
+
+@pytest.mark.parametrize("q", [1, 20])
+def test_attention_negative_scale_and_wide_rows(q):
+    # rows whose elements span forty binades, under scales of either sign
+    rng = np.random.default_rng(19)
+    c = Cache(rng, [200, 150], 1)
+    rows = (_rows(rng, 2 * q, 4).double() * 2.0 ** torch.tensor(rng.integers(-40, 1, (2 * q, 4, 128)))).bfloat16()
+    for scale in (0.5, -0.5):
+        _check(c, [q, q], rows, scale=scale)
 
 
 @pytest.mark.parametrize("q", [1, 20])
@@ -471,7 +482,7 @@ def test_attention_under_every_option(changes, pkv_opts):
     q = [1] * 12 + [3] * 4 + [31] * 4
     c = Cache(rng, lens, 2)
     pkv_opts(**changes)
-    _check(c, q, _rows(rng, sum(q), 8))
+    _check(c, q, _rows(rng, sum(q), 8), min_q=changes.get("prefill_min_q", 16) or 10 ** 9)
 
 
 def test_attention_withheld_q_times_out(pkv_opts):

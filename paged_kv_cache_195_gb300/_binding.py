@@ -435,41 +435,69 @@ def pkv_append_attention_fp8(k_new, v_new, slot_mapping, k_pool, v_pool, k_scale
     return out
 
 
-def _need_all(*args):
-    """_need for (tensor, name, dtype, ndim) tuples that have to lie on one
-    device; returns it.  One pass with the common case first: these checks
-    are most of a small call's host time."""
-    dev = None
-    for t, name, dtype, ndim in args:
-        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype
-                and t.dim() == ndim and t.is_contiguous()):
-            _need(t, name, dtype, ndim)
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, {args[0][1]} on {dev}")
-    return dev
+# The calls below are short on the GPU, so their host time is most of a small
+# step: the checks take the good case in a few attribute reads per tensor and
+# name what is wrong only when one of them fails.
+
+_BF16, _I32, _I64, _U8, _F32 = (torch.bfloat16, torch.int32, torch.int64, torch.uint8,
+                                torch.float32)
 
 
-@contextlib.contextmanager
-def _other_device(dev):
-    with torch.cuda.device(dev):
-        yield
+def _fast_need(args, spec) -> tuple:
+    """Checks the tensors ``args`` against ``spec``, (name, dtype, ndim) of each:
+    contiguous CUDA tensors on one device.  Returns (device index, pointers)."""
+    try:
+        dev = args[0].get_device()
+        ptrs = []
+        for t, (_, dtype, ndim) in zip(args, spec):
+            if (t.dtype is not dtype or t.get_device() != dev or t.dim() != ndim
+                    or not t.is_contiguous()):
+                break
+            ptrs.append(t.data_ptr())
+        else:
+            if dev >= 0:
+                return dev, ptrs
+    except AttributeError:
+        pass
+    for t, (name, dtype, ndim) in zip(args, spec):
+        _need(t, name, dtype, ndim)
+        if t.device != args[0].device:
+            raise ValueError(f"{name} is on {t.device}, {spec[0][0]} on {args[0].device}")
+    raise ValueError("tensors must be contiguous CUDA tensors on one device")
 
 
-def _on(dev):
-    """A context in which ``dev`` is current (the library launches on the
-    current device)."""
-    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() \
-        else _other_device(dev)
+def _raw_stream(stream, dev: int) -> int:
+    """The launch stream's handle: the current one of device ``dev`` unless given."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _block_pool_checks(k_pool, v_pool, k_scales, v_scales):
-    nb, Hkv = k_pool.shape[:2]
-    if v_pool.shape != k_pool.shape:
+def _call(fn, dev: int, *args):
+    """fn(*args) with device ``dev`` current (the library launches there)."""
+    if torch.cuda.current_device() == dev:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args)
+    if rc:
+        _check(rc)
+
+
+def _block_scales(k_pool, v_pool, k_scales, v_scales):
+    """The pools' [num_blocks, Hkv, 16, D], with scales and V pool to match."""
+    shape = k_pool.shape
+    if v_pool.shape != shape:
         raise ValueError("v_pool must have k_pool's shape")
-    if tuple(k_scales.shape) != (nb, Hkv) or tuple(v_scales.shape) != (nb, Hkv):
-        raise ValueError(f"k_scales and v_scales must be [num_blocks, num_kv_heads] = {(nb, Hkv)}")
+    if k_scales.shape != shape[:2] or v_scales.shape != shape[:2]:
+        raise ValueError("k_scales and v_scales must be [num_blocks, num_kv_heads] = "
+                         f"{tuple(shape[:2])}")
+    return shape
+
+
+_APPEND_BLOCK = (("k_new", _BF16, 3), ("v_new", _BF16, 3), ("block_tables", _I32, 2),
+                 ("seq_lens", _I32, 1), ("query_start_loc", _I32, 1), ("k_pool", _U8, 4),
+                 ("v_pool", _U8, 4), ("k_scales", _F32, 2), ("v_scales", _F32, 2))
 
 
 def pkv_append_fp8_block(k_new, v_new, block_tables, seq_lens, query_start_loc, k_pool, v_pool,
@@ -478,28 +506,25 @@ def pkv_append_fp8_block(k_new, v_new, block_tables, seq_lens, query_start_loc, 
     (uint8 [blocks, Hkv, 16, D]) with a scale per (block, KV head)
     (k_scales / v_scales [blocks, Hkv] fp32, updated); token i of request r
     goes to position seq_lens[r] - q_r + i through block_tables."""
-    bf, i32, u8, f32 = torch.bfloat16, torch.int32, torch.uint8, torch.float32
-    dev = _need_all((k_new, "k_new", bf, 3), (v_new, "v_new", bf, 3),
-                    (block_tables, "block_tables", i32, 2), (seq_lens, "seq_lens", i32, 1),
-                    (query_start_loc, "query_start_loc", i32, 1), (k_pool, "k_pool", u8, 4),
-                    (v_pool, "v_pool", u8, 4), (k_scales, "k_scales", f32, 2),
-                    (v_scales, "v_scales", f32, 2))
-    T, Hkv, D = k_new.shape
-    R = seq_lens.shape[0]
-    nb, hkv, bs, d = k_pool.shape
-    if v_new.shape != k_new.shape:
+    dev, ptrs = _fast_need((k_new, v_new, block_tables, seq_lens, query_start_loc, k_pool, v_pool,
+                            k_scales, v_scales), _APPEND_BLOCK)
+    T, Hkv, D = new = k_new.shape
+    R, cols = block_tables.shape
+    if v_new.shape != new:
         raise ValueError("v_new must have k_new's shape")
-    if query_start_loc.shape[0] != R + 1 or block_tables.shape[0] != R:
+    if seq_lens.shape[0] != R or query_start_loc.shape[0] != R + 1:
         raise ValueError("seq_lens, query_start_loc and block_tables disagree on num_reqs")
+    nb, hkv, bs, d = _block_scales(k_pool, v_pool, k_scales, v_scales)
     if hkv != Hkv or d != D:
         raise ValueError("pool shape does not match the new rows")
-    _block_pool_checks(k_pool, v_pool, k_scales, v_scales)
-    dims = Dims(R, T, Hkv, Hkv, D, bs, nb, block_tables.shape[1])
-    with _on(dev):
-        _check(load_library().pkv_append_fp8_block(
-            k_new.data_ptr(), v_new.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
-            query_start_loc.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
-            k_scales.data_ptr(), v_scales.data_ptr(), ctypes.byref(dims), _stream(stream, dev)))
+    dims = Dims(R, T, Hkv, Hkv, D, bs, nb, cols)
+    _call((_lib or load_library()).pkv_append_fp8_block, dev, *ptrs, ctypes.byref(dims),
+          _raw_stream(stream, dev))
+
+
+_ATTENTION_BLOCK = (("q", _BF16, 3), ("k_pool", _U8, 4), ("v_pool", _U8, 4),
+                    ("k_scales", _F32, 2), ("v_scales", _F32, 2), ("block_tables", _I32, 2),
+                    ("seq_lens", _I32, 1), ("query_start_loc", _I32, 1), ("out", _BF16, 3))
 
 
 def pkv_attention_fp8_block(q, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens,
@@ -507,30 +532,38 @@ def pkv_attention_fp8_block(q, k_pool, v_pool, k_scales, v_scales, block_tables,
                             workspace: Workspace | None = None, stream=None):
     """pkv_attention over e4m3 pools (uint8) with a scale per (block, KV head)
     (k_scales / v_scales [blocks, Hkv] fp32); returns out [Tq, Hq, D] bf16."""
-    bf, i32, u8, f32 = torch.bfloat16, torch.int32, torch.uint8, torch.float32
     if out is None:
         out = torch.empty_like(q)
-    dev = _need_all((q, "q", bf, 3), (k_pool, "k_pool", u8, 4), (v_pool, "v_pool", u8, 4),
-                    (k_scales, "k_scales", f32, 2), (v_scales, "v_scales", f32, 2),
-                    (block_tables, "block_tables", i32, 2), (seq_lens, "seq_lens", i32, 1),
-                    (query_start_loc, "query_start_loc", i32, 1), (out, "out", bf, 3))
-    R = check_attention_shapes(q, k_pool, v_pool, block_tables, seq_lens, query_start_loc, out)
-    _block_pool_checks(k_pool, v_pool, k_scales, v_scales)
-    dims = make_dims(q.shape, k_pool.shape, R, block_tables.shape[1])
-    with _on(dev):
-        ws_ptr, ws_bytes = None, 0
-        if workspace is not None:
-            if workspace.buf.device != dev:
-                raise ValueError(f"workspace is on {workspace.buf.device}, q on {dev}")
-            if workspace.counter_dims != (dims.num_q_tokens, dims.num_kv_heads):
-                pkv_workspace_init(workspace, dims, stream)
-            ws_ptr, ws_bytes = workspace.ptr, workspace.nbytes
-        _check(load_library().pkv_attention_fp8_block(
-            q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), k_scales.data_ptr(),
-            v_scales.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
-            query_start_loc.data_ptr(), scale, out.data_ptr(), ctypes.byref(dims), ws_ptr,
-            ws_bytes, _stream(stream, dev)))
+    dev, ptrs = _fast_need((q, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens,
+                            query_start_loc, out), _ATTENTION_BLOCK)
+    Tq, Hq, D = rows = q.shape
+    R, cols = block_tables.shape
+    if seq_lens.shape[0] != R or query_start_loc.shape[0] != R + 1:
+        raise ValueError("seq_lens, query_start_loc and block_tables disagree on num_reqs")
+    nb, Hkv, bs, d = _block_scales(k_pool, v_pool, k_scales, v_scales)
+    if d != D:
+        raise ValueError("head_dim of the pools must match q's")
+    if out.shape != rows:
+        raise ValueError("out must have q's shape")
+    dims = Dims(R, Tq, Hq, Hkv, D, bs, nb, cols)
+    handle = _raw_stream(stream, dev)
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        if workspace.buf.get_device() != dev:
+            raise ValueError(f"workspace is on {workspace.buf.device}, q on {q.device}")
+        if workspace.counter_dims != (Tq, Hkv):
+            with torch.cuda.device(dev):
+                pkv_workspace_init(workspace, dims, handle)
+        ws_ptr, ws_bytes = workspace.ptr, workspace.nbytes
+    _call((_lib or load_library()).pkv_attention_fp8_block, dev, *ptrs[:8], scale, ptrs[8],
+          ctypes.byref(dims), ws_ptr, ws_bytes, handle)
     return out
+
+
+_BUILD_STEP = (("prev_lens", _I32, 1), ("new_tokens", _I32, 1), ("free_list", _I32, 1),
+               ("num_free", _I32, 1), ("block_tables", _I32, 2), ("seq_lens", _I32, 1),
+               ("query_start_loc", _I32, 1), ("slot_mapping", _I64, 1),
+               ("num_free_out", _I32, 1), ("num_refused", _I32, 1))
 
 
 def pkv_build_step(prev_lens, new_tokens, free_list, num_free, block_tables, seq_lens,
@@ -544,34 +577,27 @@ def pkv_build_step(prev_lens, new_tokens, free_list, num_free, block_tables, seq
     may be prev_lens.  Requests from the first that does not fit on are
     refused (counted in num_refused, if given).  All int32 but slot_mapping
     (int64); num_free, num_free_out and num_refused hold one element."""
-    i32 = torch.int32
-    if num_free_out is None:
-        num_free_out = num_free
-    args = [(prev_lens, "prev_lens", i32, 1), (new_tokens, "new_tokens", i32, 1),
-            (free_list, "free_list", i32, 1), (num_free, "num_free", i32, 1),
-            (block_tables, "block_tables", i32, 2), (seq_lens, "seq_lens", i32, 1),
-            (query_start_loc, "query_start_loc", i32, 1),
-            (slot_mapping, "slot_mapping", torch.int64, 1),
-            (num_free_out, "num_free_out", i32, 1)]
+    args = [prev_lens, new_tokens, free_list, num_free, block_tables, seq_lens, query_start_loc,
+            slot_mapping, num_free if num_free_out is None else num_free_out]
     if num_refused is not None:
-        args.append((num_refused, "num_refused", i32, 1))
-    dev = _need_all(*args)
-    R = prev_lens.shape[0]
-    if new_tokens.shape[0] != R or seq_lens.shape[0] != R or block_tables.shape[0] != R \
+        args.append(num_refused)
+    dev, ptrs = _fast_need(args, _BUILD_STEP)
+    R, cols = block_tables.shape
+    if prev_lens.shape[0] != R or new_tokens.shape[0] != R or seq_lens.shape[0] != R \
             or query_start_loc.shape[0] != R + 1:
         raise ValueError("prev_lens, new_tokens, seq_lens, query_start_loc and block_tables "
                          "disagree on num_reqs")
-    if num_free.shape[0] != 1 or num_free_out.shape[0] != 1 or \
-            (num_refused is not None and num_refused.shape[0] != 1):
+    if num_free.shape[0] != 1 or any(t.shape[0] != 1 for t in args[8:]):
         raise ValueError("num_free, num_free_out and num_refused hold one element each")
-    dims = Dims(R, slot_mapping.shape[0], 1, 1, 128, 16, free_list.shape[0], block_tables.shape[1])
-    with _on(dev):
-        _check(load_library().pkv_build_step(
-            prev_lens.data_ptr(), new_tokens.data_ptr(), free_list.data_ptr(),
-            num_free.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
-            query_start_loc.data_ptr(), slot_mapping.data_ptr(), num_free_out.data_ptr(),
-            None if num_refused is None else num_refused.data_ptr(), ctypes.byref(dims),
-            _stream(stream, dev)))
+    if num_refused is None:
+        ptrs.append(None)
+    dims = Dims(R, slot_mapping.shape[0], 1, 1, 128, 16, free_list.shape[0], cols)
+    _call((_lib or load_library()).pkv_build_step, dev, *ptrs, ctypes.byref(dims),
+          _raw_stream(stream, dev))
+
+
+_RELEASE = (("block_tables", _I32, 2), ("seq_lens", _I32, 1), ("keep_lens", _I32, 1),
+            ("free_list", _I32, 1), ("num_free", _I32, 1), ("num_free_out", _I32, 1))
 
 
 def pkv_release_blocks(block_tables, seq_lens, keep_lens, free_list, num_free,
@@ -580,23 +606,18 @@ def pkv_release_blocks(block_tables, seq_lens, keep_lens, free_list, num_free,
     needs once it keeps keep_lens[r] tokens (0: finished): they are appended to
     free_list[:num_free] in request, then column order.  num_free_out defaults
     to num_free (in place).  All int32."""
-    i32 = torch.int32
     if num_free_out is None:
         num_free_out = num_free
-    dev = _need_all((block_tables, "block_tables", i32, 2), (seq_lens, "seq_lens", i32, 1),
-                    (keep_lens, "keep_lens", i32, 1), (free_list, "free_list", i32, 1),
-                    (num_free, "num_free", i32, 1), (num_free_out, "num_free_out", i32, 1))
-    R = seq_lens.shape[0]
-    if keep_lens.shape[0] != R or block_tables.shape[0] != R:
+    dev, ptrs = _fast_need((block_tables, seq_lens, keep_lens, free_list, num_free, num_free_out),
+                           _RELEASE)
+    R, cols = block_tables.shape
+    if seq_lens.shape[0] != R or keep_lens.shape[0] != R:
         raise ValueError("seq_lens, keep_lens and block_tables disagree on num_reqs")
     if num_free.shape[0] != 1 or num_free_out.shape[0] != 1:
         raise ValueError("num_free and num_free_out hold one element each")
-    dims = Dims(R, 0, 1, 1, 128, 16, free_list.shape[0], block_tables.shape[1])
-    with _on(dev):
-        _check(load_library().pkv_release_blocks(
-            block_tables.data_ptr(), seq_lens.data_ptr(), keep_lens.data_ptr(),
-            free_list.data_ptr(), num_free.data_ptr(), num_free_out.data_ptr(),
-            ctypes.byref(dims), _stream(stream, dev)))
+    dims = Dims(R, 0, 1, 1, 128, 16, free_list.shape[0], cols)
+    _call((_lib or load_library()).pkv_release_blocks, dev, *ptrs, ctypes.byref(dims),
+          _raw_stream(stream, dev))
 
 
 class CascadeWorkspace(Workspace):

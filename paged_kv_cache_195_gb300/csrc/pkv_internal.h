@@ -213,7 +213,6 @@ struct StepParams {
   int num_q_tokens;
   int num_blocks;
   int max_blocks;
-  int per_cta;  // requests per CTA (set by the launcher)
 };
 
 cudaError_t launch_build_step(const StepParams& p, bool pdl, cudaStream_t stream);
@@ -229,7 +228,6 @@ struct ReleaseParams {
   int num_reqs;
   int num_blocks;
   int max_blocks;
-  int per_cta;
 };
 
 cudaError_t launch_release_blocks(const ReleaseParams& p, bool pdl, cudaStream_t stream);

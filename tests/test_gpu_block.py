@@ -77,7 +77,7 @@ def _step(rng, R, cols, most, blocks=None):
 
 
 @pytest.mark.parametrize("R,cols,most", [(1, 4, 60), (2, 3, 17), (33, 9, 40), (64, 130, 3), (257, 12, 90),
-                                         (1024, 8, 2), (1025, 8, 50), (4096, 6, 30), (9001, 5, 1)])
+                                         (1024, 8, 2), (1025, 8, 50), (4096, 6, 30), (9001, 5, 1), (20000, 3, 4)])
 def test_build_matches_the_plain_form(R, cols, most):
     rng = np.random.default_rng(R)
     s = _step(rng, R, cols, most)
@@ -141,7 +141,7 @@ def _release(table, lens, keep, fl, nf, in_place=False):
     return f.cpu().numpy(), int(out)
 
 
-@pytest.mark.parametrize("R,cols", [(1, 5), (64, 130), (1024, 9), (1025, 9), (5000, 7), (3, 2048)])
+@pytest.mark.parametrize("R,cols", [(1, 5), (64, 130), (1024, 9), (1025, 9), (5000, 7), (20000, 2), (3, 2048)])
 def test_release_matches_the_plain_form(R, cols):
     rng = np.random.default_rng(R)
     lens = rng.integers(0, cols * BS + 1, R)

@@ -13,23 +13,34 @@
 // and lo's four, so the split is exact for every element above 2^-10 of the
 // row's largest, and off by at most 2^-18 of the largest below that.  Twice
 // the MMAs at twice the bf16 rate: the tensor time of a bf16 K, none of its
-// widening.
-// A key's block scale multiplies its column of S in the softmax.
+// widening.  A key's block scale multiplies its column of S in the softmax.
 //
-// O += P V takes bf16: P rows are 128 wide here, and splitting 128 x 128
+// O += P V takes f16: P rows are 128 wide here, and splitting 128 x 128
 // probabilities in the softmax, which sets the pace, would cost more than
-// widening V once per tile in warps of its own: four converter warps write
-// bf16(decode(code) * scale) -- exact for power-of-two scales -- into one of
-// two operand buffers, rows past the request's end as zeros.  They also split
-// each item's Q, ahead of its first V tile.
+// widening V once per tile in warps of its own (one hardware conversion per
+// pair of codes; every e4m3 value is an f16 value).  The value scales join the
+// probabilities: with vs = r 2^lv of key j's block,
+//     P = exp2(s - m) * F,   F = exp2(m - mo + lv + 6) * r
+// is at most 2^15, mo being a running maximum of s + lv next to the running
+// maximum m of s that the normaliser uses; both are raised when exceeded by
+// more than 2^8.  So P is precise where it weighs, however far apart the
+// blocks' scales are, and F is one factor per row and block.  (Widening V to
+// bf16 with its scale multiplied in needs no F but twelve instructions where
+// two do: 182 against 150 us on eight 512-token chunks.)
 //
-// Roles (736 threads): warps 0-15 softmax and epilogue, four threads per MMA
-// row (see pkv_prefill.cu); 16 takes items from the work queue and copies K
-// tiles and their scales; 17 issues the MMAs; 18 copies V tiles and scales;
-// 19-22 convert Q and V.  Items travel through a four-entry ring that every
-// role reads.
+// Roles (640 threads): warps 0-15 softmax and epilogue, four threads per MMA
+// row (warps with the same index mod 4 hold the same 32 rows); they also split
+// the next item's Q between an item's last probabilities and its epilogue,
+// while the tensor core finishes the item.  Warp 16 takes items from the work
+// queue and copies K and V tiles and the scales; 17 issues the MMAs; 18 and 19
+// widen V.  Items travel through a four-entry ring that every role reads.
 //
-// Bound: the softmax's instruction issue, like the bf16 kernel's.
+// Bound: the softmax's instruction issue and latencies (the tensor pipe's
+// share of a tile is about 1150 cycles: the S MMAs read 8 KB of shared memory
+// each at 128 bytes a clock).  Hence the pipeline inside each softmax warp: the
+// scores of tile t + 1 are fetched from TMEM, half a tile at a time into the
+// registers that the exponentials of tile t have freed, and P has TMEM columns
+// of its own, so that a score buffer is free as soon as it is read.
 #include <climits>
 
 #include "pkv_internal.h"
@@ -42,11 +53,10 @@ constexpr int kParts = 4;                // softmax threads per MMA row
 constexpr int kPartKeys = 128 / kParts;  // keys (and output dims) per softmax thread
 constexpr int kSoftWarps = 4 * kParts;
 constexpr int kSoftThreads = 32 * kSoftWarps;
-constexpr int kWarpK = kSoftWarps;       // items, K tiles
+constexpr int kWarpLoad = kSoftWarps;    // items, K and V tiles
 constexpr int kWarpMma = kSoftWarps + 1;
-constexpr int kWarpV = kSoftWarps + 2;
-constexpr int kWarpConv = kSoftWarps + 3;
-constexpr int kConvWarps = 4;
+constexpr int kWarpConv = kSoftWarps + 2;
+constexpr int kConvWarps = 2;
 constexpr int kThreads = 32 * (kWarpConv + kConvWarps);
 constexpr int kBarSoftmax = 1;
 constexpr int kBarQuad = 2;              // + quad: the four warps holding the same 32 rows
@@ -55,13 +65,17 @@ constexpr int kKeyTile = 128;
 constexpr int kBlkPerTile = kKeyTile / kBlockSize;
 constexpr int kCodes = kKeyTile * kHeadDim;  // a K or V tile, or a Q operand, in bytes
 constexpr int kHalfBytes = kKeyTile * 128;   // one 64-dim half of a widened V tile
-constexpr uint32_t kTmemCols = 512;      // S0: cols 0..127, S1: 128..255, O: 256..383
-constexpr float kRescaleLog2 = 8.0f;
+// TMEM columns: S0 0..127, S1 128..255, O 256..383, P0 384..447, P1 448..511.
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 256, kColP = 384;
+constexpr float kMargin = 8.0f;          // log2 of the largest exp2(s - m) allowed
+constexpr float kTop = 6.0f;             // P carries 2^kTop: below 2^(kMargin + 1 + kTop) = 2^15
 constexpr float kNegBig = -1.0e30f;
 constexpr int kPastEnd = INT_MIN;        // block-table slot past the request (not read)
-constexpr int kStages = 3;               // K stages, and raw V stages
+constexpr int kStages = 3;               // K stages
+constexpr int kStagesV = 3;              // V stages (codes)
 constexpr int kItems = 4;                // item ring
-constexpr int kScaleRing = 8;            // tiles whose K scales are held
+constexpr int kScaleRing = 8;            // tiles whose scales are held
 
 struct Item {
   int r, k;   // request, KV head
@@ -76,19 +90,18 @@ struct Item {
 struct __align__(1024) Smem {
   uint8_t q[2][kCodes];              // hi | lo
   uint8_t k[kStages][kCodes];
-  uint8_t v[kStages][kCodes];        // V codes
+  uint8_t v[kStagesV][kCodes];       // V codes
   uint8_t vb[2][2][kHalfBytes];      // widened V: [buffer][d half]
-  float xrow[kParts][kRows];         // [key part][row]: partial row maxima, then normalisers
-  float qf[kItems][kRows];           // factor of a row's raw scores (log2 units)
-  float ks[kScaleRing][kBlkPerTile]; // K scales of a tile's blocks
-  float vs[kStages][kBlkPerTile];    // V scales of a stage's blocks
+  float2 xrow[kParts][kRows];        // [key part][row]: partial row maxima, then normalisers
+  float qf[kRows];                   // factor of a row's raw scores (log2 units)
+  float sc[kScaleRing][2][kBlkPerTile];  // [K | V] scales of a tile's blocks
   Item items[kItems];
   uint64_t it_full[kItems], it_free[kItems];
-  uint64_t q_full[kItems], q_empty;
-  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t ks_full[kScaleRing];
+  uint64_t q_full;
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kStagesV], v_empty[kStagesV];
+  uint64_t sc_full[kScaleRing];
   uint64_t vb_full[2], vb_free[2];
-  uint64_t s_full[2], p_full[2], p_free[2];
+  uint64_t s_full[2], s_free[2], p_full[2], p_free[2];
   uint64_t o_full, o_empty;
   uint64_t mma_done;
   uint32_t tmem_base;
@@ -150,6 +163,52 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
   return r;
 }
 
+// Four codes (low byte first) to two f16 pairs.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float2 v) {
+  const __half2 h = __floats2half2_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)),
+        "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+
+// Waits for the TMEM loads into a and b (as operands, so that nothing reads
+// them earlier).
+__device__ __forceinline__ void wait_ld32(float (&a)[16], float (&b)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(a[0]), "+f"(a[1]), "+f"(a[2]), "+f"(a[3]), "+f"(a[4]), "+f"(a[5]),
+                 "+f"(a[6]), "+f"(a[7]), "+f"(a[8]), "+f"(a[9]), "+f"(a[10]), "+f"(a[11]),
+                 "+f"(a[12]), "+f"(a[13]), "+f"(a[14]), "+f"(a[15]), "+f"(b[0]), "+f"(b[1]),
+                 "+f"(b[2]), "+f"(b[3]), "+f"(b[4]), "+f"(b[5]), "+f"(b[6]), "+f"(b[7]),
+                 "+f"(b[8]), "+f"(b[9]), "+f"(b[10]), "+f"(b[11]), "+f"(b[12]), "+f"(b[13]),
+                 "+f"(b[14]), "+f"(b[15])
+               :
+               : "memory");
+}
+
+// A block's value scale as r 2^lv: lv an integer, r in [1, 2) (0 for a zero
+// scale, NaN for one that is not finite).
+__device__ __forceinline__ void split_scale(float vs, float& lv, float& r) {
+  const int e = min(max((int)((__float_as_uint(vs) >> 23) & 255u), 1), 253);
+  lv = (float)(e - 127);
+  r = vs - vs == 0.f ? vs * __uint_as_float((uint32_t)(254 - e) << 23) : __int_as_float(0x7fc00000);
+}
+
 template <int G>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_block_kernel(const __grid_constant__ CUtensorMap kmap,
@@ -191,21 +250,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < kItems; ++s) {
       mbar_init(&sm.it_full[s], 1);
-      mbar_init(&sm.it_free[s], kSoftWarps + kConvWarps + 2);  // softmax, converters, MMA, V
-      mbar_init(&sm.q_full[s], kConvWarps);
+      mbar_init(&sm.it_free[s], kSoftWarps + kConvWarps + 1);  // softmax, converters, MMA
     }
-    mbar_init(&sm.q_empty, 1);  // tcgen05.commit after the item's last S
+    mbar_init(&sm.q_full, kSoftWarps);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&sm.k_full[s], 1);
       mbar_init(&sm.k_empty[s], 1);
-      mbar_init(&sm.v_full[s], 1 + kBlkPerTile);  // the tile, and a scale copy per block
+    }
+    for (int s = 0; s < kStagesV; ++s) {
+      mbar_init(&sm.v_full[s], 1);
       mbar_init(&sm.v_empty[s], kConvWarps);
     }
-    for (int s = 0; s < kScaleRing; ++s) mbar_init(&sm.ks_full[s], kBlkPerTile);
+    for (int s = 0; s < kScaleRing; ++s) mbar_init(&sm.sc_full[s], 2 * kBlkPerTile);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sm.vb_full[b], kConvWarps);
       mbar_init(&sm.vb_free[b], 1);
       mbar_init(&sm.s_full[b], 1);
+      mbar_init(&sm.s_free[b], kSoftWarps);
       mbar_init(&sm.p_full[b], kSoftWarps);
       mbar_init(&sm.p_free[b], 1);
     }
@@ -216,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm.wait.limit_ns = p.wait_limit_ns;
     fence_barrier_init();
   }
-  if (warp == kWarpK && lane == 0) {
+  if (warp == kWarpLoad && lane == 0) {
     prefetch_tensormap(&kmap);
     prefetch_tensormap(&vmap);
   }
@@ -239,13 +300,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     return !it.end;
   };
 
-  if (warp == kWarpK || warp == kWarpV) {
-    // ==================== TMA producers (items + K | V) ===================
-    const bool vside = warp == kWarpV;
-    uint64_t* const full = vside ? sm.v_full : sm.k_full;
-    uint64_t* const empty = vside ? sm.v_empty : sm.k_empty;
-    const CUtensorMap* const map = vside ? &vmap : &kmap;
-    int n_item = 0, t = 0;
+  if (warp == kWarpLoad) {
+    // ==================== items, K and V tiles, scales =====================
+    int n_item = 0, t = 0, nk = 0, nv = 0;  // items, tiles; K and V copies issued
     const int oob_row = p.num_blocks * Hkv * kBlockSize;
     auto stream_item = [&](const Item& it) {
       const int nbl = ceil_div(it.L, kBlockSize);
@@ -261,36 +318,43 @@ __global__ void __launch_bounds__(kThreads, 1)
           ent_cur = ent_nxt;
           if (j + 4 < it.nj) ent_nxt = raw_entries((j + 4) * kBlkPerTile);
         }
-        const int st = t % kStages;
-        if (t >= kStages && !mbar_wait(&empty[st], ((t / kStages) - 1) & 1, p.err, abort_flag))
-          return false;
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], (uint32_t)kCodes);
-        __syncwarp();
+        // Blocks past the request (or outside the pool: recorded) are read at
+        // an out-of-range row, which TMA fills with zeros, with scale 0.
         const int phys = __shfl_sync(0xffffffffu, ent_cur, (j & 3) * kBlkPerTile + (lane & 7));
-        if (lane < kBlkPerTile) {
-          // Blocks past the request (or outside the pool: recorded) are read
-          // at an out-of-range row, which TMA fills with zeros, with scale 0.
-          const bool good = (unsigned)phys < (unsigned)p.num_blocks;
-          if (!good && phys != kPastEnd && !vside) record_error(p.err, kErrBounds);
-          tma_load_2d((vside ? sm.v[st] : sm.k[st]) + lane * 2048, map, 0,
-                      good ? (phys * Hkv + it.k) * kBlockSize : oob_row, &full[st]);
-          const float* src = (vside ? pb.v_scales : pb.k_scales) +
+        const bool good = (unsigned)phys < (unsigned)p.num_blocks;
+        const int pool_row = good ? (phys * Hkv + it.k) * kBlockSize : oob_row;
+        if (lane < kBlkPerTile && !good && phys != kPastEnd) record_error(p.err, kErrBounds);
+        const int sk = t % kStages;
+        if (t >= kStages &&
+            !mbar_wait(&sm.k_empty[sk], ((t / kStages) - 1) & 1, p.err, abort_flag))
+          return false;
+        if (lane == 0) mbar_arrive_expect_tx(&sm.k_full[sk], (uint32_t)kCodes);
+        __syncwarp();
+        if (lane < kBlkPerTile) tma_load_2d(sm.k[sk] + lane * 2048, &kmap, 0, pool_row, &sm.k_full[sk]);
+        nk = t + 1;
+        if (lane < 2 * kBlkPerTile) {
+          // Scales outlive their K stage: a ring entry is reused eight tiles
+          // on, when S of the tile three before is done, hence the softmax has
+          // taken S and the scales of the tile five before.
+          static_assert(kScaleRing >= kStages + 2, "scales outlive their tile");
+          const float* src = (lane < kBlkPerTile ? pb.k_scales : pb.v_scales) +
                              (good ? (long long)phys * Hkv + it.k : 0);
-          // K scales outlive their stage: a ring entry is reused eight tiles
-          // on, when S of the tile three before is done, hence PV of the tile
-          // five before, hence the softmax that read the entry.
-          static_assert(kScaleRing >= kStages + 3, "K scales outlive their tile's softmax");
-          copy4_async(vside ? &sm.vs[st][lane] : &sm.ks[t % kScaleRing][lane], src, good ? 4u : 0u);
-          arrive_after_copies(vside ? &sm.v_full[st] : &sm.ks_full[t % kScaleRing]);
+          copy4_async(&sm.sc[t % kScaleRing][lane >> 3][lane & 7], src, good ? 4u : 0u);
+          arrive_after_copies(&sm.sc_full[t % kScaleRing]);
         }
+        const int sv = t % kStagesV;
+        if (t >= kStagesV &&
+            !mbar_wait(&sm.v_empty[sv], ((t / kStagesV) - 1) & 1, p.err, abort_flag))
+          return false;
+        if (lane == 0) mbar_arrive_expect_tx(&sm.v_full[sv], (uint32_t)kCodes);
+        __syncwarp();
+        if (lane < kBlkPerTile) tma_load_2d(sm.v[sv] + lane * 2048, &vmap, 0, pool_row, &sm.v_full[sv]);
+        nv = t + 1;
         __syncwarp();
       }
       return true;
     };
-    if (vside) {
-      Item it;
-      while (take_item(n_item, it) && stream_item(it)) ++n_item;
-    } else {
+    {
       // Items are numbered batch of 32 requests by batch, longest request
       // first within a batch, heavier q-tiles first within a request, and
       // taken from the queue in that order (see pkv_prefill.cu).
@@ -364,20 +428,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (abort_flag->abort) {
       // Copies in flight land before the CTA's shared memory is released.
-      // (V's barriers also count scale copies, so the last stages' data may
-      // be complete without their phase; the wait is bounded.)
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      for (int m = max(0, t - kStages); m < t; ++m)
-        mbar_wait_drain(&full[m % kStages], (m / kStages) & 1, p.err, abort_flag);
+      for (int m = max(0, nk - kStages); m < nk; ++m)
+        mbar_wait_drain(&sm.k_full[m % kStages], (m / kStages) & 1, p.err, abort_flag);
+      for (int m = max(0, nv - kStagesV); m < nv; ++m)
+        mbar_wait_drain(&sm.v_full[m % kStagesV], (m / kStagesV) & 1, p.err, abort_flag);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == kWarpMma) {
     // ========================= MMA issuer =================================
-    // Tile t: S(t) into S buffer t & 1, then O += P(t-1) V(t-1), so S of the
-    // next tile runs while the softmax works on the current one.
+    // Tile t: S(t) into S buffer t & 1, then O += P(t-2) V(t-2).  An S buffer
+    // is free as soon as the softmax has taken its scores, well before it sends
+    // their P, so S runs ahead of PV by two tiles: with S(t) behind PV(t-1) the
+    // softmax waited for it (3500 cycles a tile).
     constexpr uint32_t kIdescS = idesc_e4m3_f32(kRows, kKeyTile, 0, 0);
-    constexpr uint32_t kIdescO = idesc_bf16_f32(kRows, kHeadDim, 0, 1);
-    const uint32_t tO = tmem + 2 * kKeyTile;
+    constexpr uint32_t kIdescO = idesc_f16_f32(kRows, kHeadDim, 0, 1);
+    // Descriptors of the operands' first chunks: a chunk of 32 bytes of a row
+    // is 2 further (16-byte units), a V chunk of 16 keys 128.
+    const uint64_t dq = smem_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
+    const uint64_t dk = smem_desc_sw128(smem_u32(sm.k[0]), 16, 1024);
+    const uint64_t dv = smem_desc_sw128(smem_u32(sm.vb[0][0]), kHalfBytes, 1024);
+    const bool leader = elect_one();
     int t = 0;
     bool ok = true;
     auto pv = [&](int tt, bool first, int n) {
@@ -387,255 +457,309 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (first && n > 0) ok = ok && mbar_wait(&sm.o_empty, (n - 1) & 1, p.err, abort_flag);
       if (!ok) return;
       tc_fence_after();
-      #pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        // P: keys 16kk .. +15 in columns 8kk .. +7 of S buffer b; V MN-major,
+      if (leader) {
+        // P: keys 16kk .. +15 in columns 8kk .. +7 of P buffer b; V MN-major,
         // two 64-dim halves.
-        const uint64_t db = smem_desc_sw128(smem_u32(sm.vb[b][0]) + kk * 2048, kHalfBytes, 1024);
-        tc_mma_f16_ts(tO, tmem + b * kKeyTile + kk * 8, db, kIdescO, !first || kk > 0);
+        const uint64_t db = dv + b * (2 * kHalfBytes / 16);
+        const uint32_t ta = tmem + kColP + b * 64;
+        #pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          tc_mma_f16_ts(tmem + kColO, ta + kk * 8, db + kk * 128, kIdescO, !first || kk > 0);
+        tc_commit(&sm.vb_free[b]);
+        tc_commit(&sm.p_free[b]);
       }
-      tc_commit(&sm.vb_free[b]);
-      tc_commit(&sm.p_free[b]);
+      __syncwarp();
     };
     for (int n = 0; ok; ++n) {
       Item it;
       if (!take_item(n, it)) break;
-      if (lane == 0) {
-        ok = mbar_wait(&sm.q_full[n % kItems], (n / kItems) & 1, p.err, abort_flag);
-        for (int j = 0; j < it.nj && ok; ++j, ++t) {
-          const int b = t & 1, st = t % kStages;
-          ok = ok && mbar_wait(&sm.k_full[st], (t / kStages) & 1, p.err, abort_flag);
-          if (t >= 2) ok = ok && mbar_wait(&sm.p_free[b], ((t >> 1) - 1) & 1, p.err, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
+      const int nj = it.nj;
+      ok = mbar_wait(&sm.q_full, n & 1, p.err, abort_flag);
+      int st = t % kStages, phase = (t / kStages) & 1;
+      for (int j = 0; j < nj && ok; ++j, ++t) {
+        const int b = t & 1;
+        ok = ok && mbar_wait(&sm.k_full[st], phase, p.err, abort_flag);
+        if (t >= 2) ok = ok && mbar_wait(&sm.s_free[b], ((t >> 1) - 1) & 1, p.err, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          const uint64_t db = dk + st * (kCodes / 16);
+          const uint32_t tS = tmem + b * kKeyTile;
           #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {  // hi rows, then lo rows
-            const uint64_t da = smem_desc_sw128(smem_u32(sm.q[kk >> 2]) + (kk & 3) * 32, 16, 1024);
-            const uint64_t db = smem_desc_sw128(smem_u32(sm.k[st]) + (kk & 3) * 32, 16, 1024);
-            tc_mma_f8_ss(tmem + b * kKeyTile, da, db, kIdescS, kk > 0);
-          }
+          for (int kk = 0; kk < 8; ++kk)  // hi rows, then lo rows
+            tc_mma_f8_ss(tS, dq + (kk >> 2) * (kCodes / 16) + (kk & 3) * 2, db + (kk & 3) * 2, kIdescS,
+                         kk > 0);
           tc_commit(&sm.k_empty[st]);
           tc_commit(&sm.s_full[b]);
-          if (j + 1 == it.nj) tc_commit(&sm.q_empty);
-          if (j >= 1) pv(t - 1, j == 1, n);
         }
-        if (ok) pv(t - 1, it.nj == 1, n);
-        if (ok) tc_commit(&sm.o_full);
+        __syncwarp();
+        if (++st == kStages) {
+          st = 0;
+          phase ^= 1;
+        }
+        if (j >= 2) pv(t - 2, j == 2, n);
       }
+      if (ok && nj >= 2) pv(t - 2, nj == 2, n);
+      if (ok) pv(t - 1, nj == 1, n);
+      if (ok && leader) tc_commit(&sm.o_full);
       __syncwarp();
-      ok = __shfl_sync(0xffffffffu, ok, 0);
     }
-    if (lane == 0 && abort_flag->abort) {
-      tc_commit(&sm.mma_done);  // MMAs in flight finish before TMEM is freed
+    if (abort_flag->abort) {
+      if (leader) tc_commit(&sm.mma_done);  // MMAs in flight finish before TMEM is freed
+      __syncwarp();
       mbar_wait_drain(&sm.mma_done, 0, p.err, abort_flag);
     }
     __syncwarp();
   } else if (warp >= kWarpConv) {
-    // ==================== converters: Q of an item, then its V tiles =======
-    const int row = tid - kWarpConv * 32, sw = row & 7;
+    // ==================== V converters: two key rows per thread ============
+    const int row0 = tid - kWarpConv * 32;
     int t = 0;
+    bool ok = true;
     Item it;
-    for (int n = 0; take_item(n, it); ++n) {
-      {
-        // Row `row` of Q: token row / G, head row % G; rows past the tile's
-        // tokens become zero.
-        const bool valid = row < it.nt * G;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            pb.q + ((long long)(it.row0 + row / G) * p.num_q_heads + (long long)it.k * G + row % G) *
-                       kHeadDim);
-        uint4 x[16];
-        uint32_t top = 0;
-        #pragma unroll
-        for (int c = 0; c < 16; ++c) x[c] = valid ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-        #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+    for (int n = 0; ok && take_item(n, it); ++n) {
+      for (int j = 0; j < it.nj && ok; ++j, ++t) {
+        const int st = t % kStagesV, b = t & 1;
+        ok = mbar_wait(&sm.v_full[st], (t / kStagesV) & 1, p.err, abort_flag);
+        if (ok && t >= 2) ok = mbar_wait(&sm.vb_free[b], ((t >> 1) - 1) & 1, p.err, abort_flag);
+        if (!ok) break;
+        #pragma unroll 1
+        for (int row = row0; row < kKeyTile; row += 32 * kConvWarps) {
+          // A key row widened: past the request's end a block may hold
+          // anything (NaN codes too), and 0 * V has to stay 0.
+          const bool keep = j * kKeyTile + row < it.L;
+          const int sw = row & 7;
+          uint4 c[8];
           #pragma unroll
-          for (int i = 0; i < 4; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
-        }
-        const int e = max((int)(max(top & 0xffffu, top >> 16) >> 7), 1);
-        // sigma = 2^(134 - e) in two factors within fp32's range, NaN for a
-        // row that is not finite; the sign of the softmax scale goes to q, so
-        // that a tile's largest score is its largest column times its factor.
-        const float sgn = p.scale_log2 < 0.f ? -1.f : 1.f;
-        const float s1 = e < 255 ? sgn * __uint_as_float((uint32_t)(127 + (134 - e) / 2) << 23)
-                                 : __int_as_float(0x7fc00000);
-        const float s2 = __uint_as_float((uint32_t)(127 + (134 - e) - (134 - e) / 2) << 23);
-        if (n > 0 && !mbar_wait(&sm.q_empty, (n - 1) & 1, p.err, abort_flag)) break;
-        #pragma unroll
-        for (int c = 0; c < 8; ++c) {  // 16 dims: one 16-byte chunk of each operand
-          const uint32_t w[8] = {x[2 * c].x,     x[2 * c].y,     x[2 * c].z,     x[2 * c].w,
-                                 x[2 * c + 1].x, x[2 * c + 1].y, x[2 * c + 1].z, x[2 * c + 1].w};
-          uint32_t hi[4], lo[4];
+          for (int i = 0; i < 8; ++i)
+            c[i] = keep ? lds128(sm.v[st] + row * 128 + ((i ^ sw) * 16)) : make_uint4(0, 0, 0, 0);
           #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float2 f = bf16x2_to_float2(w[i]);
-            const float a = f.x * s1 * s2, b = f.y * s1 * s2;
-            const uint32_t h = to_e4m3x2(a, b);
-            const float2 back = e4m3x2_to_float2(h);
-            const uint32_t l = to_e4m3x2(a - back.x, b - back.y);
-            if (i & 1) {
-              hi[i >> 1] |= h << 16;
-              lo[i >> 1] |= l << 16;
-            } else {
-              hi[i >> 1] = h;
-              lo[i >> 1] = l;
-            }
+            const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+            uint32_t o[8];
+            #pragma unroll
+            for (int e = 0; e < 4; ++e) e4m3x4_to_f16x4(w[e], o[2 * e], o[2 * e + 1]);
+            uint8_t* dst = sm.vb[b][i >> 2] + row * 128;
+            const int at = (i & 3) * 2;
+            *reinterpret_cast<uint4*>(dst + ((at ^ sw) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(dst + (((at + 1) ^ sw) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
           }
-          const int at = row * 128 + ((c ^ sw) * 16);
-          *reinterpret_cast<uint4*>(sm.q[0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(sm.q[1] + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-        sm.qf[n % kItems][row] = p.scale_log2 / s1 / s2;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.q_full[n % kItems]);
-      }
-      bool ok = true;
-      for (int j = 0; j < it.nj; ++j, ++t) {
-        const int st = t % kStages, b = t & 1;
-        ok = mbar_wait(&sm.v_full[st], (t / kStages) & 1, p.err, abort_flag);
-        if (!ok) break;
-        // Key row `row` of the tile, widened: past the request's end a block
-        // may hold anything (NaN codes too), and 0 * V has to stay 0.
-        const bool keep = j * kKeyTile + row < it.L;
-        const float s = sm.vs[st][row >> 4];
-        uint4 c[8];
-        #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          c[i] = keep ? lds128(sm.v[st] + row * 128 + ((i ^ sw) * 16)) : make_uint4(0, 0, 0, 0);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.v_empty[st]);
-        if (t >= 2) ok = mbar_wait(&sm.vb_free[b], ((t >> 1) - 1) & 1, p.err, abort_flag);
-        if (!ok) break;
-        #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
-          uint32_t o[8];
-          #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 u = e4m3x2_to_float2(w[e] & 0xffffu), v = e4m3x2_to_float2(w[e] >> 16);
-            o[2 * e] = pack_bf16x2(u.x * s, u.y * s);
-            o[2 * e + 1] = pack_bf16x2(v.x * s, v.y * s);
-          }
-          uint8_t* dst = sm.vb[b][i >> 2] + row * 128;
-          const int at = (i & 3) * 2;
-          *reinterpret_cast<uint4*>(dst + ((at ^ sw) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<uint4*>(dst + (((at + 1) ^ sw) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.vb_full[b]);
+        if (lane == 0) {
+          mbar_arrive(&sm.v_empty[st]);
+          mbar_arrive(&sm.vb_full[b]);
+        }
       }
-      if (!ok) break;
     }
   } else {
     // =================== softmax + epilogue (warps 0-15) ===================
     const int quad = warp & 3;
     const int part = warp >> 2;
     const int row = quad * 32 + lane;  // MMA row == TMEM lane
-    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const uint32_t tO = tmem + lane_off + 2 * kKeyTile + part * kPartKeys;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t tO = lanes + kColO + part * kPartKeys;
     const int t_local = row / G, h = row % G;
     int t = 0;
-    for (int n = 0;; ++n) {
-      Item it;
-      bool have = take_item(n, it);
-      have = have && mbar_wait(&sm.q_full[n % kItems], (n / kItems) & 1, p.err, abort_flag);
-      // Agree before any barrier: a wait that gave up (abort) stops everyone.
-      if (barrier_or(kBarSoftmax, kSoftThreads, !have)) break;
+
+    // Splits item n's Q; four threads a row, 32 dims each.
+    auto convert_q = [&](const Item& it) {
+      const int r = tid >> 2, c = tid & 3;  // token r / G, head r % G; rows past the tile's
+      const bool valid = r < it.nt * G;     // tokens become zero
+      const uint4* src = reinterpret_cast<const uint4*>(
+          pb.q + ((long long)(it.row0 + r / G) * p.num_q_heads + (long long)it.k * G + r % G) *
+                     kHeadDim) + c * 4;
+      uint4 x[4];
+      uint32_t top = 0;
+      #pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                     __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+      }
+      top = max(top & 0xffffu, top >> 16);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // sigma = 2^(134 - e), e the largest element's biased exponent (from 7
+      // on: below 2^-120 a row is as good as zero); NaN for a row that is not
+      // finite.  The sign of the softmax scale goes to q, so that a tile's
+      // largest score is its largest column times its factor.
+      const int e = max((int)(top >> 7), 7);
+      const float sigma = e < 255 ? __uint_as_float((uint32_t)(261 - e) << 23)
+                                  : __int_as_float(0x7fc00000);
+      const float s = p.scale_log2 < 0.f ? -sigma : sigma;
+      #pragma unroll
+      for (int i = 0; i < 2; ++i) {  // 16 dims: one 16-byte chunk of each operand
+        const uint32_t w[8] = {x[2 * i].x,     x[2 * i].y,     x[2 * i].z,     x[2 * i].w,
+                               x[2 * i + 1].x, x[2 * i + 1].y, x[2 * i + 1].z, x[2 * i + 1].w};
+        uint32_t hi[4], lo[4];
+        #pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float2 f = bf16x2_to_float2(w[k]);
+          const float a = f.x * s, b = f.y * s;
+          const uint32_t u = to_e4m3x2(a, b);
+          const float2 back = e4m3x2_to_float2(u);
+          const uint32_t l = to_e4m3x2(a - back.x, b - back.y);
+          hi[k >> 1] = k & 1 ? hi[k >> 1] | u << 16 : u;
+          lo[k >> 1] = k & 1 ? lo[k >> 1] | l << 16 : l;
+        }
+        const int at = r * 128 + (((c * 2 + i) ^ (r & 7)) * 16);
+        *reinterpret_cast<uint4*>(sm.q[0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(sm.q[1] + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      if (c == 0) sm.qf[r] = p.scale_log2 / s;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.q_full);
+    };
+
+    Item it;
+    bool have = take_item(0, it);
+    // Agree before any barrier: a wait that gave up (abort) stops everyone.
+    bool more = !barrier_or(kBarSoftmax, kSoftThreads, !have);
+    if (more) convert_q(it);
+    for (int n = 0; more; ++n) {
+      bool ok = mbar_wait(&sm.q_full, n & 1, p.err, abort_flag);
       const bool valid = t_local < it.nt && row < TQ * G;
       const int prow = valid ? it.pos0 + t_local : -1;  // the last key this row sees
-      const float qf = sm.qf[n % kItems][row];
-      float m = kNegBig, l = 0.f;
-      bool ok = true;
-      for (int j = 0; j < it.nj; ++j, ++t) {
-        const int sb = t & 1;
-        const uint32_t tS = tmem + lane_off + sb * kKeyTile;
-        ok = ok && mbar_wait(&sm.ks_full[t % kScaleRing], (t / kScaleRing) & 1, p.err, abort_flag);
-        // This part's 32 keys are two blocks.  (A factor of 0 would turn a
-        // masked -inf into NaN; 1e-30 leaves the scores 0.)
-        float sc0 = qf * sm.ks[t % kScaleRing][part * 2], sc1 = qf * sm.ks[t % kScaleRing][part * 2 + 1];
-        if (sc0 == 0.f) sc0 = 1e-30f;
-        if (sc1 == 0.f) sc1 = 1e-30f;
-        ok = ok && mbar_wait(&sm.s_full[sb], (t >> 1) & 1, p.err, abort_flag);
-        tc_fence_after();
-        const int kbase = j * kKeyTile + part * kPartKeys;
-        float v[kPartKeys];
-        tmem_ld32(tS + part * kPartKeys, v);
-        tc_wait_ld();
-        if (kbase + kPartKeys - 1 > prow) {
-          #pragma unroll
-          for (int i = 0; i < kPartKeys; ++i)
-            if (kbase + i > prow) v[i] = -INFINITY;
-        }
-        float mxp[4];
-        #pragma unroll
-        for (int i = 0; i < 4; ++i) mxp[i] = -INFINITY;
-        #pragma unroll
-        for (int i = 0; i < kPartKeys / 2; ++i) {
-          float& mx = mxp[(i & 1) + (i >= kPartKeys / 4 ? 2 : 0)];
-          mx = fmax3(mx, v[2 * i], v[2 * i + 1]);
-        }
-        const float mxh = fmaxf(fmaxf(mxp[0], mxp[1]) * sc0, fmaxf(mxp[2], mxp[3]) * sc1);
-        // Past an item's first tile the maximum is exchanged only when some
-        // part exceeds the reference by 2^8; the vote also orders every
-        // part's S reads before any P write over them.
-        tc_fence_before();
-        const bool exchange = barrier_or(kBarQuad + quad, 128, j == 0 || mxh > m + kRescaleLog2);
-        tc_fence_after();
-        if (exchange) {
-          sm.xrow[part][row] = mxh;
-          named_barrier(kBarQuad + quad, 128);
-          const float mx = fmaxf(fmaxf(sm.xrow[0][row], sm.xrow[1][row]),
-                                 fmaxf(sm.xrow[2][row], sm.xrow[3][row]));
-          named_barrier(kBarQuad + quad, 128);  // sm.xrow is free again
-          const bool grow = j == 0 || mx > m + kRescaleLog2;
-          if (j == 0) {
-            m = fmaxf(m, mx);
-          } else if (__any_sync(0xffffffffu, grow)) {
-            // O must first hold the previous tile's PV.
-            ok = ok && mbar_wait(&sm.p_free[(t - 1) & 1], ((t - 1) >> 1) & 1, p.err, abort_flag);
-            tc_fence_after();
-            const float m_new = grow ? fmaxf(m, mx) : m;
-            const float alpha = fast_exp2(m - m_new);
-            rescale_o(tO, alpha);
-            l *= alpha;
-            m = m_new;
-          }
-        }
-        // P = exp2(s - m) in bf16, two keys per column, over the row's S; the
-        // normaliser sums the rounded values the MMA uses.
-        const float2 nm2 = make_float2(-m, -m);
-        float sum_lo[2] = {0.f, 0.f}, sum_hi[2] = {0.f, 0.f};
-        uint32_t w[kPartKeys / 2];
-        #pragma unroll
-        for (int e = 0; e < kPartKeys / 2; ++e) {
-          const float sc = e < kPartKeys / 4 ? sc0 : sc1;
-          const float2 x = ffma2(make_float2(v[2 * e], v[2 * e + 1]), make_float2(sc, sc), nm2);
-          w[e] = pack_bf16x2(fast_exp2(x.x), fast_exp2(x.y));
-          add_bf16x2(sum_lo[e & 1], sum_hi[e & 1], w[e]);
-        }
-        tmem_st16(tS + part * (kPartKeys / 2), w);
-        tc_wait_st();
-        l += (sum_lo[0] + sum_hi[0]) + (sum_lo[1] + sum_hi[1]);
+      const int nj = it.nj;
+      __nv_bfloat16* const dst = p.out + ((long long)(it.row0 + t_local) * p.num_q_heads +
+                                          (long long)it.k * G + h) * kHeadDim + part * kPartKeys;
+      const float qf = sm.qf[row];
+      float m = kNegBig, mo = kNegBig, l = 0.f;
+      // The tile at hand: this part's 32 scores (two blocks of 16 keys), and
+      // the blocks' factors of a score and of a probability.
+      float x0[16], x1[16], sc0, sc1, f0, f1;
+      // Tile tt's scores taken from the registers they were fetched to:
+      // masked, the references raised where the maxima exceed them by
+      // 2^kMargin.  (A factor of 0 would turn a masked -inf into NaN; 1e-30
+      // leaves the scores 0.)
+      auto take = [&](int tt, int g) {
+        ok = ok && mbar_wait(&sm.sc_full[g % kScaleRing], (g / kScaleRing) & 1, p.err, abort_flag);
+        const float2 ks = *reinterpret_cast<const float2*>(&sm.sc[g % kScaleRing][0][part * 2]);
+        const float2 vs = *reinterpret_cast<const float2*>(&sm.sc[g % kScaleRing][1][part * 2]);
+        wait_ld32(x0, x1);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_full[sb]);
+        if (lane == 0) mbar_arrive(&sm.s_free[g & 1]);
+        sc0 = qf * ks.x;
+        sc1 = qf * ks.y;
+        if (sc0 == 0.f) sc0 = 1e-30f;
+        if (sc1 == 0.f) sc1 = 1e-30f;
+        float lv0, lv1, r0, r1;
+        split_scale(vs.x, lv0, r0);
+        split_scale(vs.y, lv1, r1);
+        const int kbase = tt * kKeyTile + part * kPartKeys;
+        if (kbase + kPartKeys - 1 > prow) {
+          #pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (kbase + i > prow) x0[i] = -INFINITY;
+            if (kbase + 16 + i > prow) x1[i] = -INFINITY;
+          }
+        }
+        float a0 = -INFINITY, a1 = -INFINITY, b0 = -INFINITY, b1 = -INFINITY;
+        #pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          a0 = fmax3(a0, x0[i], x0[i + 1]);
+          a1 = fmax3(a1, x0[i + 2], x0[i + 3]);
+          b0 = fmax3(b0, x1[i], x1[i + 1]);
+          b1 = fmax3(b1, x1[i + 2], x1[i + 3]);
+        }
+        const float mx0 = fmaxf(a0, a1) * sc0, mx1 = fmaxf(b0, b1) * sc1;
+        const float mxh = fmaxf(mx0, mx1), moh = fmaxf(mx0 + lv0, mx1 + lv1);
+        if (barrier_or(kBarQuad + quad, 128, tt == 0 || mxh > m + kMargin || moh > mo + kMargin)) {
+          sm.xrow[part][row] = make_float2(mxh, moh);
+          named_barrier(kBarQuad + quad, 128);
+          float m_new = m, mo_new = mo;
+          #pragma unroll
+          for (int i = 0; i < kParts; ++i) {
+            const float2 y = sm.xrow[i][row];
+            m_new = fmaxf(m_new, y.x);
+            mo_new = fmaxf(mo_new, y.y);
+          }
+          named_barrier(kBarQuad + quad, 128);  // sm.xrow is free again
+          l *= fast_exp2(m - m_new);
+          if (tt > 0 && __any_sync(0xffffffffu, mo_new != mo)) {
+            // O must first hold the previous tile's PV.
+            ok = ok && mbar_wait(&sm.p_free[(g - 1) & 1], ((g - 1) >> 1) & 1, p.err, abort_flag);
+            tc_fence_after();
+            rescale_o(tO, fast_exp2(mo - mo_new));
+            tc_fence_before();
+          }
+          m = m_new;
+          mo = mo_new;
+        }
+        // F, held to 2^100: a probability is then so small that P stays finite.
+        const float up = m - mo + kTop;
+        f0 = fast_exp2(fminf(up + lv0, 100.f)) * r0;
+        f1 = fast_exp2(fminf(up + lv1, 100.f)) * r1;
+      };
+      const uint32_t tS = lanes + part * kPartKeys;
+      ok = ok && mbar_wait(&sm.s_full[t & 1], (t >> 1) & 1, p.err, abort_flag);
+      tc_fence_after();
+      tmem_ld16(tS + (t & 1) * kKeyTile, x0);
+      tmem_ld16(tS + (t & 1) * kKeyTile + 16, x1);
+      take(0, t);
+      #pragma unroll 1
+      for (int j = 0; j < nj; ++j, ++t) {
+        const int b = t & 1;
+        const bool more_keys = j + 1 < nj;
+        const uint32_t next = tS + (b ^ 1) * kKeyTile;
+        // p = exp2(s - m) into the normaliser, P = p F in f16, two keys per
+        // column, one block after the other; each block's registers take the
+        // next tile's scores.
+        const float2 nm2 = make_float2(-m, -m);
+        float2 sum = make_float2(0.f, 0.f);
+        uint32_t w[kPartKeys / 2];
+        auto block = [&](const float (&x)[16], float sc, float f, int at) {
+          #pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float2 y = ffma2(make_float2(x[2 * e], x[2 * e + 1]), make_float2(sc, sc), nm2);
+            const float2 q = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+            sum = fadd2(sum, q);
+            w[at + e] = pack_f16x2(fmul2(q, make_float2(f, f)));
+          }
+        };
+        block(x0, sc0, f0, 0);
+        if (more_keys) {
+          ok = ok && mbar_wait(&sm.s_full[b ^ 1], ((t + 1) >> 1) & 1, p.err, abort_flag);
+          tc_fence_after();
+          tmem_ld16(next, x0);
+        }
+        block(x1, sc1, f1, 8);
+        if (more_keys) tmem_ld16(next + 16, x1);
+        l += sum.x + sum.y;
+        // P buffer b was last read by the PV of two tiles before.
+        if (t >= 2) ok = ok && mbar_wait(&sm.p_free[b], ((t >> 1) - 1) & 1, p.err, abort_flag);
+        tc_fence_after();
+        tmem_st16(lanes + kColP + b * 64 + part * (kPartKeys / 2), w);
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[b]);
+        if (more_keys) take(j + 1, t + 1);
       }
+      // The next item's Q, which the MMAs of this one no longer read (its last
+      // scores have been taken).
+      have = take_item(n + 1, it);
+      more = !barrier_or(kBarSoftmax, kSoftThreads, !have);
+      if (more) convert_q(it);
       // ---- epilogue: O / l -> bf16 -> out (this part's 32 dims) ----------
-      sm.xrow[part][row] = l;
+      sm.xrow[part][row].x = l;
       named_barrier(kBarQuad + quad, 128);
-      const float lrow = (sm.xrow[0][row] + sm.xrow[1][row]) + (sm.xrow[2][row] + sm.xrow[3][row]);
+      const float lrow = (sm.xrow[0][row].x + sm.xrow[1][row].x) +
+                         (sm.xrow[2][row].x + sm.xrow[3][row].x);
       named_barrier(kBarQuad + quad, 128);  // sm.xrow is free again
       ok = ok && mbar_wait(&sm.o_full, n & 1, p.err, abort_flag);
       tc_fence_after();
-      const float inv = lrow == 0.f ? 0.f : 1.f / lrow;
-      __nv_bfloat16* dst = p.out + ((long long)(it.row0 + t_local) * p.num_q_heads +
-                                    (long long)it.k * G + h) * kHeadDim + part * kPartKeys;
+      // O carries 2^(kTop - mo), the normaliser 2^-m.
+      const float inv = lrow == 0.f ? 0.f : exp2f(mo - m - kTop) / lrow;
       float o[32];
       tmem_ld32(tO, o);
       tc_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.o_empty);
       if (valid && ok) {
         #pragma unroll
         for (int i = 0; i < 32; i += 8) {
@@ -647,9 +771,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4*>(dst + i) = q4;
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.o_empty);
     }
   }
   // Every warp reaches this point (aborts only shorten the loops), so the

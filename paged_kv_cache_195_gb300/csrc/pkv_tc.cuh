@@ -113,6 +113,19 @@ __device__ __forceinline__ void tc_mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, u
       : "memory");
 }
 
+// True in one lane of a converged warp.  Code that issues MMAs keeps its
+// control flow warp-uniform and guards only the instructions themselves with
+// this, so that descriptors stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // Arrive on `bar` once every tcgen05 operation this thread issued so far has
 // completed.
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {

@@ -74,7 +74,7 @@ def attention(q, pools, scales, table, lens, qsl, scale, min_q=16):
     """q float64 [T, Hq, 128].  Returns (out, bound): the outputs and, element
     by element, how far a computation may be off that rounds what the kernels
     round (see bound's terms below).  Requests with at least min_q query rows
-    are taken by the prefill kernel, which rounds more."""
+    are taken by the prefill kernel, whose weights are f16."""
     out, bound = np.zeros(q.shape), np.zeros(q.shape)
     hq, hkv = q.shape[1], pools[0].shape[1]
     g = hq // hkv
@@ -110,8 +110,8 @@ def attention(q, pools, scales, table, lens, qsl, scale, min_q=16):
                 ds = ds + 2 * np.where(sees, abs(scale) * (small @ np.abs(K).T), 0).max(1, keepdims=True)
                 # A weight is a pair of e4m3 numbers: rounded by at most 2^-9,
                 # or by at most 2^-18 of the largest weight times value scale.
-                # The prefill kernel rounds weight and value to bf16: 2^-8 each.
-                rounded = 2.0 ** -7 if m >= min_q else 2.0 ** -9
+                # The prefill kernel rounds it to f16: 2^-11.
+                rounded = 2.0 ** -11 if m >= min_q else 2.0 ** -9
                 floor = 2.0 ** -18 * (w * sc[1][None]).max(1, keepdims=True) * \
                     (np.where(sees, 1.0, 0.0) @ np.abs(codes[1]))
                 mean = w @ np.abs(V)

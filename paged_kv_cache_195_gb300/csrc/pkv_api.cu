@@ -656,10 +656,10 @@ int attention_impl(const void* q, const void* k_pool, const void* v_pool, const 
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
   if (do_prefill && block_scales) {
     pkv::PrefillBlockLaunch L{};
-    rc = encode_pool_map_e4m3(&L.kmap, k_pool, dims);
+    rc = encode_q_map(&L.qmap, q, dims, group, pkv::prefill_tokens_per_tile(group));
+    if (rc == PKV_OK) rc = encode_pool_map_e4m3(&L.kmap, k_pool, dims);
     if (rc == PKV_OK) rc = encode_pool_map_e4m3(&L.vmap, v_pool, dims);
     if (rc != PKV_OK) return rc;
-    L.p.q = p.q;
     L.p.k_scales = k_scale;
     L.p.v_scales = v_scale;
     pkv::PrefillParams& f = L.p.p;

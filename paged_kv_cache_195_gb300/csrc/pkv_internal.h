@@ -309,16 +309,17 @@ struct PrefillLaunch {
 
 int prefill_tokens_per_tile(int group);
 
-// Chunked prefill over e4m3 pools with a scale per (block, KV head); kmap /
-// vmap as in DecodeBlockLaunch.  The prefix-pass fields of `p` are unused.
+// Chunked prefill over e4m3 pools with a scale per (block, KV head); qmap as
+// in PrefillLaunch, kmap / vmap as in DecodeBlockLaunch.  The prefix-pass
+// fields of `p` are unused.
 struct PrefillBlockParams {
   PrefillParams p;
-  const __nv_bfloat16* q;
   const float* k_scales;  // [num_blocks, Hkv]
   const float* v_scales;
 };
 
 struct PrefillBlockLaunch {
+  CUtensorMap qmap;
   CUtensorMap kmap;
   CUtensorMap vmap;
   PrefillBlockParams p;

@@ -29,11 +29,13 @@
 // two do: 182 against 150 us on eight 512-token chunks.)
 //
 // Roles (640 threads): warps 0-15 softmax and epilogue, four threads per MMA
-// row (warps with the same index mod 4 hold the same 32 rows); they also split
-// the next item's Q between an item's last probabilities and its epilogue,
-// while the tensor core finishes the item.  Warp 16 takes items from the work
-// queue and copies K and V tiles and the scales; 17 issues the MMAs; 18 and 19
-// widen V.  Items travel through a four-entry ring that every role reads.
+// row (warps with the same index mod 4 hold the same 32 rows); warp 16 takes
+// items from the work queue and copies Q, K and V tiles and the scales; 17
+// issues the MMAs; 18 and 19 widen V.  Items travel through a four-entry ring
+// that every role reads, published a few tiles before the previous item ends,
+// with its Q on the way; before an item's last probabilities the softmax warps
+// split the next one's Q (in place: a row's 256 bytes of bf16 become its 128 of
+// hi and 128 of lo), so that its first S is there after them.
 //
 // Bound: the softmax's instruction issue and latencies (the tensor pipe's
 // share of a tile is about 1150 cycles: the S MMAs read 8 KB of shared memory
@@ -52,14 +54,12 @@ namespace {
 constexpr int kParts = 4;                // softmax threads per MMA row
 constexpr int kPartKeys = 128 / kParts;  // keys (and output dims) per softmax thread
 constexpr int kSoftWarps = 4 * kParts;
-constexpr int kSoftThreads = 32 * kSoftWarps;
 constexpr int kWarpLoad = kSoftWarps;    // items, K and V tiles
 constexpr int kWarpMma = kSoftWarps + 1;
 constexpr int kWarpConv = kSoftWarps + 2;
 constexpr int kConvWarps = 2;
 constexpr int kThreads = 32 * (kWarpConv + kConvWarps);
-constexpr int kBarSoftmax = 1;
-constexpr int kBarQuad = 2;              // + quad: the four warps holding the same 32 rows
+constexpr int kBarQuad = 1;              // + quad: the four warps holding the same 32 rows
 constexpr int kRows = 128;               // MMA M
 constexpr int kKeyTile = 128;
 constexpr int kBlkPerTile = kKeyTile / kBlockSize;
@@ -73,8 +73,10 @@ constexpr float kTop = 6.0f;             // P carries 2^kTop: below 2^(kMargin +
 constexpr float kNegBig = -1.0e30f;
 constexpr int kPastEnd = INT_MIN;        // block-table slot past the request (not read)
 constexpr int kStages = 3;               // K stages
-constexpr int kStagesV = 3;              // V stages (codes)
+constexpr int kStagesV = 2;              // V stages (codes)
 constexpr int kItems = 4;                // item ring
+constexpr int kAhead = 4;                // an item is published this many tiles before the
+                                         // previous one's last copies
 constexpr int kScaleRing = 8;            // tiles whose scales are held
 
 struct Item {
@@ -88,16 +90,16 @@ struct Item {
 };
 
 struct __align__(1024) Smem {
-  uint8_t q[2][kCodes];              // hi | lo
+  uint8_t q[2][2][kCodes];           // [item & 1][hi | lo] (first: dims 0..63 | 64..127 in bf16)
   uint8_t k[kStages][kCodes];
   uint8_t v[kStagesV][kCodes];       // V codes
   uint8_t vb[2][2][kHalfBytes];      // widened V: [buffer][d half]
   float2 xrow[kParts][kRows];        // [key part][row]: partial row maxima, then normalisers
-  float qf[kRows];                   // factor of a row's raw scores (log2 units)
+  float qf[kItems][kRows];           // factor of a row's raw scores (log2 units)
   float sc[kScaleRing][2][kBlkPerTile];  // [K | V] scales of a tile's blocks
   Item items[kItems];
   uint64_t it_full[kItems], it_free[kItems];
-  uint64_t q_full;
+  uint64_t qr_full[2], q_full[kItems], q_empty[2];  // raw Q landed / split / read by its last S
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStagesV], v_empty[kStagesV];
   uint64_t sc_full[kScaleRing];
   uint64_t vb_full[2], vb_free[2];
@@ -209,9 +211,60 @@ __device__ __forceinline__ void split_scale(float vs, float& lv, float& r) {
   r = vs - vs == 0.f ? vs * __uint_as_float((uint32_t)(254 - e) << 23) : __int_as_float(0x7fc00000);
 }
 
+// The softmax warps split an item's Q in place: q holds its two 64-dim halves
+// in bf16 and gets the hi and the lo operand; qf gets the rows' factors of the
+// raw scores, bar every warp's arrival.  Warp w takes rows 8w .. 8w + 7, four
+// threads a row, 32 dims each.  Out of line: once per item, and inlined it
+// cost the tile loop registers.
+static __device__ __forceinline__ void split_q(uint8_t* q, float scale_log2, float* qf, uint64_t* bar) {
+  const int r = threadIdx.x >> 2, c = threadIdx.x & 3, sw = r & 7;
+  q += r * 128;
+  uint4 x[4];
+  uint32_t top = 0;
+  #pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = lds128(q + (c >> 1) * kCodes + ((((c & 1) * 4 + i) ^ sw) * 16));
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                 __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+  }
+  top = max(top & 0xffffu, top >> 16);
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  __syncwarp();  // the row's four threads (one warp) have read it
+  // sigma = 2^(134 - e), e the largest element's biased exponent (from 7 on:
+  // below 2^-120 a row is as good as zero); NaN for a row that is not finite.
+  // The sign of the softmax scale goes to q, so that a tile's largest score is
+  // its largest column times its factor.
+  const int e = max((int)(top >> 7), 7);
+  const float sigma = e < 255 ? __uint_as_float((uint32_t)(261 - e) << 23)
+                              : __int_as_float(0x7fc00000);
+  const float s = scale_log2 < 0.f ? -sigma : sigma;
+  #pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    uint32_t hi[4], lo[4];
+    #pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = bf16x2_to_float2(w[k]);
+      const float a = f.x * s, b = f.y * s;
+      hi[k] = to_e4m3x2(a, b);
+      const float2 back = e4m3x2_to_float2(hi[k]);
+      lo[k] = to_e4m3x2(a - back.x, b - back.y);
+    }
+    uint8_t* const at = q + ((c * 2 + (i >> 1)) ^ sw) * 16 + (i & 1) * 8;
+    *reinterpret_cast<uint2*>(at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+    *reinterpret_cast<uint2*>(at + kCodes) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+  }
+  if (c == 0) qf[r] = scale_log2 / s;
+  fence_proxy_async_smem();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 template <int G>
 __global__ void __launch_bounds__(kThreads, 1)
-    prefill_block_kernel(const __grid_constant__ CUtensorMap kmap,
+    prefill_block_kernel(const __grid_constant__ CUtensorMap qmap,
+                         const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap vmap, const PrefillBlockParams pb) {
   constexpr int TQ = kRows / G;  // query tokens per item
   const PrefillParams& p = pb.p;
@@ -251,8 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kItems; ++s) {
       mbar_init(&sm.it_full[s], 1);
       mbar_init(&sm.it_free[s], kSoftWarps + kConvWarps + 1);  // softmax, converters, MMA
+      mbar_init(&sm.q_full[s], kSoftWarps);
     }
-    mbar_init(&sm.q_full, kSoftWarps);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&sm.k_full[s], 1);
       mbar_init(&sm.k_empty[s], 1);
@@ -263,6 +316,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < kScaleRing; ++s) mbar_init(&sm.sc_full[s], 2 * kBlkPerTile);
     for (int b = 0; b < 2; ++b) {
+      mbar_init(&sm.qr_full[b], 1);
+      mbar_init(&sm.q_empty[b], 1);  // tcgen05.commit after the item's last S
       mbar_init(&sm.vb_full[b], kConvWarps);
       mbar_init(&sm.vb_free[b], 1);
       mbar_init(&sm.s_full[b], 1);
@@ -278,8 +333,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
   }
   if (warp == kWarpLoad && lane == 0) {
+    prefetch_tensormap(&qmap);
     prefetch_tensormap(&kmap);
     prefetch_tensormap(&vmap);
+  }
+  // Q rows that no copy writes stay zero.
+  if constexpr (TQ * G < kRows) {
+    constexpr int kPad = (kRows - TQ * G) * 8;  // 16-byte chunks of an operand
+    for (int i = tid; i < 4 * kPad; i += kThreads)
+      *reinterpret_cast<uint4*>(&sm.q[0][0][0] + (i / kPad) * kCodes + TQ * G * 128 + (i % kPad) * 16) =
+          make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
   }
   if (warp == kWarpMma) {
     tmem_alloc(&sm.tmem_base, kTmemCols);
@@ -302,8 +366,88 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == kWarpLoad) {
     // ==================== items, K and V tiles, scales =====================
-    int n_item = 0, t = 0, nk = 0, nv = 0;  // items, tiles; K and V copies issued
+    int n_item = 0, t = 0, nq = 0, nk = 0, nv = 0;  // items, tiles; Q, K and V copies issued
     const int oob_row = p.num_blocks * Hkv * kBlockSize;
+    // Items are numbered batch of 32 requests by batch, longest request first
+    // within a batch, heavier q-tiles first within a request, and taken from
+    // the queue in that order (see pkv_prefill.cu).
+    Req rq = {0, 0, 0, 0};     // this lane's request of the batch
+    long long cnt = 0, excl = 0, total = 0, base = 0;
+    int batch = -32;
+    auto next_item = [&](Item& it) {
+      unsigned long long taken = 0;
+      if (lane == 0) taken = atomicAdd(p.sched, 1ull);
+      const long long item = (long long)__shfl_sync(0xffffffffu, taken, 0);
+      while (item >= base + total) {
+        batch += 32;
+        base += total;
+        if (batch >= p.num_reqs) {
+          it = Item{};
+          it.end = 1;
+          total = 0;
+          batch = p.num_reqs;
+          return;
+        }
+        rq = Req{0, 0, 0, 0};
+        if (batch + lane < p.num_reqs) rq = load_req(p, batch + lane, TQ);
+        cnt = (long long)rq.ntiles * Hkv;
+        total = cnt;
+        #pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        const int key = cnt > 0 ? rq.L : -1;
+        excl = 0;
+        #pragma unroll 4
+        for (int s = 0; s < 32; ++s) {
+          const int ks = __shfl_sync(0xffffffffu, key, s);
+          const long long cs = __shfl_sync(0xffffffffu, cnt, s);
+          if (ks > key || (ks == key && s < lane)) excl += cs;
+        }
+      }
+      const long long rel = item - base;
+      const unsigned own = __ballot_sync(0xffffffffu, cnt > 0 && excl <= rel && rel < excl + cnt);
+      const int src = __ffs(own) - 1;
+      const long long local = rel - __shfl_sync(0xffffffffu, excl, src);
+      const int q0 = __shfl_sync(0xffffffffu, rq.q0, src);
+      const int qr = __shfl_sync(0xffffffffu, rq.qr, src);
+      const int L = __shfl_sync(0xffffffffu, rq.L, src);
+      const int qt = __shfl_sync(0xffffffffu, rq.ntiles, src) - 1 - (int)(local / Hkv);
+      it.r = batch + src;
+      it.k = (int)(local % Hkv);
+      it.row0 = q0 + qt * TQ;
+      it.nt = min(TQ, qr - qt * TQ);
+      it.pos0 = L - qr + qt * TQ;
+      it.L = L;
+      it.nj = (it.pos0 + it.nt - 1) / kKeyTile + 1;
+      it.end = 0;
+    };
+    // The next item into nx and the ring.
+    Item nx;
+    auto publish_next = [&]() {
+      next_item(nx);
+      const int s = n_item % kItems;
+      if (n_item >= kItems &&
+          !mbar_wait(&sm.it_free[s], ((n_item / kItems) - 1) & 1, p.err, abort_flag))
+        return false;
+      if (lane == 0) {
+        sm.items[s] = nx;
+        mbar_arrive(&sm.it_full[s]);
+      }
+      __syncwarp();
+      if (!nx.end) {  // its Q, into the buffer of the item before the current one
+        const int b = n_item & 1;
+        if (n_item >= 2 && !mbar_wait(&sm.q_empty[b], ((n_item >> 1) - 1) & 1, p.err, abort_flag))
+          return false;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sm.qr_full[b], 2u * 64u * TQ * G * 2u);
+          tma_load_3d(sm.q[b][0], &qmap, 0, nx.k * G, nx.row0, &sm.qr_full[b]);
+          tma_load_3d(sm.q[b][1], &qmap, 64, nx.k * G, nx.row0, &sm.qr_full[b]);
+        }
+        __syncwarp();
+        nq = n_item + 1;
+      }
+      ++n_item;
+      return true;
+    };
     auto stream_item = [&](const Item& it) {
       const int nbl = ceil_div(it.L, kBlockSize);
       const int32_t* bt = p.block_tables + (long long)it.r * p.max_blocks;
@@ -314,6 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int ent_cur = raw_entries(0);
       int ent_nxt = it.nj > 4 ? raw_entries(32) : kPastEnd;
       for (int j = 0; j < it.nj; ++j, ++t) {
+        if (j == max(0, it.nj - kAhead) && !publish_next()) return false;
         if (j > 0 && (j & 3) == 0) {
           ent_cur = ent_nxt;
           if (j + 4 < it.nj) ent_nxt = raw_entries((j + 4) * kBlkPerTile);
@@ -354,80 +499,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return true;
     };
-    {
-      // Items are numbered batch of 32 requests by batch, longest request
-      // first within a batch, heavier q-tiles first within a request, and
-      // taken from the queue in that order (see pkv_prefill.cu).
-      auto next_item = [&]() {
-        unsigned long long v = 0;
-        if (lane == 0) v = atomicAdd(p.sched, 1ull);
-        return (long long)__shfl_sync(0xffffffffu, v, 0);
-      };
-      auto publish = [&](const Item& it) {
-        const int s = n_item % kItems;
-        if (n_item >= kItems &&
-            !mbar_wait(&sm.it_free[s], ((n_item / kItems) - 1) & 1, p.err, abort_flag))
-          return false;
-        if (lane == 0) {
-          sm.items[s] = it;
-          mbar_arrive(&sm.it_full[s]);
-        }
-        __syncwarp();
-        return true;
-      };
-      long long item = next_item();
-      long long base = 0;
-      bool ok = true;
-      for (int b = 0; b < p.num_reqs && ok && !abort_flag->abort; b += 32) {
-        Req rq = {0, 0, 0, 0};
-        if (b + lane < p.num_reqs) rq = load_req(p, b + lane, TQ);
-        const long long cnt = (long long)rq.ntiles * Hkv;
-        long long total = cnt;
-        #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        if (item >= base + total) {
-          base += total;
-          continue;
-        }
-        const int key = cnt > 0 ? rq.L : -1;
-        long long excl = 0;
-        #pragma unroll 4
-        for (int s = 0; s < 32; ++s) {
-          const int ks = __shfl_sync(0xffffffffu, key, s);
-          const long long cs = __shfl_sync(0xffffffffu, cnt, s);
-          if (ks > key || (ks == key && s < lane)) excl += cs;
-        }
-        const long long incl = excl + cnt;
-        while (item < base + total && ok && !abort_flag->abort) {
-          const long long rel = item - base;
-          const unsigned own = __ballot_sync(0xffffffffu, cnt > 0 && excl <= rel && rel < incl);
-          const int src = __ffs(own) - 1;
-          const long long local = rel - __shfl_sync(0xffffffffu, excl, src);
-          const int q0 = __shfl_sync(0xffffffffu, rq.q0, src);
-          const int qr = __shfl_sync(0xffffffffu, rq.qr, src);
-          const int L = __shfl_sync(0xffffffffu, rq.L, src);
-          const int qt = __shfl_sync(0xffffffffu, rq.ntiles, src) - 1 - (int)(local / Hkv);
-          Item it;
-          it.r = b + src;
-          it.k = (int)(local % Hkv);
-          it.row0 = q0 + qt * TQ;
-          it.nt = min(TQ, qr - qt * TQ);
-          it.pos0 = L - qr + qt * TQ;
-          it.L = L;
-          it.nj = (it.pos0 + it.nt - 1) / kKeyTile + 1;
-          it.end = 0;
-          ok = publish(it) && stream_item(it);
-          ++n_item;
-          item = next_item();
-        }
-        base += total;
+    if (publish_next()) {
+      while (!nx.end) {
+        const Item it = nx;
+        if (!stream_item(it)) break;
       }
-      Item fin = {};
-      fin.end = 1;
-      if (ok) publish(fin);
     }
     if (abort_flag->abort) {
       // Copies in flight land before the CTA's shared memory is released.
+      for (int m = max(0, nq - 2); m < nq; ++m)
+        mbar_wait_drain(&sm.qr_full[m & 1], (m >> 1) & 1, p.err, abort_flag);
       for (int m = max(0, nk - kStages); m < nk; ++m)
         mbar_wait_drain(&sm.k_full[m % kStages], (m / kStages) & 1, p.err, abort_flag);
       for (int m = max(0, nv - kStagesV); m < nv; ++m)
@@ -444,13 +525,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kIdescO = idesc_f16_f32(kRows, kHeadDim, 0, 1);
     // Descriptors of the operands' first chunks: a chunk of 32 bytes of a row
     // is 2 further (16-byte units), a V chunk of 16 keys 128.
-    const uint64_t dq = smem_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
+    const uint64_t dq = smem_desc_sw128(smem_u32(sm.q[0][0]), 16, 1024);
     const uint64_t dk = smem_desc_sw128(smem_u32(sm.k[0]), 16, 1024);
     const uint64_t dv = smem_desc_sw128(smem_u32(sm.vb[0][0]), kHalfBytes, 1024);
     const bool leader = elect_one();
     int t = 0;
     bool ok = true;
-    auto pv = [&](int tt, bool first, int n) {
+    // O += P V of tile tt: item n's first, last?
+    auto pv = [&](int tt, bool first, bool last, int n) {
       const int b = tt & 1;
       ok = ok && mbar_wait(&sm.p_full[b], (tt >> 1) & 1, p.err, abort_flag);
       ok = ok && mbar_wait(&sm.vb_full[b], (tt >> 1) & 1, p.err, abort_flag);
@@ -467,15 +549,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_mma_f16_ts(tmem + kColO, ta + kk * 8, db + kk * 128, kIdescO, !first || kk > 0);
         tc_commit(&sm.vb_free[b]);
         tc_commit(&sm.p_free[b]);
+        if (last) tc_commit(&sm.o_full);
       }
       __syncwarp();
     };
+    int st = 0, phase = 0;
     for (int n = 0; ok; ++n) {
       Item it;
       if (!take_item(n, it)) break;
       const int nj = it.nj;
-      ok = mbar_wait(&sm.q_full, n & 1, p.err, abort_flag);
-      int st = t % kStages, phase = (t / kStages) & 1;
+      ok = mbar_wait(&sm.q_full[n % kItems], (n / kItems) & 1, p.err, abort_flag);
+      const uint64_t da = dq + (n & 1) * (2 * kCodes / 16);
       for (int j = 0; j < nj && ok; ++j, ++t) {
         const int b = t & 1;
         ok = ok && mbar_wait(&sm.k_full[st], phase, p.err, abort_flag);
@@ -487,22 +571,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t tS = tmem + b * kKeyTile;
           #pragma unroll
           for (int kk = 0; kk < 8; ++kk)  // hi rows, then lo rows
-            tc_mma_f8_ss(tS, dq + (kk >> 2) * (kCodes / 16) + (kk & 3) * 2, db + (kk & 3) * 2, kIdescS,
+            tc_mma_f8_ss(tS, da + (kk >> 2) * (kCodes / 16) + (kk & 3) * 2, db + (kk & 3) * 2, kIdescS,
                          kk > 0);
           tc_commit(&sm.k_empty[st]);
           tc_commit(&sm.s_full[b]);
+          if (j + 1 == nj) tc_commit(&sm.q_empty[n & 1]);
         }
         __syncwarp();
         if (++st == kStages) {
           st = 0;
           phase ^= 1;
         }
-        if (j >= 2) pv(t - 2, j == 2, n);
+        if (j >= 2) pv(t - 2, j == 2, false, n);
       }
-      if (ok && nj >= 2) pv(t - 2, nj == 2, n);
-      if (ok) pv(t - 1, nj == 1, n);
-      if (ok && leader) tc_commit(&sm.o_full);
-      __syncwarp();
+      // The item's last two PVs, before waiting for the next item: its Q is
+      // split after this one's last P.
+      for (int i = min(nj, 2); i > 0 && ok; --i) pv(t - i, nj == i, i == 1, n);
     }
     if (abort_flag->abort) {
       if (leader) tc_commit(&sm.mma_done);  // MMAs in flight finish before TMEM is freed
@@ -511,8 +595,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp >= kWarpConv) {
-    // ==================== V converters: two key rows per thread ============
-    const int row0 = tid - kWarpConv * 32;
+    // ============================ V converters =============================
+    constexpr int kConvThreads = 32 * kConvWarps;
+    const int row0 = tid - kWarpConv * 32;  // its key rows: row0, row0 + kConvThreads
     int t = 0;
     bool ok = true;
     Item it;
@@ -523,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && t >= 2) ok = mbar_wait(&sm.vb_free[b], ((t >> 1) - 1) & 1, p.err, abort_flag);
         if (!ok) break;
         #pragma unroll 1
-        for (int row = row0; row < kKeyTile; row += 32 * kConvWarps) {
+        for (int row = row0; row < kKeyTile; row += kConvThreads) {
           // A key row widened: past the request's end a block may hold
           // anything (NaN codes too), and 0 * V has to stay 0.
           const bool keep = j * kKeyTile + row < it.L;
@@ -562,70 +647,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t_local = row / G, h = row % G;
     int t = 0;
 
-    // Splits item n's Q; four threads a row, 32 dims each.
-    auto convert_q = [&](const Item& it) {
-      const int r = tid >> 2, c = tid & 3;  // token r / G, head r % G; rows past the tile's
-      const bool valid = r < it.nt * G;     // tokens become zero
-      const uint4* src = reinterpret_cast<const uint4*>(
-          pb.q + ((long long)(it.row0 + r / G) * p.num_q_heads + (long long)it.k * G + r % G) *
-                     kHeadDim) + c * 4;
-      uint4 x[4];
-      uint32_t top = 0;
-      #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
-                                     __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
-      }
-      top = max(top & 0xffffu, top >> 16);
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // sigma = 2^(134 - e), e the largest element's biased exponent (from 7
-      // on: below 2^-120 a row is as good as zero); NaN for a row that is not
-      // finite.  The sign of the softmax scale goes to q, so that a tile's
-      // largest score is its largest column times its factor.
-      const int e = max((int)(top >> 7), 7);
-      const float sigma = e < 255 ? __uint_as_float((uint32_t)(261 - e) << 23)
-                                  : __int_as_float(0x7fc00000);
-      const float s = p.scale_log2 < 0.f ? -sigma : sigma;
-      #pragma unroll
-      for (int i = 0; i < 2; ++i) {  // 16 dims: one 16-byte chunk of each operand
-        const uint32_t w[8] = {x[2 * i].x,     x[2 * i].y,     x[2 * i].z,     x[2 * i].w,
-                               x[2 * i + 1].x, x[2 * i + 1].y, x[2 * i + 1].z, x[2 * i + 1].w};
-        uint32_t hi[4], lo[4];
-        #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float2 f = bf16x2_to_float2(w[k]);
-          const float a = f.x * s, b = f.y * s;
-          const uint32_t u = to_e4m3x2(a, b);
-          const float2 back = e4m3x2_to_float2(u);
-          const uint32_t l = to_e4m3x2(a - back.x, b - back.y);
-          hi[k >> 1] = k & 1 ? hi[k >> 1] | u << 16 : u;
-          lo[k >> 1] = k & 1 ? lo[k >> 1] | l << 16 : l;
-        }
-        const int at = r * 128 + (((c * 2 + i) ^ (r & 7)) * 16);
-        *reinterpret_cast<uint4*>(sm.q[0] + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(sm.q[1] + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      }
-      if (c == 0) sm.qf[r] = p.scale_log2 / s;
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.q_full);
-    };
-
     Item it;
-    bool have = take_item(0, it);
-    // Agree before any barrier: a wait that gave up (abort) stops everyone.
-    bool more = !barrier_or(kBarSoftmax, kSoftThreads, !have);
-    if (more) convert_q(it);
+    bool ok = true, more = false;
+    // Item n into `it`, its Q split; false if there is none.
+    auto begin_item = [&](int n) {
+      bool have = take_item(n, it);
+      have = have && mbar_wait(&sm.qr_full[n & 1], (n >> 1) & 1, p.err, abort_flag);
+      // Agree before the next barrier of these rows' four warps (the only
+      // barriers there are): a wait that gave up (abort) stops them all.
+      if (barrier_or(kBarQuad + quad, 128, !have)) return false;
+      split_q(sm.q[n & 1][0], p.scale_log2, sm.qf[n % kItems], &sm.q_full[n % kItems]);
+      return true;
+    };
+    more = begin_item(0);
     for (int n = 0; more; ++n) {
-      bool ok = mbar_wait(&sm.q_full, n & 1, p.err, abort_flag);
+      ok = ok && mbar_wait(&sm.q_full[n % kItems], (n / kItems) & 1, p.err, abort_flag);
       const bool valid = t_local < it.nt && row < TQ * G;
       const int prow = valid ? it.pos0 + t_local : -1;  // the last key this row sees
       const int nj = it.nj;
       __nv_bfloat16* const dst = p.out + ((long long)(it.row0 + t_local) * p.num_q_heads +
                                           (long long)it.k * G + h) * kHeadDim + part * kPartKeys;
-      const float qf = sm.qf[row];
+      const float qf = sm.qf[n % kItems][row];
       float m = kNegBig, mo = kNegBig, l = 0.f;
       // The tile at hand: this part's 32 scores (two blocks of 16 keys), and
       // the blocks' factors of a score and of a probability.
@@ -739,36 +781,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&sm.p_full[b]);
         if (more_keys) take(j + 1, t + 1);
       }
-      // The next item's Q, which the MMAs of this one no longer read (its last
-      // scores have been taken).
-      have = take_item(n + 1, it);
-      more = !barrier_or(kBarSoftmax, kSoftThreads, !have);
-      if (more) convert_q(it);
-      // ---- epilogue: O / l -> bf16 -> out (this part's 32 dims) ----------
       sm.xrow[part][row].x = l;
-      named_barrier(kBarQuad + quad, 128);
+      more = begin_item(n + 1);  // (also the barrier between this row's parts)
+      // ---- epilogue: O / l -> bf16 -> out (this part's 32 dims) ----------
       const float lrow = (sm.xrow[0][row].x + sm.xrow[1][row].x) +
                          (sm.xrow[2][row].x + sm.xrow[3][row].x);
       named_barrier(kBarQuad + quad, 128);  // sm.xrow is free again
-      ok = ok && mbar_wait(&sm.o_full, n & 1, p.err, abort_flag);
-      tc_fence_after();
       // O carries 2^(kTop - mo), the normaliser 2^-m.
       const float inv = lrow == 0.f ? 0.f : exp2f(mo - m - kTop) / lrow;
-      float o[32];
-      tmem_ld32(tO, o);
-      tc_wait_ld();
+      ok = ok && mbar_wait(&sm.o_full, n & 1, p.err, abort_flag);
+      tc_fence_after();
+      tmem_ld16(tO, x0);
+      tmem_ld16(tO + 16, x1);
+      wait_ld32(x0, x1);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.o_empty);
       if (valid && ok) {
         #pragma unroll
-        for (int i = 0; i < 32; i += 8) {
+        for (int i = 0; i < 16; i += 8) {
           uint4 q4;
-          q4.x = pack_bf16x2(o[i] * inv, o[i + 1] * inv);
-          q4.y = pack_bf16x2(o[i + 2] * inv, o[i + 3] * inv);
-          q4.z = pack_bf16x2(o[i + 4] * inv, o[i + 5] * inv);
-          q4.w = pack_bf16x2(o[i + 6] * inv, o[i + 7] * inv);
+          q4.x = pack_bf16x2(x0[i] * inv, x0[i + 1] * inv);
+          q4.y = pack_bf16x2(x0[i + 2] * inv, x0[i + 3] * inv);
+          q4.z = pack_bf16x2(x0[i + 4] * inv, x0[i + 5] * inv);
+          q4.w = pack_bf16x2(x0[i + 6] * inv, x0[i + 7] * inv);
           *reinterpret_cast<uint4*>(dst + i) = q4;
+          q4.x = pack_bf16x2(x1[i] * inv, x1[i + 1] * inv);
+          q4.y = pack_bf16x2(x1[i + 2] * inv, x1[i + 3] * inv);
+          q4.z = pack_bf16x2(x1[i + 4] * inv, x1[i + 5] * inv);
+          q4.w = pack_bf16x2(x1[i + 6] * inv, x1[i + 7] * inv);
+          *reinterpret_cast<uint4*>(dst + 16 + i) = q4;
         }
       }
     }
@@ -818,7 +860,7 @@ cudaError_t launch_g(const PrefillBlockLaunch& L, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = L.p.p.pdl ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, prefill_block_kernel<G>, L.kmap, L.vmap, L.p);
+  e = cudaLaunchKernelEx(&cfg, prefill_block_kernel<G>, L.qmap, L.kmap, L.vmap, L.p);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

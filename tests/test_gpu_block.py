@@ -357,6 +357,35 @@ def test_attention_long_chunk_after_a_long_prefix():
     _check(c, [90, 200], _rows(rng, 290, 5))
 
 
+@pytest.mark.parametrize("g,hkv", [(4, 4), (5, 8)])
+def test_attention_many_chunks_whose_scores_rise_to_the_end(g, hkv):
+    # Several work items per SM, and the running maxima raised at every tile,
+    # an item's last one too.
+    rng = np.random.default_rng(22)
+    lens = [int(x) for x in rng.integers(100, 900, 40)]
+    q = [min(n, 100) for n in lens]
+    c = Cache(rng, lens, hkv)
+    for r, n in enumerate(lens):
+        for b in range(-(-n // BS)):
+            c.scales[0][c.table[r, b]] = 2.0 ** (b // 4 % 8 - 8)
+            c.scales[1][c.table[r, b]] = 2.0 ** (b // 8 * 3 % 16 - 12)
+    rows = _rows(rng, sum(q), g * hkv).cuda()
+    kp, vp, ks, vs = c.gpu()
+    args = (rows, kp, vp, ks, vs, i32(c.table), i32(c.lens), i32(_qsl(q)), 0.09)
+    got = pkv.pkv_attention_fp8_block(*args)
+    torch.cuda.synchronize()
+    assert pkv.pkv_get_device_error() == 0, pkv.pkv_last_error()
+    for r in (0, 7, 39):  # compared request by request
+        one = Cache.__new__(Cache)
+        one.pools, one.scales, one.table, one.lens = c.pools, c.scales, c.table[r:r + 1], lens[r:r + 1]
+        s = _qsl(q)
+        want, bound = ref.attention(rows[s[r]:s[r + 1]].double().cpu().numpy(), one.pools, one.scales, one.table,
+                                    one.lens, [0, q[r]], 0.09)
+        assert (np.abs(got[s[r]:s[r + 1]].double().cpu().numpy() - want) <= bound).all(), r
+    again = pkv.pkv_attention_fp8_block(*args)
+    assert torch.equal(again.view(torch.int16), got.view(torch.int16))
+
+
 @pytest.mark.parametrize("q", [[1, 1, 1], [30, 90, 20]])
 @pytest.mark.parametrize("spread", [6.0, 12.0])
 def test_attention_scales_far_apart(q, spread):

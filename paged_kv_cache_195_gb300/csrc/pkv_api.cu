@@ -630,6 +630,38 @@ int attention_impl(const void* q, const void* k_pool, const void* v_pool, const 
   const bool grid_forced = opt.decode_grid > 0 && 2 * opt.decode_grid <= w.num_slots;
   const int half_grid_blocks = small || grid_forced ? 0 : (int)kHalfGridBlocks;
   if (block_scales) {
+    // The prefill first: the decode's CTAs fill the SMs that have no work item
+    // of it, or have finished theirs.
+    if (do_prefill) {
+      pkv::PrefillBlockLaunch L{};
+      rc = encode_q_map(&L.qmap, q, dims, group, pkv::prefill_tokens_per_tile(group));
+      if (rc == PKV_OK) rc = encode_pool_map_e4m3(&L.kmap, k_pool, dims);
+      if (rc == PKV_OK) rc = encode_pool_map_e4m3(&L.vmap, v_pool, dims);
+      if (rc != PKV_OK) return rc;
+      L.p.k_scales = k_scale;
+      L.p.v_scales = v_scale;
+      L.p.early_plan = p.early_plan;
+      pkv::PrefillParams& f = L.p.p;
+      f.block_tables = block_tables;
+      f.seq_lens = seq_lens;
+      f.qsl = query_start_loc;
+      f.out = p.out;
+      f.err = st->err;
+      f.num_reqs = dims->num_reqs;
+      f.num_q_tokens = dims->num_q_tokens;
+      f.num_q_heads = dims->num_q_heads;
+      f.num_kv_heads = dims->num_kv_heads;
+      f.num_blocks = dims->num_blocks;
+      f.max_blocks = dims->max_blocks_per_req;
+      f.scale_log2 = p.scale_log2;
+      f.prefill_min_q = prefill_min_q;
+      f.pdl = p.pdl;
+      f.sched = reinterpret_cast<unsigned long long*>(ws + w.sched_off);
+      f.wait_limit_ns = p.wait_limit_ns;
+      L.grid = st->sm_count;
+      e = pkv::launch_prefill_block(L, group, stream);
+      if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
+    }
     pkv::DecodeBlockLaunch B{};
     rc = encode_pool_map_e4m3(&B.kmap, k_pool, dims);
     if (rc == PKV_OK) rc = encode_pool_map_e4m3(&B.vmap, v_pool, dims);
@@ -637,6 +669,7 @@ int attention_impl(const void* q, const void* k_pool, const void* v_pool, const 
     B.p = p;
     B.grid = grid_forced ? opt.decode_grid : tc_grid;
     B.p.half_grid_blocks = half_grid_blocks;
+    B.after_prefill = do_prefill;
     e = pkv::launch_decode_block(B, group, stream);
   } else if (use_tc) {
     pkv::DecodeTcLaunch T{};
@@ -654,35 +687,7 @@ int attention_impl(const void* q, const void* k_pool, const void* v_pool, const 
     e = pkv::launch_decode(p, group, grid, stream);
   }
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
-  if (do_prefill && block_scales) {
-    pkv::PrefillBlockLaunch L{};
-    rc = encode_q_map(&L.qmap, q, dims, group, pkv::prefill_tokens_per_tile(group));
-    if (rc == PKV_OK) rc = encode_pool_map_e4m3(&L.kmap, k_pool, dims);
-    if (rc == PKV_OK) rc = encode_pool_map_e4m3(&L.vmap, v_pool, dims);
-    if (rc != PKV_OK) return rc;
-    L.p.k_scales = k_scale;
-    L.p.v_scales = v_scale;
-    pkv::PrefillParams& f = L.p.p;
-    f.block_tables = block_tables;
-    f.seq_lens = seq_lens;
-    f.qsl = query_start_loc;
-    f.out = p.out;
-    f.err = st->err;
-    f.num_reqs = dims->num_reqs;
-    f.num_q_tokens = dims->num_q_tokens;
-    f.num_q_heads = dims->num_q_heads;
-    f.num_kv_heads = dims->num_kv_heads;
-    f.num_blocks = dims->num_blocks;
-    f.max_blocks = dims->max_blocks_per_req;
-    f.scale_log2 = p.scale_log2;
-    f.prefill_min_q = prefill_min_q;
-    f.pdl = p.pdl;
-    f.sched = reinterpret_cast<unsigned long long*>(ws + w.sched_off);
-    f.wait_limit_ns = p.wait_limit_ns;
-    L.grid = st->sm_count;
-    e = pkv::launch_prefill_block(L, group, stream);
-    if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
-  } else if (do_prefill) {
+  if (do_prefill && !block_scales) {
     pkv::PrefillLaunch L{};
     rc = encode_q_map(&L.qmap, q, dims, group, pkv::prefill_tokens_per_tile(group));
     if (rc == PKV_OK) rc = encode_pool_map(&L.kmap, k_pool, dims);

@@ -184,7 +184,8 @@ static __device__ __noinline__ void merge_row(const float* ws_ml, const float* w
 template <int G>
 __global__ void __launch_bounds__(kThreads, 2)
     decode_block_kernel(const __grid_constant__ CUtensorMap kmap,
-                        const __grid_constant__ CUtensorMap vmap, const DecodeParams p) {
+                        const __grid_constant__ CUtensorMap vmap, const DecodeParams p,
+                        const int after_prefill) {
   static_assert(G >= 1 && G <= 8, "group size");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -213,11 +214,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     ent_n0 = have_n ? raw_entries(pn, 0) : kPastPiece;
     ent_n1 = have_n && pn.nblk > kWindow ? raw_entries(pn, kWindow) : kPastPiece;
   };
+  // Waits for the kernel ahead, once per warp (see DecodeBlockLaunch).
+  auto launch_wait = [&]() {
+    if (!after_prefill) grid_dependency_wait();
+    allow_dependent_launch();
+  };
   if (warp == kWarpProd) {
-    if (!p.early_plan) {
-      grid_dependency_wait();
-      allow_dependent_launch();
-    }
+    if (!p.early_plan) launch_wait();
     plan::plan_cta(p, lane, rg, wk);
     have_n = true;
     #pragma unroll 1
@@ -227,8 +230,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   __syncthreads();
   if (sm.idle) {  // no work: leave, but not before the kernel ahead
-    grid_dependency_wait();
-    allow_dependent_launch();
+    launch_wait();
+    if (blockIdx.x == 0) grid_dependency_wait();
     return;
   }
 
@@ -271,10 +274,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
-  if (warp != kWarpProd || p.early_plan) {
-    grid_dependency_wait();
-    allow_dependent_launch();
-  }
+  if (warp != kWarpProd || p.early_plan) launch_wait();
 
   if (warp == kWarpProd) {
     // ========================= plan + copies ===============================
@@ -651,6 +651,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   tc_fence_after();
   if (warp == kWarpMma) tmem_dealloc(tmem, kTmemCols);
+  if (blockIdx.x == 0) grid_dependency_wait();  // (returns at once unless after_prefill)
 }
 
 static_assert(sizeof(BkSmem) + 1024 <= (228 * 1024) / 2 - 1024, "two CTAs per SM");
@@ -682,7 +683,8 @@ cudaError_t launch_g(const DecodeBlockLaunch& L, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = L.p.pdl ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, decode_block_kernel<G>, L.kmap, L.vmap, L.p);
+  e = cudaLaunchKernelEx(&cfg, decode_block_kernel<G>, L.kmap, L.vmap, L.p,
+                         L.after_prefill);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

@@ -151,6 +151,11 @@ struct DecodeBlockLaunch {
   CUtensorMap vmap;
   DecodeParams p;         // k_scale / v_scale: [num_blocks, Hkv]
   int grid;
+  // The prefill kernel of the same call was launched just before.  It waited
+  // for its own predecessor before letting this kernel launch and writes
+  // nothing that this one reads or writes, so this kernel waits for it only
+  // at its end (one CTA, so that the grid never completes first).
+  int after_prefill;
 };
 
 cudaError_t launch_decode_block(const DecodeBlockLaunch& L, int group, cudaStream_t stream);
@@ -316,6 +321,7 @@ struct PrefillBlockParams {
   PrefillParams p;
   const float* k_scales;  // [num_blocks, Hkv]
   const float* v_scales;
+  int early_plan;         // read seq_lens / query_start_loc before the PDL wait
 };
 
 struct PrefillBlockLaunch {

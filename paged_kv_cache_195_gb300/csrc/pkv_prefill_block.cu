@@ -275,11 +275,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int Hkv = p.num_kv_heads;
 
-  // Ordering.  The decode kernel launched just before this one in the same
-  // call lets it start early; everything read here was complete before the
-  // decode kernel signalled, and that kernel writes only decode rows of
-  // `out`.  The wait at the end makes this grid finish after the decode grid.
-  //
+  // Ordering.  This is the call's first kernel: it waits for the kernel ahead
+  // (before reading the lengths, unless early_plan says that they are not that
+  // kernel's to write) and only then lets the decode kernel launch, which
+  // reads nothing that this one writes and takes the SMs that have no item
+  // here, or no longer.
+  if (!pb.early_plan) grid_dependency_wait();
   // CTAs without an item leave before any set-up.
   if (warp == 0) {
     long long total = 0;
@@ -295,8 +296,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   const int n_active = sm.n_active;  // CTAs that take items
   if ((int)blockIdx.x >= n_active) {
-    allow_dependent_launch();
     grid_dependency_wait();
+    allow_dependent_launch();
     return;
   }
 
@@ -353,6 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
+  grid_dependency_wait();
   allow_dependent_launch();
 
   // Item n of this CTA from the ring; every warp that reads it releases it.
@@ -822,7 +824,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == kWarpMma) tmem_dealloc(tmem, kTmemCols);
-  grid_dependency_wait();
   // The last CTA to finish empties the work queue for the next launch.
   if (tid == 0) {
     __threadfence();

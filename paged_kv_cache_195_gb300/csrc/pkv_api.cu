@@ -118,6 +118,8 @@ int check_step_dims(const pkv_dims* d) {
     return fail(PKV_ERR_INVALID, "negative dims");
   if (d->num_reqs > pkv::kMaxReqs)
     return fail(PKV_ERR_UNSUPPORTED, "num_reqs %d beyond %d", d->num_reqs, pkv::kMaxReqs);
+  if (d->num_q_tokens > (1 << 30))
+    return fail(PKV_ERR_UNSUPPORTED, "num_q_tokens %d beyond 2^30", d->num_q_tokens);
   if ((long long)d->max_blocks_per_req * pkv::kBlockSize > (1ll << 30))
     return fail(PKV_ERR_UNSUPPORTED, "max_blocks_per_req too large");
   return PKV_OK;

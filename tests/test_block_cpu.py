@@ -120,6 +120,11 @@ def test_bad_dims(lib, name, kw, code):
     assert lib.pkv_last_error().decode()
 
 
+@pytest.mark.parametrize("name", NAMES[:3])
+def test_too_many_token_rows(lib, name):
+    assert _call(lib, name, _dims(num_q_tokens=(1 << 30) + 1)) == b.PKV_ERR_UNSUPPORTED
+
+
 @pytest.mark.parametrize("name", ["pkv_append_fp8_block", "pkv_attention_fp8_block"])
 @pytest.mark.parametrize("kw,code", [(dict(head_dim=64), b.PKV_ERR_UNSUPPORTED),
                                      (dict(num_kv_heads=0), b.PKV_ERR_INVALID)])

@@ -664,20 +664,22 @@ def test_serving_loop(graph):
     assert pkv.pkv_get_device_error() == 0
 
 
-def test_attention_right_after_build_reads_the_new_tables():
+@pytest.mark.parametrize("new,steps", [(1, 60), (20, 8)])
+def test_attention_right_after_build_reads_the_new_tables(new, steps):
     # No append between: the lengths and tables come from the kernel issued
-    # just before the attention, step after step on the same buffers.
+    # just before the attention (decode rows; prefill chunks), step after step
+    # on the same buffers.
     rng = np.random.default_rng(21)
-    loop = Loop(R=70, cols=6, nb=70 * 6, cap=70, hq=12, hkv=2)
+    R, cols = 30, -(-new * steps // BS)
+    loop = Loop(R=R, cols=cols, nb=R * cols, cap=R * new, hq=12, hkv=2)
     for p in loop.pools:
         p.copy_(dev(ref.encode(rng.normal(0, 100, tuple(p.shape)))))
     for s in loop.scales:
         s.fill_(2.0 ** -7)
-    lens = [np.full(70, 1)]
-    loop.q.copy_(_rows(rng, 70, 12))
-    loop.new.fill_(1)
+    loop.q.copy_(_rows(rng, R * new, 12))
+    loop.new.fill_(new)
     outs = []
-    for i in range(60):
+    for i in range(steps):
         pkv.pkv_build_step(loop.lens, loop.new, loop.free, loop.nfree, loop.table, loop.lens, loop.qsl, loop.slots)
         outs.append(pkv.pkv_attention_fp8_block(loop.q, *loop.pools, *loop.scales, loop.table, loop.lens, loop.qsl,
                                                 0.09, workspace=loop.ws))
@@ -685,6 +687,7 @@ def test_attention_right_after_build_reads_the_new_tables():
     table = loop.table.cpu().numpy()
     f = lambda t: t.double().cpu().numpy()  # noqa: E731
     pools, scales = [p.cpu().numpy() for p in loop.pools], [s.cpu().numpy() for s in loop.scales]
-    for i in (0, 1, 15, 16, 17, 40, 59):
-        want, bound = ref.attention(f(loop.q), pools, scales, table, [i + 1] * 70, _qsl([1] * 70), 0.09)
+    for i in sorted({0, 1, steps // 4, steps // 2, steps - 1}):
+        want, bound = ref.attention(f(loop.q), pools, scales, table, [new * (i + 1)] * R, _qsl([new] * R), 0.09)
         assert (np.abs(f(outs[i]) - want) <= bound).all(), i
+    assert pkv.pkv_get_device_error() == 0

@@ -97,16 +97,36 @@ struct __align__(1024) BkSmem {
   int idle;
 };
 
+// Largest value of a warp (NaN skipped), one instruction.
 __device__ __forceinline__ float warp_max(float v) {
-  #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Warp sums of G values: value h's sum comes back in the lanes with
+// sum_index(lane) == h.  Three halving exchanges spread the (padded) eight
+// values over the lanes, two more add up: 9 shuffles for 5 G.
+__device__ __forceinline__ int sum_index(int lane) {
+  return (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1);
+}
+
+template <int G>
+__device__ __forceinline__ float warp_sums(const float (&v)[G], int lane) {
+  float a[8];
   #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int h = 0; h < 8; ++h) a[h] = h < G ? v[h < G ? h : 0] : 0.f;
+  #pragma unroll
+  for (int n = 4, o = 16; n > 0; n >>= 1, o >>= 1) {
+    const bool up = lane & o;
+    #pragma unroll
+    for (int h = 0; h < n; ++h) {
+      const float keep = up ? a[n + h] : a[h], send = up ? a[h] : a[n + h];
+      a[h] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+  a[0] += __shfl_xor_sync(0xffffffffu, a[0], 2);
+  return a[0] + __shfl_xor_sync(0xffffffffu, a[0], 1);
 }
 
 // Two fp32 to two e4m3 codes (the first in the low byte): nearest even,
@@ -156,24 +176,33 @@ static __device__ __noinline__ void merge_row(const float* ws_ml, const float* w
     M[h] = kNegBig;
     num[h] = den[h] = 0.f;
   }
+  // Two pieces' loads in flight at a time (the second repeats the last one
+  // when S is odd, and is dropped).
   #pragma unroll 1
-  for (int s = 0; s < S; ++s) {
-    const int slot = 2 * (c0 + s) + ((s == 0 && odd0) ? 1 : 0);
-    float2 ml[G];
-    float o[G];
+  for (int s = 0; s < S; s += 2) {
+    float2 ml[2][G];
+    float o[2][G];
     #pragma unroll
-    for (int h = 0; h < G; ++h) {
-      const long long x = (long long)slot * G + h;
-      ml[h] = __ldcg(reinterpret_cast<const float2*>(ws_ml + x * 2));
-      o[h] = __ldcg(ws_o + x * kHeadDim + d);
+    for (int u = 0; u < 2; ++u) {
+      const int x = min(s + u, S - 1), slot = 2 * (c0 + x) + ((x == 0 && odd0) ? 1 : 0);
+      #pragma unroll
+      for (int h = 0; h < G; ++h) {
+        const long long at = (long long)slot * G + h;
+        ml[u][h] = __ldcg(reinterpret_cast<const float2*>(ws_ml + at * 2));
+        o[u][h] = __ldcg(ws_o + at * kHeadDim + d);
+      }
     }
     #pragma unroll
-    for (int h = 0; h < G; ++h) {
-      const float Mn = fmaxf(M[h], ml[h].x);
-      const float a = fast_exp2(M[h] - Mn), w = fast_exp2(ml[h].x - Mn) * ml[h].y;
-      num[h] = num[h] * a + w * o[h];
-      den[h] = den[h] * a + w;
-      M[h] = Mn;
+    for (int u = 0; u < 2; ++u) {
+      if (s + u >= S) break;
+      #pragma unroll
+      for (int h = 0; h < G; ++h) {
+        const float Mn = fmaxf(M[h], ml[u][h].x);
+        const float a = fast_exp2(M[h] - Mn), w = fast_exp2(ml[u][h].x - Mn) * ml[u][h].y;
+        num[h] = num[h] * a + w * o[u][h];
+        den[h] = den[h] * a + w;
+        M[h] = Mn;
+      }
     }
   }
   #pragma unroll
@@ -210,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     have = have_n;
     ent_w0 = ent_n0;
     ent_w1 = ent_n1;
-    have_n = have && wk.next(p, pn);
+    have_n = have && wk.next<true>(p, pn);
     ent_n0 = have_n ? raw_entries(pn, 0) : kPastPiece;
     ent_n1 = have_n && pn.nblk > kWindow ? raw_entries(pn, kWindow) : kPastPiece;
   };
@@ -221,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
   if (warp == kWarpProd) {
     if (!p.early_plan) launch_wait();
-    plan::plan_cta(p, lane, rg, wk);
+    plan::plan_cta<true>(p, lane, rg, wk);
     have_n = true;
     #pragma unroll 1
     for (int i = 0; i < 2; ++i) advance();
@@ -274,6 +303,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
+  if (warp == kWarpProd && lane == 0) {  // the first piece, for the q warp
+    sm.pinfo[0] = pc;
+    mbar_arrive(&sm.pc_full[0]);
+  }
   if (warp != kWarpProd || p.early_plan) launch_wait();
 
   if (warp == kWarpProd) {
@@ -290,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       // The piece's buffers are free once the MMAs of piece j - 2 are done.
       const int ub = j & 1;
       if (j >= 2 && !mbar_wait(&sm.q_empty[ub], ((j >> 1) - 1) & 1, p.err, abort_flag)) break;
-      if (lane == 0) {
+      if (lane == 0 && j > 0) {
         sm.pinfo[ub] = pc;
         mbar_arrive(&sm.pc_full[ub]);
       }
@@ -445,11 +478,14 @@ __global__ void __launch_bounds__(kThreads, 2)
         // are undefined).
         const int e = max((int)(top >> 7), 1);  // biased
         const bool finite = e < 255;
-        // 2^(134 - e biased): within fp32 for e <= 253 as 2^-119 .. 2^133, so
-        // in two factors.
-        const float s1 = finite ? __uint_as_float((uint32_t)(127 + (134 - e) / 2) << 23)
+        // 2^(134 - e), e biased: 2^-120 .. 2^133, so in two factors; b1 and b2
+        // are their inverses.
+        const int x1 = (134 - e) / 2, x2 = 134 - e - x1;
+        const float s1 = finite ? __uint_as_float((uint32_t)(127 + x1) << 23)
                                 : __int_as_float(0x7fc00000);
-        const float s2 = __uint_as_float((uint32_t)(127 + (134 - e) - (134 - e) / 2) << 23);
+        const float s2 = __uint_as_float((uint32_t)(127 + x2) << 23);
+        const float b1 = finite ? __uint_as_float((uint32_t)(127 - x1) << 23) : s1;
+        const float b2 = __uint_as_float((uint32_t)(127 - x2) << 23);
         const float2 u = bf16x2_to_float2(x[h].x), v = bf16x2_to_float2(x[h].y);
         uint32_t h0, l0, h1, l1;
         split_pair(u.x * s1 * s2, u.y * s1 * s2, h0, l0);
@@ -457,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int at = h * 128 + (((lane >> 2) ^ h) * 16) + (lane & 3) * 4;
         *reinterpret_cast<uint32_t*>(sm.q[ub][0] + at) = h0 | h1 << 16;
         *reinterpret_cast<uint32_t*>(sm.q[ub][1] + at) = l0 | l1 << 16;
-        if (lane == 0) sm.qf[ub][h] = p.scale_log2 / s1 / s2;
+        if (lane == 0) sm.qf[ub][h] = p.scale_log2 * b1 * b2;
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -591,11 +627,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (lane == 0) mbar_arrive(&sm.p_full[b]);
       }
       // ============ epilogue of the piece (same four warps) ================
-      #pragma unroll
-      for (int h = 0; h < G; ++h) {
-        const float sw = warp_sum(l[h]);
-        if (lane == 0) sm.st_l[warp][h] = sw;
-      }
+      const float sw = warp_sums<G>(l, lane);
+      if ((lane & 3) == 0) sm.st_l[warp][sum_index(lane)] = sw;
       named_barrier(kBarSoftmax, kSoftThreads);
       const bool okO = ok && mbar_wait(&sm.o_full[ub], (j >> 1) & 1, p.err, abort_flag);
       tc_fence_after();

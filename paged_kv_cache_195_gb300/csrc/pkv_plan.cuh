@@ -100,6 +100,8 @@ __device__ __forceinline__ long long rows_weight(const DecodeParams& p, const Re
 // range length (chunk) every CTA uses.  Warp-collective.
 struct Range {
   long long lo, hi, chunk;
+  long long total;  // the step's weighted blocks
+  int ctas;         // CTAs that take a share
 };
 
 // Adds request r's row-groups to this lane's running totals (its blocks over
@@ -145,6 +147,8 @@ __device__ __forceinline__ Range finish_range(const DecodeParams& p, long long m
   }
   Range rg;
   rg.chunk = chunk;
+  rg.total = W;
+  rg.ctas = ctas;
   rg.lo = (long long)blockIdx.x * chunk;
   rg.hi = min(W, rg.lo + chunk);
   return rg;
@@ -185,6 +189,8 @@ struct Walker {
   int r, i, k, nb;
   ReqInfo ri;
   bool done;
+  int own_s, own_c0;  // own pieces (plan_cta<true>): pieces of the row-group, 0 otherwise;
+                      // CTA of its first
 
   // Finds the request and row that hold block lo (a warp-wide scan).
   __device__ __forceinline__ void start(const DecodeParams& p, const Range& range, int lane) {
@@ -251,6 +257,7 @@ struct Walker {
   // exhausted.  A row-group's real blocks are [g, g + nb - rowgroup_cost) of
   // its weighted extent [g, g + nb); a range that meets only the rest of it
   // has no piece of that row-group.
+  template <bool kOwn = false>
   __device__ __forceinline__ bool next(const DecodeParams& p, Piece& pc) {
     while (!done) {
       const long long nbr = nb - p.rowgroup_cost;  // real blocks
@@ -272,10 +279,17 @@ struct Walker {
         pc.c0 = (int)c0;
         pc.odd0 = g != c0 * rg.chunk;
         pc.slot = 2 * (int)blockIdx.x + (s0 == rg.lo ? 0 : 1);
+        if (kOwn && own_s > 0) {
+          pc.S = own_s;
+          pc.c0 = own_c0;
+          pc.odd0 = 0;
+        }
       }
       // advance to the next row-group
       g += nb;
-      if (++k == p.num_kv_heads) {
+      if (g >= rg.hi) {
+        done = true;
+      } else if (++k == p.num_kv_heads) {
         k = 0;
         if (++i == ri.qr) {
           i = 0;
@@ -288,7 +302,6 @@ struct Walker {
         }
         if (!done) nb = row_weight(p, ri, i);
       }
-      if (g >= rg.hi) done = true;
       if (emit) return true;
     }
     return false;
@@ -299,6 +312,7 @@ struct Walker {
 // 32 * kPlanRegReqs requests are planned from one batch of loads.
 constexpr int kPlanRegReqs = 8;
 static_assert(32 * kPlanRegReqs <= kPlanCacheReqs, "plan cache too small");
+constexpr int kOwnMinBlocks = 16;  // own pieces are no shorter
 
 // Plan cache entry (one per CTA index, int32 words): the inputs the plan was
 // computed from -- a header of sizes and tuning values, query_start_loc and
@@ -306,11 +320,12 @@ static_assert(32 * kPlanRegReqs <= kPlanCacheReqs, "plan cache too small");
 // engine step has the same lengths, so a CTA computes its plan once per step
 // and later calls compare and reuse it; the comparison is exact, so a reused
 // plan is always the plan of the current lengths.
-constexpr int kPcHeader = 11, kPcQsl = 16, kPcLens = kPcQsl + kPlanCacheReqs + 4,
-              kPcState = kPcLens + kPlanCacheReqs, kPcStateWords = 18;
+constexpr int kPcHeader = 12, kPcQsl = 16, kPcLens = kPcQsl + kPlanCacheReqs + 4,
+              kPcState = kPcLens + kPlanCacheReqs, kPcStateWords = 20;
 static_assert(kPcState + kPcStateWords <= kPlanEntryWords, "plan cache entry layout");
 constexpr int kPcMagic = 0x504c414e;
 
+template <bool kOwn>
 __device__ __forceinline__ int plan_header_word(const DecodeParams& p, int j) {
   switch (j) {
     case 0: return p.num_reqs;
@@ -323,6 +338,7 @@ __device__ __forceinline__ int plan_header_word(const DecodeParams& p, int j) {
     case 7: return (int)gridDim.x;
     case 8: return p.max_blocks;
     case 9: return p.rowgroup_cost;
+    case 10: return kOwn;
     default: return kPcMagic ^ p.half_grid_blocks;
   }
 }
@@ -333,9 +349,19 @@ __device__ __forceinline__ int plan_header_word(const DecodeParams& p, int j) {
 // together, and each lane takes a contiguous run of requests so that one
 // warp-wide scan finds the request holding the range's first block.
 // Warp-collective.
+//
+// With kOwn a step with at most one row-group per CTA may be cut differently:
+// every row-group of request r into S_r equal pieces of its own, one piece per
+// CTA, where S_r = ceil(blocks / T) for the smallest T that needs no more
+// pieces than there are CTAs.  A CTA then has one epilogue and at most one
+// merge, where an equal share of the whole sequence leaves it the tail of one
+// row-group and the head of the next.  The price is the longest piece; taken
+// when that is at most p.align_slack blocks above the equal share.
+template <bool kOwn = false>
 __device__ __forceinline__ void plan_cta(const DecodeParams& p, int lane, Range& rg,
                                          Walker& wk) {
   const int R = p.num_reqs;
+  wk.own_s = wk.own_c0 = 0;
   if (R > 32 * kPlanRegReqs) {
     rg = cta_range(p, lane);
     wk.start(p, rg, lane);
@@ -370,7 +396,7 @@ __device__ __forceinline__ void plan_cta(const DecodeParams& p, int lane, Range&
     cL[i] = cin ? __ldcg(ce + kPcLens + r) : 0;
   }
   if (ce != nullptr) {
-    bool same = lane >= kPcHeader || ch == plan_header_word(p, lane);
+    bool same = lane >= kPcHeader || ch == plan_header_word<kOwn>(p, lane);
     #pragma unroll
     for (int i = 0; i < kPlanRegReqs; ++i)
       same = same && (i >= per || (a0[i] == c0[i] && a1[i] == c1[i] && aL[i] == cL[i]));
@@ -394,6 +420,8 @@ __device__ __forceinline__ void plan_cta(const DecodeParams& p, int lane, Range&
       wk.ri.L = word(15);
       wk.ri.fb = word(16);
       wk.ri.decode = word(17) != 0;
+      wk.own_s = word(18);
+      wk.own_c0 = word(19);
       return;
     }
   }
@@ -431,8 +459,10 @@ __device__ __forceinline__ void plan_cta(const DecodeParams& p, int lane, Range&
     put(15, wk.ri.L);
     put(16, wk.ri.fb);
     put(17, wk.ri.decode ? 1 : 0);
+    put(18, wk.own_s);
+    put(19, wk.own_c0);
     if (lane < kPcStateWords) __stcg(ce + kPcState + lane, sv);
-    if (lane < kPcHeader) __stcg(ce + lane, plan_header_word(p, lane));
+    if (lane < kPcHeader) __stcg(ce + lane, plan_header_word<kOwn>(p, lane));
     __threadfence();
   };
   long long w[kPlanRegReqs];
@@ -450,6 +480,52 @@ __device__ __forceinline__ void plan_cta(const DecodeParams& p, int lane, Range&
   }
   const long long own_total = mine;
   rg = finish_range(p, mine, nb_min, nb_max);
+  int T = 0;  // own pieces' longest (0: equal shares)
+  int ng[kPlanRegReqs], nf[kPlanRegReqs];  // a request's row-groups; blocks of its first row
+  if (kOwn && p.align && rg.total > 0) {
+    int n = 0;
+    #pragma unroll
+    for (int i = 0; i < kPlanRegReqs; ++i) {
+      ng[i] = nf[i] = 0;
+      if (i < per && w[i] > 0) {
+        const ReqInfo q = make_request(p, a0[i], a1[i], aL[i], aF[i]);
+        ng[i] = (int)min((long long)q.qr * p.num_kv_heads, 1ll << 20);
+        nf[i] = row_blocks(q, 0);
+      }
+      n += ng[i];
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
+    auto pieces = [&](int t) {
+      int c = 0;
+      #pragma unroll
+      for (int i = 0; i < kPlanRegReqs; ++i)
+        if (i < per) c += ng[i] * cdiv(nf[i], t);
+      return __reduce_add_sync(0xffffffffu, c);
+    };
+    const int ctas = n <= rg.ctas ? rg.ctas : (int)gridDim.x;
+    if (n <= ctas) {
+      const long long blocks = rg.total - (long long)n * p.rowgroup_cost;
+      int lo = (int)max(cdiv_ll(blocks, ctas), (long long)max(p.min_chunk, kOwnMinBlocks));
+      int hi = max(lo, (int)(rg.chunk - p.rowgroup_cost + p.align_slack));
+      if (pieces(hi) <= ctas) {
+        while (lo < hi) {
+          const int mid = (lo + hi) / 2;
+          if (pieces(mid) <= ctas) hi = mid; else lo = mid + 1;
+        }
+        T = hi;
+      }
+    }
+  }
+  auto weight = [&](int i) { return kOwn && T > 0 ? (long long)ng[i] * cdiv(nf[i], T) : w[i]; };
+  long long own_sum = own_total;
+  if (kOwn && T > 0) {  // the range below counts pieces, one per CTA
+    own_sum = 0;
+    #pragma unroll
+    for (int i = 0; i < kPlanRegReqs; ++i)
+      if (i < per) own_sum += weight(i);
+    rg.lo = blockIdx.x;
+    rg.hi = min(__reduce_add_sync(0xffffffffu, (int)own_sum), (int)blockIdx.x + 1);
+  }
   wk.rg = rg;
   wk.done = rg.lo >= rg.hi;
   if (wk.done) {
@@ -460,14 +536,14 @@ __device__ __forceinline__ void plan_cta(const DecodeParams& p, int lane, Range&
     return;
   }
   // Blocks of the requests before this lane's run (exclusive scan).
-  long long incl = own_total;
+  long long incl = own_sum;
   #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long t = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += t;
   }
-  const long long base = incl - own_total;
-  const unsigned own = __ballot_sync(0xffffffffu, own_total > 0 && base <= rg.lo && rg.lo < incl);
+  const long long base = incl - own_sum;
+  const unsigned own = __ballot_sync(0xffffffffu, own_sum > 0 && base <= rg.lo && rg.lo < incl);
   if (own == 0) {
     record_error(p.err, kErrBounds);  // unreachable when the lengths are stable
     wk.done = true;
@@ -482,7 +558,8 @@ __device__ __forceinline__ void plan_cta(const DecodeParams& p, int lane, Range&
     bool found = false;
     #pragma unroll
     for (int i = 0; i < kPlanRegReqs; ++i) {
-      if (i < per && !found && w[i] > 0 && rg.lo < acc + w[i]) {
+      const long long wi = weight(i);
+      if (i < per && !found && wi > 0 && rg.lo < acc + wi) {
         found = true;
         fr = r0 + i;
         f0 = a0[i];
@@ -491,7 +568,7 @@ __device__ __forceinline__ void plan_cta(const DecodeParams& p, int lane, Range&
         fF = aF[i];
         pos = acc;
       }
-      acc += w[i];
+      acc += wi;
     }
   }
   fr = __shfl_sync(0xffffffffu, fr, owner);
@@ -501,7 +578,24 @@ __device__ __forceinline__ void plan_cta(const DecodeParams& p, int lane, Range&
   fF = __shfl_sync(0xffffffffu, fF, owner);
   pos = __shfl_sync(0xffffffffu, pos, owner);
   wk.r = fr;
-  wk.finish_start(p, make_request(p, f0, f1, fL, fF), pos);
+  const ReqInfo fi = make_request(p, f0, f1, fL, fF);
+  if (kOwn && T > 0) {
+    // Piece x of the request: row-group x / S in (row, head) order, part x % S.
+    const int S = cdiv(row_blocks(fi, 0), T), x = (int)(rg.lo - pos), part = x % S;
+    wk.ri = fi;
+    wk.i = x / S / p.num_kv_heads;
+    wk.k = x / S % p.num_kv_heads;
+    wk.nb = row_weight(p, fi, wk.i);
+    const long long nb = row_blocks(fi, wk.i);
+    wk.g = 0;
+    rg.lo = nb * part / S;
+    rg.hi = nb * (part + 1) / S;
+    wk.rg = rg;
+    wk.own_s = S;
+    wk.own_c0 = (int)blockIdx.x - part;
+  } else {
+    wk.finish_start(p, fi, pos);
+  }
   record();
 }
 

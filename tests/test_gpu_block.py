@@ -502,6 +502,45 @@ def test_attention_is_deterministic_on_any_stream_and_workspace(q):
         assert torch.equal(o.view(torch.int16), want.view(torch.int16))
 
 
+@pytest.mark.parametrize("R,hkv,lo,hi", [(3, 2, 300, 5000), (40, 2, 1, 2500), (75, 2, 500, 540), (76, 2, 250, 300),
+                                         (77, 2, 1, 300), (101, 3, 100, 140), (152, 2, 1, 600), (153, 2, 1, 200),
+                                         (256, 1, 1, 700), (257, 1, 1, 700), (20, 8, 1, 900)])
+def test_attention_ragged_rows_on_every_side_of_the_grid(R, hkv, lo, hi):
+    # Fewer, as many and more rows (times KV heads) than SMs and than CTAs;
+    # one row a request, then several, on one workspace.
+    rng = np.random.default_rng(R)
+    lens = [int(x) for x in rng.integers(lo, hi + 1, R)]
+    c = Cache(rng, lens, hkv)
+    q = [1] * R
+    few = [min(n, int(x)) for n, x in zip(lens, rng.integers(0, 4, R))]
+    T = max(R, sum(few))
+    rows = _rows(rng, T, 3 * hkv)
+    kp = c.gpu()[0]
+    ws = pkv.Workspace(pkv.make_dims(tuple(rows.shape), tuple(kp.shape), R, c.table.shape[1]))
+    got = [_check(c, q, rows, workspace=ws) for _ in range(2)]
+    _check(c, few, rows, workspace=ws)
+    got.append(_check(c, q, rows, workspace=ws))
+    for o in got[1:]:
+        assert torch.equal(o[:R].view(torch.int16), got[0][:R].view(torch.int16))
+
+
+def test_attention_shares_a_workspace_with_the_other_caches():
+    # The same lengths through two kernels that cut them differently.
+    rng = np.random.default_rng(23)
+    lens = [int(x) for x in rng.integers(200, 900, 50)]
+    c = Cache(rng, lens, 2, zero=0.0)
+    c.pools = [np.where((p & 0x7F) == 0x7F, 0, p).astype(np.uint8) for p in c.pools]
+    rows = _rows(rng, 50, 8)
+    kp, vp = c.gpu()[:2]
+    ws = pkv.Workspace(pkv.make_dims(tuple(rows.shape), tuple(kp.shape), 50, c.table.shape[1]))
+    t, l, s, one = i32(c.table), i32(c.lens), i32(_qsl([1] * 50)), torch.full((2,), 0.01, device="cuda")
+    fp8 = lambda: pkv.pkv_attention_fp8kv(rows.cuda(), kp, vp, one, one, t, l, s, 0.09, workspace=ws)  # noqa: E731
+    first = fp8()
+    for _ in range(2):
+        _check(c, [1] * 50, rows, workspace=ws)
+        assert torch.equal(fp8().view(torch.int16), first.view(torch.int16))
+
+
 @pytest.mark.parametrize("changes", [dict(pdl=0), dict(early_plan=0), dict(plan_cache=0), dict(decode_grid=7),
                                      dict(min_chunk=1, align=0), dict(rowgroup_cost=0), dict(prefill_min_q=0),
                                      dict(prefill_min_q=1)])

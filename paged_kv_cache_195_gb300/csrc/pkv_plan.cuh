@@ -312,7 +312,10 @@ struct Walker {
 // 32 * kPlanRegReqs requests are planned from one batch of loads.
 constexpr int kPlanRegReqs = 8;
 static_assert(32 * kPlanRegReqs <= kPlanCacheReqs, "plan cache too small");
-constexpr int kOwnMinBlocks = 16;  // own pieces are no shorter
+// Own pieces are no shorter than two 128-key tiles: below that the merge costs
+// more than the tile saved (16 requests of 100-1000 keys, two KV heads: 9.55
+// us; a limit of one tile 10.4, of three 9.95).
+constexpr int kOwnMinBlocks = 16;
 
 // Plan cache entry (one per CTA index, int32 words): the inputs the plan was
 // computed from -- a header of sizes and tuning values, query_start_loc and
@@ -356,7 +359,10 @@ __device__ __forceinline__ int plan_header_word(const DecodeParams& p, int j) {
 // pieces than there are CTAs.  A CTA then has one epilogue and at most one
 // merge, where an equal share of the whole sequence leaves it the tail of one
 // row-group and the head of the next.  The price is the longest piece; taken
-// when that is at most p.align_slack blocks above the equal share.
+// when that is at most p.align_slack blocks above the equal share (64 rows of
+// 400-624 keys, two KV heads: 10.5 vs 14.2 us; 58 rows of 33-3001 keys, three
+// KV heads: 16.2 vs 17.5).  More row-groups than the half grid but not than
+// the whole one take the whole grid.
 template <bool kOwn = false>
 __device__ __forceinline__ void plan_cta(const DecodeParams& p, int lane, Range& rg,
                                          Walker& wk) {

@@ -459,11 +459,13 @@ typedef struct pkv_options {
     int32_t decode_tc_fp8;  /* PKV_DECODE_TC_FP8 (1): the same for e4m3 pools */
     int32_t prefill_min_q;  /* PKV_PREFILL_MIN_Q (16): requests with at least this many
                                query tokens run in the tensor-core prefill kernel
-                               (0: none do); bf16 pools only */
+                               (0: none do); bf16 and block-scaled e4m3 pools */
     int32_t align;          /* PKV_ALIGN (1): with uniform row-groups, snap decode ranges
-                               to row-group boundaries ... */
-    int32_t align_slack;    /* PKV_ALIGN_SLACK (64): ... when that lengthens every range
-                               by at most this many blocks */
+                               to row-group boundaries (block-scaled e4m3 pools: with
+                               no more row-groups than CTAs, cut each into pieces of its
+                               own) ... */
+    int32_t align_slack;    /* PKV_ALIGN_SLACK (64): ... when that lengthens the longest
+                               range by at most this many blocks */
     int32_t min_chunk;      /* PKV_MIN_CHUNK (4): smallest decode range per CTA, in
                                blocks (>= 1) */
     int32_t decode_grid;    /* PKV_DECODE_GRID (0): decode grid in CTAs (0: the

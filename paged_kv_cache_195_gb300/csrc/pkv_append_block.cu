@@ -25,7 +25,10 @@
 // 1024); units past the request's last block leave.
 //
 // Bound: HBM for prefill chunks (512 bytes read and 256 written per token and
-// head, K and V); four dependent loads for a decode step.
+// head, K and V); four dependent loads for a decode step.  Measured: eight
+// chunks of 512 tokens, eight KV heads, 8.1 us = 3.1 TB/s (0.46 of the measured
+// copy rate: a launch and its four loads are 4 us of it); 64 decode tokens, two
+// KV heads, 4.1 us.
 #include "pkv_internal.h"
 
 namespace pkv {

@@ -37,6 +37,14 @@
 // decode kernels (pkv_plan.cuh); rows of every request the caller leaves to
 // this kernel, any group size 1..8.
 //
+// Bound: HBM for long steps, the chain of latencies (plan, table, tile, S,
+// softmax, PV, merge) for short ones; the tensor pipe is busy 2.5% of the time.
+// Measured, e4m3 codes and scales read over time: 128 rows x 2048 keys, two KV
+// heads, 26.3 us = 5.1 TB/s (0.76 of the measured copy rate, launch included;
+// the kernel for one scale per head, which widens the codes, 30.4 us); 8 rows x
+// 32768 keys, eight KV heads, 86.8 us = 6.2 TB/s (0.91); 64 rows x 512 keys, two
+// KV heads, 9.2 us; four rows of up to 128 keys, 4.9 us.
+//
 // Roles (224 threads, two CTAs per SM): warps 0-3 softmax and epilogue, one
 // key (TMEM lane) per thread; warp 4 plans and issues the copies -- K and V
 // tiles by TMA into a ring of six 16 KiB slots, the sixteen scales of a tile

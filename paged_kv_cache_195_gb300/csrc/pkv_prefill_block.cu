@@ -24,25 +24,34 @@
 // is at most 2^15, mo being a running maximum of s + lv next to the running
 // maximum m of s that the normaliser uses; both are raised when exceeded by
 // more than 2^8.  So P is precise where it weighs, however far apart the
-// blocks' scales are, and F is one factor per row and block.  (Widening V to
-// bf16 with its scale multiplied in needs no F but twelve instructions where
-// two do: 182 against 150 us on eight 512-token chunks.)
+// blocks' scales are, and F is one factor per row and block.  (bf16 for V, its
+// scale multiplied in while widening, needs no F but six instructions a pair of
+// codes where one does, and would leave the probabilities eight bits for f16's
+// eleven.)
 //
 // Roles (640 threads): warps 0-15 softmax and epilogue, four threads per MMA
 // row (warps with the same index mod 4 hold the same 32 rows); warp 16 takes
 // items from the work queue and copies Q, K and V tiles and the scales; 17
 // issues the MMAs; 18 and 19 widen V.  Items travel through a four-entry ring
 // that every role reads, published a few tiles before the previous item ends,
-// with its Q on the way; before an item's last probabilities the softmax warps
-// split the next one's Q (in place: a row's 256 bytes of bf16 become its 128 of
-// hi and 128 of lo), so that its first S is there after them.
+// with its Q on the way; when an item's last probabilities are out the softmax
+// warps split the next one's Q (in place: a row's 256 bytes of bf16 become its
+// 128 of hi and 128 of lo) and write the item's output while its first S runs.
+// The MMA warp issues an item's last PVs before it waits for the next item's Q:
+// the softmax may be waiting for one of them to rescale O, and splits that Q
+// only afterwards.
 //
-// Bound: the softmax's instruction issue and latencies (the tensor pipe's
-// share of a tile is about 1150 cycles: the S MMAs read 8 KB of shared memory
-// each at 128 bytes a clock).  Hence the pipeline inside each softmax warp: the
-// scores of tile t + 1 are fetched from TMEM, half a tile at a time into the
-// registers that the exponentials of tile t have freed, and P has TMEM columns
-// of its own, so that a score buffer is free as soon as it is read.
+// Bound: the softmax, about 3000 cycles for a tile of 128 x 128 scores of which
+// the tensor pipe is busy a third (16 MMAs of 64 cycles) and the exponentials
+// take 1000; the rest is issue slots (57% used) and the latencies between a
+// tile's scores, maxima and probabilities.  Hence the pipeline inside each
+// softmax warp: the scores of tile t + 1 are fetched from TMEM, half a tile at a
+// time into the registers that the exponentials of tile t have freed, and P has
+// TMEM columns of its own, so that a score buffer is free as soon as it is read.
+//
+// Measured: eight 512-token chunks after prefixes of up to 4096 tokens, 32 query
+// and 8 KV heads: 145 us = 740 TFLOP/s of the 2 x 2 x 128 flops per visible key
+// and query head, 0.39 of cuBLAS's bf16 rate (the bf16 prefill kernel: 129 us).
 #include <climits>
 
 #include "pkv_internal.h"
@@ -214,8 +223,9 @@ __device__ __forceinline__ void split_scale(float vs, float& lv, float& r) {
 // The softmax warps split an item's Q in place: q holds its two 64-dim halves
 // in bf16 and gets the hi and the lo operand; qf gets the rows' factors of the
 // raw scores, bar every warp's arrival.  Warp w takes rows 8w .. 8w + 7, four
-// threads a row, 32 dims each.  Out of line: once per item, and inlined it
-// cost the tile loop registers.
+// threads a row, 32 dims each.  (Out of line it costs more than the registers
+// that it would spare the tile loop: 151 against 146.5 us on eight 512-token
+// chunks.)
 static __device__ __forceinline__ void split_q(uint8_t* q, float scale_log2, float* qf, uint64_t* bar) {
   const int r = threadIdx.x >> 2, c = threadIdx.x & 3, sw = r & 7;
   q += r * 128;
@@ -522,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Tile t: S(t) into S buffer t & 1, then O += P(t-2) V(t-2).  An S buffer
     // is free as soon as the softmax has taken its scores, well before it sends
     // their P, so S runs ahead of PV by two tiles: with S(t) behind PV(t-1) the
-    // softmax waited for it (3500 cycles a tile).
+    // softmax waited for it (3500 cycles a tile against 3000).
     constexpr uint32_t kIdescS = idesc_e4m3_f32(kRows, kKeyTile, 0, 0);
     constexpr uint32_t kIdescO = idesc_f16_f32(kRows, kHeadDim, 0, 1);
     // Descriptors of the operands' first chunks: a chunk of 32 bytes of a row

@@ -26,7 +26,9 @@
 // thousand of them.
 //
 // Bound: latency.  The bytes (16 per request, 8 per token, 8 per block) are
-// far below what a launch costs.
+// far below what a launch costs.  Measured: build 4.1 us for 64 decodes, 11.1
+// for 4096 requests with 42 thousand tokens (two launches); release 2.8 us for
+// 64 requests, 8.8 for 4096.
 #include <climits>
 
 #include "pkv_internal.h"

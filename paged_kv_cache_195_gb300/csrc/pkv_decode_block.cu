@@ -218,10 +218,114 @@ static __device__ __noinline__ void merge_row(const float* ws_ml, const float* w
     out[h * kHeadDim] = __float2bfloat16_rn(den[h] == 0.f ? 0.f : num[h] / den[h]);
 }
 
+// The plan of a step with more requests than plan_cta keeps in registers, by
+// the whole CTA: every thread sums a contiguous run of requests, the producer
+// warp scans the run sums, and only the run that holds the range's first block
+// is read again.  (One warp reading all requests twice, 32 at a time, takes
+// 0.8 us for every 32 of them.)
+struct RunSums {
+  long long w[kThreads];
+  int nb_min[kThreads / 32], nb_max[kThreads / 32];
+  plan::Walker at;  // the result
+};
+
+static __device__ plan::Walker find_start(const DecodeParams& p, const RunSums& rs, int per) {
+  const int lane = threadIdx.x & 31;
+  plan::Walker wk{};
+  constexpr int kRuns = kThreads / 32;  // a lane's runs: lane * kRuns ..
+  long long part = 0;
+  #pragma unroll
+  for (int i = 0; i < kRuns; ++i) part += rs.w[lane * kRuns + i];
+  const plan::Range rg = plan::finish_range(p, part, rs.nb_min[min(lane, kRuns - 1)],
+                                            rs.nb_max[min(lane, kRuns - 1)]);
+  wk.rg = rg;
+  wk.done = rg.lo >= rg.hi;
+  if (wk.done) return wk;
+  long long incl = part;
+  #pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  long long pos = incl - part;
+  const unsigned own = __ballot_sync(0xffffffffu, pos <= rg.lo && rg.lo < incl);
+  if (own == 0) {
+    record_error(p.err, kErrBounds);  // unreachable when the lengths are stable
+    wk.done = true;
+    return wk;
+  }
+  int run = 0;
+  const int src = __ffs(own) - 1;
+  if (lane == src) {
+    run = lane * kRuns;
+    #pragma unroll 1
+    while (pos + rs.w[run] <= rg.lo) pos += rs.w[run++];
+  }
+  run = __shfl_sync(0xffffffffu, run, src);
+  pos = __shfl_sync(0xffffffffu, pos, src);
+  const int end = min(p.num_reqs, (run + 1) * per);
+  #pragma unroll 1
+  for (int b = run * per; b < end; b += 32) {
+    const int r = b + lane;
+    long long w = 0;
+    if (r < end) {
+      const plan::ReqInfo q = plan::load_request(p, r);
+      if (q.decode) w = plan::rows_weight(p, q, q.qr) * p.num_kv_heads;
+    }
+    long long sum = w;
+    #pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += t;
+    }
+    const long long before = pos + sum - w;
+    const unsigned hit = __ballot_sync(0xffffffffu, w > 0 && before <= rg.lo && rg.lo < before + w);
+    if (hit) {
+      const int x = __ffs(hit) - 1;
+      wk.r = b + x;
+      wk.finish_start(p, plan::load_request(p, wk.r), __shfl_sync(0xffffffffu, before, x));
+      return wk;
+    }
+    pos += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  record_error(p.err, kErrBounds);  // (as above)
+  wk.done = true;
+  return wk;
+}
+
+static __device__ __noinline__ void plan_many(const DecodeParams& p, RunSums& rs) {
+  constexpr int kBatch = 4;  // requests whose loads are in flight together
+  const int R = p.num_reqs, per = plan::cdiv(R, kThreads), tid = threadIdx.x, lane = tid & 31;
+  const int r0 = min(R, tid * per), r1 = min(R, r0 + per);
+  long long mine = 0;
+  int nb_min = INT_MAX, nb_max = 0;
+  for (int r = r0; r < r1; r += kBatch) {
+    plan::ReqInfo q[kBatch];
+    #pragma unroll
+    for (int i = 0; i < kBatch; ++i) q[i] = plan::load_request(p, min(r + i, r1 - 1));
+    #pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (r + i < r1) plan::tally_request(p, q[i], r + i, mine, nb_min, nb_max);
+  }
+  rs.w[tid] = mine;
+  nb_min = __reduce_min_sync(0xffffffffu, nb_min);
+  nb_max = __reduce_max_sync(0xffffffffu, nb_max);
+  if (lane == 0) {
+    rs.nb_min[tid >> 5] = nb_min;
+    rs.nb_max[tid >> 5] = nb_max;
+  }
+  __syncthreads();
+  if ((tid >> 5) != kWarpProd) return;
+  const plan::Walker wk = find_start(p, rs, per);
+  if (lane == 0) rs.at = wk;
+  __syncwarp();
+}
+
 template <int G>
 __global__ void __launch_bounds__(kThreads, 2)
     decode_block_kernel(const __grid_constant__ CUtensorMap kmap,
-                        const __grid_constant__ CUtensorMap vmap, const DecodeParams p,
+                        const __grid_constant__ CUtensorMap vmap,
+                        const __grid_constant__ DecodeParams p,
                         const int after_prefill) {
   static_assert(G >= 1 && G <= 8, "group size");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -256,9 +360,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (!after_prefill) grid_dependency_wait();
     allow_dependent_launch();
   };
+  const bool many = p.num_reqs > 32 * plan::kPlanRegReqs;
+  if (many) {
+    if (!p.early_plan && !after_prefill) grid_dependency_wait();
+    static_assert(sizeof(RunSums) <= sizeof(sm.slot), "scratch");
+    plan_many(p, *reinterpret_cast<RunSums*>(sm.slot));
+  }
   if (warp == kWarpProd) {
     if (!p.early_plan) launch_wait();
-    plan::plan_cta<true>(p, lane, rg, wk);
+    if (many)
+      wk = reinterpret_cast<const RunSums*>(sm.slot)->at;
+    else
+      plan::plan_cta<true>(p, lane, rg, wk);
     have_n = true;
     #pragma unroll 1
     for (int i = 0; i < 2; ++i) advance();

@@ -88,7 +88,7 @@ struct __align__(1024) BkSmem {
   uint8_t pt[2][2][kAtom];           // [tile & 1][hi | lo][8 heads x 128 keys]
   float sc[kScales][2][kBlkPerTile]; // [tile % kScales][K | V][block of the tile]
   float qf[2][8];                    // [piece buffer]: factor of a head's raw scores (log2 units)
-  float red[2][4][8];                // per-warp partial maxima (of s, of s + lv)
+  float4 red[2][4][2];               // per-warp partial maxima (of s, of s + lv), 8 heads
   float st_l[4][8];
   Piece pinfo[2];
   uint64_t pc_full[2];               // piece published by the producer
@@ -163,6 +163,19 @@ __device__ __forceinline__ void copy4_async(void* dst, const void* src, uint32_t
 __device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
+}
+
+// mbar_wait with its spin out of line, one copy for all the waits of the kernel.
+// The five roles' code is what bounds steps of many short rows: with every spin
+// in line, two copies of the MMA warp's PV and of q's conversion one per head,
+// the instruction cache missed on a third of its requests (1024 rows of 100-500
+// keys, two KV heads: 61.6 us against 45.0 without).
+static __device__ __noinline__ bool spin_on(uint64_t* bar, uint32_t parity, int* err, WaitCtl* ctl) {
+  return mbar_wait(bar, parity, err, ctl);
+}
+
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* err, WaitCtl* ctl) {
+  return mbar_try_wait(bar, parity) || spin_on(bar, parity, err, ctl);
 }
 
 // Key row `row` of a staged V tile set to zero.
@@ -443,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       int ent_nn = ntile > 8 ? raw_entries(pc, 2 * kWindow) : kPastPiece;
       // The piece's buffers are free once the MMAs of piece j - 2 are done.
       const int ub = j & 1;
-      if (j >= 2 && !mbar_wait(&sm.q_empty[ub], ((j >> 1) - 1) & 1, p.err, abort_flag)) break;
+      if (j >= 2 && !wait_on(&sm.q_empty[ub], ((j >> 1) - 1) & 1, p.err, abort_flag)) break;
       if (lane == 0 && j > 0) {
         sm.pinfo[ub] = pc;
         mbar_arrive(&sm.pc_full[ub]);
@@ -463,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int kv = 0; kv < 2; ++kv) {
           const int n = 2 * t + kv, s = n % kSlots;
           if (n >= kSlots &&
-              !mbar_wait(&sm.empty[s], ((n / kSlots) - 1) & 1, p.err, abort_flag)) {
+              !wait_on(&sm.empty[s], ((n / kSlots) - 1) & 1, p.err, abort_flag)) {
             ok = false;
             break;
           }
@@ -493,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (!abort_flag->abort) {
       const int ub = j & 1;  // end marker
-      if (j < 2 || mbar_wait(&sm.q_empty[ub], ((j >> 1) - 1) & 1, p.err, abort_flag)) {
+      if (j < 2 || wait_on(&sm.q_empty[ub], ((j >> 1) - 1) & 1, p.err, abort_flag)) {
         if (lane == 0) {
           sm.pinfo[ub].row = kEndRow;
           mbar_arrive(&sm.pc_full[ub]);
@@ -511,53 +524,58 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (lane == 0) {
       constexpr uint32_t kIdescS = idesc_e4m3_f32(kTile, kN, 0, 0);
       constexpr uint32_t kIdescO = idesc_e4m3_f32(kHeadDim, kN, 1, 0);
+      // Descriptors of the first operands: 32 bytes further along a row is 2
+      // (16-byte units), 32 rows of V 256.
+      const uint64_t dk = smem_desc_sw128(smem_u32(sm.slot[0]), 16, 1024);
+      const uint64_t dv = smem_desc_sw128(smem_u32(sm.slot[0]), 1024, 1024);
+      const uint64_t dq = smem_desc_sw128(smem_u32(sm.q[0][0]), 16, kAtom);
+      const uint64_t dp = smem_desc_sw128(smem_u32(sm.pt[0][0]), 16, kAtom);
       int t = 0;
       bool ok = true;
       auto pv = [&](int tt, bool first, int j) {
         const int n = 2 * tt + 1, s = n % kSlots, ob = j & 1, b = tt & 1;
         const uint32_t tO = tmem + kColO + ob * kN;
-        ok = ok && mbar_wait(&sm.p_full[b], (tt >> 1) & 1, p.err, abort_flag);
-        ok = ok && mbar_wait(&sm.full[s], (n / kSlots) & 1, p.err, abort_flag);
+        ok = ok && wait_on(&sm.p_full[b], (tt >> 1) & 1, p.err, abort_flag);
+        ok = ok && wait_on(&sm.full[s], (n / kSlots) & 1, p.err, abort_flag);
         if (first && j >= 2)
-          ok = ok && mbar_wait(&sm.o_empty[ob], ((j >> 1) - 1) & 1, p.err, abort_flag);
+          ok = ok && wait_on(&sm.o_empty[ob], ((j >> 1) - 1) & 1, p.err, abort_flag);
         if (!ok) return;
         tc_fence_after();
+        // V^T is MN-major: one 128-byte atom holds all 128 dims, 8-key
+        // groups 1024 bytes apart; 32 keys per MMA.
+        const uint64_t da = dv + s * (kTileCodes / 16), db = dp + b * (2 * kAtom / 16);
         #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          // V^T is MN-major: one 128-byte atom holds all 128 dims, 8-key
-          // groups 1024 bytes apart; 32 keys per MMA.
-          const uint64_t da = smem_desc_sw128(smem_u32(sm.slot[s]) + kk * 4096, 1024, 1024);
-          const uint64_t db = smem_desc_sw128(smem_u32(sm.pt[b][0]) + kk * 32, 16, kAtom);
-          tc_mma_f8_ss(tO, da, db, kIdescO, !first || kk > 0);
-        }
+        for (int kk = 0; kk < 4; ++kk)
+          tc_mma_f8_ss(tO, da + kk * 256, db + kk * 2, kIdescO, !first || kk > 0);
         tc_commit(&sm.empty[s]);
         tc_commit(&sm.p_free[b]);
       };
       for (int j = 0; ok; ++j) {
         const int ub = j & 1;
-        if (!mbar_wait(&sm.q_full[ub], (j >> 1) & 1, p.err, abort_flag)) break;
+        if (!wait_on(&sm.q_full[ub], (j >> 1) & 1, p.err, abort_flag)) break;
         const int row = sm.pinfo[ub].row;
         if (row == kEndRow) break;
         const int ntile = plan::cdiv(sm.pinfo[ub].nblk, kBlkPerTile);
         tc_fence_after();
-        for (int tt = 0; tt < ntile && ok; ++tt, ++t) {
-          const int b = t & 1, n = 2 * t, s = n % kSlots;
-          ok = ok && mbar_wait(&sm.full[s], (n / kSlots) & 1, p.err, abort_flag);
-          if (t >= 2) ok = ok && mbar_wait(&sm.s_free[b], ((t >> 1) - 1) & 1, p.err, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t tS = tmem + b * kN;
-          #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t da = smem_desc_sw128(smem_u32(sm.slot[s]) + kk * 32, 16, 1024);
-            const uint64_t db = smem_desc_sw128(smem_u32(sm.q[ub][0]) + kk * 32, 16, kAtom);
-            tc_mma_f8_ss(tS, da, db, kIdescS, kk > 0);
+        // S of tile tt, then PV of the tile before it (one copy of each).
+        #pragma unroll 1
+        for (int tt = 0; tt <= ntile && ok; ++tt) {
+          if (tt < ntile) {
+            const int b = t & 1, n = 2 * t, s = n % kSlots;
+            ok = ok && wait_on(&sm.full[s], (n / kSlots) & 1, p.err, abort_flag);
+            if (t >= 2) ok = ok && wait_on(&sm.s_free[b], ((t >> 1) - 1) & 1, p.err, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t tS = tmem + b * kN;
+            const uint64_t da = dk + s * (kTileCodes / 16), db = dq + ub * (2 * kAtom / 16);
+            #pragma unroll
+            for (int kk = 0; kk < 4; ++kk) tc_mma_f8_ss(tS, da + kk * 2, db + kk * 2, kIdescS, kk > 0);
+            tc_commit(&sm.empty[s]);
+            tc_commit(&sm.s_full[b]);
+            ++t;
           }
-          tc_commit(&sm.empty[s]);
-          tc_commit(&sm.s_full[b]);
-          if (tt >= 1) pv(t - 1, tt == 1, j);
+          if (tt > 0) pv(tt < ntile ? t - 2 : t - 1, tt == 1, j);
         }
-        if (ok) pv(t - 1, ntile == 1, j);
         tc_commit(&sm.o_full[ub]);
         tc_commit(&sm.q_empty[ub]);
       }
@@ -572,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ============================ q, a piece ahead ========================
     for (int j = 0;; ++j) {
       const int ub = j & 1;
-      if (!mbar_wait(&sm.pc_full[ub], (j >> 1) & 1, p.err, abort_flag)) break;
+      if (!wait_on(&sm.pc_full[ub], (j >> 1) & 1, p.err, abort_flag)) break;
       const int row = sm.pinfo[ub].row, k = sm.pinfo[ub].k;
       if (row == kEndRow) {
         __syncwarp();
@@ -581,18 +599,24 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       // Testing only: the first piece's q never comes, so the waits on it run out.
       if (p.debug_withhold_q && j == 0) continue;
-      // Four dims of every head per lane.
-      const uint2* src = reinterpret_cast<const uint2*>(
-                             p.q + ((long long)row * p.num_q_heads + (long long)k * G) * kHeadDim) +
-                         lane;
-      uint2 x[G];
-      #pragma unroll
-      for (int h = 0; h < G; ++h) x[h] = __ldg(src + h * (kHeadDim / 4));
-      #pragma unroll
-      for (int h = 0; h < G; ++h) {
-        const uint32_t a = x[h].x & 0x7fff7fffu, c = x[h].y & 0x7fff7fffu;
-        uint32_t top = max(max(a & 0xffffu, a >> 16), max(c & 0xffffu, c >> 16));
-        top = __reduce_max_sync(0xffffffffu, top);
+      // Four lanes a head, 32 dims each.
+      const int h = lane >> 2, c = lane & 3;
+      if (h < G) {
+        const uint4* src = reinterpret_cast<const uint4*>(
+                               p.q + ((long long)row * p.num_q_heads + (long long)k * G + h) * kHeadDim) +
+                           c * 4;
+        uint4 x[4];
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = __ldg(src + i);
+        uint32_t top = 0;
+        #pragma unroll
+        for (int i = 0; i < 4; ++i)
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                       __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+        top = max(top & 0xffffu, top >> 16);
+        const unsigned rows = __activemask();
+        top = max(top, __shfl_xor_sync(rows, top, 1));
+        top = max(top, __shfl_xor_sync(rows, top, 2));
         // sigma = 2^(7 - e) of the largest |q| = 1.f 2^e puts it in [128, 256);
         // a zero or subnormal row is scaled like the smallest normal one.
         // A row with an infinity or a NaN becomes NaN throughout (its scores
@@ -607,14 +631,20 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float s2 = __uint_as_float((uint32_t)(127 + x2) << 23);
         const float b1 = finite ? __uint_as_float((uint32_t)(127 - x1) << 23) : s1;
         const float b2 = __uint_as_float((uint32_t)(127 - x2) << 23);
-        const float2 u = bf16x2_to_float2(x[h].x), v = bf16x2_to_float2(x[h].y);
-        uint32_t h0, l0, h1, l1;
-        split_pair(u.x * s1 * s2, u.y * s1 * s2, h0, l0);
-        split_pair(v.x * s1 * s2, v.y * s1 * s2, h1, l1);
-        const int at = h * 128 + (((lane >> 2) ^ h) * 16) + (lane & 3) * 4;
-        *reinterpret_cast<uint32_t*>(sm.q[ub][0] + at) = h0 | h1 << 16;
-        *reinterpret_cast<uint32_t*>(sm.q[ub][1] + at) = l0 | l1 << 16;
-        if (lane == 0) sm.qf[ub][h] = p.scale_log2 * b1 * b2;
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {  // 8 dims: half a 16-byte chunk of either row
+          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          uint32_t hi[4], lo[4];
+          #pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float2 f = bf16x2_to_float2(w[y]);
+            split_pair(f.x * s1 * s2, f.y * s1 * s2, hi[y], lo[y]);
+          }
+          const int at = h * 128 + (((c * 2 + (i >> 1)) ^ h) * 16) + (i & 1) * 8;
+          *reinterpret_cast<uint2*>(sm.q[ub][0] + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+          *reinterpret_cast<uint2*>(sm.q[ub][1] + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+        }
+        if (c == 0) sm.qf[ub][h] = p.scale_log2 * b1 * b2;
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -627,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     int t = 0;
     for (int j = 0;; ++j) {
       const int ub = j & 1;
-      const bool got = mbar_wait(&sm.q_full[ub], (j >> 1) & 1, p.err, abort_flag);
+      const bool got = wait_on(&sm.q_full[ub], (j >> 1) & 1, p.err, abort_flag);
       const Piece pc = sm.pinfo[ub];
       // Agree before any barrier: a wait that gave up (abort) stops everyone.
       if (barrier_or(kBarSoftmax, kSoftThreads, !got || pc.row == kEndRow)) break;
@@ -643,10 +673,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       for (int tt = 0; tt < ntile; ++tt, ++t) {
         const int b = t & 1;
-        ok = ok && mbar_wait(&sm.sc_full[t % kScales], (t / kScales) & 1, p.err, abort_flag);
+        ok = ok && wait_on(&sm.sc_full[t % kScales], (t / kScales) & 1, p.err, abort_flag);
         const float ks = sm.sc[t % kScales][0][row >> 4];
         const float vs = sm.sc[t % kScales][1][row >> 4];
-        ok = ok && mbar_wait(&sm.s_full[b], (t >> 1) & 1, p.err, abort_flag);
+        ok = ok && wait_on(&sm.s_full[b], (t >> 1) & 1, p.err, abort_flag);
         tc_fence_after();
         float v[16];
         tmem_ld16(tmem + lane_off + b * kN, v);
@@ -672,30 +702,48 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (lane == 0) mbar_arrive(&sm.s_free[b]);
         if (barrier_or(kBarSoftmax, kSoftThreads, over)) {
           // Raise the running maxima to this tile's; O^T and l move along.
+          float mx[2][8];
           #pragma unroll
-          for (int h = 0; h < G; ++h) {
-            const float a = warp_max(s[h]), c = warp_max(s[h] + lv);
-            if (lane == 0) {
-              sm.red[0][warp][h] = a;
-              sm.red[1][warp][h] = c;
-            }
+          for (int h = 0; h < 8; ++h) {
+            mx[0][h] = h < G ? warp_max(s[h < G ? h : 0]) : 0.f;
+            mx[1][h] = h < G ? warp_max(s[h < G ? h : 0] + lv) : 0.f;
+          }
+          if (lane == 0) {
+            #pragma unroll
+            for (int x = 0; x < 2; ++x)
+              #pragma unroll
+              for (int c = 0; c < (G + 3) / 4; ++c)
+                sm.red[x][warp][c] = make_float4(mx[x][4 * c], mx[x][4 * c + 1], mx[x][4 * c + 2],
+                                                 mx[x][4 * c + 3]);
           }
           // O^T must hold the PV of tile t - 1 before it is rescaled.
-          if (tt > 0) ok = ok && mbar_wait(&sm.p_free[(t - 1) & 1], ((t - 1) >> 1) & 1, p.err, abort_flag);
+          if (tt > 0) ok = ok && wait_on(&sm.p_free[(t - 1) & 1], ((t - 1) >> 1) & 1, p.err, abort_flag);
           named_barrier(kBarSoftmax, kSoftThreads);
+          #pragma unroll
+          for (int x = 0; x < 2; ++x)
+            #pragma unroll
+            for (int h = 0; h < 8; ++h) mx[x][h] = h < G ? (x ? mo : m)[h < G ? h : 0] : 0.f;
+          #pragma unroll
+          for (int x = 0; x < 2; ++x)
+            #pragma unroll
+            for (int c = 0; c < (G + 3) / 4; ++c)
+              #pragma unroll
+              for (int w = 0; w < 4; w += 2) {
+                const float4 y = sm.red[x][w][c], z = sm.red[x][w + 1][c];
+                mx[x][4 * c] = fmax3(mx[x][4 * c], y.x, z.x);
+                mx[x][4 * c + 1] = fmax3(mx[x][4 * c + 1], y.y, z.y);
+                mx[x][4 * c + 2] = fmax3(mx[x][4 * c + 2], y.z, z.z);
+                mx[x][4 * c + 3] = fmax3(mx[x][4 * c + 3], y.w, z.w);
+              }
           float alpha[G];
           bool grow = false;
           #pragma unroll
           for (int h = 0; h < G; ++h) {
-            const float mn = fmaxf(m[h], fmaxf(fmaxf(sm.red[0][0][h], sm.red[0][1][h]),
-                                               fmaxf(sm.red[0][2][h], sm.red[0][3][h])));
-            const float mon = fmaxf(mo[h], fmaxf(fmaxf(sm.red[1][0][h], sm.red[1][1][h]),
-                                                 fmaxf(sm.red[1][2][h], sm.red[1][3][h])));
-            l[h] *= fast_exp2(m[h] - mn);
-            alpha[h] = fast_exp2(mo[h] - mon);
-            grow |= mon != mo[h];
-            m[h] = mn;
-            mo[h] = mon;
+            l[h] *= fast_exp2(m[h] - mx[0][h]);
+            alpha[h] = fast_exp2(mo[h] - mx[1][h]);
+            grow |= mx[1][h] != mo[h];
+            m[h] = mx[0][h];
+            mo[h] = mx[1][h];
           }
           if (tt > 0 && grow) {
             tc_fence_after();
@@ -713,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           named_barrier(kBarSoftmax, kSoftThreads);  // sm.red is free again
         }
         // P buffer b was last read by the PV of tile t - 2.
-        if (t >= 2) ok = ok && mbar_wait(&sm.p_free[b], ((t >> 1) - 1) & 1, p.err, abort_flag);
+        if (t >= 2) ok = ok && wait_on(&sm.p_free[b], ((t >> 1) - 1) & 1, p.err, abort_flag);
         uint8_t* const hi_row = sm.pt[b][0] + (row & 15);
         uint8_t* const lo_row = sm.pt[b][1] + (row & 15);
         const float lt = lv + kTop;
@@ -739,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         // (NaN codes too): their V rows become zero, so that 0 * V stays 0.
         if (x < pc.nblk && pos >= pc.L) {
           const int n = 2 * t + 1, sv = n % kSlots;
-          ok = ok && mbar_wait(&sm.full[sv], (n / kSlots) & 1, p.err, abort_flag);
+          ok = ok && wait_on(&sm.full[sv], (n / kSlots) & 1, p.err, abort_flag);
           zero_row(sm.slot[sv], row);
         }
         fence_proxy_async_smem();
@@ -751,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const float sw = warp_sums<G>(l, lane);
       if ((lane & 3) == 0) sm.st_l[warp][sum_index(lane)] = sw;
       named_barrier(kBarSoftmax, kSoftThreads);
-      const bool okO = ok && mbar_wait(&sm.o_full[ub], (j >> 1) & 1, p.err, abort_flag);
+      const bool okO = ok && wait_on(&sm.o_full[ub], (j >> 1) & 1, p.err, abort_flag);
       tc_fence_after();
       float v[16];
       tmem_ld16(tO, v);

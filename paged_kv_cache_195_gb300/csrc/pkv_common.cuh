@@ -234,6 +234,15 @@ __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
   return d;
 }
 
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)),
+        "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+
 // Two packed bf16 -> two fp32 (exact: a bf16 is the top half of an fp32).
 __device__ __forceinline__ float2 bf16x2_to_float2(uint32_t w) {
   float2 r;

@@ -40,10 +40,11 @@
 // Bound: HBM for long steps, the chain of latencies (plan, table, tile, S,
 // softmax, PV, merge) for short ones; the tensor pipe is busy 2.5% of the time.
 // Measured, e4m3 codes and scales read over time: 128 rows x 2048 keys, two KV
-// heads, 26.3 us = 5.1 TB/s (0.76 of the measured copy rate, launch included;
+// heads, 25.7 us = 5.3 TB/s (0.78 of the measured copy rate, launch included;
 // the kernel for one scale per head, which widens the codes, 30.4 us); 8 rows x
-// 32768 keys, eight KV heads, 86.8 us = 6.2 TB/s (0.91); 64 rows x 512 keys, two
-// KV heads, 9.2 us; four rows of up to 128 keys, 4.9 us.
+// 32768 keys, eight KV heads, 84.9 us = 6.3 TB/s (0.93); 1024 rows x 100-500
+// keys, two KV heads, 41.7 us = 3.3 TB/s; 64 rows x 512 keys, two KV heads, 7.9
+// us; four rows of up to 128 keys, 5.0 us.
 //
 // Roles (224 threads, two CTAs per SM): warps 0-3 softmax and epilogue, one
 // key (TMEM lane) per thread; warp 4 plans and issues the copies -- K and V
@@ -87,9 +88,9 @@ struct __align__(1024) BkSmem {
   uint8_t q[2][2][kAtom];            // [piece buffer][hi | lo][8 heads x 128 d], 128-byte swizzle
   uint8_t pt[2][2][kAtom];           // [tile & 1][hi | lo][8 heads x 128 keys]
   float sc[kScales][2][kBlkPerTile]; // [tile % kScales][K | V][block of the tile]
-  float qf[2][8];                    // [piece buffer]: factor of a head's raw scores (log2 units)
+  __align__(16) float qf[2][8];      // [piece buffer]: factor of a head's raw scores (log2 units)
   float4 red[2][4][2];               // per-warp partial maxima (of s, of s + lv), 8 heads
-  float st_l[4][8];
+  __align__(16) float st_l[4][8];
   Piece pinfo[2];
   uint64_t pc_full[2];               // piece published by the producer
   uint64_t q_full[2], q_empty[2];    // q converted / read by the piece's last MMA
@@ -112,18 +113,21 @@ __device__ __forceinline__ float warp_max(float v) {
   return r;
 }
 
-// Warp sums of G values: value h's sum comes back in the lanes with
-// sum_index(lane) == h.  Three halving exchanges spread the (padded) eight
-// values over the lanes, two more add up: 9 shuffles for 5 G.
+// Warp sums of up to eight values in N pairs: value h's sum comes back in the
+// lanes with sum_index(lane) == h.  Three halving exchanges spread the values
+// over the lanes, two more add up: 9 shuffles for 40.
 __device__ __forceinline__ int sum_index(int lane) {
   return (lane >> 4 & 1) * 4 + (lane >> 3 & 1) * 2 + (lane >> 2 & 1);
 }
 
-template <int G>
-__device__ __forceinline__ float warp_sums(const float (&v)[G], int lane) {
+template <int N>
+__device__ __forceinline__ float warp_sums(const float2 (&v)[N], int lane) {
   float a[8];
   #pragma unroll
-  for (int h = 0; h < 8; ++h) a[h] = h < G ? v[h < G ? h : 0] : 0.f;
+  for (int i = 0; i < 4; ++i) {
+    a[2 * i] = i < N ? v[i < N ? i : 0].x : 0.f;
+    a[2 * i + 1] = i < N ? v[i < N ? i : 0].y : 0.f;
+  }
   #pragma unroll
   for (int n = 4, o = 16; n > 0; n >>= 1, o >>= 1) {
     const bool up = lane & o;
@@ -341,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         const __grid_constant__ DecodeParams p,
                         const int after_prefill) {
   static_assert(G >= 1 && G <= 8, "group size");
+  constexpr int kPairs = (G + 1) / 2;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   BkSmem& sm = *reinterpret_cast<BkSmem*>(smem_raw + (((raw + 1023u) & ~1023u) - raw));
@@ -631,9 +636,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float s2 = __uint_as_float((uint32_t)(127 + x2) << 23);
         const float b1 = finite ? __uint_as_float((uint32_t)(127 - x1) << 23) : s1;
         const float b2 = __uint_as_float((uint32_t)(127 - x2) << 23);
-        #pragma unroll
+        #pragma unroll 1
         for (int i = 0; i < 4; ++i) {  // 8 dims: half a 16-byte chunk of either row
-          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          const uint4 y4 = __ldg(src + i);
+          const uint32_t w[4] = {y4.x, y4.y, y4.z, y4.w};
           uint32_t hi[4], lo[4];
           #pragma unroll
           for (int y = 0; y < 4; ++y) {
@@ -664,13 +670,17 @@ __global__ void __launch_bounds__(kThreads, 2)
       bool ok = true;
       const uint32_t tO = tmem + lane_off + kColO + ub * kN;
       const int ntile = plan::cdiv(pc.nblk, kBlkPerTile);
-      float m[G], mo[G], l[G], qf[G];
+      // Heads in pairs; an odd group's last pair has a head whose scores are
+      // all -inf.
+      float2 m[kPairs], mo[kPairs], l[kPairs], qf[kPairs];
       #pragma unroll
-      for (int h = 0; h < G; ++h) {
-        m[h] = mo[h] = kNegBig;
-        l[h] = 0.f;
-        qf[h] = sm.qf[ub][h];
+      for (int i = 0; i < kPairs; ++i) {
+        m[i] = mo[i] = make_float2(kNegBig, kNegBig);
+        l[i] = make_float2(0.f, 0.f);
+        qf[i] = *reinterpret_cast<const float2*>(&sm.qf[ub][2 * i]);
+        if (2 * i + 1 == G) qf[i].y = 0.f;
       }
+      #pragma unroll 1
       for (int tt = 0; tt < ntile; ++tt, ++t) {
         const int b = t & 1;
         ok = ok && wait_on(&sm.sc_full[t % kScales], (t / kScales) & 1, p.err, abort_flag);
@@ -689,13 +699,27 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float lv = (float)(ve - 127);
         const float r = vs - vs == 0.f ? vs * __uint_as_float((uint32_t)(254 - ve) << 23)
                                        : __int_as_float(0x7fc00000);
-        bool over = false;
-        float s[G];
+        // Exponents of the normaliser's and of the MMA's probabilities, and
+        // whether one is beyond the margin.
+        const float2 lt2 = make_float2(lv + kTop, lv + kTop);
+        float2 s[kPairs], y[kPairs], z[kPairs];
+        float top_y = -INFINITY, top_z = -INFINITY;
+        auto exponents = [&](int i) {
+          y[i] = fadd2(s[i], make_float2(-m[i].x, -m[i].y));
+          z[i] = fadd2(fadd2(s[i], lt2), make_float2(-mo[i].x, -mo[i].y));
+        };
         #pragma unroll
-        for (int h = 0; h < G; ++h) {
-          s[h] = valid ? fmaf(v[8 + h], 1.f / kLo, v[h]) * (qf[h] * ks) : -INFINITY;
-          over |= s[h] > m[h] + kMargin || s[h] + lv > mo[h] + kMargin;
+        for (int i = 0; i < kPairs; ++i) {
+          const float2 c = ffma2(make_float2(v[8 + 2 * i], v[9 + 2 * i]),
+                                 make_float2(1.f / kLo, 1.f / kLo), make_float2(v[2 * i], v[2 * i + 1]));
+          s[i] = fmul2(c, fmul2(qf[i], make_float2(ks, ks)));
+          if (!valid) s[i].x = -INFINITY;
+          if (!valid || 2 * i + 1 == G) s[i].y = -INFINITY;
+          exponents(i);
+          top_y = fmax3(top_y, y[i].x, y[i].y);
+          top_z = fmax3(top_z, z[i].x, z[i].y);
         }
+        const bool over = top_y > kMargin || top_z > kMargin + kTop;
         // S buffer b has been read: the MMA may overwrite it (tile t + 2).
         tc_fence_before();
         __syncwarp();
@@ -704,9 +728,12 @@ __global__ void __launch_bounds__(kThreads, 2)
           // Raise the running maxima to this tile's; O^T and l move along.
           float mx[2][8];
           #pragma unroll
-          for (int h = 0; h < 8; ++h) {
-            mx[0][h] = h < G ? warp_max(s[h < G ? h : 0]) : 0.f;
-            mx[1][h] = h < G ? warp_max(s[h < G ? h : 0] + lv) : 0.f;
+          for (int i = 0; i < 4; ++i) {
+            const float2 x = i < kPairs ? s[i < kPairs ? i : 0] : make_float2(0.f, 0.f);
+            mx[0][2 * i] = i < kPairs ? warp_max(x.x) : 0.f;
+            mx[0][2 * i + 1] = 2 * i + 1 < G ? warp_max(x.y) : kNegBig;
+            mx[1][2 * i] = i < kPairs ? warp_max(x.x + lv) : 0.f;
+            mx[1][2 * i + 1] = 2 * i + 1 < G ? warp_max(x.y + lv) : kNegBig;
           }
           if (lane == 0) {
             #pragma unroll
@@ -720,9 +747,12 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (tt > 0) ok = ok && wait_on(&sm.p_free[(t - 1) & 1], ((t - 1) >> 1) & 1, p.err, abort_flag);
           named_barrier(kBarSoftmax, kSoftThreads);
           #pragma unroll
-          for (int x = 0; x < 2; ++x)
-            #pragma unroll
-            for (int h = 0; h < 8; ++h) mx[x][h] = h < G ? (x ? mo : m)[h < G ? h : 0] : 0.f;
+          for (int i = 0; i < kPairs; ++i) {
+            mx[0][2 * i] = m[i].x;
+            mx[0][2 * i + 1] = m[i].y;
+            mx[1][2 * i] = mo[i].x;
+            mx[1][2 * i + 1] = mo[i].y;
+          }
           #pragma unroll
           for (int x = 0; x < 2; ++x)
             #pragma unroll
@@ -735,15 +765,18 @@ __global__ void __launch_bounds__(kThreads, 2)
                 mx[x][4 * c + 2] = fmax3(mx[x][4 * c + 2], y.z, z.z);
                 mx[x][4 * c + 3] = fmax3(mx[x][4 * c + 3], y.w, z.w);
               }
-          float alpha[G];
+          float2 alpha[kPairs];
           bool grow = false;
           #pragma unroll
-          for (int h = 0; h < G; ++h) {
-            l[h] *= fast_exp2(m[h] - mx[0][h]);
-            alpha[h] = fast_exp2(mo[h] - mx[1][h]);
-            grow |= mx[1][h] != mo[h];
-            m[h] = mx[0][h];
-            mo[h] = mx[1][h];
+          for (int i = 0; i < kPairs; ++i) {
+            const float2 mn = make_float2(mx[0][2 * i], mx[0][2 * i + 1]);
+            const float2 mon = make_float2(mx[1][2 * i], mx[1][2 * i + 1]);
+            l[i] = fmul2(l[i], make_float2(fast_exp2(m[i].x - mn.x), fast_exp2(m[i].y - mn.y)));
+            alpha[i] = make_float2(fast_exp2(mo[i].x - mon.x), fast_exp2(mo[i].y - mon.y));
+            grow |= mon.x != mo[i].x || mon.y != mo[i].y;
+            m[i] = mn;
+            mo[i] = mon;
+            exponents(i);
           }
           if (tt > 0 && grow) {
             tc_fence_after();
@@ -752,8 +785,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             tc_wait_ld();
             #pragma unroll
             for (int h = 0; h < G; ++h) {
-              o[h] *= alpha[h];
-              o[8 + h] *= alpha[h];
+              const float a = h & 1 ? alpha[h / 2].y : alpha[h / 2].x;
+              o[h] *= a;
+              o[8 + h] *= a;
             }
             tmem_st16(tO, reinterpret_cast<const uint32_t(&)[16]>(o));
             tc_wait_st();
@@ -764,20 +798,16 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (t >= 2) ok = ok && wait_on(&sm.p_free[b], ((t >> 1) - 1) & 1, p.err, abort_flag);
         uint8_t* const hi_row = sm.pt[b][0] + (row & 15);
         uint8_t* const lo_row = sm.pt[b][1] + (row & 15);
-        const float lt = lv + kTop;
         #pragma unroll
-        for (int h = 0; h < G; h += 2) {
-          const bool two = h + 1 < G;
-          const float p0 = fast_exp2(s[h] + lt - mo[h]) * r;
-          const float p1 = two ? fast_exp2(s[two ? h + 1 : h] + lt - mo[two ? h + 1 : h]) * r : 0.f;
-          l[h] += fast_exp2(s[h] - m[h]);
-          if (two) l[two ? h + 1 : h] += fast_exp2(s[two ? h + 1 : h] - m[two ? h + 1 : h]);
+        for (int i = 0; i < kPairs; ++i) {
+          const int h = 2 * i;
+          l[i] = fadd2(l[i], make_float2(fast_exp2(y[i].x), fast_exp2(y[i].y)));
           uint32_t hi, lo;
-          split_pair(p0, p1, hi, lo);
+          split_pair(fast_exp2(z[i].x) * r, fast_exp2(z[i].y) * r, hi, lo);
           const int at = h * 128 + (((row >> 4) ^ h) * 16);
           hi_row[at] = (uint8_t)hi;
           lo_row[at] = (uint8_t)lo;
-          if (two) {
+          if (h + 1 < G) {
             const int at1 = (h + 1) * 128 + (((row >> 4) ^ (h + 1)) * 16);
             hi_row[at1] = (uint8_t)(hi >> 8);
             lo_row[at1] = (uint8_t)(lo >> 8);
@@ -796,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (lane == 0) mbar_arrive(&sm.p_full[b]);
       }
       // ============ epilogue of the piece (same four warps) ================
-      const float sw = warp_sums<G>(l, lane);
+      const float sw = warp_sums(l, lane);
       if ((lane & 3) == 0) sm.st_l[warp][sum_index(lane)] = sw;
       named_barrier(kBarSoftmax, kSoftThreads);
       const bool okO = ok && wait_on(&sm.o_full[ub], (j >> 1) & 1, p.err, abort_flag);
@@ -804,12 +834,23 @@ __global__ void __launch_bounds__(kThreads, 2)
       float v[16];
       tmem_ld16(tO, v);
       tc_wait_ld();
-      float o[G], lt[G];
+      float o[G], lt[8], mh[G];
+      #pragma unroll
+      for (int c = 0; c < (G + 3) / 4; ++c) {
+        float4 w[4];
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(&sm.st_l[i][4 * c]);
+        lt[4 * c] = (w[0].x + w[1].x) + (w[2].x + w[3].x);
+        lt[4 * c + 1] = (w[0].y + w[1].y) + (w[2].y + w[3].y);
+        lt[4 * c + 2] = (w[0].z + w[1].z) + (w[2].z + w[3].z);
+        lt[4 * c + 3] = (w[0].w + w[1].w) + (w[2].w + w[3].w);
+      }
       #pragma unroll
       for (int h = 0; h < G; ++h) {
-        lt[h] = (sm.st_l[0][h] + sm.st_l[1][h]) + (sm.st_l[2][h] + sm.st_l[3][h]);
+        mh[h] = h & 1 ? m[h / 2].y : m[h / 2].x;
+        const float moh = h & 1 ? mo[h / 2].y : mo[h / 2].x;
         // O carries 2^(kTop - mo), the normaliser 2^-m
-        const float num = fmaf(v[8 + h], 1.f / kLo, v[h]) * exp2f(mo[h] - m[h] - kTop);
+        const float num = fmaf(v[8 + h], 1.f / kLo, v[h]) * exp2f(moh - mh[h] - kTop);
         o[h] = lt[h] == 0.f ? 0.f : __fdividef(num, lt[h]);
       }
       tc_fence_before();
@@ -832,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int h = 0; h < G; ++h) {
             const long long slot = (long long)pc.slot * G + h;
             p.ws_o[slot * kHeadDim + d] = o[h];
-            if (d == 0) *reinterpret_cast<float2*>(p.ws_ml + slot * 2) = make_float2(m[h], lt[h]);
+            if (d == 0) *reinterpret_cast<float2*>(p.ws_ml + slot * 2) = make_float2(mh[h], lt[h]);
           }
         }
         named_barrier(kBarSoftmax, kSoftThreads);

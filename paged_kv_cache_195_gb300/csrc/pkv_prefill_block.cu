@@ -189,15 +189,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float2 v) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
-  float2 d;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<unsigned long long&>(d))
-      : "l"(reinterpret_cast<unsigned long long&>(a)),
-        "l"(reinterpret_cast<unsigned long long&>(b)));
-  return d;
-}
-
 // Waits for the TMEM loads into a and b (as operands, so that nothing reads
 // them earlier).
 __device__ __forceinline__ void wait_ld32(float (&a)[16], float (&b)[16]) {

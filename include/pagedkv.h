@@ -113,7 +113,9 @@ int pkv_copy_blocks(const void *k_src, const void *v_src, void *k_dst, void *v_d
 
 /*
  * Bytes of workspace pkv_attention needs for these dims (split-context
- * partial outputs, their log-sum-exp statistics and per-row merge counters).
+ * partial outputs, their log-sum-exp statistics and per-row merge counters;
+ * for steps with more tokens than requests also 10 MB of partial states for
+ * prefill work items that pkv_attention_fp8_block splits over their keys).
  * Depends only on dims and the device's SM count, not on the lengths, so one
  * buffer serves every step of a captured CUDA graph.
  */
@@ -351,7 +353,9 @@ int pkv_append_fp8_block(const void *k_new, const void *v_new, const int32_t *bl
  * (q, out, lengths, tables, workspace, errors, launch overlap) as in
  * pkv_attention.  Both products take the codes themselves (e4m3 tensor-core
  * operands); q and the probabilities enter them as pairs of e4m3 numbers with
- * eight significant bits.  num_blocks * num_kv_heads * 16 must be below 2^31.
+ * eight significant bits (chunks: P in f16).  Requests with at least half of
+ * PKV_PREFILL_MIN_Q query tokens run in the prefill kernel.
+ * num_blocks * num_kv_heads * 16 must be below 2^31.
  * Source: as pkv_attention_fp8kv.
  */
 int pkv_attention_fp8_block(const void *q, const void *k_pool, const void *v_pool,
@@ -459,7 +463,8 @@ typedef struct pkv_options {
     int32_t decode_tc_fp8;  /* PKV_DECODE_TC_FP8 (1): the same for e4m3 pools */
     int32_t prefill_min_q;  /* PKV_PREFILL_MIN_Q (16): requests with at least this many
                                query tokens run in the tensor-core prefill kernel
-                               (0: none do); bf16 and block-scaled e4m3 pools */
+                               (0: none do); bf16 pools, and block-scaled e4m3
+                               pools from half as many on */
     int32_t align;          /* PKV_ALIGN (1): with uniform row-groups, snap decode ranges
                                to row-group boundaries (block-scaled e4m3 pools: with
                                no more row-groups than CTAs, cut each into pieces of its

@@ -125,9 +125,28 @@ int check_step_dims(const pkv_dims* d) {
   return PKV_OK;
 }
 
+constexpr int kPartsPerSm = 1;
+
 pkv::WorkspaceLayout layout_for(const pkv_dims* d, int sm_count) {
   return pkv::decode_workspace_layout(d->num_q_tokens, d->num_kv_heads,
                                       d->num_q_heads / d->num_kv_heads, sm_count);
+}
+
+// Partial states of the block-scaled prefill's split items, behind the rest of
+// the workspace: for steps that may hold a chunk, one part per SM.
+struct PartsLayout {
+  size_t ml, o, total;
+  int parts;
+};
+
+PartsLayout parts_layout(const pkv::WorkspaceLayout& w, const pkv_dims* d, int sm_count) {
+  PartsLayout l;
+  l.parts = d->num_q_tokens > d->num_reqs ? kPartsPerSm * sm_count : 0;
+  const size_t rows = (size_t)l.parts * pkv::kPrefillRows;
+  l.ml = (w.total + 255) & ~(size_t)255;
+  l.o = l.ml + rows * sizeof(float2);
+  l.total = l.parts ? l.o + rows * pkv::kHeadDim * sizeof(float) : w.total;
+  return l;
 }
 
 // ----------------------------------------------------------------- options
@@ -390,8 +409,10 @@ int pkv_copy_blocks(const void* k_src, const void* v_src, void* k_dst, void* v_d
 }
 
 size_t pkv_attention_workspace_size(const pkv_dims* dims) {
-  size_t bytes = 0;
-  return pkv::attention_workspace_bytes(dims, &bytes) == PKV_OK ? bytes : 0;
+  if (check_dims(dims, true) != PKV_OK) return 0;
+  DeviceState* st = device_state();
+  if (!st) return 0;
+  return parts_layout(layout_for(dims, st->sm_count), dims, st->sm_count).total;
 }
 
 int pkv_workspace_init(void* workspace, size_t workspace_bytes, const pkv_dims* dims,
@@ -470,17 +491,19 @@ int attention_impl(const void* q, const void* k_pool, const void* v_pool, const 
       return fail(PKV_ERR_WORKSPACE, "cascade workspace %zu bytes, need %zu (caller-owned)",
                   workspace_bytes, cl.total);
   }
+  const PartsLayout parts = parts_layout(w, dims, st->sm_count);
+  const size_t full = block_scales ? parts.total : w.total;
   if (workspace == nullptr) {
     std::lock_guard<std::mutex> lock(g_mutex);
-    if (st->own_ws_bytes < w.total) {
+    if (st->own_ws_bytes < full) {
       if (st->own_ws) cudaFree(st->own_ws);
       st->own_ws = nullptr;
       st->own_ws_bytes = 0;
-      cudaError_t e = cudaMalloc(&st->own_ws, w.total);
+      cudaError_t e = cudaMalloc(&st->own_ws, full);
       if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc(workspace)");
-      e = cudaMemset(st->own_ws, 0, w.total);
+      e = cudaMemset(st->own_ws, 0, full);
       if (e != cudaSuccess) return cuda_fail(e, "cudaMemset(workspace)");
-      st->own_ws_bytes = w.total;
+      st->own_ws_bytes = full;
       st->own_ws_cnt_bytes = w.ml_off;
     } else if (st->own_ws_cnt_bytes != w.ml_off) {
       // The counter region moved with the dims: zero it again.
@@ -528,6 +551,11 @@ int attention_impl(const void* q, const void* k_pool, const void* v_pool, const 
   // prefill kernel (when the step has that many query tokens at all).
   int prefill_min_q = opt.prefill_min_q;
   if (prefill_min_q < 1) prefill_min_q = 0x7fffffff;
+  // Over block scales the decode reads a request's keys once per query token
+  // and the prefill splits long items, so it takes over at half as many (64
+  // requests of 9 tokens, 500-1000 keys, eight KV heads: 53 us for 132; 8 of 4,
+  // 4000 keys: 37 for 48; but 30 of 5, 100-4000 keys, three KV heads: 50 for 33).
+  else if (block_scales) prefill_min_q = prefill_min_q / 2 + prefill_min_q % 2;
   // Launch it only when the step can hold such a request next to one query
   // for every other request; otherwise the decode kernel serves every row
   // (it is correct for any q_r, the prefill kernel is only faster).
@@ -643,6 +671,16 @@ int attention_impl(const void* q, const void* k_pool, const void* v_pool, const 
       L.p.k_scales = k_scale;
       L.p.v_scales = v_scale;
       L.p.early_plan = p.early_plan;
+      // No splitting when the step's rows, if they are all in use, are more
+      // than half as many items as parts (each request has at most
+      // prefill_min_q - 1 tokens that are no chunk's), or the workspace has no
+      // room for the parts.
+      const long long chunk_rows = dims->num_q_tokens - (prefill_min_q - 1ll) * dims->num_reqs;
+      const long long items = chunk_rows / pkv::prefill_tokens_per_tile(group) * dims->num_kv_heads;
+      L.p.max_parts = 2 * items <= parts.parts && workspace_bytes >= parts.total ? parts.parts : 0;
+      L.p.part_ml = reinterpret_cast<float2*>(ws + parts.ml);
+      L.p.part_o = reinterpret_cast<float4*>(ws + parts.o);
+      L.p.cnt = p.ws_cnt;
       pkv::PrefillParams& f = L.p.p;
       f.block_tables = block_tables;
       f.seq_lens = seq_lens;

@@ -322,7 +322,15 @@ struct PrefillBlockParams {
   const float* k_scales;  // [num_blocks, Hkv]
   const float* v_scales;
   int early_plan;         // read seq_lens / query_start_loc before the PDL wait
+  // Work items split over the keys: partial states of up to max_parts parts
+  // (0: no splitting), kPrefillRows rows each, and the arrival counters (those
+  // of the decode's row-groups, which have other rows).
+  int max_parts;
+  float2* part_ml;        // [part][row]: running maximum, normaliser
+  float4* part_o;         // [part][dim / 4][row]: normalised outputs
+  int* cnt;               // [query row, KV head]
 };
+constexpr int kPrefillRows = 128;
 
 struct PrefillBlockLaunch {
   CUtensorMap qmap;

@@ -41,6 +41,14 @@
 // the softmax may be waiting for one of them to rescale O, and splits that Q
 // only afterwards.
 //
+// A step with fewer items than half its CTAs cuts them over their keys, into equal
+// parts of four key tiles or more, each an item of the queue; a part leaves its
+// normalised output and (maximum, normaliser) per row in the workspace, and the
+// last to arrive merges them by log-sum-exp in part order.  (One chunk of 64
+// tokens on 30000 keys, 12 query and two KV heads: 51 us against 333 whole; 16
+// chunks of 16 on 500-2000 keys: 20 against 29.  At two parts per CTA the merges
+// cost more than the balance gains: 48 against 41 us on a mixed step.)
+//
 // Bound: the softmax, about 3000 cycles for a tile of 128 x 128 scores of which
 // the tensor pipe is busy a third (16 MMAs of 64 cycles) and the exponentials
 // take 1000; the rest is issue slots (57% used) and the latencies between a
@@ -69,7 +77,7 @@ constexpr int kWarpConv = kSoftWarps + 2;
 constexpr int kConvWarps = 2;
 constexpr int kThreads = 32 * (kWarpConv + kConvWarps);
 constexpr int kBarQuad = 1;              // + quad: the four warps holding the same 32 rows
-constexpr int kRows = 128;               // MMA M
+constexpr int kRows = kPrefillRows;      // MMA M
 constexpr int kKeyTile = 128;
 constexpr int kBlkPerTile = kKeyTile / kBlockSize;
 constexpr int kCodes = kKeyTile * kHeadDim;  // a K or V tile, or a Q operand, in bytes
@@ -87,6 +95,8 @@ constexpr int kItems = 4;                // item ring
 constexpr int kAhead = 4;                // an item is published this many tiles before the
                                          // previous one's last copies
 constexpr int kScaleRing = 8;            // tiles whose scales are held
+constexpr int kMaxSplit = 16;            // parts of an item's keys
+constexpr int kMinPart = 4;              // key tiles a part is worth
 
 struct Item {
   int r, k;   // request, KV head
@@ -94,7 +104,10 @@ struct Item {
   int nt;     // valid tokens in the tile
   int pos0;   // position of its first token
   int L;      // request length
+  int j0;     // first key tile
   int nj;     // key tiles
+  int parts;  // parts of the item's keys (1: this is all of them)
+  int slot;   // partial state of this part
   int end;    // no more items
 };
 
@@ -117,6 +130,8 @@ struct __align__(1024) Smem {
   uint64_t mma_done;
   uint32_t tmem_base;
   int n_active;
+  int split;                         // parts a long item is cut into
+  int last[4];                       // [quad]: the last part to arrive
   WaitCtl wait;
 };
 
@@ -262,11 +277,97 @@ static __device__ __forceinline__ void split_q(uint8_t* q, float scale_log2, flo
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
+// Partial states lie with a row's neighbours next to it: float4 c of the 32 of
+// row r of slot s at (32 s + c) * 128 + r, so that a warp's accesses are whole
+// lines.  The merge of an item's parts (slots `first` on) for one row and 32 of
+// its dims, by log-sum-exp: a part's weight is 2^m l.
+static __device__ __forceinline__ void merge_parts(const PrefillBlockParams& pb, long long first, int parts,
+                                                int row, int part, __nv_bfloat16* dst) {
+  float M = kNegBig, den = 0.f;
+  #pragma unroll 1
+  for (int s = 0; s < parts; ++s) {
+    const float2 ml = __ldcg(pb.part_ml + (first + s) * kRows + row);
+    const float Mn = fmaxf(M, ml.x);
+    den = den * fast_exp2(M - Mn) + fast_exp2(ml.x - Mn) * ml.y;
+    M = Mn;
+  }
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  float4 x[8];
+  #pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  #pragma unroll 1
+  for (int s = 0; s < parts; ++s) {
+    const float4* o = pb.part_o + ((first + s) * 32 + part * 8) * kRows + row;
+    float4 a[8];
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = __ldcg(o + i * kRows);
+    const float2 ml = __ldcg(pb.part_ml + (first + s) * kRows + row);
+    const float w = fast_exp2(ml.x - M) * ml.y * inv;
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i].x += w * a[i].x;
+      x[i].y += w * a[i].y;
+      x[i].z += w * a[i].z;
+      x[i].w += w * a[i].w;
+    }
+  }
+  #pragma unroll
+  for (int i = 0; i < 8; i += 2)
+    reinterpret_cast<uint4*>(dst)[i / 2] =
+        make_uint4(pack_bf16x2(x[i].x, x[i].y), pack_bf16x2(x[i].z, x[i].w),
+                   pack_bf16x2(x[i + 1].x, x[i + 1].y), pack_bf16x2(x[i + 1].z, x[i + 1].w));
+}
+
+// The epilogue of one part of item n: its state to memory, and the merge by the
+// part that arrives last -- each quad of warps by itself, whose rows are complete
+// in all parts.  Out of line, which keeps its registers out of the tile loop.
 template <int G>
+static __device__ __noinline__ void finish_part(Smem& sm, const PrefillBlockParams& pb, int n, int split,
+                                                uint32_t tO, float m, float l, float inv, bool write,
+                                                __nv_bfloat16* dst) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quad = warp & 3, part = warp >> 2;
+  const int row = quad * 32 + lane;
+  float x0[16], x1[16];
+  tmem_ld16(tO, x0);
+  tmem_ld16(tO + 16, x1);
+  wait_ld32(x0, x1);
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&sm.o_empty);
+  const Item& it = sm.items[n % kItems];
+  if (quad * 32 >= it.nt * G) return;  // no query in these rows
+  const int slot = it.slot, parts = it.parts;
+  if (write) {
+    float4* o = pb.part_o + ((long long)slot * 32 + part * 8) * kRows + row;
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[i * kRows] = make_float4(x0[4 * i] * inv, x0[4 * i + 1] * inv, x0[4 * i + 2] * inv, x0[4 * i + 3] * inv);
+      o[(4 + i) * kRows] =
+          make_float4(x1[4 * i] * inv, x1[4 * i + 1] * inv, x1[4 * i + 2] * inv, x1[4 * i + 3] * inv);
+    }
+    if (part == 0) pb.part_ml[slot * kRows + row] = make_float2(m, l);
+  }
+  named_barrier(kBarQuad + quad, 128);
+  if (part == 0 && lane == 0) {
+    // (a row of the item for each quad that has one: 32 quad < G nt)
+    int* const cnt = pb.cnt + (long long)(it.row0 + quad) * pb.p.num_kv_heads + it.k;
+    const int old = atom_add_acq_rel_gpu(cnt, 1);
+    sm.last[quad] = old == parts - 1;
+    if (old == parts - 1) *cnt = 0;
+  }
+  named_barrier(kBarQuad + quad, 128);
+  if (sm.last[quad] && write) merge_parts(pb, slot - slot % split, parts, row, part, dst);
+}
+
+// kSplit: whether items may be cut over their keys.  (A variant of its own for
+// steps that hold too many items for that: the calls of the other one cost the
+// tile loop registers, 150 against 145 us on eight 512-token chunks.)
+template <int G, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_block_kernel(const __grid_constant__ CUtensorMap qmap,
                          const __grid_constant__ CUtensorMap kmap,
-                         const __grid_constant__ CUtensorMap vmap, const PrefillBlockParams pb) {
+                         const __grid_constant__ CUtensorMap vmap,
+                         const __grid_constant__ PrefillBlockParams pb) {
   constexpr int TQ = kRows / G;  // query tokens per item
   const PrefillParams& p = pb.p;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -292,10 +393,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int o = 16; o > 0; o >>= 1) cnt += __shfl_xor_sync(0xffffffffu, cnt, o);
       total += cnt;
     }
-    if (lane == 0) sm.n_active = (int)min(total, (long long)gridDim.x);
+    // Few items are cut over their keys.
+    const int split = kSplit && total > 0
+                          ? (int)min((long long)kMaxSplit, max(1ll, pb.max_parts / total)) : 1;
+    if (lane == 0) {
+      sm.n_active = (int)min(total * split, (long long)gridDim.x);
+      sm.split = split;
+    }
   }
   __syncthreads();
   const int n_active = sm.n_active;  // CTAs that take items
+  const int split = kSplit ? sm.split : 1;
   if ((int)blockIdx.x >= n_active) {
     grid_dependency_wait();
     allow_dependent_launch();
@@ -358,12 +466,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dependency_wait();
   allow_dependent_launch();
 
-  // Item n of this CTA from the ring; every warp that reads it releases it.
-  auto take_item = [&](int n, Item& it) {
-    if (!mbar_wait(&sm.it_full[n % kItems], (n / kItems) & 1, p.err, abort_flag)) return false;
-    it = sm.items[n % kItems];
+  // Item n of this CTA from the ring; every warp that reads it releases it (when
+  // split, the softmax warps after their epilogue, which reads it again).
+  auto release_item = [&](int n) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.it_free[n % kItems]);
+  };
+  auto take_item = [&](int n, Item& it, bool keep = false) {
+    if (!mbar_wait(&sm.it_full[n % kItems], (n / kItems) & 1, p.err, abort_flag)) return false;
+    it = sm.items[n % kItems];
+    if (!keep) release_item(n);
     return !it.end;
   };
 
@@ -377,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Req rq = {0, 0, 0, 0};     // this lane's request of the batch
     long long cnt = 0, excl = 0, total = 0, base = 0;
     int batch = -32;
-    auto next_item = [&](Item& it) {
+    auto take_next = [&](Item& it) {
       unsigned long long taken = 0;
       if (lane == 0) taken = atomicAdd(p.sched, 1ull);
       const long long item = (long long)__shfl_sync(0xffffffffu, taken, 0);
@@ -393,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         rq = Req{0, 0, 0, 0};
         if (batch + lane < p.num_reqs) rq = load_req(p, batch + lane, TQ);
-        cnt = (long long)rq.ntiles * Hkv;
+        cnt = (long long)rq.ntiles * Hkv * split;
         total = cnt;
         #pragma unroll
         for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -409,7 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long long rel = item - base;
       const unsigned own = __ballot_sync(0xffffffffu, cnt > 0 && excl <= rel && rel < excl + cnt);
       const int src = __ffs(own) - 1;
-      const long long local = rel - __shfl_sync(0xffffffffu, excl, src);
+      const long long at = rel - __shfl_sync(0xffffffffu, excl, src), local = at / split;
+      const int part = (int)(at - local * split);
       const int q0 = __shfl_sync(0xffffffffu, rq.q0, src);
       const int qr = __shfl_sync(0xffffffffu, rq.qr, src);
       const int L = __shfl_sync(0xffffffffu, rq.L, src);
@@ -420,8 +533,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       it.nt = min(TQ, qr - qt * TQ);
       it.pos0 = L - qr + qt * TQ;
       it.L = L;
-      it.nj = (it.pos0 + it.nt - 1) / kKeyTile + 1;
+      const int tiles = (it.pos0 + it.nt - 1) / kKeyTile + 1;
+      it.parts = kSplit ? min(split, ceil_div(tiles, kMinPart)) : 1;
+      it.j0 = kSplit ? tiles * min(part, it.parts) / it.parts : 0;
+      it.nj = kSplit ? tiles * min(part + 1, it.parts) / it.parts - it.j0 : tiles;  // 0: no such part
+      it.slot = (int)item;  // (below max_parts when split)
       it.end = 0;
+    };
+    auto next_item = [&](Item& it) {
+      do take_next(it); while (kSplit && !it.end && it.nj == 0);
     };
     // The next item into nx and the ring.
     Item nx;
@@ -455,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nbl = ceil_div(it.L, kBlockSize);
       const int32_t* bt = p.block_tables + (long long)it.r * p.max_blocks;
       auto raw_entries = [&](int x0) {
-        const int x = x0 + lane;
+        const int x = (kSplit ? it.j0 * kBlkPerTile : 0) + x0 + lane;
         return x < nbl ? __ldg(bt + x) : kPastEnd;
       };
       int ent_cur = raw_entries(0);
@@ -614,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int row = row0; row < kKeyTile; row += kConvThreads) {
           // A key row widened: past the request's end a block may hold
           // anything (NaN codes too), and 0 * V has to stay 0.
-          const bool keep = j * kKeyTile + row < it.L;
+          const bool keep = ((kSplit ? it.j0 : 0) + j) * kKeyTile + row < it.L;
           const int sw = row & 7;
           uint4 c[8];
           #pragma unroll
@@ -654,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true, more = false;
     // Item n into `it`, its Q split; false if there is none.
     auto begin_item = [&](int n) {
-      bool have = take_item(n, it);
+      bool have = take_item(n, it, kSplit);
       have = have && mbar_wait(&sm.qr_full[n & 1], (n >> 1) & 1, p.err, abort_flag);
       // Agree before the next barrier of these rows' four warps (the only
       // barriers there are): a wait that gave up (abort) stops them all.
@@ -666,7 +786,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int n = 0; more; ++n) {
       ok = ok && mbar_wait(&sm.q_full[n % kItems], (n / kItems) & 1, p.err, abort_flag);
       const bool valid = t_local < it.nt && row < TQ * G;
-      const int prow = valid ? it.pos0 + t_local : -1;  // the last key this row sees
+      // the last key this row sees, from the item's first key on
+      const int prow = valid ? it.pos0 + t_local - (kSplit ? it.j0 * kKeyTile : 0) : -1;
       const int nj = it.nj;
       __nv_bfloat16* const dst = p.out + ((long long)(it.row0 + t_local) * p.num_q_heads +
                                           (long long)it.k * G + h) * kHeadDim + part * kPartKeys;
@@ -794,28 +915,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = lrow == 0.f ? 0.f : exp2f(mo - m - kTop) / lrow;
       ok = ok && mbar_wait(&sm.o_full, n & 1, p.err, abort_flag);
       tc_fence_after();
-      tmem_ld16(tO, x0);
-      tmem_ld16(tO + 16, x1);
-      wait_ld32(x0, x1);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.o_empty);
-      if (valid && ok) {
-        #pragma unroll
-        for (int i = 0; i < 16; i += 8) {
-          uint4 q4;
-          q4.x = pack_bf16x2(x0[i] * inv, x0[i + 1] * inv);
-          q4.y = pack_bf16x2(x0[i + 2] * inv, x0[i + 3] * inv);
-          q4.z = pack_bf16x2(x0[i + 4] * inv, x0[i + 5] * inv);
-          q4.w = pack_bf16x2(x0[i + 6] * inv, x0[i + 7] * inv);
-          *reinterpret_cast<uint4*>(dst + i) = q4;
-          q4.x = pack_bf16x2(x1[i] * inv, x1[i + 1] * inv);
-          q4.y = pack_bf16x2(x1[i + 2] * inv, x1[i + 3] * inv);
-          q4.z = pack_bf16x2(x1[i + 4] * inv, x1[i + 5] * inv);
-          q4.w = pack_bf16x2(x1[i + 6] * inv, x1[i + 7] * inv);
-          *reinterpret_cast<uint4*>(dst + 16 + i) = q4;
+      if (kSplit && sm.items[n % kItems].parts > 1) {  // (`it` is the next item)
+        finish_part<G>(sm, pb, n, split, tO, m, lrow, inv, valid && ok, dst);
+      } else {
+        tmem_ld16(tO, x0);
+        tmem_ld16(tO + 16, x1);
+        wait_ld32(x0, x1);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.o_empty);
+        if (valid && ok) {
+          #pragma unroll
+          for (int i = 0; i < 16; i += 8) {
+            uint4 q4;
+            q4.x = pack_bf16x2(x0[i] * inv, x0[i + 1] * inv);
+            q4.y = pack_bf16x2(x0[i + 2] * inv, x0[i + 3] * inv);
+            q4.z = pack_bf16x2(x0[i + 4] * inv, x0[i + 5] * inv);
+            q4.w = pack_bf16x2(x0[i + 6] * inv, x0[i + 7] * inv);
+            *reinterpret_cast<uint4*>(dst + i) = q4;
+            q4.x = pack_bf16x2(x1[i] * inv, x1[i + 1] * inv);
+            q4.y = pack_bf16x2(x1[i + 2] * inv, x1[i + 3] * inv);
+            q4.z = pack_bf16x2(x1[i + 4] * inv, x1[i + 5] * inv);
+            q4.w = pack_bf16x2(x1[i + 6] * inv, x1[i + 7] * inv);
+            *reinterpret_cast<uint4*>(dst + 16 + i) = q4;
+          }
         }
       }
+      if (kSplit) release_item(n);
     }
   }
   // Every warp reaches this point (aborts only shorten the loops), so the
@@ -838,8 +964,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "prefill shared memory");
 
-template <int G>
-cudaError_t launch_g(const PrefillBlockLaunch& L, cudaStream_t stream) {
+template <int G, bool kSplit>
+cudaError_t launch_variant(const PrefillBlockLaunch& L, cudaStream_t stream) {
   const size_t smem = sizeof(Smem) + 1024;  // + alignment slack
   static unsigned long long configured = 0;
   int dev = 0;
@@ -847,7 +973,7 @@ cudaError_t launch_g(const PrefillBlockLaunch& L, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & bit)) {
-    e = cudaFuncSetAttribute(prefill_block_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(prefill_block_kernel<G, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)smem);
     if (e != cudaSuccess) return e;
     __atomic_fetch_or(&configured, bit, __ATOMIC_RELEASE);
@@ -862,9 +988,14 @@ cudaError_t launch_g(const PrefillBlockLaunch& L, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = L.p.p.pdl ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, prefill_block_kernel<G>, L.qmap, L.kmap, L.vmap, L.p);
+  e = cudaLaunchKernelEx(&cfg, prefill_block_kernel<G, kSplit>, L.qmap, L.kmap, L.vmap, L.p);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
+}
+
+template <int G>
+cudaError_t launch_g(const PrefillBlockLaunch& L, cudaStream_t stream) {
+  return L.p.max_parts > 0 ? launch_variant<G, true>(L, stream) : launch_variant<G, false>(L, stream);
 }
 
 }  // namespace

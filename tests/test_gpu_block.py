@@ -334,6 +334,15 @@ def test_attention_several_rows_a_request(hkv):
     _check(c, q, _rows(rng, sum(q) + 3, 4 * hkv))
 
 
+@pytest.mark.parametrize("q", range(2, 17))
+def test_attention_every_draft_length(q):
+    # around the number of query tokens from which a request is a chunk
+    rng = np.random.default_rng(250 + q)
+    c = Cache(rng, [q, 40, 513, 127 + q, 1000, 16], 2)
+    n = [q, q, q, 1, q, 1]
+    _check(c, n, _rows(rng, sum(n), 12), min_q=8)
+
+
 @pytest.mark.parametrize("g,hkv", [(1, 2), (3, 1), (4, 2), (6, 1), (7, 1), (8, 2)])
 def test_attention_chunks(g, hkv):
     # query chunks around every tile edge, ragged ends, beside decode rows
@@ -355,6 +364,30 @@ def test_attention_long_chunk_after_a_long_prefix():
     rng = np.random.default_rng(18)
     c = Cache(rng, [5000, 1100], 1)
     _check(c, [90, 200], _rows(rng, 290, 5))
+
+
+@pytest.mark.parametrize("g,hkv,lens,q", [(6, 2, [4000], [64]), (4, 1, [3000, 2100, 40], [40, 33, 1]),
+                                          (8, 1, [2500], [17]), (1, 1, [6000], [130]), (7, 3, [1500], [19]),
+                                          (3, 2, [700, 5000, 129], [45, 16, 129]), (2, 8, [2000, 1999], [65, 16]),
+                                          (5, 1, [9000], [26])])
+def test_attention_few_chunks_split_over_the_keys(g, hkv, lens, q):
+    # Work items cut into parts; q-tiles of one token, quads of rows without a
+    # query, parts behind a row's last key; the same sums every time.
+    rng = np.random.default_rng(1000 + g)
+    c = Cache(rng, lens, hkv, pow2=False)
+    rows = _rows(rng, sum(q) + 2, g * hkv)
+    kp = c.gpu()[0]
+    ws = pkv.Workspace(pkv.make_dims(tuple(rows.shape), tuple(kp.shape), len(q), c.table.shape[1]))
+    first = _check(c, q, rows, workspace=ws)
+    again = _check(c, q, rows)
+    for _ in range(3):
+        again = _attend(c, q, rows, 0.09, workspace=ws)
+    T = sum(q)
+    assert torch.equal(again[:T].view(torch.int16), first[:T].view(torch.int16))
+    ws.nbytes -= 1  # no room for the parts: the calls split nothing
+    whole = _check(c, q, rows, workspace=ws)
+    d = (whole[:T].double() - first[:T].double()).abs().max() / first[:T].double().abs().max()
+    assert d <= 2.0 ** -7  # two roundings to bf16, and the sums' order
 
 
 @pytest.mark.parametrize("g,hkv", [(4, 4), (5, 8)])

@@ -511,8 +511,9 @@ __device__ __forceinline__ void plan_cta(const DecodeParams& p, int lane, Range&
     const int ctas = n <= rg.ctas ? rg.ctas : (int)gridDim.x;
     if (n <= ctas) {
       const long long blocks = rg.total - (long long)n * p.rowgroup_cost;
-      int lo = (int)max(cdiv_ll(blocks, ctas), (long long)max(p.min_chunk, kOwnMinBlocks));
-      int hi = max(lo, (int)(rg.chunk - p.rowgroup_cost + p.align_slack));
+      const long long most = 1ll << 28;  // (no row has as many blocks)
+      int lo = (int)min(most, max(cdiv_ll(blocks, ctas), (long long)max(p.min_chunk, kOwnMinBlocks)));
+      int hi = max(lo, (int)min(most, rg.chunk - p.rowgroup_cost + p.align_slack));
       if (pieces(hi) <= ctas) {
         while (lo < hi) {
           const int mid = (lo + hi) / 2;

@@ -129,6 +129,8 @@ struct __align__(1024) Smem {
   uint64_t o_full, o_empty;
   uint64_t mma_done;
   uint32_t tmem_base;
+  long long counts[kThreads / 32];   // items, by the warp that counted them
+  int batch_items[kMaxReqs / 32];    // uncut items of 32 requests
   int n_active;
   int split;                         // parts a long item is cut into
   int last[4];                       // [quad]: the last part to arrive
@@ -384,15 +386,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   // here, or no longer.
   if (!pb.early_plan) grid_dependency_wait();
   // CTAs without an item leave before any set-up.
+  long long count = 0;
+  for (int b = warp; b * 32 < p.num_reqs; b += kThreads / 32) {
+    const int r = b * 32 + lane;
+    const int c = __reduce_add_sync(0xffffffffu, r < p.num_reqs ? load_req(p, r, TQ).ntiles * Hkv : 0);
+    if (lane == 0) sm.batch_items[b] = c;
+    count += c;
+  }
+  if (lane == 0) sm.counts[warp] = count;
+  __syncthreads();
   if (warp == 0) {
-    long long total = 0;
-    for (int b = 0; b < p.num_reqs; b += 32) {
-      const int r = b + lane;
-      long long cnt = r < p.num_reqs ? (long long)load_req(p, r, TQ).ntiles * Hkv : 0;
-      #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) cnt += __shfl_xor_sync(0xffffffffu, cnt, o);
-      total += cnt;
-    }
+    long long total = lane < kThreads / 32 ? sm.counts[lane] : 0;
+    #pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     // Few items are cut over their keys.
     const int split = kSplit && total > 0
                           ? (int)min((long long)kMaxSplit, max(1ll, pb.max_parts / total)) : 1;
@@ -494,8 +500,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) taken = atomicAdd(p.sched, 1ull);
       const long long item = (long long)__shfl_sync(0xffffffffu, taken, 0);
       while (item >= base + total) {
-        batch += 32;
         base += total;
+        do batch += 32; while (batch < p.num_reqs && sm.batch_items[batch / 32] == 0);
         if (batch >= p.num_reqs) {
           it = Item{};
           it.end = 1;
@@ -503,12 +509,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           batch = p.num_reqs;
           return;
         }
+        total = (long long)sm.batch_items[batch / 32] * split;
+        if (item >= base + total) continue;
         rq = Req{0, 0, 0, 0};
         if (batch + lane < p.num_reqs) rq = load_req(p, batch + lane, TQ);
         cnt = (long long)rq.ntiles * Hkv * split;
-        total = cnt;
-        #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
         const int key = cnt > 0 ? rq.L : -1;
         excl = 0;
         #pragma unroll 4

@@ -353,6 +353,18 @@ def test_attention_chunks(g, hkv):
     _check(c, q, _rows(rng, sum(q), g * hkv))
 
 
+@pytest.mark.parametrize("R", [300, 1500])
+def test_attention_chunks_among_many_requests(R):
+    # batches of requests with no chunk, with one, with several
+    rng = np.random.default_rng(260 + R)
+    lens = [int(x) for x in rng.integers(1, 70, R)]
+    q = [1] * R
+    for r in [0, 1, 33, R // 2, R // 2 + 1, R - 1] + [int(x) for x in rng.integers(0, R, 5)]:
+        q[r] = lens[r]
+    c = Cache(rng, lens, 2)
+    _check(c, q, _rows(rng, sum(q), 8), min_q=8)
+
+
 def test_attention_long_rows_split_over_the_grid():
     rng = np.random.default_rng(8)
     c = Cache(rng, [9000, 20001, 3], 2)
@@ -575,7 +587,8 @@ def test_attention_shares_a_workspace_with_the_other_caches():
 
 
 @pytest.mark.parametrize("changes", [dict(pdl=0), dict(early_plan=0), dict(plan_cache=0), dict(decode_grid=7),
-                                     dict(min_chunk=1, align=0), dict(rowgroup_cost=0), dict(prefill_min_q=0),
+                                     dict(min_chunk=1, align=0), dict(rowgroup_cost=0),
+                                     dict(min_chunk=2 ** 31 - 1), dict(align_slack=2 ** 31 - 1), dict(align_slack=0), dict(prefill_min_q=0),
                                      dict(prefill_min_q=1)])
 def test_attention_under_every_option(changes, pkv_opts):
     rng = np.random.default_rng(15)

@@ -26,20 +26,16 @@
 //
 // Bound: HBM for prefill chunks (512 bytes read and 256 written per token and
 // head, K and V); four dependent loads for a decode step.  Measured: eight
-// chunks of 512 tokens, eight KV heads, 8.1 us = 3.1 TB/s (0.46 of the measured
-// copy rate: a launch and its four loads are 4 us of it); 64 decode tokens, two
-// KV heads, 4.1 us.
+// chunks of 512 tokens, eight KV heads, 7.5 us = 3.4 TB/s (0.50 of the measured
+// copy rate: a launch and its four loads are 3 us of it); 64 decode tokens, two
+// KV heads, 3.1 us.  (With sixty-four inlined divisions for scales that are no
+// powers of two and 64-bit indices, 8.2 and 4.0 us: the instruction cache.)
 #include "pkv_internal.h"
 
 namespace pkv {
 namespace {
 
 constexpr int kWarps = 8;
-
-// a / b: exactly a times the reciprocal when b is a power of two.
-__device__ __forceinline__ float quotient(float a, float b, float inv, bool pow2) {
-  return pow2 ? a * inv : __fdiv_rn(a, b);
-}
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
@@ -49,25 +45,29 @@ __global__ void __launch_bounds__(32 * kWarps) append_fp8_block_kernel(const App
   grid_dependency_wait();  // inputs and pools may belong to the previous kernel
   allow_dependent_launch();
   const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const unsigned w = blockIdx.x * kWarps + (threadIdx.x >> 5), uh = w >> 1;
   const int tensor = (int)(w & 1);
-  const long long uh = w >> 1;
-  const int unit = (int)(uh / p.num_kv_heads), h = (int)(uh % p.num_kv_heads);
+  const int unit = (int)(uh / (unsigned)p.num_kv_heads), h = (int)(uh % (unsigned)p.num_kv_heads);
   const int units = p.num_tokens / kBlockSize + 2 * p.num_reqs;
   if (unit >= units) return;
-  // The last request with F(r) <= unit.
-  int r = 0;
-  for (int n = p.num_reqs; n > 1;) {
-    const int step = (n + 31) / 32;
-    const int x = lane * step;
-    const bool in = x < n && (x == 0 || __ldg(p.query_start_loc + r + x) / kBlockSize +
-                                             2 * (r + x) <= unit);
+  // The last request with F(r) <= unit; the last round's lanes bring the
+  // requests' records along.
+  int r = 0, n = p.num_reqs;
+  auto before = [&](int x, int start) { return start / kBlockSize + 2 * x <= unit; };
+  while (n > 32) {
+    const int step = (n + 31) / 32, x = lane * step;
+    const bool in = x < n && (x == 0 || before(r + x, __ldg(p.query_start_loc + r + x)));
     const int at = __popc(__ballot_sync(0xffffffffu, in)) - 1;  // F rises: a prefix of the lanes
     r += at * step;
     n = min(step, n - at * step);
   }
-  const int q0 = __ldg(p.query_start_loc + r), q1 = __ldg(p.query_start_loc + r + 1);
-  const int L = __ldg(p.seq_lens + r), q = q1 - q0;
+  const int own = r + min(lane, n - 1);
+  const int s0 = __ldg(p.query_start_loc + own), s1 = __ldg(p.query_start_loc + own + 1);
+  const int len = __ldg(p.seq_lens + own);
+  const int at = __popc(__ballot_sync(0xffffffffu, lane < n && (lane == 0 || before(own, s0)))) - 1;
+  r += at;
+  const int q0 = __shfl_sync(0xffffffffu, s0, at), q1 = __shfl_sync(0xffffffffu, s1, at);
+  const int L = __shfl_sync(0xffffffffu, len, at), q = q1 - q0;
   if (q == 0) return;
   const int j = unit - (q0 / kBlockSize + 2 * r);
   if (q0 < 0 || q < 0 || q1 > p.num_tokens || q > L ||
@@ -115,22 +115,30 @@ __global__ void __launch_bounds__(32 * kWarps) append_fp8_block_kernel(const App
   const int ebits = max((int)(top >> 7) - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0), 1);
   const float need = __uint_as_float((uint32_t)ebits << 23);
   const float s_new = f0 > 0 ? fmaxf(s_old, need) : need;
-  const bool pow2 = (__float_as_uint(s_new) & 0x7fffffu) == 0;
-  const float inv = 1.f / s_new;
   uint8_t* const rows = (tensor ? p.v_pool : p.k_pool) + head * (kBlockSize * kHeadDim) + c * 8;
-  #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = 2 * i + half;
-    const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+  auto store = [&](int row, const uint4& y, auto quotient) {
+    const uint32_t in[4] = {y.x, y.y, y.z, y.w};
     uint32_t code[2] = {0u, 0u};
     #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float2 v = bf16x2_to_float2(in[e]);
-      code[e >> 1] |= e4m3x2(quotient(v.x, s_new, inv, pow2), quotient(v.y, s_new, inv, pow2))
-                      << (16 * (e & 1));
+      code[e >> 1] |= e4m3x2(quotient(v.x), quotient(v.y)) << (16 * (e & 1));
     }
-    if (row >= f0 && row < f1)
-      *reinterpret_cast<uint2*>(rows + row * kHeadDim) = make_uint2(code[0], code[1]);
+    *reinterpret_cast<uint2*>(rows + row * kHeadDim) = make_uint2(code[0], code[1]);
+  };
+  if ((__float_as_uint(s_new) & 0x7fffffu) == 0) {  // a power of two: x / s is x times 1 / s
+    const float inv = 1.f / s_new;
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = 2 * i + half;
+      if (row >= f0 && row < f1) store(row, x[i], [&](float v) { return v * inv; });
+    }
+  } else {  // a scale that the block came with (rows read again: less code)
+    #pragma unroll 1
+    for (int row = half; row < f1; row += 2)
+      if (row >= f0)
+        store(row, __ldg(src + ((long long)(t0 + row) * p.num_kv_heads + h) * (kHeadDim / 8) + c),
+              [&](float v) { return __fdiv_rn(v, s_new); });
   }
   if (f0 > 0 && s_new != s_old) {
     const float ratio = __fdiv_rn(s_old, s_new);
@@ -156,6 +164,7 @@ __global__ void __launch_bounds__(32 * kWarps) append_fp8_block_kernel(const App
 cudaError_t launch_append_fp8_block(const AppendBlockParams& p, cudaStream_t stream) {
   const long long units = (long long)p.num_tokens / kBlockSize + 2ll * p.num_reqs;
   const long long blocks = (units * p.num_kv_heads * 2 + kWarps - 1) / kWarps;
+  if (blocks > 0x0fffffff) return cudaErrorInvalidValue;  // (8 TB of new rows; warps are 32-bit)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(32 * kWarps);

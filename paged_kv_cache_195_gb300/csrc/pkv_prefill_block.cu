@@ -47,7 +47,7 @@
 // last to arrive merges them by log-sum-exp in part order.  (One chunk of 64
 // tokens on 30000 keys, 12 query and two KV heads: 51 us against 333 whole; 16
 // chunks of 16 on 500-2000 keys: 20 against 29.  At two parts per CTA the merges
-// cost more than the balance gains: 48 against 41 us on a mixed step.)
+// cost more than the balance gains: 30 us on those, 44 against 40 on a mixed step.)
 //
 // Bound: the softmax, about 3000 cycles for a tile of 128 x 128 scores of which
 // the tensor pipe is busy a third (16 MMAs of 64 cycles) and the exponentials

@@ -672,12 +672,13 @@ int attention_impl(const void* q, const void* k_pool, const void* v_pool, const 
       L.p.v_scales = v_scale;
       L.p.early_plan = p.early_plan;
       // No splitting when the step's rows, if they are all in use, are more
-      // than half as many items as parts (each request has at most
-      // prefill_min_q - 1 tokens that are no chunk's), or the workspace has no
-      // room for the parts.
+      // items than two thirds of the parts (each request has at most
+      // prefill_min_q - 1 tokens that are no chunk's) -- little is left to cut
+      // with then, and the kernel without it is 3% faster -- or the workspace
+      // has no room for the parts.
       const long long chunk_rows = dims->num_q_tokens - (prefill_min_q - 1ll) * dims->num_reqs;
       const long long items = chunk_rows / pkv::prefill_tokens_per_tile(group) * dims->num_kv_heads;
-      L.p.max_parts = 2 * items <= parts.parts && workspace_bytes >= parts.total ? parts.parts : 0;
+      L.p.max_parts = 3 * items <= 2 * parts.parts && workspace_bytes >= parts.total ? parts.parts : 0;
       L.p.part_ml = reinterpret_cast<float2*>(ws + parts.ml);
       L.p.part_o = reinterpret_cast<float4*>(ws + parts.o);
       L.p.cnt = p.ws_cnt;

@@ -41,11 +41,11 @@
 // the softmax may be waiting for one of them to rescale O, and splits that Q
 // only afterwards.
 //
-// A step with fewer items than half its CTAs cuts them over their keys, into equal
-// parts of four key tiles or more, each an item of the queue; a part leaves its
+// A step with fewer items than CTAs cuts the longer ones over their keys, into
+// equal parts of four key tiles or more, each an item of the queue; a part leaves its
 // normalised output and (maximum, normaliser) per row in the workspace, and the
 // last to arrive merges them by log-sum-exp in part order.  (One chunk of 64
-// tokens on 30000 keys, 12 query and two KV heads: 51 us against 333 whole; 16
+// tokens on 30000 keys, 12 query and two KV heads: 53 us against 333 whole; 16
 // chunks of 16 on 500-2000 keys: 20 against 29.  At two parts per CTA the merges
 // cost more than the balance gains: 30 us on those, 44 against 40 on a mixed step.)
 //
@@ -107,7 +107,8 @@ struct Item {
   int j0;     // first key tile
   int nj;     // key tiles
   int parts;  // parts of the item's keys (1: this is all of them)
-  int slot;   // partial state of this part
+  int part;   // this one
+  int slot;   // its partial state; the others' are beside it, in order
   int end;    // no more items
 };
 
@@ -130,9 +131,10 @@ struct __align__(1024) Smem {
   uint64_t mma_done;
   uint32_t tmem_base;
   long long counts[kThreads / 32];   // items, by the warp that counted them
-  int batch_items[kMaxReqs / 32];    // uncut items of 32 requests
+  int batch_items[kMaxReqs / 32];    // items (parts) of 32 requests
   int n_active;
-  int split;                         // parts a long item is cut into
+  int longest_part;                  // key tiles of a split item's longest part (0: none is)
+  uint2 extents[kThreads / 32];      // key tiles, the longest request's, by warp
   int last[4];                       // [quad]: the last part to arrive
   WaitCtl wait;
 };
@@ -324,7 +326,7 @@ static __device__ __forceinline__ void merge_parts(const PrefillBlockParams& pb,
 // part that arrives last -- each quad of warps by itself, whose rows are complete
 // in all parts.  Out of line, which keeps its registers out of the tile loop.
 template <int G>
-static __device__ __noinline__ void finish_part(Smem& sm, const PrefillBlockParams& pb, int n, int split,
+static __device__ __noinline__ void finish_part(Smem& sm, const PrefillBlockParams& pb, int n,
                                                 uint32_t tO, float m, float l, float inv, bool write,
                                                 __nv_bfloat16* dst) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quad = warp & 3, part = warp >> 2;
@@ -358,7 +360,7 @@ static __device__ __noinline__ void finish_part(Smem& sm, const PrefillBlockPara
     if (old == parts - 1) *cnt = 0;
   }
   named_barrier(kBarQuad + quad, 128);
-  if (sm.last[quad] && write) merge_parts(pb, slot - slot % split, parts, row, part, dst);
+  if (sm.last[quad] && write) merge_parts(pb, slot - it.part, parts, row, part, dst);
 }
 
 // kSplit: whether items may be cut over their keys.  (A variant of its own for
@@ -386,30 +388,77 @@ __global__ void __launch_bounds__(kThreads, 1)
   // here, or no longer.
   if (!pb.early_plan) grid_dependency_wait();
   // CTAs without an item leave before any set-up.
-  long long count = 0;
-  for (int b = warp; b * 32 < p.num_reqs; b += kThreads / 32) {
-    const int r = b * 32 + lane;
-    const int c = __reduce_add_sync(0xffffffffu, r < p.num_reqs ? load_req(p, r, TQ).ntiles * Hkv : 0);
-    if (lane == 0) sm.batch_items[b] = c;
-    count += c;
-  }
-  if (lane == 0) sm.counts[warp] = count;
-  __syncthreads();
-  if (warp == 0) {
+  auto count_batches = [&](auto items_of) {  // into sm.batch_items; this warp's sum
+    long long count = 0;
+    for (int b = warp; b * 32 < p.num_reqs; b += kThreads / 32) {
+      const int r = b * 32 + lane;
+      const int c = __reduce_add_sync(0xffffffffu,
+                                      r < p.num_reqs ? items_of(load_req(p, r, TQ)) : 0);
+      if (lane == 0) sm.batch_items[b] = c;
+      count += c;
+    }
+    if (lane == 0) sm.counts[warp] = count;
+  };
+  auto total_count = [&]() {  // (warp 0, after a barrier)
     long long total = lane < kThreads / 32 ? sm.counts[lane] : 0;
     #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    // Few items are cut over their keys.
-    const int split = kSplit && total > 0
-                          ? (int)min((long long)kMaxSplit, max(1ll, pb.max_parts / total)) : 1;
-    if (lane == 0) {
-      sm.n_active = (int)min(total * split, (long long)gridDim.x);
-      sm.split = split;
+    return total;
+  };
+  // Key tiles over all items (where they matter the items are few), and of the
+  // longest request.
+  unsigned tiles = 0, longest = 0;
+  count_batches([&](const Req& a) {
+    const int c = a.ntiles * Hkv;
+    if (kSplit && c > 0) {
+      tiles += (unsigned)c * (unsigned)ceil_div(a.L, kKeyTile);
+      longest = max(longest, (unsigned)ceil_div(a.L, kKeyTile));
+    }
+    return c;
+  });
+  if (kSplit) {
+    tiles = __reduce_add_sync(0xffffffffu, tiles);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) sm.extents[warp] = make_uint2(tiles, longest);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const long long total = total_count();
+    if (lane == 0) sm.n_active = (int)min(total, (long long)gridDim.x);
+    if (kSplit) {
+      // The longest part, in key tiles: a request of n tiles is cut into ceil(n
+      // / T) parts.  T = tiles / (parts - items) leaves room for every item's
+      // rounded-up part, T = longest / (parts / items) gives all as many.
+      const uint2 x = lane < kThreads / 32 ? sm.extents[lane] : make_uint2(0u, 0u);
+      const unsigned sum = __reduce_add_sync(0xffffffffu, x.x), n = __reduce_max_sync(0xffffffffu, x.y);
+      unsigned T = 0;
+      if (total > 0 && total <= pb.max_parts) {
+        const unsigned items = (unsigned)total, room = (unsigned)pb.max_parts;
+        auto up = [](unsigned a, unsigned b) { return (a + b - 1) / b; };
+        T = up(n, room / items);
+        if (room > items) T = min(T, up(sum, room - items));
+        T = max(T, max(up(n, kMaxSplit), (unsigned)kMinPart));
+        if (T >= n) T = 0;
+      }
+      if (lane == 0) sm.longest_part = (int)T;
     }
   }
   __syncthreads();
+  const int longest_part = kSplit ? sm.longest_part : 0;
+  // Parts of each of a request's items (some may be empty, see take_next).
+  auto parts_of = [&](int L) {
+    return longest_part > 0 ? ceil_div(ceil_div(L, kKeyTile), longest_part) : 1;
+  };
+  if (kSplit && longest_part > 0) {
+    count_batches([&](const Req& a) { return a.ntiles * Hkv * parts_of(a.L); });
+    __syncthreads();
+    if (warp == 0) {
+      const long long total = total_count();
+      if (lane == 0) sm.n_active = (int)min(total, (long long)gridDim.x);
+    }
+    __syncthreads();
+  }
   const int n_active = sm.n_active;  // CTAs that take items
-  const int split = kSplit ? sm.split : 1;
   if ((int)blockIdx.x >= n_active) {
     grid_dependency_wait();
     allow_dependent_launch();
@@ -509,11 +558,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           batch = p.num_reqs;
           return;
         }
-        total = (long long)sm.batch_items[batch / 32] * split;
+        total = sm.batch_items[batch / 32];
         if (item >= base + total) continue;
         rq = Req{0, 0, 0, 0};
         if (batch + lane < p.num_reqs) rq = load_req(p, batch + lane, TQ);
-        cnt = (long long)rq.ntiles * Hkv * split;
+        cnt = (long long)rq.ntiles * Hkv * parts_of(rq.L);
         const int key = cnt > 0 ? rq.L : -1;
         excl = 0;
         #pragma unroll 4
@@ -526,11 +575,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long long rel = item - base;
       const unsigned own = __ballot_sync(0xffffffffu, cnt > 0 && excl <= rel && rel < excl + cnt);
       const int src = __ffs(own) - 1;
-      const long long at = rel - __shfl_sync(0xffffffffu, excl, src), local = at / split;
-      const int part = (int)(at - local * split);
+      long long local = rel - __shfl_sync(0xffffffffu, excl, src);
       const int q0 = __shfl_sync(0xffffffffu, rq.q0, src);
       const int qr = __shfl_sync(0xffffffffu, rq.qr, src);
       const int L = __shfl_sync(0xffffffffu, rq.L, src);
+      const int cut = parts_of(L);
+      it.part = 0;
+      if (kSplit && cut > 1) {
+        it.part = (int)(local % cut);
+        local /= cut;
+      }
       const int qt = __shfl_sync(0xffffffffu, rq.ntiles, src) - 1 - (int)(local / Hkv);
       it.r = batch + src;
       it.k = (int)(local % Hkv);
@@ -539,9 +593,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       it.pos0 = L - qr + qt * TQ;
       it.L = L;
       const int tiles = (it.pos0 + it.nt - 1) / kKeyTile + 1;
-      it.parts = kSplit ? min(split, ceil_div(tiles, kMinPart)) : 1;
-      it.j0 = kSplit ? tiles * min(part, it.parts) / it.parts : 0;
-      it.nj = kSplit ? tiles * min(part + 1, it.parts) / it.parts - it.j0 : tiles;  // 0: no such part
+      it.parts = kSplit ? min(cut, ceil_div(tiles, kMinPart)) : 1;
+      it.j0 = kSplit ? tiles * min(it.part, it.parts) / it.parts : 0;
+      it.nj = kSplit ? tiles * min(it.part + 1, it.parts) / it.parts - it.j0 : tiles;  // 0: no such part
       it.slot = (int)item;  // (below max_parts when split)
       it.end = 0;
     };
@@ -921,7 +975,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = ok && mbar_wait(&sm.o_full, n & 1, p.err, abort_flag);
       tc_fence_after();
       if (kSplit && sm.items[n % kItems].parts > 1) {  // (`it` is the next item)
-        finish_part<G>(sm, pb, n, split, tO, m, lrow, inv, valid && ok, dst);
+        finish_part<G>(sm, pb, n, tO, m, lrow, inv, valid && ok, dst);
       } else {
         tmem_ld16(tO, x0);
         tmem_ld16(tO + 16, x1);

@@ -381,7 +381,9 @@ def test_attention_long_chunk_after_a_long_prefix():
 @pytest.mark.parametrize("g,hkv,lens,q", [(6, 2, [4000], [64]), (4, 1, [3000, 2100, 40], [40, 33, 1]),
                                           (8, 1, [2500], [17]), (1, 1, [6000], [130]), (7, 3, [1500], [19]),
                                           (3, 2, [700, 5000, 129], [45, 16, 129]), (2, 8, [2000, 1999], [65, 16]),
-                                          (5, 1, [9000], [26])])
+                                          (5, 1, [9000], [26]),
+                                          (7, 3, [100, 3000, 160, 250, 4000, 400, 90, 640, 1000] * 3, [9] * 27),
+                                          (8, 2, [300, 2500, 64, 900], [60, 33, 64, 1])])
 def test_attention_few_chunks_split_over_the_keys(g, hkv, lens, q):
     # Work items cut into parts; q-tiles of one token, quads of rows without a
     # query, parts behind a row's last key; the same sums every time.

@@ -33,9 +33,10 @@
 // stays below 2^8 and an error of half of lo's last subnormal step is 2^-18
 // of the largest probability.
 //
-// Plan, pieces, workspace and the log-sum-exp merge are those of the other
-// decode kernels (pkv_plan.cuh); rows of every request the caller leaves to
-// this kernel, any group size 1..8.
+// Plan, workspace and the log-sum-exp merge are those of the other decode
+// kernels (pkv_plan.cuh), but for steps of few rows, which are cut into pieces of
+// their own; rows of every request the caller leaves to this kernel, any group
+// size 1..8.
 //
 // Bound: HBM for long steps, the chain of latencies (plan, table, tile, S,
 // softmax, PV, merge) for short ones; the tensor pipe is busy 2.5% of the time.

@@ -19,8 +19,8 @@
 // probabilities in the softmax, which sets the pace, would cost more than
 // widening V once per tile in warps of its own (one hardware conversion per
 // pair of codes; every e4m3 value is an f16 value).  The value scales join the
-// probabilities: with vs = r 2^lv of key j's block,
-//     P = exp2(s - m) * F,   F = exp2(m - mo + lv + 6) * r
+// probabilities: with 2^lv <= vs < 2^(lv + 1) of key j's block,
+//     P = exp2(s - m) * F,   F = exp2(m - mo + 6) * vs
 // is at most 2^15, mo being a running maximum of s + lv next to the running
 // maximum m of s that the normaliser uses; both are raised when exceeded by
 // more than 2^8.  So P is precise where it weighs, however far apart the
@@ -58,7 +58,7 @@
 // TMEM columns of its own, so that a score buffer is free as soon as it is read.
 //
 // Measured: eight 512-token chunks after prefixes of up to 4096 tokens, 32 query
-// and 8 KV heads: 145 us = 740 TFLOP/s of the 2 x 2 x 128 flops per visible key
+// and 8 KV heads: 143 us = 752 TFLOP/s of the 2 x 2 x 128 flops per visible key
 // and query head, 0.39 of cuBLAS's bf16 rate (the bf16 prefill kernel: 129 us).
 #include <climits>
 
@@ -88,6 +88,7 @@ constexpr uint32_t kColO = 256, kColP = 384;
 constexpr float kMargin = 8.0f;          // log2 of the largest exp2(s - m) allowed
 constexpr float kTop = 6.0f;             // P carries 2^kTop: below 2^(kMargin + 1 + kTop) = 2^15
 constexpr float kNegBig = -1.0e30f;
+constexpr float kMostF = 0x1p100f;
 constexpr int kPastEnd = INT_MIN;        // block-table slot past the request (not read)
 constexpr int kStages = 3;               // K stages
 constexpr int kStagesV = 2;              // V stages (codes)
@@ -222,12 +223,10 @@ __device__ __forceinline__ void wait_ld32(float (&a)[16], float (&b)[16]) {
                : "memory");
 }
 
-// A block's value scale as r 2^lv: lv an integer, r in [1, 2) (0 for a zero
-// scale, NaN for one that is not finite).
-__device__ __forceinline__ void split_scale(float vs, float& lv, float& r) {
-  const int e = min(max((int)((__float_as_uint(vs) >> 23) & 255u), 1), 253);
-  lv = (float)(e - 127);
-  r = vs - vs == 0.f ? vs * __uint_as_float((uint32_t)(254 - e) << 23) : __int_as_float(0x7fc00000);
+// The exponent of a block's value scale: 2^lv <= vs < 2^(lv + 1) (0 and
+// subnormals: -127).
+__device__ __forceinline__ float scale_exponent(float vs) {
+  return __uint_as_float((__float_as_uint(vs) >> 23) | 0x4b000000u) - (8388608.f + 127.f);
 }
 
 // The softmax warps split an item's Q in place: q holds its two 64-dim halves
@@ -851,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __nv_bfloat16* const dst = p.out + ((long long)(it.row0 + t_local) * p.num_q_heads +
                                           (long long)it.k * G + h) * kHeadDim + part * kPartKeys;
       const float qf = sm.qf[n % kItems][row];
-      float m = kNegBig, mo = kNegBig, l = 0.f;
+      float m = kNegBig, mo = kNegBig, l = 0.f, root = 0.f;
       // The tile at hand: this part's 32 scores (two blocks of 16 keys), and
       // the blocks' factors of a score and of a probability.
       float x0[16], x1[16], sc0, sc1, f0, f1;
@@ -871,9 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sc1 = qf * ks.y;
         if (sc0 == 0.f) sc0 = 1e-30f;
         if (sc1 == 0.f) sc1 = 1e-30f;
-        float lv0, lv1, r0, r1;
-        split_scale(vs.x, lv0, r0);
-        split_scale(vs.y, lv1, r1);
+        const float lv0 = scale_exponent(vs.x), lv1 = scale_exponent(vs.y);
         const int kbase = tt * kKeyTile + part * kPartKeys;
         if (kbase + kPartKeys - 1 > prow) {
           #pragma unroll
@@ -913,11 +910,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           m = m_new;
           mo = mo_new;
+          // 2^up in two factors: either alone is in range
+          root = fast_exp2(0.5f * (m - mo + kTop));
         }
         // F, held to 2^100: a probability is then so small that P stays finite.
-        const float up = m - mo + kTop;
-        f0 = fast_exp2(fminf(up + lv0, 100.f)) * r0;
-        f1 = fast_exp2(fminf(up + lv1, 100.f)) * r1;
+        f0 = root * vs.x * root;
+        f1 = root * vs.y * root;
+        if (f0 > kMostF) f0 = kMostF;
+        if (f1 > kMostF) f1 = kMostF;
       };
       const uint32_t tS = lanes + part * kPartKeys;
       ok = ok && mbar_wait(&sm.s_full[t & 1], (t >> 1) & 1, p.err, abort_flag);

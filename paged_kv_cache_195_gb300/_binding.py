@@ -443,13 +443,19 @@ _BF16, _I32, _I64, _U8, _F32 = (torch.bfloat16, torch.int32, torch.int64, torch.
                                 torch.float32)
 
 
+def _spec(*tensors):
+    """(names, dtypes, ndims) of a call's (name, dtype, ndim) tensors."""
+    return tuple(zip(*tensors))
+
+
 def _fast_need(args, spec) -> tuple:
-    """Checks the tensors ``args`` against ``spec``, (name, dtype, ndim) of each:
-    contiguous CUDA tensors on one device.  Returns (device index, pointers)."""
+    """Checks the tensors ``args`` against ``spec`` (see _spec): contiguous CUDA
+    tensors on one device.  Returns (device index, pointers)."""
+    names, dtypes, ndims = spec
     try:
         dev = args[0].get_device()
         ptrs = []
-        for t, (_, dtype, ndim) in zip(args, spec):
+        for t, dtype, ndim in zip(args, dtypes, ndims):
             if (t.dtype is not dtype or t.get_device() != dev or t.dim() != ndim
                     or not t.is_contiguous()):
                 break
@@ -459,10 +465,10 @@ def _fast_need(args, spec) -> tuple:
                 return dev, ptrs
     except AttributeError:
         pass
-    for t, (name, dtype, ndim) in zip(args, spec):
+    for t, name, dtype, ndim in zip(args, names, dtypes, ndims):
         _need(t, name, dtype, ndim)
         if t.device != args[0].device:
-            raise ValueError(f"{name} is on {t.device}, {spec[0][0]} on {args[0].device}")
+            raise ValueError(f"{name} is on {t.device}, {names[0]} on {args[0].device}")
     raise ValueError("tensors must be contiguous CUDA tensors on one device")
 
 
@@ -475,7 +481,7 @@ def _raw_stream(stream, dev: int) -> int:
 
 def _call(fn, dev: int, *args):
     """fn(*args) with device ``dev`` current (the library launches there)."""
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         rc = fn(*args)
     else:
         with torch.cuda.device(dev):
@@ -489,15 +495,16 @@ def _block_scales(k_pool, v_pool, k_scales, v_scales):
     shape = k_pool.shape
     if v_pool.shape != shape:
         raise ValueError("v_pool must have k_pool's shape")
-    if k_scales.shape != shape[:2] or v_scales.shape != shape[:2]:
+    each = shape[:2]
+    if k_scales.shape != each or v_scales.shape != each:
         raise ValueError("k_scales and v_scales must be [num_blocks, num_kv_heads] = "
-                         f"{tuple(shape[:2])}")
+                         f"{tuple(each)}")
     return shape
 
 
-_APPEND_BLOCK = (("k_new", _BF16, 3), ("v_new", _BF16, 3), ("block_tables", _I32, 2),
-                 ("seq_lens", _I32, 1), ("query_start_loc", _I32, 1), ("k_pool", _U8, 4),
-                 ("v_pool", _U8, 4), ("k_scales", _F32, 2), ("v_scales", _F32, 2))
+_APPEND_BLOCK = _spec(("k_new", _BF16, 3), ("v_new", _BF16, 3), ("block_tables", _I32, 2),
+                      ("seq_lens", _I32, 1), ("query_start_loc", _I32, 1), ("k_pool", _U8, 4),
+                      ("v_pool", _U8, 4), ("k_scales", _F32, 2), ("v_scales", _F32, 2))
 
 
 def pkv_append_fp8_block(k_new, v_new, block_tables, seq_lens, query_start_loc, k_pool, v_pool,
@@ -522,9 +529,9 @@ def pkv_append_fp8_block(k_new, v_new, block_tables, seq_lens, query_start_loc, 
           _raw_stream(stream, dev))
 
 
-_ATTENTION_BLOCK = (("q", _BF16, 3), ("k_pool", _U8, 4), ("v_pool", _U8, 4),
-                    ("k_scales", _F32, 2), ("v_scales", _F32, 2), ("block_tables", _I32, 2),
-                    ("seq_lens", _I32, 1), ("query_start_loc", _I32, 1), ("out", _BF16, 3))
+_ATTENTION_BLOCK = _spec(("q", _BF16, 3), ("k_pool", _U8, 4), ("v_pool", _U8, 4),
+                         ("k_scales", _F32, 2), ("v_scales", _F32, 2), ("block_tables", _I32, 2),
+                         ("seq_lens", _I32, 1), ("query_start_loc", _I32, 1), ("out", _BF16, 3))
 
 
 def pkv_attention_fp8_block(q, k_pool, v_pool, k_scales, v_scales, block_tables, seq_lens,
@@ -560,10 +567,10 @@ def pkv_attention_fp8_block(q, k_pool, v_pool, k_scales, v_scales, block_tables,
     return out
 
 
-_BUILD_STEP = (("prev_lens", _I32, 1), ("new_tokens", _I32, 1), ("free_list", _I32, 1),
-               ("num_free", _I32, 1), ("block_tables", _I32, 2), ("seq_lens", _I32, 1),
-               ("query_start_loc", _I32, 1), ("slot_mapping", _I64, 1),
-               ("num_free_out", _I32, 1), ("num_refused", _I32, 1))
+_BUILD_STEP = _spec(("prev_lens", _I32, 1), ("new_tokens", _I32, 1), ("free_list", _I32, 1),
+                    ("num_free", _I32, 1), ("block_tables", _I32, 2), ("seq_lens", _I32, 1),
+                    ("query_start_loc", _I32, 1), ("slot_mapping", _I64, 1),
+                    ("num_free_out", _I32, 1), ("num_refused", _I32, 1))
 
 
 def pkv_build_step(prev_lens, new_tokens, free_list, num_free, block_tables, seq_lens,
@@ -596,8 +603,8 @@ def pkv_build_step(prev_lens, new_tokens, free_list, num_free, block_tables, seq
           _raw_stream(stream, dev))
 
 
-_RELEASE = (("block_tables", _I32, 2), ("seq_lens", _I32, 1), ("keep_lens", _I32, 1),
-            ("free_list", _I32, 1), ("num_free", _I32, 1), ("num_free_out", _I32, 1))
+_RELEASE = _spec(("block_tables", _I32, 2), ("seq_lens", _I32, 1), ("keep_lens", _I32, 1),
+                 ("free_list", _I32, 1), ("num_free", _I32, 1), ("num_free_out", _I32, 1))
 
 
 def pkv_release_blocks(block_tables, seq_lens, keep_lens, free_list, num_free,

@@ -660,14 +660,18 @@ int attention_impl(const void* q, const void* k_pool, const void* v_pool, const 
   const bool grid_forced = opt.decode_grid > 0 && 2 * opt.decode_grid <= w.num_slots;
   const int half_grid_blocks = small || grid_forced ? 0 : (int)kHalfGridBlocks;
   if (block_scales) {
+    pkv::DecodeBlockLaunch B{};
+    rc = encode_pool_map_e4m3(&B.kmap, k_pool, dims);
+    if (rc == PKV_OK) rc = encode_pool_map_e4m3(&B.vmap, v_pool, dims);
+    if (rc != PKV_OK) return rc;
     // The prefill first: the decode's CTAs fill the SMs that have no work item
     // of it, or have finished theirs.
     if (do_prefill) {
       pkv::PrefillBlockLaunch L{};
       rc = encode_q_map(&L.qmap, q, dims, group, pkv::prefill_tokens_per_tile(group));
-      if (rc == PKV_OK) rc = encode_pool_map_e4m3(&L.kmap, k_pool, dims);
-      if (rc == PKV_OK) rc = encode_pool_map_e4m3(&L.vmap, v_pool, dims);
       if (rc != PKV_OK) return rc;
+      L.kmap = B.kmap;
+      L.vmap = B.vmap;
       L.p.k_scales = k_scale;
       L.p.v_scales = v_scale;
       L.p.early_plan = p.early_plan;
@@ -703,10 +707,6 @@ int attention_impl(const void* q, const void* k_pool, const void* v_pool, const 
       e = pkv::launch_prefill_block(L, group, stream);
       if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
     }
-    pkv::DecodeBlockLaunch B{};
-    rc = encode_pool_map_e4m3(&B.kmap, k_pool, dims);
-    if (rc == PKV_OK) rc = encode_pool_map_e4m3(&B.vmap, v_pool, dims);
-    if (rc != PKV_OK) return rc;
     B.p = p;
     // More row-groups than SMs: two CTAs per SM however short they are, one
     // per row-group (plan_cta; 303 row-groups of one tile: 12.0 vs 16.6 us).

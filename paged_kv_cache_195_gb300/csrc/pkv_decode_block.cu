@@ -6,32 +6,43 @@
 //     s_j = scale * <q, decode(K_j)> * ks,   p_j = exp(s_j - max s),
 //     out = sum_j p_j * vs * decode(V_j) / sum_j p_j.
 //
-// No widening.  Both products run as e4m3 x e4m3 (tcgen05 kind::f8f6f4) on
-// the pool's own bytes; what is split instead is the small operand.  A head's
-// q is scaled by a power of two so that its largest element lies in
-// [224, 448) and written as two e4m3 rows, q = hi + lo / 16 with lo =
-// e4m3(16 (q - hi)): e4m3 keeps four significant bits, so hi leaves at most
-// 2^-4 of an element and the pair at most 2^-9 -- half a bf16 step; for q,
-// which is bf16, the pair is exact except below 2^-19 of the row's largest
-// element.  The probabilities are split the same way.  The eight (at most)
-// heads' hi rows and lo rows are the sixteen columns the smallest N of an
-// M = 128 MMA has anyway:
+// No widening.  Both products run on the pool's own bytes (tcgen05
+// kind::f8f6f4); what is split instead is the small operand.  A head's q is
+// scaled by a power of two so that its largest element lies in [128, 256) and
+// written as two e4m3 rows, q = hi + lo / 16 with lo = e4m3(16 (q - hi)): e4m3
+// keeps four significant bits and the residual's sign is a fifth, so the pair
+// holds bf16's eight exactly for every element whose last bit is no less than
+// lo's smallest step, 2^-13 -- from 2^-13 of the largest element's binade up --
+// and is off by at most half that step, 2^-14 (2^-21 of that binade), below.
+// The eight (at most) heads' hi rows and lo rows are the sixteen columns the
+// smallest N of an M = 128 MMA has anyway:
 //     S^T[128 keys x (8 hi | 8 lo)] = K[128 x 128 d] . Qhl^T         (A, B K-major)
-//     O^T[128 d x (8 hi | 8 lo)]   += V^T[128 d x 128 keys] . Phl^T  (A MN-major)
-// so the split costs no tensor time.  A kernel that widens the codes to 16
-// bits in shared memory or TMEM first is bound by that widening's latency.
+//
+// The probabilities are three e5m2 rows, P = a + b / 8 + c / 64 with b = e5m2(8
+// (P - a)), c what is left of 64 (P - a - b / 8): e5m2's three bits, with a sign
+// in each remainder, make up the eleven of an f16, and its five exponent bits
+// the range.  P lies in [2^11, 2^15) where it is largest, so every weight from
+// 2^-23 of the largest on is an f16's rounding, 2^-11 of it, and the smaller ones
+// are off by at most 2^-33 of the largest: no row loses its many small weights
+// beside a heavy one, however long it is.  (A pair of e4m3 rows ends at 2^-18 of
+// the largest: a key of weight 0.9 and value 0 then costs a row of 32768 keys 0.4
+// of its output.)
+//     O^T[128 d x (G a | G b | G c)] += V^T[128 d x 128 keys] . Pabc^T  (A MN-major)
+// fits sixteen columns for groups of up to five heads and takes thirty-two
+// beyond; the split costs no tensor time that shows.  A kernel that widens the
+// codes to 16 bits in shared memory or TMEM first is bound by that widening's
+// latency.
 //
 // Scales.  ks multiplies the scores after the MMA (a tile's 128 keys are 8
 // blocks; TMEM lane = key).  vs joins the probabilities before they are
 // rounded: with vs = r 2^lv, r in [1, 2), the value fed to the MMA is
-//     P = exp2(s + lv - mo) * r * 2^4,
+//     P = exp2(s + lv - mo) * r * 2^11,
 // where mo is a running maximum of s + lv, next to the running maximum m of s
 // that the normaliser uses.  A second maximum because a block that holds most
 // of the probability may have a V scale far below its neighbours': P is then
 // still of order one where it matters.  The two are raised, and O^T rescaled,
 // when a value exceeds its maximum by more than 2^3 (a CTA-wide vote), so P
-// stays below 2^8 and an error of half of lo's last subnormal step is 2^-18
-// of the largest probability.
+// stays below 2^15.
 //
 // Plan, workspace and the log-sum-exp merge are those of the other decode
 // kernels (pkv_plan.cuh), but for steps of few rows, which are cut into pieces of
@@ -71,14 +82,15 @@ constexpr int kBlkPerTile = kTile / kBlockSize;
 constexpr int kTileCodes = kTile * kHeadDim; // one K or V tile, bytes
 constexpr int kSlots = 6;                    // ring: K of tile t, V of tile t, K of t + 1, ...
 constexpr int kScales = 4;                   // tiles whose scales are held (see the producer)
-constexpr int kN = 16;                       // MMA N: 8 hi columns, 8 lo columns
+constexpr int kN = 16;                       // MMA N of S: 8 hi columns, 8 lo columns
 constexpr int kAtom = 8 * 128;               // 8 operand rows of 128 bytes
-constexpr uint32_t kTmemCols = 64;           // S0 0..15, S1 16..31, O0 32..47, O1 48..63
-constexpr uint32_t kColO = 32;
+constexpr int kPAtoms = 4;                   // operand rows of P, in eights (the most: N = 32)
+constexpr uint32_t kColO = 32;               // TMEM columns: S0 0..15, S1 16..31, O0, O1
 constexpr float kNegBig = -1.0e30f;
 constexpr float kMargin = 3.f;               // log2 of the largest exp2(s - m) allowed
-constexpr float kTop = 4.f;                  // P carries 2^kTop: P < 2^(kMargin + 1 + kTop) = 2^8
-constexpr float kLo = 16.f;                  // weight of the lo rows' reciprocal
+constexpr float kTop = 11.f;                 // P carries 2^kTop: P < 2^(kMargin + 1 + kTop) = 2^15
+constexpr float kLo = 16.f;                  // reciprocal of the weight of q's lo rows
+constexpr float kPart = 8.f;                 // ... of each row of P relative to the one before
 constexpr int kBarSoftmax = 1;
 constexpr int kSoftThreads = 128;
 constexpr int kPastPiece = INT_MIN;
@@ -87,7 +99,7 @@ constexpr int kWindow = 32;                  // block-table entries loaded at a 
 struct __align__(1024) BkSmem {
   uint8_t slot[kSlots][kTileCodes];  // occupant n: K (n even) or V (n odd) of tile n / 2
   uint8_t q[2][2][kAtom];            // [piece buffer][hi | lo][8 heads x 128 d], 128-byte swizzle
-  uint8_t pt[2][2][kAtom];           // [tile & 1][hi | lo][8 heads x 128 keys]
+  uint8_t pt[2][kPAtoms][kAtom];     // [tile & 1][rows G a, G b, G c x 128 keys]
   float sc[kScales][2][kBlkPerTile]; // [tile % kScales][K | V][block of the tile]
   __align__(16) float qf[2][8];      // [piece buffer]: factor of a head's raw scores (log2 units)
   float4 red[2][4][2];               // per-warp partial maxima (of s, of s + lv), 8 heads
@@ -155,6 +167,24 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t& hi, uint3
   hi = to_e4m3x2(a, b);
   const float2 h = e4m3x2_to_float2(hi);
   lo = to_e4m3x2((a - h.x) * kLo, (b - h.y) * kLo);
+}
+
+// a = e5m2(x), b = e5m2(8 (x - a)), c = e5m2(64 (x - a - b / 8)) of a pair
+// rounded to f16, low byte first.  The differences are exact in f16.
+__device__ __forceinline__ void split_three(float x, float y, uint32_t (&part)[3]) {
+  __half2 v = __floats2half2_rn(x, y);
+  #pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    unsigned short code;
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;"
+        : "=h"(code)
+        : "r"(*reinterpret_cast<const uint32_t*>(&v)));
+    part[i] = code;
+    if (i == 2) break;
+    uint32_t back;
+    asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(back) : "h"(code));
+    v = __hmul2(__hsub2(v, *reinterpret_cast<const __half2*>(&back)), __float2half2_rn(kPart));
+  }
 }
 
 // 4 bytes global -> shared, asynchronously; `bytes` 0 writes zero instead.
@@ -347,6 +377,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                         const int after_prefill) {
   static_assert(G >= 1 && G <= 8, "group size");
   constexpr int kPairs = (G + 1) / 2;
+  constexpr int kNO = 3 * G <= 16 ? 16 : 32;                // MMA N of O
+  constexpr uint32_t kTmemCols = kColO + 2 * kNO <= 64 ? 64 : 128;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   BkSmem& sm = *reinterpret_cast<BkSmem*>(smem_raw + (((raw + 1023u) & ~1023u) - raw));
@@ -529,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ============================ MMA issuer ==============================
     if (lane == 0) {
       constexpr uint32_t kIdescS = idesc_e4m3_f32(kTile, kN, 0, 0);
-      constexpr uint32_t kIdescO = idesc_e4m3_f32(kHeadDim, kN, 1, 0);
+      constexpr uint32_t kIdescO = idesc_e4m3_e5m2_f32(kHeadDim, kNO, 1, 0);
       // Descriptors of the first operands: 32 bytes further along a row is 2
       // (16-byte units), 32 rows of V 256.
       const uint64_t dk = smem_desc_sw128(smem_u32(sm.slot[0]), 16, 1024);
@@ -540,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       bool ok = true;
       auto pv = [&](int tt, bool first, int j) {
         const int n = 2 * tt + 1, s = n % kSlots, ob = j & 1, b = tt & 1;
-        const uint32_t tO = tmem + kColO + ob * kN;
+        const uint32_t tO = tmem + kColO + ob * kNO;
         ok = ok && wait_on(&sm.p_full[b], (tt >> 1) & 1, p.err, abort_flag);
         ok = ok && wait_on(&sm.full[s], (n / kSlots) & 1, p.err, abort_flag);
         if (first && j >= 2)
@@ -549,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         tc_fence_after();
         // V^T is MN-major: one 128-byte atom holds all 128 dims, 8-key
         // groups 1024 bytes apart; 32 keys per MMA.
-        const uint64_t da = dv + s * (kTileCodes / 16), db = dp + b * (2 * kAtom / 16);
+        const uint64_t da = dv + s * (kTileCodes / 16), db = dp + b * (kPAtoms * kAtom / 16);
         #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           tc_mma_f8_ss(tO, da + kk * 256, db + kk * 2, kIdescO, !first || kk > 0);
@@ -669,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       // Agree before any barrier: a wait that gave up (abort) stops everyone.
       if (barrier_or(kBarSoftmax, kSoftThreads, !got || pc.row == kEndRow)) break;
       bool ok = true;
-      const uint32_t tO = tmem + lane_off + kColO + ub * kN;
+      const uint32_t tO = tmem + lane_off + kColO + ub * kNO;
       const int ntile = plan::cdiv(pc.nblk, kBlkPerTile);
       // Heads in pairs; an odd group's last pair has a head whose scores are
       // all -inf.
@@ -781,37 +813,39 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           if (tt > 0 && grow) {
             tc_fence_after();
-            float o[16];
+            float o[16], oc[8];
             tmem_ld16(tO, o);
+            if (kNO > 16) tmem_ld8(tO + 16, oc);
             tc_wait_ld();
             #pragma unroll
-            for (int h = 0; h < G; ++h) {
+            for (int n = 0; n < 3 * G; ++n) {
+              const int h = n % G;
               const float a = h & 1 ? alpha[h / 2].y : alpha[h / 2].x;
-              o[h] *= a;
-              o[8 + h] *= a;
+              if (n < 16) o[n < 16 ? n : 0] *= a; else oc[n >= 16 ? n - 16 : 0] *= a;
             }
             tmem_st16(tO, reinterpret_cast<const uint32_t(&)[16]>(o));
+            if (kNO > 16) tmem_st8(tO + 16, oc);
             tc_wait_st();
           }
           named_barrier(kBarSoftmax, kSoftThreads);  // sm.red is free again
         }
         // P buffer b was last read by the PV of tile t - 2.
         if (t >= 2) ok = ok && wait_on(&sm.p_free[b], ((t >> 1) - 1) & 1, p.err, abort_flag);
-        uint8_t* const hi_row = sm.pt[b][0] + (row & 15);
-        uint8_t* const lo_row = sm.pt[b][1] + (row & 15);
+        // Row n of the operand is part n / G of head n % G.
+        uint8_t* const rows = sm.pt[b][0] + (row & 15);
+        auto put = [&](int n, uint32_t code) {
+          rows[(n >> 3) * kAtom + (n & 7) * 128 + (((row >> 4) ^ (n & 7)) * 16)] = (uint8_t)code;
+        };
         #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
           const int h = 2 * i;
           l[i] = fadd2(l[i], make_float2(fast_exp2(y[i].x), fast_exp2(y[i].y)));
-          uint32_t hi, lo;
-          split_pair(fast_exp2(z[i].x) * r, fast_exp2(z[i].y) * r, hi, lo);
-          const int at = h * 128 + (((row >> 4) ^ h) * 16);
-          hi_row[at] = (uint8_t)hi;
-          lo_row[at] = (uint8_t)lo;
-          if (h + 1 < G) {
-            const int at1 = (h + 1) * 128 + (((row >> 4) ^ (h + 1)) * 16);
-            hi_row[at1] = (uint8_t)(hi >> 8);
-            lo_row[at1] = (uint8_t)(lo >> 8);
+          uint32_t part[3];
+          split_three(fast_exp2(z[i].x) * r, fast_exp2(z[i].y) * r, part);
+          #pragma unroll
+          for (int c = 0; c < 3; ++c) {
+            put(c * G + h, part[c]);
+            if (h + 1 < G) put(c * G + h + 1, part[c] >> 8);
           }
         }
         // Keys past the request's end inside its last block may hold anything
@@ -832,9 +866,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       named_barrier(kBarSoftmax, kSoftThreads);
       const bool okO = ok && wait_on(&sm.o_full[ub], (j >> 1) & 1, p.err, abort_flag);
       tc_fence_after();
-      float v[16];
+      float v[16], vc[8];
       tmem_ld16(tO, v);
+      if (kNO > 16) tmem_ld8(tO + 16, vc);
       tc_wait_ld();
+      auto column = [&](int n) { return n < 16 ? v[n < 16 ? n : 0] : vc[n >= 16 ? n - 16 : 0]; };
       float o[G], lt[8], mh[G];
       #pragma unroll
       for (int c = 0; c < (G + 3) / 4; ++c) {
@@ -851,7 +887,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         mh[h] = h & 1 ? m[h / 2].y : m[h / 2].x;
         const float moh = h & 1 ? mo[h / 2].y : mo[h / 2].x;
         // O carries 2^(kTop - mo), the normaliser 2^-m
-        const float num = fmaf(v[8 + h], 1.f / kLo, v[h]) * exp2f(moh - mh[h] - kTop);
+        const float sum = fmaf(fmaf(column(2 * G + h), 1.f / kPart, column(G + h)), 1.f / kPart, column(h));
+        const float num = sum * exp2f(moh - mh[h] - kTop);
         o[h] = lt[h] == 0.f ? 0.f : __fdividef(num, lt[h]);
       }
       tc_fence_before();

@@ -101,8 +101,9 @@ __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, 
       : "memory");
 }
 
-// D[tmem] (+)= A[smem] x B[smem]^T (kind::f8f6f4: here e4m3 A and B, fp32
-// accumulate; K = 32 per instruction), issued by one thread.
+// D[tmem] (+)= A[smem] x B[smem]^T (kind::f8f6f4: 8-bit A and B, each of the
+// type that idesc names, fp32 accumulate; K = 32 per instruction), issued by
+// one thread.
 __device__ __forceinline__ void tc_mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                              uint32_t idesc, bool accumulate) {
   asm volatile(
@@ -252,6 +253,11 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn, int
 // Instruction descriptor, kind::f8f6f4: e4m3 A and B (format 0), fp32 D.
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, int a_mn, int b_mn) {
   return idesc_f16_f32(M, N, a_mn, b_mn);  // the same fields, element format code 0
+}
+
+// The same with e5m2 B (format 1).
+__host__ __device__ constexpr uint32_t idesc_e4m3_e5m2_f32(int M, int N, int a_mn, int b_mn) {
+  return idesc_e4m3_f32(M, N, a_mn, b_mn) | (1u << 10);
 }
 
 }  // namespace pkv

@@ -1,0 +1,123 @@
+"""Attention over the block-scaled e4m3 cache on the rows that a number format
+or a mask can spoil: one heavy key beside a long tail of light ones."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_195_gb300 as pkv
+
+import blk_reference as ref
+from test_gpu_block import Cache, _attend, _built, _rows  # noqa: F401  (_built: the module's fixture)
+
+pytestmark = pytest.mark.gpu
+BS = 16
+
+
+def _plain(c, q, rows, scale):
+    """Outputs in 64 bits and, element by element, how far a computation may
+    be off that holds scores and sums in 32 bits and a weight in f16's eleven
+    bits: half a bf16 step of the output (2^-8), of the weighted mean of |V|
+    the f16 half step (2^-11) and the scores' error (an fp32 sum of 128
+    products, 2^-20 of their magnitudes, twice: in the weight and in the
+    normaliser; as much for q's elements below 2^-9 of the largest's binade,
+    which its pair of e4m3 numbers holds to 2^-17 of that; 2^-16 for exp2 of
+    the scores here, below 2^7), and for each weight 2^-33 of the largest
+    (times value scale), where f16 ends."""
+    out, bound = np.zeros(rows.shape), np.zeros(rows.shape)
+    hkv = c.pools[0].shape[1]
+    g, t = rows.shape[1] // hkv, 0
+    for r, (n, m) in enumerate(zip(c.lens, q)):
+        ids = c.table[r, :-(-n // BS)]
+        sees = np.arange(n)[None] <= np.arange(n - m, n)[:, None]
+        for k in range(hkv):
+            K, V = (ref.E4M3[p[ids, k]].reshape(-1, 128)[:n] for p in c.pools)
+            ks, vs = (np.repeat(s[ids, k].astype(np.float64), BS)[:n] for s in c.scales)
+            for h in range(k * g, k * g + g):
+                x = rows[t:t + m, h]
+                s = np.where(sees, scale * (x @ (K * ks[:, None]).T), -np.inf)
+                w = np.exp(s - s.max(1, keepdims=True))
+                w /= w.sum(1, keepdims=True)
+                o = np.where(w > 0, w, 0) @ (V * vs[:, None])
+                mag = np.where(sees, abs(scale) * (np.abs(x) @ np.abs(K * ks[:, None]).T), 0).max(1, keepdims=True)
+                unit = 2.0 ** np.floor(np.log2(np.maximum(np.abs(x).max(1, keepdims=True), 2.0 ** -100)))
+                fine = np.where(np.abs(x) < unit * 2.0 ** -9, unit, 0) @ np.abs(K * ks[:, None]).T
+                ds = mag * 2.0 ** -20 + abs(scale) * np.where(sees, fine, 0).max(1, keepdims=True) * 2.0 ** -17
+                floor = 2.0 ** -33 * (w * vs).max(1, keepdims=True) * (sees @ np.abs(V))
+                out[t:t + m, h] = o
+                bound[t:t + m, h] = 2.0 ** -8 * np.abs(o) + floor + \
+                    (2.0 ** -11 + 2 * ds + 2.0 ** -16) * (1 + 2.0 ** -7) * (w @ np.abs(V * vs[:, None]))
+        t += m
+    return out, bound
+
+
+def _sinks(rng, n, m, g, hkv, at, shares):
+    """One request of n keys whose last m tokens attend: the key at position
+    `at` has value 0 and takes the head's share of the weight, the other keys'
+    scores are normal.  (Dim 0 of K is the heavy key's alone, so q's dim 0
+    sets its score.)"""
+    c = Cache(rng, [n], hkv, spread=0.0)
+    ids = c.table[0]
+    K = c.pools[0][ids].transpose(1, 0, 2, 3).reshape(hkv, -1, 128)
+    K[:, :, 0], K[:, at] = 0, 0
+    K[:, at, 0] = ref.encode(np.array([448.0]))[0]
+    c.pools[0][ids] = K.reshape(hkv, -1, BS, 128).transpose(1, 0, 2, 3)
+    c.pools[1][ids[at // BS], :, at % BS] = 0
+    scale = 0.09
+    rows = _rows(rng, m, g * hkv).double().numpy()
+    rows[:, :, 0] = 0
+    for h in range(g * hkv):
+        s = scale * rows[:, h] @ (ref.E4M3[K[h // g, :n - m + 1]] * 2.0 ** -7).T
+        share = shares[h % len(shares)]
+        rows[:, h, 0] = np.log(share / (1 - share) * np.exp(s).sum(1)) / (scale * 448 * 2.0 ** -7)
+    return c, torch.tensor(rows).bfloat16(), scale
+
+
+def _check_tight(c, q, rows, scale, norm=True):
+    got = _attend(c, q, rows, scale)
+    torch.cuda.synchronize()
+    assert pkv.pkv_get_device_error() == 0, pkv.pkv_last_error()
+    want, bound = _plain(c, q, rows.double().numpy(), scale)
+    got = got.double().cpu().numpy()
+    off = np.abs(got - want)
+    assert (off <= bound).all(), ((off / bound).max(), np.unravel_index((off / bound).argmax(), off.shape))
+    if norm:  # independent roundings: the output's 2^-8, the weights' below it
+        rel = np.linalg.norm(got - want, axis=2) / np.linalg.norm(want, axis=2)
+        assert rel.max() <= 2.0 ** -8 + 2.0 ** -9, rel
+
+
+@pytest.mark.parametrize("g", [1, 4, 5, 6, 8])
+@pytest.mark.parametrize("n,at", [(512, 0), (4096, 0), (4096, 4000), (32768, 0), (32768, 20000), (131072, 5)])
+def test_attention_one_heavy_key_beside_a_long_tail(n, at, g, pkv_opts):
+    # On one CTA, so that the heavy key and the tail share their references.
+    rng = np.random.default_rng(n + at + g)
+    c, rows, scale = _sinks(rng, n, 1, g, 1, at, [0.9, 0.97, 0.5, 0.8, 0.999])
+    pkv_opts(decode_grid=1)
+    _check_tight(c, [1], rows, scale)
+
+
+@pytest.mark.parametrize("m", [1, 5, 7, 8, 40])
+def test_attention_heavy_keys_whatever_kernel_serves_the_row(m):
+    # one token, drafts, chunks; split over the grid as the step's plan has it
+    rng = np.random.default_rng(m)
+    c, rows, scale = _sinks(rng, 6000, m, 6, 2, 3, [0.97, 0.9, 0.5])
+    _check_tight(c, [m], rows, scale)
+
+
+def test_attention_heavy_keys_of_more_rows_than_ctas():
+    rng = np.random.default_rng(77)
+    parts = [_sinks(rng, n, 1, 4, 2, 0, [0.97, 0.9, 0.5, 0.999]) for n in rng.integers(500, 3000, 12)]
+    c = parts[0][0]
+    lens, tables, base = [], [], 0
+    cols = max(p[0].table.shape[1] for p in parts)
+    for p, _, _ in parts:
+        t = np.full((1, cols), -9, np.int32)
+        t[:, :p.table.shape[1]] = np.where(p.table >= 0, p.table + base, -9)
+        tables.append(t)
+        lens += p.lens
+        base += len(p.pools[0])
+    c.pools = [np.concatenate([p[0].pools[i] for p in parts]) for i in range(2)]
+    c.scales = [np.concatenate([p[0].scales[i] for p in parts]) for i in range(2)]
+    pick = rng.permutation(np.repeat(np.arange(12), 30))  # 360 requests, 720 rows and KV heads
+    c.table, c.lens = np.concatenate(tables)[pick], [lens[i] for i in pick]
+    rows = torch.cat([parts[i][1] for i in pick])
+    _check_tight(c, [1] * len(pick), rows, parts[0][2])

@@ -848,9 +848,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (h + 1 < G) put(c * G + h + 1, part[c] >> 8);
           }
         }
-        // Keys past the request's end inside its last block may hold anything
-        // (NaN codes too): their V rows become zero, so that 0 * V stays 0.
-        if (x < pc.nblk && pos >= pc.L) {
+        // Keys that the row does not see inside its last block -- later tokens of
+        // the request, or what lies past its end -- may hold anything (NaN codes
+        // too): their V rows become zero, so that 0 * V stays 0.
+        if (x < pc.nblk && pos >= pc.limit) {
           const int n = 2 * t + 1, sv = n % kSlots;
           ok = ok && wait_on(&sm.full[sv], (n / kSlots) & 1, p.err, abort_flag);
           zero_row(sm.slot[sv], row);

@@ -1,5 +1,6 @@
 """Attention over the block-scaled e4m3 cache on the rows that a number format
-or a mask can spoil: one heavy key beside a long tail of light ones."""
+or a mask can spoil: one heavy key beside a long tail of light ones, NaN in
+keys that a row must not see."""
 import numpy as np
 import pytest
 import torch
@@ -121,3 +122,37 @@ def test_attention_heavy_keys_of_more_rows_than_ctas():
     c.table, c.lens = np.concatenate(tables)[pick], [lens[i] for i in pick]
     rows = torch.cat([parts[i][1] for i in pick])
     _check_tight(c, [1] * len(pick), rows, parts[0][2])
+
+
+def _check_nan_stays_behind(n, m, g, hkv, bad):
+    """NaN codes stored for tokens `bad` (counted from the first of the m that
+    attend) of the middle one of three requests: every row that comes before
+    the first of them is bit for bit what it was, a value's NaN reaches the
+    rows that see it in its own dim alone, a key's in every dim."""
+    rng = np.random.default_rng(n + 31 * m + g)
+    c = Cache(rng, [40, n, 300], hkv)
+    q = [1, m, 1]
+    rows = _rows(rng, m + 2, g * hkv)
+    clean = _attend(c, q, rows, 0.09).cpu()
+    assert clean.isfinite().all()
+    at = [(c.table[1, (n - m + i) // BS], hkv - 1, (n - m + i) % BS) for i in bad]
+    mine = slice((hkv - 1) * g, hkv * g)
+    for tensor in (1, 0):
+        keep = c.pools[tensor].copy()
+        for j, a in enumerate(at):
+            c.pools[tensor][a][(j * 50 + 7) % 128] = 0x7F if j % 2 else 0xFF
+        got = _attend(c, q, rows, 0.09).cpu()
+        c.pools[tensor] = keep
+        nan = torch.zeros(clean.shape, dtype=torch.bool)
+        for j, i in enumerate(bad):
+            nan[1 + i:1 + m, mine, (j * 50 + 7) % 128 if tensor else slice(None)] = True
+        assert (got.isnan() == nan).all(), (tensor, (got.isnan() != nan).nonzero()[:5])
+        assert torch.equal(got[~nan].view(torch.int16), clean[~nan].view(torch.int16))
+    assert pkv.pkv_get_device_error() == 0
+
+
+@pytest.mark.parametrize("g,hkv", [(1, 1), (4, 2), (7, 1)])
+@pytest.mark.parametrize("n,m,bad", [(2, 2, [1]), (40, 3, [1, 2]), (33, 7, [0, 3, 6]), (130, 5, [2]), (129, 7, [6]),
+                                     (3000, 6, [1, 4])])
+def test_attention_nan_of_a_later_draft_token_stays_behind(n, m, bad, g, hkv):
+    _check_nan_stays_behind(n, m, g, hkv, bad)

@@ -41,6 +41,12 @@
 // the softmax may be waiting for one of them to rescale O, and splits that Q
 // only afterwards.
 //
+// NaN.  A masked probability is 0, and 0 times a NaN code would spoil rows that
+// must not see its key.  So the converters set the NaN codes of keys that only
+// some of an item's rows see to zero, and note in which dims and from which
+// token on; the epilogue writes the NaNs of those rows.  (Keys that every row
+// sees are left alone, keys that none does become zero.)
+//
 // A step with fewer items than CTAs cuts the longer ones over their keys, into
 // equal parts of four key tiles or more, each an item of the queue; a part leaves its
 // normalised output and (maximum, normaliser) per row in the workspace, and the
@@ -95,6 +101,8 @@ constexpr int kStagesV = 2;              // V stages (codes)
 constexpr int kItems = 4;                // item ring
 constexpr int kAhead = 4;                // an item is published this many tiles before the
                                          // previous one's last copies
+constexpr int kNanRing = 3;              // items whose NaN notes are held (see note_nans)
+constexpr int kNoNan = 255;
 constexpr int kScaleRing = 8;            // tiles whose scales are held
 constexpr int kMaxSplit = 16;            // parts of an item's keys
 constexpr int kMinPart = 4;              // key tiles a part is worth
@@ -137,6 +145,11 @@ struct __align__(1024) Smem {
   int longest_part;                  // key tiles of a split item's longest part (0: none is)
   uint2 extents[kThreads / 32];      // key tiles, the longest request's, by warp
   int last[4];                       // [quad]: the last part to arrive
+  // NaN values among the keys that only some rows see, by converter warp: the
+  // item that the notes are of; a dim's first such key, counted from the first
+  // token's own.
+  int nan_item[kNanRing][kConvWarps];
+  __align__(16) uint8_t nan_from[kNanRing][kConvWarps][kHeadDim];
   WaitCtl wait;
 };
 
@@ -221,6 +234,54 @@ __device__ __forceinline__ void wait_ld32(float (&a)[16], float (&b)[16]) {
                  "+f"(b[14]), "+f"(b[15])
                :
                : "memory");
+}
+
+// Bit 7 of every byte whose code is NaN.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
+// A converter warp's 32 rows `row` on of a staged V tile (first key `key0`),
+// whose rows beyond the first token's own position pos0 and below `end` hold a
+// NaN code somewhere: those codes become zero, and are noted for item n.  Notes
+// of item n - kNanRing are no longer read: a converter is two tiles ahead of PV
+// at most, hence past item n - 1 only when item n - 2's probabilities are out,
+// which follow item n - 3's epilogue.
+static __device__ __noinline__ void note_nans(Smem& sm, uint8_t* tile, int row, int key0, int pos0, int end,
+                                              int n) {
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kWarpConv;
+  uint32_t* const from = reinterpret_cast<uint32_t*>(sm.nan_from[n % kNanRing][w]) + lane;  // 4 dims a lane
+  const bool first = sm.nan_item[n % kNanRing][w] != n;
+  __syncwarp();
+  if (first) {
+    *from = kNoNan * 0x01010101u;
+    if (lane == 0) sm.nan_item[n % kNanRing][w] = n;
+  }
+  for (int i = row; i < row + 32; ++i) {
+    const int key = key0 + i;
+    if (key <= pos0 || key >= end) continue;
+    uint32_t* const at = reinterpret_cast<uint32_t*>(tile + i * 128 + (((lane >> 2) ^ (i & 7)) * 16)) + (lane & 3);
+    const uint32_t bad = nan_bytes(*at) >> 7;
+    if (bad == 0) continue;
+    *at &= ~(bad * 0xffu);
+    *from = __vminu4(*from, (uint32_t)(key - pos0) * bad | ~(bad * 0xffu));
+  }
+  __syncwarp();
+}
+
+// The noted NaNs of item n into a row's 32 output dims.
+__device__ __forceinline__ void put_nans(const Smem& sm, int n, int part, int token, float (&x0)[16],
+                                         float (&x1)[16]) {
+  #pragma unroll 1
+  for (int w = 0; w < kConvWarps; ++w) {
+    if (sm.nan_item[n % kNanRing][w] != n) continue;
+    const uint8_t* from = sm.nan_from[n % kNanRing][w] + part * kPartKeys;
+    #pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (from[i] <= token) x0[i] = __int_as_float(0x7fc00000);
+      if (from[16 + i] <= token) x1[i] = __int_as_float(0x7fc00000);
+    }
+  }
 }
 
 // The exponent of a block's value scale: 2^lv <= vs < 2^(lv + 1) (0 and
@@ -337,6 +398,7 @@ static __device__ __noinline__ void finish_part(Smem& sm, const PrefillBlockPara
   tc_fence_before();
   __syncwarp();
   if (lane == 0) mbar_arrive(&sm.o_empty);
+  put_nans(sm, n, part, row / G, x0, x1);
   const Item& it = sm.items[n % kItems];
   if (quad * 32 >= it.nt * G) return;  // no query in these rows
   const int slot = it.slot, parts = it.parts;
@@ -492,6 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.o_full, 1);
     mbar_init(&sm.o_empty, kSoftWarps);
     mbar_init(&sm.mma_done, 1);
+    for (int i = 0; i < kNanRing * kConvWarps; ++i) sm.nan_item[i / kConvWarps][i % kConvWarps] = -1;
     sm.wait.abort = 0;
     sm.wait.limit_ns = p.wait_limit_ns;
     fence_barrier_init();
@@ -790,14 +853,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         #pragma unroll 1
         for (int row = row0; row < kKeyTile; row += kConvThreads) {
-          // A key row widened: past the request's end a block may hold
+          // A key row widened: past the item's last key a block may hold
           // anything (NaN codes too), and 0 * V has to stay 0.
-          const bool keep = ((kSplit ? it.j0 : 0) + j) * kKeyTile + row < it.L;
+          const int key0 = ((kSplit ? it.j0 : 0) + j) * kKeyTile, end = it.pos0 + it.nt;
+          const bool keep = key0 + row < end;
           const int sw = row & 7;
           uint4 c[8];
-          #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            c[i] = keep ? lds128(sm.v[st] + row * 128 + ((i ^ sw) * 16)) : make_uint4(0, 0, 0, 0);
+          auto fetch = [&]() {
+            #pragma unroll
+            for (int i = 0; i < 8; ++i)
+              c[i] = keep ? lds128(sm.v[st] + row * 128 + ((i ^ sw) * 16)) : make_uint4(0, 0, 0, 0);
+          };
+          fetch();
+          uint32_t bad = 0;
+          if (key0 + row > it.pos0) {  // seen by some of the item's rows only
+            #pragma unroll
+            for (int i = 0; i < 8; ++i)
+              bad |= nan_bytes(c[i].x) | nan_bytes(c[i].y) | nan_bytes(c[i].z) | nan_bytes(c[i].w);
+          }
+          if (__any_sync(0xffffffffu, bad != 0)) {
+            note_nans(sm, sm.v[st], row - lane, key0, it.pos0, end, n);
+            fetch();
+          }
           #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
@@ -983,6 +1060,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.o_empty);
+        put_nans(sm, n, part, t_local, x0, x1);
         if (valid && ok) {
           #pragma unroll
           for (int i = 0; i < 16; i += 8) {

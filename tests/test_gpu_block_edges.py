@@ -156,3 +156,38 @@ def _check_nan_stays_behind(n, m, g, hkv, bad):
                                      (3000, 6, [1, 4])])
 def test_attention_nan_of_a_later_draft_token_stays_behind(n, m, bad, g, hkv):
     _check_nan_stays_behind(n, m, g, hkv, bad)
+
+
+@pytest.mark.parametrize("g,hkv", [(1, 1), (4, 2), (7, 1), (8, 1)])
+@pytest.mark.parametrize("n,m,bad", [(8, 8, [7]), (40, 20, [1, 2, 19]), (33, 33, [0, 16, 32]), (130, 30, [2, 28, 29]),
+                                     (400, 300, [0, 15, 16, 17, 127, 128, 129, 200, 299]), (900, 17, [5]),
+                                     (9000, 40, [1, 33])])
+def test_attention_nan_of_a_later_chunk_token_stays_behind(n, m, bad, g, hkv):
+    # items of one tile and of several, whole and split over their keys
+    _check_nan_stays_behind(n, m, g, hkv, bad)
+
+
+@pytest.mark.parametrize("split", [False, True])
+def test_attention_nan_in_some_of_many_chunks(split):
+    # Several items per SM, in a row on the same notes; every fourth request
+    # holds NaN values at two of its tokens.
+    rng = np.random.default_rng(5)
+    R, g, hkv = (12, 4, 2) if split else (150, 2, 3)
+    q = [int(x) for x in rng.integers(9, 200, R)]
+    lens = [n + int(x) for n, x in zip(q, rng.integers(0, 2000 if split else 150, R))]
+    c = Cache(rng, lens, hkv)
+    rows = _rows(rng, sum(q), g * hkv)
+    clean = _attend(c, q, rows, 0.09).cpu()
+    nan = torch.zeros(clean.shape, dtype=torch.bool)
+    start = np.concatenate([[0], np.cumsum(q)])
+    for r in range(0, R, 4):
+        for d in (3, 90):
+            i, k = int(rng.integers(0, q[r])), int(rng.integers(0, hkv))
+            pos = lens[r] - q[r] + i
+            c.pools[1][c.table[r, pos // BS], k, pos % BS, d + k] = 0x7F
+            nan[start[r] + i:start[r + 1], k * g:k * g + g, d + k] = True
+    for _ in range(3):
+        got = _attend(c, q, rows, 0.09).cpu()
+        assert (got.isnan() == nan).all(), (got.isnan() != nan).nonzero()[:5]
+        assert torch.equal(got[~nan].view(torch.int16), clean[~nan].view(torch.int16))
+    assert pkv.pkv_get_device_error() == 0

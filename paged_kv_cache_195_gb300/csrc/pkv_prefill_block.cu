@@ -94,6 +94,7 @@ constexpr uint32_t kColO = 256, kColP = 384;
 constexpr float kMargin = 8.0f;          // log2 of the largest exp2(s - m) allowed
 constexpr float kTop = 6.0f;             // P carries 2^kTop: below 2^(kMargin + 1 + kTop) = 2^15
 constexpr float kNegBig = -1.0e30f;
+constexpr float kTopF = 100.f;           // log2 of the largest F, about
 constexpr float kMostF = 0x1p100f;
 constexpr int kPastEnd = INT_MIN;        // block-table slot past the request (not read)
 constexpr int kStages = 3;               // K stages
@@ -929,12 +930,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float qf = sm.qf[n % kItems][row];
       float m = kNegBig, mo = kNegBig, l = 0.f, root = 0.f;
       // The tile at hand: this part's 32 scores (two blocks of 16 keys), and
-      // the blocks' factors of a score and of a probability.
-      float x0[16], x1[16], sc0, sc1, f0, f1;
+      // the blocks' factors of a score and of a probability, and what is added
+      // to a score.
+      float x0[16], x1[16], sc0, sc1, f0, f1, up0, up1;
       // Tile tt's scores taken from the registers they were fetched to:
       // masked, the references raised where the maxima exceed them by
       // 2^kMargin.  (A factor of 0 would turn a masked -inf into NaN; 1e-30
-      // leaves the scores 0.)
+      // leaves the scores below 2^-70.)
       auto take = [&](int tt, int g) {
         ok = ok && mbar_wait(&sm.sc_full[g % kScaleRing], (g / kScaleRing) & 1, p.err, abort_flag);
         const float2 ks = *reinterpret_cast<const float2*>(&sm.sc[g % kScaleRing][0][part * 2]);
@@ -945,8 +947,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&sm.s_free[g & 1]);
         sc0 = qf * ks.x;
         sc1 = qf * ks.y;
-        if (sc0 == 0.f) sc0 = 1e-30f;
-        if (sc1 == 0.f) sc1 = 1e-30f;
+        if (sc0 < 1e-30f) sc0 = 1e-30f;
+        if (sc1 < 1e-30f) sc1 = 1e-30f;
         const float lv0 = scale_exponent(vs.x), lv1 = scale_exponent(vs.y);
         const int kbase = tt * kKeyTile + part * kPartKeys;
         if (kbase + kPartKeys - 1 > prow) {
@@ -990,11 +992,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           // 2^up in two factors: either alone is in range
           root = fast_exp2(0.5f * (m - mo + kTop));
         }
-        // F, held to 2^100: a probability is then so small that P stays finite.
+        // What F has beyond 2^100 joins the exponent: P is below 2^15, so these
+        // probabilities are below 2^-84 of the normaliser with it or without.
         f0 = root * vs.x * root;
         f1 = root * vs.y * root;
-        if (f0 > kMostF) f0 = kMostF;
-        if (f1 > kMostF) f1 = kMostF;
+        up0 = up1 = -m;
+        auto reach = [&](float& up, float& f, float v) {
+          if (f > kMostF) {
+            up += m - mo + kTop + scale_exponent(v) - kTopF;
+            f = kMostF * __uint_as_float((__float_as_uint(v) & 0x7fffffu) | 0x3f800000u);
+          }
+        };
+        if (f0 > kMostF || f1 > kMostF) {
+          reach(up0, f0, vs.x);
+          reach(up1, f1, vs.y);
+        }
       };
       const uint32_t tS = lanes + part * kPartKeys;
       ok = ok && mbar_wait(&sm.s_full[t & 1], (t >> 1) & 1, p.err, abort_flag);
@@ -1007,13 +1019,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int b = t & 1;
         const bool more_keys = j + 1 < nj;
         const uint32_t next = tS + (b ^ 1) * kKeyTile;
-        // p = exp2(s - m) into the normaliser, P = p F in f16, two keys per
+        // p = exp2(s + up) into the normaliser, P = p F in f16, two keys per
         // column, one block after the other; each block's registers take the
         // next tile's scores.
-        const float2 nm2 = make_float2(-m, -m);
         float2 sum = make_float2(0.f, 0.f);
         uint32_t w[kPartKeys / 2];
-        auto block = [&](const float (&x)[16], float sc, float f, int at) {
+        auto block = [&](const float (&x)[16], float sc, float f, float up, int at) {
+          const float2 nm2 = make_float2(up, up);
           #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float2 y = ffma2(make_float2(x[2 * e], x[2 * e + 1]), make_float2(sc, sc), nm2);
@@ -1022,13 +1034,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             w[at + e] = pack_f16x2(fmul2(q, make_float2(f, f)));
           }
         };
-        block(x0, sc0, f0, 0);
+        block(x0, sc0, f0, up0, 0);
         if (more_keys) {
           ok = ok && mbar_wait(&sm.s_full[b ^ 1], ((t + 1) >> 1) & 1, p.err, abort_flag);
           tc_fence_after();
           tmem_ld16(next, x0);
         }
-        block(x1, sc1, f1, 8);
+        block(x1, sc1, f1, up1, 8);
         if (more_keys) tmem_ld16(next + 16, x1);
         l += sum.x + sum.y;
         // P buffer b was last read by the PV of two tiles before.

@@ -14,15 +14,15 @@ pytestmark = pytest.mark.gpu
 BS = 16
 
 
-def _plain(c, q, rows, scale):
+def _plain(c, q, rows, scale, exp2_off=2.0 ** -16):
     """Outputs in 64 bits and, element by element, how far a computation may
     be off that holds scores and sums in 32 bits and a weight in f16's eleven
     bits: half a bf16 step of the output (2^-8), of the weighted mean of |V|
     the f16 half step (2^-11) and the scores' error (an fp32 sum of 128
     products, 2^-20 of their magnitudes, twice: in the weight and in the
     normaliser; as much for q's elements below 2^-9 of the largest's binade,
-    which its pair of e4m3 numbers holds to 2^-17 of that; 2^-16 for exp2 of
-    the scores here, below 2^7), and for each weight 2^-33 of the largest
+    which its pair of e4m3 numbers holds to 2^-17 of that; exp2_off for
+    exp2 of the scores, 2^-16 where they are below 2^7), and for each weight 2^-33 of the largest
     (times value scale), where f16 ends."""
     out, bound = np.zeros(rows.shape), np.zeros(rows.shape)
     hkv = c.pools[0].shape[1]
@@ -46,7 +46,7 @@ def _plain(c, q, rows, scale):
                 floor = 2.0 ** -33 * (w * vs).max(1, keepdims=True) * (sees @ np.abs(V))
                 out[t:t + m, h] = o
                 bound[t:t + m, h] = 2.0 ** -8 * np.abs(o) + floor + \
-                    (2.0 ** -11 + 2 * ds + 2.0 ** -16) * (1 + 2.0 ** -7) * (w @ np.abs(V * vs[:, None]))
+                    (2.0 ** -11 + 2 * ds + exp2_off) * (1 + 2.0 ** -7) * (w @ np.abs(V * vs[:, None]))
         t += m
     return out, bound
 
@@ -73,11 +73,11 @@ def _sinks(rng, n, m, g, hkv, at, shares):
     return c, torch.tensor(rows).bfloat16(), scale
 
 
-def _check_tight(c, q, rows, scale, norm=True):
+def _check_tight(c, q, rows, scale, norm=True, **kw):
     got = _attend(c, q, rows, scale)
     torch.cuda.synchronize()
     assert pkv.pkv_get_device_error() == 0, pkv.pkv_last_error()
-    want, bound = _plain(c, q, rows.double().numpy(), scale)
+    want, bound = _plain(c, q, rows.double().numpy(), scale, **kw)
     got = got.double().cpu().numpy()
     off = np.abs(got - want)
     assert (off <= bound).all(), ((off / bound).max(), np.unravel_index((off / bound).argmax(), off.shape))
@@ -191,3 +191,24 @@ def test_attention_nan_in_some_of_many_chunks(split):
         assert (got.isnan() == nan).all(), (got.isnan() != nan).nonzero()[:5]
         assert torch.equal(got[~nan].view(torch.int16), clean[~nan].view(torch.int16))
     assert pkv.pkv_get_device_error() == 0
+
+
+@pytest.mark.parametrize("q", [[1], [5], [8], [30], [300], [64, 1, 40]])
+@pytest.mark.parametrize("apart", [80, 100, 110, 124])
+def test_attention_value_scales_as_far_apart_as_the_weights(apart, q):
+    # Blocks whose keys weigh 2^-apart of the heaviest ones' and whose value
+    # scales are 2^apart times theirs, so that both carry the output.
+    rng = np.random.default_rng(apart + len(q))
+    c = Cache(rng, [n + 600 for n in q], 2, spread=0.0)
+    for i, n in enumerate(c.lens):
+        for b, x in enumerate(c.table[i, :-(-n // BS)]):
+            heavy = b % 3 == 0
+            c.scales[1][x] = (1 + rng.random(2)) * 2.0 ** (-65 if heavy else apart - 65 + int(rng.integers(-2, 3)))
+            c.pools[0][x, :, :, 0] = ref.encode(np.array([384.0 if heavy else -384.0]))[0]
+    rows = _rows(rng, sum(q), 8, 0.25).double()
+    # scores of -s and s, 2 s = apart in log2 units
+    scale = 0.25
+    rows[:, :, 0] = apart / 2 * np.log(2) / (scale * 3)
+    # Scores, shifts and their sums stay below 2^8 in log2 units: four
+    # roundings of them, 2^-24 relative each, are 2^-14 of a weight.
+    _check_tight(c, q, rows.bfloat16(), scale, norm=False, exp2_off=2.0 ** -14)

@@ -813,18 +813,23 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           if (tt > 0 && grow) {
             tc_fence_after();
-            float o[16], oc[8];
+            auto times = [&](int n, float& x) {
+              if (n < 3 * G) x *= n % G & 1 ? alpha[n % G / 2].y : alpha[n % G / 2].x;
+            };
+            float o[16];
             tmem_ld16(tO, o);
-            if (kNO > 16) tmem_ld8(tO + 16, oc);
             tc_wait_ld();
             #pragma unroll
-            for (int n = 0; n < 3 * G; ++n) {
-              const int h = n % G;
-              const float a = h & 1 ? alpha[h / 2].y : alpha[h / 2].x;
-              if (n < 16) o[n < 16 ? n : 0] *= a; else oc[n >= 16 ? n - 16 : 0] *= a;
-            }
+            for (int n = 0; n < 16; ++n) times(n, o[n]);
             tmem_st16(tO, reinterpret_cast<const uint32_t(&)[16]>(o));
-            if (kNO > 16) tmem_st8(tO + 16, oc);
+            if (kNO > 16) {
+              float oc[8];
+              tmem_ld8(tO + 16, oc);
+              tc_wait_ld();
+              #pragma unroll
+              for (int n = 0; n < 8; ++n) times(16 + n, oc[n]);
+              tmem_st8(tO + 16, oc);
+            }
             tc_wait_st();
           }
           named_barrier(kBarSoftmax, kSoftThreads);  // sm.red is free again

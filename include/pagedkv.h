@@ -114,8 +114,9 @@ int pkv_copy_blocks(const void *k_src, const void *v_src, void *k_dst, void *v_d
 /*
  * Bytes of workspace pkv_attention needs for these dims (split-context
  * partial outputs, their log-sum-exp statistics and per-row merge counters;
- * for steps with more tokens than requests also 10 MB of partial states for
- * prefill work items that pkv_attention_fp8_block splits over their keys).
+ * for steps with more tokens than requests, or fewer but many, also 10 MB of
+ * partial states for prefill work items that pkv_attention_fp8_block splits over
+ * their keys).
  * Depends only on dims and the device's SM count, not on the lengths, so one
  * buffer serves every step of a captured CUDA graph.
  */
@@ -465,7 +466,12 @@ typedef struct pkv_options {
     int32_t prefill_min_q;  /* PKV_PREFILL_MIN_Q (16): requests with at least this many
                                query tokens run in the tensor-core prefill kernel
                                (0: none do); bf16 pools, and block-scaled e4m3
-                               pools from half as many on */
+                               pools from half as many on.  Only in steps whose
+                               num_q_tokens has room for one such request beside a
+                               row for each other request (block-scaled pools: or
+                               is below num_reqs and, times num_kv_heads, 512 at
+                               least); elsewhere the decode serves a chunk, token
+                               by token */
     int32_t align;          /* PKV_ALIGN (1): with uniform row-groups, snap decode ranges
                                to row-group boundaries (block-scaled e4m3 pools: with
                                no more row-groups than CTAs, cut each into pieces of its

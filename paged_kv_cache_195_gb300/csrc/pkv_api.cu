@@ -132,6 +132,18 @@ pkv::WorkspaceLayout layout_for(const pkv_dims* d, int sm_count) {
                                       d->num_q_heads / d->num_kv_heads, sm_count);
 }
 
+// Fewer rows than requests: some sit the step out (pkv_build_step makes such
+// steps), and the rows may all be one chunk's.  The block-scaled attention
+// launches its prefill for that from 512 rows times KV heads on: without it a
+// 512-token chunk on 2000 keys takes 229 us for 34 at eight KV heads and 70 for
+// 31 at two, 64 tokens on 4000 keys 75 for 29 at eight; a step that holds no
+// chunk pays 5.6 us for the launch (100 decodes of 500 keys, eight KV heads: 27
+// for 21; 500 of them 96 for 85).  Below, a chunk loses little or nothing (64
+// tokens on 4000 keys at two KV heads 26 for 28, 40 on 1000 11 for 20).
+bool idle_chunk(const pkv_dims* d) {
+  return d->num_q_tokens < d->num_reqs && (long long)d->num_q_tokens * d->num_kv_heads >= 512;
+}
+
 // Partial states of the block-scaled prefill's split items, behind the rest of
 // the workspace: for steps that may hold a chunk, one part per SM.
 struct PartsLayout {
@@ -141,7 +153,7 @@ struct PartsLayout {
 
 PartsLayout parts_layout(const pkv::WorkspaceLayout& w, const pkv_dims* d, int sm_count) {
   PartsLayout l;
-  l.parts = d->num_q_tokens > d->num_reqs ? kPartsPerSm * sm_count : 0;
+  l.parts = d->num_q_tokens > d->num_reqs || idle_chunk(d) ? kPartsPerSm * sm_count : 0;
   const size_t rows = (size_t)l.parts * pkv::kPrefillRows;
   l.ml = (w.total + 255) & ~(size_t)255;
   l.o = l.ml + rows * sizeof(float2);
@@ -560,8 +572,9 @@ int attention_impl(const void* q, const void* k_pool, const void* v_pool, const 
   // for every other request; otherwise the decode kernel serves every row
   // (it is correct for any q_r, the prefill kernel is only faster).
   // e4m3 pools with scales per head: every row runs in the decode kernel.
+  const long long others = block_scales && idle_chunk(dims) ? 0 : dims->num_reqs - 1;
   const bool run_prefill =
-      (!fp8 || block_scales) && (long long)dims->num_q_tokens - dims->num_reqs + 1 >= (long long)prefill_min_q;
+      (!fp8 || block_scales) && dims->num_q_tokens - others >= (long long)prefill_min_q;
   p.prefill_min_q = run_prefill ? prefill_min_q : 0x7fffffff;
   p.num_slots = w.num_slots;
   p.pdl = opt.pdl != 0;

@@ -28,6 +28,8 @@ def _plain(c, q, rows, scale, exp2_off=2.0 ** -16):
     hkv = c.pools[0].shape[1]
     g, t = rows.shape[1] // hkv, 0
     for r, (n, m) in enumerate(zip(c.lens, q)):
+        if m == 0:
+            continue
         ids = c.table[r, :-(-n // BS)]
         sees = np.arange(n)[None] <= np.arange(n - m, n)[:, None]
         for k in range(hkv):
@@ -212,3 +214,22 @@ def test_attention_value_scales_as_far_apart_as_the_weights(apart, q):
     # Scores, shifts and their sums stay below 2^8 in log2 units: four
     # roundings of them, 2^-24 relative each, are 2^-14 of a weight.
     _check_tight(c, q, rows.bfloat16(), scale, norm=False, exp2_off=2.0 ** -14)
+
+
+@pytest.mark.parametrize("R,q,n,hkv", [(9, 8, 60, 2), (300, 256, 300, 2), (1000, 400, 2000, 2), (65, 64, 70, 8)])
+def test_attention_chunk_among_idle_requests(R, q, n, hkv):
+    # Fewer rows than requests.  From 512 rows times KV heads on the chunk runs
+    # as one: its outputs are bit for bit those of a step that holds nothing else.
+    rng = np.random.default_rng(R)
+    lens = [0] * R
+    lens[R // 2] = n
+    c = Cache(rng, lens, hkv)
+    rows = _rows(rng, q, 3 * hkv)
+    m = [0] * R
+    m[R // 2] = q
+    _check_tight(c, m, rows, 0.09)
+    idle = _attend(c, m, rows, 0.09)
+    c.table, c.lens = c.table[R // 2:R // 2 + 1], [n]
+    alone = _attend(c, [q], rows, 0.09)
+    if q * hkv >= 512:
+        assert torch.equal(idle.view(torch.int16), alone.view(torch.int16))

@@ -353,9 +353,11 @@ int pkv_append_fp8_block(const void *k_new, const void *v_new, const int32_t *bl
  * scales are finite and >= 0 (any, not only powers of two).  Everything else
  * (q, out, lengths, tables, workspace, errors, launch overlap) as in
  * pkv_attention.  The codes enter the products as they are (chunks: V's as
- * f16), q as a pair of e4m3 numbers and a probability with the eleven bits of an
- * f16: off by at most 2^-11 of itself, or by 2^-33 of the row's largest
- * (times value scale) where that is more.  Requests with at least half of
+ * f16); q as two 8-bit numbers, exact for elements from 2^-12 of the row's
+ * largest on and off by at most 2^-20 of that below; a probability with the
+ * eleven bits of an f16, off by at most 2^-11 of itself, or by 2^-31 of the row's
+ * largest (times value scale) where that is more.  A NaN in a key or value
+ * reaches the rows that see it and no other.  Requests with at least half of
  * PKV_PREFILL_MIN_Q query tokens run in the prefill kernel.
  * num_blocks * num_kv_heads * 16 must be below 2^31.
  * Source: as pkv_attention_fp8kv.

@@ -8,12 +8,13 @@
 //
 // S = Q K^T takes the K codes as they lie in the pool (kind::f8f6f4): a row of
 // Q is scaled by a power of two so that its largest element lies in [128,
-// 256) and split into two e4m3 operands, hi = e4m3(q) and lo = e4m3(q - hi),
-// whose products accumulate in one TMEM tile.  bf16's eight bits are hi's four
-// and lo's four, so the split is exact for every element above 2^-10 of the
-// row's largest, and off by at most 2^-18 of the largest below that.  Twice
-// the MMAs at twice the bf16 rate: the tensor time of a bf16 K, none of its
-// widening.  A key's block scale multiplies its column of S in the softmax.
+// 256) and split into two operands, hi = e4m3(q) and lo = e5m2(q - hi), whose
+// products accumulate in one TMEM tile.  bf16's eight bits are hi's four, lo's
+// sign and lo's three, and lo needs e5m2's range where hi is subnormal: the split
+// is exact from 2^-13 of the largest element's binade up, and off by at most
+// 2^-20 of that binade below (lo in e4m3: from 2^-9, and 2^-17).  Twice the MMAs
+// at twice the bf16 rate: the tensor time of a bf16 K, none of its widening.  A
+// key's block scale multiplies its column of S in the softmax.
 //
 // O += P V takes f16: P rows are 128 wide here, and splitting 128 x 128
 // probabilities in the softmax, which sets the pace, would cost more than
@@ -200,11 +201,16 @@ static __device__ __noinline__ void rescale_o(uint32_t tO, float alpha) {
   tc_wait_st();
 }
 
-// Two fp32 to e4m3 codes (the first in the low byte), and back to fp32 what
-// they hold.
+// Two fp32 to e4m3 or e5m2 codes (the first in the low byte).
 __device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
   unsigned short r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t to_e5m2x2(float a, float b) {
+  unsigned short r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;
 }
 
@@ -330,7 +336,7 @@ static __device__ __forceinline__ void split_q(uint8_t* q, float scale_log2, flo
       const float a = f.x * s, b = f.y * s;
       hi[k] = to_e4m3x2(a, b);
       const float2 back = e4m3x2_to_float2(hi[k]);
-      lo[k] = to_e4m3x2(a - back.x, b - back.y);
+      lo[k] = to_e5m2x2(a - back.x, b - back.y);
     }
     uint8_t* const at = q + ((c * 2 + (i >> 1)) ^ sw) * 16 + (i & 1) * 8;
     *reinterpret_cast<uint2*>(at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
@@ -766,7 +772,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // is free as soon as the softmax has taken its scores, well before it sends
     // their P, so S runs ahead of PV by two tiles: with S(t) behind PV(t-1) the
     // softmax waited for it (3500 cycles a tile against 3000).
-    constexpr uint32_t kIdescS = idesc_e4m3_f32(kRows, kKeyTile, 0, 0);
+    constexpr uint32_t kIdescHi = idesc_e4m3_f32(kRows, kKeyTile, 0, 0);
+    constexpr uint32_t kIdescLo = idesc_e5m2_e4m3_f32(kRows, kKeyTile, 0, 0);
     constexpr uint32_t kIdescO = idesc_f16_f32(kRows, kHeadDim, 0, 1);
     // Descriptors of the operands' first chunks: a chunk of 32 bytes of a row
     // is 2 further (16-byte units), a V chunk of 16 keys 128.
@@ -816,8 +823,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t tS = tmem + b * kKeyTile;
           #pragma unroll
           for (int kk = 0; kk < 8; ++kk)  // hi rows, then lo rows
-            tc_mma_f8_ss(tS, da + (kk >> 2) * (kCodes / 16) + (kk & 3) * 2, db + (kk & 3) * 2, kIdescS,
-                         kk > 0);
+            tc_mma_f8_ss(tS, da + (kk >> 2) * (kCodes / 16) + (kk & 3) * 2, db + (kk & 3) * 2,
+                         kk < 4 ? kIdescHi : kIdescLo, kk > 0);
           tc_commit(&sm.k_empty[st]);
           tc_commit(&sm.s_full[b]);
           if (j + 1 == nj) tc_commit(&sm.q_empty[n & 1]);

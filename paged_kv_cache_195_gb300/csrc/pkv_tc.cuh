@@ -255,7 +255,11 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, int a_mn, in
   return idesc_f16_f32(M, N, a_mn, b_mn);  // the same fields, element format code 0
 }
 
-// The same with e5m2 B (format 1).
+// The same with e5m2 A, or B (format 1).
+__host__ __device__ constexpr uint32_t idesc_e5m2_e4m3_f32(int M, int N, int a_mn, int b_mn) {
+  return idesc_e4m3_f32(M, N, a_mn, b_mn) | (1u << 7);
+}
+
 __host__ __device__ constexpr uint32_t idesc_e4m3_e5m2_f32(int M, int N, int a_mn, int b_mn) {
   return idesc_e4m3_f32(M, N, a_mn, b_mn) | (1u << 10);
 }

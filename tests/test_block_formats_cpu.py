@@ -32,3 +32,20 @@ def test_a_probability_keeps_eleven_bits_far_below_the_largest():
     big = x >= 2.0 ** -11
     assert (off[big] <= 2.0 ** -11 * x[big].double()).all()
     assert off[~big].max() <= 2.0 ** -33 * 2.0 ** 11
+
+
+def _e4m3(x):
+    return x.clamp(-448, 448).to(torch.float8_e4m3fn).double()
+
+
+def test_the_pairs_that_hold_q():
+    # bf16 elements of a row whose largest is scaled into [128, 256): decode,
+    # hi + lo / 16; prefill, hi + lo with lo in e5m2.
+    m = torch.arange(128, 256, dtype=torch.float64)
+    for e in range(0, 40):
+        x = m * 2.0 ** -e  # a binade, the largest element's times 2^-e
+        hi = _e4m3(x.float())
+        off = (x - hi - _e4m3((16 * (x - hi)).float()) / 16).abs().max() / 128
+        assert off == 0 if e <= 13 else off <= 2.0 ** -21, e
+        off = (x - hi - (x - hi).float().to(torch.float8_e5m2).double()).abs().max() / 128
+        assert off == 0 if e <= 13 else off <= 2.0 ** -20, e

@@ -20,8 +20,8 @@ def _plain(c, q, rows, scale, exp2_off=2.0 ** -16):
     bits: half a bf16 step of the output (2^-8), of the weighted mean of |V|
     the f16 half step (2^-11) and the scores' error (an fp32 sum of 128
     products, 2^-20 of their magnitudes, twice: in the weight and in the
-    normaliser; as much for q's elements below 2^-9 of the largest's binade,
-    which its pair of e4m3 numbers holds to 2^-17 of that; exp2_off for
+    normaliser; as much for q's elements below 2^-13 of the largest's
+    binade, which the two 8-bit numbers hold to 2^-20 of that; exp2_off for
     exp2 of the scores, 2^-16 where they are below 2^7), and for each weight 2^-33 of the largest
     (times value scale), where f16 ends."""
     out, bound = np.zeros(rows.shape), np.zeros(rows.shape)
@@ -43,8 +43,8 @@ def _plain(c, q, rows, scale, exp2_off=2.0 ** -16):
                 o = np.where(w > 0, w, 0) @ (V * vs[:, None])
                 mag = np.where(sees, abs(scale) * (np.abs(x) @ np.abs(K * ks[:, None]).T), 0).max(1, keepdims=True)
                 unit = 2.0 ** np.floor(np.log2(np.maximum(np.abs(x).max(1, keepdims=True), 2.0 ** -100)))
-                fine = np.where(np.abs(x) < unit * 2.0 ** -9, unit, 0) @ np.abs(K * ks[:, None]).T
-                ds = mag * 2.0 ** -20 + abs(scale) * np.where(sees, fine, 0).max(1, keepdims=True) * 2.0 ** -17
+                fine = np.where(np.abs(x) < unit * 2.0 ** -13, unit, 0) @ np.abs(K * ks[:, None]).T
+                ds = mag * 2.0 ** -20 + abs(scale) * np.where(sees, fine, 0).max(1, keepdims=True) * 2.0 ** -20
                 floor = 2.0 ** -33 * (w * vs).max(1, keepdims=True) * (sees @ np.abs(V))
                 out[t:t + m, h] = o
                 bound[t:t + m, h] = 2.0 ** -8 * np.abs(o) + floor + \
@@ -233,3 +233,17 @@ def test_attention_chunk_among_idle_requests(R, q, n, hkv):
     alone = _attend(c, [q], rows, 0.09)
     if q * hkv >= 512:
         assert torch.equal(idle.view(torch.int16), alone.view(torch.int16))
+
+
+@pytest.mark.parametrize("m", [1, 7, 8, 40])
+@pytest.mark.parametrize("binades", [6, 9, 12])
+def test_attention_one_large_dim_of_q_beside_the_rest(binades, m):
+    # q's dim 0 is 2^binades times the others and meets nothing in K: the
+    # scores are the other dims' alone, none of them below 2^-13 of its binade.
+    rng = np.random.default_rng(binades)
+    c = Cache(rng, [500, 130], 2)
+    c.pools[0][..., 0] = np.where(c.pools[0][..., 0] & 0x7F == 0x7F, c.pools[0][..., 0], 0)
+    rows = _rows(rng, 2 * m, 8)
+    rows = torch.where(rows.abs() < 0.5, 0.5, rows)
+    rows[:, :, 0] = 1.5 * 2.0 ** binades
+    _check_tight(c, [m, m], rows, 0.09, norm=False)

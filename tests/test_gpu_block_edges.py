@@ -257,3 +257,31 @@ def test_attention_one_large_dim_of_q_beside_the_rest(binades, m):
     rows = torch.where(rows.abs() < 0.5, 0.5, rows)
     rows[:, :, 0] = 1.5 * 2.0 ** binades
     _check_tight(c, [m, m], rows, 0.09, norm=False)
+
+
+@pytest.mark.parametrize("m", [1, 3, 20])
+def test_append_and_attention_past_32_bits(m):
+    # the request's blocks lie beyond 2^32 bytes of either pool
+    rng = np.random.default_rng(m)
+    nb, n, hkv = 2_200_000, 70, 1
+    small = Cache(rng, [n], hkv)
+    ids = torch.tensor(nb - 1 - np.arange(5) * 3).cuda()
+    pools = [torch.zeros((nb, hkv, BS, 128), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.zeros((nb, hkv), device="cuda") for _ in range(2)]
+    for big, x in zip(pools + scales, small.pools + small.scales):
+        big[ids] = torch.tensor(x[small.table[0, :5]]).cuda()
+    table = ids.int()[None].contiguous()
+    lens, qsl = torch.tensor([n], dtype=torch.int32).cuda(), torch.tensor([0, m], dtype=torch.int32).cuda()
+    k, v = _rows(rng, m, hkv), _rows(rng, m, hkv)
+    pkv.pkv_append_fp8_block(k.cuda(), v.cuda(), table, lens, qsl, *pools, *scales)
+    rows = _rows(rng, m, 4)
+    got = pkv.pkv_attention_fp8_block(rows.cuda(), *pools, *scales, table, lens, qsl, 0.09)
+    torch.cuda.synchronize()
+    assert pkv.pkv_get_device_error() == 0, pkv.pkv_last_error()
+    codes, sc = ref.append(k.double().numpy(), v.double().numpy(), small.table, [n], [0, m], small.pools, small.scales)
+    for big, x in zip(pools + scales, codes + sc):
+        assert np.array_equal(big[ids].cpu().numpy(), x[small.table[0, :5]])
+        assert int((big != 0).flatten(1).any(1).sum()) == 5
+    small.pools, small.scales = codes, sc
+    want, bound, _ = _plain(small, [m], rows.double().numpy(), 0.09)
+    assert (np.abs(got.double().cpu().numpy() - want) <= bound).all()

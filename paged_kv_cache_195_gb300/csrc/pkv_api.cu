@@ -565,8 +565,9 @@ int attention_impl(const void* q, const void* k_pool, const void* v_pool, const 
   if (prefill_min_q < 1) prefill_min_q = 0x7fffffff;
   // Over block scales the decode reads a request's keys once per query token
   // and the prefill splits long items, so it takes over at half as many (64
-  // requests of 9 tokens, 500-1000 keys, eight KV heads: 53 us for 132; 8 of 4,
-  // 4000 keys: 37 for 48; but 30 of 5, 100-4000 keys, three KV heads: 50 for 33).
+  // requests of 9 tokens, 500-1000 keys, eight KV heads: 55 us for 132; below,
+  // little is left to gain: 8 of 4, 4000 keys, eight KV heads: 40 for 41, four:
+  // 28 for 27; 30 of 5, 100-4000 keys, three KV heads: 32 for 34).
   else if (block_scales) prefill_min_q = prefill_min_q / 2 + prefill_min_q % 2;
   // Launch it only when the step can hold such a request next to one query
   // for every other request; otherwise the decode kernel serves every row

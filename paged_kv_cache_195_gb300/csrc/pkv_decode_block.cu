@@ -50,13 +50,14 @@
 // size 1..8.
 //
 // Bound: HBM for long steps, the chain of latencies (plan, table, tile, S,
-// softmax, PV, merge) for short ones; the tensor pipe is busy 2.5% of the time.
+// softmax, PV, merge) for short ones; the tensor pipe is busy 4% of the time.
 // Measured, e4m3 codes and scales read over time: 128 rows x 2048 keys, two KV
-// heads, 25.7 us = 5.3 TB/s (0.78 of the measured copy rate, launch included;
+// heads, 26.1 us = 5.2 TB/s (0.77 of the measured copy rate, launch included;
 // the kernel for one scale per head, which widens the codes, 30.4 us); 8 rows x
-// 32768 keys, eight KV heads, 84.9 us = 6.3 TB/s (0.93); 1024 rows x 100-500
-// keys, two KV heads, 41.7 us = 3.3 TB/s; 64 rows x 512 keys, two KV heads, 7.9
-// us; four rows of up to 128 keys, 5.0 us.
+// 32768 keys, eight KV heads, 86.4 us = 6.2 TB/s (0.92); 1024 rows x 100-500
+// keys, two KV heads, 42.6 us = 3.2 TB/s; 64 rows x 512 keys, two KV heads, 8.0
+// us; four rows of up to 128 keys, 4.8 us.  (With P in two e4m3 rows 25.9, 86.5,
+// 41.7, 8.0 and 4.8: the third row's stores; eight heads 26.4 against 26.2.)
 //
 // Roles (224 threads, two CTAs per SM): warps 0-3 softmax and epilogue, one
 // key (TMEM lane) per thread; warp 4 plans and issues the copies -- K and V

@@ -52,21 +52,24 @@
 // equal parts of four key tiles or more, each an item of the queue; a part leaves its
 // normalised output and (maximum, normaliser) per row in the workspace, and the
 // last to arrive merges them by log-sum-exp in part order.  (One chunk of 64
-// tokens on 30000 keys, 12 query and two KV heads: 53 us against 333 whole; 16
-// chunks of 16 on 500-2000 keys: 20 against 29.  At two parts per CTA the merges
+// tokens on 30000 keys, 12 query and two KV heads: 51 us against 333 whole; 16
+// chunks of 16 on 500-2000 keys: 21 against 29.  At two parts per CTA the merges
 // cost more than the balance gains: 30 us on those, 44 against 40 on a mixed step.)
 //
 // Bound: the softmax, about 3000 cycles for a tile of 128 x 128 scores of which
 // the tensor pipe is busy a third (16 MMAs of 64 cycles) and the exponentials
-// take 1000; the rest is issue slots (57% used) and the latencies between a
+// take 1000; the rest is issue slots (56% used) and the latencies between a
 // tile's scores, maxima and probabilities.  Hence the pipeline inside each
 // softmax warp: the scores of tile t + 1 are fetched from TMEM, half a tile at a
 // time into the registers that the exponentials of tile t have freed, and P has
 // TMEM columns of its own, so that a score buffer is free as soon as it is read.
 //
 // Measured: eight 512-token chunks after prefixes of up to 4096 tokens, 32 query
-// and 8 KV heads: 143 us = 752 TFLOP/s of the 2 x 2 x 128 flops per visible key
+// and 8 KV heads: 145 us = 742 TFLOP/s of the 2 x 2 x 128 flops per visible key
 // and query head, 0.39 of cuBLAS's bf16 rate (the bf16 prefill kernel: 129 us).
+// Of that, 1 us is the largest factors' way into the exponents; 64 chunks of 9
+// tokens on 500-1000 keys, eight KV heads, take 55.6 us, 52.5 without the notes
+// of NaNs.
 #include <climits>
 
 #include "pkv_internal.h"

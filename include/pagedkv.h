@@ -370,6 +370,93 @@ int pkv_attention_fp8_block(const void *q, const void *k_pool, const void *v_poo
                             cudaStream_t stream);
 
 /*
+ * What lies between a layer's projections and its attention, in one pass over
+ * the step's rows: root-mean-square norm of every query and key head, rotation
+ * by the token's position, and the append of pkv_append.
+ *   n = w * x / sqrt(mean over the head's 128 dims of x^2 + eps)
+ *   pair (a, b): a' = a cos - b sin, b' = b cos + a sin
+ * q [num_q_tokens, num_q_heads, 128], k and v [num_q_tokens, num_kv_heads, 128]:
+ * bf16, a token's heads contiguous, tokens q_stride / k_stride / v_stride
+ * elements apart (multiples of 8), so that the three may be parts of one joint
+ * projection's rows.  q_weight, k_weight [128] bf16, or NULL: no norm.  eps in
+ * [2^-64, 1] (not read without a weight).  positions [num_q_tokens] int64 name
+ * rows of cos_sin [max_position, rotary_dim] fp32: the cos of each pair in the
+ * first half of a row, the sin in the second.  The leading rotary_dim dims (16,
+ * 32, .. 128) are rotated; pair i is dims i and i + rotary_dim / 2, or with
+ * interleaved != 0 dims 2i and 2i + 1.  Computed in fp32 and rounded once.
+ * Queries go to q_out (token stride q_out_stride; may be q with its stride),
+ * keys and values to the pools at slot_mapping [num_q_tokens].  A token whose
+ * slot is negative is padding: nothing of it is written, its position not
+ * looked at.  A slot or position out of range: the token is skipped and
+ * PKV_ERR_DEVICE_BOUNDS recorded.  Read of dims: num_q_tokens, num_q_heads (up
+ * to 4096, any; 0: no queries), num_kv_heads, head_dim, block_size, num_blocks.
+ * Source: LLM 7 - Efficient LLM Serving, sec. 3 "What the Cache Stores" (the
+ * keys that attention reads are the rotated ones).
+ */
+int pkv_norm_rope_append(const void *q, const void *k, const void *v, int64_t q_stride,
+                         int64_t k_stride, int64_t v_stride, const int64_t *positions,
+                         const float *cos_sin, int64_t max_position, int32_t rotary_dim,
+                         int32_t interleaved, const void *q_weight, const void *k_weight, float eps,
+                         const int64_t *slot_mapping, void *q_out, int64_t q_out_stride, void *k_pool,
+                         void *v_pool, const pkv_dims *dims, cudaStream_t stream);
+
+/*
+ * The latent cache.  In place of keys and values a token caches one latent c of
+ * 512 dims and one rotated key of 64, shared by all query heads: a row of 576
+ * bf16 in pool [num_blocks, 16, 576], through the same block tables and slots as
+ * any other cache here (pkv_build_step, pkv_release_blocks).  For head h with
+ * expansion W_h [256, 512] the keys are k_j = (W_h[0:128] c_j, r_j) and the
+ * values v_j = W_h[128:256] c_j.  Two ways to attend give the same result:
+ * absorbed (pkv_attention_latent), the queries taken through W_h[0:128]^T and
+ * the outputs through W_h[128:256] by the caller, which reads 1152 bytes a key
+ * for all heads and suits decodes; and expanded (pkv_expand_latent, then
+ * pkv_attention_expanded), which needs less than a third of the products a (row, key) and
+ * suits chunks.  In these calls dims->head_dim is 576 and num_kv_heads 1.
+ *
+ * pkv_append_latent: of each row of kv [num_q_tokens][512 latent | 64 key] bf16,
+ * rows kv_stride elements apart (a multiple of 8), the latent is normed as in
+ * pkv_norm_rope_append (over its 512 dims, weight [512] bf16 or NULL), the key
+ * rotated (cos_sin [max_position, 64]), and both written to the pool at
+ * slot_mapping.  q_rope [num_q_tokens, num_q_heads, 64], if not NULL and
+ * num_q_heads > 0 (up to 4096), is the queries' part that meets the rotated keys: it is
+ * rotated into q_rope_out (which may be q_rope with its strides); tokens and
+ * heads lie any multiples of 8 elements apart.  Padding and errors as in
+ * pkv_norm_rope_append.
+ */
+int pkv_append_latent(const void *kv, int64_t kv_stride, const int64_t *positions,
+                      const float *cos_sin, int64_t max_position, int32_t interleaved,
+                      const void *weight, float eps, const int64_t *slot_mapping, void *pool,
+                      const void *q_rope, int64_t q_stride, int64_t q_head_stride, void *q_rope_out,
+                      int64_t q_out_stride, int64_t q_out_head_stride, const pkv_dims *dims,
+                      cudaStream_t stream);
+
+/*
+ * Bytes of workspace for pkv_attention_latent and pkv_attention_expanded: the same for all dims on a
+ * device (about 40 MB).  Its first 256 bytes must be zero before the first call
+ * with it, and after a call that ended with PKV_ERR_TIMEOUT; calls leave them
+ * zero.  The rest needs no initialisation, and nothing in it is kept from one
+ * call for the next: one workspace serves any calls (and captured graphs) that
+ * do not overlap.  0 on error.
+ */
+size_t pkv_latent_workspace_size(const pkv_dims *dims);
+
+/*
+ * Absorbed attention over a latent cache: for row (token, head) with query q
+ * [num_q_tokens, num_q_heads, 576] and the rows x_j = (c_j, r_j) of its request,
+ *   s_j = scale <q, x_j>, out [num_q_tokens, num_q_heads, 512] = sum_j softmax(s)_j c_j
+ * over the keys j that the token sees.  num_q_heads 1..128.  Lengths, tables,
+ * causal order, padded steps, errors and launch overlap as in pkv_attention.
+ * Softmax and sums in fp32, weights bf16 in the product (their sum adds the
+ * rounded values).  A NaN or infinity in a cached row reaches the tokens that
+ * see it and no other; what lies behind a request's end is not looked at.
+ * workspace: caller-owned, 256-byte aligned (pkv_latent_workspace_size).
+ */
+int pkv_attention_latent(const void *q, const void *pool, const int32_t *block_tables,
+                         const int32_t *seq_lens, const int32_t *query_start_loc, float scale,
+                         void *out, const pkv_dims *dims, void *workspace, size_t workspace_bytes,
+                         cudaStream_t stream);
+
+/*
  * Bytes of workspace pkv_attention_cascade needs for these dims: the
  * pkv_attention workspace (same head, initialised the same way with
  * pkv_workspace_init), plus partial states for up to 8 chunks of each shared

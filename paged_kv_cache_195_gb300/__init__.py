@@ -22,5 +22,6 @@ from ._binding import (  # noqa: F401
     CascadeWorkspace, pkv_attention_cascade, pkv_append_attention, pkv_append_attention_fp8,
     pkv_get_device_error, pkv_last_error, pkv_workspace_init,
     pkv_build_step, pkv_release_blocks, pkv_append_fp8_block, pkv_attention_fp8_block,
+    LatentWorkspace, pkv_norm_rope_append, pkv_append_latent, pkv_attention_latent,
     Options, get_options, set_options, options,
 )

@@ -32,7 +32,8 @@ EXPORTED = ("pkv_append", "pkv_attention", "pkv_attention_workspace_size",
             "pkv_attention_fp8kv", "pkv_cascade_workspace_size", "pkv_attention_cascade",
             "pkv_append_attention", "pkv_append_attention_fp8", "pkv_get_options",
             "pkv_set_options", "pkv_build_step", "pkv_release_blocks", "pkv_append_fp8_block",
-            "pkv_attention_fp8_block")
+            "pkv_attention_fp8_block", "pkv_norm_rope_append", "pkv_append_latent",
+            "pkv_latent_workspace_size", "pkv_attention_latent")
 
 # Fields of pkv_options, in declaration order (int32 each).
 OPTION_FIELDS = ("pdl", "early_plan", "early_kv", "early_trigger", "plan_cache", "decode_tc",
@@ -115,6 +116,17 @@ def load_library(path: str = LIB_PATH):
         lib.pkv_append_fp8_block.restype = ctypes.c_int
         lib.pkv_attention_fp8_block.argtypes = [vp] * 8 + [ctypes.c_float, vp, dp, vp, sz, vp]
         lib.pkv_attention_fp8_block.restype = ctypes.c_int
+        i64, f32 = ctypes.c_int64, ctypes.c_float
+        lib.pkv_norm_rope_append.argtypes = [vp] * 3 + [i64] * 3 + [vp] * 2 + [i64, i32, i32, vp, vp,
+                                             f32, vp, vp, i64, vp, vp, dp, vp]
+        lib.pkv_norm_rope_append.restype = ctypes.c_int
+        lib.pkv_append_latent.argtypes = [vp, i64, vp, vp, i64, i32, vp, f32, vp, vp, vp, i64, i64,
+                                          vp, i64, i64, dp, vp]
+        lib.pkv_append_latent.restype = ctypes.c_int
+        lib.pkv_latent_workspace_size.argtypes = [dp]
+        lib.pkv_latent_workspace_size.restype = sz
+        lib.pkv_attention_latent.argtypes = [vp] * 5 + [f32, vp, dp, vp, sz, vp]
+        lib.pkv_attention_latent.restype = ctypes.c_int
         lib.pkv_get_options.argtypes = [ctypes.POINTER(Options)]
         lib.pkv_get_options.restype = None
         lib.pkv_set_options.argtypes = [ctypes.POINTER(Options)]
@@ -625,6 +637,236 @@ def pkv_release_blocks(block_tables, seq_lens, keep_lens, free_list, num_free,
     dims = Dims(R, 0, 1, 1, 128, 16, free_list.shape[0], cols)
     _call((_lib or load_library()).pkv_release_blocks, dev, *ptrs, ctypes.byref(dims),
           _raw_stream(stream, dev))
+
+
+# ------------------------------------------------- norm and rotation, latent cache
+LATENT, ROPE = 512, 64  # a cached latent, and the rotated key beside it
+
+
+def _rows(t, name: str, dev: int, dims: tuple):
+    """Checks a bf16 [tokens, *dims] tensor whose tokens may lie apart, each of
+    them contiguous; returns (pointer, elements between tokens)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not _BF16 or t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be a bf16 CUDA tensor on the call's device, got {t.dtype} "
+                         f"on {t.device}")
+    if t.dim() != len(dims) + 1 or tuple(t.shape[1:]) != dims:
+        raise ValueError(f"{name} must be [tokens, {', '.join(map(str, dims))}], got {tuple(t.shape)}")
+    want, strides = 1, t.stride()
+    for n, s in zip(dims[::-1], strides[:0:-1]):
+        if n > 1 and s != want:
+            raise ValueError(f"{name}: a token's row must be contiguous, got strides {strides}")
+        want *= n
+    return t.data_ptr(), strides[0] if t.shape[0] > 1 else want
+
+
+def _overlap(a, b) -> bool:
+    """Whether the address ranges of two tensors meet."""
+    def span(t):
+        n = sum((k - 1) * s for k, s in zip(t.shape, t.stride())) + 1 if t.numel() else 0
+        return t.data_ptr(), t.data_ptr() + n * t.element_size()
+    (a0, a1), (b0, b1) = span(a), span(b)
+    return a0 < b1 and b0 < a1
+
+
+def _shares(a, b) -> bool:
+    """Whether two [tokens, heads, 128] tensors (see _rows) share elements, rather
+    than lie side by side in the rows of one tensor."""
+    if not _overlap(a, b):
+        return False
+    if a.stride(0) != b.stride(0) or a.shape[0] < 2:
+        return True
+    row = a.stride(0) * a.element_size()
+    wa, wb = (t[0].numel() * t.element_size() for t in (a, b))
+    gap = (b.data_ptr() - a.data_ptr()) % row
+    return gap < wa or gap + wb > row
+
+
+def _token_args(positions, cos_sin, slot_mapping, T: int, dev: int):
+    for t, name, dtype in ((positions, "positions", _I64), (slot_mapping, "slot_mapping", _I64)):
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev \
+                or t.dim() != 1 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int64 [tokens] tensor on the call's device")
+        if t.shape[0] != T:
+            raise ValueError(f"{name} needs one entry per token")
+    if not isinstance(cos_sin, torch.Tensor) or cos_sin.dtype is not _F32 or cos_sin.dim() != 2 \
+            or cos_sin.get_device() != dev or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be a contiguous fp32 [positions, rotary dims] tensor on the "
+                         "call's device")
+
+
+def _weight(t, name: str, n: int, dev: int):
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or tuple(t.shape) != (n,) \
+            or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous bf16 [{n}] tensor on the call's device")
+    return t.data_ptr()
+
+
+def _pool(t, name: str, ndim: int, dev: int):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not _BF16 or t.dim() != ndim or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous bf16 tensor of {ndim} dims on the call's device")
+    return t.data_ptr()
+
+
+def pkv_norm_rope_append(q, k, v, positions, cos_sin, slot_mapping, k_pool, v_pool,
+                         q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None,
+                         stream=None):
+    """What lies between a layer's projections and its attention, in one pass:
+    every query and key head of q [T, Hq, 128] and k [T, Hkv, 128] (bf16; views
+    into a joint projection's output will do) is normed (root mean square over
+    its 128 dims, times q_weight / k_weight [128] bf16; None: no norm) and its
+    leading dims are rotated by the token's position (positions [T] int64 into
+    cos_sin [positions, rotary dims] fp32, cos in the first half of a row, sin
+    in the second; pairs are dims i and i + half, or 2i and 2i + 1 if
+    interleaved); the queries go to q_out (default: a new tensor; q itself:
+    in place), keys and v [T, Hkv, 128] into the pools at slot_mapping [T]
+    int64.  A token with a negative slot is padding: nothing of it is written.
+    Returns q_out."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a [tokens, heads, 128] tensor")
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a [tokens, heads, 128] tensor")
+    dev = q.get_device()
+    T, Hq, Hkv = q.shape[0], q.shape[1], k.shape[1]
+    qp, qs = _rows(q, "q", dev, (Hq, 128))
+    kp, ks = _rows(k, "k", dev, (Hkv, 128))
+    vp, vs = _rows(v, "v", dev, (Hkv, 128))
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError("q, k and v disagree on the token count")
+    _token_args(positions, cos_sin, slot_mapping, T, dev)
+    kpool, vpool = _pool(k_pool, "k_pool", 4, dev), _pool(v_pool, "v_pool", 4, dev)
+    if v_pool.shape != k_pool.shape or k_pool.shape[1] != Hkv:
+        raise ValueError("pool shape does not match the new rows")
+    wq, wk = _weight(q_weight, "q_weight", 128, dev), _weight(k_weight, "k_weight", 128, dev)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    op, os_ = _rows(q_out, "q_out", dev, (Hq, 128))
+    if q_out.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    if T and ((op, os_) != (qp, qs) and _shares(q_out, q) or _shares(q_out, k) or _shares(q_out, v)):
+        raise ValueError("q_out may be q, but not overlap the inputs otherwise")
+    nb, _, bs, D = k_pool.shape
+    dims = Dims(0, T, Hq, Hkv, D, bs, nb, 0)
+    _call((_lib or load_library()).pkv_norm_rope_append, dev, qp, kp, vp, qs, ks, vs,
+          positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1],
+          int(bool(interleaved)), wq, wk, eps, slot_mapping.data_ptr(), op, os_, kpool, vpool,
+          ctypes.byref(dims), _raw_stream(stream, dev))
+    return q_out
+
+
+def pkv_append_latent(kv, positions, cos_sin, slot_mapping, pool, weight=None, eps=1e-6,
+                      interleaved=False, q_rope=None, q_rope_out=None, stream=None):
+    """Append to a latent cache: of each token's row of kv [T, 576] (bf16; rows
+    may lie apart) the first 512 dims, the latent, are normed (root mean square,
+    times weight [512] bf16; None: no norm), the last 64 rotated by its position
+    (positions, cos_sin [positions, 64] and interleaved as in
+    pkv_norm_rope_append), and the row written to pool [blocks, 16, 576] at
+    slot_mapping [T] int64.  q_rope [T, heads, 64], the part of the queries that
+    meets the rotated keys (any strides between tokens and heads), is rotated
+    too, into q_rope_out (default: in place).  A token with a negative slot is
+    padding: nothing of it is written."""
+    if not isinstance(kv, torch.Tensor):
+        raise TypeError("kv must be a torch.Tensor")
+    dev = kv.get_device()
+    ptr, stride = _rows(kv, "kv", dev, (LATENT + ROPE,))
+    T = kv.shape[0]
+    _token_args(positions, cos_sin, slot_mapping, T, dev)
+    if cos_sin.shape[1] != ROPE:
+        raise ValueError(f"cos_sin must have {ROPE} columns")
+    pp = _pool(pool, "pool", 3, dev)
+    w = _weight(weight, "weight", LATENT, dev)
+    heads, qp, qs, qo, os_ = 0, None, (0, 0), None, (0, 0)
+    if q_rope is not None:
+        if q_rope_out is None:
+            q_rope_out = q_rope
+        for t, name in ((q_rope, "q_rope"), (q_rope_out, "q_rope_out")):
+            if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.get_device() != dev \
+                    or t.dim() != 3 or t.shape[0] != T or t.shape[2] != ROPE \
+                    or t.shape[1] != q_rope.shape[1] or t.stride(2) != 1:
+                raise ValueError(f"{name} must be a bf16 [tokens, heads, {ROPE}] tensor on kv's device, "
+                                 "its last dim contiguous")
+        heads = q_rope.shape[1]
+        (qp, qs), (qo, os_) = ((t.data_ptr(), tuple(s if n > 1 else 0 for s, n in zip(t.stride(), t.shape[:2])))
+                               for t in (q_rope, q_rope_out))
+        if any(s < ROPE for s, n in zip(os_, q_rope.shape[:2]) if n > 1):
+            raise ValueError("q_rope_out's rows overlap")
+        if (qp, qs) != (qo, os_) and T and heads and _overlap(q_rope, q_rope_out):
+            raise ValueError("q_rope_out may be q_rope, but not overlap it otherwise")
+    elif q_rope_out is not None:
+        raise ValueError("q_rope_out without q_rope")
+    nb, bs, D = pool.shape
+    dims = Dims(0, T, heads, 1, D, bs, nb, 0)
+    _call((_lib or load_library()).pkv_append_latent, dev, ptr, stride, positions.data_ptr(),
+          cos_sin.data_ptr(), cos_sin.shape[0], int(bool(interleaved)), w, eps,
+          slot_mapping.data_ptr(), pp, qp, qs[0], qs[1], qo, os_[0], os_[1], ctypes.byref(dims),
+          _raw_stream(stream, dev))
+
+
+class LatentWorkspace:
+    """A device workspace for pkv_attention_latent and pkv_attention_expanded,
+    ready for use on the current stream.  One serves calls of any size on its
+    device, one after the other."""
+
+    def __init__(self, num_q_tokens=1, num_q_heads=1, num_reqs=1, device="cuda"):
+        dims = Dims(num_reqs, num_q_tokens, num_q_heads, 1, LATENT + ROPE, 16, 1, 1)
+        device = torch.device(device)
+        with torch.cuda.device(device):
+            self.nbytes = int(load_library().pkv_latent_workspace_size(ctypes.byref(dims)))
+        if self.nbytes == 0:
+            raise PagedKVError(PKV_ERR_INVALID, pkv_last_error() or "bad dims")
+        self.buf = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device)
+        off = (-self.buf.data_ptr()) % 256
+        self.buf[off:off + 256].zero_()  # the work queue; the rest needs no initialisation
+        self.ptr = self.buf.data_ptr() + off
+
+
+def _latent_workspace(workspace, like, dev: int, stream):
+    if workspace is None:
+        if stream is None:
+            return LatentWorkspace(device=like.device)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+        with torch.cuda.stream(stream):  # its memory and first bytes in the call's own order
+            return LatentWorkspace(device=like.device)
+    if not isinstance(workspace, LatentWorkspace):
+        raise TypeError("workspace must be a LatentWorkspace")
+    if workspace.buf.get_device() != dev:
+        raise ValueError(f"workspace is on {workspace.buf.device}, q on {like.device}")
+    return workspace
+
+
+_ATTENTION_LATENT = _spec(("q", _BF16, 3), ("pool", _BF16, 3), ("block_tables", _I32, 2),
+                          ("seq_lens", _I32, 1), ("query_start_loc", _I32, 1), ("out", _BF16, 3))
+
+
+def pkv_attention_latent(q, pool, block_tables, seq_lens, query_start_loc, scale, out=None,
+                         workspace: LatentWorkspace | None = None, stream=None):
+    """Attention over a paged latent cache, absorbed form: q [Tq, Hq, 576] bf16
+    (up to 128 heads: the part that meets the latents, then the rotated part)
+    against the rows of pool [blocks, 16, 576]; the values are the rows' first
+    512 dims.  Returns out [Tq, Hq, 512] bf16."""
+    if out is None and isinstance(q, torch.Tensor) and q.dim() == 3:
+        out = torch.empty((*q.shape[:2], LATENT), dtype=_BF16, device=q.device)
+    dev, ptrs = _fast_need((q, pool, block_tables, seq_lens, query_start_loc, out), _ATTENTION_LATENT)
+    Tq, Hq, D = q.shape
+    R, cols = block_tables.shape
+    if seq_lens.shape[0] != R or query_start_loc.shape[0] != R + 1:
+        raise ValueError("seq_lens, query_start_loc and block_tables disagree on num_reqs")
+    nb, bs, d = pool.shape
+    if d != D:
+        raise ValueError("the pool's rows must have q's dims")
+    if tuple(out.shape) != (Tq, Hq, LATENT):
+        raise ValueError(f"out must be [{Tq}, {Hq}, {LATENT}]")
+    ws = _latent_workspace(workspace, q, dev, stream)
+    dims = Dims(R, Tq, Hq, 1, D, bs, nb, cols)
+    _call((_lib or load_library()).pkv_attention_latent, dev, *ptrs[:5], scale, ptrs[5],
+          ctypes.byref(dims), ws.ptr, ws.nbytes, _raw_stream(stream, dev))
+    return out
 
 
 class CascadeWorkspace(Workspace):

@@ -11,6 +11,7 @@
 
 #include "../../include/pagedkv.h"
 #include "pkv_internal.h"
+#include "pkv_latent.h"
 
 static_assert(PKV_MAX_REQS == pkv::kMaxReqs, "request limit mismatch");
 
@@ -283,6 +284,97 @@ int encode_q_map(CUtensorMap* m, const void* q, const pkv_dims* d, int group, in
                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(PKV_ERR_CUDA, "encode q tensor map: CUresult %d", (int)r);
+  return PKV_OK;
+}
+
+// ---------------------------------------------------- the latent cache's calls
+constexpr int kMaxRopeHeads = 4096;
+
+bool eps_ok(float eps) { return eps >= 0x1p-64f && eps <= 1.f; }
+
+// A token stride in elements: rows 16-byte aligned, a token inside one (any for a single token).
+bool stride_ok(int64_t stride, int row, int tokens) {
+  return stride >= 0 && stride % 8 == 0 && (stride >= row || tokens <= 1);
+}
+
+int check_latent_dims(const pkv_dims* d, bool attention) {
+  if (d == nullptr) return fail(PKV_ERR_INVALID, "dims is NULL");
+  if (d->head_dim != pkv::kLatRow)
+    return fail(PKV_ERR_UNSUPPORTED, "head_dim %d unsupported (a latent row has 576)", d->head_dim);
+  if (d->num_kv_heads != 1)
+    return fail(PKV_ERR_UNSUPPORTED, "num_kv_heads %d unsupported (a latent cache has 1)", d->num_kv_heads);
+  const int rc = check_step_dims(d);
+  if (rc != PKV_OK) return rc;
+  // (tensor-map rows are addressed with 32-bit coordinates)
+  if ((long long)d->num_blocks * pkv::kBlockSize > 0x7fffffffll)
+    return fail(PKV_ERR_UNSUPPORTED, "pool beyond 2^31 - 1 rows");
+  if (d->num_q_heads < 0 || d->num_q_heads > (attention ? pkv::kMaxLatentHeads : kMaxRopeHeads) ||
+      (attention && d->num_q_heads == 0))
+    return fail(PKV_ERR_UNSUPPORTED, "num_q_heads %d unsupported", d->num_q_heads);
+  return PKV_OK;
+}
+
+// How a step's (token, head) rows are grouped into work items of at most 64.
+// With no more rows than requests nearly every request has one; then an item is
+// one token's heads.
+struct LatentGroups {
+  int head_groups, group_heads, group_tokens;
+};
+
+LatentGroups latent_groups(const pkv_dims* d) {
+  LatentGroups l;
+  l.head_groups = d->num_q_heads > pkv::kLatMaxRows ? 2 : 1;
+  l.group_heads = (d->num_q_heads + l.head_groups - 1) / l.head_groups;
+  const int most = d->num_q_tokens - d->num_reqs + 1;  // tokens that a request can have beside one each
+  l.group_tokens = pkv::kLatMaxRows / l.group_heads;
+  if (l.group_tokens > most) l.group_tokens = most < 1 ? 1 : most;
+  return l;
+}
+
+// The workspace: the prefill's work queue (zero between calls), then records,
+// statistics and outputs of the pieces of rows that are cut, written anew by
+// every call.
+struct LatentLayout {
+  size_t piece, ml, o, total;
+};
+
+LatentLayout latent_layout(int sm_count) {
+  const size_t slots = 2 * (size_t)sm_count;
+  LatentLayout l;
+  l.piece = 256;
+  l.ml = (l.piece + slots * pkv::kPieceWords * sizeof(int) + 255) & ~(size_t)255;
+  l.o = l.ml + slots * pkv::kLatMaxRows * 2 * sizeof(float);
+  l.total = l.o + slots * pkv::kLatMaxRows * pkv::kLatent * sizeof(float);
+  return l;
+}
+
+// 3-D map of a bf16 tensor [n2][n1][n0] with strides s2, s1 (elements), 128-byte swizzle.
+int encode_bf16_3d(CUtensorMap* m, const void* base, long long n0, long long n1, long long n2,
+                   long long s1, long long s2, const cuuint32_t* box, const char* what) {
+  EncodeTiledFn enc = encode_tiled();
+  if (!enc) return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  const cuuint64_t dims[3] = {(cuuint64_t)n0, (cuuint64_t)n1, (cuuint64_t)n2};
+  const cuuint64_t strides[2] = {(cuuint64_t)s1 * 2, (cuuint64_t)s2 * 2};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(PKV_ERR_CUDA, "encode %s tensor map: CUresult %d", what, (int)r);
+  return PKV_OK;
+}
+
+// 2-D map of a latent pool as [num_blocks * 16 rows][576] bf16, 64 x 16 boxes.
+int encode_latent_map(CUtensorMap* m, const void* pool, const pkv_dims* d) {
+  EncodeTiledFn enc = encode_tiled();
+  if (!enc) return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  const cuuint64_t dims[2] = {(cuuint64_t)pkv::kLatRow, (cuuint64_t)d->num_blocks * pkv::kBlockSize};
+  const cuuint64_t strides[1] = {(cuuint64_t)pkv::kLatRow * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)pkv::kBlockSize};
+  const cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(pool), dims, strides,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(PKV_ERR_CUDA, "encode latent pool tensor map: CUresult %d", (int)r);
   return PKV_OK;
 }
 
@@ -985,6 +1077,190 @@ int pkv_release_blocks(const int32_t* block_tables, const int32_t* seq_lens,
   p.max_blocks = dims->max_blocks_per_req;
   const cudaError_t e = pkv::launch_release_blocks(p, current_options().pdl != 0, stream);
   if (e != cudaSuccess) return cuda_fail(e, "release_blocks launch");
+  return PKV_OK;
+}
+
+int pkv_norm_rope_append(const void* q, const void* k, const void* v, int64_t q_stride,
+                         int64_t k_stride, int64_t v_stride, const int64_t* positions,
+                         const float* cos_sin, int64_t max_position, int32_t rotary_dim,
+                         int32_t interleaved, const void* q_weight, const void* k_weight, float eps,
+                         const int64_t* slot_mapping, void* q_out, int64_t q_out_stride, void* k_pool,
+                         void* v_pool, const pkv_dims* dims, cudaStream_t stream) {
+  g_last_error[0] = '\0';
+  int rc = check_dims(dims, false);
+  if (rc != PKV_OK) return rc;
+  if (dims->num_q_tokens < 0 || dims->num_q_heads < 0) return fail(PKV_ERR_INVALID, "negative dims");
+  if (dims->num_q_heads > kMaxRopeHeads || dims->num_kv_heads > kMaxRopeHeads)
+    return fail(PKV_ERR_UNSUPPORTED, "more than %d heads", kMaxRopeHeads);
+  if (rotary_dim < 16 || rotary_dim > pkv::kHeadDim || rotary_dim % 16 != 0)
+    return fail(PKV_ERR_UNSUPPORTED, "rotary_dim %d unsupported (16, 32, .. 128)", rotary_dim);
+  if ((q_weight || k_weight) && !eps_ok(eps)) return fail(PKV_ERR_INVALID, "eps must be in [2^-64, 1]");
+  if (dims->num_q_tokens == 0) return PKV_OK;
+  if (!k || !v || !positions || !cos_sin || !slot_mapping || !k_pool || !v_pool ||
+      (dims->num_q_heads > 0 && (!q || !q_out)))
+    return fail(PKV_ERR_INVALID, "NULL pointer argument");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_pool) ||
+      !aligned16(v_pool) || !aligned16(cos_sin) || !aligned16(q_weight) || !aligned16(k_weight))
+    return fail(PKV_ERR_INVALID, "buffers must be 16-byte aligned");
+  if (!stride_ok(q_stride, dims->num_q_heads * pkv::kHeadDim, dims->num_q_tokens) ||
+      !stride_ok(q_out_stride, dims->num_q_heads * pkv::kHeadDim, dims->num_q_tokens) ||
+      !stride_ok(k_stride, dims->num_kv_heads * pkv::kHeadDim, dims->num_q_tokens) ||
+      !stride_ok(v_stride, dims->num_kv_heads * pkv::kHeadDim, dims->num_q_tokens))
+    return fail(PKV_ERR_INVALID, "token strides must be multiples of 8 elements and hold a token");
+  DeviceState* st = device_state();
+  if (!st) return PKV_ERR_CUDA;
+  pkv::NormRopeParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.out_stride = q_out_stride;
+  p.positions = positions;
+  p.cos_sin = cos_sin;
+  p.slot_mapping = slot_mapping;
+  p.q_weight = static_cast<const __nv_bfloat16*>(q_weight);
+  p.k_weight = static_cast<const __nv_bfloat16*>(k_weight);
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.k_pool = static_cast<__nv_bfloat16*>(k_pool);
+  p.v_pool = static_cast<__nv_bfloat16*>(v_pool);
+  p.err = st->err;
+  p.eps = eps;
+  p.max_position = max_position;
+  p.rot = rotary_dim;
+  p.interleaved = interleaved != 0;
+  p.num_tokens = dims->num_q_tokens;
+  p.num_q_heads = dims->num_q_heads;
+  p.num_kv_heads = dims->num_kv_heads;
+  p.num_blocks = dims->num_blocks;
+  p.pdl = current_options().pdl != 0;
+  const cudaError_t e = pkv::launch_norm_rope_append(p, st->sm_count, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "norm_rope_append launch");
+  return PKV_OK;
+}
+
+int pkv_append_latent(const void* kv, int64_t kv_stride, const int64_t* positions,
+                      const float* cos_sin, int64_t max_position, int32_t interleaved,
+                      const void* weight, float eps, const int64_t* slot_mapping, void* pool,
+                      const void* q_rope, int64_t q_stride, int64_t q_head_stride, void* q_rope_out,
+                      int64_t q_out_stride, int64_t q_out_head_stride, const pkv_dims* dims,
+                      cudaStream_t stream) {
+  g_last_error[0] = '\0';
+  int rc = check_latent_dims(dims, false);
+  if (rc != PKV_OK) return rc;
+  if (weight && !eps_ok(eps)) return fail(PKV_ERR_INVALID, "eps must be in [2^-64, 1]");
+  if (dims->num_q_tokens == 0) return PKV_OK;
+  if (!kv || !positions || !cos_sin || !slot_mapping || !pool)
+    return fail(PKV_ERR_INVALID, "NULL pointer argument");
+  const bool turn = dims->num_q_heads > 0 && q_rope != nullptr;
+  if (turn && !q_rope_out) return fail(PKV_ERR_INVALID, "q_rope_out is NULL");
+  if (!aligned16(kv) || !aligned16(cos_sin) || !aligned16(weight) || !aligned16(pool) ||
+      !aligned16(q_rope) || !aligned16(q_rope_out))
+    return fail(PKV_ERR_INVALID, "buffers must be 16-byte aligned");
+  if (!stride_ok(kv_stride, pkv::kLatRow, dims->num_q_tokens))
+    return fail(PKV_ERR_INVALID, "kv_stride must be a multiple of 8 elements and hold a token");
+  // (heads and tokens of the queries may lie in either order)
+  if (turn && (q_stride % 8 || q_head_stride % 8 || q_out_stride % 8 || q_out_head_stride % 8 ||
+               q_stride < 0 || q_head_stride < 0 || q_out_stride < 0 || q_out_head_stride < 0))
+    return fail(PKV_ERR_INVALID, "query strides must be multiples of 8 elements");
+  DeviceState* st = device_state();
+  if (!st) return PKV_ERR_CUDA;
+  pkv::AppendLatentParams p{};
+  p.kv = static_cast<const __nv_bfloat16*>(kv);
+  p.kv_stride = kv_stride;
+  p.positions = positions;
+  p.cos_sin = cos_sin;
+  p.slot_mapping = slot_mapping;
+  p.weight = static_cast<const __nv_bfloat16*>(weight);
+  p.pool = static_cast<__nv_bfloat16*>(pool);
+  p.q_rope = static_cast<const __nv_bfloat16*>(turn ? q_rope : nullptr);
+  p.q_rope_out = static_cast<__nv_bfloat16*>(q_rope_out);
+  p.q_stride = q_stride;
+  p.q_head_stride = q_head_stride;
+  p.out_stride = q_out_stride;
+  p.out_head_stride = q_out_head_stride;
+  p.err = st->err;
+  p.eps = eps;
+  p.max_position = max_position;
+  p.interleaved = interleaved != 0;
+  p.num_tokens = dims->num_q_tokens;
+  p.num_q_heads = turn ? dims->num_q_heads : 0;
+  p.num_blocks = dims->num_blocks;
+  p.pdl = current_options().pdl != 0;
+  const cudaError_t e = pkv::launch_append_latent(p, st->sm_count, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "append_latent launch");
+  return PKV_OK;
+}
+
+size_t pkv_latent_workspace_size(const pkv_dims* dims) {
+  g_last_error[0] = '\0';
+  if (check_latent_dims(dims, false) != PKV_OK) return 0;
+  DeviceState* st = device_state();
+  if (!st) return 0;
+  return latent_layout(st->sm_count).total;
+}
+
+int pkv_attention_latent(const void* q, const void* pool, const int32_t* block_tables,
+                         const int32_t* seq_lens, const int32_t* query_start_loc, float scale,
+                         void* out, const pkv_dims* dims, void* workspace, size_t workspace_bytes,
+                         cudaStream_t stream) {
+  g_last_error[0] = '\0';
+  int rc = check_latent_dims(dims, true);
+  if (rc != PKV_OK) return rc;
+  if (dims->num_reqs == 0 || dims->num_q_tokens == 0) return PKV_OK;
+  if (dims->num_blocks == 0) return fail(PKV_ERR_INVALID, "the pool has no blocks");
+  if (!q || !pool || !block_tables || !seq_lens || !query_start_loc || !out || !workspace)
+    return fail(PKV_ERR_INVALID, "NULL pointer argument");
+  if (!aligned16(q) || !aligned16(pool) || !aligned16(out))
+    return fail(PKV_ERR_INVALID, "q, out and the pool must be 16-byte aligned");
+  if (!(scale - scale == 0.f) || scale == 0.f)
+    return fail(PKV_ERR_INVALID, "scale must be finite, non-zero");
+  DeviceState* st = device_state();
+  if (!st) return PKV_ERR_CUDA;
+  const LatentLayout w = latent_layout(st->sm_count);
+  if (workspace_bytes < w.total)
+    return fail(PKV_ERR_WORKSPACE, "workspace %zu bytes, need %zu", workspace_bytes, w.total);
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0)
+    return fail(PKV_ERR_INVALID, "workspace must be 256-byte aligned");
+  const pkv_options opt = current_options();
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const LatentGroups g = latent_groups(dims);
+  pkv::LatentDecodeLaunch L{};
+  pkv::LatentDecodeParams& p = L.p;
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.qsl = query_start_loc;
+  p.pool = static_cast<const __nv_bfloat16*>(pool);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.piece = reinterpret_cast<int*>(ws + w.piece);
+  p.piece_ml = reinterpret_cast<float*>(ws + w.ml);
+  p.piece_o = reinterpret_cast<float*>(ws + w.o);
+  p.piece_rows = g.group_heads * g.group_tokens;
+  p.err = st->err;
+  p.num_reqs = dims->num_reqs;
+  p.num_q_tokens = dims->num_q_tokens;
+  p.num_q_heads = dims->num_q_heads;
+  p.num_blocks = dims->num_blocks;
+  p.max_blocks = dims->max_blocks_per_req;
+  p.head_groups = g.head_groups;
+  p.group_heads = g.group_heads;
+  p.group_tokens = g.group_tokens;
+  p.item_cost = 128;
+  p.min_keys = 256;
+  p.merge = 1;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.pdl = opt.pdl != 0;
+  p.early_plan = p.pdl && opt.early_plan != 0;
+  p.wait_limit_ns = (unsigned long long)opt.wait_limit_us * 1000ull;
+  const cuuint32_t qbox[3] = {64, (cuuint32_t)g.group_heads, (cuuint32_t)g.group_tokens};
+  rc = encode_bf16_3d(&L.qmap, q, pkv::kLatRow, dims->num_q_heads, dims->num_q_tokens, pkv::kLatRow,
+                      (long long)dims->num_q_heads * pkv::kLatRow, qbox, "q");
+  if (rc == PKV_OK) rc = encode_latent_map(&L.kmap, pool, dims);
+  if (rc != PKV_OK) return rc;
+  L.grid = st->sm_count / g.head_groups * g.head_groups;
+  const cudaError_t e = pkv::launch_latent_decode(L, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "latent attention launch");
   return PKV_OK;
 }
 

@@ -1,0 +1,857 @@
+// pkv_latent_decode.cu -- attention over a paged cache of latents, absorbed
+// form, on tcgen05 tensor cores.
+//
+// A cached row is one token's 512-dim latent c and 64-dim rotated key k,
+// shared by all query heads; the queries took the key expansion into them, so
+// a row (token, head) has 576 dims:
+//
+//   s_j = scale (<q[0:512], c_j> + <q[512:576], k_j>),  out = sum_j softmax(s)_j c_j
+//
+// The values are the first 512 dims of the keys: a tile that came in for the
+// scores is there for the products too, and a key costs 1152 bytes of HBM and
+// 2176 flops a head.  Up to 64 heads that is bound by HBM; 128 heads bring the
+// tensor core near its own bound.
+//
+// Tiling.  A work item is a request's `group_tokens` query tokens times
+// `group_heads` heads: its (token, head) pairs are the N <= 64 columns of the
+// MMAs, so that few heads cost little.  A tile is 64 keys = 4 pool blocks, nine
+// 64-dim chunks of [64 keys][128 bytes], fetched block by block with 2-D TMA
+// copies (128-byte swizzle).  S^T[64 keys x N] = K Q^T accumulates over the
+// chunks; O^T[512 dims x N] += C^T P is four M = 128 tiles whose A operand is
+// the same chunks read MN-major.  O^T takes 256 TMEM columns, S^T two buffers
+// of 64.  The other way round (rows as M) O would need all 512 columns.
+// Shared memory holds Q (72 KB), two tiles (144 KB) and P (8 KB), all there
+// is; a tile is therefore loaded and released in five parts (the rotated keys,
+// four pairs of latent chunks), each going back as soon as its last MMA is
+// done, so that copies stay in flight while the other tile is worked on.
+//
+// Roles (576 threads).  Sixteen softmax warps: warpgroup g has columns 16 g ..
+// 16 g + 15, its four warps 16 keys each (an M = 64 accumulator lies in 16 of
+// every 32 TMEM lanes; the 16x256b load spreads it over all lanes, two keys by
+// four columns a thread).  The running maximum moves only when a score exceeds
+// it by 2^8, on a vote of the warpgroup; then the warps agree on it through
+// shared memory and O^T is rescaled.  Warp 16 walks the CTA's work and issues
+// the copies, warp 17 the MMAs.
+//
+// Work split.  The items' keys (plus a fixed cost an item) form one sequence
+// that is cut in equal ranges, one a CTA -- or, with more than 64 heads, one a
+// pair of CTAs that read the same keys for half of the heads each.  Rows cut
+// by a range end leave unnormalised partial states, which latent_merge_kernel
+// joins; it needs no counters, so the workspace holds no state between calls.
+#include <climits>
+
+#include "pkv_latent.h"
+#include "pkv_tc.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kSoftWarps = 16;
+constexpr int kSoftThreads = 32 * kSoftWarps;
+constexpr int kWarpLoad = kSoftWarps;
+constexpr int kWarpMma = kSoftWarps + 1;
+constexpr int kThreads = 32 * (kSoftWarps + 2);
+constexpr int kBarSoft = 1;   // all softmax warps
+constexpr int kBarGroup = 2;  // + warpgroup
+
+constexpr int kTile = 64;                 // keys
+constexpr int kTileBlocks = kTile / kBlockSize;
+constexpr int kChunks = kLatRow / 64;     // 64-dim chunks of a row
+constexpr int kChunkBytes = kTile * 128;
+constexpr int kParts = 5;                 // release units of a tile: rotated keys, four latent pairs
+constexpr int kStages = 2;
+constexpr int kItems = 4;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kColO = 2 * kLatMaxRows;    // TMEM: S^T buffers, then O^T
+constexpr float kRescaleLog2 = 8.0f;
+
+__device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
+
+// A piece of a work item: key tiles t0 .. t1 - 1 of its keys.
+struct Item {
+  int req;      // block-table row
+  int row0;     // first query row
+  int nt;       // query tokens
+  int pos0;     // position of the first (it sees keys 0 .. pos0)
+  int vis;      // keys that the last one sees
+  int t0, t1;
+  int end;      // no more items
+};
+
+// Flags of a piece's record (besides its rows).
+constexpr int kPieceFirst = 1;  // holds the item's first tile
+constexpr int kPieceLast = 2;   // holds its last
+
+struct __align__(1024) Smem {
+  uint8_t q[kChunks][kChunkBytes];
+  uint8_t kv[kStages][kChunks][kChunkBytes];
+  uint8_t p[kLatMaxRows * 128];  // P^T: [column][64 keys] bf16, 128-byte swizzle
+  uint64_t kv_full[kStages][kParts], kv_empty[kStages][kParts];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full, p_free, o_full, o_empty;
+  uint64_t item_full[kItems];
+  uint64_t drained;
+  Item items[kItems];
+  float xrow[4][kLatMaxRows];        // a warpgroup's exchange of maxima and sums
+  unsigned long long bad[2];         // boundary keys taken out of the item's tiles, by item parity
+  uint32_t tmem_base;
+  WaitCtl wait;
+  // the plan: exclusive sums of the threads' requests, then the range
+  long long range_lo, range_hi, start_base;
+  int start_req;
+};
+static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "latent decode shared memory");
+
+// Part p's chunks: part 0 is chunk 8 (the rotated keys), part 1 + j the pair
+// 2 j, 2 j + 1.
+__device__ __forceinline__ int part_chunk(int part) { return part == 0 ? 8 : 2 * (part - 1); }
+__device__ __forceinline__ int part_chunks(int part) { return part == 0 ? 1 : 2; }
+
+// --------------------------------------------------------------------- plan
+struct Req {
+  int q0, qr, L;
+  int ng;  // token groups (0: nothing to do)
+};
+
+__device__ __forceinline__ Req make_req(const LatentDecodeParams& p, int q0, int q1, int L,
+                                        bool* bad) {
+  Req a{q0, q1 - q0, L, 0};
+  const bool ok = q0 >= 0 && q1 >= q0 && q1 <= p.num_q_tokens && a.qr <= L &&
+                  L <= p.max_blocks * kBlockSize;
+  if (ok && a.qr > 0) a.ng = cdiv(a.qr, p.group_tokens);
+  *bad = !ok;
+  return a;
+}
+
+__device__ __forceinline__ Req load_req(const LatentDecodeParams& p, int r) {
+  bool bad;
+  return make_req(p, __ldg(p.qsl + r), __ldg(p.qsl + r + 1), __ldg(p.seq_lens + r), &bad);
+}
+
+// Weight of token groups 0 .. i - 1, i <= ng: group m sees L - qr + min((m + 1)
+// group_tokens, qr) keys.
+__device__ __forceinline__ long long groups_weight(const LatentDecodeParams& p, const Req& a, int i) {
+  const long long n = i;
+  long long w = n * ((long long)a.L - a.qr + p.item_cost) + (long long)p.group_tokens * (n * (n + 1) / 2);
+  if (i == a.ng && i > 0) w -= (long long)a.ng * p.group_tokens - a.qr;
+  return w;
+}
+
+// The CTA's range of the weighted key sequence, and the request that its start
+// lies in.  All threads.
+__device__ __forceinline__ void plan_range(const LatentDecodeParams& p, Smem& sm, int unit, int units) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = cdiv(p.num_reqs, kThreads);
+  const int r0 = min(tid * per, p.num_reqs), r1 = min(r0 + per, p.num_reqs);
+  long long mine = 0;
+  for (int r = r0; r < r1; ++r) {
+    bool bad;
+    const Req a = make_req(p, __ldg(p.qsl + r), __ldg(p.qsl + r + 1), __ldg(p.seq_lens + r), &bad);
+    if (bad && blockIdx.x == 0) record_error(p.err, kErrBounds);  // the request is skipped
+    mine += groups_weight(p, a, a.ng);
+  }
+  // Exclusive sums over the threads.
+  long long incl = mine;
+  #pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  long long* part = reinterpret_cast<long long*>(sm.xrow);
+  if (lane == 31) part[warp] = incl;
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const long long v = part[w];
+    if (w < warp) before += v;
+    total += v;
+  }
+  const long long excl = before + incl - mine;
+  long long chunk = (total + units - 1) / units;
+  if (chunk < p.min_keys) chunk = p.min_keys;
+  const long long lo = min((long long)unit * chunk, total), hi = min(lo + chunk, total);
+  if (tid == 0) {
+    sm.range_lo = lo;
+    sm.range_hi = hi;
+  }
+  if (lo < hi && excl <= lo && lo < excl + mine) {
+    long long base = excl;
+    for (int r = r0; r < r1; ++r) {
+      const Req a = load_req(p, r);
+      const long long w = groups_weight(p, a, a.ng);
+      if (lo < base + w) {
+        sm.start_req = r;
+        sm.start_base = base;
+        break;
+      }
+      base += w;
+    }
+  }
+  __syncthreads();
+}
+
+// --------------------------------------------------------------- TMEM, smem
+// Two 8-column groups of 16 accumulator rows (TMEM lanes base .. base + 15):
+// v[4 c + 2 h + e] is row lane / 4 + 8 h, column 8 c + 2 (lane % 4) + e.
+__device__ __forceinline__ void tmem_ld_16x16(uint32_t taddr, float (&v)[8]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16f(uint32_t taddr, const float (&v)[16]) {
+  tmem_st16(taddr, reinterpret_cast<const uint32_t(&)[16]>(v));
+}
+
+// Four 8x8 matrices of 16-bit elements, each stored transposed: lane i gives
+// the address of row i % 8 of matrix i / 8 as it is to lie in memory.
+__device__ __forceinline__ void stmatrix4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                                uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Address of 16-byte piece `piece` (0 .. 63) of key row `row`'s latent in a tile.
+__device__ __forceinline__ uint4* latent_piece(uint8_t (*tile)[kChunkBytes], int row, int piece) {
+  return reinterpret_cast<uint4*>(tile[piece >> 3] + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ bool non_finite(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+// Rows of the tile that no row of the item sees (rows vis - key0 .. 63) must
+// not reach the product, whatever they hold: 0 * NaN.  Rows that only some of
+// the item's tokens see (keys pos0 + 1 .. vis - 1) may hold NaN or infinities
+// that the others must not get: those are taken out too and noted, and the
+// epilogue gives them to the rows that see them.  Rare or at a range's last
+// tiles; one warp a row, out of line.
+static __device__ __noinline__ void clean_tile(Smem& sm, uint8_t (*tile)[kChunkBytes], int key0,
+                                               int pos0, int vis, unsigned long long* bad, int warp,
+                                               int lane) {
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int row = max(pos0 + 1 - key0, 0) + warp; row < kTile; row += kSoftWarps) {
+    const int key = key0 + row;
+    bool out = key >= vis;
+    if (!out) {
+      const uint4 a = *latent_piece(tile, row, lane), b = *latent_piece(tile, row, lane + 32);
+      out = __any_sync(0xffffffffu, non_finite(a.x) || non_finite(a.y) || non_finite(a.z) ||
+                                        non_finite(a.w) || non_finite(b.x) || non_finite(b.y) ||
+                                        non_finite(b.z) || non_finite(b.w));
+      if (out && lane == 0) atomicOr(bad, 1ull << (key - pos0 - 1));
+    }
+    if (out) {
+      *latent_piece(tile, row, lane) = zero;
+      *latent_piece(tile, row, lane + 32) = zero;
+    }
+  }
+  fence_proxy_async_smem();
+}
+
+// Bit b of the result: boundary key b, taken out of the products, holds a
+// non-finite value in dim d.  A row that sees such a key scored it NaN or
+// infinite; only where it scored it -inf is the row not all NaN already, and
+// then its weight 0 times the value is NaN in this dim.
+static __device__ __noinline__ unsigned long long bad_dim(const LatentDecodeParams& p, const Item& it,
+                                                          unsigned long long bad, int d) {
+  unsigned long long hit = 0;
+  for (unsigned long long m = bad; m; m &= m - 1) {
+    const int b = __ffsll((long long)m) - 1;
+    const int key = it.pos0 + 1 + b;
+    const int blk = __ldg(p.block_tables + (long long)it.req * p.max_blocks + key / kBlockSize);
+    if ((unsigned)blk >= (unsigned)p.num_blocks) continue;
+    const uint16_t v = __ldg(reinterpret_cast<const uint16_t*>(p.pool) +
+                             ((long long)blk * kBlockSize + key % kBlockSize) * kLatRow + d);
+    if ((v & 0x7f80u) == 0x7f80u) hit |= 1ull << b;
+  }
+  return hit;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
+                         const __grid_constant__ CUtensorMap kmap, const LatentDecodeParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw + (((raw + 1023u) & ~1023u) - raw));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  WaitCtl* ctl = &sm.wait;
+  // CTA b: head group b % head_groups of range b / head_groups.
+  const int hg = blockIdx.x % p.head_groups;
+  const int head0 = hg * p.group_heads;
+  const int heads = min(p.group_heads, p.num_q_heads - head0);
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s)
+      for (int i = 0; i < kParts; ++i) {
+        mbar_init(&sm.kv_full[s][i], 1);
+        mbar_init(&sm.kv_empty[s][i], 1);
+      }
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_empty, 1);
+    mbar_init(&sm.s_full[0], 1);
+    mbar_init(&sm.s_full[1], 1);
+    mbar_init(&sm.p_full, kSoftWarps);
+    mbar_init(&sm.p_free, 1);
+    mbar_init(&sm.o_full, 1);
+    mbar_init(&sm.o_empty, kSoftWarps);
+    for (int i = 0; i < kItems; ++i) mbar_init(&sm.item_full[i], 1);
+    mbar_init(&sm.drained, 1);
+    sm.wait.abort = 0;
+    sm.wait.limit_ns = p.wait_limit_ns;
+    sm.bad[0] = sm.bad[1] = 0;
+    fence_barrier_init();
+  }
+  if (warp == kWarpLoad && lane == 0) {
+    prefetch_tensormap(&qmap);
+    prefetch_tensormap(&kmap);
+  }
+  if (!p.early_plan) grid_dependency_wait();
+  plan_range(p, sm, blockIdx.x / p.head_groups, gridDim.x / p.head_groups);
+  if (p.early_plan) grid_dependency_wait();
+  allow_dependent_launch();
+  const long long lo = sm.range_lo, hi = sm.range_hi;
+  // This CTA's piece records, written again by the pieces that it cuts.
+  if (p.merge && tid < 2) p.piece[(2 * blockIdx.x + tid) * kPieceWords] = 0;
+  if (lo >= hi) return;
+  if (warp == kWarpMma) {
+    tmem_alloc(&sm.tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+
+  if (warp == kWarpLoad) {
+    // =========================== copies ===================================
+    int n_item = 0, t = 0;  // items and tiles so far
+    int parts = 0;          // parts of tile t that were issued
+    bool ok = true;
+    int r = sm.start_req;
+    long long base = sm.start_base;
+    const int oob_row = p.num_blocks * kBlockSize;
+    const uint32_t q_bytes = (uint32_t)(kChunks * 128) * p.group_heads * p.group_tokens;
+    // A request's raw fields, the next one's ahead of its turn.
+    int f0 = __ldg(p.qsl + r), f1 = __ldg(p.qsl + r + 1), fl = __ldg(p.seq_lens + r);
+    while (ok && base < hi && r < p.num_reqs) {
+      bool bad;
+      const Req a = make_req(p, f0, f1, fl, &bad);
+      if (r + 1 < p.num_reqs) {
+        f0 = f1;
+        f1 = __ldg(p.qsl + r + 2);
+        fl = __ldg(p.seq_lens + r + 1);
+      }
+      const long long w = groups_weight(p, a, a.ng);
+      // First token group that the range reaches.
+      int g = 0;
+      if (base < lo) {
+        int top = a.ng;  // groups_weight(g) <= lo - base < groups_weight(top)
+        while (top - g > 1) {
+          const int mid = (g + top) >> 1;
+          if (groups_weight(p, a, mid) <= lo - base) g = mid;
+          else top = mid;
+        }
+      }
+      const int32_t* bt = p.block_tables + (long long)r * p.max_blocks;
+      for (; g < a.ng && ok; ++g) {
+        const long long gbase = base + groups_weight(p, a, g);
+        if (gbase >= hi) break;
+        Item it;
+        it.req = r;
+        it.row0 = a.q0 + g * p.group_tokens;
+        it.nt = min(p.group_tokens, a.qr - g * p.group_tokens);
+        it.pos0 = a.L - a.qr + g * p.group_tokens;
+        it.vis = it.pos0 + it.nt;
+        // Tile j belongs to the range that holds weight unit gbase + 64 j.
+        it.t0 = gbase >= lo ? 0 : (int)((lo - gbase + kTile - 1) / kTile);
+        it.t1 = hi - gbase >= it.vis ? cdiv(it.vis, kTile) : (int)((hi - gbase + kTile - 1) / kTile);
+        it.end = 0;
+        if (it.t0 >= it.t1) continue;
+        const int nbl = cdiv(it.vis, kBlockSize);
+        // Block ids 32 at a time (eight tiles).
+        auto ids = [&](int tile) {
+          const int x = tile * kTileBlocks + lane;
+          return x < nbl ? __ldg(bt + x) : INT_MIN;
+        };
+        int cur = ids(it.t0), nxt = it.t0 + 8 < it.t1 ? ids(it.t0 + 8) : INT_MIN;
+        for (int j = it.t0; j < it.t1; ++j, ++t) {
+          const int k = (j - it.t0) & 7;
+          if (k == 0 && j > it.t0) {
+            cur = nxt;
+            if (j + 8 < it.t1) nxt = ids(j + 8);
+          }
+          const int st = t % kStages;
+          // Lane b + 4 c copies block b of the part's chunk c; blocks past the
+          // last are read at a row outside the pool, which fills zeros.
+          const int id = __shfl_sync(0xffffffffu, cur, k * kTileBlocks + (lane & 3));
+          int row = oob_row;
+          if ((unsigned)id < (unsigned)p.num_blocks) row = id * kBlockSize;
+          else if (id != INT_MIN && lane < 4) record_error(p.err, kErrBounds);
+          parts = 0;
+          for (int part = 0; part < kParts; ++part) {
+            if (j == it.t0 && part == 0) {
+              // The item and its queries, ahead of its first keys.
+              if (n_item > 0) ok = mbar_wait(&sm.q_empty, (n_item - 1) & 1, p.err, ctl);
+              if (!ok) break;
+              if (lane == 0) {
+                sm.items[n_item % kItems] = it;
+                mbar_arrive(&sm.item_full[n_item % kItems]);
+                mbar_arrive_expect_tx(&sm.q_full, q_bytes);
+              }
+              __syncwarp();
+              if (lane < kChunks) tma_load_3d(sm.q[lane], &qmap, lane * 64, head0, it.row0, &sm.q_full);
+              ++n_item;
+            }
+            if (t >= kStages) ok = mbar_wait(&sm.kv_empty[st][part], ((t / kStages) - 1) & 1, p.err, ctl);
+            if (!ok) break;
+            const int n = part_chunks(part), c = part_chunk(part) + (lane >> 2);
+            if (lane == 0) mbar_arrive_expect_tx(&sm.kv_full[st][part], (uint32_t)n * kChunkBytes);
+            __syncwarp();
+            if (lane < 4 * n)
+              tma_load_2d(sm.kv[st][c] + (lane & 3) * 2048, &kmap, c * 64, row, &sm.kv_full[st][part]);
+            ++parts;
+          }
+          if (!ok) break;
+          parts = 0;
+        }
+      }
+      base += w;
+      ++r;
+    }
+    // End marker, for the MMA warp (behind its last item) and the softmax warps.
+    if (ok && n_item > 0) ok = mbar_wait(&sm.q_empty, (n_item - 1) & 1, p.err, ctl);
+    if (ok && lane == 0) {
+      sm.items[n_item % kItems].end = 1;
+      mbar_arrive(&sm.item_full[n_item % kItems]);
+      mbar_arrive(&sm.q_full);
+    }
+    __syncwarp();
+    if (!ok) {
+      // Aborted: the copies in flight must land before the CTA ends.
+      for (int part = 0; part < kParts; ++part) {
+        const int n = t + (part < parts ? 1 : 0);  // tiles whose part was issued
+        for (int i = max(0, n - kStages); i < n; ++i)
+          mbar_wait_drain(&sm.kv_full[i % kStages][part], (i / kStages) & 1, p.err, ctl);
+      }
+      if (n_item > 0) mbar_wait_drain(&sm.q_full, (n_item - 1) & 1, p.err, ctl);
+    }
+  } else if (warp == kWarpMma) {
+    // ============================ MMAs ====================================
+    // Order: S(t), then PV(t - 1): the softmax of a tile runs beside both.
+    const int n_cols = ((p.group_heads * p.group_tokens + 15) / 16) * 16;
+    const uint32_t idesc_s = idesc_bf16_f32(kTile, n_cols, 0, 0);
+    const uint32_t idesc_o = idesc_bf16_f32(128, n_cols, 1, 0);
+    bool ok = true;
+    int t = 0, n_item = 0;
+    auto pv = [&](int tt, bool first, bool last) {
+      const int st = tt % kStages;
+      ok = ok && mbar_wait(&sm.p_full, tt & 1, p.err, ctl);
+      if (first && n_item > 0) ok = ok && mbar_wait(&sm.o_empty, (n_item - 1) & 1, p.err, ctl);
+      if (!ok) return;
+      tc_fence_after();
+      if (elect_one()) {
+        #pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          #pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk) {
+            // C^T: atoms of 64 dims x 8 keys; the chunks kChunkBytes apart,
+            // 8-key groups 1024 bytes apart.
+            const uint64_t da = smem_desc_sw128(smem_u32(sm.kv[st][2 * m]) + kk * 2048, kChunkBytes, 1024);
+            const uint64_t db = smem_desc_sw128(smem_u32(sm.p) + kk * 32, 16, 1024);
+            tc_mma_f16_ss(tmem + kColO + m * kLatMaxRows, da, db, idesc_o, !first || kk > 0);
+          }
+          tc_commit(&sm.kv_empty[st][1 + m]);
+        }
+        tc_commit(&sm.p_free);
+        if (last) tc_commit(&sm.o_full);
+      }
+      __syncwarp();
+    };
+    // The tile whose PV is still to be issued belongs to the item before when
+    // an item's first S goes out.
+    bool pending = false, pend_first = false;
+    for (;; ++n_item) {
+      if (!mbar_wait(&sm.q_full, n_item & 1, p.err, ctl)) {
+        ok = false;
+        break;
+      }
+      const Item it = sm.items[n_item % kItems];
+      if (it.end) break;
+      for (int j = it.t0; j < it.t1 && ok; ++j, ++t) {
+        const int st = t % kStages;
+        const uint32_t tS = tmem + (t & 1) * kLatMaxRows;
+        for (int part = 0; part < kParts && ok; ++part) {
+          ok = mbar_wait(&sm.kv_full[st][part], (t / kStages) & 1, p.err, ctl);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            for (int c = part_chunk(part); c < part_chunk(part) + part_chunks(part); ++c) {
+              #pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {
+                const uint64_t da = smem_desc_sw128(smem_u32(sm.kv[st][c]) + kk * 32, 16, 1024);
+                const uint64_t db = smem_desc_sw128(smem_u32(sm.q[c]) + kk * 32, 16, 1024);
+                tc_mma_f16_ss(tS, da, db, idesc_s, part > 0 || kk > 0);
+              }
+            }
+          }
+          __syncwarp();
+        }
+        if (ok && elect_one()) {
+          tc_commit(&sm.kv_empty[st][0]);
+          tc_commit(&sm.s_full[t & 1]);
+          if (j == it.t1 - 1) tc_commit(&sm.q_empty);
+        }
+        __syncwarp();
+        if (pending) {
+          // (an item's first tile: the tile before is the last of the item before)
+          if (j == it.t0) {
+            --n_item;
+            pv(t - 1, pend_first, true);
+            ++n_item;
+          } else {
+            pv(t - 1, pend_first, false);
+          }
+        }
+        pending = true;
+        pend_first = j == it.t0;
+      }
+      if (!ok) break;
+    }
+    if (ok && pending) {
+      --n_item;
+      pv(t - 1, pend_first, true);
+    }
+    if (!ok) {
+      // Aborted: the issued MMAs must end before TMEM is freed.
+      if (elect_one()) tc_commit(&sm.drained);
+      __syncwarp();
+      mbar_wait_drain(&sm.drained, 0, p.err, ctl);
+    }
+  } else {
+    // ==================== softmax and epilogue (warps 0-15) ==================
+    const int wg = warp >> 2, quad = warp & 3;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const int rows = p.group_heads * p.group_tokens;
+    const bool mine = wg * 16 < rows;
+    // This thread's columns 16 wg + 8 c + 2 (lane % 4) + e, its keys' places
+    // 16 quad + lane / 4 + 8 h.
+    const int col0 = wg * 16 + 2 * (lane & 3);
+    const int key_lo = quad * 16 + (lane >> 2);
+    int tok[4];  // query token of each column; -1: none
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int col = col0 + 8 * (i >> 1) + (i & 1);
+      tok[i] = col < rows && col % p.group_heads < heads ? col / p.group_heads : -1;
+    }
+    // P^T: this warp's stmatrix rows -- matrix 2 c + h holds columns 8 c .., keys
+    // 16 quad + 8 h ..
+    const int st_col = wg * 16 + ((lane >> 4) & 1) * 8 + (lane & 7);
+    const int st_piece = quad * 2 + ((lane >> 3) & 1);
+    const uint32_t st_addr = smem_u32(sm.p) + st_col * 128 + ((st_piece ^ (st_col & 7)) << 4);
+    bool ok = true;
+    int t = 0;
+    for (int n_item = 0;; ++n_item) {
+      const bool have = mbar_wait(&sm.item_full[n_item % kItems], (n_item / kItems) & 1, p.err, ctl);
+      const Item it = sm.items[n_item % kItems];
+      // Agree before any barrier: a wait that gave up stops everyone.
+      if (barrier_or(kBarSoft, kSoftThreads, !have || it.end)) break;
+      unsigned long long* bad = &sm.bad[n_item & 1];
+      int limit[4];  // the last key that each column sees
+      #pragma unroll
+      for (int i = 0; i < 4; ++i) limit[i] = tok[i] >= 0 && tok[i] < it.nt ? it.pos0 + tok[i] : -1;
+      float m[4], l[4];
+      #pragma unroll
+      for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.f;
+      for (int j = it.t0; j < it.t1; ++j, ++t) {
+        const int key0 = j * kTile;
+        ok = ok && mbar_wait(&sm.s_full[t & 1], (t >> 1) & 1, p.err, ctl);
+        tc_fence_after();
+        uint32_t w[4];
+        if (mine) {
+          float v[8];
+          tmem_ld_16x16(tmem + lane_off + (t & 1) * kLatMaxRows + wg * 16, v);
+          tc_wait_ld();
+          float mx[4];
+          #pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // v: column i = 2 c + e at 4 c + e (first key) and 4 c + 2 + e.
+            float& a = v[4 * (i >> 1) + (i & 1)];
+            float& b = v[4 * (i >> 1) + 2 + (i & 1)];
+            a *= p.scale_log2;
+            b *= p.scale_log2;
+            if (key0 + key_lo > limit[i]) a = -INFINITY;
+            if (key0 + key_lo + 8 > limit[i]) b = -INFINITY;
+            mx[i] = fmaxf(a, b);
+          }
+          bool grow = j == it.t0;
+          #pragma unroll
+          for (int i = 0; i < 4; ++i) grow = grow || mx[i] > m[i] + kRescaleLog2;
+          if (barrier_or(kBarGroup + wg, 128, grow)) {
+            // The warpgroup's maxima of this tile.
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              #pragma unroll
+              for (int o = 4; o < 32; o <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
+            }
+            if (lane < 4) {
+              #pragma unroll
+              for (int i = 0; i < 4; ++i) sm.xrow[quad][col0 + 8 * (i >> 1) + (i & 1)] = mx[i];
+            }
+            named_barrier(kBarGroup + wg, 128);
+            // New references, for all 16 columns: this thread's, and in lane i
+            // < 16 the factor of column i.
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int col = col0 + 8 * (i >> 1) + (i & 1);
+              mx[i] = fmaxf(fmaxf(sm.xrow[0][col], sm.xrow[1][col]), fmaxf(sm.xrow[2][col], sm.xrow[3][col]));
+            }
+            named_barrier(kBarGroup + wg, 128);
+            float alpha[4];
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const bool up = mx[i] > m[i] + kRescaleLog2 || (m[i] == -INFINITY && mx[i] > m[i]);
+              const float m_new = up ? mx[i] : m[i];
+              // (nothing summed so far: any factor will do, but not NaN)
+              alpha[i] = up && m[i] != -INFINITY ? fast_exp2(m[i] - m_new) : 1.f;
+              m[i] = m_new;
+              l[i] *= alpha[i];
+            }
+            if (j > it.t0) {
+              // O^T of this warpgroup's columns, 32 dims a warp: it must hold
+              // the tile before.
+              if (lane < 4) {
+                #pragma unroll
+                for (int i = 0; i < 4; ++i) sm.xrow[quad][col0 + 8 * (i >> 1) + (i & 1)] = alpha[i];
+              }
+              __syncwarp();
+              ok = ok && mbar_wait(&sm.p_free, (t - 1) & 1, p.err, ctl);
+              tc_fence_after();
+              #pragma unroll 1
+              for (int mt = 0; mt < 4; ++mt) {
+                float o[16];
+                const uint32_t ta = tmem + lane_off + kColO + mt * kLatMaxRows + wg * 16;
+                tmem_ld16(ta, o);
+                tc_wait_ld();
+                #pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] *= sm.xrow[quad][wg * 16 + i];
+                tmem_st16f(ta, o);
+              }
+              tc_wait_st();
+              named_barrier(kBarGroup + wg, 128);  // sm.xrow is free again
+            }
+          }
+          // P = exp2(s - m) in bf16; the sums add the rounded values that the
+          // product uses.  A column that saw no key yet has m = -inf.
+          #pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float ref = m[i] == -INFINITY ? 0.f : m[i];
+            float& a = v[4 * (i >> 1) + (i & 1)];
+            float& b = v[4 * (i >> 1) + 2 + (i & 1)];
+            a = fast_exp2(a - ref);
+            b = fast_exp2(b - ref);
+          }
+          #pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            w[2 * c] = pack_bf16(v[4 * c], v[4 * c + 1]);
+            w[2 * c + 1] = pack_bf16(v[4 * c + 2], v[4 * c + 3]);
+            add_bf16x2(l[2 * c], l[2 * c + 1], w[2 * c]);
+            add_bf16x2(l[2 * c], l[2 * c + 1], w[2 * c + 1]);
+          }
+        }
+        if (key0 + kTile > it.pos0 + 1) {
+          // (landed long since: the scores came from them)
+          for (int part = 1; part < kParts; ++part)
+            ok = ok && mbar_wait(&sm.kv_full[t % kStages][part], (t / kStages) & 1, p.err, ctl);
+          clean_tile(sm, sm.kv[t % kStages], key0, it.pos0, it.vis, bad, warp, lane);
+        }
+        // P's buffer is free once the product before has read it.
+        if (t > 0) ok = ok && mbar_wait(&sm.p_free, (t - 1) & 1, p.err, ctl);
+        if (mine) {
+          stmatrix4_trans(st_addr, w[0], w[1], w[2], w[3]);
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full);
+      }
+      // ---- epilogue ---------------------------------------------------------
+      const int n_tiles = cdiv(it.vis, kTile);
+      const bool whole = it.t0 == 0 && it.t1 == n_tiles;
+      if (mine) {
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          #pragma unroll
+          for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+        }
+        if (lane < 4) {
+          #pragma unroll
+          for (int i = 0; i < 4; ++i) sm.xrow[quad][col0 + 8 * (i >> 1) + (i & 1)] = l[i];
+        }
+        named_barrier(kBarGroup + wg, 128);
+      }
+      ok = ok && mbar_wait(&sm.o_full, n_item & 1, p.err, ctl);
+      tc_fence_after();
+      // Boundary keys that were taken out, by any warp.
+      if (it.nt > 1) named_barrier(kBarSoft, kSoftThreads);
+      const unsigned long long gone = *bad;
+      if (mine) {
+        const int slot = 2 * blockIdx.x + (it.t0 == 0 ? 1 : 0);
+        if (!whole && ok) {
+          if (quad == 0 && lane < 4) {
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int col = col0 + 8 * (i >> 1) + (i & 1);
+              if (col >= rows) continue;
+              const float sum = (sm.xrow[0][col] + sm.xrow[1][col]) + (sm.xrow[2][col] + sm.xrow[3][col]);
+              *reinterpret_cast<float2*>(p.piece_ml + ((long long)slot * p.piece_rows + col) * 2) =
+                  make_float2(m[i], sum);
+            }
+          }
+          if (tid == 0) {
+            int* rec = p.piece + slot * kPieceWords;
+            rec[1] = it.row0;
+            rec[2] = it.nt;
+            rec[0] = 4 | (it.t0 == 0 ? kPieceFirst : 0) | (it.t1 == n_tiles ? kPieceLast : 0);
+          }
+        }
+        #pragma unroll 1
+        for (int mt = 0; mt < 4; ++mt) {
+          const int d = mt * 128 + quad * 32 + lane;
+          float o[16];
+          tmem_ld16(tmem + lane_off + kColO + mt * kLatMaxRows + wg * 16, o);
+          tc_wait_ld();
+          unsigned long long hit = 0;
+          if (gone) hit = bad_dim(p, it, gone, d);
+          #pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int col = wg * 16 + i;
+            const int tk = col / p.group_heads, h = col - tk * p.group_heads;
+            if (tk >= it.nt || col >= rows || h >= heads) continue;
+            // Token tk sees boundary keys 0 .. tk - 1.
+            if (hit & ((1ull << tk) - 1)) o[i] = NAN;
+            if (whole) {
+              const float sum = (sm.xrow[0][col] + sm.xrow[1][col]) + (sm.xrow[2][col] + sm.xrow[3][col]);
+              if (ok)
+                p.out[((long long)(it.row0 + tk) * p.num_q_heads + head0 + h) * kLatent + d] =
+                    __float2bfloat16_rn(o[i] / sum);
+            } else if (ok) {
+              p.piece_o[((long long)slot * p.piece_rows + col) * kLatent + d] = o[i];
+            }
+          }
+        }
+      }
+      // Every warp has read sm.bad, sm.xrow; O^T goes back.
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.o_empty);
+      if (barrier_or(kBarSoft, kSoftThreads, !ok)) break;
+      if (tid == 0) *bad = 0;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) tmem_dealloc(tmem, kTmemCols);
+}
+
+// Joins the pieces of rows that were cut.  Block (b, y): the row whose first
+// piece CTA b's last slot holds, if any; its later pieces are the first slots of
+// the next CTAs of the same head group.  A warp a (token, head) row, 16 dims a
+// lane.
+constexpr int kMergeWarps = 8;
+
+__global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const LatentDecodeParams p, int grid) {
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int cta = blockIdx.x, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  const int* rec = p.piece + (2 * cta + 1) * kPieceWords;
+  if (rec[0] == 0) return;  // CTA cta cut nothing that begins with it
+  const int hg = cta % p.head_groups, head0 = hg * p.group_heads;
+  const int row0 = rec[1], nt = rec[2];
+  const int tk = row / p.group_heads, h = row - tk * p.group_heads;
+  if (tk >= nt || tk >= p.group_tokens || head0 + h >= p.num_q_heads) return;
+  // The running state over the pieces in order.
+  float m = -INFINITY, l = 0.f;
+  float4 o[4];
+  #pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = cta, slot = 2 * cta + 1;;) {
+    const int flags = p.piece[slot * kPieceWords];
+    if (flags == 0) break;  // (a piece that an aborted CTA did not write)
+    const float2 ml = *reinterpret_cast<const float2*>(p.piece_ml + ((long long)slot * p.piece_rows + row) * 2);
+    const float top = fmaxf(m, ml.x);
+    const float a = m == -INFINITY ? 0.f : fast_exp2(m - top);
+    const float b = ml.x == -INFINITY && ml.y == 0.f ? 0.f : fast_exp2(ml.x - top);
+    const float4* src = reinterpret_cast<const float4*>(p.piece_o + ((long long)slot * p.piece_rows + row) * kLatent);
+    l = l * a + ml.y * b;
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = src[i * 32 + lane];
+      o[i].x = o[i].x * a + v.x * b;
+      o[i].y = o[i].y * a + v.y * b;
+      o[i].z = o[i].z * a + v.z * b;
+      o[i].w = o[i].w * a + v.w * b;
+    }
+    m = top;
+    if (flags & kPieceLast) break;
+    c += p.head_groups;
+    if (c >= grid) break;
+    slot = 2 * c;
+  }
+  __nv_bfloat16* dst = p.out + ((long long)(row0 + tk) * p.num_q_heads + head0 + h) * kLatent;
+  #pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint2 v;
+    v.x = pack_bf16(o[i].x / l, o[i].y / l);
+    v.y = pack_bf16(o[i].z / l, o[i].w / l);
+    *reinterpret_cast<uint2*>(dst + (i * 32 + lane) * 4) = v;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_latent_decode(const LatentDecodeLaunch& L, cudaStream_t stream) {
+  const size_t smem = sizeof(Smem) + 1024;
+  static unsigned long long configured = 0;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & bit)) {
+    e = cudaFuncSetAttribute(latent_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    __atomic_fetch_or(&configured, bit, __ATOMIC_RELEASE);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(L.grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = L.p.pdl ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, latent_decode_kernel, L.qmap, L.kmap, L.p);
+  if (e != cudaSuccess || !L.p.merge) return e != cudaSuccess ? e : cudaGetLastError();
+  const int rows = L.p.group_heads * L.p.group_tokens;
+  cfg.gridDim = dim3(L.grid, (rows + kMergeWarps - 1) / kMergeWarps);
+  cfg.blockDim = dim3(32 * kMergeWarps);
+  cfg.dynamicSmemBytes = 0;
+  e = cudaLaunchKernelEx(&cfg, latent_merge_kernel, L.p, L.grid);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+}  // namespace pkv

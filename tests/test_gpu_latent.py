@@ -1,0 +1,272 @@
+"""The latent cache's operators and the norm and rotation ahead of the append,
+on a GPU, against plain 64-bit implementations."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_195_gb300 as pkv
+from paged_kv_cache_195_gb300 import build as pkv_build
+
+import lat_reference as ref
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    pkv_build.build()
+    pkv.load_library()
+
+
+@pytest.fixture(autouse=True)
+def _clean():
+    yield
+    torch.cuda.synchronize()
+    assert pkv.pkv_get_device_error() == 0
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def dev(x, dtype):
+    return torch.as_tensor(np.ascontiguousarray(x)).to(dtype).cuda()
+
+
+def close(got, want, bound, what=""):
+    got = f64(got) if isinstance(got, torch.Tensor) else got
+    nan = np.isnan(want)
+    assert (np.isnan(got) == nan).all(), f"{what}: NaN in other places ({np.isnan(got).sum()} for {nan.sum()})"
+    inf = np.isinf(want)
+    assert (got[inf] == want[inf]).all(), what
+    fin = ~nan & ~inf
+    off = np.abs(got[fin] - want[fin]) - bound[fin]
+    assert (off <= 0).all(), f"{what}: off by {off.max():.3g} more than the bound, " \
+        f"at {np.argwhere(fin)[off.argmax()]}, {np.abs(got[fin] - want[fin])[off.argmax()]:.3g}"
+
+
+# ------------------------------------------------------------ norm, rotation, append
+def rope_case(T, hq, hkv, rot, inter, wq, wk, seed=0, eps=1e-6, max_pos=5000):
+    g = torch.Generator().manual_seed(seed)
+    qkv = (torch.randn(T, hq + 2 * hkv, 128, generator=g) * 2).to(BF).cuda()
+    w = [(1 + 0.3 * torch.randn(128, generator=g)).to(BF).cuda() if on else None for on in (wq, wk)]
+    nb = T // 16 + 3
+    slots = torch.randperm(nb * 16, generator=g)[:T].cuda()
+    pos = torch.randint(0, max_pos, (T,), generator=g).cuda()
+    pools = [torch.randn(nb, hkv, 16, 128, generator=g).to(BF).cuda() for _ in range(2)]
+    return qkv, w, slots, pos, pools, torch.from_numpy(ref.table(max_pos, rot)).cuda()
+
+
+def rope_check(qkv, before, w, slots, pos, pools, cs, inter, out, hq, hkv, eps, old_out):
+    T = qkv.shape[0]
+    live = (slots >= 0).cpu().numpy()
+    x = f64(before)
+    rows = cs.cpu().numpy()[np.where(live, pos.cpu().numpy(), 0)]
+    want, size = [], []
+    for a, ww in ((x[:, :hq], w[0]), (x[:, hq:hq + hkv], w[1])):
+        y, s = ref.rotate(a if ww is None else ref.norm(a, f64(ww), eps), rows, inter)
+        want.append(y)
+        size.append(s)
+    close(f64(out)[live], want[0][live], ref.turned_bound(want[0], size[0])[live], "q")
+    assert torch.equal(out[~torch.from_numpy(live).cuda()], old_out[~torch.from_numpy(live).cuda()])
+    k, v = (f64(p) for p in pools[1])
+    k0, v0 = (f64(p) for p in pools[0])
+    bound = np.zeros_like(k0)
+    s = slots.cpu().numpy()[live]
+    k0[s // 16, :, s % 16] = want[1][live]
+    bound[s // 16, :, s % 16] = ref.turned_bound(want[1], size[1])[live]
+    v0[s // 16, :, s % 16] = x[:, hq + hkv:][live]
+    close(k, k0, bound, "k pool")
+    assert np.array_equal(v, v0), "v pool"
+
+
+@pytest.mark.parametrize("T,hq,hkv,rot,inter,wq,wk", [
+    (1, 1, 1, 128, False, True, True), (1, 12, 2, 128, True, True, True), (3, 5, 5, 64, False, True, False),
+    (7, 21, 3, 96, False, False, True), (64, 12, 2, 128, False, True, True), (33, 8, 8, 16, True, False, False),
+    (130, 32, 8, 112, False, True, True), (701, 32, 8, 48, True, True, True), (2000, 4, 1, 128, False, True, True),
+    (5, 0, 2, 128, False, True, True), (300, 70, 7, 80, True, True, True)])
+@pytest.mark.parametrize("place", ["split", "in place", "apart"])
+def test_norm_rope_append(T, hq, hkv, rot, inter, wq, wk, place):
+    eps = 1e-5
+    qkv, w, slots, pos, pools, cs = rope_case(T, hq, hkv, rot, inter, wq, wk, seed=T + hq)
+    if T > 4:
+        slots[T // 2] = -1
+        pos[T // 2] = 1 << 40  # not looked at
+    before, old = qkv.clone(), [p.clone() for p in pools]
+    q, k, v = qkv.split([hq, hkv, hkv], 1)
+    if place == "split":
+        kw, old_out = dict(q_out=torch.full((T, hq, 128), 7.0, dtype=BF, device="cuda")), None
+        old_out = kw["q_out"].clone()
+    elif place == "in place":
+        kw, old_out = dict(q_out=q), before[:, :hq].clone()
+    else:
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+        wide = torch.full((T, hq + 3, 128), 7.0, dtype=BF, device="cuda")
+        kw, old_out = dict(q_out=wide[:, 2:2 + hq]), wide[:, 2:2 + hq].clone()
+    out = pkv.pkv_norm_rope_append(q, k, v, pos, cs, slots, *pools, q_weight=w[0], k_weight=w[1], eps=eps,
+                                   interleaved=inter, **kw)
+    rope_check(qkv, before, w, slots, pos, (old, pools), cs, inter, out, hq, hkv, eps, old_out)
+    if place == "apart":
+        assert (wide[:, :2] == 7).all() and (wide[:, 2 + hq:] == 7).all()
+
+
+def test_norm_rope_extremes():
+    """Rows of zeros, of one huge and of tiny values, infinities and NaN."""
+    qkv, w, slots, pos, pools, cs = rope_case(8, 2, 1, 128, False, True, True)
+    qkv[0] = 0
+    qkv[1] = 3e38
+    qkv[2, :, 5] = 2e38
+    qkv[3] = 1e-20
+    qkv[4, 0, 3] = float("inf")
+    qkv[5, 1, 4] = float("nan")
+    qkv[6] *= 1e19
+    before, old = qkv.clone(), [p.clone() for p in pools]
+    q, k, v = qkv.split([2, 1, 1], 1)
+    out = pkv.pkv_norm_rope_append(q, k, v, pos, cs, slots, *pools, q_weight=w[0], k_weight=w[1], eps=1e-6)
+    x = f64(before)
+    rows = cs.cpu().numpy()[pos.cpu().numpy()]
+    y, s = ref.rotate(ref.norm(x[:, :2], f64(w[0]), 1e-6), rows, False)
+    ok = np.isfinite(x[:, :2]).all(2)
+    close(f64(out)[ok], y[ok], ref.turned_bound(y, s)[ok])
+    assert np.isnan(f64(out)[5, 1]).all()
+    got = f64(out)[4, 0]  # x / inf: zeros but for inf / inf, which its pair gets too
+    assert np.isnan(got[[3, 67]]).all() and (np.delete(got, [3, 67]) == 0).all()
+
+
+def test_norm_rope_errors_skip_the_token():
+    qkv, w, slots, pos, pools, cs = rope_case(6, 4, 2, 128, False, True, True)
+    old = [p.clone() for p in pools]
+    bad_slots, bad_pos = slots.clone(), pos.clone()
+    bad_slots[1] = pools[0].shape[0] * 16
+    bad_pos[2], bad_pos[4] = cs.shape[0], -1
+    q, k, v = qkv.split([4, 2, 2], 1)
+    out = torch.full((6, 4, 128), 7.0, dtype=BF, device="cuda")
+    pkv.pkv_norm_rope_append(q, k, v, bad_pos, cs, bad_slots, *pools, q_weight=w[0], k_weight=w[1], q_out=out)
+    assert pkv.pkv_get_device_error() == pkv._binding.PKV_ERR_DEVICE_BOUNDS
+    bad_slots[[1, 2, 4]] = -1
+    rope_check(qkv, qkv, w, bad_slots, bad_pos, (old, pools), cs, False, out, 4, 2, 1e-6,
+               torch.full((6, 4, 128), 7.0, dtype=BF, device="cuda"))
+
+
+@pytest.mark.parametrize("T,heads,inter,weight,place", [
+    (1, 1, False, True, "out"), (1, 16, True, True, "in"), (5, 128, True, False, "out"), (64, 16, True, True, "out"),
+    (7, 0, False, True, "none"), (130, 33, False, True, "in"), (1500, 40, True, True, "out"), (300, 128, False, True, "turned")])
+def test_append_latent(T, heads, inter, weight, place):
+    g = torch.Generator().manual_seed(T + heads)
+    wide = (torch.randn(T, 1600, generator=g) * 2).to(BF).cuda()
+    kv = wide[:, 1024:]
+    w = (1 + 0.3 * torch.randn(512, generator=g)).to(BF).cuda() if weight else None
+    nb = T // 16 + 3
+    slots = torch.randperm(nb * 16, generator=g)[:T].cuda()
+    pos = torch.randint(0, 3000, (T,), generator=g).cuda()
+    if T > 4:
+        slots[3] = -1
+        pos[3] = -5
+    live = (slots >= 0).cpu().numpy()
+    pool = torch.randn(nb, 16, 576, generator=g).to(BF).cuda()
+    cs = torch.from_numpy(ref.table(3000, 64)).cuda()
+    want_pool, bound = f64(pool), np.zeros((nb, 16, 576))
+    rows = cs.cpu().numpy()[np.where(live, pos.cpu().numpy(), 0)]
+    x = f64(kv)
+    c = x[:, None, :512] if w is None else ref.norm(x[:, None, :512], f64(w), 1e-6)
+    r, size = ref.rotate(x[:, None, 512:], rows, inter)
+    s = slots.cpu().numpy()[live]
+    y, z = np.concatenate([c, r], 2)[:, 0], np.concatenate([np.abs(c), size], 2)[:, 0]
+    want_pool.reshape(-1, 576)[s] = y[live]
+    bound.reshape(-1, 576)[s] = ref.turned_bound(y, z)[live]
+    kw, out = {}, None
+    if place != "none":
+        full = torch.randn(T, heads, 192, generator=g).to(BF).cuda()
+        qr = full[:, :, 128:]
+        if place == "turned":  # heads outermost
+            qr = torch.randn(heads, T, 192, generator=g).to(BF).cuda()[:, :, 128:].transpose(0, 1)
+        q0 = qr.clone()
+        out = qr if place == "in" else torch.full((T, heads, 576), 7.0, dtype=BF, device="cuda")[:, :, 512:]
+        old = out.clone()
+        kw = dict(q_rope=qr) if place == "in" else dict(q_rope=qr, q_rope_out=out)
+    pkv.pkv_append_latent(kv, pos, cs, slots, pool, weight=w, interleaved=inter, **kw)
+    close(pool, want_pool, bound, "pool")
+    if out is not None:
+        y, z = ref.rotate(f64(q0), rows, inter)
+        close(f64(out)[live], y[live], ref.turned_bound(y, z)[live], "q")
+        assert np.array_equal(f64(out)[~live], f64(old)[~live])
+
+
+def test_append_latent_errors_skip_the_token():
+    T = 5
+    kv = torch.randn(T, 576, device="cuda").to(BF)
+    pool = torch.zeros(2, 16, 576, dtype=BF, device="cuda")
+    cs = torch.from_numpy(ref.table(100, 64)).cuda()
+    slots = torch.tensor([0, 32, 2, 3, 4], device="cuda")
+    pos = torch.tensor([1, 1, 100, -1, 99], device="cuda")
+    qr = torch.ones(T, 3, 64, device="cuda", dtype=BF)
+    pkv.pkv_append_latent(kv, pos, cs, slots, pool, q_rope=qr)
+    assert pkv.pkv_get_device_error() == pkv._binding.PKV_ERR_DEVICE_BOUNDS
+    rows = pool.view(32, 576).any(1).cpu().tolist()
+    assert [i for i, on in enumerate(rows) if on] == [0, 4]
+    assert (qr[[1, 2, 3]] == 1).all() and (qr[0] != 1).any()
+
+
+# --------------------------------------------------------------- absorbed attention
+def lat_case(lens, qs, heads, seed=0, pad=0, poison=True):
+    """A step over a latent cache, every slot that no request owns NaN."""
+    g = torch.Generator().manual_seed(seed)
+    cols = max([ref.cdiv(n, 16) for n in lens] + [1]) + 1
+    need = sum(ref.cdiv(n, 16) for n in lens)
+    nb = need + 3
+    perm = torch.randperm(nb, generator=g).tolist()
+    tab = np.full((len(lens), cols), 10 ** 8, np.int32)
+    pool = torch.full((nb, 16, 576), float("nan") if poison else 0.0)
+    for r, n in enumerate(lens):
+        for b in range(ref.cdiv(n, 16)):
+            tab[r, b] = perm.pop()
+            k = min(16, n - 16 * b)
+            pool[tab[r, b], :k] = torch.randn(k, 576, generator=g)
+    qsl = np.concatenate([[0], np.cumsum(qs)]).astype(np.int32)
+    q = torch.randn(int(qsl[-1]) + pad, heads, 576, generator=g)
+    return dict(q=q.to(BF).cuda(), pool=pool.to(BF).cuda(), tab=tab, lens=np.array(lens, np.int32), qsl=qsl,
+                scale=192 ** -0.5)
+
+
+def lat_run(c, **kw):
+    return pkv.pkv_attention_latent(c["q"], c["pool"], dev(c["tab"], torch.int32), dev(c["lens"], torch.int32),
+                                    dev(c["qsl"], torch.int32), c["scale"], **kw)
+
+
+def lat_check(c, out):
+    n = int(c["qsl"][-1])
+    want, bound = ref.absorbed(f64(c["q"]), f64(c["pool"]), c["tab"], c["lens"], c["qsl"], c["scale"])
+    close(f64(out)[:n], want[:n], bound[:n])
+
+
+@pytest.mark.parametrize("heads", [1, 5, 16, 17, 32, 33, 48, 64, 65, 100, 128])
+@pytest.mark.parametrize("lens", [[1], [64], [65], [17, 64, 100, 128], [1, 2, 15, 16, 63, 130, 700]])
+def test_absorbed_decode(heads, lens):
+    c = lat_case(lens, [1] * len(lens), heads, seed=heads + len(lens))
+    lat_check(c, lat_run(c))
+
+
+@pytest.mark.parametrize("heads", [1, 3, 16, 20, 64, 128])
+@pytest.mark.parametrize("lens,qs", [([4], [4]), ([70, 9, 300], [5, 9, 1]), ([200, 130, 64, 1], [130, 1, 64, 1]),
+                                     ([1000, 67], [3, 66])])
+def test_absorbed_chunks(heads, lens, qs):
+    c = lat_case(lens, qs, heads, seed=heads)
+    lat_check(c, lat_run(c))
+
+
+@pytest.mark.parametrize("heads,lens,qs", [(16, [5000], [1]), (128, [5000, 300], [1, 1]), (16, [3000, 50, 2000], [4, 1, 70]),
+                                           (40, [20000], [2]), (8, [900] * 40, [1] * 40)])
+def test_absorbed_split_rows(heads, lens, qs):
+    c = lat_case(lens, qs, heads, seed=1)
+    lat_check(c, lat_run(c))
+
+
+def test_absorbed_many_requests():
+    rng = np.random.default_rng(5)
+    lens = rng.integers(1, 90, 1500).tolist()
+    qs = [min(n, int(q)) for n, q in zip(lens, rng.integers(0, 3, 1500))]
+    c = lat_case(lens, qs, 2, seed=3)
+    lat_check(c, lat_run(c))

@@ -457,6 +457,37 @@ int pkv_attention_latent(const void *q, const void *pool, const int32_t *block_t
                          cudaStream_t stream);
 
 /*
+ * Expands cached latents: for every request r and cached position j < seq_lens[r],
+ *   kv[kv_start_loc[r] + j, h, :] = W_h c_j   (256 numbers: key 0..127 | value 128..255)
+ *   k_rope[kv_start_loc[r] + j, :] = the rotated key of position j
+ * kv [num_rows, num_q_heads, 256], k_rope [num_rows, 64], weight [num_q_heads, 256,
+ * 512], all bf16; products summed in fp32 and rounded once.  kv_start_loc
+ * [num_reqs + 1] int32 is the running sum of seq_lens; a request for which it is
+ * not, or whose rows or table do not hold it, is skipped and recorded as
+ * PKV_ERR_DEVICE_BOUNDS.  Rows of no request are not written.  num_q_heads up to
+ * 4096; num_q_tokens is not read.
+ */
+int pkv_expand_latent(const void *pool, const void *weight, const int32_t *block_tables,
+                      const int32_t *seq_lens, const int32_t *kv_start_loc, void *kv, void *k_rope,
+                      int32_t num_rows, const pkv_dims *dims, cudaStream_t stream);
+
+/*
+ * Causal attention over expanded keys and values: for row (token, head) with
+ * query q [num_q_tokens, num_q_heads, 192],
+ *   s_j = scale (<q[0:128], kv[j, h, 0:128]> + <q[128:192], k_rope[j]>)
+ *   out [num_q_tokens, num_q_heads, 128] = sum_j softmax(s)_j kv[j, h, 128:256]
+ * over the keys j of its request (rows kv_start_loc[r] .. + seq_lens[r] - 1) that
+ * the token sees: those up to its own position, the request's query tokens being
+ * its last.  Padded steps, special values, roundings and workspace as in
+ * pkv_attention_latent; requests without query tokens cost nothing.  Of dims,
+ * num_reqs, num_q_tokens and num_q_heads (up to 4096) count.
+ */
+int pkv_attention_expanded(const void *q, const void *kv, const void *k_rope, const int32_t *seq_lens,
+                           const int32_t *query_start_loc, const int32_t *kv_start_loc, float scale,
+                           void *out, int32_t num_rows, const pkv_dims *dims, void *workspace,
+                           size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Bytes of workspace pkv_attention_cascade needs for these dims: the
  * pkv_attention workspace (same head, initialised the same way with
  * pkv_workspace_init), plus partial states for up to 8 chunks of each shared

@@ -12,7 +12,11 @@ reads prompts shared by groups of requests once per group, and
 ``pkv_copy_blocks`` copies or swaps whole blocks.  ``pkv_append_fp8_block`` /
 ``pkv_attention_fp8_block`` keep an e4m3 cache with a scale per (block, KV
 head), and ``pkv_build_step`` / ``pkv_release_blocks`` build a step's block
-tables and slot map on the GPU and give blocks back.  ``get_options`` /
+tables and slot map on the GPU and give blocks back.  ``pkv_norm_rope_append``
+norms and rotates queries and keys on the way into the cache.  A cache of
+latents is filled by ``pkv_append_latent`` and read by ``pkv_attention_latent``
+(absorbed queries: decode) or ``pkv_expand_latent`` and
+``pkv_attention_expanded`` (chunks).  ``get_options`` /
 ``set_options`` / ``options`` read and change the launch and routing options.
 """
 from ._binding import (  # noqa: F401
@@ -23,5 +27,6 @@ from ._binding import (  # noqa: F401
     pkv_get_device_error, pkv_last_error, pkv_workspace_init,
     pkv_build_step, pkv_release_blocks, pkv_append_fp8_block, pkv_attention_fp8_block,
     LatentWorkspace, pkv_norm_rope_append, pkv_append_latent, pkv_attention_latent,
+    pkv_expand_latent, pkv_attention_expanded,
     Options, get_options, set_options, options,
 )

@@ -33,7 +33,8 @@ EXPORTED = ("pkv_append", "pkv_attention", "pkv_attention_workspace_size",
             "pkv_append_attention", "pkv_append_attention_fp8", "pkv_get_options",
             "pkv_set_options", "pkv_build_step", "pkv_release_blocks", "pkv_append_fp8_block",
             "pkv_attention_fp8_block", "pkv_norm_rope_append", "pkv_append_latent",
-            "pkv_latent_workspace_size", "pkv_attention_latent")
+            "pkv_latent_workspace_size", "pkv_attention_latent", "pkv_expand_latent",
+            "pkv_attention_expanded")
 
 # Fields of pkv_options, in declaration order (int32 each).
 OPTION_FIELDS = ("pdl", "early_plan", "early_kv", "early_trigger", "plan_cache", "decode_tc",
@@ -127,6 +128,10 @@ def load_library(path: str = LIB_PATH):
         lib.pkv_latent_workspace_size.restype = sz
         lib.pkv_attention_latent.argtypes = [vp] * 5 + [f32, vp, dp, vp, sz, vp]
         lib.pkv_attention_latent.restype = ctypes.c_int
+        lib.pkv_expand_latent.argtypes = [vp] * 7 + [i32, dp, vp]
+        lib.pkv_expand_latent.restype = ctypes.c_int
+        lib.pkv_attention_expanded.argtypes = [vp] * 6 + [f32, vp, i32, dp, vp, sz, vp]
+        lib.pkv_attention_expanded.restype = ctypes.c_int
         lib.pkv_get_options.argtypes = [ctypes.POINTER(Options)]
         lib.pkv_get_options.restype = None
         lib.pkv_set_options.argtypes = [ctypes.POINTER(Options)]
@@ -865,6 +870,63 @@ def pkv_attention_latent(q, pool, block_tables, seq_lens, query_start_loc, scale
     ws = _latent_workspace(workspace, q, dev, stream)
     dims = Dims(R, Tq, Hq, 1, D, bs, nb, cols)
     _call((_lib or load_library()).pkv_attention_latent, dev, *ptrs[:5], scale, ptrs[5],
+          ctypes.byref(dims), ws.ptr, ws.nbytes, _raw_stream(stream, dev))
+    return out
+
+
+_EXPAND = _spec(("pool", _BF16, 3), ("weight", _BF16, 3), ("block_tables", _I32, 2),
+                ("seq_lens", _I32, 1), ("kv_start_loc", _I32, 1), ("kv", _BF16, 3),
+                ("k_rope", _BF16, 2))
+
+
+def pkv_expand_latent(pool, weight, block_tables, seq_lens, kv_start_loc, kv, k_rope, stream=None):
+    """Expand cached latents for pkv_attention_expanded: row kv_start_loc[r] + j of
+    kv [rows, heads, 256] becomes weight[h] c_j (weight [heads, 256, 512] bf16: 128
+    key rows, then 128 value rows a head), that of k_rope [rows, 64] the rotated
+    key, for the seq_lens[r] cached positions j of every request r.  kv_start_loc
+    [R + 1] is the running sum of seq_lens; rows past its last are not written."""
+    dev, ptrs = _fast_need((pool, weight, block_tables, seq_lens, kv_start_loc, kv, k_rope), _EXPAND)
+    nb, bs, D = pool.shape
+    H = weight.shape[0]
+    R, cols = block_tables.shape
+    if seq_lens.shape[0] != R or kv_start_loc.shape[0] != R + 1:
+        raise ValueError("seq_lens, kv_start_loc and block_tables disagree on num_reqs")
+    if weight.shape[1:] != (256, LATENT):
+        raise ValueError(f"weight must be [heads, 256, {LATENT}]")
+    rows = kv.shape[0]
+    if kv.shape[1:] != (H, 256) or k_rope.shape != (rows, ROPE):
+        raise ValueError(f"kv must be [rows, {H}, 256] and k_rope [rows, {ROPE}]")
+    dims = Dims(R, 0, H, 1, D, bs, nb, cols)
+    _call((_lib or load_library()).pkv_expand_latent, dev, *ptrs, rows, ctypes.byref(dims),
+          _raw_stream(stream, dev))
+
+
+_ATTENTION_EXPANDED = _spec(("q", _BF16, 3), ("kv", _BF16, 3), ("k_rope", _BF16, 2),
+                            ("seq_lens", _I32, 1), ("query_start_loc", _I32, 1),
+                            ("kv_start_loc", _I32, 1), ("out", _BF16, 3))
+
+
+def pkv_attention_expanded(q, kv, k_rope, seq_lens, query_start_loc, kv_start_loc, scale, out=None,
+                           workspace: LatentWorkspace | None = None, stream=None):
+    """Causal attention of prefill chunks over expanded keys and values (see
+    pkv_expand_latent): q [Tq, heads, 192] bf16 (128 dims that meet the expanded
+    keys, then the 64 rotated ones).  Returns out [Tq, heads, 128] bf16."""
+    if out is None and isinstance(q, torch.Tensor) and q.dim() == 3:
+        out = torch.empty((*q.shape[:2], 128), dtype=_BF16, device=q.device)
+    dev, ptrs = _fast_need((q, kv, k_rope, seq_lens, query_start_loc, kv_start_loc, out),
+                           _ATTENTION_EXPANDED)
+    Tq, H, D = q.shape
+    R = seq_lens.shape[0]
+    if query_start_loc.shape[0] != R + 1 or kv_start_loc.shape[0] != R + 1:
+        raise ValueError("seq_lens, query_start_loc and kv_start_loc disagree on num_reqs")
+    rows = kv.shape[0]
+    if D != 192 or kv.shape[1:] != (H, 256) or k_rope.shape != (rows, ROPE):
+        raise ValueError(f"q must be [tokens, heads, 192], kv [rows, heads, 256], k_rope [rows, {ROPE}]")
+    if tuple(out.shape) != (Tq, H, 128):
+        raise ValueError(f"out must be [{Tq}, {H}, 128]")
+    ws = _latent_workspace(workspace, q, dev, stream)
+    dims = Dims(R, Tq, H, 1, LATENT + ROPE, 16, 1, 1)
+    _call((_lib or load_library()).pkv_attention_expanded, dev, *ptrs[:6], scale, ptrs[6], rows,
           ctypes.byref(dims), ws.ptr, ws.nbytes, _raw_stream(stream, dev))
     return out
 

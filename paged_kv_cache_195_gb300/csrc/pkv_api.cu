@@ -1264,6 +1264,118 @@ int pkv_attention_latent(const void* q, const void* pool, const int32_t* block_t
   return PKV_OK;
 }
 
+int pkv_expand_latent(const void* pool, const void* weight, const int32_t* block_tables,
+                      const int32_t* seq_lens, const int32_t* kv_start_loc, void* kv, void* k_rope,
+                      int32_t num_rows, const pkv_dims* dims, cudaStream_t stream) {
+  g_last_error[0] = '\0';
+  int rc = check_latent_dims(dims, false);
+  if (rc != PKV_OK) return rc;
+  if (dims->num_q_heads == 0) return fail(PKV_ERR_INVALID, "num_q_heads is 0");
+  if (num_rows < 0) return fail(PKV_ERR_INVALID, "num_rows < 0");
+  if (dims->num_reqs == 0 || num_rows == 0) return PKV_OK;
+  if (dims->num_blocks == 0) return fail(PKV_ERR_INVALID, "the pool has no blocks");
+  if (!pool || !weight || !block_tables || !seq_lens || !kv_start_loc || !kv || !k_rope)
+    return fail(PKV_ERR_INVALID, "NULL pointer argument");
+  if (!aligned16(pool) || !aligned16(weight) || !aligned16(kv) || !aligned16(k_rope))
+    return fail(PKV_ERR_INVALID, "the pool, weight, kv and k_rope must be 16-byte aligned");
+  DeviceState* st = device_state();
+  if (!st) return PKV_ERR_CUDA;
+  const pkv_options opt = current_options();
+  pkv::LatentExpandLaunch L{};
+  pkv::LatentExpandParams& p = L.p;
+  p.block_tables = block_tables;
+  p.seq_lens = seq_lens;
+  p.kv_start = kv_start_loc;
+  p.pool = static_cast<const __nv_bfloat16*>(pool);
+  p.kv = static_cast<__nv_bfloat16*>(kv);
+  p.k_rope = static_cast<__nv_bfloat16*>(k_rope);
+  p.err = st->err;
+  p.num_reqs = dims->num_reqs;
+  p.num_rows = num_rows;
+  p.num_heads = dims->num_q_heads;
+  p.num_blocks = dims->num_blocks;
+  p.max_blocks = dims->max_blocks_per_req;
+  p.pdl = opt.pdl != 0;
+  p.early_plan = p.pdl && opt.early_plan != 0;
+  p.wait_limit_ns = (unsigned long long)opt.wait_limit_us * 1000ull;
+  const cuuint32_t wbox[3] = {64, 128, 1};
+  rc = encode_latent_map(&L.kmap, pool, dims);
+  if (rc == PKV_OK)
+    rc = encode_bf16_3d(&L.wmap, weight, pkv::kLatent, dims->num_q_heads * (pkv::kNope + pkv::kValDim), 1,
+                        pkv::kLatent, (long long)dims->num_q_heads * (pkv::kNope + pkv::kValDim) * pkv::kLatent,
+                        wbox, "weight");
+  if (rc != PKV_OK) return rc;
+  L.grid = st->sm_count;
+  const cudaError_t e = pkv::launch_latent_expand(L, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "expand_latent launch");
+  return PKV_OK;
+}
+
+int pkv_attention_expanded(const void* q, const void* kv, const void* k_rope, const int32_t* seq_lens,
+                           const int32_t* query_start_loc, const int32_t* kv_start_loc, float scale,
+                           void* out, int32_t num_rows, const pkv_dims* dims, void* workspace,
+                           size_t workspace_bytes, cudaStream_t stream) {
+  g_last_error[0] = '\0';
+  int rc = check_latent_dims(dims, false);
+  if (rc != PKV_OK) return rc;
+  if (dims->num_q_heads == 0) return fail(PKV_ERR_INVALID, "num_q_heads is 0");
+  if (num_rows < 0) return fail(PKV_ERR_INVALID, "num_rows < 0");
+  if (dims->num_reqs == 0 || dims->num_q_tokens == 0) return PKV_OK;
+  if (num_rows == 0) return fail(PKV_ERR_INVALID, "query tokens without keys");
+  if (!q || !kv || !k_rope || !seq_lens || !query_start_loc || !kv_start_loc || !out || !workspace)
+    return fail(PKV_ERR_INVALID, "NULL pointer argument");
+  if (!aligned16(q) || !aligned16(kv) || !aligned16(k_rope) || !aligned16(out))
+    return fail(PKV_ERR_INVALID, "q, kv, k_rope and out must be 16-byte aligned");
+  if (!(scale - scale == 0.f) || scale == 0.f)
+    return fail(PKV_ERR_INVALID, "scale must be finite, non-zero");
+  DeviceState* st = device_state();
+  if (!st) return PKV_ERR_CUDA;
+  const LatentLayout w = latent_layout(st->sm_count);
+  if (workspace_bytes < w.total)
+    return fail(PKV_ERR_WORKSPACE, "workspace %zu bytes, need %zu", workspace_bytes, w.total);
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0)
+    return fail(PKV_ERR_INVALID, "workspace must be 256-byte aligned");
+  const pkv_options opt = current_options();
+  const int heads = dims->num_q_heads;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  pkv::LatentPrefillLaunch L{};
+  pkv::LatentPrefillParams& p = L.p;
+  p.seq_lens = seq_lens;
+  p.qsl = query_start_loc;
+  p.kv_start = kv_start_loc;
+  p.kv = static_cast<const __nv_bfloat16*>(kv);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.piece_ml = reinterpret_cast<float*>(ws + w.ml);
+  p.piece_o = reinterpret_cast<float*>(ws + w.o);
+  p.sched = reinterpret_cast<unsigned long long*>(ws);
+  p.err = st->err;
+  p.num_reqs = dims->num_reqs;
+  p.num_q_tokens = dims->num_q_tokens;
+  p.num_rows = num_rows;
+  p.num_heads = heads;
+  // Items are split, and the joining kernel follows, only where the step's rows,
+  // were they all in use, are fewer items than CTAs.
+  const long long items = ((long long)dims->num_q_tokens + 127) / 128 * heads;
+  p.max_pieces = items < st->sm_count ? 2 * st->sm_count : 0;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.pdl = opt.pdl != 0;
+  p.early_plan = p.pdl && opt.early_plan != 0;
+  p.wait_limit_ns = (unsigned long long)opt.wait_limit_us * 1000ull;
+  const cuuint32_t box[3] = {64, 1, 128}, rbox[3] = {64, 128, 1};
+  constexpr int kQ = pkv::kNope + pkv::kRopeDim, kKv = pkv::kNope + pkv::kValDim;
+  rc = encode_bf16_3d(&L.qmap, q, kQ, heads, dims->num_q_tokens, kQ, (long long)heads * kQ, box, "q");
+  if (rc == PKV_OK)
+    rc = encode_bf16_3d(&L.kvmap, kv, kKv, heads, num_rows, kKv, (long long)heads * kKv, box, "kv");
+  if (rc == PKV_OK)
+    rc = encode_bf16_3d(&L.rmap, k_rope, pkv::kRopeDim, num_rows, 1, pkv::kRopeDim,
+                        (long long)num_rows * pkv::kRopeDim, rbox, "k_rope");
+  if (rc != PKV_OK) return rc;
+  L.grid = st->sm_count;
+  const cudaError_t e = pkv::launch_latent_prefill(L, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "expanded attention launch");
+  return PKV_OK;
+}
+
 void pkv_get_options(pkv_options* opts) {
   if (opts) *opts = current_options();
 }

@@ -100,4 +100,58 @@ struct LatentDecodeLaunch {
 
 cudaError_t launch_latent_decode(const LatentDecodeLaunch& L, cudaStream_t stream);
 
+// Cached latents expanded to keys and values of every head.
+struct LatentExpandParams {
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* kv_start;     // [num_reqs + 1]: rows of kv of each request
+  const __nv_bfloat16* pool;   // [num_blocks, 16, 576]
+  __nv_bfloat16* kv;           // [num_rows, num_heads, 256]
+  __nv_bfloat16* k_rope;       // [num_rows, 64]
+  int* err;
+  int num_reqs, num_rows, num_heads, num_blocks, max_blocks;
+  int early_plan;
+  int pdl;
+  unsigned long long wait_limit_ns;
+};
+
+struct LatentExpandLaunch {
+  CUtensorMap kmap;  // as LatentDecodeLaunch::kmap
+  CUtensorMap wmap;  // weight as [1][num_heads * 256][512], box (64, 128, 1), 128-byte swizzle
+  LatentExpandParams p;
+  int grid;
+};
+
+cudaError_t launch_latent_expand(const LatentExpandLaunch& L, cudaStream_t stream);
+
+// Causal attention of chunks over expanded keys and values.
+struct LatentPrefillParams {
+  const int32_t* seq_lens;
+  const int32_t* qsl;
+  const int32_t* kv_start;
+  const __nv_bfloat16* kv;     // [num_rows, H, 256]: key | value
+  __nv_bfloat16* out;          // [num_q_tokens, H, 128]
+  // Partial states of items split over their keys, by piece number.
+  float* piece_ml;             // [max_pieces][128][2]
+  float* piece_o;              // [max_pieces][128][128]
+  unsigned long long* sched;   // [0] next piece, [1] CTAs done; zero between launches
+  int* err;
+  int num_reqs, num_q_tokens, num_rows, num_heads;
+  int max_pieces;              // 0: items are not split
+  float scale_log2;
+  int early_plan;
+  int pdl;
+  unsigned long long wait_limit_ns;
+};
+
+struct LatentPrefillLaunch {
+  CUtensorMap qmap;   // q as [tokens][H][192], box (64, 1, 128), 128-byte swizzle
+  CUtensorMap kvmap;  // kv as [rows][H][256], same box
+  CUtensorMap rmap;   // k_rope as [1][rows][64], box (64, 128, 1)
+  LatentPrefillParams p;
+  int grid;
+};
+
+cudaError_t launch_latent_prefill(const LatentPrefillLaunch& L, cudaStream_t stream);
+
 }  // namespace pkv

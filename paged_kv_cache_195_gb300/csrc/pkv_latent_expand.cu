@@ -1,0 +1,391 @@
+// pkv_latent_expand.cu -- cached latents expanded to keys and values of every
+// head, on tcgen05 tensor cores: for key j and head h the 256 numbers
+//
+//   kv[j, h, :] = W_h c_j,   W_h [256 x 512], c_j the latent of position j
+//
+// a matrix product whose left operand is gathered through the block table.
+// Bound: tensor core (512 flops a byte written, the largest stream).
+//
+// Tiling.  A unit of work is (128 keys of one request, head): D[128 x 256] =
+// C[128 x 512] W_h^T.  The units form one sequence, heads fastest, cut in equal
+// ranges, one a CTA: a tile's latents (128 KB, eight 64-dim chunks gathered by
+// 2-D TMA copies of pool blocks) stay in shared memory for all of its heads, and
+// the weights stream by from L2 in [128 outputs x 64 dims] pieces.  D has two
+// TMEM buffers of 256 columns, so that a unit's rows are rounded and stored
+// while the next unit is multiplied.  Keys behind the request's end are rows of
+// D that nobody stores.
+//
+// Roles (192 threads): warps 0-3 take D's rows, one a thread, round them once,
+// and store each through a row of its own in shared memory with bulk copies, so
+// that global writes are whole rows; warp 4 copies, warp 5 issues the MMAs.
+#include <climits>
+
+#include "pkv_latent.h"
+#include "pkv_tc.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kEpiWarps = 4;
+constexpr int kWarpLoad = kEpiWarps;
+constexpr int kWarpMma = kEpiWarps + 1;
+constexpr int kThreads = 32 * (kEpiWarps + 2);
+constexpr int kKeys = 128;                 // keys of a unit: MMA M
+constexpr int kOut = kNope + kValDim;      // outputs of a unit
+constexpr int kHalf = 128;                 // MMA N
+constexpr int kChunks = kLatent / 64;
+constexpr int kChunkBytes = 128 * 128;     // 128 rows of 64 bf16
+constexpr int kStages = 4;                 // weight pieces in flight
+constexpr int kRowCols = 64;               // columns that a row stores at a time
+constexpr int kRowBytes = kRowCols * 2 + 16;  // (16 bytes apart from a bank-aligned stride)
+
+struct __align__(1024) Smem {
+  uint8_t a[kChunks][kChunkBytes];
+  uint8_t b[kStages][kChunkBytes];
+  uint8_t row[kKeys][kRowBytes];
+  uint64_t a_full[kChunks], a_empty[kChunks];
+  uint64_t b_full[kStages], b_empty[kStages];
+  uint64_t d_full[2], d_empty[2];
+  uint64_t drained;
+  uint32_t tmem_base;
+  WaitCtl wait;
+  long long part[kThreads / 32];
+  long long range_lo, range_hi, start_base;
+  int start_req;
+};
+static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "latent expand shared memory");
+
+__device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
+
+// A request's keys and the first row of kv that they go to; keys 0: nothing to do.
+struct Req {
+  int keys, row0;
+};
+
+__device__ __forceinline__ Req load_req(const LatentExpandParams& p, int r, bool* bad) {
+  const int n = __ldg(p.seq_lens + r), a = __ldg(p.kv_start + r), b = __ldg(p.kv_start + r + 1);
+  *bad = !(n >= 0 && n <= p.max_blocks * kBlockSize && a >= 0 && b <= p.num_rows && b - a == n);
+  return Req{*bad ? 0 : n, a};
+}
+
+__device__ __forceinline__ long long units(const LatentExpandParams& p, const Req& a) {
+  return (long long)cdiv(a.keys, kKeys) * p.num_heads;
+}
+
+// The CTA's range of the units and the request that it starts in.  All threads.
+__device__ __forceinline__ void plan_range(const LatentExpandParams& p, Smem& sm) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = cdiv(p.num_reqs, kThreads);
+  const int r0 = min(tid * per, p.num_reqs), r1 = min(r0 + per, p.num_reqs);
+  long long mine = 0;
+  for (int r = r0; r < r1; ++r) {
+    bool bad;
+    mine += units(p, load_req(p, r, &bad));
+    if (bad && blockIdx.x == 0) record_error(p.err, kErrBounds);  // the request is skipped
+  }
+  long long incl = mine;
+  #pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) sm.part[warp] = incl;
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += sm.part[w];
+    total += sm.part[w];
+  }
+  const long long excl = before + incl - mine;
+  const long long chunk = (total + gridDim.x - 1) / gridDim.x;
+  const long long lo = min(blockIdx.x * chunk, total), hi = min(lo + chunk, total);
+  if (tid == 0) {
+    sm.range_lo = lo;
+    sm.range_hi = hi;
+  }
+  if (lo < hi && excl <= lo && lo < excl + mine) {
+    long long base = excl;
+    for (int r = r0; r < r1; ++r) {
+      bool bad;
+      const long long w = units(p, load_req(p, r, &bad));
+      if (lo < base + w) {
+        sm.start_req = r;
+        sm.start_base = base;
+        break;
+      }
+      base += w;
+    }
+  }
+  __syncthreads();
+}
+
+// The range's runs in order -- heads h0 .. h1 - 1 of key tile `tile` of request
+// `req` -- which every role walks for itself.
+struct Walk {
+  int req, tile, h0, h1;
+  Req a;
+  long long base, pos;
+
+  __device__ __forceinline__ void start(const Smem& sm) {
+    req = sm.start_req;
+    base = sm.start_base;
+    pos = sm.range_lo;
+    a.keys = -1;  // not read yet
+  }
+  __device__ __forceinline__ bool next(const LatentExpandParams& p, const Smem& sm) {
+    if (pos >= sm.range_hi) return false;
+    bool bad;
+    if (a.keys < 0) a = load_req(p, req, &bad);
+    while (pos >= base + units(p, a)) {  // (pos < range_hi: there is a later request)
+      base += units(p, a);
+      a = load_req(p, ++req, &bad);
+    }
+    const long long local = pos - base;
+    tile = (int)(local / p.num_heads);
+    h0 = (int)(local - (long long)tile * p.num_heads);
+    const long long left = sm.range_hi - pos;
+    h1 = (int)min((long long)p.num_heads, h0 + left);
+    pos += h1 - h0;
+    return true;
+  }
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+               "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_expand_kernel(const __grid_constant__ CUtensorMap kmap,
+                         const __grid_constant__ CUtensorMap wmap, const LatentExpandParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw + (((raw + 1023u) & ~1023u) - raw));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  WaitCtl* ctl = &sm.wait;
+  if (tid == 0) {
+    for (int i = 0; i < kChunks; ++i) {
+      mbar_init(&sm.a_full[i], 1);
+      mbar_init(&sm.a_empty[i], 1);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sm.b_full[i], 1);
+      mbar_init(&sm.b_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.d_full[i], 1);
+      mbar_init(&sm.d_empty[i], kEpiWarps);
+    }
+    mbar_init(&sm.drained, 1);
+    sm.wait.abort = 0;
+    sm.wait.limit_ns = p.wait_limit_ns;
+    fence_barrier_init();
+  }
+  if (warp == kWarpLoad && lane == 0) {
+    prefetch_tensormap(&kmap);
+    prefetch_tensormap(&wmap);
+  }
+  if (!p.early_plan) grid_dependency_wait();
+  plan_range(p, sm);
+  if (p.early_plan) grid_dependency_wait();
+  allow_dependent_launch();
+  if (sm.range_lo >= sm.range_hi) return;
+  if (warp == kWarpMma) {
+    tmem_alloc(&sm.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  Walk w;
+  w.start(sm);
+
+  if (warp == kWarpLoad) {
+    // =========================== copies ===================================
+    const int oob_row = p.num_blocks * kBlockSize;
+    int n_tile = 0, n_b = 0, chunks = 0;  // runs and weight pieces so far; chunks of run n_tile
+    bool ok = true;
+    while (ok && w.next(p, sm)) {
+      // Lane b < 8 copies block b of each chunk; blocks past the end are read at
+      // a row outside the pool, which fills zeros.
+      const int blk = w.tile * (kKeys / kBlockSize) + lane;
+      int row = oob_row;
+      if (lane < 8 && blk * kBlockSize < w.a.keys) {
+        const int id = __ldg(p.block_tables + (long long)w.req * p.max_blocks + blk);
+        if ((unsigned)id < (unsigned)p.num_blocks) row = id * kBlockSize;
+        else record_error(p.err, kErrBounds);
+      }
+      chunks = 0;
+      for (int h = w.h0; h < w.h1 && ok; ++h) {
+        for (int i = 0; i < 2 * kChunks; ++i) {
+          const int c = i % kChunks;
+          if (h == w.h0 && i < kChunks) {
+            if (n_tile > 0) ok = mbar_wait(&sm.a_empty[c], (n_tile - 1) & 1, p.err, ctl);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&sm.a_full[c], kChunkBytes);
+            __syncwarp();
+            if (lane < 8) tma_load_2d(sm.a[c] + lane * 2048, &kmap, c * 64, row, &sm.a_full[c]);
+            ++chunks;
+          }
+          const int st = n_b % kStages;
+          if (n_b >= kStages) ok = mbar_wait(&sm.b_empty[st], ((n_b / kStages) - 1) & 1, p.err, ctl);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sm.b_full[st], kChunkBytes);
+            tma_load_3d(sm.b[st], &wmap, c * 64, h * kOut + (i / kChunks) * kHalf, 0, &sm.b_full[st]);
+          }
+          ++n_b;
+          __syncwarp();
+        }
+      }
+      if (ok) ++n_tile, chunks = 0;
+    }
+    if (!ok) {
+      // Aborted: the copies in flight must land before the CTA ends.
+      for (int i = max(0, n_b - kStages); i < n_b; ++i)
+        mbar_wait_drain(&sm.b_full[i % kStages], (i / kStages) & 1, p.err, ctl);
+      for (int c = 0; c < kChunks; ++c) {
+        const int n = n_tile + (c < chunks ? 1 : 0);
+        if (n > 0) mbar_wait_drain(&sm.a_full[c], (n - 1) & 1, p.err, ctl);
+      }
+    }
+  } else if (warp == kWarpMma) {
+    // ============================ MMAs ====================================
+    constexpr uint32_t kIdesc = idesc_bf16_f32(kKeys, kHalf, 0, 0);
+    int n_tile = 0, n_b = 0, n_d = 0;
+    bool ok = true;
+    while (ok && w.next(p, sm)) {
+      for (int h = w.h0; h < w.h1 && ok; ++h, ++n_d) {
+        const int d = n_d & 1;
+        if (n_d >= 2) ok = mbar_wait(&sm.d_empty[d], ((n_d >> 1) - 1) & 1, p.err, ctl);
+        for (int i = 0; i < 2 * kChunks && ok; ++i) {
+          const int c = i % kChunks, half = i / kChunks, st = n_b % kStages;
+          if (h == w.h0 && half == 0) ok = mbar_wait(&sm.a_full[c], n_tile & 1, p.err, ctl);
+          ok = ok && mbar_wait(&sm.b_full[st], (n_b / kStages) & 1, p.err, ctl);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            #pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t da = smem_desc_sw128(smem_u32(sm.a[c]) + kk * 32, 16, 1024);
+              const uint64_t db = smem_desc_sw128(smem_u32(sm.b[st]) + kk * 32, 16, 1024);
+              tc_mma_f16_ss(tmem + d * kOut + half * kHalf, da, db, kIdesc, c > 0 || kk > 0);
+            }
+            tc_commit(&sm.b_empty[st]);
+            if (h == w.h1 - 1 && half == 1) tc_commit(&sm.a_empty[c]);
+            if (i == 2 * kChunks - 1) tc_commit(&sm.d_full[d]);
+          }
+          __syncwarp();
+          ++n_b;
+        }
+      }
+      ++n_tile;
+    }
+    if (!ok) {
+      // Aborted: the issued MMAs must end before TMEM is freed.
+      if (elect_one()) tc_commit(&sm.drained);
+      __syncwarp();
+      mbar_wait_drain(&sm.drained, 0, p.err, ctl);
+    }
+  } else {
+    // ====================== rounding and stores (warps 0-3) ==================
+    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    uint8_t* mine = sm.row[tid];
+    int n_d = 0;
+    bool ok = true;
+    while (ok && w.next(p, sm)) {
+      const int key = w.tile * kKeys + tid;
+      const bool live = key < w.a.keys;
+      const long long row = w.a.row0 + key;
+      if (w.h0 == 0) {
+        // The rotated keys of these 128 keys, eight lanes a row.
+        for (int i = tid; i < kKeys * 8; i += 32 * kEpiWarps) {
+          const int k = w.tile * kKeys + (i >> 3);
+          if (k >= w.a.keys) break;
+          const int id = __ldg(p.block_tables + (long long)w.req * p.max_blocks + k / kBlockSize);
+          if ((unsigned)id >= (unsigned)p.num_blocks) continue;
+          const uint4* src = reinterpret_cast<const uint4*>(
+              p.pool + ((long long)id * kBlockSize + k % kBlockSize) * kLatRow + kLatent);
+          reinterpret_cast<uint4*>(p.k_rope + ((long long)w.a.row0 + k) * kRopeDim)[i & 7] = src[i & 7];
+        }
+      }
+      for (int h = w.h0; h < w.h1 && ok; ++h, ++n_d) {
+        const int d = n_d & 1;
+        ok = mbar_wait(&sm.d_full[d], (n_d >> 1) & 1, p.err, ctl);
+        if (__any_sync(0xffffffffu, !ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        __nv_bfloat16* dst = p.kv + (row * p.num_heads + h) * kOut;
+        #pragma unroll 1
+        for (int q = 0; q < kOut / kRowCols; ++q) {
+          float v[kRowCols / 2], u[kRowCols / 2];
+          tmem_ld32(tmem + lane_off + d * kOut + q * kRowCols, v);
+          tmem_ld32(tmem + lane_off + d * kOut + q * kRowCols + 32, u);
+          tc_wait_ld();
+          // The row's last copy has left shared memory.
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          #pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            *reinterpret_cast<uint4*>(mine + 16 * i) =
+                make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                           pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+            *reinterpret_cast<uint4*>(mine + 64 + 16 * i) =
+                make_uint4(pack_bf16(u[8 * i], u[8 * i + 1]), pack_bf16(u[8 * i + 2], u[8 * i + 3]),
+                           pack_bf16(u[8 * i + 4], u[8 * i + 5]), pack_bf16(u[8 * i + 6], u[8 * i + 7]));
+          }
+          fence_proxy_async_smem();
+          if (live) bulk_store(dst + q * kRowCols, mine, kRowCols * 2);
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.d_empty[d]);
+      }
+    }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace
+
+cudaError_t launch_latent_expand(const LatentExpandLaunch& L, cudaStream_t stream) {
+  const size_t smem = sizeof(Smem) + 1024;
+  static unsigned long long configured = 0;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & bit)) {
+    e = cudaFuncSetAttribute(latent_expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    __atomic_fetch_or(&configured, bit, __ATOMIC_RELEASE);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(L.grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = L.p.pdl ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, latent_expand_kernel, L.kmap, L.wmap, L.p);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+}  // namespace pkv

@@ -1,0 +1,765 @@
+// pkv_latent_prefill.cu -- causal attention of prefill chunks over expanded keys
+// and values of a latent cache, on tcgen05 tensor cores.
+//
+//   s_j = scale (<q[0:128], k_j,h> + <q[128:192], r_j>),  out = sum_j softmax(s)_j v_j,h
+//
+// with keys and values of each head side by side in kv [rows, H, 256] and the
+// rotated keys r, shared by the heads, in a tensor of their own: a key tile takes
+// its three 64-dim chunks from both, and no head's copy of r is ever made.
+// Bound: tensor core (640 flops a (row, key, head)).
+//
+// Tiling.  A work item is (request, head, 128 query tokens); a key tile is 128
+// keys.  S = Q K^T (12 MMAs of K = 16) has two TMEM buffers, P (bf16) replaces its
+// S there and O += P V (8 MMAs, A from TMEM) accumulates in 128 columns.  Four
+// threads a row run the softmax, 32 keys each; the row maximum moves, and O is
+// rescaled, only when a score exceeds it by 2^8, on a vote of the four warps that
+// hold the same rows.  Keys and values have rings of their own, two stages each.
+//
+// Order.  Items come from a queue, longest requests first, a head's query tiles
+// one after the other (the CTAs that run them at one time read the same keys:
+// L2), later tiles first, as they see more keys.  With too few items for the
+// GPU each is cut over its keys into pieces, numbered like items, whose
+// unnormalised states a second kernel joins.
+//
+// A value that only some rows of an item see must not reach the others, whatever
+// it holds (0 * NaN): rows of V with a NaN or infinity among the item's own
+// tokens are taken out and added to the rows that see them at the end.
+#include <climits>
+
+#include "pkv_latent.h"
+#include "pkv_tc.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kParts = 4;                // softmax threads a row
+constexpr int kPartKeys = 128 / kParts;  // keys, and output dims, of each
+constexpr int kSoftWarps = 4 * kParts;
+constexpr int kSoftThreads = 32 * kSoftWarps;
+constexpr int kWarpK = kSoftWarps;       // items, Q, keys
+constexpr int kWarpMma = kSoftWarps + 1;
+constexpr int kWarpV = kSoftWarps + 2;   // values
+constexpr int kThreads = 32 * (kSoftWarps + 3);
+constexpr int kBarSoft = 1;              // all softmax warps
+constexpr int kBarQuad = 2;              // + quad: the four warps with the same rows
+
+constexpr int kRows = 128;
+constexpr int kTile = 128;
+constexpr int kChunkBytes = 128 * 128;
+constexpr int kQDim = kNope + kRopeDim;
+constexpr int kKChunks = kQDim / 64;
+constexpr int kVChunks = kValDim / 64;
+constexpr int kStages = 2;
+constexpr int kItems = 4;
+constexpr uint32_t kTmemCols = 512;      // S: columns 0 .. 255, O: 256 .. 383
+constexpr float kRescaleLog2 = 8.0f;
+constexpr int kMinPieceTiles = 4;
+
+// A piece of an item: key tiles t0 .. t1 - 1 of its keys.
+struct Item {
+  int row0, nt;  // first query row, query tokens
+  int pos0;      // position of the first
+  int head;
+  int k0;        // first row of the request's keys
+  int t0, t1;
+  int slot;      // piece number, if the item is split; else -1
+  int end;
+};
+
+struct __align__(1024) Smem {
+  uint8_t q[kKChunks][kChunkBytes];
+  uint8_t k[kStages][kKChunks][kChunkBytes];
+  uint8_t v[kStages][kVChunks][kChunkBytes];
+  uint64_t q_full, q_empty;
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t s_full[2], p_full[2], p_free[2];
+  uint64_t o_full, o_empty;
+  uint64_t item_full[kItems], vitem_full[kItems], vitem_empty[kItems];
+  uint64_t drained;
+  Item items[kItems], vitems[kItems];
+  float xrow[kParts][kRows];
+  unsigned long long bad[2][2];  // own tokens whose values were taken out, by item parity
+  uint32_t tmem_base;
+  int active;  // CTAs that take pieces
+  int split;   // key tiles of a piece (INT_MAX: items are whole)
+  WaitCtl wait;
+};
+static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "latent prefill shared memory");
+
+__device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+struct Req {
+  int q0, qr, L, k0;
+  int nq;  // query tiles of a head (0: nothing to do)
+};
+
+__device__ __forceinline__ Req load_req(const LatentPrefillParams& p, int r, bool* bad) {
+  Req a;
+  a.q0 = __ldg(p.qsl + r);
+  const int q1 = __ldg(p.qsl + r + 1);
+  a.L = __ldg(p.seq_lens + r);
+  a.k0 = __ldg(p.kv_start + r);
+  const int k1 = __ldg(p.kv_start + r + 1);
+  a.qr = q1 - a.q0;
+  *bad = !(a.q0 >= 0 && a.qr >= 0 && q1 <= p.num_q_tokens && a.qr <= a.L && a.k0 >= 0 &&
+           k1 <= p.num_rows && k1 - a.k0 == a.L);
+  a.nq = *bad ? 0 : cdiv(a.qr, kRows);
+  return a;
+}
+
+// Key tiles of query tile i.
+__device__ __forceinline__ int item_tiles(const Req& a, int i) {
+  return cdiv(a.L - a.qr + min((i + 1) * kRows, a.qr), kTile);
+}
+
+// Pieces of a request's head.
+__device__ __forceinline__ int head_pieces(const Req& a, int split) {
+  if (split == INT_MAX) return a.nq;
+  int n = 0;
+  for (int i = 0; i < a.nq; ++i) n += cdiv(item_tiles(a, i), split);
+  return n;
+}
+
+__device__ __forceinline__ long long warp_sum(long long v) {
+  #pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Key tiles of a piece, from the step's items: whole while they are enough for
+// the grid (or there is no room for more), else the key tiles in equal parts.
+// One warp; also counts the pieces.
+__device__ __forceinline__ int plan_split(const LatentPrefillParams& p, int grid, bool report,
+                                          long long* pieces) {
+  const int lane = threadIdx.x & 31;
+  long long items = 0, tiles = 0;
+  for (int r = lane; r < p.num_reqs; r += 32) {
+    bool bad;
+    const Req a = load_req(p, r, &bad);
+    if (bad && report) record_error(p.err, kErrBounds);  // the request is skipped
+    items += (long long)a.nq * p.num_heads;
+    if (p.max_pieces > 0)
+      for (int i = 0; i < a.nq; ++i) tiles += (long long)item_tiles(a, i) * p.num_heads;
+  }
+  items = warp_sum(items);
+  *pieces = items;
+  if (p.max_pieces == 0 || 3 * items >= 2 * grid) return INT_MAX;
+  tiles = warp_sum(tiles);
+  // ceil(tiles / split) summed over the items is at most grid + items < 2 grid.
+  const int split = max(kMinPieceTiles, (int)((tiles + grid - 1) / grid));
+  long long n = 0;
+  for (int r = lane; r < p.num_reqs; r += 32) {
+    bool bad;
+    n += (long long)head_pieces(load_req(p, r, &bad), split) * p.num_heads;
+  }
+  *pieces = warp_sum(n);
+  return split;
+}
+
+// Finds pieces by number, forward.  Pieces are numbered by batches of 32
+// requests, within a batch the longest request first, then head by head, then
+// from the last query tile to the first, then along the keys.  One warp.
+struct Finder {
+  int batch;       // first request of the batch
+  long long base;  // pieces before it
+  Req a;           // this lane's request
+  int per_head;
+  long long cnt, excl, total;
+
+  __device__ __forceinline__ void load(const LatentPrefillParams& p, int split) {
+    const int lane = threadIdx.x & 31, r = batch + lane;
+    bool bad;
+    a = Req{0, 0, 0, 0, 0};
+    if (r < p.num_reqs) a = load_req(p, r, &bad);
+    per_head = head_pieces(a, split);
+    cnt = (long long)per_head * p.num_heads;
+    total = warp_sum(cnt);
+    const int key = cnt > 0 ? a.L : -1;
+    excl = 0;
+    #pragma unroll 4
+    for (int s = 0; s < 32; ++s) {
+      const int ks = __shfl_sync(0xffffffffu, key, s);
+      const long long cs = __shfl_sync(0xffffffffu, cnt, s);
+      if (ks > key || (ks == key && s < lane)) excl += cs;
+    }
+  }
+  __device__ __forceinline__ void start(const LatentPrefillParams& p, int split) {
+    batch = 0;
+    base = 0;
+    load(p, split);
+  }
+  // Numbers must not decrease from call to call.  False: there is no such piece.
+  __device__ __forceinline__ bool find(const LatentPrefillParams& p, int split, long long piece,
+                                       Item* it, int* of) {
+    while (piece >= base + total) {
+      base += total;
+      batch += 32;
+      if (batch >= p.num_reqs) return false;
+      load(p, split);
+    }
+    const long long rel = piece - base;
+    const unsigned own = __ballot_sync(0xffffffffu, cnt > 0 && excl <= rel && rel < excl + cnt);
+    const int src = __ffs(own) - 1;
+    const long long local = rel - __shfl_sync(0xffffffffu, excl, src);
+    Req b;
+    b.q0 = __shfl_sync(0xffffffffu, a.q0, src);
+    b.qr = __shfl_sync(0xffffffffu, a.qr, src);
+    b.L = __shfl_sync(0xffffffffu, a.L, src);
+    b.k0 = __shfl_sync(0xffffffffu, a.k0, src);
+    b.nq = __shfl_sync(0xffffffffu, a.nq, src);
+    const int each = __shfl_sync(0xffffffffu, per_head, src);
+    it->head = (int)(local / each);
+    int x = (int)(local - (long long)it->head * each), i = b.nq - 1, n = 1;
+    if (split == INT_MAX) {
+      i -= x;
+      x = 0;
+    } else {
+      for (; (n = cdiv(item_tiles(b, i), split)) <= x; --i) x -= n;
+    }
+    const int tiles = item_tiles(b, i);
+    it->row0 = b.q0 + i * kRows;
+    it->nt = min(kRows, b.qr - i * kRows);
+    it->pos0 = b.L - b.qr + i * kRows;
+    it->k0 = b.k0;
+    // n pieces of equal length, but for the rounding
+    it->t0 = (int)((long long)tiles * x / n);
+    it->t1 = (int)((long long)tiles * (x + 1) / n);
+    it->slot = n > 1 ? (int)piece : -1;
+    it->end = 0;
+    *of = n > 1 && x == 0 ? n : 0;
+    return true;
+  }
+};
+
+// O (32 columns at TMEM address tO) times alpha.
+static __device__ __noinline__ void rescale_o32(uint32_t tO, float alpha) {
+  float o[32];
+  tmem_ld32(tO, o);
+  tc_wait_ld();
+  #pragma unroll
+  for (int i = 0; i < 32; ++i) o[i] *= alpha;
+  tmem_st32(tO, o);
+  tc_wait_st();
+}
+
+__device__ __forceinline__ bool non_finite(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+// Values of the tile's keys from pos0 + 1 on: those that no row of the item sees
+// (from its last token's position on) become zeros; those of its own tokens that
+// are not finite too, noted in bad.  Half a warp a row.
+static __device__ __noinline__ void clean_values(uint8_t (*v)[kChunkBytes], int key0, int pos0, int nt,
+                                                 unsigned long long* bad, int warp, int lane) {
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const int first = max(pos0 + 1 - key0, 0);
+  const int piece = lane & 15;
+  for (int r2 = first + 2 * warp; r2 < kTile; r2 += 2 * kSoftWarps) {
+    const int row = r2 + (lane >> 4);
+    const bool in = row < kTile;
+    const int b = key0 + row - pos0 - 1;  // the item's token b + 1
+    uint4* at = reinterpret_cast<uint4*>(v[piece >> 3] + (in ? row : 0) * 128 +
+                                         (((piece & 7) ^ (row & 7)) << 4));
+    bool hit = false;
+    if (in && b < nt - 1) {
+      const uint4 x = *at;
+      hit = non_finite(x.x) || non_finite(x.y) || non_finite(x.z) || non_finite(x.w);
+    }
+    const unsigned votes = __ballot_sync(0xffffffffu, hit);
+    const bool out = in && (b >= nt - 1 || ((votes >> (lane & 16)) & 0xffffu) != 0);
+    if (out && b < nt - 1 && piece == 0) atomicOr(bad + (b >> 6), 1ull << (b & 63));
+    if (out) *at = zero;
+  }
+  fence_proxy_async_smem();
+}
+
+// What the values taken out add to a row that sees the first `seen` of them: its
+// weight is positive, so a NaN stays one and an infinity keeps its sign.
+static __device__ __noinline__ void add_bad(const LatentPrefillParams& p, const Item& it,
+                                            unsigned long long lo, unsigned long long hi, int seen,
+                                            int d0, float (&o)[32]) {
+  for (int b = 0; b < seen; ++b) {
+    if (!(((b < 64 ? lo : hi) >> (b & 63)) & 1)) continue;
+    const __nv_bfloat16* v =
+        p.kv + ((long long)(it.k0 + it.pos0 + 1 + b) * p.num_heads + it.head) * (kNope + kValDim) + kNope + d0;
+    #pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float x = __bfloat162float(v[i]);
+      if (!(x - x == 0.f)) o[i] += x;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
+                          const __grid_constant__ CUtensorMap kvmap,
+                          const __grid_constant__ CUtensorMap rmap, const LatentPrefillParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw + (((raw + 1023u) & ~1023u) - raw));
+  WaitCtl* ctl = &sm.wait;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_empty, 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sm.k_full[s], 1);
+      mbar_init(&sm.k_empty[s], 1);
+      mbar_init(&sm.v_full[s], 1);
+      mbar_init(&sm.v_empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sm.s_full[b], 1);
+      mbar_init(&sm.p_full[b], kSoftWarps);
+      mbar_init(&sm.p_free[b], 1);
+      sm.bad[b][0] = sm.bad[b][1] = 0;
+    }
+    mbar_init(&sm.o_full, 1);
+    mbar_init(&sm.o_empty, kSoftWarps);
+    for (int b = 0; b < kItems; ++b) {
+      mbar_init(&sm.item_full[b], 1);
+      mbar_init(&sm.vitem_full[b], 1);
+      mbar_init(&sm.vitem_empty[b], 1);
+    }
+    mbar_init(&sm.drained, 1);
+    sm.wait.abort = 0;
+    sm.wait.limit_ns = p.wait_limit_ns;
+    fence_barrier_init();
+  }
+  if (warp == kWarpV && lane == 0) {
+    prefetch_tensormap(&qmap);
+    prefetch_tensormap(&kvmap);
+    prefetch_tensormap(&rmap);
+  }
+  if (!p.early_plan) grid_dependency_wait();
+  if (warp == kWarpK) {
+    long long pieces;
+    const int split = plan_split(p, gridDim.x, blockIdx.x == 0, &pieces);
+    if (lane == 0) {
+      sm.split = split;
+      sm.active = (int)min(pieces, (long long)gridDim.x);
+    }
+  }
+  __syncthreads();
+  if (p.early_plan) grid_dependency_wait();
+  allow_dependent_launch();
+  const int active = sm.active, split = sm.split;
+  if ((int)blockIdx.x >= active) return;
+  if (warp == kWarpMma) {
+    tmem_alloc(&sm.tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+
+  if (warp == kWarpK || warp == kWarpV) {
+    // =========================== copies ===================================
+    const bool vside = warp == kWarpV;
+    uint64_t* const full = vside ? sm.v_full : sm.k_full;
+    uint64_t* const empty = vside ? sm.v_empty : sm.k_empty;
+    int n_item = 0, t = 0;
+    bool ok = true;
+    auto stream = [&](const Item& it) {
+      for (int j = it.t0; j < it.t1; ++j, ++t) {
+        const int st = t % kStages;
+        if (t >= kStages && !mbar_wait(&empty[st], ((t / kStages) - 1) & 1, p.err, ctl)) return false;
+        if (lane == 0) {
+          const int y = it.k0 + j * kTile;
+          if (vside) {
+            mbar_arrive_expect_tx(&full[st], kVChunks * kChunkBytes);
+            for (int c = 0; c < kVChunks; ++c)
+              tma_load_3d(sm.v[st][c], &kvmap, kNope + c * 64, it.head, y, &full[st]);
+          } else {
+            mbar_arrive_expect_tx(&full[st], kKChunks * kChunkBytes);
+            tma_load_3d(sm.k[st][0], &kvmap, 0, it.head, y, &full[st]);
+            tma_load_3d(sm.k[st][1], &kvmap, 64, it.head, y, &full[st]);
+            tma_load_3d(sm.k[st][2], &rmap, 0, y, 0, &full[st]);
+          }
+        }
+        __syncwarp();
+        if (j == it.t0 && !vside) {
+          // The item's queries, once the MMAs of the item before are done with
+          // theirs (its first keys are on their way).
+          if (n_item > 0 && !mbar_wait(&sm.q_empty, (n_item - 1) & 1, p.err, ctl)) return false;
+          if (lane == 0) {
+            sm.items[n_item % kItems] = it;
+            mbar_arrive(&sm.item_full[n_item % kItems]);
+            mbar_arrive_expect_tx(&sm.q_full, kKChunks * kChunkBytes);
+            for (int c = 0; c < kKChunks; ++c)
+              tma_load_3d(sm.q[c], &qmap, c * 64, it.head, it.row0, &sm.q_full);
+          }
+          ++n_item;
+          __syncwarp();
+        }
+      }
+      return true;
+    };
+    if (vside) {
+      for (;; ++n_item) {
+        const int b = n_item % kItems;
+        ok = mbar_wait(&sm.vitem_full[b], (n_item / kItems) & 1, p.err, ctl);
+        if (!ok) break;
+        const Item it = sm.vitems[b];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.vitem_empty[b]);
+        if (it.end) break;
+        ok = stream(it);
+        if (!ok) break;
+      }
+    } else {
+      int handed = 0;
+      auto hand_over = [&](const Item& it) {
+        const int b = handed % kItems;
+        if (handed >= kItems && !mbar_wait(&sm.vitem_empty[b], ((handed / kItems) - 1) & 1, p.err, ctl))
+          return false;
+        if (lane == 0) {
+          sm.vitems[b] = it;
+          mbar_arrive(&sm.vitem_full[b]);
+        }
+        ++handed;
+        __syncwarp();
+        return true;
+      };
+      Finder f;
+      f.start(p, split);
+      while (ok) {
+        unsigned long long v = 0;
+        if (lane == 0) v = atomicAdd(p.sched, 1ull);
+        v = __shfl_sync(0xffffffffu, v, 0);
+        Item it;
+        int of;
+        if (!f.find(p, split, (long long)v, &it, &of)) break;
+        ok = hand_over(it) && stream(it);
+      }
+      Item fin = {};
+      fin.end = 1;
+      if (ok) ok = hand_over(fin);
+      if (ok && n_item > 0) ok = mbar_wait(&sm.q_empty, (n_item - 1) & 1, p.err, ctl);
+      if (ok && lane == 0) {
+        sm.items[n_item % kItems].end = 1;
+        mbar_arrive(&sm.item_full[n_item % kItems]);
+        mbar_arrive(&sm.q_full);
+      }
+      __syncwarp();
+      if (!ok && n_item > 0) mbar_wait_drain(&sm.q_full, (n_item - 1) & 1, p.err, ctl);
+    }
+    // Aborted: the copies in flight must land before the CTA ends.
+    if (!ok)
+      for (int i = max(0, t - kStages); i < t; ++i)
+        mbar_wait_drain(&full[i % kStages], (i / kStages) & 1, p.err, ctl);
+  } else if (warp == kWarpMma) {
+    // ============================ MMAs ====================================
+    // Order: S(t), then PV(t - 1), across items.
+    constexpr uint32_t kIdescS = idesc_bf16_f32(kRows, kTile, 0, 0);
+    constexpr uint32_t kIdescO = idesc_bf16_f32(kRows, kValDim, 0, 1);
+    const uint32_t tO = tmem + 2 * kTile;
+    bool ok = true;
+    int t = 0;
+    auto pv = [&](int tt, int item, bool first, bool last) {
+      const int b = tt & 1, st = tt % kStages;
+      ok = ok && mbar_wait(&sm.p_full[b], (tt >> 1) & 1, p.err, ctl);
+      ok = ok && mbar_wait(&sm.v_full[st], (tt / kStages) & 1, p.err, ctl);
+      if (first && item > 0) ok = ok && mbar_wait(&sm.o_empty, (item - 1) & 1, p.err, ctl);
+      if (!ok) return;
+      tc_fence_after();
+      if (elect_one()) {
+        #pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk) {
+          // P: two keys a column, in the first 64 columns of its S buffer.  V is
+          // MN-major: atoms of 64 dims x 8 keys, the chunks kChunkBytes apart.
+          const uint64_t db = smem_desc_sw128(smem_u32(sm.v[st][0]) + kk * 2048, kChunkBytes, 1024);
+          tc_mma_f16_ts(tO, tmem + b * kTile + kk * 8, db, kIdescO, !first || kk > 0);
+        }
+        tc_commit(&sm.v_empty[st]);
+        tc_commit(&sm.p_free[b]);
+        if (last) tc_commit(&sm.o_full);
+      }
+      __syncwarp();
+    };
+    bool pend_first = false;
+    for (int n_item = 0;; ++n_item) {
+      ok = ok && mbar_wait(&sm.q_full, n_item & 1, p.err, ctl);
+      if (!ok) break;
+      const Item it = sm.items[n_item % kItems];
+      if (it.end) {
+        if (t > 0) pv(t - 1, n_item - 1, pend_first, true);
+        break;
+      }
+      for (int j = it.t0; j < it.t1 && ok; ++j, ++t) {
+        const int b = t & 1, st = t % kStages;
+        ok = ok && mbar_wait(&sm.k_full[st], (t / kStages) & 1, p.err, ctl);
+        // S buffer b holds P(t - 2) until its product is done.
+        if (t >= 2) ok = ok && mbar_wait(&sm.p_free[b], ((t >> 1) - 1) & 1, p.err, ctl);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          #pragma unroll
+          for (int kk = 0; kk < kQDim / 16; ++kk) {
+            const uint64_t da = smem_desc_sw128(smem_u32(sm.q[kk >> 2]) + (kk & 3) * 32, 16, 1024);
+            const uint64_t db = smem_desc_sw128(smem_u32(sm.k[st][kk >> 2]) + (kk & 3) * 32, 16, 1024);
+            tc_mma_f16_ss(tmem + b * kTile, da, db, kIdescS, kk > 0);
+          }
+          tc_commit(&sm.k_empty[st]);
+          tc_commit(&sm.s_full[b]);
+          if (j == it.t1 - 1) tc_commit(&sm.q_empty);
+        }
+        __syncwarp();
+        if (t > 0) pv(t - 1, j == it.t0 ? n_item - 1 : n_item, pend_first, j == it.t0);
+        pend_first = j == it.t0;
+      }
+    }
+    if (!ok) {
+      // Aborted: the issued MMAs must end before TMEM is freed.
+      if (elect_one()) tc_commit(&sm.drained);
+      __syncwarp();
+      mbar_wait_drain(&sm.drained, 0, p.err, ctl);
+    }
+  } else {
+    // ==================== softmax and epilogue (warps 0-15) ==================
+    // Warps 4 c .. 4 c + 3 take keys 32 c .. 32 c + 31 of a tile and output dims
+    // 32 c ..; warp w reaches TMEM lanes 32 (w % 4) ..
+    const int quad = warp & 3, part = warp >> 2;
+    const int row = quad * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const uint32_t tO = tmem + lane_off + 2 * kTile + part * kPartKeys;
+    int t = 0;
+    bool ok = true;
+    for (int n_item = 0;; ++n_item) {
+      const bool have = mbar_wait(&sm.item_full[n_item % kItems], (n_item / kItems) & 1, p.err, ctl);
+      const Item it = sm.items[n_item % kItems];
+      // Agree before any barrier: a wait that gave up stops everyone.
+      if (barrier_or(kBarSoft, kSoftThreads, !have || it.end)) break;
+      unsigned long long* bad = sm.bad[n_item & 1];
+      const bool valid = row < it.nt;
+      const int prow = valid ? it.pos0 + row : -1;  // the last key that the row sees
+      float m = -INFINITY, l = 0.f;
+      for (int j = it.t0; j < it.t1; ++j, ++t) {
+        const int sb = t & 1;
+        const uint32_t tS = tmem + lane_off + sb * kTile;
+        ok = ok && mbar_wait(&sm.s_full[sb], (t >> 1) & 1, p.err, ctl);
+        tc_fence_after();
+        const int kbase = j * kTile + part * kPartKeys;
+        float v[kPartKeys];
+        tmem_ld32(tS + part * kPartKeys, v);
+        tc_wait_ld();
+        if (kbase + kPartKeys - 1 > prow) {
+          #pragma unroll
+          for (int i = 0; i < kPartKeys; ++i)
+            if (kbase + i > prow) v[i] = -INFINITY;
+        }
+        // The largest of the scaled scores (a negative scale turns the order).
+        float mxp[4];
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) mxp[i] = -INFINITY;
+        if (p.scale_log2 > 0.f) {
+          #pragma unroll
+          for (int i = 0; i < kPartKeys / 2; ++i) mxp[i & 3] = fmax3(mxp[i & 3], v[2 * i], v[2 * i + 1]);
+          #pragma unroll
+          for (int i = 0; i < 4; ++i) mxp[i] *= p.scale_log2;
+        } else {
+          #pragma unroll
+          for (int i = 0; i < kPartKeys; ++i)
+            if (kbase + i <= prow) mxp[i & 3] = fmaxf(mxp[i & 3], v[i] * p.scale_log2);
+        }
+        const float mxh = fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3]));
+        // The vote also orders the four warps' reads of S before any P write.
+        tc_fence_before();
+        const bool exchange = barrier_or(kBarQuad + quad, 128, j == it.t0 || mxh > m + kRescaleLog2);
+        tc_fence_after();
+        if (exchange) {
+          sm.xrow[part][row] = mxh;
+          named_barrier(kBarQuad + quad, 128);
+          const float mx = fmaxf(fmaxf(sm.xrow[0][row], sm.xrow[1][row]),
+                                 fmaxf(sm.xrow[2][row], sm.xrow[3][row]));
+          named_barrier(kBarQuad + quad, 128);
+          const bool grow = mx > m + kRescaleLog2 || (m == -INFINITY && mx > m);
+          const float m_new = grow ? mx : m;
+          if (j > it.t0 && __any_sync(0xffffffffu, grow)) {
+            // O and l move to the new reference; O must hold the tile before.
+            ok = ok && mbar_wait(&sm.p_free[(t - 1) & 1], ((t - 1) >> 1) & 1, p.err, ctl);
+            tc_fence_after();
+            const float alpha = grow && m != -INFINITY ? fast_exp2(m - m_new) : 1.f;
+            rescale_o32(tO, alpha);
+            l *= alpha;
+          }
+          m = m_new;
+        }
+        // P = exp2(s scale - m), two keys a column over the row's S; the sum adds
+        // the rounded values that the product uses.  (A row that saw no key yet
+        // has m = -inf.)
+        const float ref = m == -INFINITY ? 0.f : m;
+        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+        const float2 nm2 = make_float2(-ref, -ref);
+        float sum_lo[2] = {0.f, 0.f}, sum_hi[2] = {0.f, 0.f};
+        uint32_t w[kPartKeys / 2];
+        if (p.scale_log2 < 0.f && kbase + kPartKeys - 1 > prow) {
+          #pragma unroll
+          for (int i = 0; i < kPartKeys; ++i)
+            if (kbase + i > prow) v[i] = INFINITY;  // times a negative scale
+        }
+        #pragma unroll
+        for (int e = 0; e < kPartKeys / 2; ++e) {
+          const float2 x = ffma2(make_float2(v[2 * e], v[2 * e + 1]), sc2, nm2);
+          w[e] = pack_bf16(fast_exp2(x.x), fast_exp2(x.y));
+          add_bf16x2(sum_lo[e & 1], sum_hi[e & 1], w[e]);
+        }
+        tmem_st16(tS + part * (kPartKeys / 2), w);
+        tc_wait_st();
+        l += (sum_lo[0] + sum_hi[0]) + (sum_lo[1] + sum_hi[1]);
+        if ((j + 1) * kTile > it.pos0 + 1) {
+          ok = ok && mbar_wait(&sm.v_full[t % kStages], (t / kStages) & 1, p.err, ctl);
+          clean_values(sm.v[t % kStages], j * kTile, it.pos0, it.nt, bad, warp, lane);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[sb]);
+      }
+      // ---- epilogue ---------------------------------------------------------
+      sm.xrow[part][row] = l;
+      named_barrier(kBarQuad + quad, 128);
+      const float lrow = (sm.xrow[0][row] + sm.xrow[1][row]) + (sm.xrow[2][row] + sm.xrow[3][row]);
+      if (it.nt > 1) named_barrier(kBarSoft, kSoftThreads);  // sm.bad is complete
+      const unsigned long long gone0 = bad[0], gone1 = bad[1];
+      ok = ok && mbar_wait(&sm.o_full, n_item & 1, p.err, ctl);
+      tc_fence_after();
+      {
+        float o[32];
+        tmem_ld32(tO, o);
+        tc_wait_ld();
+        if (gone0 | gone1) {
+          float x[32];  // (a copy, so that o itself stays in registers)
+          #pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = o[i];
+          add_bad(p, it, gone0, gone1, valid ? row : 0, part * kPartKeys, x);
+          #pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = x[i];
+        }
+        if (valid && ok && it.slot >= 0) {
+          if (part == 0)
+            *reinterpret_cast<float2*>(p.piece_ml + ((long long)it.slot * kRows + row) * 2) = make_float2(m, lrow);
+          float* dst = p.piece_o + ((long long)it.slot * kRows + row) * kValDim + part * kPartKeys;
+          #pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        } else if (valid && ok) {
+          const float inv = 1.f / lrow;
+          __nv_bfloat16* dst =
+              p.out + ((long long)(it.row0 + row) * p.num_heads + it.head) * kValDim + part * kPartKeys;
+          #pragma unroll
+          for (int i = 0; i < 32; i += 8)
+            *reinterpret_cast<uint4*>(dst + i) =
+                make_uint4(pack_bf16(o[i] * inv, o[i + 1] * inv), pack_bf16(o[i + 2] * inv, o[i + 3] * inv),
+                           pack_bf16(o[i + 4] * inv, o[i + 5] * inv), pack_bf16(o[i + 6] * inv, o[i + 7] * inv));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.o_empty);
+      // Every warp has read sm.bad and sm.xrow.
+      if (barrier_or(kBarSoft, kSoftThreads, !ok)) break;
+      if (tid == 0) bad[0] = bad[1] = 0;
+    }
+  }
+  // (an abort only shortens the loops: every warp gets here)
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) tmem_dealloc(tmem, kTmemCols);
+  // The last CTA to finish empties the queue for the next launch.
+  if (tid == 0) {
+    __threadfence();
+    if (atomicAdd(p.sched + 1, 1ull) == (unsigned long long)(active - 1)) {
+      p.sched[0] = 0;
+      p.sched[1] = 0;
+      __threadfence();
+    }
+  }
+}
+
+// Joins the pieces of split items.  Block (b, y): the item whose first piece is
+// number b, if any; a warp a row, four dims a lane.
+constexpr int kMergeWarps = 8;
+
+__global__ void __launch_bounds__(32 * kMergeWarps) latent_prefill_merge_kernel(const LatentPrefillParams p, int grid) {
+  if (!p.early_plan) grid_dependency_wait();
+  const int lane = threadIdx.x & 31;
+  long long pieces;
+  const int split = plan_split(p, grid, false, &pieces);
+  Item it;
+  int of = 0;
+  bool mine = false;
+  if (split != INT_MAX && blockIdx.x < pieces) {
+    Finder f;
+    f.start(p, split);
+    mine = f.find(p, split, blockIdx.x, &it, &of) && of > 0;
+  }
+  if (p.early_plan) grid_dependency_wait();
+  allow_dependent_launch();
+  const int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  if (!mine || row >= it.nt) return;
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < of; ++i) {
+    const long long at = (long long)(blockIdx.x + i) * kRows + row;
+    const float2 ml = *reinterpret_cast<const float2*>(p.piece_ml + at * 2);
+    const float4 v = reinterpret_cast<const float4*>(p.piece_o + at * kValDim)[lane];
+    const float top = fmaxf(m, ml.x);
+    const float a = m == -INFINITY ? 0.f : fast_exp2(m - top);
+    const float b = ml.x == -INFINITY && ml.y == 0.f ? 0.f : fast_exp2(ml.x - top);
+    l = l * a + ml.y * b;
+    o.x = o.x * a + v.x * b;
+    o.y = o.y * a + v.y * b;
+    o.z = o.z * a + v.z * b;
+    o.w = o.w * a + v.w * b;
+    m = top;
+  }
+  const float inv = 1.f / l;
+  uint2 w;
+  w.x = pack_bf16(o.x * inv, o.y * inv);
+  w.y = pack_bf16(o.z * inv, o.w * inv);
+  reinterpret_cast<uint2*>(p.out + ((long long)(it.row0 + row) * p.num_heads + it.head) * kValDim)[lane] = w;
+}
+
+}  // namespace
+
+cudaError_t launch_latent_prefill(const LatentPrefillLaunch& L, cudaStream_t stream) {
+  const size_t smem = sizeof(Smem) + 1024;
+  static unsigned long long configured = 0;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & bit)) {
+    e = cudaFuncSetAttribute(latent_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    __atomic_fetch_or(&configured, bit, __ATOMIC_RELEASE);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(L.grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = L.p.pdl ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, latent_prefill_kernel, L.qmap, L.kvmap, L.rmap, L.p);
+  if (e != cudaSuccess || L.p.max_pieces == 0) return e != cudaSuccess ? e : cudaGetLastError();
+  cfg.gridDim = dim3(L.p.max_pieces, kRows / kMergeWarps);
+  cfg.blockDim = dim3(32 * kMergeWarps);
+  cfg.dynamicSmemBytes = 0;
+  e = cudaLaunchKernelEx(&cfg, latent_prefill_merge_kernel, L.p, L.grid);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+}  // namespace pkv

@@ -86,3 +86,35 @@ def absorbed(q, pool, tab, lens, qsl, scale):
             o, b = _attend(q[t], c[:p], c[:p, :LAT], scale, np.ones((H, p), bool))
             out[t], bound[t] = o, b
     return out, bound
+
+
+def expand(pool, w, tab, lens):
+    """pool float64, w float64 [H, 256, 512]: (kv, k_rope, bound of kv)."""
+    c = np.concatenate([pool[tab[r, :cdiv(n, BS)]].reshape(-1, ROW)[:n] for r, n in enumerate(lens)])
+    kv = np.einsum("jc,hoc->jho", c[:, :LAT], w, optimize=True)
+    size = np.einsum("jc,hoc->jho", np.abs(c[:, :LAT]), np.abs(w), optimize=True)
+    # fp32 sums of 512 products, 2^-20 of the magnitudes, and the rounding
+    return kv, c[:, LAT:], 2.0 ** -8 * np.abs(kv) + 2.0 ** -19 * size
+
+
+def expanded(q, kv, k_rope, lens, qsl, scale):
+    """q float64 [T, H, 192], kv [rows, H, 256], k_rope [rows, 64]: (out, bound) [T, H, 128]."""
+    T, H = q.shape[:2]
+    out, bound = np.zeros((T, H, VAL)), np.zeros((T, H, VAL))
+    k0 = 0
+    for r, n in enumerate(lens):
+        m = qsl[r + 1] - qsl[r]
+        for h in range(H if m > 0 else 0):
+            x = q[qsl[r]:qsl[r + 1], h]
+            k = np.concatenate([kv[k0:k0 + n, h, :NOPE], k_rope[k0:k0 + n]], 1)
+            v = kv[k0:k0 + n, h, NOPE:]
+            if np.isfinite(k).all() and np.isfinite(v).all():
+                sees = np.arange(n)[None, :] <= np.arange(n - m, n)[:, None]
+                out[qsl[r]:qsl[r + 1], h], bound[qsl[r]:qsl[r + 1], h] = _attend(x, k, v, scale, sees)
+            else:  # row by row, over the keys that it sees
+                for i in range(m):
+                    p = n - m + i + 1
+                    o, b = _attend(x[i:i + 1], k[:p], v[:p], scale, np.ones((1, p), bool))
+                    out[qsl[r] + i, h], bound[qsl[r] + i, h] = o[0], b[0]
+        k0 += n
+    return out, bound

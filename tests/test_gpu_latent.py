@@ -270,3 +270,65 @@ def test_absorbed_many_requests():
     qs = [min(n, int(q)) for n, q in zip(lens, rng.integers(0, 3, 1500))]
     c = lat_case(lens, qs, 2, seed=3)
     lat_check(c, lat_run(c))
+
+
+# ------------------------------------------------------------------ expanded form
+@pytest.mark.parametrize("lens,heads", [([1], 1), ([128], 1), ([129], 3), ([17, 64, 100, 128], 16), ([0, 5, 0, 700], 2),
+                                        ([1000, 1, 333], 7), ([40] * 300, 1), ([260, 2000], 33)])
+def test_expand(lens, heads):
+    c = lat_case(lens, [min(n, 1) for n in lens], 1, seed=heads)
+    g = torch.Generator().manual_seed(heads)
+    w = (torch.randn(heads, 256, 512, generator=g) * 512 ** -0.5).to(BF).cuda()
+    n = sum(lens)
+    kv = torch.full((n + 5, heads, 256), 7.0, dtype=BF, device="cuda")
+    kr = torch.full((n + 5, 64), 7.0, dtype=BF, device="cuda")
+    ksl = dev(np.concatenate([[0], np.cumsum(lens)]), torch.int32)
+    pkv.pkv_expand_latent(c["pool"], w, dev(c["tab"], torch.int32), dev(c["lens"], torch.int32), ksl, kv, kr)
+    want, rope, bound = ref.expand(f64(c["pool"]), f64(w), c["tab"], lens)
+    close(f64(kv)[:n], want, bound)
+    assert np.array_equal(f64(kr)[:n], rope)
+    assert (kv[n:] == 7).all() and (kr[n:] == 7).all()
+
+
+def exp_case(lens, qs, heads, seed=0, pad=0):
+    g = torch.Generator().manual_seed(seed)
+    n = sum(lens)
+    qsl = np.concatenate([[0], np.cumsum(qs)]).astype(np.int32)
+    return dict(q=torch.randn(int(qsl[-1]) + pad, heads, 192, generator=g).to(BF).cuda(),
+                kv=torch.randn(n, heads, 256, generator=g).to(BF).cuda(),
+                kr=torch.randn(n, 64, generator=g).to(BF).cuda(), lens=np.array(lens, np.int32), qsl=qsl,
+                ksl=np.concatenate([[0], np.cumsum(lens)]).astype(np.int32), scale=192 ** -0.5)
+
+
+def exp_run(c, **kw):
+    return pkv.pkv_attention_expanded(c["q"], c["kv"], c["kr"], dev(c["lens"], torch.int32), dev(c["qsl"], torch.int32),
+                                      dev(c["ksl"], torch.int32), c["scale"], **kw)
+
+
+def exp_check(c, out):
+    n = int(c["qsl"][-1])
+    want, bound = ref.expanded(f64(c["q"]), f64(c["kv"]), f64(c["kr"]), c["lens"], c["qsl"], c["scale"])
+    close(f64(out)[:n], want[:n], bound[:n])
+
+
+@pytest.mark.parametrize("heads", [1, 3, 16])
+@pytest.mark.parametrize("lens,qs", [([1], [1]), ([128], [128]), ([129, 5], [129, 5]), ([70, 9, 300], [5, 9, 1]),
+                                     ([200, 0, 130, 64, 1], [130, 0, 1, 64, 1]), ([1000, 67], [300, 66]),
+                                     ([257] * 40, [33] * 40)])
+def test_expanded(heads, lens, qs):
+    c = exp_case(lens, qs, heads, seed=heads)
+    exp_check(c, exp_run(c))
+
+
+@pytest.mark.parametrize("heads,lens,qs", [(1, [6000], [1]), (2, [3000, 700], [200, 3]), (1, [900, 5000, 2], [129, 64, 2]),
+                                           (130, [300], [200])])
+def test_expanded_split_items(heads, lens, qs):
+    c = exp_case(lens, qs, heads, seed=2)
+    exp_check(c, exp_run(c))
+
+
+def test_expanded_many_requests():
+    rng = np.random.default_rng(6)
+    lens = rng.integers(0, 150, 500).tolist()
+    c = exp_case(lens, [min(n, int(q)) for n, q in zip(lens, rng.integers(0, 140, 500))], 1, seed=3)
+    exp_check(c, exp_run(c))

@@ -1248,7 +1248,10 @@ int pkv_attention_latent(const void* q, const void* pool, const int32_t* block_t
   p.group_tokens = g.group_tokens;
   p.item_cost = 128;
   p.min_keys = 256;
-  p.merge = 1;
+  // Without cuts, a step whose items have a CTA each and few keys needs no second
+  // kernel.
+  const long long units = st->sm_count / g.head_groups;
+  p.merge = dims->num_q_tokens > units || (long long)dims->max_blocks_per_req * pkv::kBlockSize > 512;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.pdl = opt.pdl != 0;
   p.early_plan = p.pdl && opt.early_plan != 0;

@@ -6,6 +6,19 @@
 
 namespace pkv {
 
+#ifdef __CUDACC__
+// mbar_wait with everything past its first probe out of line: the kernels that
+// use it run several roles' code at once, and a step of few rows runs most of it
+// once, at the price of its instruction fetches.
+static __device__ __noinline__ bool wait_spin(uint64_t* bar, uint32_t parity, int* err, WaitCtl* ctl) {
+  return mbar_wait(bar, parity, err, ctl);
+}
+
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, int* err, WaitCtl* ctl) {
+  return mbar_try_wait(bar, parity) || wait_spin(bar, parity, err, ctl);
+}
+#endif
+
 constexpr int kLatent = 512;               // dims of a cached latent (the values)
 constexpr int kRopeDim = 64;               // dims of the rotated key beside it
 constexpr int kLatRow = kLatent + kRopeDim;  // a cached row

@@ -25,13 +25,16 @@
 // four pairs of latent chunks), each going back as soon as its last MMA is
 // done, so that copies stay in flight while the other tile is worked on.
 //
-// Roles (576 threads).  Sixteen softmax warps: warpgroup g has columns 16 g ..
+// Roles (608 threads).  Sixteen softmax warps: warpgroup g has columns 16 g ..
 // 16 g + 15, its four warps 16 keys each (an M = 64 accumulator lies in 16 of
 // every 32 TMEM lanes; the 16x256b load spreads it over all lanes, two keys by
 // four columns a thread).  The running maximum moves only when a score exceeds
 // it by 2^8, on a vote of the warpgroup; then the warps agree on it through
 // shared memory and O^T is rescaled.  Warp 16 walks the CTA's work and issues
-// the copies, warp 17 the MMAs.
+// the copies, warp 17 the MMAs of S^T, warp 18 those of O^T: neither waits for
+// the other, so that a tile goes back to the copies as soon as its own P is
+// there (one warp that issued S(t + 1) before PV(t) held every slot until the
+// next tile had landed: 106 us for ...).
 //
 // Work split.  The items' keys (plus a fixed cost an item) form one sequence
 // that is cut in equal ranges, one a CTA -- or, with more than 64 heads, one a
@@ -49,8 +52,9 @@ namespace {
 constexpr int kSoftWarps = 16;
 constexpr int kSoftThreads = 32 * kSoftWarps;
 constexpr int kWarpLoad = kSoftWarps;
-constexpr int kWarpMma = kSoftWarps + 1;
-constexpr int kThreads = 32 * (kSoftWarps + 2);
+constexpr int kWarpS = kSoftWarps + 1;   // MMAs of the scores
+constexpr int kWarpO = kSoftWarps + 2;   // MMAs of the outputs
+constexpr int kThreads = 32 * (kSoftWarps + 3);
 constexpr int kBarSoft = 1;   // all softmax warps
 constexpr int kBarGroup = 2;  // + warpgroup
 
@@ -58,7 +62,8 @@ constexpr int kTile = 64;                 // keys
 constexpr int kTileBlocks = kTile / kBlockSize;
 constexpr int kChunks = kLatRow / 64;     // 64-dim chunks of a row
 constexpr int kChunkBytes = kTile * 128;
-constexpr int kParts = 5;                 // release units of a tile: rotated keys, four latent pairs
+constexpr int kStep = kChunkBytes >> 4;   // a chunk in the unit of the MMA's descriptors
+constexpr int kParts = 5;                 // release units of a tile: four latent pairs, rotated keys
 constexpr int kStages = 2;
 constexpr int kItems = 4;
 constexpr uint32_t kTmemCols = 512;
@@ -82,31 +87,6 @@ struct Item {
 constexpr int kPieceFirst = 1;  // holds the item's first tile
 constexpr int kPieceLast = 2;   // holds its last
 
-struct __align__(1024) Smem {
-  uint8_t q[kChunks][kChunkBytes];
-  uint8_t kv[kStages][kChunks][kChunkBytes];
-  uint8_t p[kLatMaxRows * 128];  // P^T: [column][64 keys] bf16, 128-byte swizzle
-  uint64_t kv_full[kStages][kParts], kv_empty[kStages][kParts];
-  uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full, p_free, o_full, o_empty;
-  uint64_t item_full[kItems];
-  uint64_t drained;
-  Item items[kItems];
-  float xrow[4][kLatMaxRows];        // a warpgroup's exchange of maxima and sums
-  unsigned long long bad[2];         // boundary keys taken out of the item's tiles, by item parity
-  uint32_t tmem_base;
-  WaitCtl wait;
-  // the plan: exclusive sums of the threads' requests, then the range
-  long long range_lo, range_hi, start_base;
-  int start_req;
-};
-static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "latent decode shared memory");
-
-// Part p's chunks: part 0 is chunk 8 (the rotated keys), part 1 + j the pair
-// 2 j, 2 j + 1.
-__device__ __forceinline__ int part_chunk(int part) { return part == 0 ? 8 : 2 * (part - 1); }
-__device__ __forceinline__ int part_chunks(int part) { return part == 0 ? 1 : 2; }
-
 // --------------------------------------------------------------------- plan
 struct Req {
   int q0, qr, L;
@@ -128,59 +108,147 @@ __device__ __forceinline__ Req load_req(const LatentDecodeParams& p, int r) {
   return make_req(p, __ldg(p.qsl + r), __ldg(p.qsl + r + 1), __ldg(p.seq_lens + r), &bad);
 }
 
-// Weight of token groups 0 .. i - 1, i <= ng: group m sees L - qr + min((m + 1)
+struct __align__(1024) Smem {
+  uint8_t q[kChunks][kChunkBytes];
+  uint8_t kv[kStages][kChunks][kChunkBytes];
+  uint8_t p[kLatMaxRows * 128];  // P^T: [column][64 keys] bf16, 128-byte swizzle
+  uint64_t kv_full[kStages][kParts], kv_empty[kStages][kParts];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full, p_free, o_full, o_empty;
+  uint64_t item_full[kItems];
+  uint64_t drained[2];
+  Item items[kItems];
+  float xrow[4][kLatMaxRows];        // a warpgroup's exchange of maxima and sums
+  float inv[kLatMaxRows];            // reciprocals of the columns' sums
+  unsigned long long bad[2];         // boundary keys taken out of the item's tiles, by item parity
+  uint32_t tmem_base;
+  WaitCtl wait;
+  // the plan: the CTA's range of units, the request it starts in and the units
+  // before that
+  long long range_lo, range_hi, start_base;
+  Req start;
+  int start_req, piece;
+};
+static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "latent decode shared memory");
+
+// Part i's chunks: 2 i and 2 i + 1, of the last part the one with the rotated keys.
+__device__ __forceinline__ int part_chunks(int part) { return part == kParts - 1 ? 1 : 2; }
+
+// The unit that the work is cut in.  Many items: keys, and item_cost more an item;
+// every CTA takes an equal range, whatever items it holds.  Few (`piece` > 0):
+// pieces of at most so many keys, an item's of equal length, one a CTA.
+//
+// Units of token groups 0 .. i - 1, i <= ng: group m sees L - qr + min((m + 1)
 // group_tokens, qr) keys.
-__device__ __forceinline__ long long groups_weight(const LatentDecodeParams& p, const Req& a, int i) {
+__device__ __forceinline__ int group_keys(const LatentDecodeParams& p, const Req& a, int m) {
+  return a.L - a.qr + min((m + 1) * p.group_tokens, a.qr);
+}
+
+__device__ __forceinline__ long long groups_keys(const LatentDecodeParams& p, const Req& a, int i) {
   const long long n = i;
-  long long w = n * ((long long)a.L - a.qr + p.item_cost) + (long long)p.group_tokens * (n * (n + 1) / 2);
+  long long w = n * ((long long)a.L - a.qr) + (long long)p.group_tokens * (n * (n + 1) / 2);
   if (i == a.ng && i > 0) w -= (long long)a.ng * p.group_tokens - a.qr;
   return w;
 }
 
-// The CTA's range of the weighted key sequence, and the request that its start
-// lies in.  All threads.
-__device__ __forceinline__ void plan_range(const LatentDecodeParams& p, Smem& sm, int unit, int units) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = cdiv(p.num_reqs, kThreads);
-  const int r0 = min(tid * per, p.num_reqs), r1 = min(r0 + per, p.num_reqs);
-  long long mine = 0;
-  for (int r = r0; r < r1; ++r) {
-    bool bad;
-    const Req a = make_req(p, __ldg(p.qsl + r), __ldg(p.qsl + r + 1), __ldg(p.seq_lens + r), &bad);
-    if (bad && blockIdx.x == 0) record_error(p.err, kErrBounds);  // the request is skipped
-    mine += groups_weight(p, a, a.ng);
-  }
-  // Exclusive sums over the threads.
+static __device__ __noinline__ long long groups_units(const LatentDecodeParams& p, const Req& a, int i, int piece) {
+  if (piece == 0) return groups_keys(p, a, i) + (long long)i * p.item_cost;
+  long long w = 0;
+  #pragma unroll 1
+  for (int m = 0; m < i; ++m) w += (group_keys(p, a, m) - 1) / piece + 1;
+  return w;
+}
+
+// Block-wide: the sum of `mine` over the threads before this one, and the sums of
+// it and of `count` over all.
+__device__ __forceinline__ long long scan(long long* part, long long mine, int count, long long* total,
+                                          int* counts) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int* const part_count = reinterpret_cast<int*>(part + 32);
   long long incl = mine;
   #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
-  long long* part = reinterpret_cast<long long*>(sm.xrow);
-  if (lane == 31) part[warp] = incl;
-  __syncthreads();
-  long long before = 0, total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    const long long v = part[w];
-    if (w < warp) before += v;
-    total += v;
+  count = __reduce_add_sync(0xffffffffu, count);
+  if (lane == 31) {
+    part[warp] = incl;
+    part_count[warp] = count;
   }
-  const long long excl = before + incl - mine;
-  long long chunk = (total + units - 1) / units;
-  if (chunk < p.min_keys) chunk = p.min_keys;
-  const long long lo = min((long long)unit * chunk, total), hi = min(lo + chunk, total);
+  __syncthreads();
+  const bool in = lane < kThreads / 32;
+  long long all = in ? part[lane] : 0, before = lane < warp ? all : 0;
+  #pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  *total = all;
+  *counts = __reduce_add_sync(0xffffffffu, in ? part_count[lane] : 0);
+  return before + incl - mine;
+}
+
+// The CTA's range of units, and the request that its start lies in.  All threads.
+__device__ __forceinline__ void plan_range(const LatentDecodeParams& p, Smem& sm, int unit, int units) {
+  const int tid = threadIdx.x;
+  const int per = cdiv(p.num_reqs, kThreads);
+  const int r0 = min(tid * per, p.num_reqs), r1 = min(r0 + per, p.num_reqs);
+  long long* const part = reinterpret_cast<long long*>(sm.xrow);  // (free until the softmax)
+  long long keys = 0;
+  int items = 0;
+  Req a;
+  #pragma unroll 1
+  for (int r = r0; r < r1; ++r) {
+    bool bad;
+    a = make_req(p, __ldg(p.qsl + r), __ldg(p.qsl + r + 1), __ldg(p.seq_lens + r), &bad);
+    if (bad && blockIdx.x == 0) record_error(p.err, kErrBounds);  // the request is skipped
+    keys += groups_keys(p, a, a.ng);
+    items += a.ng;
+  }
+  int piece = INT_MAX, all_items;
+  long long total, mine = items, excl, lo, hi;
+  if (p.merge) {
+    mine = keys + (long long)items * p.item_cost;
+    excl = scan(part, mine, items, &total, &all_items);
+    piece = 0;
+    if (3ll * all_items <= 2 * units) {
+      // ceil(keys / piece) summed over the items is at most their keys / piece + all_items.
+      const long long all_keys = total - (long long)all_items * p.item_cost, room = units - all_items;
+      const long long least = ((all_keys + room - 1) / room + kTile - 1) / kTile * kTile;
+      piece = (int)min(max(least, (long long)p.min_keys), 1ll << 30);
+      mine = 0;
+      #pragma unroll 1
+      for (int r = r0; r < r1; ++r) {
+        if (per > 1) a = load_req(p, r);
+        mine += groups_units(p, a, a.ng, piece);
+      }
+      __syncthreads();  // part is free again
+    }
+  }
+  if (piece > 0) {
+    excl = scan(part, mine, 0, &total, &all_items);
+    lo = min((long long)unit, total);
+    hi = min(lo + 1, total);
+  } else {
+    const long long chunk = max((total + units - 1) / units, (long long)p.min_keys);
+    lo = min(unit * chunk, total);
+    hi = min(lo + chunk, total);
+  }
   if (tid == 0) {
     sm.range_lo = lo;
     sm.range_hi = hi;
+    sm.piece = piece;
   }
   if (lo < hi && excl <= lo && lo < excl + mine) {
     long long base = excl;
+    #pragma unroll 1
     for (int r = r0; r < r1; ++r) {
-      const Req a = load_req(p, r);
-      const long long w = groups_weight(p, a, a.ng);
+      if (per > 1) a = load_req(p, r);
+      const long long w = groups_units(p, a, a.ng, piece);
       if (lo < base + w) {
         sm.start_req = r;
+        sm.start = a;
         sm.start_base = base;
         break;
       }
@@ -277,6 +345,45 @@ static __device__ __noinline__ unsigned long long bad_dim(const LatentDecodePara
   return hit;
 }
 
+// O^T of a warpgroup's 16 columns, 32 dims a warp, from TMEM address ta on: column
+// i times the factor that the threads of lanes 0 .. 3 hold for it (alpha[2 c + e]
+// of lane q: column 8 c + 2 q + e).  x: room for 16 numbers of this warp's.
+static __device__ __noinline__ void rescale_o(float* x, uint32_t ta, const float (&alpha)[4]) {
+  const int lane = threadIdx.x & 31;
+  if (lane < 4) {
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) x[2 * lane + 8 * (i >> 1) + (i & 1)] = alpha[i];
+  }
+  __syncwarp();
+  #pragma unroll 1
+  for (int mt = 0; mt < 4; ++mt, ta += kLatMaxRows) {
+    float o[16];
+    tmem_ld16(ta, o);
+    tc_wait_ld();
+    #pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] *= x[i];
+    tmem_st16f(ta, o);
+  }
+  tc_wait_st();
+}
+
+// What the boundary keys that were taken out mean for the item's outputs, which
+// this warp has written (16 columns from col0 on, dims 128 mt + 32 quad + lane):
+// NaN where a row sees a key that is not finite in the dim.  dst: the row of
+// column 0, out or a piece's.
+template <class T>
+static __device__ __noinline__ void spread_bad(const LatentDecodeParams& p, const Item& it,
+                                               unsigned long long bad, T* dst, int col0, int cols, int quad) {
+  __syncwarp();
+  for (int mt = 0; mt < 4; ++mt) {
+    const int d = mt * 128 + quad * 32 + (threadIdx.x & 31);
+    const unsigned long long hit = bad_dim(p, it, bad, d);
+    for (int col = col0; col < min(col0 + 16, cols); ++col)
+      // Token tk sees boundary keys 0 .. tk - 1.
+      if (hit & ((1ull << (col / p.group_heads)) - 1)) dst[(long long)col * kLatent + d] = T(NAN);
+  }
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
                          const __grid_constant__ CUtensorMap kmap, const LatentDecodeParams p) {
@@ -305,7 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.o_full, 1);
     mbar_init(&sm.o_empty, kSoftWarps);
     for (int i = 0; i < kItems; ++i) mbar_init(&sm.item_full[i], 1);
-    mbar_init(&sm.drained, 1);
+    mbar_init(&sm.drained[0], 1);
+    mbar_init(&sm.drained[1], 1);
     sm.wait.abort = 0;
     sm.wait.limit_ns = p.wait_limit_ns;
     sm.bad[0] = sm.bad[1] = 0;
@@ -323,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // This CTA's piece records, written again by the pieces that it cuts.
   if (p.merge && tid < 2) p.piece[(2 * blockIdx.x + tid) * kPieceWords] = 0;
   if (lo >= hi) return;
-  if (warp == kWarpMma) {
+  if (warp == kWarpS) {
     tmem_alloc(&sm.tmem_base, kTmemCols);
     tmem_relinquish();
   }
@@ -339,32 +447,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int r = sm.start_req;
     long long base = sm.start_base;
+    const int piece = sm.piece;
     const int oob_row = p.num_blocks * kBlockSize;
     const uint32_t q_bytes = (uint32_t)(kChunks * 128) * p.group_heads * p.group_tokens;
-    // A request's raw fields, the next one's ahead of its turn.
-    int f0 = __ldg(p.qsl + r), f1 = __ldg(p.qsl + r + 1), fl = __ldg(p.seq_lens + r);
+    Req a = sm.start;
+    // The next request's raw fields, ahead of its turn.
+    int f0 = a.q0 + a.qr, f1 = 0, fl = 0;
     while (ok && base < hi && r < p.num_reqs) {
-      bool bad;
-      const Req a = make_req(p, f0, f1, fl, &bad);
       if (r + 1 < p.num_reqs) {
-        f0 = f1;
         f1 = __ldg(p.qsl + r + 2);
         fl = __ldg(p.seq_lens + r + 1);
       }
-      const long long w = groups_weight(p, a, a.ng);
+      const long long w = a.ng > 0 ? groups_units(p, a, a.ng, piece) : 0;
       // First token group that the range reaches.
       int g = 0;
       if (base < lo) {
-        int top = a.ng;  // groups_weight(g) <= lo - base < groups_weight(top)
+        int top = a.ng;  // groups_units(g) <= lo - base < groups_units(top)
         while (top - g > 1) {
           const int mid = (g + top) >> 1;
-          if (groups_weight(p, a, mid) <= lo - base) g = mid;
+          if (groups_units(p, a, mid, piece) <= lo - base) g = mid;
           else top = mid;
         }
       }
       const int32_t* bt = p.block_tables + (long long)r * p.max_blocks;
       for (; g < a.ng && ok; ++g) {
-        const long long gbase = base + groups_weight(p, a, g);
+        const long long gbase = g > 0 ? base + groups_units(p, a, g, piece) : base;
         if (gbase >= hi) break;
         Item it;
         it.req = r;
@@ -372,9 +479,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         it.nt = min(p.group_tokens, a.qr - g * p.group_tokens);
         it.pos0 = a.L - a.qr + g * p.group_tokens;
         it.vis = it.pos0 + it.nt;
-        // Tile j belongs to the range that holds weight unit gbase + 64 j.
-        it.t0 = gbase >= lo ? 0 : (int)((lo - gbase + kTile - 1) / kTile);
-        it.t1 = hi - gbase >= it.vis ? cdiv(it.vis, kTile) : (int)((hi - gbase + kTile - 1) / kTile);
+        const int tiles = cdiv(it.vis, kTile);
+        it.t0 = 0;
+        it.t1 = tiles;
+        if (piece > 0) {
+          // Piece lo - gbase of n.
+          const int n = (it.vis - 1) / piece + 1, x = (int)(lo - gbase);
+          if (n > 1) {
+            it.t0 = (int)((long long)tiles * x / n);
+            it.t1 = (int)((long long)tiles * (x + 1) / n);
+          }
+        } else {
+          // Tile j belongs to the range that holds unit gbase + 64 j.
+          if (gbase < lo) it.t0 = (int)((lo - gbase + kTile - 1) / kTile);
+          if (hi - gbase < it.vis) it.t1 = (int)((hi - gbase + kTile - 1) / kTile);
+        }
         it.end = 0;
         if (it.t0 >= it.t1) continue;
         const int nbl = cdiv(it.vis, kBlockSize);
@@ -398,10 +517,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if ((unsigned)id < (unsigned)p.num_blocks) row = id * kBlockSize;
           else if (id != INT_MIN && lane < 4) record_error(p.err, kErrBounds);
           parts = 0;
+          #pragma unroll 1
           for (int part = 0; part < kParts; ++part) {
             if (j == it.t0 && part == 0) {
               // The item and its queries, ahead of its first keys.
-              if (n_item > 0) ok = mbar_wait(&sm.q_empty, (n_item - 1) & 1, p.err, ctl);
+              if (n_item > 0) ok = wait_for(&sm.q_empty, (n_item - 1) & 1, p.err, ctl);
               if (!ok) break;
               if (lane == 0) {
                 sm.items[n_item % kItems] = it;
@@ -412,9 +532,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (lane < kChunks) tma_load_3d(sm.q[lane], &qmap, lane * 64, head0, it.row0, &sm.q_full);
               ++n_item;
             }
-            if (t >= kStages) ok = mbar_wait(&sm.kv_empty[st][part], ((t / kStages) - 1) & 1, p.err, ctl);
+            if (t >= kStages) ok = wait_for(&sm.kv_empty[st][part], ((t / kStages) - 1) & 1, p.err, ctl);
             if (!ok) break;
-            const int n = part_chunks(part), c = part_chunk(part) + (lane >> 2);
+            const int n = part_chunks(part), c = 2 * part + (lane >> 2);
             if (lane == 0) mbar_arrive_expect_tx(&sm.kv_full[st][part], (uint32_t)n * kChunkBytes);
             __syncwarp();
             if (lane < 4 * n)
@@ -427,9 +547,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       base += w;
       ++r;
+      bool bad;
+      a = make_req(p, f0, f1, fl, &bad);
+      f0 = f1;
     }
     // End marker, for the MMA warp (behind its last item) and the softmax warps.
-    if (ok && n_item > 0) ok = mbar_wait(&sm.q_empty, (n_item - 1) & 1, p.err, ctl);
+    if (ok && n_item > 0) ok = wait_for(&sm.q_empty, (n_item - 1) & 1, p.err, ctl);
     if (ok && lane == 0) {
       sm.items[n_item % kItems].end = 1;
       mbar_arrive(&sm.item_full[n_item % kItems]);
@@ -438,6 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (!ok) {
       // Aborted: the copies in flight must land before the CTA ends.
+      #pragma unroll 1
       for (int part = 0; part < kParts; ++part) {
         const int n = t + (part < parts ? 1 : 0);  // tiles whose part was issued
         for (int i = max(0, n - kStages); i < n; ++i)
@@ -445,97 +569,96 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (n_item > 0) mbar_wait_drain(&sm.q_full, (n_item - 1) & 1, p.err, ctl);
     }
-  } else if (warp == kWarpMma) {
-    // ============================ MMAs ====================================
-    // Order: S(t), then PV(t - 1): the softmax of a tile runs beside both.
+  } else if (warp == kWarpS) {
+    // ========================= MMAs of the scores =========================
+    // As soon as a tile's chunks land.  The buffer of S(t) was read by the softmax
+    // before the PV of tile t - 2, whose end tile t's latents waited for.  Loops
+    // stay rolled but for the four MMAs of a chunk.
     const int n_cols = ((p.group_heads * p.group_tokens + 15) / 16) * 16;
-    const uint32_t idesc_s = idesc_bf16_f32(kTile, n_cols, 0, 0);
-    const uint32_t idesc_o = idesc_bf16_f32(128, n_cols, 1, 0);
+    const uint32_t idesc = idesc_bf16_f32(kTile, n_cols, 0, 0);
+    const uint64_t desc_k = smem_desc_sw128(smem_u32(sm.kv[0][0]), 16, 1024);
+    const uint64_t desc_q = smem_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
     bool ok = true;
-    int t = 0, n_item = 0;
-    auto pv = [&](int tt, bool first, bool last) {
-      const int st = tt % kStages;
-      ok = ok && mbar_wait(&sm.p_full, tt & 1, p.err, ctl);
-      if (first && n_item > 0) ok = ok && mbar_wait(&sm.o_empty, (n_item - 1) & 1, p.err, ctl);
-      if (!ok) return;
-      tc_fence_after();
-      if (elect_one()) {
-        #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          #pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk) {
-            // C^T: atoms of 64 dims x 8 keys; the chunks kChunkBytes apart,
-            // 8-key groups 1024 bytes apart.
-            const uint64_t da = smem_desc_sw128(smem_u32(sm.kv[st][2 * m]) + kk * 2048, kChunkBytes, 1024);
-            const uint64_t db = smem_desc_sw128(smem_u32(sm.p) + kk * 32, 16, 1024);
-            tc_mma_f16_ss(tmem + kColO + m * kLatMaxRows, da, db, idesc_o, !first || kk > 0);
-          }
-          tc_commit(&sm.kv_empty[st][1 + m]);
-        }
-        tc_commit(&sm.p_free);
-        if (last) tc_commit(&sm.o_full);
-      }
-      __syncwarp();
-    };
-    // The tile whose PV is still to be issued belongs to the item before when
-    // an item's first S goes out.
-    bool pending = false, pend_first = false;
-    for (;; ++n_item) {
-      if (!mbar_wait(&sm.q_full, n_item & 1, p.err, ctl)) {
-        ok = false;
-        break;
-      }
-      const Item it = sm.items[n_item % kItems];
+    for (int n_item = 0, t = 0; ok; ++n_item) {
+      ok = wait_for(&sm.q_full, n_item & 1, p.err, ctl);
+      if (!ok) break;
+      const Item& it = sm.items[n_item % kItems];
       if (it.end) break;
-      for (int j = it.t0; j < it.t1 && ok; ++j, ++t) {
+      for (int left = it.t1 - it.t0; left > 0 && ok; --left, ++t) {
         const int st = t % kStages;
-        const uint32_t tS = tmem + (t & 1) * kLatMaxRows;
-        for (int part = 0; part < kParts && ok; ++part) {
-          ok = mbar_wait(&sm.kv_full[st][part], (t / kStages) & 1, p.err, ctl);
-          if (!ok) break;
-          tc_fence_after();
+        #pragma unroll 1
+        for (int c = 0; c < kChunks; ++c) {
+          if ((c & 1) == 0) {
+            ok = wait_for(&sm.kv_full[st][c >> 1], (t / kStages) & 1, p.err, ctl);
+            if (!ok) break;
+            tc_fence_after();
+          }
           if (elect_one()) {
-            for (int c = part_chunk(part); c < part_chunk(part) + part_chunks(part); ++c) {
-              #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {
-                const uint64_t da = smem_desc_sw128(smem_u32(sm.kv[st][c]) + kk * 32, 16, 1024);
-                const uint64_t db = smem_desc_sw128(smem_u32(sm.q[c]) + kk * 32, 16, 1024);
-                tc_mma_f16_ss(tS, da, db, idesc_s, part > 0 || kk > 0);
-              }
-            }
+            const uint64_t da = desc_k + (uint64_t)((st * kChunks + c) * kStep);
+            const uint64_t db = desc_q + (uint64_t)(c * kStep);
+            #pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_f16_ss(tmem + (t & 1) * kLatMaxRows, da + 2 * kk, db + 2 * kk, idesc, c > 0 || kk > 0);
           }
           __syncwarp();
         }
         if (ok && elect_one()) {
-          tc_commit(&sm.kv_empty[st][0]);
           tc_commit(&sm.s_full[t & 1]);
-          if (j == it.t1 - 1) tc_commit(&sm.q_empty);
+          tc_commit(&sm.kv_empty[st][kParts - 1]);
+          if (left == 1) tc_commit(&sm.q_empty);
         }
         __syncwarp();
-        if (pending) {
-          // (an item's first tile: the tile before is the last of the item before)
-          if (j == it.t0) {
-            --n_item;
-            pv(t - 1, pend_first, true);
-            ++n_item;
-          } else {
-            pv(t - 1, pend_first, false);
-          }
-        }
-        pending = true;
-        pend_first = j == it.t0;
       }
-      if (!ok) break;
-    }
-    if (ok && pending) {
-      --n_item;
-      pv(t - 1, pend_first, true);
     }
     if (!ok) {
       // Aborted: the issued MMAs must end before TMEM is freed.
-      if (elect_one()) tc_commit(&sm.drained);
+      if (elect_one()) tc_commit(&sm.drained[0]);
       __syncwarp();
-      mbar_wait_drain(&sm.drained, 0, p.err, ctl);
+      mbar_wait_drain(&sm.drained[0], 0, p.err, ctl);
+    }
+  } else if (warp == kWarpO) {
+    // ========================= MMAs of the outputs ========================
+    const int n_cols = ((p.group_heads * p.group_tokens + 15) / 16) * 16;
+    const uint32_t idesc = idesc_bf16_f32(128, n_cols, 1, 0);
+    // C^T: MN-major atoms of 64 dims x 8 keys, the chunks kChunkBytes apart.
+    const uint64_t desc_v = smem_desc_sw128(smem_u32(sm.kv[0][0]), kChunkBytes, 1024);
+    const uint64_t desc_p = smem_desc_sw128(smem_u32(sm.p), 16, 1024);
+    bool ok = true;
+    for (int n_item = 0, t = 0; ok; ++n_item) {
+      ok = wait_for(&sm.item_full[n_item % kItems], (n_item / kItems) & 1, p.err, ctl);
+      if (!ok) break;
+      const Item& it = sm.items[n_item % kItems];
+      if (it.end) break;
+      const int n = it.t1 - it.t0;
+      for (int j = 0; j < n; ++j, ++t) {
+        const int st = t % kStages;
+        ok = wait_for(&sm.p_full, t & 1, p.err, ctl);
+        if (ok && j == 0 && n_item > 0) ok = wait_for(&sm.o_empty, (n_item - 1) & 1, p.err, ctl);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          #pragma unroll 1
+          for (int m = 0; m < 4; ++m) {
+            // (landed long since: the scores came from it)
+            if (!wait_for(&sm.kv_full[st][m], (t / kStages) & 1, p.err, ctl)) break;
+            const uint64_t da = desc_v + (uint64_t)((st * kChunks + 2 * m) * kStep);
+            #pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              tc_mma_f16_ss(tmem + kColO + m * kLatMaxRows, da + kk * (2048 >> 4), desc_p + 2 * kk, idesc,
+                            j > 0 || kk > 0);
+            tc_commit(&sm.kv_empty[st][m]);
+          }
+          tc_commit(&sm.p_free);
+          if (j == n - 1) tc_commit(&sm.o_full);
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok) {
+      // Aborted: the issued MMAs must end before TMEM is freed.
+      if (elect_one()) tc_commit(&sm.drained[1]);
+      __syncwarp();
+      mbar_wait_drain(&sm.drained[1], 0, p.err, ctl);
     }
   } else {
     // ==================== softmax and epilogue (warps 0-15) ==================
@@ -561,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int t = 0;
     for (int n_item = 0;; ++n_item) {
-      const bool have = mbar_wait(&sm.item_full[n_item % kItems], (n_item / kItems) & 1, p.err, ctl);
+      const bool have = wait_for(&sm.item_full[n_item % kItems], (n_item / kItems) & 1, p.err, ctl);
       const Item it = sm.items[n_item % kItems];
       // Agree before any barrier: a wait that gave up stops everyone.
       if (barrier_or(kBarSoft, kSoftThreads, !have || it.end)) break;
@@ -574,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.f;
       for (int j = it.t0; j < it.t1; ++j, ++t) {
         const int key0 = j * kTile;
-        ok = ok && mbar_wait(&sm.s_full[t & 1], (t >> 1) & 1, p.err, ctl);
+        ok = ok && wait_for(&sm.s_full[t & 1], (t >> 1) & 1, p.err, ctl);
         tc_fence_after();
         uint32_t w[4];
         if (mine) {
@@ -627,26 +750,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               l[i] *= alpha[i];
             }
             if (j > it.t0) {
-              // O^T of this warpgroup's columns, 32 dims a warp: it must hold
-              // the tile before.
-              if (lane < 4) {
-                #pragma unroll
-                for (int i = 0; i < 4; ++i) sm.xrow[quad][col0 + 8 * (i >> 1) + (i & 1)] = alpha[i];
-              }
-              __syncwarp();
-              ok = ok && mbar_wait(&sm.p_free, (t - 1) & 1, p.err, ctl);
+              // O^T must hold the tile before.
+              ok = ok && wait_for(&sm.p_free, (t - 1) & 1, p.err, ctl);
               tc_fence_after();
-              #pragma unroll 1
-              for (int mt = 0; mt < 4; ++mt) {
-                float o[16];
-                const uint32_t ta = tmem + lane_off + kColO + mt * kLatMaxRows + wg * 16;
-                tmem_ld16(ta, o);
-                tc_wait_ld();
-                #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] *= sm.xrow[quad][wg * 16 + i];
-                tmem_st16f(ta, o);
-              }
-              tc_wait_st();
+              rescale_o(sm.xrow[quad] + wg * 16, tmem + lane_off + kColO + wg * 16, alpha);
               named_barrier(kBarGroup + wg, 128);  // sm.xrow is free again
             }
           }
@@ -670,12 +777,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (key0 + kTile > it.pos0 + 1) {
           // (landed long since: the scores came from them)
-          for (int part = 1; part < kParts; ++part)
-            ok = ok && mbar_wait(&sm.kv_full[t % kStages][part], (t / kStages) & 1, p.err, ctl);
+          #pragma unroll 1
+          for (int part = 0; part < kParts - 1; ++part)
+            ok = ok && wait_for(&sm.kv_full[t % kStages][part], (t / kStages) & 1, p.err, ctl);
           clean_tile(sm, sm.kv[t % kStages], key0, it.pos0, it.vis, bad, warp, lane);
         }
         // P's buffer is free once the product before has read it.
-        if (t > 0) ok = ok && mbar_wait(&sm.p_free, (t - 1) & 1, p.err, ctl);
+        if (t > 0) ok = ok && wait_for(&sm.p_free, (t - 1) & 1, p.err, ctl);
         if (mine) {
           stmatrix4_trans(st_addr, w[0], w[1], w[2], w[3]);
           fence_proxy_async_smem();
@@ -687,6 +795,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- epilogue ---------------------------------------------------------
       const int n_tiles = cdiv(it.vis, kTile);
       const bool whole = it.t0 == 0 && it.t1 == n_tiles;
+      const int slot = 2 * blockIdx.x + (it.t0 == 0 ? 1 : 0);
+      // Columns in use: rows (token, head) of out from the first on, in order
+      // (with two head groups an item has one token).
+      const int cols = (it.nt - 1) * p.group_heads + heads;
       if (mine) {
         #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -698,56 +810,62 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 4; ++i) sm.xrow[quad][col0 + 8 * (i >> 1) + (i & 1)] = l[i];
         }
         named_barrier(kBarGroup + wg, 128);
+        if (quad == 0 && lane < 4) {
+          #pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int col = col0 + 8 * (i >> 1) + (i & 1);
+            const float sum = (sm.xrow[0][col] + sm.xrow[1][col]) + (sm.xrow[2][col] + sm.xrow[3][col]);
+            sm.inv[col] = 1.f / sum;
+            if (!whole && ok && col < cols)
+              *reinterpret_cast<float2*>(p.piece_ml + ((long long)slot * p.piece_rows + col) * 2) =
+                  make_float2(m[i], sum);
+          }
+        }
+        named_barrier(kBarGroup + wg, 128);
       }
-      ok = ok && mbar_wait(&sm.o_full, n_item & 1, p.err, ctl);
+      if (!whole && ok && tid == 0) {
+        int* rec = p.piece + slot * kPieceWords;
+        rec[1] = it.row0;
+        rec[2] = cols;
+        rec[0] = 4 | (it.t0 == 0 ? kPieceFirst : 0) | (it.t1 == n_tiles ? kPieceLast : 0);
+      }
+      ok = ok && wait_for(&sm.o_full, n_item & 1, p.err, ctl);
       tc_fence_after();
       // Boundary keys that were taken out, by any warp.
       if (it.nt > 1) named_barrier(kBarSoft, kSoftThreads);
       const unsigned long long gone = *bad;
-      if (mine) {
-        const int slot = 2 * blockIdx.x + (it.t0 == 0 ? 1 : 0);
-        if (!whole && ok) {
-          if (quad == 0 && lane < 4) {
-            #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int col = col0 + 8 * (i >> 1) + (i & 1);
-              if (col >= rows) continue;
-              const float sum = (sm.xrow[0][col] + sm.xrow[1][col]) + (sm.xrow[2][col] + sm.xrow[3][col]);
-              *reinterpret_cast<float2*>(p.piece_ml + ((long long)slot * p.piece_rows + col) * 2) =
-                  make_float2(m[i], sum);
-            }
-          }
-          if (tid == 0) {
-            int* rec = p.piece + slot * kPieceWords;
-            rec[1] = it.row0;
-            rec[2] = it.nt;
-            rec[0] = 4 | (it.t0 == 0 ? kPieceFirst : 0) | (it.t1 == n_tiles ? kPieceLast : 0);
-          }
-        }
+      if (mine && ok) {
+        const int n = cols - wg * 16;  // columns of this warpgroup in use (16 at most)
+        __nv_bfloat16* dst = p.out + ((long long)it.row0 * p.num_q_heads + head0) * kLatent;
+        float* part = p.piece_o + (long long)slot * p.piece_rows * kLatent;
+        const uint32_t ta = tmem + lane_off + kColO + wg * 16;
         #pragma unroll 1
         for (int mt = 0; mt < 4; ++mt) {
           const int d = mt * 128 + quad * 32 + lane;
           float o[16];
-          tmem_ld16(tmem + lane_off + kColO + mt * kLatMaxRows + wg * 16, o);
+          tmem_ld16(ta + mt * kLatMaxRows, o);
           tc_wait_ld();
-          unsigned long long hit = 0;
-          if (gone) hit = bad_dim(p, it, gone, d);
-          #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int col = wg * 16 + i;
-            const int tk = col / p.group_heads, h = col - tk * p.group_heads;
-            if (tk >= it.nt || col >= rows || h >= heads) continue;
-            // Token tk sees boundary keys 0 .. tk - 1.
-            if (hit & ((1ull << tk) - 1)) o[i] = NAN;
-            if (whole) {
-              const float sum = (sm.xrow[0][col] + sm.xrow[1][col]) + (sm.xrow[2][col] + sm.xrow[3][col]);
-              if (ok)
-                p.out[((long long)(it.row0 + tk) * p.num_q_heads + head0 + h) * kLatent + d] =
-                    __float2bfloat16_rn(o[i] / sum);
-            } else if (ok) {
-              p.piece_o[((long long)slot * p.piece_rows + col) * kLatent + d] = o[i];
+          if (whole) {
+            // Lanes 2 k and 2 k + 1 hold dims d and d + 1 of both columns of a
+            // pair: they swap, so that each stores two dims of one column.
+            __nv_bfloat16* at = dst + (long long)(wg * 16 + (lane & 1)) * kLatent + (d & ~1);
+            #pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const float a = o[i] * sm.inv[wg * 16 + i], b = o[i + 1] * sm.inv[wg * 16 + i + 1];
+              const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
+              if (i + (lane & 1) < n)
+                *reinterpret_cast<uint32_t*>(at + i * kLatent) = lane & 1 ? pack_bf16(other, b) : pack_bf16(a, other);
             }
+          } else {
+            float* at = part + (long long)(wg * 16) * kLatent + d;
+            #pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (i < n) at[i * kLatent] = o[i];
           }
+        }
+        if (gone) {
+          if (whole) spread_bad(p, it, gone, dst, wg * 16, cols, quad);
+          else spread_bad(p, it, gone, part, wg * 16, cols, quad);
         }
       }
       // Every warp has read sm.bad, sm.xrow; O^T goes back.
@@ -761,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kWarpMma) tmem_dealloc(tmem, kTmemCols);
+  if (warp == kWarpS) tmem_dealloc(tmem, kTmemCols);
 }
 
 // Joins the pieces of rows that were cut.  Block (b, y): the row whose first
@@ -777,10 +895,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const La
   const int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
   const int* rec = p.piece + (2 * cta + 1) * kPieceWords;
   if (rec[0] == 0) return;  // CTA cta cut nothing that begins with it
-  const int hg = cta % p.head_groups, head0 = hg * p.group_heads;
-  const int row0 = rec[1], nt = rec[2];
-  const int tk = row / p.group_heads, h = row - tk * p.group_heads;
-  if (tk >= nt || tk >= p.group_tokens || head0 + h >= p.num_q_heads) return;
+  if (row >= rec[2]) return;
+  // (the item's columns are rows of out, in order)
+  const long long out_row = (long long)rec[1] * p.num_q_heads + (cta % p.head_groups) * p.group_heads + row;
   // The running state over the pieces in order.
   float m = -INFINITY, l = 0.f;
   float4 o[4];
@@ -809,12 +926,13 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const La
     if (c >= grid) break;
     slot = 2 * c;
   }
-  __nv_bfloat16* dst = p.out + ((long long)(row0 + tk) * p.num_q_heads + head0 + h) * kLatent;
+  __nv_bfloat16* dst = p.out + out_row * kLatent;
+  const float inv = 1.f / l;
   #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint2 v;
-    v.x = pack_bf16(o[i].x / l, o[i].y / l);
-    v.y = pack_bf16(o[i].z / l, o[i].w / l);
+    v.x = pack_bf16(o[i].x * inv, o[i].y * inv);
+    v.y = pack_bf16(o[i].z * inv, o[i].w * inv);
     *reinterpret_cast<uint2*>(dst + (i * 32 + lane) * 4) = v;
   }
 }

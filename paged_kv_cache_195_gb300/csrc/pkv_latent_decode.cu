@@ -58,14 +58,10 @@ constexpr int kThreads = 32 * (kSoftWarps + 3);
 constexpr int kBarSoft = 1;   // all softmax warps
 constexpr int kBarGroup = 2;  // + warpgroup
 
-constexpr int kTile = 64;                 // keys
-constexpr int kTileBlocks = kTile / kBlockSize;
 constexpr int kChunks = kLatRow / 64;     // 64-dim chunks of a row
-constexpr int kChunkBytes = kTile * 128;
-constexpr int kStep = kChunkBytes >> 4;   // a chunk in the unit of the MMA's descriptors
 constexpr int kParts = 5;                 // release units of a tile: four latent pairs, rotated keys
-constexpr int kStages = 2;
 constexpr int kItems = 4;
+constexpr int kMmaKeys = 64;              // M of the scores' MMAs
 constexpr uint32_t kTmemCols = 512;
 constexpr int kColO = 2 * kLatMaxRows;    // TMEM: S^T buffers, then O^T
 constexpr float kRescaleLog2 = 8.0f;
@@ -108,28 +104,43 @@ __device__ __forceinline__ Req load_req(const LatentDecodeParams& p, int r) {
   return make_req(p, __ldg(p.qsl + r), __ldg(p.qsl + r + 1), __ldg(p.seq_lens + r), &bad);
 }
 
-struct __align__(1024) Smem {
-  uint8_t q[kChunks][kChunkBytes];
-  uint8_t kv[kStages][kChunks][kChunkBytes];
-  uint8_t p[kLatMaxRows * 128];  // P^T: [column][64 keys] bf16, 128-byte swizzle
-  uint64_t kv_full[kStages][kParts], kv_empty[kStages][kParts];
+// The CTA's part of the plan: its range of units, the request that it starts in and
+// the units before that.
+struct Plan {
+  long long part[32];
+  int part_count[32];
+  long long range_lo, range_hi, start_base;
+  Req start;
+  int start_req, piece;
+};
+
+// COLS: columns that there is room for; TILE keys in each of STAGES tiles.
+template <int COLS, int TILE, int STAGES>
+struct __align__(1024) SmemT {
+  uint8_t q[kChunks][COLS * 128];
+  uint8_t kv[STAGES][kChunks][TILE * 128];
+  uint8_t p[COLS * 128];  // P^T: [column][64 keys] bf16, 128-byte swizzle
+  uint64_t kv_full[STAGES][kParts], kv_empty[STAGES][kParts];
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full, p_free, o_full, o_empty;
   uint64_t item_full[kItems];
   uint64_t drained[2];
   Item items[kItems];
-  float xrow[4][kLatMaxRows];        // a warpgroup's exchange of maxima and sums
-  float inv[kLatMaxRows];            // reciprocals of the columns' sums
-  unsigned long long bad[2];         // boundary keys taken out of the item's tiles, by item parity
+  union {
+    Plan plan;                  // until the softmax begins
+    struct {
+      float xrow[4][kLatMaxRows];  // a warpgroup's exchange of maxima and sums
+      float inv[kLatMaxRows];      // reciprocals of the columns' sums
+    };
+  };
+  unsigned long long bad[2];    // boundary keys taken out of the item's tiles, by item parity
   uint32_t tmem_base;
   WaitCtl wait;
-  // the plan: the CTA's range of units, the request it starts in and the units
-  // before that
-  long long range_lo, range_hi, start_base;
-  Req start;
-  int start_req, piece;
 };
-static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "latent decode shared memory");
+
+// The same value in all lanes, in a uniform register.
+__device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
+__device__ __forceinline__ bool all_of(bool v) { return __all_sync(0xffffffffu, v); }
 
 // Part i's chunks: 2 i and 2 i + 1, of the last part the one with the rotated keys.
 __device__ __forceinline__ int part_chunks(int part) { return part == kParts - 1 ? 1 : 2; }
@@ -159,12 +170,11 @@ static __device__ __noinline__ long long groups_units(const LatentDecodeParams& 
   return w;
 }
 
-// Block-wide: the sum of `mine` over the threads before this one, and the sums of
-// it and of `count` over all.
-__device__ __forceinline__ long long scan(long long* part, long long mine, int count, long long* total,
-                                          int* counts) {
+// Over THREADS threads (a warp, or the block): the sum of `mine` over those before
+// this one, and the sums of it and of `count` over all.
+template <int THREADS>
+__device__ __forceinline__ long long scan(Plan& pl, long long mine, int count, long long* total, int* counts) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int* const part_count = reinterpret_cast<int*>(part + 32);
   long long incl = mine;
   #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -172,29 +182,38 @@ __device__ __forceinline__ long long scan(long long* part, long long mine, int c
     if (lane >= o) incl += v;
   }
   count = __reduce_add_sync(0xffffffffu, count);
+  if (THREADS == 32) {
+    *total = __shfl_sync(0xffffffffu, incl, 31);
+    *counts = count;
+    return incl - mine;
+  }
   if (lane == 31) {
-    part[warp] = incl;
-    part_count[warp] = count;
+    pl.part[warp] = incl;
+    pl.part_count[warp] = count;
   }
   __syncthreads();
-  const bool in = lane < kThreads / 32;
-  long long all = in ? part[lane] : 0, before = lane < warp ? all : 0;
+  const bool in = lane < THREADS / 32;
+  long long all = in ? pl.part[lane] : 0, before = lane < warp ? all : 0;
   #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     all += __shfl_xor_sync(0xffffffffu, all, o);
     before += __shfl_xor_sync(0xffffffffu, before, o);
   }
   *total = all;
-  *counts = __reduce_add_sync(0xffffffffu, in ? part_count[lane] : 0);
+  *counts = __reduce_add_sync(0xffffffffu, in ? pl.part_count[lane] : 0);
   return before + incl - mine;
 }
 
-// The CTA's range of units, and the request that its start lies in.  All threads.
-__device__ __forceinline__ void plan_range(const LatentDecodeParams& p, Smem& sm, int unit, int units) {
-  const int tid = threadIdx.x;
-  const int per = cdiv(p.num_reqs, kThreads);
+// Unit `unit` of `units` CTAs' (or pairs') share.  THREADS threads: one warp for
+// steps of up to kWarpReqs requests, beside which the rest of the CTA is set up, else
+// the block (which then needs a __syncthreads before it reads the result).
+constexpr int kWarpReqs = 256;
+
+template <int THREADS>
+static __device__ __noinline__ void plan_range(const LatentDecodeParams& p, Plan& pl, int unit, int units, int tile) {
+  const int tid = THREADS == 32 ? threadIdx.x & 31 : threadIdx.x;
+  const int per = cdiv(p.num_reqs, THREADS);
   const int r0 = min(tid * per, p.num_reqs), r1 = min(r0 + per, p.num_reqs);
-  long long* const part = reinterpret_cast<long long*>(sm.xrow);  // (free until the softmax)
   long long keys = 0;
   int items = 0;
   Req a;
@@ -210,12 +229,12 @@ __device__ __forceinline__ void plan_range(const LatentDecodeParams& p, Smem& sm
   long long total, mine = items, excl, lo, hi;
   if (p.merge) {
     mine = keys + (long long)items * p.item_cost;
-    excl = scan(part, mine, items, &total, &all_items);
+    excl = scan<THREADS>(pl, mine, items, &total, &all_items);
     piece = 0;
     if (3ll * all_items <= 2 * units) {
       // ceil(keys / piece) summed over the items is at most their keys / piece + all_items.
       const long long all_keys = total - (long long)all_items * p.item_cost, room = units - all_items;
-      const long long least = ((all_keys + room - 1) / room + kTile - 1) / kTile * kTile;
+      const long long least = ((all_keys + room - 1) / room + tile - 1) / tile * tile;
       piece = (int)min(max(least, (long long)p.min_keys), 1ll << 30);
       mine = 0;
       #pragma unroll 1
@@ -223,11 +242,11 @@ __device__ __forceinline__ void plan_range(const LatentDecodeParams& p, Smem& sm
         if (per > 1) a = load_req(p, r);
         mine += groups_units(p, a, a.ng, piece);
       }
-      __syncthreads();  // part is free again
+      if (THREADS > 32) __syncthreads();  // pl.part is free again
     }
   }
   if (piece > 0) {
-    excl = scan(part, mine, 0, &total, &all_items);
+    excl = scan<THREADS>(pl, mine, 0, &total, &all_items);
     lo = min((long long)unit, total);
     hi = min(lo + 1, total);
   } else {
@@ -236,9 +255,9 @@ __device__ __forceinline__ void plan_range(const LatentDecodeParams& p, Smem& sm
     hi = min(lo + chunk, total);
   }
   if (tid == 0) {
-    sm.range_lo = lo;
-    sm.range_hi = hi;
-    sm.piece = piece;
+    pl.range_lo = lo;
+    pl.range_hi = hi;
+    pl.piece = piece;
   }
   if (lo < hi && excl <= lo && lo < excl + mine) {
     long long base = excl;
@@ -247,15 +266,14 @@ __device__ __forceinline__ void plan_range(const LatentDecodeParams& p, Smem& sm
       if (per > 1) a = load_req(p, r);
       const long long w = groups_units(p, a, a.ng, piece);
       if (lo < base + w) {
-        sm.start_req = r;
-        sm.start = a;
-        sm.start_base = base;
+        pl.start_req = r;
+        pl.start = a;
+        pl.start_base = base;
         break;
       }
       base += w;
     }
   }
-  __syncthreads();
 }
 
 // --------------------------------------------------------------- TMEM, smem
@@ -290,7 +308,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // Address of 16-byte piece `piece` (0 .. 63) of key row `row`'s latent in a tile.
-__device__ __forceinline__ uint4* latent_piece(uint8_t (*tile)[kChunkBytes], int row, int piece) {
+template <int TILE>
+__device__ __forceinline__ uint4* latent_piece(uint8_t (*tile)[TILE * 128], int row, int piece) {
   return reinterpret_cast<uint4*>(tile[piece >> 3] + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
 }
 
@@ -298,29 +317,29 @@ __device__ __forceinline__ bool non_finite(uint32_t w) {
   return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
-// Rows of the tile that no row of the item sees (rows vis - key0 .. 63) must
+// Rows of the tile that no row of the item sees (from row vis - key0 on) must
 // not reach the product, whatever they hold: 0 * NaN.  Rows that only some of
 // the item's tokens see (keys pos0 + 1 .. vis - 1) may hold NaN or infinities
 // that the others must not get: those are taken out too and noted, and the
 // epilogue gives them to the rows that see them.  Rare or at a range's last
 // tiles; one warp a row, out of line.
-static __device__ __noinline__ void clean_tile(Smem& sm, uint8_t (*tile)[kChunkBytes], int key0,
-                                               int pos0, int vis, unsigned long long* bad, int warp,
-                                               int lane) {
+template <int TILE>
+static __device__ __noinline__ void clean_tile(uint8_t (*tile)[TILE * 128], int key0, int pos0, int vis,
+                                               unsigned long long* bad, int warp, int lane) {
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int row = max(pos0 + 1 - key0, 0) + warp; row < kTile; row += kSoftWarps) {
+  for (int row = max(pos0 + 1 - key0, 0) + warp; row < TILE; row += kSoftWarps) {
     const int key = key0 + row;
     bool out = key >= vis;
     if (!out) {
-      const uint4 a = *latent_piece(tile, row, lane), b = *latent_piece(tile, row, lane + 32);
+      const uint4 a = *latent_piece<TILE>(tile, row, lane), b = *latent_piece<TILE>(tile, row, lane + 32);
       out = __any_sync(0xffffffffu, non_finite(a.x) || non_finite(a.y) || non_finite(a.z) ||
                                         non_finite(a.w) || non_finite(b.x) || non_finite(b.y) ||
                                         non_finite(b.z) || non_finite(b.w));
       if (out && lane == 0) atomicOr(bad, 1ull << (key - pos0 - 1));
     }
     if (out) {
-      *latent_piece(tile, row, lane) = zero;
-      *latent_piece(tile, row, lane + 32) = zero;
+      *latent_piece<TILE>(tile, row, lane) = zero;
+      *latent_piece<TILE>(tile, row, lane + 32) = zero;
     }
   }
   fence_proxy_async_smem();
@@ -384,24 +403,53 @@ static __device__ __noinline__ void spread_bad(const LatentDecodeParams& p, cons
   }
 }
 
+// The pair's side of the copies and of their release: a copy lands in both CTAs of
+// the cluster, at the same place, and counts on both barriers; a commit arrives on
+// both.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".multicast::cluster [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)), "h"((uint16_t)3)
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <int COLS, int TILE, int STAGES, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
                          const __grid_constant__ CUtensorMap kmap, const LatentDecodeParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
+  using Smem = SmemT<COLS, TILE, STAGES>;
+  constexpr int kTileBlocks = TILE / kBlockSize;
+  constexpr int kWindow = 32 / kTileBlocks;         // tiles of a load of block ids
+  constexpr int kKvStep = TILE * 128 >> 4;          // a chunk in the unit of the MMA's descriptors
+  constexpr int kQStep = COLS * 128 >> 4;
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw + (((raw + 1023u) & ~1023u) - raw));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   WaitCtl* ctl = &sm.wait;
-  // CTA b: head group b % head_groups of range b / head_groups.
-  const int hg = blockIdx.x % p.head_groups;
+  // CTA b of a pair: head group b % 2 of range b / 2.
+  const int hg = PAIR ? blockIdx.x & 1 : 0;
   const int head0 = hg * p.group_heads;
   const int heads = min(p.group_heads, p.num_q_heads - head0);
 
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s)
+    for (int s = 0; s < STAGES; ++s)
       for (int i = 0; i < kParts; ++i) {
         mbar_init(&sm.kv_full[s][i], 1);
-        mbar_init(&sm.kv_empty[s][i], 1);
+        mbar_init(&sm.kv_empty[s][i], PAIR ? 2 : 1);
       }
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, 1);
@@ -423,34 +471,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&qmap);
     prefetch_tensormap(&kmap);
   }
-  if (!p.early_plan) grid_dependency_wait();
-  plan_range(p, sm, blockIdx.x / p.head_groups, gridDim.x / p.head_groups);
-  if (p.early_plan) grid_dependency_wait();
-  allow_dependent_launch();
-  const long long lo = sm.range_lo, hi = sm.range_hi;
-  // This CTA's piece records, written again by the pieces that it cuts.
-  if (p.merge && tid < 2) p.piece[(2 * blockIdx.x + tid) * kPieceWords] = 0;
-  if (lo >= hi) return;
   if (warp == kWarpS) {
     tmem_alloc(&sm.tmem_base, kTmemCols);
     tmem_relinquish();
   }
+  const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x, units = PAIR ? gridDim.x >> 1 : gridDim.x;
+  if (p.num_reqs <= kWarpReqs) {
+    if (warp == kWarpLoad) {
+      if (!p.early_plan) grid_dependency_wait();
+      plan_range<32>(p, sm.plan, unit, units, TILE);
+    }
+  } else {
+    if (!p.early_plan) grid_dependency_wait();
+    plan_range<kThreads>(p, sm.plan, unit, units, TILE);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm.tmem_base;
+  const uint32_t tmem = uniform(sm.tmem_base);
+  const Plan& pl = sm.plan;
+  const long long lo = pl.range_lo, hi = pl.range_hi, start_base = pl.start_base;
+  const int piece = pl.piece, start_req = pl.start_req;
+  const Req start = pl.start;
+  grid_dependency_wait();
+  allow_dependent_launch();
+  // This CTA's piece records, written again by the pieces that it cuts.
+  if (p.merge && tid < 2) p.piece[(2 * blockIdx.x + tid) * kPieceWords] = 0;
+  // The plan's room is the softmax warps' from here on; and the pair's barriers are
+  // ready before either CTA's copies or commits arrive on them.
+  __syncthreads();
+  if (PAIR) cluster_barrier();
 
-  if (warp == kWarpLoad) {
+  // Columns of the MMAs.  Their operands are to be in uniform registers, for which
+  // the issuing warps' control flow is uniform by construction (votes, reductions)
+  // and one thread guards nothing but the instructions: 24 cycles an MMA of the
+  // scores with 16 columns and 32 with 64, as shared memory allows, for 50 and more
+  // when a single thread runs the loop.
+  const int n_cols = ((p.group_heads * p.group_tokens + 15) / 16) * 16;
+  if (lo >= hi) {
+    // no work (nor for the pair's other CTA)
+  } else if (warp == kWarpLoad) {
     // =========================== copies ===================================
     int n_item = 0, t = 0;  // items and tiles so far
     int parts = 0;          // parts of tile t that were issued
     bool ok = true;
-    int r = sm.start_req;
-    long long base = sm.start_base;
-    const int piece = sm.piece;
+    int r = start_req;
+    long long base = start_base;
     const int oob_row = p.num_blocks * kBlockSize;
     const uint32_t q_bytes = (uint32_t)(kChunks * 128) * p.group_heads * p.group_tokens;
-    Req a = sm.start;
+    Req a = start;
     // The next request's raw fields, ahead of its turn.
     int f0 = a.q0 + a.qr, f1 = 0, fl = 0;
     while (ok && base < hi && r < p.num_reqs) {
@@ -479,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         it.nt = min(p.group_tokens, a.qr - g * p.group_tokens);
         it.pos0 = a.L - a.qr + g * p.group_tokens;
         it.vis = it.pos0 + it.nt;
-        const int tiles = cdiv(it.vis, kTile);
+        const int tiles = cdiv(it.vis, TILE);
         it.t0 = 0;
         it.t1 = tiles;
         if (piece > 0) {
@@ -490,55 +559,71 @@ __global__ void __launch_bounds__(kThreads, 1)
             it.t1 = (int)((long long)tiles * (x + 1) / n);
           }
         } else {
-          // Tile j belongs to the range that holds unit gbase + 64 j.
-          if (gbase < lo) it.t0 = (int)((lo - gbase + kTile - 1) / kTile);
-          if (hi - gbase < it.vis) it.t1 = (int)((hi - gbase + kTile - 1) / kTile);
+          // Tile j belongs to the range that holds unit gbase + TILE j.
+          if (gbase < lo) it.t0 = (int)((lo - gbase + TILE - 1) / TILE);
+          if (hi - gbase < it.vis) it.t1 = (int)((hi - gbase + TILE - 1) / TILE);
         }
         it.end = 0;
         if (it.t0 >= it.t1) continue;
         const int nbl = cdiv(it.vis, kBlockSize);
-        // Block ids 32 at a time (eight tiles).
+        // Block ids, a window of tiles at a time.
         auto ids = [&](int tile) {
           const int x = tile * kTileBlocks + lane;
           return x < nbl ? __ldg(bt + x) : INT_MIN;
         };
-        int cur = ids(it.t0), nxt = it.t0 + 8 < it.t1 ? ids(it.t0 + 8) : INT_MIN;
+        int cur = ids(it.t0), nxt = it.t0 + kWindow < it.t1 ? ids(it.t0 + kWindow) : INT_MIN;
+        // The item and its queries, ahead of its first keys.
+        if (n_item > 0) ok = wait_for(&sm.q_empty, (n_item - 1) & 1, p.err, ctl);
+        if (!ok) break;
+        if (elect_one()) {
+          sm.items[n_item % kItems] = it;
+          mbar_arrive(&sm.item_full[n_item % kItems]);
+          mbar_arrive_expect_tx(&sm.q_full, q_bytes);
+          #pragma unroll 1
+          for (int c = 0; c < kChunks; ++c) tma_load_3d(sm.q[c], &qmap, c * 64, head0, it.row0, &sm.q_full);
+        }
+        __syncwarp();
+        ++n_item;
         for (int j = it.t0; j < it.t1; ++j, ++t) {
-          const int k = (j - it.t0) & 7;
+          const int k = (j - it.t0) % kWindow;
           if (k == 0 && j > it.t0) {
             cur = nxt;
-            if (j + 8 < it.t1) nxt = ids(j + 8);
+            if (j + kWindow < it.t1) nxt = ids(j + kWindow);
           }
-          const int st = t % kStages;
-          // Lane b + 4 c copies block b of the part's chunk c; blocks past the
-          // last are read at a row outside the pool, which fills zeros.
-          const int id = __shfl_sync(0xffffffffu, cur, k * kTileBlocks + (lane & 3));
-          int row = oob_row;
-          if ((unsigned)id < (unsigned)p.num_blocks) row = id * kBlockSize;
-          else if (id != INT_MIN && lane < 4) record_error(p.err, kErrBounds);
+          const int st = t % STAGES;
+          // Blocks past the last are read at a row outside the pool, which fills
+          // zeros.  One thread issues all copies (a thread a copy, eight at a time,
+          // took 1.76 us a tile).
+          int rows[kTileBlocks];
+          #pragma unroll
+          for (int b = 0; b < kTileBlocks; ++b) {
+            const int id = uniform(__shfl_sync(0xffffffffu, cur, k * kTileBlocks + b));
+            rows[b] = oob_row;
+            if ((unsigned)id < (unsigned)p.num_blocks) rows[b] = id * kBlockSize;
+            else if (id != INT_MIN) record_error(p.err, kErrBounds);
+          }
           parts = 0;
           #pragma unroll 1
           for (int part = 0; part < kParts; ++part) {
-            if (j == it.t0 && part == 0) {
-              // The item and its queries, ahead of its first keys.
-              if (n_item > 0) ok = wait_for(&sm.q_empty, (n_item - 1) & 1, p.err, ctl);
-              if (!ok) break;
-              if (lane == 0) {
-                sm.items[n_item % kItems] = it;
-                mbar_arrive(&sm.item_full[n_item % kItems]);
-                mbar_arrive_expect_tx(&sm.q_full, q_bytes);
-              }
-              __syncwarp();
-              if (lane < kChunks) tma_load_3d(sm.q[lane], &qmap, lane * 64, head0, it.row0, &sm.q_full);
-              ++n_item;
-            }
-            if (t >= kStages) ok = wait_for(&sm.kv_empty[st][part], ((t / kStages) - 1) & 1, p.err, ctl);
+            if (t >= STAGES) ok = wait_for(&sm.kv_empty[st][part], ((t / STAGES) - 1) & 1, p.err, ctl);
             if (!ok) break;
-            const int n = part_chunks(part), c = 2 * part + (lane >> 2);
-            if (lane == 0) mbar_arrive_expect_tx(&sm.kv_full[st][part], (uint32_t)n * kChunkBytes);
+            if (elect_one()) {
+              const int n = part_chunks(part);
+              mbar_arrive_expect_tx(&sm.kv_full[st][part], (uint32_t)n * TILE * 128);
+              #pragma unroll 1
+              for (int c = 2 * part; c < 2 * part + n; ++c) {
+                #pragma unroll
+                for (int b = 0; b < kTileBlocks; ++b) {
+                  if (!PAIR) {
+                    tma_load_2d(sm.kv[st][c] + b * 2048, &kmap, c * 64, rows[b], &sm.kv_full[st][part]);
+                  } else if (((c * kTileBlocks + b) & 1) == hg) {
+                    // (every other copy is the other CTA's)
+                    tma_load_2d_pair(sm.kv[st][c] + b * 2048, &kmap, c * 64, rows[b], &sm.kv_full[st][part]);
+                  }
+                }
+              }
+            }
             __syncwarp();
-            if (lane < 4 * n)
-              tma_load_2d(sm.kv[st][c] + (lane & 3) * 2048, &kmap, c * 64, row, &sm.kv_full[st][part]);
             ++parts;
           }
           if (!ok) break;
@@ -564,99 +649,109 @@ __global__ void __launch_bounds__(kThreads, 1)
       #pragma unroll 1
       for (int part = 0; part < kParts; ++part) {
         const int n = t + (part < parts ? 1 : 0);  // tiles whose part was issued
-        for (int i = max(0, n - kStages); i < n; ++i)
-          mbar_wait_drain(&sm.kv_full[i % kStages][part], (i / kStages) & 1, p.err, ctl);
+        for (int i = max(0, n - STAGES); i < n; ++i)
+          mbar_wait_drain(&sm.kv_full[i % STAGES][part], (i / STAGES) & 1, p.err, ctl);
       }
       if (n_item > 0) mbar_wait_drain(&sm.q_full, (n_item - 1) & 1, p.err, ctl);
     }
   } else if (warp == kWarpS) {
     // ========================= MMAs of the scores =========================
     // As soon as a tile's chunks land.  The buffer of S(t) was read by the softmax
-    // before the PV of tile t - 2, whose end tile t's latents waited for.  Loops
-    // stay rolled but for the four MMAs of a chunk.
-    const int n_cols = ((p.group_heads * p.group_tokens + 15) / 16) * 16;
-    const uint32_t idesc = idesc_bf16_f32(kTile, n_cols, 0, 0);
+    // before the PV of tile t - 2, whose end tile t's latents waited for.
+    const uint32_t idesc = idesc_bf16_f32(kMmaKeys, n_cols, 0, 0);
     const uint64_t desc_k = smem_desc_sw128(smem_u32(sm.kv[0][0]), 16, 1024);
     const uint64_t desc_q = smem_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
+    const bool leader = elect_one();
     bool ok = true;
-    for (int n_item = 0, t = 0; ok; ++n_item) {
-      ok = wait_for(&sm.q_full, n_item & 1, p.err, ctl);
+    int st = 0, phase = 0, b = 0;
+    for (int n_item = 0;; ++n_item) {
+      ok = all_of(wait_for(&sm.q_full, n_item & 1, p.err, ctl));
       if (!ok) break;
       const Item& it = sm.items[n_item % kItems];
-      if (it.end) break;
-      for (int left = it.t1 - it.t0; left > 0 && ok; --left, ++t) {
-        const int st = t % kStages;
-        #pragma unroll 1
-        for (int c = 0; c < kChunks; ++c) {
-          if ((c & 1) == 0) {
-            ok = wait_for(&sm.kv_full[st][c >> 1], (t / kStages) & 1, p.err, ctl);
-            if (!ok) break;
-            tc_fence_after();
-          }
-          if (elect_one()) {
-            const uint64_t da = desc_k + (uint64_t)((st * kChunks + c) * kStep);
-            const uint64_t db = desc_q + (uint64_t)(c * kStep);
+      if (uniform(it.end)) break;
+      #pragma unroll 1
+      for (int left = uniform(it.t1 - it.t0); left > 0; --left) {
+        const uint64_t da = desc_k + (uint64_t)(st * (kChunks * kKvStep));
+        #pragma unroll
+        for (int part = 0; part < kParts; ++part) {
+          ok = all_of(wait_for(&sm.kv_full[st][part], phase, p.err, ctl));
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
             #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc_mma_f16_ss(tmem + (t & 1) * kLatMaxRows, da + 2 * kk, db + 2 * kk, idesc, c > 0 || kk > 0);
+            for (int kk = 0; kk < (part == kParts - 1 ? 4 : 8); ++kk) {
+              const int c = 2 * part + (kk >> 2);
+              tc_mma_f16_ss(tmem + b * kLatMaxRows, da + (c * kKvStep + 2 * (kk & 3)),
+                            desc_q + (c * kQStep + 2 * (kk & 3)), idesc, part > 0 || kk > 0);
+            }
           }
           __syncwarp();
         }
-        if (ok && elect_one()) {
-          tc_commit(&sm.s_full[t & 1]);
-          tc_commit(&sm.kv_empty[st][kParts - 1]);
+        if (!ok) break;
+        if (leader) {
+          tc_commit(&sm.s_full[b]);
+          PAIR ? tc_commit_pair(&sm.kv_empty[st][kParts - 1]) : tc_commit(&sm.kv_empty[st][kParts - 1]);
           if (left == 1) tc_commit(&sm.q_empty);
         }
         __syncwarp();
+        b ^= 1;
+        if (++st == STAGES) st = 0, phase ^= 1;
       }
+      if (!ok) break;
     }
     if (!ok) {
       // Aborted: the issued MMAs must end before TMEM is freed.
-      if (elect_one()) tc_commit(&sm.drained[0]);
+      if (leader) tc_commit(&sm.drained[0]);
       __syncwarp();
       mbar_wait_drain(&sm.drained[0], 0, p.err, ctl);
     }
   } else if (warp == kWarpO) {
     // ========================= MMAs of the outputs ========================
-    const int n_cols = ((p.group_heads * p.group_tokens + 15) / 16) * 16;
     const uint32_t idesc = idesc_bf16_f32(128, n_cols, 1, 0);
-    // C^T: MN-major atoms of 64 dims x 8 keys, the chunks kChunkBytes apart.
-    const uint64_t desc_v = smem_desc_sw128(smem_u32(sm.kv[0][0]), kChunkBytes, 1024);
+    // C^T: MN-major atoms of 64 dims x 8 keys, the chunks TILE * 128 bytes apart.
+    const uint64_t desc_v = smem_desc_sw128(smem_u32(sm.kv[0][0]), TILE * 128, 1024);
     const uint64_t desc_p = smem_desc_sw128(smem_u32(sm.p), 16, 1024);
+    const bool leader = elect_one();
     bool ok = true;
-    for (int n_item = 0, t = 0; ok; ++n_item) {
-      ok = wait_for(&sm.item_full[n_item % kItems], (n_item / kItems) & 1, p.err, ctl);
+    int st = 0, phase = 0, p_phase = 0;
+    for (int n_item = 0;; ++n_item) {
+      ok = all_of(wait_for(&sm.item_full[n_item % kItems], (n_item / kItems) & 1, p.err, ctl));
       if (!ok) break;
       const Item& it = sm.items[n_item % kItems];
-      if (it.end) break;
-      const int n = it.t1 - it.t0;
-      for (int j = 0; j < n; ++j, ++t) {
-        const int st = t % kStages;
-        ok = wait_for(&sm.p_full, t & 1, p.err, ctl);
-        if (ok && j == 0 && n_item > 0) ok = wait_for(&sm.o_empty, (n_item - 1) & 1, p.err, ctl);
+      if (uniform(it.end)) break;
+      const int n = uniform(it.t1 - it.t0);
+      #pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        // The tile landed long since, the scores came from it.
+        #pragma unroll 1
+        for (int m = 0; m < 4; ++m) ok = ok && wait_for(&sm.kv_full[st][m], phase, p.err, ctl);
+        ok = ok && wait_for(&sm.p_full, p_phase, p.err, ctl);
+        if (j == 0 && n_item > 0) ok = ok && wait_for(&sm.o_empty, (n_item - 1) & 1, p.err, ctl);
+        ok = all_of(ok);
         if (!ok) break;
         tc_fence_after();
-        if (elect_one()) {
-          #pragma unroll 1
+        if (leader) {
+          const uint64_t da = desc_v + (uint64_t)(st * (kChunks * kKvStep));
+          #pragma unroll
           for (int m = 0; m < 4; ++m) {
-            // (landed long since: the scores came from it)
-            if (!wait_for(&sm.kv_full[st][m], (t / kStages) & 1, p.err, ctl)) break;
-            const uint64_t da = desc_v + (uint64_t)((st * kChunks + 2 * m) * kStep);
             #pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-              tc_mma_f16_ss(tmem + kColO + m * kLatMaxRows, da + kk * (2048 >> 4), desc_p + 2 * kk, idesc,
-                            j > 0 || kk > 0);
-            tc_commit(&sm.kv_empty[st][m]);
+            for (int kk = 0; kk < TILE / 16; ++kk)
+              tc_mma_f16_ss(tmem + kColO + m * kLatMaxRows, da + (2 * m * kKvStep + kk * (2048 >> 4)),
+                            desc_p + 2 * kk, idesc, j > 0 || kk > 0);
+            PAIR ? tc_commit_pair(&sm.kv_empty[st][m]) : tc_commit(&sm.kv_empty[st][m]);
           }
           tc_commit(&sm.p_free);
           if (j == n - 1) tc_commit(&sm.o_full);
         }
         __syncwarp();
+        p_phase ^= 1;
+        if (++st == STAGES) st = 0, phase ^= 1;
       }
+      if (!ok) break;
     }
     if (!ok) {
       // Aborted: the issued MMAs must end before TMEM is freed.
-      if (elect_one()) tc_commit(&sm.drained[1]);
+      if (leader) tc_commit(&sm.drained[1]);
       __syncwarp();
       mbar_wait_drain(&sm.drained[1], 0, p.err, ctl);
     }
@@ -670,6 +765,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // 16 quad + lane / 4 + 8 h.
     const int col0 = wg * 16 + 2 * (lane & 3);
     const int key_lo = quad * 16 + (lane >> 2);
+    // (rows of the MMA past the tile's keys are scores of nothing)
+    const bool in_tile = quad * 16 < TILE;
     int tok[4];  // query token of each column; -1: none
     #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -696,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       #pragma unroll
       for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.f;
       for (int j = it.t0; j < it.t1; ++j, ++t) {
-        const int key0 = j * kTile;
+        const int key0 = j * TILE;
         ok = ok && wait_for(&sm.s_full[t & 1], (t >> 1) & 1, p.err, ctl);
         tc_fence_after();
         uint32_t w[4];
@@ -712,8 +809,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             float& b = v[4 * (i >> 1) + 2 + (i & 1)];
             a *= p.scale_log2;
             b *= p.scale_log2;
-            if (key0 + key_lo > limit[i]) a = -INFINITY;
-            if (key0 + key_lo + 8 > limit[i]) b = -INFINITY;
+            if (!in_tile || key0 + key_lo > limit[i]) a = -INFINITY;
+            if (!in_tile || key0 + key_lo + 8 > limit[i]) b = -INFINITY;
             mx[i] = fmaxf(a, b);
           }
           bool grow = j == it.t0;
@@ -775,12 +872,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             add_bf16x2(l[2 * c], l[2 * c + 1], w[2 * c + 1]);
           }
         }
-        if (key0 + kTile > it.pos0 + 1) {
+        if (key0 + TILE > it.pos0 + 1) {
           // (landed long since: the scores came from them)
           #pragma unroll 1
           for (int part = 0; part < kParts - 1; ++part)
-            ok = ok && wait_for(&sm.kv_full[t % kStages][part], (t / kStages) & 1, p.err, ctl);
-          clean_tile(sm, sm.kv[t % kStages], key0, it.pos0, it.vis, bad, warp, lane);
+            ok = ok && wait_for(&sm.kv_full[t % STAGES][part], (t / STAGES) & 1, p.err, ctl);
+          clean_tile<TILE>(sm.kv[t % STAGES], key0, it.pos0, it.vis, bad, warp, lane);
         }
         // P's buffer is free once the product before has read it.
         if (t > 0) ok = ok && wait_for(&sm.p_free, (t - 1) & 1, p.err, ctl);
@@ -793,7 +890,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&sm.p_full);
       }
       // ---- epilogue ---------------------------------------------------------
-      const int n_tiles = cdiv(it.vis, kTile);
+      const int n_tiles = cdiv(it.vis, TILE);
       const bool whole = it.t0 == 0 && it.t1 == n_tiles;
       const int slot = 2 * blockIdx.x + (it.t0 == 0 ? 1 : 0);
       // Columns in use: rows (token, head) of out from the first on, in order
@@ -880,74 +977,100 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == kWarpS) tmem_dealloc(tmem, kTmemCols);
+  // A CTA's memory and barriers outlive the copies and commits of the other.
+  if (PAIR) cluster_barrier();
 }
 
-// Joins the pieces of rows that were cut.  Block (b, y): the row whose first
-// piece CTA b's last slot holds, if any; its later pieces are the first slots of
-// the next CTAs of the same head group.  A warp a (token, head) row, 16 dims a
-// lane.
+// Joins the pieces of rows that were cut.  Block (b, y): eight columns of the item
+// whose first piece is in CTA b's last slot, if any; its later pieces are in the
+// first slots of the next CTAs of the same head group.  A warp a column, 16 dims a
+// lane; flags and statistics of up to 32 pieces are read at once, a lane each, and
+// the loads of the outputs depend on nothing but them.
 constexpr int kMergeWarps = 8;
 
 __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const LatentDecodeParams p, int grid) {
   grid_dependency_wait();
   allow_dependent_launch();
-  const int cta = blockIdx.x, lane = threadIdx.x & 31;
-  const int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
-  const int* rec = p.piece + (2 * cta + 1) * kPieceWords;
-  if (rec[0] == 0) return;  // CTA cta cut nothing that begins with it
-  if (row >= rec[2]) return;
-  // (the item's columns are rows of out, in order)
-  const long long out_row = (long long)rec[1] * p.num_q_heads + (cta % p.head_groups) * p.group_heads + row;
-  // The running state over the pieces in order.
+  const int cta = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = blockIdx.y * kMergeWarps + warp;
+  const int4 rec = *reinterpret_cast<const int4*>(p.piece + (2 * cta + 1) * kPieceWords);
   float m = -INFINITY, l = 0.f;
   float4 o[4];
   #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = cta, slot = 2 * cta + 1;;) {
-    const int flags = p.piece[slot * kPieceWords];
-    if (flags == 0) break;  // (a piece that an aborted CTA did not write)
-    const float2 ml = *reinterpret_cast<const float2*>(p.piece_ml + ((long long)slot * p.piece_rows + row) * 2);
-    const float top = fmaxf(m, ml.x);
-    const float a = m == -INFINITY ? 0.f : fast_exp2(m - top);
-    const float b = ml.x == -INFINITY && ml.y == 0.f ? 0.f : fast_exp2(ml.x - top);
-    const float4* src = reinterpret_cast<const float4*>(p.piece_o + ((long long)slot * p.piece_rows + row) * kLatent);
-    l = l * a + ml.y * b;
-    #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = src[i * 32 + lane];
-      o[i].x = o[i].x * a + v.x * b;
-      o[i].y = o[i].y * a + v.y * b;
-      o[i].z = o[i].z * a + v.z * b;
-      o[i].w = o[i].w * a + v.w * b;
+  for (int k = 0; k < 4; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  bool last = false;
+  for (int first = 0; !last; first += 32) {
+    // Lane i: piece first + i.
+    const int c = cta + (first + lane) * p.head_groups;
+    const int slot = first + lane == 0 ? 2 * cta + 1 : 2 * c;
+    int flags = 0;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (c < grid && row < p.piece_rows) {
+      flags = p.piece[slot * kPieceWords];
+      ml = *reinterpret_cast<const float2*>(p.piece_ml + ((long long)slot * p.piece_rows + row) * 2);
     }
+    if (rec.x == 0 || row >= rec.z) return;  // CTA cta cut nothing that begins with it
+    const unsigned ends = __ballot_sync(0xffffffffu, (flags & kPieceLast) != 0);
+    // (a record that is missing, of an aborted CTA, ends the item as well)
+    const unsigned holes = __ballot_sync(0xffffffffu, flags == 0);
+    int n = 32;
+    if (ends) n = min(n, __ffs(ends));
+    if (holes) n = min(n, __ffs(holes) - 1);
+    last = n < 32 || ends != 0;
+    float top = lane < n ? ml.x : -INFINITY;
+    #pragma unroll
+    for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+    top = fmaxf(top, m);
+    const float keep = m == -INFINITY ? 0.f : fast_exp2(m - top);
+    // (a piece of which the row saw no key weighs nothing)
+    const float w = lane < n && !(ml.x == -INFINITY && ml.y == 0.f) ? fast_exp2(ml.x - top) : 0.f;
+    float sum = lane < n ? ml.y * w : 0.f;
+    #pragma unroll
+    for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+    l = l * keep + sum;
+    #pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = make_float4(o[k].x * keep, o[k].y * keep, o[k].z * keep, o[k].w * keep);
     m = top;
-    if (flags & kPieceLast) break;
-    c += p.head_groups;
-    if (c >= grid) break;
-    slot = 2 * c;
+    #pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const int si = __shfl_sync(0xffffffffu, slot, i);
+      const float4* src = reinterpret_cast<const float4*>(p.piece_o + ((long long)si * p.piece_rows + row) * kLatent);
+      #pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 v = src[k * 32 + lane];
+        o[k].x += v.x * wi;
+        o[k].y += v.y * wi;
+        o[k].z += v.z * wi;
+        o[k].w += v.w * wi;
+      }
+    }
   }
-  __nv_bfloat16* dst = p.out + out_row * kLatent;
+  // (the item's columns are rows of out, in order)
+  const long long out_row = (long long)rec.y * p.num_q_heads + (cta % p.head_groups) * p.group_heads + row;
   const float inv = 1.f / l;
   #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int k = 0; k < 4; ++k) {
     uint2 v;
-    v.x = pack_bf16(o[i].x * inv, o[i].y * inv);
-    v.y = pack_bf16(o[i].z * inv, o[i].w * inv);
-    *reinterpret_cast<uint2*>(dst + (i * 32 + lane) * 4) = v;
+    v.x = pack_bf16(o[k].x * inv, o[k].y * inv);
+    v.y = pack_bf16(o[k].z * inv, o[k].w * inv);
+    reinterpret_cast<uint2*>(p.out + out_row * kLatent)[k * 32 + lane] = v;
   }
 }
 
-}  // namespace
-
-cudaError_t launch_latent_decode(const LatentDecodeLaunch& L, cudaStream_t stream) {
-  const size_t smem = sizeof(Smem) + 1024;
+template <int COLS, int TILE, int STAGES, bool PAIR>
+cudaError_t launch_decode(const LatentDecodeLaunch& L, cudaStream_t stream) {
+  using Smem = SmemT<COLS, TILE, STAGES>;
+  constexpr size_t smem = sizeof(Smem) + 1024;
+  static_assert(smem <= 227 * 1024, "latent decode shared memory");
   static unsigned long long configured = 0;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & bit)) {
-    e = cudaFuncSetAttribute(latent_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(latent_decode_kernel<COLS, TILE, STAGES, PAIR>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     __atomic_fetch_or(&configured, bit, __ATOMIC_RELEASE);
   }
@@ -956,18 +1079,37 @@ cudaError_t launch_latent_decode(const LatentDecodeLaunch& L, cudaStream_t strea
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = L.p.pdl ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, latent_decode_kernel, L.qmap, L.kmap, L.p);
-  if (e != cudaSuccess || !L.p.merge) return e != cudaSuccess ? e : cudaGetLastError();
+  cfg.numAttrs = PAIR ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, latent_decode_kernel<COLS, TILE, STAGES, PAIR>, L.qmap, L.kmap, L.p);
+}
+
+}  // namespace
+
+cudaError_t launch_latent_decode(const LatentDecodeLaunch& L, cudaStream_t stream) {
+  // Up to 48 columns leave room for three tiles of 48 keys.
   const int rows = L.p.group_heads * L.p.group_tokens;
-  cfg.gridDim = dim3(L.grid, (rows + kMergeWarps - 1) / kMergeWarps);
-  cfg.blockDim = dim3(32 * kMergeWarps);
-  cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, latent_merge_kernel, L.p, L.grid);
+  const bool pair = L.p.head_groups == 2;
+  cudaError_t e = rows <= 48 ? (pair ? launch_decode<48, 48, 3, true>(L, stream) : launch_decode<48, 48, 3, false>(L, stream))
+                             : (pair ? launch_decode<64, 64, 2, true>(L, stream) : launch_decode<64, 64, 2, false>(L, stream));
+  if (e == cudaSuccess && L.p.merge) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(L.grid, (rows + kMergeWarps - 1) / kMergeWarps);
+    cfg.blockDim = dim3(32 * kMergeWarps);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = L.p.pdl ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, latent_merge_kernel, L.p, L.grid);
+  }
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

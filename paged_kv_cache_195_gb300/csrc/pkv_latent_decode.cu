@@ -89,19 +89,18 @@ struct Req {
   int ng;  // token groups (0: nothing to do)
 };
 
-__device__ __forceinline__ Req make_req(const LatentDecodeParams& p, int q0, int q1, int L,
-                                        bool* bad) {
+// (ng < 0: the fields do not fit together or the step)
+__device__ __forceinline__ Req make_req(const LatentDecodeParams& p, int q0, int q1, int L) {
   Req a{q0, q1 - q0, L, 0};
   const bool ok = q0 >= 0 && q1 >= q0 && q1 <= p.num_q_tokens && a.qr <= L &&
                   L <= p.max_blocks * kBlockSize;
-  if (ok && a.qr > 0) a.ng = cdiv(a.qr, p.group_tokens);
-  *bad = !ok;
+  if (!ok) a.ng = -1;
+  else if (a.qr > 0) a.ng = p.group_tokens == 1 ? a.qr : cdiv(a.qr, p.group_tokens);
   return a;
 }
 
 __device__ __forceinline__ Req load_req(const LatentDecodeParams& p, int r) {
-  bool bad;
-  return make_req(p, __ldg(p.qsl + r), __ldg(p.qsl + r + 1), __ldg(p.seq_lens + r), &bad);
+  return make_req(p, __ldg(p.qsl + r), __ldg(p.qsl + r + 1), __ldg(p.seq_lens + r));
 }
 
 // The CTA's part of the plan: its range of units, the request that it starts in and
@@ -143,7 +142,7 @@ __device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xfffff
 __device__ __forceinline__ bool all_of(bool v) { return __all_sync(0xffffffffu, v); }
 
 // Part i's chunks: 2 i and 2 i + 1, of the last part the one with the rotated keys.
-__device__ __forceinline__ int part_chunks(int part) { return part == kParts - 1 ? 1 : 2; }
+__host__ __device__ constexpr int part_chunks(int part) { return part == kParts - 1 ? 1 : 2; }
 
 // The unit that the work is cut in.  Many items: keys, and item_cost more an item;
 // every CTA takes an equal range, whatever items it holds.  Few (`piece` > 0):
@@ -156,14 +155,18 @@ __device__ __forceinline__ int group_keys(const LatentDecodeParams& p, const Req
 }
 
 __device__ __forceinline__ long long groups_keys(const LatentDecodeParams& p, const Req& a, int i) {
+  if (i <= 0) return 0;
+  if (a.ng == 1) return a.L;
   const long long n = i;
   long long w = n * ((long long)a.L - a.qr) + (long long)p.group_tokens * (n * (n + 1) / 2);
-  if (i == a.ng && i > 0) w -= (long long)a.ng * p.group_tokens - a.qr;
+  if (i == a.ng) w -= (long long)a.ng * p.group_tokens - a.qr;
   return w;
 }
 
-static __device__ __noinline__ long long groups_units(const LatentDecodeParams& p, const Req& a, int i, int piece) {
+__device__ __forceinline__ long long groups_units(const LatentDecodeParams& p, const Req& a, int i, int piece) {
+  if (i <= 0) return 0;
   if (piece == 0) return groups_keys(p, a, i) + (long long)i * p.item_cost;
+  if (a.ng == 1) return (a.L - 1) / piece + 1;
   long long w = 0;
   #pragma unroll 1
   for (int m = 0; m < i; ++m) w += (group_keys(p, a, m) - 1) / piece + 1;
@@ -204,27 +207,54 @@ __device__ __forceinline__ long long scan(Plan& pl, long long mine, int count, l
   return before + incl - mine;
 }
 
-// Unit `unit` of `units` CTAs' (or pairs') share.  THREADS threads: one warp for
-// steps of up to kWarpReqs requests, beside which the rest of the CTA is set up, else
-// the block (which then needs a __syncthreads before it reads the result).
-constexpr int kWarpReqs = 256;
+// a / b for a >= 0, b > 0: in 32 bits whenever both fit.
+__device__ __forceinline__ long long div_ll(long long a, long long b) {
+  if ((unsigned long long)(a | b) <= 0xffffffffull) return (unsigned)a / (unsigned)b;
+  return a / b;
+}
 
-template <int THREADS>
+// Unit `unit` of `units` CTAs' (or pairs') share.  THREADS threads with up to PER
+// requests each in registers: one warp for steps of up to kWarpReqs requests, beside
+// which the rest of the CTA is set up, else the block (which then needs a
+// __syncthreads before it reads the result), PER = 0: any number, read again.
+constexpr int kWarpPer = 4;
+constexpr int kWarpReqs = 32 * kWarpPer;
+
+template <int THREADS, int PER>
 static __device__ __noinline__ void plan_range(const LatentDecodeParams& p, Plan& pl, int unit, int units, int tile) {
   const int tid = THREADS == 32 ? threadIdx.x & 31 : threadIdx.x;
   const int per = cdiv(p.num_reqs, THREADS);
   const int r0 = min(tid * per, p.num_reqs), r1 = min(r0 + per, p.num_reqs);
+  Req held[PER > 0 ? PER : 1];
+  // f(request, its number) of this thread's requests, until it returns false.
+  auto each = [&](auto f) {
+    if constexpr (PER > 0) {
+      #pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (r0 + i < r1 && !f(held[i], r0 + i)) break;
+    } else {
+      #pragma unroll 1
+      for (int r = r0; r < r1; ++r)
+        if (!f(load_req(p, r), r)) break;
+    }
+  };
+  if constexpr (PER > 0) {
+    int f[PER + 1], n[PER];
+    #pragma unroll
+    for (int i = 0; i <= PER; ++i) f[i] = r0 + i <= p.num_reqs ? __ldg(p.qsl + r0 + i) : 0;
+    #pragma unroll
+    for (int i = 0; i < PER; ++i) n[i] = r0 + i < p.num_reqs ? __ldg(p.seq_lens + r0 + i) : 0;
+    #pragma unroll
+    for (int i = 0; i < PER; ++i) held[i] = make_req(p, f[i], f[i + 1], n[i]);
+  }
   long long keys = 0;
   int items = 0;
-  Req a;
-  #pragma unroll 1
-  for (int r = r0; r < r1; ++r) {
-    bool bad;
-    a = make_req(p, __ldg(p.qsl + r), __ldg(p.qsl + r + 1), __ldg(p.seq_lens + r), &bad);
-    if (bad && blockIdx.x == 0) record_error(p.err, kErrBounds);  // the request is skipped
+  each([&](const Req& a, int) {
+    if (a.ng < 0 && blockIdx.x == 0) record_error(p.err, kErrBounds);  // the request is skipped
     keys += groups_keys(p, a, a.ng);
-    items += a.ng;
-  }
+    items += max(a.ng, 0);
+    return true;
+  });
   int piece = INT_MAX, all_items;
   long long total, mine = items, excl, lo, hi;
   if (p.merge) {
@@ -234,14 +264,13 @@ static __device__ __noinline__ void plan_range(const LatentDecodeParams& p, Plan
     if (3ll * all_items <= 2 * units) {
       // ceil(keys / piece) summed over the items is at most their keys / piece + all_items.
       const long long all_keys = total - (long long)all_items * p.item_cost, room = units - all_items;
-      const long long least = ((all_keys + room - 1) / room + tile - 1) / tile * tile;
+      const long long least = (div_ll(all_keys + room - 1, room) + tile - 1) / tile * tile;
       piece = (int)min(max(least, (long long)p.min_keys), 1ll << 30);
       mine = 0;
-      #pragma unroll 1
-      for (int r = r0; r < r1; ++r) {
-        if (per > 1) a = load_req(p, r);
+      each([&](const Req& a, int) {
         mine += groups_units(p, a, a.ng, piece);
-      }
+        return true;
+      });
       if (THREADS > 32) __syncthreads();  // pl.part is free again
     }
   }
@@ -250,7 +279,7 @@ static __device__ __noinline__ void plan_range(const LatentDecodeParams& p, Plan
     lo = min((long long)unit, total);
     hi = min(lo + 1, total);
   } else {
-    const long long chunk = max((total + units - 1) / units, (long long)p.min_keys);
+    const long long chunk = max(div_ll(total + units - 1, units), (long long)p.min_keys);
     lo = min(unit * chunk, total);
     hi = min(lo + chunk, total);
   }
@@ -261,18 +290,17 @@ static __device__ __noinline__ void plan_range(const LatentDecodeParams& p, Plan
   }
   if (lo < hi && excl <= lo && lo < excl + mine) {
     long long base = excl;
-    #pragma unroll 1
-    for (int r = r0; r < r1; ++r) {
-      if (per > 1) a = load_req(p, r);
+    each([&](const Req& a, int r) {
       const long long w = groups_units(p, a, a.ng, piece);
-      if (lo < base + w) {
-        pl.start_req = r;
-        pl.start = a;
-        pl.start_base = base;
-        break;
+      if (lo >= base + w) {
+        base += w;
+        return true;
       }
-      base += w;
-    }
+      pl.start_req = r;
+      pl.start = a;
+      pl.start_base = base;
+      return false;
+    });
   }
 }
 
@@ -479,11 +507,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (p.num_reqs <= kWarpReqs) {
     if (warp == kWarpLoad) {
       if (!p.early_plan) grid_dependency_wait();
-      plan_range<32>(p, sm.plan, unit, units, TILE);
+      plan_range<32, kWarpPer>(p, sm.plan, unit, units, TILE);
     }
   } else {
     if (!p.early_plan) grid_dependency_wait();
-    plan_range<kThreads>(p, sm.plan, unit, units, TILE);
+    plan_range<kThreads, 0>(p, sm.plan, unit, units, TILE);
   }
   tc_fence_before();
   __syncthreads();
@@ -512,8 +540,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // no work (nor for the pair's other CTA)
   } else if (warp == kWarpLoad) {
     // =========================== copies ===================================
-    int n_item = 0, t = 0;  // items and tiles so far
-    int parts = 0;          // parts of tile t that were issued
+    // One thread issues all copies, from uniform registers (a thread a copy, eight
+    // at a time, took 1.76 us a tile of 36).
+    const bool leader = elect_one();
+    int n_item = 0, t = 0;     // items and tiles so far
+    int st = 0, phase = 1;     // the tile's stage and the parity that it waits for (the first ones pass)
+    int parts = 0;             // parts of tile t that were issued
     bool ok = true;
     int r = start_req;
     long long base = start_base;
@@ -527,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         f1 = __ldg(p.qsl + r + 2);
         fl = __ldg(p.seq_lens + r + 1);
       }
-      const long long w = a.ng > 0 ? groups_units(p, a, a.ng, piece) : 0;
+      const long long w = groups_units(p, a, a.ng, piece);
       // First token group that the range reaches.
       int g = 0;
       if (base < lo) {
@@ -566,16 +598,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         it.end = 0;
         if (it.t0 >= it.t1) continue;
         const int nbl = cdiv(it.vis, kBlockSize);
-        // Block ids, a window of tiles at a time.
-        auto ids = [&](int tile) {
+        // The rows of the pool that blocks begin at, a window of tiles at a time, a
+        // lane each.  Blocks past the last are read at a row outside the pool,
+        // which fills zeros.
+        auto block_rows = [&](int tile) {
           const int x = tile * kTileBlocks + lane;
-          return x < nbl ? __ldg(bt + x) : INT_MIN;
+          int row = oob_row;
+          if (x < nbl && lane < kWindow * kTileBlocks) {
+            const int id = __ldg(bt + x);
+            if ((unsigned)id < (unsigned)p.num_blocks) row = id * kBlockSize;
+            else record_error(p.err, kErrBounds);
+          }
+          return row;
         };
-        int cur = ids(it.t0), nxt = it.t0 + kWindow < it.t1 ? ids(it.t0 + kWindow) : INT_MIN;
+        int cur = block_rows(it.t0);
         // The item and its queries, ahead of its first keys.
-        if (n_item > 0) ok = wait_for(&sm.q_empty, (n_item - 1) & 1, p.err, ctl);
+        if (n_item > 0) ok = all_of(wait_for(&sm.q_empty, (n_item - 1) & 1, p.err, ctl));
         if (!ok) break;
-        if (elect_one()) {
+        if (leader) {
           sm.items[n_item % kItems] = it;
           mbar_arrive(&sm.item_full[n_item % kItems]);
           mbar_arrive_expect_tx(&sm.q_full, q_bytes);
@@ -584,56 +624,52 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         ++n_item;
-        for (int j = it.t0; j < it.t1; ++j, ++t) {
-          const int k = (j - it.t0) % kWindow;
-          if (k == 0 && j > it.t0) {
-            cur = nxt;
-            if (j + kWindow < it.t1) nxt = ids(j + kWindow);
-          }
-          const int st = t % STAGES;
-          // Blocks past the last are read at a row outside the pool, which fills
-          // zeros.  One thread issues all copies (a thread a copy, eight at a time,
-          // took 1.76 us a tile).
+        int nxt = oob_row;
+        int k = 0;  // lane of the tile's first block
+        int j = uniform(it.t0);
+        const int j1 = uniform(it.t1);
+        #pragma unroll 1
+        for (; j < j1; ++j) {
+          if (k == 0 && j + kWindow < j1) nxt = block_rows(j + kWindow);
           int rows[kTileBlocks];
           #pragma unroll
-          for (int b = 0; b < kTileBlocks; ++b) {
-            const int id = uniform(__shfl_sync(0xffffffffu, cur, k * kTileBlocks + b));
-            rows[b] = oob_row;
-            if ((unsigned)id < (unsigned)p.num_blocks) rows[b] = id * kBlockSize;
-            else if (id != INT_MIN) record_error(p.err, kErrBounds);
+          for (int b = 0; b < kTileBlocks; ++b) rows[b] = uniform(__shfl_sync(0xffffffffu, cur, k + b));
+          k += kTileBlocks;
+          if (k == kWindow * kTileBlocks) {
+            k = 0;
+            cur = nxt;
           }
-          parts = 0;
-          #pragma unroll 1
+          #pragma unroll
           for (int part = 0; part < kParts; ++part) {
-            if (t >= STAGES) ok = wait_for(&sm.kv_empty[st][part], ((t / STAGES) - 1) & 1, p.err, ctl);
+            ok = all_of(wait_for(&sm.kv_empty[st][part], phase, p.err, ctl));
             if (!ok) break;
-            if (elect_one()) {
-              const int n = part_chunks(part);
-              mbar_arrive_expect_tx(&sm.kv_full[st][part], (uint32_t)n * TILE * 128);
-              #pragma unroll 1
-              for (int c = 2 * part; c < 2 * part + n; ++c) {
+            if (leader) {
+              uint64_t* const bar = &sm.kv_full[st][part];
+              mbar_arrive_expect_tx(bar, (uint32_t)part_chunks(part) * TILE * 128);
+              #pragma unroll
+              for (int i = 0; i < part_chunks(part); ++i) {
+                const int c = 2 * part + i;
                 #pragma unroll
                 for (int b = 0; b < kTileBlocks; ++b) {
-                  if (!PAIR) {
-                    tma_load_2d(sm.kv[st][c] + b * 2048, &kmap, c * 64, rows[b], &sm.kv_full[st][part]);
-                  } else if (((c * kTileBlocks + b) & 1) == hg) {
-                    // (every other copy is the other CTA's)
-                    tma_load_2d_pair(sm.kv[st][c] + b * 2048, &kmap, c * 64, rows[b], &sm.kv_full[st][part]);
-                  }
+                  if (!PAIR) tma_load_2d(sm.kv[st][c] + b * 2048, &kmap, c * 64, rows[b], bar);
+                  // (every other copy is the other CTA's)
+                  else if (((c * kTileBlocks + b) & 1) == hg)
+                    tma_load_2d_pair(sm.kv[st][c] + b * 2048, &kmap, c * 64, rows[b], bar);
                 }
               }
             }
             __syncwarp();
-            ++parts;
+            parts = part + 1;
           }
           if (!ok) break;
           parts = 0;
+          ++t;
+          if (++st == STAGES) st = 0, phase ^= 1;
         }
       }
       base += w;
       ++r;
-      bool bad;
-      a = make_req(p, f0, f1, fl, &bad);
+      a = make_req(p, f0, f1, fl);
       f0 = f1;
     }
     // End marker, for the MMA warp (behind its last item) and the softmax warps.
@@ -983,21 +1019,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the pieces of rows that were cut.  Block (b, y): eight columns of the item
 // whose first piece is in CTA b's last slot, if any; its later pieces are in the
-// first slots of the next CTAs of the same head group.  A warp a column, 16 dims a
-// lane; flags and statistics of up to 32 pieces are read at once, a lane each, and
-// the loads of the outputs depend on nothing but them.
+// first slots of the next CTAs of the same head group.  SPLIT warps a column, 16 /
+// SPLIT dims a lane (few columns have many pieces, and few warps else); flags and
+// statistics of up to 32 pieces are read at once, a lane each, and the loads of the
+// outputs depend on nothing but them.
 constexpr int kMergeWarps = 8;
 
+template <int SPLIT>
 __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const LatentDecodeParams p, int grid) {
   grid_dependency_wait();
   allow_dependent_launch();
   const int cta = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row = blockIdx.y * kMergeWarps + warp;
+  constexpr int kVecs = 4 / SPLIT;  // of four dims, a lane
+  const int row = (blockIdx.y * kMergeWarps + warp) / SPLIT, at = warp % SPLIT * kVecs * 32 + lane;
   const int4 rec = *reinterpret_cast<const int4*>(p.piece + (2 * cta + 1) * kPieceWords);
   float m = -INFINITY, l = 0.f;
-  float4 o[4];
+  float4 o[kVecs];
   #pragma unroll
-  for (int k = 0; k < 4; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = 0; k < kVecs; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   bool last = false;
   for (int first = 0; !last; first += 32) {
     // Lane i: piece first + i.
@@ -1029,16 +1068,16 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const La
     for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
     l = l * keep + sum;
     #pragma unroll
-    for (int k = 0; k < 4; ++k) o[k] = make_float4(o[k].x * keep, o[k].y * keep, o[k].z * keep, o[k].w * keep);
+    for (int k = 0; k < kVecs; ++k) o[k] = make_float4(o[k].x * keep, o[k].y * keep, o[k].z * keep, o[k].w * keep);
     m = top;
-    #pragma unroll 4
+    #pragma unroll SPLIT == 1 ? 4 : 8
     for (int i = 0; i < n; ++i) {
       const float wi = __shfl_sync(0xffffffffu, w, i);
       const int si = __shfl_sync(0xffffffffu, slot, i);
       const float4* src = reinterpret_cast<const float4*>(p.piece_o + ((long long)si * p.piece_rows + row) * kLatent);
       #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float4 v = src[k * 32 + lane];
+      for (int k = 0; k < kVecs; ++k) {
+        const float4 v = src[k * 32 + at];
         o[k].x += v.x * wi;
         o[k].y += v.y * wi;
         o[k].z += v.z * wi;
@@ -1050,11 +1089,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const La
   const long long out_row = (long long)rec.y * p.num_q_heads + (cta % p.head_groups) * p.group_heads + row;
   const float inv = 1.f / l;
   #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < kVecs; ++k) {
     uint2 v;
     v.x = pack_bf16(o[k].x * inv, o[k].y * inv);
     v.y = pack_bf16(o[k].z * inv, o[k].w * inv);
-    reinterpret_cast<uint2*>(p.out + out_row * kLatent)[k * 32 + lane] = v;
+    reinterpret_cast<uint2*>(p.out + out_row * kLatent)[k * 32 + at] = v;
   }
 }
 
@@ -1100,7 +1139,8 @@ cudaError_t launch_latent_decode(const LatentDecodeLaunch& L, cudaStream_t strea
                              : (pair ? launch_decode<64, 64, 2, true>(L, stream) : launch_decode<64, 64, 2, false>(L, stream));
   if (e == cudaSuccess && L.p.merge) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(L.grid, (rows + kMergeWarps - 1) / kMergeWarps);
+    const int split = rows <= 16 ? 4 : 1;
+    cfg.gridDim = dim3(L.grid, (rows * split + kMergeWarps - 1) / kMergeWarps);
     cfg.blockDim = dim3(32 * kMergeWarps);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -1108,7 +1148,8 @@ cudaError_t launch_latent_decode(const LatentDecodeLaunch& L, cudaStream_t strea
     attr[0].val.programmaticStreamSerializationAllowed = L.p.pdl ? 1 : 0;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, latent_merge_kernel, L.p, L.grid);
+    e = split == 4 ? cudaLaunchKernelEx(&cfg, latent_merge_kernel<4>, L.p, L.grid)
+                   : cudaLaunchKernelEx(&cfg, latent_merge_kernel<1>, L.p, L.grid);
   }
   if (e != cudaSuccess) return e;
   return cudaGetLastError();

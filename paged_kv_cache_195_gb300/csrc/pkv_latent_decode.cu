@@ -129,7 +129,7 @@ struct __align__(1024) SmemT {
     Plan plan;                  // until the softmax begins
     struct {
       float xrow[4][kLatMaxRows];  // a warpgroup's exchange of maxima and sums
-      float inv[kLatMaxRows];      // reciprocals of the columns' sums
+      float top[kLatMaxRows];      // the columns' maxima
     };
   };
   unsigned long long bad[2];    // boundary keys taken out of the item's tiles, by item parity
@@ -328,6 +328,12 @@ __device__ __forceinline__ void stmatrix4_trans(uint32_t addr, uint32_t a, uint3
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
                "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
+}
+
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -598,20 +604,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         it.end = 0;
         if (it.t0 >= it.t1) continue;
         const int nbl = cdiv(it.vis, kBlockSize);
-        // The rows of the pool that blocks begin at, a window of tiles at a time, a
-        // lane each.  Blocks past the last are read at a row outside the pool,
-        // which fills zeros.
-        auto block_rows = [&](int tile) {
+        // Block ids, a window of tiles at a time, a lane each; they become rows of the
+        // pool when their window begins.  Blocks past the last are read at a row
+        // outside the pool, which fills zeros.
+        auto ids = [&](int tile) {
           const int x = tile * kTileBlocks + lane;
-          int row = oob_row;
-          if (x < nbl && lane < kWindow * kTileBlocks) {
-            const int id = __ldg(bt + x);
-            if ((unsigned)id < (unsigned)p.num_blocks) row = id * kBlockSize;
-            else record_error(p.err, kErrBounds);
-          }
-          return row;
+          return x < nbl && lane < kWindow * kTileBlocks ? __ldg(bt + x) : INT_MIN;
         };
-        int cur = block_rows(it.t0);
+        auto row_of = [&](int id) {
+          if ((unsigned)id < (unsigned)p.num_blocks) return id * kBlockSize;
+          if (id != INT_MIN) record_error(p.err, kErrBounds);
+          return oob_row;
+        };
+        int nxt = ids(it.t0), cur = 0;
         // The item and its queries, ahead of its first keys.
         if (n_item > 0) ok = all_of(wait_for(&sm.q_empty, (n_item - 1) & 1, p.err, ctl));
         if (!ok) break;
@@ -624,21 +629,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         ++n_item;
-        int nxt = oob_row;
         int k = 0;  // lane of the tile's first block
         int j = uniform(it.t0);
         const int j1 = uniform(it.t1);
         #pragma unroll 1
         for (; j < j1; ++j) {
-          if (k == 0 && j + kWindow < j1) nxt = block_rows(j + kWindow);
+          if (k == 0) {
+            cur = row_of(nxt);
+            if (j + kWindow < j1) nxt = ids(j + kWindow);
+          }
           int rows[kTileBlocks];
           #pragma unroll
           for (int b = 0; b < kTileBlocks; ++b) rows[b] = uniform(__shfl_sync(0xffffffffu, cur, k + b));
           k += kTileBlocks;
-          if (k == kWindow * kTileBlocks) {
-            k = 0;
-            cur = nxt;
-          }
+          if (k == kWindow * kTileBlocks) k = 0;
           #pragma unroll
           for (int part = 0; part < kParts; ++part) {
             ok = all_of(wait_for(&sm.kv_empty[st][part], phase, p.err, ctl));
@@ -932,6 +936,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Columns in use: rows (token, head) of out from the first on, in order
       // (with two head groups an item has one token).
       const int cols = (it.nt - 1) * p.group_heads + heads;
+      float inv = 0.f;
       if (mine) {
         #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -941,20 +946,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane < 4) {
           #pragma unroll
           for (int i = 0; i < 4; ++i) sm.xrow[quad][col0 + 8 * (i >> 1) + (i & 1)] = l[i];
-        }
-        named_barrier(kBarGroup + wg, 128);
-        if (quad == 0 && lane < 4) {
-          #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int col = col0 + 8 * (i >> 1) + (i & 1);
-            const float sum = (sm.xrow[0][col] + sm.xrow[1][col]) + (sm.xrow[2][col] + sm.xrow[3][col]);
-            sm.inv[col] = 1.f / sum;
-            if (!whole && ok && col < cols)
-              *reinterpret_cast<float2*>(p.piece_ml + ((long long)slot * p.piece_rows + col) * 2) =
-                  make_float2(m[i], sum);
+          if (!whole && ok && quad == 0) {
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) sm.top[col0 + 8 * (i >> 1) + (i & 1)] = m[i];
           }
         }
         named_barrier(kBarGroup + wg, 128);
+        // Lane i < 16: column i's sum.
+        const int col = wg * 16 + (lane & 15);
+        const float sum = (sm.xrow[0][col] + sm.xrow[1][col]) + (sm.xrow[2][col] + sm.xrow[3][col]);
+        inv = reciprocal(sum);
+        if (!whole && ok && quad == 0 && lane < 16 && col < cols)
+          *reinterpret_cast<float2*>(p.piece_ml + ((long long)slot * p.piece_rows + col) * 2) =
+              make_float2(sm.top[col], sum);
       }
       if (!whole && ok && tid == 0) {
         int* rec = p.piece + slot * kPieceWords;
@@ -984,7 +988,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __nv_bfloat16* at = dst + (long long)(wg * 16 + (lane & 1)) * kLatent + (d & ~1);
             #pragma unroll
             for (int i = 0; i < 16; i += 2) {
-              const float a = o[i] * sm.inv[wg * 16 + i], b = o[i + 1] * sm.inv[wg * 16 + i + 1];
+              const float a = o[i] * __shfl_sync(0xffffffffu, inv, i), b = o[i + 1] * __shfl_sync(0xffffffffu, inv, i + 1);
               const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
               if (i + (lane & 1) < n)
                 *reinterpret_cast<uint32_t*>(at + i * kLatent) = lane & 1 ? pack_bf16(other, b) : pack_bf16(a, other);

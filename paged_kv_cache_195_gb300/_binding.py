@@ -649,8 +649,8 @@ LATENT, ROPE = 512, 64  # a cached latent, and the rotated key beside it
 
 
 def _rows(t, name: str, dev: int, dims: tuple):
-    """Checks a bf16 [tokens, *dims] tensor whose tokens may lie apart, each of
-    them contiguous; returns (pointer, elements between tokens)."""
+    """Says what is wrong with a bf16 [tokens, *dims] tensor, whose tokens may lie
+    apart, each of them contiguous."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not _BF16 or t.get_device() != dev or dev < 0:
@@ -663,7 +663,21 @@ def _rows(t, name: str, dev: int, dims: tuple):
         if n > 1 and s != want:
             raise ValueError(f"{name}: a token's row must be contiguous, got strides {strides}")
         want *= n
-    return t.data_ptr(), strides[0] if t.shape[0] > 1 else want
+
+
+def _heads(t, name: str, dev: int, T: int, H: int):
+    """(pointer, elements between tokens) of a bf16 [T, H, 128] tensor (see _rows)."""
+    try:
+        if t.dtype is _BF16 and t.get_device() == dev and dev >= 0 and t.shape == (T, H, 128):
+            a, b, c = t.stride()
+            if c == 1 and (b == 128 or H < 2):
+                return t.data_ptr(), a if T > 1 else 128 * H
+    except AttributeError:
+        pass
+    _rows(t, name, dev, (H, 128))
+    if t.shape[0] != T:
+        raise ValueError("q, k, v and q_out disagree on the token count")
+    return t.data_ptr(), t.stride(0) if T > 1 else 128 * H
 
 
 def _overlap(a, b) -> bool:
@@ -688,19 +702,6 @@ def _shares(a, b) -> bool:
     return gap < wa or gap + wb > row
 
 
-def _token_args(positions, cos_sin, slot_mapping, T: int, dev: int):
-    for t, name, dtype in ((positions, "positions", _I64), (slot_mapping, "slot_mapping", _I64)):
-        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev \
-                or t.dim() != 1 or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int64 [tokens] tensor on the call's device")
-        if t.shape[0] != T:
-            raise ValueError(f"{name} needs one entry per token")
-    if not isinstance(cos_sin, torch.Tensor) or cos_sin.dtype is not _F32 or cos_sin.dim() != 2 \
-            or cos_sin.get_device() != dev or not cos_sin.is_contiguous():
-        raise ValueError("cos_sin must be a contiguous fp32 [positions, rotary dims] tensor on the "
-                         "call's device")
-
-
 def _weight(t, name: str, n: int, dev: int):
     if t is None:
         return None
@@ -710,12 +711,8 @@ def _weight(t, name: str, n: int, dev: int):
     return t.data_ptr()
 
 
-def _pool(t, name: str, ndim: int, dev: int):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not _BF16 or t.dim() != ndim or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous bf16 tensor of {ndim} dims on the call's device")
-    return t.data_ptr()
+_ROPE_FIXED = _spec(("positions", _I64, 1), ("cos_sin", _F32, 2), ("slot_mapping", _I64, 1),
+                    ("k_pool", _BF16, 4), ("v_pool", _BF16, 4))
 
 
 def pkv_norm_rope_append(q, k, v, positions, cos_sin, slot_mapping, k_pool, v_pool,
@@ -732,36 +729,53 @@ def pkv_norm_rope_append(q, k, v, positions, cos_sin, slot_mapping, k_pool, v_po
     in place), keys and v [T, Hkv, 128] into the pools at slot_mapping [T]
     int64.  A token with a negative slot is padding: nothing of it is written.
     Returns q_out."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be a [tokens, heads, 128] tensor")
-    if not isinstance(k, torch.Tensor) or k.dim() != 3:
-        raise ValueError("k must be a [tokens, heads, 128] tensor")
-    dev = q.get_device()
-    T, Hq, Hkv = q.shape[0], q.shape[1], k.shape[1]
-    qp, qs = _rows(q, "q", dev, (Hq, 128))
-    kp, ks = _rows(k, "k", dev, (Hkv, 128))
-    vp, vs = _rows(v, "v", dev, (Hkv, 128))
-    if k.shape[0] != T or v.shape[0] != T:
-        raise ValueError("q, k and v disagree on the token count")
-    _token_args(positions, cos_sin, slot_mapping, T, dev)
-    kpool, vpool = _pool(k_pool, "k_pool", 4, dev), _pool(v_pool, "v_pool", 4, dev)
-    if v_pool.shape != k_pool.shape or k_pool.shape[1] != Hkv:
-        raise ValueError("pool shape does not match the new rows")
-    wq, wk = _weight(q_weight, "q_weight", 128, dev), _weight(k_weight, "k_weight", 128, dev)
+    dev, (pos, table, slots, kpool, vpool) = _fast_need((positions, cos_sin, slot_mapping, k_pool, v_pool),
+                                                        _ROPE_FIXED)
+    try:
+        T, Hq, _ = q.shape
+        Hkv = k.shape[1]
+    except (AttributeError, ValueError, IndexError):
+        raise ValueError("q and k must be [tokens, heads, 128] tensors") from None
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    op, os_ = _rows(q_out, "q_out", dev, (Hq, 128))
-    if q_out.shape != q.shape:
-        raise ValueError("q_out must have q's shape")
-    if T and ((op, os_) != (qp, qs) and _shares(q_out, q) or _shares(q_out, k) or _shares(q_out, v)):
-        raise ValueError("q_out may be q, but not overlap the inputs otherwise")
-    nb, _, bs, D = k_pool.shape
+        q_out = torch.empty((T, Hq, 128), dtype=_BF16, device=q.device)
+    qp, qs = _heads(q, "q", dev, T, Hq)
+    kp, ks = _heads(k, "k", dev, T, Hkv)
+    vp, vs = _heads(v, "v", dev, T, Hkv)
+    op, os_ = _heads(q_out, "q_out", dev, T, Hq)
+    if positions.shape[0] != T or slot_mapping.shape[0] != T:
+        raise ValueError("positions and slot_mapping need one entry per token")
+    nb, h, bs, D = pool = k_pool.shape
+    if v_pool.shape != pool or h != Hkv:
+        raise ValueError("pool shape does not match the new rows")
+    wq = None if q_weight is None else _weight(q_weight, "q_weight", 128, dev)
+    wk = None if k_weight is None else _weight(k_weight, "k_weight", 128, dev)
+    if T and Hq:
+        # Ranges that meet: side by side in the rows of one tensor, or overlapping?
+        end = op + 2 * ((T - 1) * os_ + 128 * Hq)
+        for t, ptr, stride, H in ((q, qp, qs, Hq), (k, kp, ks, Hkv), (v, vp, vs, Hkv)):
+            if ptr < end and op < ptr + 2 * ((T - 1) * stride + 128 * H):
+                if not (t is q and ptr == op and stride == os_) and _shares(q_out, t):
+                    raise ValueError("q_out may be q, but not overlap the inputs otherwise")
+    n, rot = cos_sin.shape
     dims = Dims(0, T, Hq, Hkv, D, bs, nb, 0)
-    _call((_lib or load_library()).pkv_norm_rope_append, dev, qp, kp, vp, qs, ks, vs,
-          positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1],
-          int(bool(interleaved)), wq, wk, eps, slot_mapping.data_ptr(), op, os_, kpool, vpool,
-          ctypes.byref(dims), _raw_stream(stream, dev))
+    _call((_lib or load_library()).pkv_norm_rope_append, dev, qp, kp, vp, qs, ks, vs, pos, table, n, rot,
+          1 if interleaved else 0, wq, wk, eps, slots, op, os_, kpool, vpool, ctypes.byref(dims),
+          _raw_stream(stream, dev))
     return q_out
+
+
+_LATENT_FIXED = _spec(("positions", _I64, 1), ("cos_sin", _F32, 2), ("slot_mapping", _I64, 1),
+                      ("pool", _BF16, 3))
+
+
+def _rope_part(t, name: str, dev: int, shape: tuple):
+    """(pointer, strides of tokens and heads) of a bf16 [tokens, heads, 64] tensor."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.get_device() != dev or t.shape != shape:
+        raise ValueError(f"{name} must be a bf16 [tokens, heads, {ROPE}] tensor like q_rope on kv's device")
+    a, b, c = t.stride()
+    if c != 1:
+        raise ValueError(f"{name}: the rotated dims must be contiguous")
+    return t.data_ptr(), a if shape[0] > 1 else 0, b if shape[1] > 1 else 0
 
 
 def pkv_append_latent(kv, positions, cos_sin, slot_mapping, pool, weight=None, eps=1e-6,
@@ -775,41 +789,46 @@ def pkv_append_latent(kv, positions, cos_sin, slot_mapping, pool, weight=None, e
     meets the rotated keys (any strides between tokens and heads), is rotated
     too, into q_rope_out (default: in place).  A token with a negative slot is
     padding: nothing of it is written."""
-    if not isinstance(kv, torch.Tensor):
-        raise TypeError("kv must be a torch.Tensor")
-    dev = kv.get_device()
-    ptr, stride = _rows(kv, "kv", dev, (LATENT + ROPE,))
-    T = kv.shape[0]
-    _token_args(positions, cos_sin, slot_mapping, T, dev)
-    if cos_sin.shape[1] != ROPE:
+    dev, (pos, table, slots, pp) = _fast_need((positions, cos_sin, slot_mapping, pool), _LATENT_FIXED)
+    try:
+        T, width = kv.shape
+        stride, one = kv.stride()
+        good = kv.dtype is _BF16 and kv.get_device() == dev and width == LATENT + ROPE and one == 1
+    except (AttributeError, ValueError):
+        good = False
+    if not good:
+        _rows(kv, "kv", dev, (LATENT + ROPE,))
+    if T < 2:
+        stride = LATENT + ROPE
+    if positions.shape[0] != T or slot_mapping.shape[0] != T:
+        raise ValueError("positions and slot_mapping need one entry per token")
+    n, rot = cos_sin.shape
+    if rot != ROPE:
         raise ValueError(f"cos_sin must have {ROPE} columns")
-    pp = _pool(pool, "pool", 3, dev)
-    w = _weight(weight, "weight", LATENT, dev)
-    heads, qp, qs, qo, os_ = 0, None, (0, 0), None, (0, 0)
+    w = None if weight is None else _weight(weight, "weight", LATENT, dev)
+    heads, q, out = 0, (None, 0, 0), (None, 0, 0)
     if q_rope is not None:
-        if q_rope_out is None:
-            q_rope_out = q_rope
-        for t, name in ((q_rope, "q_rope"), (q_rope_out, "q_rope_out")):
-            if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.get_device() != dev \
-                    or t.dim() != 3 or t.shape[0] != T or t.shape[2] != ROPE \
-                    or t.shape[1] != q_rope.shape[1] or t.stride(2) != 1:
-                raise ValueError(f"{name} must be a bf16 [tokens, heads, {ROPE}] tensor on kv's device, "
-                                 "its last dim contiguous")
-        heads = q_rope.shape[1]
-        (qp, qs), (qo, os_) = ((t.data_ptr(), tuple(s if n > 1 else 0 for s, n in zip(t.stride(), t.shape[:2])))
-                               for t in (q_rope, q_rope_out))
-        if any(s < ROPE for s, n in zip(os_, q_rope.shape[:2]) if n > 1):
-            raise ValueError("q_rope_out's rows overlap")
-        if (qp, qs) != (qo, os_) and T and heads and _overlap(q_rope, q_rope_out):
-            raise ValueError("q_rope_out may be q_rope, but not overlap it otherwise")
+        if not isinstance(q_rope, torch.Tensor) or q_rope.dim() != 3 or q_rope.shape[0] != T \
+                or q_rope.shape[2] != ROPE:
+            raise ValueError(f"q_rope must be a [tokens, heads, {ROPE}] tensor")
+        shape = q_rope.shape
+        heads = shape[1]
+        q = out = _rope_part(q_rope, "q_rope", dev, shape)
+        if q_rope_out is not None and q_rope_out is not q_rope:
+            out = _rope_part(q_rope_out, "q_rope_out", dev, shape)
+        if T and heads:
+            if 0 < out[1] < ROPE or 0 < out[2] < ROPE or (T > 1 and out[1] == 0) or (heads > 1 and out[2] == 0):
+                raise ValueError("q_rope_out's rows overlap")
+            # (one thread's rows may be another's: only ranges apart, or the same rows)
+            size = [2 * ((T - 1) * a + (heads - 1) * b + ROPE) for _, a, b in (q, out)]
+            if out != q and q[0] < out[0] + size[1] and out[0] < q[0] + size[0]:
+                raise ValueError("q_rope_out may be q_rope, but not overlap it otherwise")
     elif q_rope_out is not None:
         raise ValueError("q_rope_out without q_rope")
     nb, bs, D = pool.shape
     dims = Dims(0, T, heads, 1, D, bs, nb, 0)
-    _call((_lib or load_library()).pkv_append_latent, dev, ptr, stride, positions.data_ptr(),
-          cos_sin.data_ptr(), cos_sin.shape[0], int(bool(interleaved)), w, eps,
-          slot_mapping.data_ptr(), pp, qp, qs[0], qs[1], qo, os_[0], os_[1], ctypes.byref(dims),
-          _raw_stream(stream, dev))
+    _call((_lib or load_library()).pkv_append_latent, dev, kv.data_ptr(), stride, pos, table, n,
+          1 if interleaved else 0, w, eps, slots, pp, *q, *out, ctypes.byref(dims), _raw_stream(stream, dev))
 
 
 class LatentWorkspace:

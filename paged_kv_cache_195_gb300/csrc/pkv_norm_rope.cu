@@ -10,11 +10,12 @@
 // at the store.
 //
 // Bound: HBM for chunks, latency for decodes (slot and position, then the
-// table's row, then the store).  Sixteen lanes hold a 128-dim head, eight
-// elements (16 bytes) each; a head's sum of squares is four shuffles, and a
-// pair of a half-split rotation lies in two lanes one shuffle apart.  A thread
-// keeps its cos and sin over all the heads that it turns and issues the loads
-// of up to four heads before it uses the first.
+// table's row, then the store).  Sixteen lanes hold a 128-dim head, eight lanes
+// the 64 rotated dims of a latent's head, each lane two runs of four dims that
+// make four whole pairs -- dims i .. i + 3 and i + rot/2 .. of a half-split
+// rotation -- so that a rotation needs no shuffles and a lane keeps four cos and
+// four sin over all the heads that it turns.  A thread issues the loads of up to
+// four heads before it uses the first.
 #include "pkv_latent.h"
 
 namespace pkv {
@@ -22,27 +23,50 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
-  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-  #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = bf16x2_to_float2(in[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
+// Eight bf16 of a lane, as two runs of four.
+struct Raw {
+  uint2 a, b;
+};
+
+// Where lane l's runs lie in a vector whose leading `rot` dims are rotated.  Lanes
+// behind those hold eight dims in a row that stay as they are.
+struct Place {
+  int a, b;
+  bool turned;
+};
+
+__device__ __forceinline__ Place place(int l, int rot, bool inter) {
+  const bool turned = 8 * l < rot;
+  if (inter || !turned) return Place{8 * l, 8 * l + 4, turned};
+  return Place{4 * l, rot / 2 + 4 * l, turned};
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  uint32_t o[4];
-  #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    o[i] = *reinterpret_cast<const uint32_t*>(&v);
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
+__device__ __forceinline__ Raw load8(const __nv_bfloat16* v, const Place& at) {
+  return Raw{*reinterpret_cast<const uint2*>(v + at.a), *reinterpret_cast<const uint2*>(v + at.b)};
 }
 
-// Sum of v over the aligned `width` lanes.
+__device__ __forceinline__ void store8(__nv_bfloat16* v, const Place& at, const Raw& r) {
+  *reinterpret_cast<uint2*>(v + at.a) = r.a;
+  *reinterpret_cast<uint2*>(v + at.b) = r.b;
+}
+
+__device__ __forceinline__ void unpack8(const Raw& r, float2 (&x)[4]) {
+  x[0] = bf16x2_to_float2(r.a.x);
+  x[1] = bf16x2_to_float2(r.a.y);
+  x[2] = bf16x2_to_float2(r.b.x);
+  x[3] = bf16x2_to_float2(r.b.y);
+}
+
+__device__ __forceinline__ uint32_t pack2(float2 v) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ Raw pack8(const float2 (&x)[4]) {
+  return Raw{make_uint2(pack2(x[0]), pack2(x[1])), make_uint2(pack2(x[2]), pack2(x[3]))};
+}
+
+// Sum of v over the aligned `WIDTH` lanes.
 template <int WIDTH>
 __device__ __forceinline__ float lane_sum(float v) {
   #pragma unroll
@@ -50,78 +74,64 @@ __device__ __forceinline__ float lane_sum(float v) {
   return v;
 }
 
-// 1 / sqrt(mean of squares + eps) of the N * WIDTH elements that WIDTH lanes
-// hold; `pre` is a factor the elements are to be multiplied with first.  Where
-// the squares of finite elements leave fp32's range, they are summed again,
-// scaled down: x * 2^-70 has squares below 2^116, and eps no weight beside them.
+// x to x / sqrt(mean of squares + eps) over the N float2 of each of WIDTH lanes.
+// rsqrt is off by 2^-22, and the result is rounded to bf16's 2^-8.  Where the
+// squares of finite elements leave fp32's range, they are summed again, scaled
+// down: x * 2^-70 has squares below 2^116, and eps no weight beside them.
 template <int N, int WIDTH>
-__device__ __forceinline__ float inv_rms(const float (&x)[N], float eps, float* pre) {
-  constexpr float kMean = 1.f / (N * WIDTH);
-  float s = 0.f;
+__device__ __forceinline__ void norm(float2 (&x)[N], float eps) {
+  constexpr float kMean = 1.f / (2 * N * WIDTH);
+  float2 s2 = make_float2(0.f, 0.f);
   #pragma unroll
-  for (int i = 0; i < N; ++i) s = fmaf(x[i], x[i], s);
-  s = lane_sum<WIDTH>(s);
-  *pre = 1.f;
+  for (int i = 0; i < N; ++i) s2 = ffma2(x[i], x[i], s2);
+  float s = lane_sum<WIDTH>(s2.x + s2.y);
   const bool over = s == INFINITY;
   if (__any_sync(0xffffffffu, over)) {
-    float z = 0.f;
+    const float k = over ? 0x1p-70f : 1.f;
+    s2 = make_float2(0.f, 0.f);
     #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float y = x[i] * 0x1p-70f;
-      z = fmaf(y, y, z);
+      x[i] = fmul2(x[i], make_float2(k, k));
+      s2 = ffma2(x[i], x[i], s2);
     }
-    z = lane_sum<WIDTH>(z);
-    if (over) {
-      *pre = 0x1p-70f;
-      return 1.f / sqrtf(z * kMean);
-    }
+    s = lane_sum<WIDTH>(s2.x + s2.y);
+    if (over) eps = 0.f;
   }
-  return 1.f / sqrtf(fmaf(s, kMean, eps));
+  const float r = rsqrtf(fmaf(s, kMean, eps));
+  #pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = fmul2(x[i], make_float2(r, r));
 }
 
-// The cos and sin that a lane needs for its eight dims 8 l .. 8 l + 7 of a
-// rotated vector: of the eight pairs that they belong to (half split: dims i
-// and i + rot/2) or of the four pairs that they are (interleaved).
+// cos and sin of a lane's four pairs.
 struct Turn {
-  float c[8], s[8];
+  float4 c, s;
 };
 
-__device__ __forceinline__ void load_turn(Turn& r, const float* row, int rot, int l, bool inter) {
-  const int half = rot / 2;
-  const int i0 = inter ? 4 * l : (8 * l) % half;
-  #pragma unroll
-  for (int i = 0; i < 8; i += 4) {
-    if (i == 4 && inter) break;
-    const float4 c = __ldg(reinterpret_cast<const float4*>(row + i0 + i));
-    const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + i0 + i));
-    r.c[i] = c.x, r.c[i + 1] = c.y, r.c[i + 2] = c.z, r.c[i + 3] = c.w;
-    r.s[i] = s.x, r.s[i + 1] = s.y, r.s[i + 2] = s.z, r.s[i + 3] = s.w;
-  }
+__device__ __forceinline__ Turn load_turn(const float* row, int rot, int l) {
+  Turn r;
+  r.c = __ldg(reinterpret_cast<const float4*>(row + 4 * l));
+  r.s = __ldg(reinterpret_cast<const float4*>(row + rot / 2 + 4 * l));
+  return r;
 }
 
-// Turns this lane's eight elements; `l` is the lane's place in the vector (and
-// in the shuffle's `width` lanes), all of a warp's lanes take part.
-__device__ __forceinline__ void turn(float (&x)[8], const Turn& r, int rot, int l, int width,
-                                     bool inter) {
-  const bool in = 8 * l < rot;
+__device__ __forceinline__ void turn_pair(float& a, float& b, float c, float s) {
+  const float u = a * c - b * s;
+  b = b * c + a * s;
+  a = u;
+}
+
+// Turns a lane's four pairs: (i, i + 4) of its eight elements, or (2 i, 2 i + 1).
+__device__ __forceinline__ void turn(float2 (&x)[4], const Turn& t, bool inter) {
   if (inter) {
-    if (in) {
-      #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = x[2 * i], b = x[2 * i + 1];
-        x[2 * i] = a * r.c[i] - b * r.s[i];
-        x[2 * i + 1] = b * r.c[i] + a * r.s[i];
-      }
-    }
-    return;
-  }
-  const int step = rot / 16;  // lanes between the halves
-  const bool low = l < step;
-  const int src = !in ? l : low ? l + step : l - step;
-  #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float o = __shfl_sync(0xffffffffu, x[i], src, width);
-    if (in) x[i] = low ? x[i] * r.c[i] - o * r.s[i] : x[i] * r.c[i] + o * r.s[i];
+    turn_pair(x[0].x, x[0].y, t.c.x, t.s.x);
+    turn_pair(x[1].x, x[1].y, t.c.y, t.s.y);
+    turn_pair(x[2].x, x[2].y, t.c.z, t.s.z);
+    turn_pair(x[3].x, x[3].y, t.c.w, t.s.w);
+  } else {
+    turn_pair(x[0].x, x[2].x, t.c.x, t.s.x);
+    turn_pair(x[0].y, x[2].y, t.c.y, t.s.y);
+    turn_pair(x[1].x, x[3].x, t.c.z, t.s.z);
+    turn_pair(x[1].y, x[3].y, t.c.w, t.s.w);
   }
 }
 
@@ -138,133 +148,138 @@ __device__ __forceinline__ bool token_ok(long long slot, long long pos, int num_
 
 // Block (t, y): vectors 16 U y .. of token t; its heads in the order q, k, v.
 template <int U>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_append_kernel(const NormRopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 5) norm_rope_append_kernel(const NormRopeParams p) {
   grid_dependency_wait();  // inputs and pools may belong to the previous kernel
   allow_dependent_launch();
-  const int t = blockIdx.x;
   const int sub = threadIdx.x >> 4, l = threadIdx.x & 15;
   const int hq = p.num_q_heads, hkv = p.num_kv_heads;
   const int total = hq + 2 * hkv;
+  const int first = blockIdx.y * (U * kRopeThreads / 16) + sub;
+  const bool inter = p.interleaved != 0;
+  const Place at = place(l, p.rot, inter);
+  const int t = blockIdx.x;
   const long long slot = __ldg(p.slot_mapping + t), pos = __ldg(p.positions + t);
-  uint4 raw[U];
+  Raw raw[U];
   #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int vec = (blockIdx.y * U + u) * (kRopeThreads / 16) + sub;
-    raw[u] = make_uint4(0, 0, 0, 0);
+    const int vec = first + u * (kRopeThreads / 16);
+    raw[u] = Raw{make_uint2(0, 0), make_uint2(0, 0)};
     if (vec < total) {
       const __nv_bfloat16* src = vec < hq         ? p.q + t * p.q_stride + vec * kHeadDim
                                  : vec < hq + hkv ? p.k + t * p.k_stride + (vec - hq) * kHeadDim
                                                   : p.v + t * p.v_stride + (vec - hq - hkv) * kHeadDim;
-      raw[u] = *reinterpret_cast<const uint4*>(src + 8 * l);
+      raw[u] = load8(src, at);
     }
   }
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  const uint4 wq = p.q_weight ? __ldg(reinterpret_cast<const uint4*>(p.q_weight) + l) : zero;
-  const uint4 wk = p.k_weight ? __ldg(reinterpret_cast<const uint4*>(p.k_weight) + l) : zero;
+  Raw wq{make_uint2(0, 0), make_uint2(0, 0)}, wk = wq;
+  if (p.q_weight) wq = load8(p.q_weight, at);
+  if (p.k_weight) wk = load8(p.k_weight, at);
   if (!token_ok(slot, pos, p.num_blocks, p.max_position, p.err)) return;
-  const bool inter = p.interleaved != 0;
-  Turn tr;
-  if (8 * l < p.rot) load_turn(tr, p.cos_sin + pos * p.rot, p.rot, l, inter);
-  const long long blk = slot / kBlockSize;
-  const int off = (int)(slot % kBlockSize);
+  Turn tr{};
+  if (at.turned) tr = load_turn(p.cos_sin + pos * p.rot, p.rot, l);
+  const long long row = (slot / kBlockSize * hkv * kBlockSize + slot % kBlockSize) * kHeadDim;
   #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int vec = (blockIdx.y * U + u) * (kRopeThreads / 16) + sub;
+    const int vec = first + u * (kRopeThreads / 16);
     const bool is_q = vec < hq, is_v = vec >= hq + hkv;
-    float x[8];
-    unpack8(raw[u], x);
-    const bool norm = is_q ? p.q_weight != nullptr : p.k_weight != nullptr;
-    float pre;
-    const float r = inv_rms<8, 16>(x, p.eps, &pre);
-    if (norm) {
-      float w[8];
-      unpack8(is_q ? wq : wk, w);
-      #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * pre * r * w[i];
+    // (a warp's two vectors, both values or past the end: nothing to compute)
+    if (!__all_sync(0xffffffffu, is_v)) {
+      float2 x[4];
+      unpack8(raw[u], x);
+      const bool by_q = p.q_weight != nullptr, by_k = p.k_weight != nullptr;
+      if (by_q || by_k) {
+        float2 y[4], w[4];
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = x[i];
+        norm<4, 16>(y, p.eps);
+        unpack8(is_q ? wq : wk, w);
+        if (is_q ? by_q : by_k) {
+          #pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = fmul2(y[i], w[i]);
+        }
+      }
+      if (at.turned) turn(x, tr, inter);
+      if (!is_v) raw[u] = pack8(x);
     }
-    turn(x, tr, p.rot, l, 16, inter);
-    if (vec >= total) continue;
-    __nv_bfloat16* dst;
-    if (is_q) {
-      dst = p.q_out + t * p.out_stride + vec * kHeadDim;
-    } else {
-      const int h = is_v ? vec - hq - hkv : vec - hq;
-      dst = (is_v ? p.v_pool : p.k_pool) + ((blk * hkv + h) * kBlockSize + off) * kHeadDim;
+    if (vec < total) {
+      __nv_bfloat16* dst = is_q ? p.q_out + t * p.out_stride + vec * kHeadDim
+                           : is_v ? p.v_pool + row + (vec - hq - hkv) * (kBlockSize * kHeadDim)
+                                  : p.k_pool + row + (vec - hq) * (kBlockSize * kHeadDim);
+      store8(dst, at, raw[u]);
     }
-    *reinterpret_cast<uint4*>(dst + 8 * l) = is_v ? raw[u] : pack8(x);
   }
 }
 
 // Block (t, y): warp 0 of the blocks y = 0 writes token t's cache row (the
-// latent as 16 elements a lane, two runs of eight; the rotated key on eight
-// lanes); all warps turn the queries' vectors, eight lanes each, the first
-// vectors by the last warps.
+// latent as 16 elements a lane; the rotated key on eight lanes); all warps turn
+// the queries' vectors, eight lanes each, the first vectors by the last warps.
 template <int U>
-__global__ void __launch_bounds__(kRopeThreads) append_latent_kernel(const AppendLatentParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 4) append_latent_kernel(const AppendLatentParams p) {
   grid_dependency_wait();  // inputs and pool may belong to the previous kernel
   allow_dependent_launch();
-  const int t = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int l = lane & 7;
-  const int sub = (kRopeThreads / 32 - 1 - warp) * 4 + (lane >> 3);
   constexpr int kVecs = kRopeThreads / 8;
+  const int first = blockIdx.y * (U * kVecs) + (kRopeThreads / 32 - 1 - warp) * 4 + (lane >> 3);
+  const bool inter = p.interleaved != 0;
+  const Place at = place(l, kRopeDim, inter);
+  const int t = blockIdx.x;
   const long long slot = __ldg(p.slot_mapping + t), pos = __ldg(p.positions + t);
   const bool row = warp == 0 && blockIdx.y == 0;
-  uint4 raw[U], lat[2], key;
+  Raw raw[U], key;
+  uint4 lat[2];
   #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int vec = (blockIdx.y * U + u) * kVecs + sub;
-    raw[u] = make_uint4(0, 0, 0, 0);
-    if (vec < p.num_q_heads)
-      raw[u] = *reinterpret_cast<const uint4*>(p.q_rope + t * p.q_stride + vec * p.q_head_stride + 8 * l);
+    const int vec = first + u * kVecs;
+    raw[u] = Raw{make_uint2(0, 0), make_uint2(0, 0)};
+    if (vec < p.num_q_heads) raw[u] = load8(p.q_rope + t * p.q_stride + vec * p.q_head_stride, at);
   }
   if (row) {
     const uint4* src = reinterpret_cast<const uint4*>(p.kv + t * p.kv_stride);
     lat[0] = src[lane];
     lat[1] = src[lane + 32];
-    key = src[kLatent / 8 + l];
+    key = load8(p.kv + t * p.kv_stride + kLatent, at);
   }
   if (!token_ok(slot, pos, p.num_blocks, p.max_position, p.err)) return;
-  const bool inter = p.interleaved != 0;
-  Turn tr;
-  load_turn(tr, p.cos_sin + pos * kRopeDim, kRopeDim, l, inter);
+  const Turn tr = load_turn(p.cos_sin + pos * kRopeDim, kRopeDim, l);
   if (row) {
-    uint4* dst = reinterpret_cast<uint4*>(p.pool + slot * kLatRow);
+    __nv_bfloat16* dst = p.pool + slot * kLatRow;
     if (p.weight != nullptr) {
-      float x[16];
-      float a[8], b[8];
-      unpack8(lat[0], a);
-      unpack8(lat[1], b);
+      const uint4* const wp = reinterpret_cast<const uint4*>(p.weight);
+      float2 x[8];
       #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = a[i], x[8 + i] = b[i];
-      float pre;
-      const float r = inv_rms<16, 32>(x, p.eps, &pre);
-      float w0[8], w1[8];
-      unpack8(__ldg(reinterpret_cast<const uint4*>(p.weight) + lane), w0);
-      unpack8(__ldg(reinterpret_cast<const uint4*>(p.weight) + lane + 32), w1);
-      #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        a[i] = a[i] * pre * r * w0[i];
-        b[i] = b[i] * pre * r * w1[i];
+      for (int h = 0; h < 2; ++h) {
+        x[4 * h] = bf16x2_to_float2(lat[h].x);
+        x[4 * h + 1] = bf16x2_to_float2(lat[h].y);
+        x[4 * h + 2] = bf16x2_to_float2(lat[h].z);
+        x[4 * h + 3] = bf16x2_to_float2(lat[h].w);
       }
-      lat[0] = pack8(a);
-      lat[1] = pack8(b);
+      norm<8, 32>(x, p.eps);
+      #pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 w = __ldg(wp + lane + 32 * h);
+        lat[h] = make_uint4(pack2(fmul2(x[4 * h], bf16x2_to_float2(w.x))),
+                            pack2(fmul2(x[4 * h + 1], bf16x2_to_float2(w.y))),
+                            pack2(fmul2(x[4 * h + 2], bf16x2_to_float2(w.z))),
+                            pack2(fmul2(x[4 * h + 3], bf16x2_to_float2(w.w))));
+      }
     }
-    dst[lane] = lat[0];
-    dst[lane + 32] = lat[1];
-    float x[8];
+    reinterpret_cast<uint4*>(dst)[lane] = lat[0];
+    reinterpret_cast<uint4*>(dst)[lane + 32] = lat[1];
+    float2 x[4];
     unpack8(key, x);
-    turn(x, tr, kRopeDim, l, 8, inter);
-    if (lane < 8) dst[kLatent / 8 + l] = pack8(x);
+    turn(x, tr, inter);
+    if (lane < 8) store8(dst + kLatent, at, pack8(x));
   }
   #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int vec = (blockIdx.y * U + u) * kVecs + sub;
-    float x[8];
-    unpack8(raw[u], x);
-    turn(x, tr, kRopeDim, l, 8, inter);
-    if (vec < p.num_q_heads)
-      *reinterpret_cast<uint4*>(p.q_rope_out + t * p.out_stride + vec * p.out_head_stride + 8 * l) = pack8(x);
+    const int vec = first + u * kVecs;
+    if (vec < p.num_q_heads) {
+      float2 x[4];
+      unpack8(raw[u], x);
+      turn(x, tr, inter);
+      store8(p.q_rope_out + t * p.out_stride + vec * p.out_head_stride, at, pack8(x));
+    }
   }
 }
 
@@ -284,27 +299,41 @@ cudaError_t launch(void (*kernel)(P), const P& p, dim3 grid, cudaStream_t stream
   return cudaGetLastError();
 }
 
-// One vector a thread while the blocks are few (latency), four when they would
+// Vectors a thread holds of the `passes` over a block that a token has: one while
+// the blocks are few (latency), up to four, as evenly as it goes, when they would
 // fill the GPU several times over (loads in flight, cos and sin used again).
-bool few(long long blocks, int sm_count) { return blocks <= 8ll * sm_count; }
+int vectors(long long tokens, int passes, int sm_count) {
+  if (tokens * passes <= 8ll * sm_count) return 1;
+  const int blocks = (passes + 3) / 4;
+  return (passes + blocks - 1) / blocks;
+}
 
 }  // namespace
 
 cudaError_t launch_norm_rope_append(const NormRopeParams& p, int sm_count, cudaStream_t stream) {
   constexpr int kVecs = kRopeThreads / 16;
   const int passes = (p.num_q_heads + 2 * p.num_kv_heads + kVecs - 1) / kVecs;
-  if (few((long long)p.num_tokens * passes, sm_count))
-    return launch(norm_rope_append_kernel<1>, p, dim3(p.num_tokens, passes), stream);
-  return launch(norm_rope_append_kernel<4>, p, dim3(p.num_tokens, (passes + 3) / 4), stream);
+  const int u = vectors(p.num_tokens, passes, sm_count);
+  const dim3 grid(p.num_tokens, (passes + u - 1) / u);
+  switch (u) {
+    case 1: return launch(norm_rope_append_kernel<1>, p, grid, stream);
+    case 2: return launch(norm_rope_append_kernel<2>, p, grid, stream);
+    case 3: return launch(norm_rope_append_kernel<3>, p, grid, stream);
+    default: return launch(norm_rope_append_kernel<4>, p, grid, stream);
+  }
 }
 
 cudaError_t launch_append_latent(const AppendLatentParams& p, int sm_count, cudaStream_t stream) {
   constexpr int kVecs = kRopeThreads / 8;
-  const int heads = p.q_rope ? p.num_q_heads : 0;
-  const int passes = heads > 0 ? (heads + kVecs - 1) / kVecs : 1;
-  if (few((long long)p.num_tokens * passes, sm_count))
-    return launch(append_latent_kernel<1>, p, dim3(p.num_tokens, passes), stream);
-  return launch(append_latent_kernel<4>, p, dim3(p.num_tokens, (passes + 3) / 4), stream);
+  const int passes = p.num_q_heads > 0 ? (p.num_q_heads + kVecs - 1) / kVecs : 1;
+  const int u = vectors(p.num_tokens, passes, sm_count);
+  const dim3 grid(p.num_tokens, (passes + u - 1) / u);
+  switch (u) {
+    case 1: return launch(append_latent_kernel<1>, p, grid, stream);
+    case 2: return launch(append_latent_kernel<2>, p, grid, stream);
+    case 3: return launch(append_latent_kernel<3>, p, grid, stream);
+    default: return launch(append_latent_kernel<4>, p, grid, stream);
+  }
 }
 
 }  // namespace pkv

@@ -6,18 +6,23 @@
 // a matrix product whose left operand is gathered through the block table.
 // Bound: tensor core (512 flops a byte written, the largest stream).
 //
-// Tiling.  A unit of work is (128 keys of one request, head): D[128 x 256] =
-// C[128 x 512] W_h^T.  The units form one sequence, heads fastest, cut in equal
-// ranges, one a CTA: a tile's latents (128 KB, eight 64-dim chunks gathered by
-// 2-D TMA copies of pool blocks) stay in shared memory for all of its heads, and
-// the weights stream by from L2 in [128 outputs x 64 dims] pieces.  D has two
-// TMEM buffers of 256 columns, so that a unit's rows are rounded and stored
-// while the next unit is multiplied.  Keys behind the request's end are rows of
-// D that nobody stores.
+// Tiling.  Two CTAs work as one (cta_group::2): a unit is (256 keys of one request,
+// head), D[256 x 256] = C[256 x 512] W_h^T, each CTA holding 128 of the keys, 128
+// of the outputs' weight rows, and the 128 x 256 part of D of its own keys in TMEM.
+// Alone, a CTA would take each weight row for half as many products: 64 bytes a
+// cycle of L2 and, with the MMA's own reads, more than shared memory gives.
+// The units form one sequence, heads fastest, cut in equal ranges, one a pair: a
+// tile's latents (128 KB a CTA, eight 64-dim chunks gathered by 2-D TMA copies of
+// pool blocks) stay in shared memory for all of its heads, and the weights stream
+// by from L2, a 64-dim chunk at a time.  D has two TMEM buffers of 256 columns, so
+// that a unit's rows are rounded and stored while the next is multiplied.  Keys
+// behind the request's end are rows of D that nobody stores.
 //
 // Roles (192 threads): warps 0-3 take D's rows, one a thread, round them once,
-// and store each through a row of its own in shared memory with bulk copies, so
-// that global writes are whole rows; warp 4 copies, warp 5 issues the MMAs.
+// and turn them through shared memory into stores of whole 128-byte lines (a bulk
+// copy a row took longer to issue than the products); warp 4 copies, warp 5 of the pair's first CTA
+// issues the MMAs of both.  Copies of both CTAs count on the first one's barriers,
+// commits arrive on both's.
 #include <climits>
 
 #include "pkv_latent.h"
@@ -30,9 +35,10 @@ constexpr int kEpiWarps = 4;
 constexpr int kWarpLoad = kEpiWarps;
 constexpr int kWarpMma = kEpiWarps + 1;
 constexpr int kThreads = 32 * (kEpiWarps + 2);
-constexpr int kKeys = 128;                 // keys of a unit: MMA M
-constexpr int kOut = kNope + kValDim;      // outputs of a unit
-constexpr int kHalf = 128;                 // MMA N
+constexpr int kKeys = 128;                 // keys of a CTA: half of the MMA's M
+constexpr int kPairKeys = 2 * kKeys;
+constexpr int kOut = kNope + kValDim;      // outputs of a unit: MMA N
+constexpr int kHalf = 128;                 // weight rows of a CTA
 constexpr int kChunks = kLatent / 64;
 constexpr int kChunkBytes = 128 * 128;     // 128 rows of 64 bf16
 constexpr int kStages = 4;                 // weight pieces in flight
@@ -69,7 +75,7 @@ __device__ __forceinline__ Req load_req(const LatentExpandParams& p, int r, bool
 }
 
 __device__ __forceinline__ long long units(const LatentExpandParams& p, const Req& a) {
-  return (long long)cdiv(a.keys, kKeys) * p.num_heads;
+  return (long long)cdiv(a.keys, kPairKeys) * p.num_heads;
 }
 
 // The CTA's range of the units and the request that it starts in.  All threads.
@@ -97,8 +103,9 @@ __device__ __forceinline__ void plan_range(const LatentExpandParams& p, Smem& sm
     total += sm.part[w];
   }
   const long long excl = before + incl - mine;
-  const long long chunk = (total + gridDim.x - 1) / gridDim.x;
-  const long long lo = min(blockIdx.x * chunk, total), hi = min(lo + chunk, total);
+  const int pairs = gridDim.x >> 1;
+  const long long chunk = (total + pairs - 1) / pairs;
+  const long long lo = min((blockIdx.x >> 1) * chunk, total), hi = min(lo + chunk, total);
   if (tid == 0) {
     sm.range_lo = lo;
     sm.range_hi = hi;
@@ -119,7 +126,7 @@ __device__ __forceinline__ void plan_range(const LatentExpandParams& p, Smem& sm
   __syncthreads();
 }
 
-// The range's runs in order -- heads h0 .. h1 - 1 of key tile `tile` of request
+// The range's runs in order -- heads h0 .. h1 - 1 of the 256-key tile `tile` of request
 // `req` -- which every role walks for itself.
 struct Walk {
   int req, tile, h0, h1;
@@ -155,11 +162,60 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
-               "r"(smem_u32(src)), "r"(bytes)
-               : "memory");
+// ------------------------------------------------------------ the pair's plumbing
+// The address, in the cluster's shared memory, of the first CTA's copy of `p`.
+__device__ __forceinline__ uint32_t first_cta(const void* p) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
+  return a;
 }
+
+// Copies into this CTA that count on a barrier of the pair's first CTA.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                                 uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+
+// Arrive on both CTAs' copies of `bar` once this thread's MMAs so far are done.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ bool all_of(bool v) { return __all_sync(0xffffffffu, v); }
 
 __global__ void __launch_bounds__(kThreads, 1)
     latent_expand_kernel(const __grid_constant__ CUtensorMap kmap,
@@ -168,6 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw + (((raw + 1023u) & ~1023u) - raw));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x & 1;  // in the pair
   WaitCtl* ctl = &sm.wait;
   if (tid == 0) {
     for (int i = 0; i < kChunks; ++i) {
@@ -180,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.d_full[i], 1);
-      mbar_init(&sm.d_empty[i], kEpiWarps);
+      mbar_init(&sm.d_empty[i], 2 * kEpiWarps);
     }
     mbar_init(&sm.drained, 1);
     sm.wait.abort = 0;
@@ -195,27 +252,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   plan_range(p, sm);
   if (p.early_plan) grid_dependency_wait();
   allow_dependent_launch();
-  if (sm.range_lo >= sm.range_hi) return;
+  if (sm.range_lo >= sm.range_hi) return;  // (so does the pair's other CTA)
   if (warp == kWarpMma) {
-    tmem_alloc(&sm.tmem_base, 512);
-    tmem_relinquish();
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
+  cluster_barrier();  // both CTAs' barriers are ready
   tc_fence_after();
-  const uint32_t tmem = sm.tmem_base;
+  const uint32_t tmem = __reduce_max_sync(0xffffffffu, sm.tmem_base);
   Walk w;
   w.start(sm);
 
   if (warp == kWarpLoad) {
     // =========================== copies ===================================
+    const bool leader = elect_one();
     const int oob_row = p.num_blocks * kBlockSize;
-    int n_tile = 0, n_b = 0, chunks = 0;  // runs and weight pieces so far; chunks of run n_tile
+    int n_tile = 0, chunks = 0;  // runs so far; chunks of run n_tile
+    int n_b = 0, st = 0, phase = 1;  // weight pieces; their stage and the parity it waits for
     bool ok = true;
     while (ok && w.next(p, sm)) {
-      // Lane b < 8 copies block b of each chunk; blocks past the end are read at
-      // a row outside the pool, which fills zeros.
-      const int blk = w.tile * (kKeys / kBlockSize) + lane;
+      // Lane b < 8 holds the row of block b; blocks past the end are read at a row
+      // outside the pool, which fills zeros.
+      const int blk = w.tile * (kPairKeys / kBlockSize) + rank * (kKeys / kBlockSize) + lane;
       int row = oob_row;
       if (lane < 8 && blk * kBlockSize < w.a.keys) {
         const int id = __ldg(p.block_tables + (long long)w.req * p.max_blocks + blk);
@@ -223,32 +285,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         else record_error(p.err, kErrBounds);
       }
       chunks = 0;
-      for (int h = w.h0; h < w.h1 && ok; ++h) {
-        for (int i = 0; i < 2 * kChunks; ++i) {
-          const int c = i % kChunks;
-          if (h == w.h0 && i < kChunks) {
-            if (n_tile > 0) ok = mbar_wait(&sm.a_empty[c], (n_tile - 1) & 1, p.err, ctl);
+      #pragma unroll 1
+      for (int h = w.h0; h < w.h1; ++h) {
+        #pragma unroll 1
+        for (int c = 0; c < kChunks; ++c) {
+          if (h == w.h0) {
+            if (n_tile > 0) ok = all_of(wait_for(&sm.a_empty[c], (n_tile - 1) & 1, p.err, ctl));
             if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(&sm.a_full[c], kChunkBytes);
+            if (leader && rank == 0) mbar_arrive_expect_tx(&sm.a_full[c], 2 * kChunkBytes);
             __syncwarp();
-            if (lane < 8) tma_load_2d(sm.a[c] + lane * 2048, &kmap, c * 64, row, &sm.a_full[c]);
+            if (lane < 8) tma_load_2d_pair(sm.a[c] + lane * 2048, &kmap, c * 64, row, first_cta(&sm.a_full[c]));
+            __syncwarp();
             ++chunks;
           }
-          const int st = n_b % kStages;
-          if (n_b >= kStages) ok = mbar_wait(&sm.b_empty[st], ((n_b / kStages) - 1) & 1, p.err, ctl);
+          ok = all_of(wait_for(&sm.b_empty[st], phase, p.err, ctl));
           if (!ok) break;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&sm.b_full[st], kChunkBytes);
-            tma_load_3d(sm.b[st], &wmap, c * 64, h * kOut + (i / kChunks) * kHalf, 0, &sm.b_full[st]);
+          if (leader) {
+            if (rank == 0) mbar_arrive_expect_tx(&sm.b_full[st], 2 * kChunkBytes);
+            tma_load_3d_pair(sm.b[st], &wmap, c * 64, h * kOut + rank * kHalf, 0, first_cta(&sm.b_full[st]));
           }
-          ++n_b;
           __syncwarp();
+          ++n_b;
+          if (++st == kStages) st = 0, phase ^= 1;
         }
+        if (!ok) break;
       }
       if (ok) ++n_tile, chunks = 0;
     }
-    if (!ok) {
-      // Aborted: the copies in flight must land before the CTA ends.
+    if (!ok && rank == 0) {
+      // Aborted: the copies in flight must land before the pair ends (the barrier
+      // at the end keeps the other CTA's memory until then).
       for (int i = max(0, n_b - kStages); i < n_b; ++i)
         mbar_wait_drain(&sm.b_full[i % kStages], (i / kStages) & 1, p.err, ctl);
       for (int c = 0; c < kChunks; ++c) {
@@ -256,58 +322,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n > 0) mbar_wait_drain(&sm.a_full[c], (n - 1) & 1, p.err, ctl);
       }
     }
-  } else if (warp == kWarpMma) {
+  } else if (warp == kWarpMma && rank == 0) {
     // ============================ MMAs ====================================
-    constexpr uint32_t kIdesc = idesc_bf16_f32(kKeys, kHalf, 0, 0);
-    int n_tile = 0, n_b = 0, n_d = 0;
+    constexpr uint32_t kIdesc = idesc_bf16_f32(kPairKeys, kOut, 0, 0);
+    const uint64_t desc_a = smem_desc_sw128(smem_u32(sm.a[0]), 16, 1024);
+    const uint64_t desc_b = smem_desc_sw128(smem_u32(sm.b[0]), 16, 1024);
+    const bool leader = elect_one();
+    int n_tile = 0, n_d = 0, st = 0, phase = 0;
     bool ok = true;
     while (ok && w.next(p, sm)) {
-      for (int h = w.h0; h < w.h1 && ok; ++h, ++n_d) {
+      #pragma unroll 1
+      for (int h = w.h0; h < w.h1; ++h, ++n_d) {
         const int d = n_d & 1;
-        if (n_d >= 2) ok = mbar_wait(&sm.d_empty[d], ((n_d >> 1) - 1) & 1, p.err, ctl);
-        for (int i = 0; i < 2 * kChunks && ok; ++i) {
-          const int c = i % kChunks, half = i / kChunks, st = n_b % kStages;
-          if (h == w.h0 && half == 0) ok = mbar_wait(&sm.a_full[c], n_tile & 1, p.err, ctl);
-          ok = ok && mbar_wait(&sm.b_full[st], (n_b / kStages) & 1, p.err, ctl);
+        if (n_d >= 2) ok = all_of(wait_for(&sm.d_empty[d], ((n_d >> 1) - 1) & 1, p.err, ctl));
+        #pragma unroll 1
+        for (int c = 0; c < kChunks && ok; ++c) {
+          if (h == w.h0) ok = all_of(wait_for(&sm.a_full[c], n_tile & 1, p.err, ctl));
+          ok = ok && all_of(wait_for(&sm.b_full[st], phase, p.err, ctl));
           if (!ok) break;
           tc_fence_after();
-          if (elect_one()) {
+          if (leader) {
+            const uint64_t da = desc_a + (uint64_t)(c * (kChunkBytes >> 4));
+            const uint64_t db = desc_b + (uint64_t)(st * (kChunkBytes >> 4));
             #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t da = smem_desc_sw128(smem_u32(sm.a[c]) + kk * 32, 16, 1024);
-              const uint64_t db = smem_desc_sw128(smem_u32(sm.b[st]) + kk * 32, 16, 1024);
-              tc_mma_f16_ss(tmem + d * kOut + half * kHalf, da, db, kIdesc, c > 0 || kk > 0);
-            }
-            tc_commit(&sm.b_empty[st]);
-            if (h == w.h1 - 1 && half == 1) tc_commit(&sm.a_empty[c]);
-            if (i == 2 * kChunks - 1) tc_commit(&sm.d_full[d]);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_pair(tmem + d * kOut, da + 2 * kk, db + 2 * kk, kIdesc, c > 0 || kk > 0);
+            commit_pair(&sm.b_empty[st]);
+            if (h == w.h1 - 1) commit_pair(&sm.a_empty[c]);
+            if (c == kChunks - 1) commit_pair(&sm.d_full[d]);
           }
           __syncwarp();
-          ++n_b;
+          if (++st == kStages) st = 0, phase ^= 1;
         }
+        if (!ok) break;
       }
       ++n_tile;
     }
     if (!ok) {
       // Aborted: the issued MMAs must end before TMEM is freed.
-      if (elect_one()) tc_commit(&sm.drained);
+      if (leader) commit_pair(&sm.drained);
       __syncwarp();
       mbar_wait_drain(&sm.drained, 0, p.err, ctl);
     }
-  } else {
+  } else if (warp < kEpiWarps) {
     // ====================== rounding and stores (warps 0-3) ==================
     const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
     uint8_t* mine = sm.row[tid];
     int n_d = 0;
     bool ok = true;
     while (ok && w.next(p, sm)) {
-      const int key = w.tile * kKeys + tid;
-      const bool live = key < w.a.keys;
-      const long long row = w.a.row0 + key;
+      const int key0 = w.tile * kPairKeys + rank * kKeys;  // of this CTA
       if (w.h0 == 0) {
         // The rotated keys of these 128 keys, eight lanes a row.
         for (int i = tid; i < kKeys * 8; i += 32 * kEpiWarps) {
-          const int k = w.tile * kKeys + (i >> 3);
+          const int k = key0 + (i >> 3);
           if (k >= w.a.keys) break;
           const int id = __ldg(p.block_tables + (long long)w.req * p.max_blocks + k / kBlockSize);
           if ((unsigned)id >= (unsigned)p.num_blocks) continue;
@@ -318,21 +386,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int h = w.h0; h < w.h1 && ok; ++h, ++n_d) {
         const int d = n_d & 1;
-        ok = mbar_wait(&sm.d_full[d], (n_d >> 1) & 1, p.err, ctl);
+        ok = wait_for(&sm.d_full[d], (n_d >> 1) & 1, p.err, ctl);
         if (__any_sync(0xffffffffu, !ok)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        __nv_bfloat16* dst = p.kv + (row * p.num_heads + h) * kOut;
+        __nv_bfloat16* dst = p.kv + (((long long)w.a.row0 + key0) * p.num_heads + h) * kOut;
         #pragma unroll 1
         for (int q = 0; q < kOut / kRowCols; ++q) {
           float v[kRowCols / 2], u[kRowCols / 2];
           tmem_ld32(tmem + lane_off + d * kOut + q * kRowCols, v);
           tmem_ld32(tmem + lane_off + d * kOut + q * kRowCols + 32, u);
           tc_wait_ld();
-          // The row's last copy has left shared memory.
-          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();  // the warp has read its rows of before
           #pragma unroll
           for (int i = 0; i < 4; ++i) {
             *reinterpret_cast<uint4*>(mine + 16 * i) =
@@ -342,21 +409,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_uint4(pack_bf16(u[8 * i], u[8 * i + 1]), pack_bf16(u[8 * i + 2], u[8 * i + 3]),
                            pack_bf16(u[8 * i + 4], u[8 * i + 5]), pack_bf16(u[8 * i + 6], u[8 * i + 7]));
           }
-          fence_proxy_async_smem();
-          if (live) bulk_store(dst + q * kRowCols, mine, kRowCols * 2);
-          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          __syncwarp();
+          // Eight lanes a row of 128 bytes, four rows at a time.
+          #pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = warp * 32 + i * 4 + (lane >> 3);
+            if (key0 + r < w.a.keys)
+              *reinterpret_cast<uint4*>(dst + (long long)r * p.num_heads * kOut + q * kRowCols + (lane & 7) * 8) =
+                  *reinterpret_cast<const uint4*>(sm.row[r] + (lane & 7) * 16);
+          }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.d_empty[d]);
+        if (lane == 0) arrive_at(first_cta(&sm.d_empty[d]));
       }
     }
-    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
+  cluster_barrier();  // nothing of either CTA is under way in the other
   tc_fence_after();
-  if (warp == kWarpMma) tmem_dealloc(tmem, 512);
+  if (warp == kWarpMma)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  cluster_barrier();
 }
 
 }  // namespace
@@ -374,15 +449,18 @@ cudaError_t launch_latent_expand(const LatentExpandLaunch& L, cudaStream_t strea
     __atomic_fetch_or(&configured, bit, __ATOMIC_RELEASE);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(L.grid);
+  cfg.gridDim = dim3(L.grid / 2 * 2);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = L.p.pdl ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, latent_expand_kernel, L.kmap, L.wmap, L.p);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();

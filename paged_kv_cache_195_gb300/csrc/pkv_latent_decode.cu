@@ -137,10 +137,6 @@ struct __align__(1024) SmemT {
   WaitCtl wait;
 };
 
-// The same value in all lanes, in a uniform register.
-__device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
-__device__ __forceinline__ bool all_of(bool v) { return __all_sync(0xffffffffu, v); }
-
 // Part i's chunks: 2 i and 2 i + 1, of the last part the one with the rotated keys.
 __host__ __device__ constexpr int part_chunks(int part) { return part == kParts - 1 ? 1 : 2; }
 
@@ -536,11 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (PAIR) cluster_barrier();
 
-  // Columns of the MMAs.  Their operands are to be in uniform registers, for which
-  // the issuing warps' control flow is uniform by construction (votes, reductions)
-  // and one thread guards nothing but the instructions: 24 cycles an MMA of the
-  // scores with 16 columns and 32 with 64, as shared memory allows, for 50 and more
-  // when a single thread runs the loop.
+  // Columns of the MMAs.
   const int n_cols = ((p.group_heads * p.group_tokens + 15) / 16) * 16;
   if (lo >= hi) {
     // no work (nor for the pair's other CTA)

@@ -215,8 +215,6 @@ __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ bool all_of(bool v) { return __all_sync(0xffffffffu, v); }
-
 __global__ void __launch_bounds__(kThreads, 1)
     latent_expand_kernel(const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap wmap, const LatentExpandParams p) {
@@ -263,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_barrier();  // both CTAs' barriers are ready
   tc_fence_after();
-  const uint32_t tmem = __reduce_max_sync(0xffffffffu, sm.tmem_base);
+  const uint32_t tmem = uniform(sm.tmem_base);
   Walk w;
   w.start(sm);
 

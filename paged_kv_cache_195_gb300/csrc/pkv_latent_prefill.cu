@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm.tmem_base;
+  const uint32_t tmem = uniform(sm.tmem_base);
 
   if (warp == kWarpK || warp == kWarpV) {
     // =========================== copies ===================================
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto stream = [&](const Item& it) {
       for (int j = it.t0; j < it.t1; ++j, ++t) {
         const int st = t % kStages;
-        if (t >= kStages && !mbar_wait(&empty[st], ((t / kStages) - 1) & 1, p.err, ctl)) return false;
+        if (t >= kStages && !wait_for(&empty[st], ((t / kStages) - 1) & 1, p.err, ctl)) return false;
         if (lane == 0) {
           const int y = it.k0 + j * kTile;
           if (vside) {
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j == it.t0 && !vside) {
           // The item's queries, once the MMAs of the item before are done with
           // theirs (its first keys are on their way).
-          if (n_item > 0 && !mbar_wait(&sm.q_empty, (n_item - 1) & 1, p.err, ctl)) return false;
+          if (n_item > 0 && !wait_for(&sm.q_empty, (n_item - 1) & 1, p.err, ctl)) return false;
           if (lane == 0) {
             sm.items[n_item % kItems] = it;
             mbar_arrive(&sm.item_full[n_item % kItems]);
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (vside) {
       for (;; ++n_item) {
         const int b = n_item % kItems;
-        ok = mbar_wait(&sm.vitem_full[b], (n_item / kItems) & 1, p.err, ctl);
+        ok = wait_for(&sm.vitem_full[b], (n_item / kItems) & 1, p.err, ctl);
         if (!ok) break;
         const Item it = sm.vitems[b];
         __syncwarp();
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int handed = 0;
       auto hand_over = [&](const Item& it) {
         const int b = handed % kItems;
-        if (handed >= kItems && !mbar_wait(&sm.vitem_empty[b], ((handed / kItems) - 1) & 1, p.err, ctl))
+        if (handed >= kItems && !wait_for(&sm.vitem_empty[b], ((handed / kItems) - 1) & 1, p.err, ctl))
           return false;
         if (lane == 0) {
           sm.vitems[b] = it;
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       Item fin = {};
       fin.end = 1;
       if (ok) ok = hand_over(fin);
-      if (ok && n_item > 0) ok = mbar_wait(&sm.q_empty, (n_item - 1) & 1, p.err, ctl);
+      if (ok && n_item > 0) ok = wait_for(&sm.q_empty, (n_item - 1) & 1, p.err, ctl);
       if (ok && lane == 0) {
         sm.items[n_item % kItems].end = 1;
         mbar_arrive(&sm.item_full[n_item % kItems]);
@@ -460,65 +460,74 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Order: S(t), then PV(t - 1), across items.
     constexpr uint32_t kIdescS = idesc_bf16_f32(kRows, kTile, 0, 0);
     constexpr uint32_t kIdescO = idesc_bf16_f32(kRows, kValDim, 0, 1);
+    constexpr int kStep = kChunkBytes >> 4;
     const uint32_t tO = tmem + 2 * kTile;
-    bool ok = true;
-    int t = 0;
-    auto pv = [&](int tt, int item, bool first, bool last) {
-      const int b = tt & 1, st = tt % kStages;
-      ok = ok && mbar_wait(&sm.p_full[b], (tt >> 1) & 1, p.err, ctl);
-      ok = ok && mbar_wait(&sm.v_full[st], (tt / kStages) & 1, p.err, ctl);
-      if (first && item > 0) ok = ok && mbar_wait(&sm.o_empty, (item - 1) & 1, p.err, ctl);
-      if (!ok) return;
-      tc_fence_after();
-      if (elect_one()) {
-        #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk) {
-          // P: two keys a column, in the first 64 columns of its S buffer.  V is
-          // MN-major: atoms of 64 dims x 8 keys, the chunks kChunkBytes apart.
-          const uint64_t db = smem_desc_sw128(smem_u32(sm.v[st][0]) + kk * 2048, kChunkBytes, 1024);
-          tc_mma_f16_ts(tO, tmem + b * kTile + kk * 8, db, kIdescO, !first || kk > 0);
-        }
-        tc_commit(&sm.v_empty[st]);
-        tc_commit(&sm.p_free[b]);
-        if (last) tc_commit(&sm.o_full);
+    const uint64_t desc_q = smem_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
+    const uint64_t desc_k = smem_desc_sw128(smem_u32(sm.k[0][0]), 16, 1024);
+    // V is MN-major: atoms of 64 dims x 8 keys, the chunks kChunkBytes apart.
+    const uint64_t desc_v = smem_desc_sw128(smem_u32(sm.v[0][0]), kChunkBytes, 1024);
+    const bool leader = elect_one();
+    bool ok = true, first = false;  // first: tile t - 1 began its item
+    int n_item = -1, left = 0;
+    for (int t = 0;; ++t) {
+      const bool fresh = left == 0;  // tile t begins an item
+      bool end = false;
+      if (fresh) {
+        ++n_item;
+        ok = all_of(wait_for(&sm.q_full, n_item & 1, p.err, ctl));
+        if (!ok) break;
+        const Item& it = sm.items[n_item % kItems];
+        end = uniform(it.end) != 0;
+        left = uniform(it.t1 - it.t0);
       }
-      __syncwarp();
-    };
-    bool pend_first = false;
-    for (int n_item = 0;; ++n_item) {
-      ok = ok && mbar_wait(&sm.q_full, n_item & 1, p.err, ctl);
-      if (!ok) break;
-      const Item it = sm.items[n_item % kItems];
-      if (it.end) {
-        if (t > 0) pv(t - 1, n_item - 1, pend_first, true);
-        break;
-      }
-      for (int j = it.t0; j < it.t1 && ok; ++j, ++t) {
+      if (!end) {
         const int b = t & 1, st = t % kStages;
-        ok = ok && mbar_wait(&sm.k_full[st], (t / kStages) & 1, p.err, ctl);
+        ok = wait_for(&sm.k_full[st], (t / kStages) & 1, p.err, ctl);
         // S buffer b holds P(t - 2) until its product is done.
-        if (t >= 2) ok = ok && mbar_wait(&sm.p_free[b], ((t >> 1) - 1) & 1, p.err, ctl);
+        if (t >= 2) ok = ok && wait_for(&sm.p_free[b], ((t >> 1) - 1) & 1, p.err, ctl);
+        ok = all_of(ok);
         if (!ok) break;
         tc_fence_after();
-        if (elect_one()) {
+        if (leader) {
+          const uint64_t db = desc_k + (uint64_t)(st * (kKChunks * kStep));
           #pragma unroll
-          for (int kk = 0; kk < kQDim / 16; ++kk) {
-            const uint64_t da = smem_desc_sw128(smem_u32(sm.q[kk >> 2]) + (kk & 3) * 32, 16, 1024);
-            const uint64_t db = smem_desc_sw128(smem_u32(sm.k[st][kk >> 2]) + (kk & 3) * 32, 16, 1024);
-            tc_mma_f16_ss(tmem + b * kTile, da, db, kIdescS, kk > 0);
-          }
+          for (int kk = 0; kk < kQDim / 16; ++kk)
+            tc_mma_f16_ss(tmem + b * kTile, desc_q + ((kk >> 2) * kStep + 2 * (kk & 3)),
+                          db + ((kk >> 2) * kStep + 2 * (kk & 3)), kIdescS, kk > 0);
           tc_commit(&sm.k_empty[st]);
           tc_commit(&sm.s_full[b]);
-          if (j == it.t1 - 1) tc_commit(&sm.q_empty);
+          if (left == 1) tc_commit(&sm.q_empty);
         }
         __syncwarp();
-        if (t > 0) pv(t - 1, j == it.t0 ? n_item - 1 : n_item, pend_first, j == it.t0);
-        pend_first = j == it.t0;
+        --left;
       }
+      if (t > 0) {
+        // PV of tile t - 1: the last of its item if tile t begins another.
+        const int b = (t - 1) & 1, st = (t - 1) % kStages, item = fresh ? n_item - 1 : n_item;
+        ok = wait_for(&sm.v_full[st], ((t - 1) / kStages) & 1, p.err, ctl);
+        if (first && item > 0) ok = ok && wait_for(&sm.o_empty, (item - 1) & 1, p.err, ctl);
+        ok = ok && wait_for(&sm.p_full[b], ((t - 1) >> 1) & 1, p.err, ctl);
+        ok = all_of(ok);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          const uint64_t db = desc_v + (uint64_t)(st * (kVChunks * kStep));
+          #pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            // P: two keys a column, in the first 64 columns of its S buffer.
+            tc_mma_f16_ts(tO, tmem + b * kTile + kk * 8, db + kk * (2048 >> 4), kIdescO, !first || kk > 0);
+          tc_commit(&sm.v_empty[st]);
+          tc_commit(&sm.p_free[b]);
+          if (fresh) tc_commit(&sm.o_full);
+        }
+        __syncwarp();
+      }
+      if (end) break;
+      first = fresh;
     }
     if (!ok) {
       // Aborted: the issued MMAs must end before TMEM is freed.
-      if (elect_one()) tc_commit(&sm.drained);
+      if (leader) tc_commit(&sm.drained);
       __syncwarp();
       mbar_wait_drain(&sm.drained, 0, p.err, ctl);
     }
@@ -533,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int t = 0;
     bool ok = true;
     for (int n_item = 0;; ++n_item) {
-      const bool have = mbar_wait(&sm.item_full[n_item % kItems], (n_item / kItems) & 1, p.err, ctl);
+      const bool have = wait_for(&sm.item_full[n_item % kItems], (n_item / kItems) & 1, p.err, ctl);
       const Item it = sm.items[n_item % kItems];
       // Agree before any barrier: a wait that gave up stops everyone.
       if (barrier_or(kBarSoft, kSoftThreads, !have || it.end)) break;
@@ -544,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = it.t0; j < it.t1; ++j, ++t) {
         const int sb = t & 1;
         const uint32_t tS = tmem + lane_off + sb * kTile;
-        ok = ok && mbar_wait(&sm.s_full[sb], (t >> 1) & 1, p.err, ctl);
+        ok = ok && wait_for(&sm.s_full[sb], (t >> 1) & 1, p.err, ctl);
         tc_fence_after();
         const int kbase = j * kTile + part * kPartKeys;
         float v[kPartKeys];
@@ -584,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float m_new = grow ? mx : m;
           if (j > it.t0 && __any_sync(0xffffffffu, grow)) {
             // O and l move to the new reference; O must hold the tile before.
-            ok = ok && mbar_wait(&sm.p_free[(t - 1) & 1], ((t - 1) >> 1) & 1, p.err, ctl);
+            ok = ok && wait_for(&sm.p_free[(t - 1) & 1], ((t - 1) >> 1) & 1, p.err, ctl);
             tc_fence_after();
             const float alpha = grow && m != -INFINITY ? fast_exp2(m - m_new) : 1.f;
             rescale_o32(tO, alpha);
@@ -615,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_wait_st();
         l += (sum_lo[0] + sum_hi[0]) + (sum_lo[1] + sum_hi[1]);
         if ((j + 1) * kTile > it.pos0 + 1) {
-          ok = ok && mbar_wait(&sm.v_full[t % kStages], (t / kStages) & 1, p.err, ctl);
+          ok = ok && wait_for(&sm.v_full[t % kStages], (t / kStages) & 1, p.err, ctl);
           clean_values(sm.v[t % kStages], j * kTile, it.pos0, it.nt, bad, warp, lane);
         }
         tc_fence_before();
@@ -628,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float lrow = (sm.xrow[0][row] + sm.xrow[1][row]) + (sm.xrow[2][row] + sm.xrow[3][row]);
       if (it.nt > 1) named_barrier(kBarSoft, kSoftThreads);  // sm.bad is complete
       const unsigned long long gone0 = bad[0], gone1 = bad[1];
-      ok = ok && mbar_wait(&sm.o_full, n_item & 1, p.err, ctl);
+      ok = ok && wait_for(&sm.o_full, n_item & 1, p.err, ctl);
       tc_fence_after();
       {
         float o[32];

@@ -432,7 +432,7 @@ int pkv_append_latent(const void *kv, int64_t kv_stride, const int64_t *position
 
 /*
  * Bytes of workspace for pkv_attention_latent and pkv_attention_expanded: the same for all dims on a
- * device (about 40 MB).  Its first 256 bytes must be zero before the first call
+ * device (about 40 MB).  Its first 128 bytes must be zero before the first call
  * with it, and after a call that ended with PKV_ERR_TIMEOUT; calls leave them
  * zero.  The rest needs no initialisation, and nothing in it is kept from one
  * call for the next: one workspace serves any calls (and captured graphs) that

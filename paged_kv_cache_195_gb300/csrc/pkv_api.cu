@@ -331,9 +331,10 @@ LatentGroups latent_groups(const pkv_dims* d) {
   return l;
 }
 
-// The workspace: the prefill's work queue (zero between calls), then records,
-// statistics and outputs of the pieces of rows that are cut, written anew by
-// every call.
+// The workspace: the prefill's work queue (zero between calls) and, from byte 128
+// on, its count of pieces; then records, statistics and outputs of the pieces of
+// rows that are cut, written anew by every call.  The prefill's statistics and
+// outputs (twice 128 x 130 numbers an SM) take the room of the decode's outputs.
 struct LatentLayout {
   size_t piece, ml, o, total;
 };
@@ -1348,8 +1349,10 @@ int pkv_attention_expanded(const void* q, const void* kv, const void* k_rope, co
   p.kv_start = kv_start_loc;
   p.kv = static_cast<const __nv_bfloat16*>(kv);
   p.out = static_cast<__nv_bfloat16*>(out);
-  p.piece_ml = reinterpret_cast<float*>(ws + w.ml);
-  p.piece_o = reinterpret_cast<float*>(ws + w.o);
+  p.piece = reinterpret_cast<int*>(ws + w.piece);
+  p.num_pieces = reinterpret_cast<int*>(ws + 128);
+  p.piece_ml = reinterpret_cast<float*>(ws + w.o);
+  p.piece_o = p.piece_ml + 4 * (size_t)st->sm_count * 128;
   p.sched = reinterpret_cast<unsigned long long*>(ws);
   p.err = st->err;
   p.num_reqs = dims->num_reqs;
@@ -1357,9 +1360,10 @@ int pkv_attention_expanded(const void* q, const void* kv, const void* k_rope, co
   p.num_rows = num_rows;
   p.num_heads = heads;
   // Items are split, and the joining kernel follows, only where the step's rows,
-  // were they all in use, are fewer items than CTAs.
+  // were they all in use, are fewer items than CTAs, and an item can see more keys
+  // than are worth two pieces.
   const long long items = ((long long)dims->num_q_tokens + 127) / 128 * heads;
-  p.max_pieces = items < st->sm_count ? 2 * st->sm_count : 0;
+  p.max_pieces = items < st->sm_count && num_rows > 1024 ? 2 * st->sm_count : 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.pdl = opt.pdl != 0;
   p.early_plan = p.pdl && opt.early_plan != 0;

@@ -152,6 +152,8 @@ struct LatentPrefillParams {
   const __nv_bfloat16* kv;     // [num_rows, H, 256]: key | value
   __nv_bfloat16* out;          // [num_q_tokens, H, 128]
   // Partial states of items split over their keys, by piece number.
+  int* piece;                  // [max_pieces][4]: pieces of the item (first pieces only), its rows, head
+  int* num_pieces;
   float* piece_ml;             // [max_pieces][128][2]
   float* piece_o;              // [max_pieces][128][128]
   unsigned long long* sched;   // [0] next piece, [1] CTAs done; zero between launches

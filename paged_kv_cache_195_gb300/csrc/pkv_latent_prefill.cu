@@ -134,14 +134,13 @@ __device__ __forceinline__ long long warp_sum(long long v) {
 // Key tiles of a piece, from the step's items: whole while they are enough for
 // the grid (or there is no room for more), else the key tiles in equal parts.
 // One warp; also counts the pieces.
-__device__ __forceinline__ int plan_split(const LatentPrefillParams& p, int grid, bool report,
-                                          long long* pieces) {
+__device__ __forceinline__ int plan_split(const LatentPrefillParams& p, int grid, long long* pieces) {
   const int lane = threadIdx.x & 31;
   long long items = 0, tiles = 0;
   for (int r = lane; r < p.num_reqs; r += 32) {
     bool bad;
     const Req a = load_req(p, r, &bad);
-    if (bad && report) record_error(p.err, kErrBounds);  // the request is skipped
+    if (bad && blockIdx.x == 0) record_error(p.err, kErrBounds);  // the request is skipped
     items += (long long)a.nq * p.num_heads;
     if (p.max_pieces > 0)
       for (int i = 0; i < a.nq; ++i) tiles += (long long)item_tiles(a, i) * p.num_heads;
@@ -338,10 +337,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&rmap);
   }
   if (!p.early_plan) grid_dependency_wait();
+  int first_pieces = 0;
   if (warp == kWarpK) {
     long long pieces;
-    const int split = plan_split(p, gridDim.x, blockIdx.x == 0, &pieces);
+    const int split = plan_split(p, gridDim.x, &pieces);
     if (lane == 0) {
+      if (blockIdx.x == 0) first_pieces = split != INT_MAX ? (int)pieces : 0;
       sm.split = split;
       sm.active = (int)min(pieces, (long long)gridDim.x);
     }
@@ -349,6 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (p.early_plan) grid_dependency_wait();
   allow_dependent_launch();
+  // How many pieces the joining kernel has to look at.
+  if (p.max_pieces > 0 && blockIdx.x == 0 && tid == 32 * kWarpK) *p.num_pieces = first_pieces;
   const int active = sm.active, split = sm.split;
   if ((int)blockIdx.x >= active) return;
   if (warp == kWarpMma) {
@@ -437,6 +440,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         Item it;
         int of;
         if (!f.find(p, split, (long long)v, &it, &of)) break;
+        // For the joining kernel: every piece's record is written anew by whoever
+        // takes it.
+        if (split != INT_MAX && lane == 0)
+          *reinterpret_cast<int4*>(p.piece + 4 * v) = make_int4(of, it.row0, it.nt, it.head);
         ok = hand_over(it) && stream(it);
       }
       Item fin = {};
@@ -697,26 +704,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 // number b, if any; a warp a row, four dims a lane.
 constexpr int kMergeWarps = 8;
 
-__global__ void __launch_bounds__(32 * kMergeWarps) latent_prefill_merge_kernel(const LatentPrefillParams p, int grid) {
-  if (!p.early_plan) grid_dependency_wait();
-  const int lane = threadIdx.x & 31;
-  long long pieces;
-  const int split = plan_split(p, grid, false, &pieces);
-  Item it;
-  int of = 0;
-  bool mine = false;
-  if (split != INT_MAX && blockIdx.x < pieces) {
-    Finder f;
-    f.start(p, split);
-    mine = f.find(p, split, blockIdx.x, &it, &of) && of > 0;
-  }
-  if (p.early_plan) grid_dependency_wait();
+__global__ void __launch_bounds__(32 * kMergeWarps) latent_prefill_merge_kernel(const LatentPrefillParams p) {
+  grid_dependency_wait();
   allow_dependent_launch();
-  const int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
-  if (!mine || row >= it.nt) return;
+  const int lane = threadIdx.x & 31, row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  const int4 rec = *reinterpret_cast<const int4*>(p.piece + 4 * blockIdx.x);  // pieces, row0, nt, head
+  if ((int)blockIdx.x >= *p.num_pieces || rec.x == 0 || row >= rec.z) return;
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = 0; i < of; ++i) {
+  #pragma unroll 4
+  for (int i = 0; i < rec.x; ++i) {
     const long long at = (long long)(blockIdx.x + i) * kRows + row;
     const float2 ml = *reinterpret_cast<const float2*>(p.piece_ml + at * 2);
     const float4 v = reinterpret_cast<const float4*>(p.piece_o + at * kValDim)[lane];
@@ -734,7 +731,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_prefill_merge_kernel(
   uint2 w;
   w.x = pack_bf16(o.x * inv, o.y * inv);
   w.y = pack_bf16(o.z * inv, o.w * inv);
-  reinterpret_cast<uint2*>(p.out + ((long long)(it.row0 + row) * p.num_heads + it.head) * kValDim)[lane] = w;
+  reinterpret_cast<uint2*>(p.out + ((long long)(rec.y + row) * p.num_heads + rec.w) * kValDim)[lane] = w;
 }
 
 }  // namespace
@@ -766,7 +763,7 @@ cudaError_t launch_latent_prefill(const LatentPrefillLaunch& L, cudaStream_t str
   cfg.gridDim = dim3(L.p.max_pieces, kRows / kMergeWarps);
   cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, latent_prefill_merge_kernel, L.p, L.grid);
+  e = cudaLaunchKernelEx(&cfg, latent_prefill_merge_kernel, L.p);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

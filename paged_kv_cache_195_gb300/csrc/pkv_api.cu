@@ -1377,6 +1377,9 @@ int pkv_attention_expanded(const void* q, const void* kv, const void* k_rope, co
     rc = encode_bf16_3d(&L.rmap, k_rope, pkv::kRopeDim, num_rows, 1, pkv::kRopeDim,
                         (long long)num_rows * pkv::kRopeDim, rbox, "k_rope");
   if (rc != PKV_OK) return rc;
+  // In pairs where chunks are long enough for two query tiles on average, and enough.
+  L.pairs = dims->num_q_tokens >= 192ll * dims->num_reqs &&
+            (long long)dims->num_q_tokens * heads >= 256ll * st->sm_count;
   L.grid = st->sm_count;
   const cudaError_t e = pkv::launch_latent_prefill(L, stream);
   if (e != cudaSuccess) return cuda_fail(e, "expanded attention launch");

@@ -171,6 +171,7 @@ struct LatentPrefillLaunch {
   CUtensorMap kvmap;  // kv as [rows][H][256], same box
   CUtensorMap rmap;   // k_rope as [1][rows][64], box (64, 128, 1)
   LatentPrefillParams p;
+  int pairs;          // two query tiles of a head by two CTAs, keys and values by multicast
   int grid;
 };
 

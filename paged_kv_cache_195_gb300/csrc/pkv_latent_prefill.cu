@@ -13,7 +13,12 @@
 // S there and O += P V (8 MMAs, A from TMEM) accumulates in 128 columns.  Four
 // threads a row run the softmax, 32 keys each; the row maximum moves, and O is
 // rescaled, only when a score exceeds it by 2^8, on a vote of the four warps that
-// hold the same rows.  Keys and values have rings of their own, two stages each.
+// hold the same rows.  Keys and values have rings of their own, of 64-dim chunks,
+// each of which goes back as soon as its MMAs are done.
+// Steps of long chunks run in pairs of CTAs: the pair takes two query tiles of one
+// head, a CTA each, and every key tile comes in once for both, by multicast.  Alone,
+// 152 CTAs read 80 KB a tile each, 11 TB/s from L2, and that set the pace (1.09 us a
+// tile).
 //
 // Order.  Items come from a queue, longest requests first, a head's query tiles
 // one after the other (the CTAs that run them at one time read the same keys:
@@ -23,7 +28,8 @@
 //
 // A value that only some rows of an item see must not reach the others, whatever
 // it holds (0 * NaN): rows of V with a NaN or infinity among the item's own
-// tokens are taken out and added to the rows that see them at the end.
+// tokens are taken out, by the warp that copies them, and added to the rows that
+// see them at the end.
 #include <climits>
 
 #include "pkv_latent.h"
@@ -37,9 +43,10 @@ constexpr int kPartKeys = 128 / kParts;  // keys, and output dims, of each
 constexpr int kSoftWarps = 4 * kParts;
 constexpr int kSoftThreads = 32 * kSoftWarps;
 constexpr int kWarpK = kSoftWarps;       // items, Q, keys
-constexpr int kWarpMma = kSoftWarps + 1;
+constexpr int kWarpS = kSoftWarps + 1;   // MMAs of the scores
 constexpr int kWarpV = kSoftWarps + 2;   // values
-constexpr int kThreads = 32 * (kSoftWarps + 3);
+constexpr int kWarpO = kSoftWarps + 3;   // MMAs of the outputs
+constexpr int kThreads = 32 * (kSoftWarps + 4);  // five warps a quarter SM: up to 96 registers
 constexpr int kBarSoft = 1;              // all softmax warps
 constexpr int kBarQuad = 2;              // + quad: the four warps with the same rows
 
@@ -49,7 +56,8 @@ constexpr int kChunkBytes = 128 * 128;
 constexpr int kQDim = kNope + kRopeDim;
 constexpr int kKChunks = kQDim / 64;
 constexpr int kVChunks = kValDim / 64;
-constexpr int kStages = 2;
+constexpr int kRingK = 7;                // chunks in flight: two tiles and a third of keys, ...
+constexpr int kRingV = 2 * kVChunks;     // ... two tiles of values
 constexpr int kItems = 4;
 constexpr uint32_t kTmemCols = 512;      // S: columns 0 .. 255, O: 256 .. 383
 constexpr float kRescaleLog2 = 8.0f;
@@ -68,23 +76,25 @@ struct Item {
 
 struct __align__(1024) Smem {
   uint8_t q[kKChunks][kChunkBytes];
-  uint8_t k[kStages][kKChunks][kChunkBytes];
-  uint8_t v[kStages][kVChunks][kChunkBytes];
+  uint8_t k[kRingK][kChunkBytes];
+  uint8_t v[kRingV][kChunkBytes];
   uint64_t q_full, q_empty;
-  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t k_full[kRingK], k_empty[kRingK], v_full[kRingV], v_empty[kRingV];
   uint64_t s_full[2], p_full[2], p_free[2];
   uint64_t o_full, o_empty;
-  uint64_t item_full[kItems], vitem_full[kItems], vitem_empty[kItems];
-  uint64_t drained;
+  uint64_t item_full[kItems], vitem_full[kItems], vitem_empty[kItems], next_full[kItems];
+  uint64_t drained[2];
   Item items[kItems], vitems[kItems];
+  unsigned long long next[kItems];    // a pair: the piece's number, from its first CTA
   float xrow[kParts][kRows];
-  unsigned long long bad[2][2];  // own tokens whose values were taken out, by item parity
+  unsigned long long bad[kItems][2];  // own tokens whose values were taken out
   uint32_t tmem_base;
   int active;  // CTAs that take pieces
   int split;   // key tiles of a piece (INT_MAX: items are whole)
   WaitCtl wait;
 };
-static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "latent prefill shared memory");
+// (no room to align it in: a block without static shared memory has it on a KiB)
+static_assert(sizeof(Smem) <= 227 * 1024, "latent prefill shared memory");
 
 __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
 
@@ -98,6 +108,8 @@ struct Req {
   int nq;  // query tiles of a head (0: nothing to do)
 };
 
+// GROUP: query tokens of an item (of a pair's two).
+template <int GROUP>
 __device__ __forceinline__ Req load_req(const LatentPrefillParams& p, int r, bool* bad) {
   Req a;
   a.q0 = __ldg(p.qsl + r);
@@ -108,20 +120,22 @@ __device__ __forceinline__ Req load_req(const LatentPrefillParams& p, int r, boo
   a.qr = q1 - a.q0;
   *bad = !(a.q0 >= 0 && a.qr >= 0 && q1 <= p.num_q_tokens && a.qr <= a.L && a.k0 >= 0 &&
            k1 <= p.num_rows && k1 - a.k0 == a.L);
-  a.nq = *bad ? 0 : cdiv(a.qr, kRows);
+  a.nq = *bad ? 0 : cdiv(a.qr, GROUP);
   return a;
 }
 
-// Key tiles of query tile i.
+// Key tiles of query tile (or pair) i.
+template <int GROUP>
 __device__ __forceinline__ int item_tiles(const Req& a, int i) {
-  return cdiv(a.L - a.qr + min((i + 1) * kRows, a.qr), kTile);
+  return cdiv(a.L - a.qr + min((i + 1) * GROUP, a.qr), kTile);
 }
 
 // Pieces of a request's head.
+template <int GROUP>
 __device__ __forceinline__ int head_pieces(const Req& a, int split) {
   if (split == INT_MAX) return a.nq;
   int n = 0;
-  for (int i = 0; i < a.nq; ++i) n += cdiv(item_tiles(a, i), split);
+  for (int i = 0; i < a.nq; ++i) n += cdiv(item_tiles<GROUP>(a, i), split);
   return n;
 }
 
@@ -134,16 +148,17 @@ __device__ __forceinline__ long long warp_sum(long long v) {
 // Key tiles of a piece, from the step's items: whole while they are enough for
 // the grid (or there is no room for more), else the key tiles in equal parts.
 // One warp; also counts the pieces.
+template <int GROUP>
 __device__ __forceinline__ int plan_split(const LatentPrefillParams& p, int grid, long long* pieces) {
   const int lane = threadIdx.x & 31;
   long long items = 0, tiles = 0;
   for (int r = lane; r < p.num_reqs; r += 32) {
     bool bad;
-    const Req a = load_req(p, r, &bad);
+    const Req a = load_req<GROUP>(p, r, &bad);
     if (bad && blockIdx.x == 0) record_error(p.err, kErrBounds);  // the request is skipped
     items += (long long)a.nq * p.num_heads;
     if (p.max_pieces > 0)
-      for (int i = 0; i < a.nq; ++i) tiles += (long long)item_tiles(a, i) * p.num_heads;
+      for (int i = 0; i < a.nq; ++i) tiles += (long long)item_tiles<GROUP>(a, i) * p.num_heads;
   }
   items = warp_sum(items);
   *pieces = items;
@@ -154,7 +169,7 @@ __device__ __forceinline__ int plan_split(const LatentPrefillParams& p, int grid
   long long n = 0;
   for (int r = lane; r < p.num_reqs; r += 32) {
     bool bad;
-    n += (long long)head_pieces(load_req(p, r, &bad), split) * p.num_heads;
+    n += (long long)head_pieces<GROUP>(load_req<GROUP>(p, r, &bad), split) * p.num_heads;
   }
   *pieces = warp_sum(n);
   return split;
@@ -163,6 +178,7 @@ __device__ __forceinline__ int plan_split(const LatentPrefillParams& p, int grid
 // Finds pieces by number, forward.  Pieces are numbered by batches of 32
 // requests, within a batch the longest request first, then head by head, then
 // from the last query tile to the first, then along the keys.  One warp.
+template <int GROUP>
 struct Finder {
   int batch;       // first request of the batch
   long long base;  // pieces before it
@@ -174,8 +190,8 @@ struct Finder {
     const int lane = threadIdx.x & 31, r = batch + lane;
     bool bad;
     a = Req{0, 0, 0, 0, 0};
-    if (r < p.num_reqs) a = load_req(p, r, &bad);
-    per_head = head_pieces(a, split);
+    if (r < p.num_reqs) a = load_req<GROUP>(p, r, &bad);
+    per_head = head_pieces<GROUP>(a, split);
     cnt = (long long)per_head * p.num_heads;
     total = warp_sum(cnt);
     const int key = cnt > 0 ? a.L : -1;
@@ -193,7 +209,8 @@ struct Finder {
     load(p, split);
   }
   // Numbers must not decrease from call to call.  False: there is no such piece.
-  __device__ __forceinline__ bool find(const LatentPrefillParams& p, int split, long long piece,
+  // (rank: which of a pair's query tiles)
+  __device__ __forceinline__ bool find(const LatentPrefillParams& p, int split, long long piece, int rank,
                                        Item* it, int* of) {
     while (piece >= base + total) {
       base += total;
@@ -218,12 +235,13 @@ struct Finder {
       i -= x;
       x = 0;
     } else {
-      for (; (n = cdiv(item_tiles(b, i), split)) <= x; --i) x -= n;
+      for (; (n = cdiv(item_tiles<GROUP>(b, i), split)) <= x; --i) x -= n;
     }
-    const int tiles = item_tiles(b, i);
-    it->row0 = b.q0 + i * kRows;
-    it->nt = min(kRows, b.qr - i * kRows);
-    it->pos0 = b.L - b.qr + i * kRows;
+    const int tiles = item_tiles<GROUP>(b, i);
+    const int first = i * GROUP + rank * kRows;  // (past the request's tokens: a pair's second may have none)
+    it->row0 = b.q0 + first;
+    it->nt = min(kRows, b.qr - first);
+    it->pos0 = b.L - b.qr + first;
     it->k0 = b.k0;
     // n pieces of equal length, but for the rounding
     it->t0 = (int)((long long)tiles * x / n);
@@ -252,27 +270,47 @@ __device__ __forceinline__ bool non_finite(uint32_t w) {
 
 // Values of the tile's keys from pos0 + 1 on: those that no row of the item sees
 // (from its last token's position on) become zeros; those of its own tokens that
-// are not finite too, noted in bad.  Half a warp a row.
+// are not finite too, noted in bad.  One warp, half of it a row, eight rows at a time;
+// only where a first look at the rows' exponents finds any that is not finite.
 static __device__ __noinline__ void clean_values(uint8_t (*v)[kChunkBytes], int key0, int pos0, int nt,
-                                                 unsigned long long* bad, int warp, int lane) {
+                                                 unsigned long long* bad, int lane) {
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  const int first = max(pos0 + 1 - key0, 0);
   const int piece = lane & 15;
-  for (int r2 = first + 2 * warp; r2 < kTile; r2 += 2 * kSoftWarps) {
-    const int row = r2 + (lane >> 4);
-    const bool in = row < kTile;
-    const int b = key0 + row - pos0 - 1;  // the item's token b + 1
-    uint4* at = reinterpret_cast<uint4*>(v[piece >> 3] + (in ? row : 0) * 128 +
-                                         (((piece & 7) ^ (row & 7)) << 4));
-    bool hit = false;
-    if (in && b < nt - 1) {
-      const uint4 x = *at;
-      hit = non_finite(x.x) || non_finite(x.y) || non_finite(x.z) || non_finite(x.w);
+  uint32_t top = 0;  // the largest exponents, two to a word
+  #pragma unroll 1
+  for (int r0 = max(pos0 + 1 - key0, 0); r0 < kTile; r0 += 16) {
+    uint4 x[8];
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = min(r0 + 2 * i + (lane >> 4), kTile - 1);
+      x[i] = *reinterpret_cast<uint4*>(v[piece >> 3] + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
     }
-    const unsigned votes = __ballot_sync(0xffffffffu, hit);
-    const bool out = in && (b >= nt - 1 || ((votes >> (lane & 16)) & 0xffffu) != 0);
-    if (out && b < nt - 1 && piece == 0) atomicOr(bad + (b >> 6), 1ull << (b & 63));
-    if (out) *at = zero;
+    #pragma unroll
+    for (int i = 0; i < 8; ++i)
+      top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7f807f80u, x[i].y & 0x7f807f80u),
+                                   __vmaxu2(x[i].z & 0x7f807f80u, x[i].w & 0x7f807f80u)));
+  }
+  if (!__any_sync(0xffffffffu, non_finite(top))) return;
+  #pragma unroll 1
+  for (int r0 = max(pos0 + 1 - key0, 0) + (lane >> 4); __any_sync(0xffffffffu, r0 < kTile); r0 += 8) {
+    uint4* at[4];
+    uint4 x[4];
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = min(r0 + 2 * i, kTile - 1);
+      at[i] = reinterpret_cast<uint4*>(v[piece >> 3] + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
+      x[i] = *at[i];
+    }
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = r0 + 2 * i, b = key0 + row - pos0 - 1;  // the item's token b + 1
+      const bool in = row < kTile, own = b < nt - 1;
+      const bool hit = in && own && (non_finite(x[i].x) || non_finite(x[i].y) || non_finite(x[i].z) || non_finite(x[i].w));
+      const unsigned votes = __ballot_sync(0xffffffffu, hit);
+      const bool out = in && (!own || ((votes >> (lane & 16)) & 0xffffu) != 0);
+      if (out && own && piece == 0) atomicOr(bad + (b >> 6), 1ull << (b & 63));
+      if (out) *at[i] = zero;
+    }
   }
   fence_proxy_async_smem();
 }
@@ -294,30 +332,72 @@ static __device__ __noinline__ void add_bad(const LatentPrefillParams& p, const 
   }
 }
 
+// ------------------------------------------------------------ a pair's plumbing
+// Copies that land in both CTAs of the cluster, at the same place, and count on both
+// barriers; commits that arrive on both.
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".multicast::cluster [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "h"((uint16_t)3)
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Leaves a number in the second CTA's shared memory and arrives on its barrier.
+__device__ __forceinline__ void send(unsigned long long* slot, uint64_t* bar, unsigned long long v) {
+  asm volatile(
+      "{\n\t.reg .b32 a, b;\n\t"
+      "mapa.shared::cluster.u32 a, %0, 1;\n\t"
+      "mapa.shared::cluster.u32 b, %1, 1;\n\t"
+      "st.shared::cluster.u64 [a], %2;\n\t"
+      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [b];\n\t}" ::"r"(smem_u32(slot)),
+      "r"(smem_u32(bar)), "l"(v)
+      : "memory");
+}
+
+template <bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
                           const __grid_constant__ CUtensorMap kvmap,
                           const __grid_constant__ CUtensorMap rmap, const LatentPrefillParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  Smem& sm = *reinterpret_cast<Smem*>(smem_raw + (((raw + 1023u) & ~1023u) - raw));
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+  if ((smem_u32(smem_raw) & 1023u) != 0) {
+    if (threadIdx.x == 0) record_error(p.err, kErrCapacity);
+    return;
+  }
   WaitCtl* ctl = &sm.wait;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int GROUP = PAIR ? 2 * kRows : kRows;
+  const int rank = PAIR ? blockIdx.x & 1 : 0;
 
   if (tid == 0) {
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, 1);
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kRingK; ++s) {
       mbar_init(&sm.k_full[s], 1);
-      mbar_init(&sm.k_empty[s], 1);
+      mbar_init(&sm.k_empty[s], PAIR ? 2 : 1);
+    }
+    for (int s = 0; s < kRingV; ++s) {
       mbar_init(&sm.v_full[s], 1);
-      mbar_init(&sm.v_empty[s], 1);
+      mbar_init(&sm.v_empty[s], PAIR ? 2 : 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sm.s_full[b], 1);
-      mbar_init(&sm.p_full[b], kSoftWarps);
+      mbar_init(&sm.p_full[b], kSoftWarps + 1);
       mbar_init(&sm.p_free[b], 1);
-      sm.bad[b][0] = sm.bad[b][1] = 0;
     }
     mbar_init(&sm.o_full, 1);
     mbar_init(&sm.o_empty, kSoftWarps);
@@ -325,8 +405,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.item_full[b], 1);
       mbar_init(&sm.vitem_full[b], 1);
       mbar_init(&sm.vitem_empty[b], 1);
+      mbar_init(&sm.next_full[b], 1);
     }
-    mbar_init(&sm.drained, 1);
+    mbar_init(&sm.drained[0], 1);
+    mbar_init(&sm.drained[1], 1);
     sm.wait.abort = 0;
     sm.wait.limit_ns = p.wait_limit_ns;
     fence_barrier_init();
@@ -340,11 +422,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   int first_pieces = 0;
   if (warp == kWarpK) {
     long long pieces;
-    const int split = plan_split(p, gridDim.x, &pieces);
+    const int split = plan_split<GROUP>(p, gridDim.x, &pieces);
     if (lane == 0) {
       if (blockIdx.x == 0) first_pieces = split != INT_MAX ? (int)pieces : 0;
       sm.split = split;
-      sm.active = (int)min(pieces, (long long)gridDim.x);
+      sm.active = (int)min(pieces, (long long)(PAIR ? gridDim.x >> 1 : gridDim.x));  // CTAs, or pairs
     }
   }
   __syncthreads();
@@ -353,8 +435,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // How many pieces the joining kernel has to look at.
   if (p.max_pieces > 0 && blockIdx.x == 0 && tid == 32 * kWarpK) *p.num_pieces = first_pieces;
   const int active = sm.active, split = sm.split;
-  if ((int)blockIdx.x >= active) return;
-  if (warp == kWarpMma) {
+  if ((int)(PAIR ? blockIdx.x >> 1 : blockIdx.x) >= active) return;
+  if (warp == kWarpS) {
     tmem_alloc(&sm.tmem_base, kTmemCols);
     tmem_relinquish();
   }
@@ -362,48 +444,75 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(sm.tmem_base);
+  if (PAIR) cluster_barrier();  // both CTAs' barriers are ready
 
   if (warp == kWarpK || warp == kWarpV) {
     // =========================== copies ===================================
     const bool vside = warp == kWarpV;
     uint64_t* const full = vside ? sm.v_full : sm.k_full;
     uint64_t* const empty = vside ? sm.v_empty : sm.k_empty;
+    const int ring = vside ? kRingV : kRingK;
+    const bool leader = elect_one();
     int n_item = 0, t = 0;
+    int n_chunk = 0, slot = 0, phase = 1;  // chunks so far; their slot and the parity it waits for
     bool ok = true;
+    // Tile tt of the item's values, key tile j, has landed: what not every row may
+    // see is taken out.  The arrival, beside the softmax warps', lets the tile's
+    // product begin.
+    auto finish = [&](const Item& it, int j, int tt) {
+      const int first = (tt & 1) * kVChunks;
+      for (int c = first; c < first + kVChunks; ++c)
+        if (!all_of(wait_for(&sm.v_full[c], (tt >> 1) & 1, p.err, ctl))) return false;
+      if ((j + 1) * kTile > it.pos0 + 1)
+        clean_values(sm.v + first, j * kTile, it.pos0, it.nt, sm.bad[n_item % kItems], lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.p_full[tt & 1]);
+      return true;
+    };
     auto stream = [&](const Item& it) {
-      for (int j = it.t0; j < it.t1; ++j, ++t) {
-        const int st = t % kStages;
-        if (t >= kStages && !wait_for(&empty[st], ((t / kStages) - 1) & 1, p.err, ctl)) return false;
-        if (lane == 0) {
-          const int y = it.k0 + j * kTile;
-          if (vside) {
-            mbar_arrive_expect_tx(&full[st], kVChunks * kChunkBytes);
-            for (int c = 0; c < kVChunks; ++c)
-              tma_load_3d(sm.v[st][c], &kvmap, kNope + c * 64, it.head, y, &full[st]);
-          } else {
-            mbar_arrive_expect_tx(&full[st], kKChunks * kChunkBytes);
-            tma_load_3d(sm.k[st][0], &kvmap, 0, it.head, y, &full[st]);
-            tma_load_3d(sm.k[st][1], &kvmap, 64, it.head, y, &full[st]);
-            tma_load_3d(sm.k[st][2], &rmap, 0, y, 0, &full[st]);
+      if (vside && lane < 2) sm.bad[n_item % kItems][lane] = 0;
+      __syncwarp();
+      const int head = uniform(it.head), t1 = uniform(it.t1);
+      int y = uniform(it.k0 + it.t0 * kTile);
+      #pragma unroll 1
+      for (int j = uniform(it.t0); j < t1; ++j, ++t, y += kTile) {
+        const int chunks = vside ? kVChunks : kKChunks;
+        #pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+          if (!all_of(wait_for(&empty[slot], phase, p.err, ctl))) return false;
+          if (leader) {
+            mbar_arrive_expect_tx(&full[slot], kChunkBytes);
+            // A pair's CTAs take turns at the chunks.
+            if (!PAIR || (n_chunk & 1) == rank) {
+              const bool rope = !vside && c == kKChunks - 1;
+              const CUtensorMap* map = rope ? &rmap : &kvmap;
+              const int x = rope ? 0 : (vside ? kNope : 0) + c * 64;
+              const int a = rope ? y : head, b = rope ? 0 : y;
+              void* dst = vside ? sm.v[slot] : sm.k[slot];
+              PAIR ? tma_load_3d_pair(dst, map, x, a, b, &full[slot]) : tma_load_3d(dst, map, x, a, b, &full[slot]);
+            }
           }
+          __syncwarp();
+          ++n_chunk;
+          if (++slot == ring) slot = 0, phase ^= 1;
         }
-        __syncwarp();
         if (j == it.t0 && !vside) {
           // The item's queries, once the MMAs of the item before are done with
           // theirs (its first keys are on their way).
-          if (n_item > 0 && !wait_for(&sm.q_empty, (n_item - 1) & 1, p.err, ctl)) return false;
-          if (lane == 0) {
+          if (n_item > 0 && !all_of(wait_for(&sm.q_empty, (n_item - 1) & 1, p.err, ctl))) return false;
+          if (leader) {
             sm.items[n_item % kItems] = it;
             mbar_arrive(&sm.item_full[n_item % kItems]);
             mbar_arrive_expect_tx(&sm.q_full, kKChunks * kChunkBytes);
             for (int c = 0; c < kKChunks; ++c)
-              tma_load_3d(sm.q[c], &qmap, c * 64, it.head, it.row0, &sm.q_full);
+              tma_load_3d(sm.q[c], &qmap, c * 64, head, it.row0, &sm.q_full);
           }
           ++n_item;
           __syncwarp();
         }
+        if (vside && j > it.t0 && !finish(it, j - 1, t - 1)) return false;
       }
-      return true;
+      return !vside || finish(it, t1 - 1, t - 1);
     };
     if (vside) {
       for (;; ++n_item) {
@@ -431,15 +540,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         return true;
       };
-      Finder f;
+      Finder<GROUP> f;
       f.start(p, split);
-      while (ok) {
+      for (int n = 0; ok; ++n) {
+        // A pair's first CTA takes the number for both.
         unsigned long long v = 0;
-        if (lane == 0) v = atomicAdd(p.sched, 1ull);
-        v = __shfl_sync(0xffffffffu, v, 0);
+        if (!PAIR || rank == 0) {
+          if (lane == 0) v = atomicAdd(p.sched, 1ull);
+          v = __shfl_sync(0xffffffffu, v, 0);
+          if (PAIR && lane == 0) send(&sm.next[n % kItems], &sm.next_full[n % kItems], v);
+        } else {
+          ok = wait_for(&sm.next_full[n % kItems], (n / kItems) & 1, p.err, ctl);
+          if (!ok) break;
+          asm volatile("fence.acq_rel.cluster;" ::: "memory");
+          v = *(volatile unsigned long long*)&sm.next[n % kItems];
+        }
         Item it;
         int of;
-        if (!f.find(p, split, (long long)v, &it, &of)) break;
+        if (!f.find(p, split, (long long)v, rank, &it, &of)) break;
         // For the joining kernel: every piece's record is written anew by whoever
         // takes it.
         if (split != INT_MAX && lane == 0)
@@ -460,83 +578,105 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // Aborted: the copies in flight must land before the CTA ends.
     if (!ok)
-      for (int i = max(0, t - kStages); i < t; ++i)
-        mbar_wait_drain(&full[i % kStages], (i / kStages) & 1, p.err, ctl);
-  } else if (warp == kWarpMma) {
-    // ============================ MMAs ====================================
-    // Order: S(t), then PV(t - 1), across items.
-    constexpr uint32_t kIdescS = idesc_bf16_f32(kRows, kTile, 0, 0);
-    constexpr uint32_t kIdescO = idesc_bf16_f32(kRows, kValDim, 0, 1);
+      for (int i = max(0, n_chunk - ring); i < n_chunk; ++i)
+        mbar_wait_drain(&full[i % ring], (i / ring) & 1, p.err, ctl);
+  } else if (warp == kWarpS) {
+    // ========================= MMAs of the scores =========================
+    constexpr uint32_t kIdesc = idesc_bf16_f32(kRows, kTile, 0, 0);
     constexpr int kStep = kChunkBytes >> 4;
-    const uint32_t tO = tmem + 2 * kTile;
     const uint64_t desc_q = smem_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
-    const uint64_t desc_k = smem_desc_sw128(smem_u32(sm.k[0][0]), 16, 1024);
-    // V is MN-major: atoms of 64 dims x 8 keys, the chunks kChunkBytes apart.
-    const uint64_t desc_v = smem_desc_sw128(smem_u32(sm.v[0][0]), kChunkBytes, 1024);
+    const uint64_t desc_k = smem_desc_sw128(smem_u32(sm.k[0]), 16, 1024);
     const bool leader = elect_one();
-    bool ok = true, first = false;  // first: tile t - 1 began its item
-    int n_item = -1, left = 0;
-    for (int t = 0;; ++t) {
-      const bool fresh = left == 0;  // tile t begins an item
-      bool end = false;
-      if (fresh) {
-        ++n_item;
-        ok = all_of(wait_for(&sm.q_full, n_item & 1, p.err, ctl));
-        if (!ok) break;
-        const Item& it = sm.items[n_item % kItems];
-        end = uniform(it.end) != 0;
-        left = uniform(it.t1 - it.t0);
-      }
-      if (!end) {
-        const int b = t & 1, st = t % kStages;
-        ok = wait_for(&sm.k_full[st], (t / kStages) & 1, p.err, ctl);
+    bool ok = true;
+    int slot = 0, phase = 0;
+    for (int n_item = 0, t = 0;; ++n_item) {
+      ok = all_of(wait_for(&sm.q_full, n_item & 1, p.err, ctl));
+      if (!ok) break;
+      const Item& it = sm.items[n_item % kItems];
+      if (uniform(it.end)) break;
+      #pragma unroll 1
+      for (int left = uniform(it.t1 - it.t0); left > 0; --left, ++t) {
+        const int b = t & 1;
         // S buffer b holds P(t - 2) until its product is done.
-        if (t >= 2) ok = ok && wait_for(&sm.p_free[b], ((t >> 1) - 1) & 1, p.err, ctl);
-        ok = all_of(ok);
+        if (t >= 2) ok = all_of(wait_for(&sm.p_free[b], ((t >> 1) - 1) & 1, p.err, ctl));
+        #pragma unroll
+        for (int c = 0; c < kKChunks; ++c) {
+          ok = ok && all_of(wait_for(&sm.k_full[slot], phase, p.err, ctl));
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            const uint64_t db = desc_k + (uint64_t)(slot * kStep);
+            #pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_f16_ss(tmem + b * kTile, desc_q + (c * kStep + 2 * kk), db + 2 * kk, kIdesc, c > 0 || kk > 0);
+            PAIR ? tc_commit_pair(&sm.k_empty[slot]) : tc_commit(&sm.k_empty[slot]);
+          }
+          __syncwarp();
+          if (++slot == kRingK) slot = 0, phase ^= 1;
+        }
         if (!ok) break;
-        tc_fence_after();
         if (leader) {
-          const uint64_t db = desc_k + (uint64_t)(st * (kKChunks * kStep));
-          #pragma unroll
-          for (int kk = 0; kk < kQDim / 16; ++kk)
-            tc_mma_f16_ss(tmem + b * kTile, desc_q + ((kk >> 2) * kStep + 2 * (kk & 3)),
-                          db + ((kk >> 2) * kStep + 2 * (kk & 3)), kIdescS, kk > 0);
-          tc_commit(&sm.k_empty[st]);
           tc_commit(&sm.s_full[b]);
           if (left == 1) tc_commit(&sm.q_empty);
         }
         __syncwarp();
-        --left;
       }
-      if (t > 0) {
-        // PV of tile t - 1: the last of its item if tile t begins another.
-        const int b = (t - 1) & 1, st = (t - 1) % kStages, item = fresh ? n_item - 1 : n_item;
-        ok = wait_for(&sm.v_full[st], ((t - 1) / kStages) & 1, p.err, ctl);
-        if (first && item > 0) ok = ok && wait_for(&sm.o_empty, (item - 1) & 1, p.err, ctl);
-        ok = ok && wait_for(&sm.p_full[b], ((t - 1) >> 1) & 1, p.err, ctl);
-        ok = all_of(ok);
-        if (!ok) break;
-        tc_fence_after();
-        if (leader) {
-          const uint64_t db = desc_v + (uint64_t)(st * (kVChunks * kStep));
-          #pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            // P: two keys a column, in the first 64 columns of its S buffer.
-            tc_mma_f16_ts(tO, tmem + b * kTile + kk * 8, db + kk * (2048 >> 4), kIdescO, !first || kk > 0);
-          tc_commit(&sm.v_empty[st]);
-          tc_commit(&sm.p_free[b]);
-          if (fresh) tc_commit(&sm.o_full);
-        }
-        __syncwarp();
-      }
-      if (end) break;
-      first = fresh;
+      if (!ok) break;
     }
     if (!ok) {
       // Aborted: the issued MMAs must end before TMEM is freed.
-      if (leader) tc_commit(&sm.drained);
+      if (leader) tc_commit(&sm.drained[0]);
       __syncwarp();
-      mbar_wait_drain(&sm.drained, 0, p.err, ctl);
+      mbar_wait_drain(&sm.drained[0], 0, p.err, ctl);
+    }
+  } else if (warp == kWarpO) {
+    // ========================= MMAs of the outputs ========================
+    constexpr uint32_t kIdesc = idesc_bf16_f32(kRows, 64, 0, 1);
+    constexpr int kStep = kChunkBytes >> 4;
+    // V is MN-major: atoms of 64 dims x 8 keys.  A chunk's 64 dims at a time (A comes
+    // from TMEM: no slower than all 128).
+    const uint64_t desc_v = smem_desc_sw128(smem_u32(sm.v[0]), kChunkBytes, 1024);
+    const bool leader = elect_one();
+    bool ok = true;
+    for (int n_item = 0, t = 0;; ++n_item) {
+      ok = all_of(wait_for(&sm.item_full[n_item % kItems], (n_item / kItems) & 1, p.err, ctl));
+      if (!ok) break;
+      const Item& it = sm.items[n_item % kItems];
+      if (uniform(it.end)) break;
+      const int n = uniform(it.t1 - it.t0);
+      #pragma unroll 1
+      for (int j = 0; j < n; ++j, ++t) {
+        const int b = t & 1, first = b * kVChunks;
+        // (the tile's values landed: the warp that copies them arrived on p_full too)
+        #pragma unroll
+        for (int c = 0; c < kVChunks; ++c) ok = ok && wait_for(&sm.v_full[first + c], (t >> 1) & 1, p.err, ctl);
+        if (j == 0 && n_item > 0) ok = ok && wait_for(&sm.o_empty, (n_item - 1) & 1, p.err, ctl);
+        ok = all_of(ok && wait_for(&sm.p_full[b], (t >> 1) & 1, p.err, ctl));
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          #pragma unroll
+          for (int c = 0; c < kVChunks; ++c) {
+            const uint64_t db = desc_v + (uint64_t)((first + c) * kStep);
+            #pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              // P: two keys a column, in the first 64 columns of its S buffer.
+              tc_mma_f16_ts(tmem + 2 * kTile + c * 64, tmem + b * kTile + kk * 8, db + kk * (2048 >> 4), kIdesc,
+                            j > 0 || kk > 0);
+            PAIR ? tc_commit_pair(&sm.v_empty[first + c]) : tc_commit(&sm.v_empty[first + c]);
+          }
+          tc_commit(&sm.p_free[b]);
+          if (j == n - 1) tc_commit(&sm.o_full);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+    }
+    if (!ok) {
+      // Aborted: the issued MMAs must end before TMEM is freed.
+      if (leader) tc_commit(&sm.drained[1]);
+      __syncwarp();
+      mbar_wait_drain(&sm.drained[1], 0, p.err, ctl);
     }
   } else {
     // ==================== softmax and epilogue (warps 0-15) ==================
@@ -551,9 +691,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int n_item = 0;; ++n_item) {
       const bool have = wait_for(&sm.item_full[n_item % kItems], (n_item / kItems) & 1, p.err, ctl);
       const Item it = sm.items[n_item % kItems];
-      // Agree before any barrier: a wait that gave up stops everyone.
-      if (barrier_or(kBarSoft, kSoftThreads, !have || it.end)) break;
-      unsigned long long* bad = sm.bad[n_item & 1];
+      // Agree before any other barrier: a wait that gave up stops everyone.  (Also:
+      // sm.xrow is free again.)
+      if (barrier_or(kBarSoft, kSoftThreads, !have || !ok || it.end)) break;
+      const unsigned long long* bad = sm.bad[n_item % kItems];
       const bool valid = row < it.nt;
       const int prow = valid ? it.pos0 + row : -1;  // the last key that the row sees
       float m = -INFINITY, l = 0.f;
@@ -630,10 +771,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st16(tS + part * (kPartKeys / 2), w);
         tc_wait_st();
         l += (sum_lo[0] + sum_hi[0]) + (sum_lo[1] + sum_hi[1]);
-        if ((j + 1) * kTile > it.pos0 + 1) {
-          ok = ok && wait_for(&sm.v_full[t % kStages], (t / kStages) & 1, p.err, ctl);
-          clean_values(sm.v[t % kStages], j * kTile, it.pos0, it.nt, bad, warp, lane);
-        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.p_full[sb]);
@@ -642,10 +779,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm.xrow[part][row] = l;
       named_barrier(kBarQuad + quad, 128);
       const float lrow = (sm.xrow[0][row] + sm.xrow[1][row]) + (sm.xrow[2][row] + sm.xrow[3][row]);
-      if (it.nt > 1) named_barrier(kBarSoft, kSoftThreads);  // sm.bad is complete
-      const unsigned long long gone0 = bad[0], gone1 = bad[1];
       ok = ok && wait_for(&sm.o_full, n_item & 1, p.err, ctl);
       tc_fence_after();
+      const unsigned long long gone0 = bad[0], gone1 = bad[1];
       {
         float o[32];
         tmem_ld32(tO, o);
@@ -679,18 +815,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.o_empty);
-      // Every warp has read sm.bad and sm.xrow.
-      if (barrier_or(kBarSoft, kSoftThreads, !ok)) break;
-      if (tid == 0) bad[0] = bad[1] = 0;
     }
   }
   // (an abort only shortens the loops: every warp gets here)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kWarpMma) tmem_dealloc(tmem, kTmemCols);
+  if (warp == kWarpS) tmem_dealloc(tmem, kTmemCols);
+  // A CTA's memory and barriers outlive the copies and commits of the other.
+  if (PAIR) cluster_barrier();
   // The last CTA to finish empties the queue for the next launch.
-  if (tid == 0) {
+  if (tid == 0 && rank == 0) {
     __threadfence();
     if (atomicAdd(p.sched + 1, 1ull) == (unsigned long long)(active - 1)) {
       p.sched[0] = 0;
@@ -734,36 +869,51 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_prefill_merge_kernel(
   reinterpret_cast<uint2*>(p.out + ((long long)(rec.y + row) * p.num_heads + rec.w) * kValDim)[lane] = w;
 }
 
-}  // namespace
-
-cudaError_t launch_latent_prefill(const LatentPrefillLaunch& L, cudaStream_t stream) {
-  const size_t smem = sizeof(Smem) + 1024;
+template <bool PAIR>
+cudaError_t launch_prefill(const LatentPrefillLaunch& L, cudaStream_t stream) {
+  const size_t smem = sizeof(Smem);
   static unsigned long long configured = 0;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & bit)) {
-    e = cudaFuncSetAttribute(latent_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(latent_prefill_kernel<PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     __atomic_fetch_or(&configured, bit, __ATOMIC_RELEASE);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(L.grid);
+  cfg.gridDim = dim3(PAIR ? L.grid / 2 * 2 : L.grid);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = L.p.pdl ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, latent_prefill_kernel, L.qmap, L.kvmap, L.rmap, L.p);
-  if (e != cudaSuccess || L.p.max_pieces == 0) return e != cudaSuccess ? e : cudaGetLastError();
-  cfg.gridDim = dim3(L.p.max_pieces, kRows / kMergeWarps);
-  cfg.blockDim = dim3(32 * kMergeWarps);
-  cfg.dynamicSmemBytes = 0;
-  e = cudaLaunchKernelEx(&cfg, latent_prefill_merge_kernel, L.p);
+  cfg.numAttrs = PAIR ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, latent_prefill_kernel<PAIR>, L.qmap, L.kvmap, L.rmap, L.p);
+}
+
+}  // namespace
+
+cudaError_t launch_latent_prefill(const LatentPrefillLaunch& L, cudaStream_t stream) {
+  cudaError_t e = L.pairs ? launch_prefill<true>(L, stream) : launch_prefill<false>(L, stream);
+  if (e == cudaSuccess && L.p.max_pieces > 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(L.p.max_pieces, kRows / kMergeWarps);
+    cfg.blockDim = dim3(32 * kMergeWarps);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = L.p.pdl ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, latent_prefill_merge_kernel, L.p);
+  }
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

@@ -1368,18 +1368,21 @@ int pkv_attention_expanded(const void* q, const void* kv, const void* k_rope, co
   p.pdl = opt.pdl != 0;
   p.early_plan = p.pdl && opt.early_plan != 0;
   p.wait_limit_ns = (unsigned long long)opt.wait_limit_us * 1000ull;
-  const cuuint32_t box[3] = {64, 1, 128}, rbox[3] = {64, 128, 1};
+  // In pairs where chunks are long enough for two query tiles on average, and enough.
+  L.pairs = dims->num_q_tokens >= 192ll * dims->num_reqs &&
+            (long long)dims->num_q_tokens * heads >= 256ll * st->sm_count;
+  const cuuint32_t keys = L.pairs ? 64 : 128;
+  const cuuint32_t box[3] = {64, 1, 128}, kbox[3] = {64, 1, keys}, rbox[3] = {64, keys, 1};
   constexpr int kQ = pkv::kNope + pkv::kRopeDim, kKv = pkv::kNope + pkv::kValDim;
   rc = encode_bf16_3d(&L.qmap, q, kQ, heads, dims->num_q_tokens, kQ, (long long)heads * kQ, box, "q");
   if (rc == PKV_OK)
     rc = encode_bf16_3d(&L.kvmap, kv, kKv, heads, num_rows, kKv, (long long)heads * kKv, box, "kv");
   if (rc == PKV_OK)
+    rc = encode_bf16_3d(&L.kmap, kv, kKv, heads, num_rows, kKv, (long long)heads * kKv, kbox, "kv");
+  if (rc == PKV_OK)
     rc = encode_bf16_3d(&L.rmap, k_rope, pkv::kRopeDim, num_rows, 1, pkv::kRopeDim,
                         (long long)num_rows * pkv::kRopeDim, rbox, "k_rope");
   if (rc != PKV_OK) return rc;
-  // In pairs where chunks are long enough for two query tiles on average, and enough.
-  L.pairs = dims->num_q_tokens >= 192ll * dims->num_reqs &&
-            (long long)dims->num_q_tokens * heads >= 256ll * st->sm_count;
   L.grid = st->sm_count;
   const cudaError_t e = pkv::launch_latent_prefill(L, stream);
   if (e != cudaSuccess) return cuda_fail(e, "expanded attention launch");

@@ -44,7 +44,7 @@
 #include <climits>
 
 #include "pkv_latent.h"
-#include "pkv_tc.cuh"
+#include "pkv_pair.cuh"
 
 namespace pkv {
 namespace {
@@ -436,7 +436,7 @@ static __device__ __noinline__ void spread_bad(const LatentDecodeParams& p, cons
 // The pair's side of the copies and of their release: a copy lands in both CTAs of
 // the cluster, at the same place, and counts on both barriers; a commit arrives on
 // both.
-__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+__device__ __forceinline__ void tma_load_2d_both(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
       ".multicast::cluster [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
@@ -444,16 +444,12 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
-__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+__device__ __forceinline__ void tc_commit_both(uint64_t* bar) {
   asm volatile(
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
       "[%0], %1;" ::"r"(smem_u32(bar)),
       "h"((uint16_t)3)
       : "memory");
-}
-
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 template <int COLS, int TILE, int STAGES, bool PAIR>
@@ -650,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   if (!PAIR) tma_load_2d(sm.kv[st][c] + b * 2048, &kmap, c * 64, rows[b], bar);
                   // (every other copy is the other CTA's)
                   else if (((c * kTileBlocks + b) & 1) == hg)
-                    tma_load_2d_pair(sm.kv[st][c] + b * 2048, &kmap, c * 64, rows[b], bar);
+                    tma_load_2d_both(sm.kv[st][c] + b * 2048, &kmap, c * 64, rows[b], bar);
                 }
               }
             }
@@ -722,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         if (leader) {
           tc_commit(&sm.s_full[b]);
-          PAIR ? tc_commit_pair(&sm.kv_empty[st][kParts - 1]) : tc_commit(&sm.kv_empty[st][kParts - 1]);
+          PAIR ? tc_commit_both(&sm.kv_empty[st][kParts - 1]) : tc_commit(&sm.kv_empty[st][kParts - 1]);
           if (left == 1) tc_commit(&sm.q_empty);
         }
         __syncwarp();
@@ -770,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int kk = 0; kk < TILE / 16; ++kk)
               tc_mma_f16_ss(tmem + kColO + m * kLatMaxRows, da + (2 * m * kKvStep + kk * (2048 >> 4)),
                             desc_p + 2 * kk, idesc, j > 0 || kk > 0);
-            PAIR ? tc_commit_pair(&sm.kv_empty[st][m]) : tc_commit(&sm.kv_empty[st][m]);
+            PAIR ? tc_commit_both(&sm.kv_empty[st][m]) : tc_commit(&sm.kv_empty[st][m]);
           }
           tc_commit(&sm.p_free);
           if (j == n - 1) tc_commit(&sm.o_full);

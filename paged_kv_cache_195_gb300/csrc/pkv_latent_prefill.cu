@@ -15,10 +15,12 @@
 // rescaled, only when a score exceeds it by 2^8, on a vote of the four warps that
 // hold the same rows.  Keys and values have rings of their own, of 64-dim chunks,
 // each of which goes back as soon as its MMAs are done.
-// Steps of long chunks run in pairs of CTAs: the pair takes two query tiles of one
-// head, a CTA each, and every key tile comes in once for both, by multicast.  Alone,
-// 152 CTAs read 80 KB a tile each, 11 TB/s from L2, and that set the pace (1.09 us a
-// tile).
+// Steps of long chunks run in pairs of CTAs (cta_group::2): the pair takes two query
+// tiles of one head, 256 MMA rows, and each CTA holds half of the keys and half of
+// the value dims of a tile: half the copies, half the operand reads, and room for
+// four tiles in flight.  A CTA alone holds all 80 KB of a tile, which with the
+// MMAs' own reads is more than shared memory and the copies give (1.04-1.09 us a
+// tile, with the keys multicast or not).
 //
 // Order.  Items come from a queue, longest requests first, a head's query tiles
 // one after the other (the CTAs that run them at one time read the same keys:
@@ -33,7 +35,7 @@
 #include <climits>
 
 #include "pkv_latent.h"
-#include "pkv_tc.cuh"
+#include "pkv_pair.cuh"
 
 namespace pkv {
 namespace {
@@ -56,9 +58,13 @@ constexpr int kChunkBytes = 128 * 128;
 constexpr int kQDim = kNope + kRopeDim;
 constexpr int kKChunks = kQDim / 64;
 constexpr int kVChunks = kValDim / 64;
-constexpr int kRingK = 7;                // chunks in flight: two tiles and a third of keys, ...
-constexpr int kRingV = 2 * kVChunks;     // ... two tiles of values
+// Chunks in flight.  Alone: of 128 keys, two tiles and a third of keys and two of
+// values; a pair's CTA: of 64 keys, four tiles and two thirds, and (64 of the dims of
+// all keys) four of values.
+constexpr int kBytesK = 7 * kChunkBytes;
+constexpr int kRingV = 4;
 constexpr int kItems = 4;
+constexpr int kBadItems = 8;
 constexpr uint32_t kTmemCols = 512;      // S: columns 0 .. 255, O: 256 .. 383
 constexpr float kRescaleLog2 = 8.0f;
 constexpr int kMinPieceTiles = 4;
@@ -71,23 +77,25 @@ struct Item {
   int k0;        // first row of the request's keys
   int t0, t1;
   int slot;      // piece number, if the item is split; else -1
+  int gpos0;     // of the pair's two query tiles: position of the first token, ...
+  int gnt;       // ... query tokens
   int end;
 };
 
 struct __align__(1024) Smem {
   uint8_t q[kKChunks][kChunkBytes];
-  uint8_t k[kRingK][kChunkBytes];
+  uint8_t k[kBytesK];
   uint8_t v[kRingV][kChunkBytes];
   uint64_t q_full, q_empty;
-  uint64_t k_full[kRingK], k_empty[kRingK], v_full[kRingV], v_empty[kRingV];
+  uint64_t k_full[14], k_empty[14], v_full[kRingV], v_empty[kRingV];
   uint64_t s_full[2], p_full[2], p_free[2];
   uint64_t o_full, o_empty;
-  uint64_t item_full[kItems], vitem_full[kItems], vitem_empty[kItems], next_full[kItems];
+  uint64_t item_full[kItems], next_full[kItems];
   uint64_t drained[2];
-  Item items[kItems], vitems[kItems];
+  Item items[kItems];
   unsigned long long next[kItems];    // a pair: the piece's number, from its first CTA
   float xrow[kParts][kRows];
-  unsigned long long bad[kItems][2];  // own tokens whose values were taken out
+  unsigned long long bad[kBadItems][4];  // own tokens whose values were taken out
   uint32_t tmem_base;
   int active;  // CTAs that take pieces
   int split;   // key tiles of a piece (INT_MAX: items are whole)
@@ -242,6 +250,8 @@ struct Finder {
     it->row0 = b.q0 + first;
     it->nt = min(kRows, b.qr - first);
     it->pos0 = b.L - b.qr + first;
+    it->gpos0 = b.L - b.qr + i * GROUP;
+    it->gnt = min(GROUP, b.qr - i * GROUP);
     it->k0 = b.k0;
     // n pieces of equal length, but for the rounding
     it->t0 = (int)((long long)tiles * x / n);
@@ -268,23 +278,26 @@ __device__ __forceinline__ bool non_finite(uint32_t w) {
   return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
-// Values of the tile's keys from pos0 + 1 on: those that no row of the item sees
-// (from its last token's position on) become zeros; those of its own tokens that
-// are not finite too, noted in bad.  One warp, half of it a row, eight rows at a time;
-// only where a first look at the rows' exponents finds any that is not finite.
+// Values of the tile's keys from pos0 + 1 on, the item's first token's position:
+// where any is not finite, those that no row of the item sees (from its last
+// token's position on) become zeros, and those of its own tokens that are not finite
+// too, noted in bad (a pair's: in both CTAs').  One warp; v: CHUNKS chunks of 64 dims.
+template <int CHUNKS, bool PAIR>
 static __device__ __noinline__ void clean_values(uint8_t (*v)[kChunkBytes], int key0, int pos0, int nt,
-                                                 unsigned long long* bad, int lane) {
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  const int piece = lane & 15;
+                                                 unsigned long long* bad, int rank, int lane) {
+  constexpr int kPieces = 8 * CHUNKS;   // of 16 bytes, a row
+  constexpr int kRowsAt = 32 / kPieces; // a warp's rows at a time
+  const int piece = lane % kPieces;
+  auto at = [&](int row) {
+    return reinterpret_cast<uint4*>(v[piece >> 3] + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
+  };
+  const int first = max(pos0 + 1 - key0, 0);
   uint32_t top = 0;  // the largest exponents, two to a word
   #pragma unroll 1
-  for (int r0 = max(pos0 + 1 - key0, 0); r0 < kTile; r0 += 16) {
+  for (int r0 = first + lane / kPieces; __any_sync(0xffffffffu, r0 < kTile); r0 += 8 * kRowsAt) {
     uint4 x[8];
     #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int row = min(r0 + 2 * i + (lane >> 4), kTile - 1);
-      x[i] = *reinterpret_cast<uint4*>(v[piece >> 3] + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
-    }
+    for (int i = 0; i < 8; ++i) x[i] = *at(min(r0 + i * kRowsAt, kTile - 1));
     #pragma unroll
     for (int i = 0; i < 8; ++i)
       top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7f807f80u, x[i].y & 0x7f807f80u),
@@ -292,38 +305,27 @@ static __device__ __noinline__ void clean_values(uint8_t (*v)[kChunkBytes], int 
   }
   if (!__any_sync(0xffffffffu, non_finite(top))) return;
   #pragma unroll 1
-  for (int r0 = max(pos0 + 1 - key0, 0) + (lane >> 4); __any_sync(0xffffffffu, r0 < kTile); r0 += 8) {
-    uint4* at[4];
-    uint4 x[4];
-    #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = min(r0 + 2 * i, kTile - 1);
-      at[i] = reinterpret_cast<uint4*>(v[piece >> 3] + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
-      x[i] = *at[i];
+  for (int row = first; row < kTile; ++row) {
+    const int b = key0 + row - pos0 - 1;  // the item's token b + 1
+    const uint4 x = *at(row);
+    if (!__any_sync(0xffffffffu, non_finite(x.x) || non_finite(x.y) || non_finite(x.z) || non_finite(x.w))) continue;
+    if (b < nt - 1 && lane == 0) {
+      atomicOr(bad + (b >> 6), 1ull << (b & 63));
+      if (PAIR) or_other(bad + (b >> 6), rank, 1ull << (b & 63));
     }
-    #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = r0 + 2 * i, b = key0 + row - pos0 - 1;  // the item's token b + 1
-      const bool in = row < kTile, own = b < nt - 1;
-      const bool hit = in && own && (non_finite(x[i].x) || non_finite(x[i].y) || non_finite(x[i].z) || non_finite(x[i].w));
-      const unsigned votes = __ballot_sync(0xffffffffu, hit);
-      const bool out = in && (!own || ((votes >> (lane & 16)) & 0xffffu) != 0);
-      if (out && own && piece == 0) atomicOr(bad + (b >> 6), 1ull << (b & 63));
-      if (out) *at[i] = zero;
-    }
+    __syncwarp();
+    if (lane < kPieces) *at(row) = make_uint4(0, 0, 0, 0);
   }
-  fence_proxy_async_smem();
 }
 
 // What the values taken out add to a row that sees the first `seen` of them: its
 // weight is positive, so a NaN stays one and an infinity keeps its sign.
 static __device__ __noinline__ void add_bad(const LatentPrefillParams& p, const Item& it,
-                                            unsigned long long lo, unsigned long long hi, int seen,
-                                            int d0, float (&o)[32]) {
+                                            const unsigned long long* bad, int seen, int d0, float (&o)[32]) {
   for (int b = 0; b < seen; ++b) {
-    if (!(((b < 64 ? lo : hi) >> (b & 63)) & 1)) continue;
+    if (!((bad[b >> 6] >> (b & 63)) & 1)) continue;
     const __nv_bfloat16* v =
-        p.kv + ((long long)(it.k0 + it.pos0 + 1 + b) * p.num_heads + it.head) * (kNope + kValDim) + kNope + d0;
+        p.kv + ((long long)(it.k0 + it.gpos0 + 1 + b) * p.num_heads + it.head) * (kNope + kValDim) + kNope + d0;
     #pragma unroll
     for (int i = 0; i < 32; ++i) {
       const float x = __bfloat162float(v[i]);
@@ -332,45 +334,10 @@ static __device__ __noinline__ void add_bad(const LatentPrefillParams& p, const 
   }
 }
 
-// ------------------------------------------------------------ a pair's plumbing
-// Copies that land in both CTAs of the cluster, at the same place, and count on both
-// barriers; commits that arrive on both.
-__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      ".multicast::cluster [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "h"((uint16_t)3)
-      : "memory");
-}
-
-__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-      "[%0], %1;" ::"r"(smem_u32(bar)),
-      "h"((uint16_t)3)
-      : "memory");
-}
-
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// Leaves a number in the second CTA's shared memory and arrives on its barrier.
-__device__ __forceinline__ void send(unsigned long long* slot, uint64_t* bar, unsigned long long v) {
-  asm volatile(
-      "{\n\t.reg .b32 a, b;\n\t"
-      "mapa.shared::cluster.u32 a, %0, 1;\n\t"
-      "mapa.shared::cluster.u32 b, %1, 1;\n\t"
-      "st.shared::cluster.u64 [a], %2;\n\t"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [b];\n\t}" ::"r"(smem_u32(slot)),
-      "r"(smem_u32(bar)), "l"(v)
-      : "memory");
-}
-
 template <bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
-                          const __grid_constant__ CUtensorMap kvmap,
+                          const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap kmap,
                           const __grid_constant__ CUtensorMap rmap, const LatentPrefillParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
@@ -381,32 +348,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   WaitCtl* ctl = &sm.wait;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int GROUP = PAIR ? 2 * kRows : kRows;
-  const int rank = PAIR ? blockIdx.x & 1 : 0;
+  constexpr int kCtas = PAIR ? 2 : 1;
+  constexpr int kKeyRows = kTile / kCtas;        // keys of a tile that this CTA holds
+  constexpr int kKBytes = kKeyRows * 128;        // ... a chunk of them
+  constexpr int kRingK = kBytesK / kKBytes;
+  constexpr int kVCount = kVChunks / kCtas;      // chunks of a tile's values that it holds
+  const int rank = PAIR ? blockIdx.x & 1 : 0;    // in the pair, whose first CTA issues all MMAs
 
   if (tid == 0) {
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, 1);
     for (int s = 0; s < kRingK; ++s) {
       mbar_init(&sm.k_full[s], 1);
-      mbar_init(&sm.k_empty[s], PAIR ? 2 : 1);
+      mbar_init(&sm.k_empty[s], 1);
     }
     for (int s = 0; s < kRingV; ++s) {
       mbar_init(&sm.v_full[s], 1);
-      mbar_init(&sm.v_empty[s], PAIR ? 2 : 1);
+      mbar_init(&sm.v_empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sm.s_full[b], 1);
-      mbar_init(&sm.p_full[b], kSoftWarps + 1);
+      mbar_init(&sm.p_full[b], kCtas * (kSoftWarps + 1));
       mbar_init(&sm.p_free[b], 1);
     }
     mbar_init(&sm.o_full, 1);
-    mbar_init(&sm.o_empty, kSoftWarps);
+    mbar_init(&sm.o_empty, kCtas * kSoftWarps);
     for (int b = 0; b < kItems; ++b) {
       mbar_init(&sm.item_full[b], 1);
-      mbar_init(&sm.vitem_full[b], 1);
-      mbar_init(&sm.vitem_empty[b], 1);
       mbar_init(&sm.next_full[b], 1);
     }
+    for (int b = 0; b < 4 * kBadItems; ++b) sm.bad[b >> 2][b & 3] = 0;
     mbar_init(&sm.drained[0], 1);
     mbar_init(&sm.drained[1], 1);
     sm.wait.abort = 0;
@@ -416,6 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kWarpV && lane == 0) {
     prefetch_tensormap(&qmap);
     prefetch_tensormap(&kvmap);
+    prefetch_tensormap(&kmap);
     prefetch_tensormap(&rmap);
   }
   if (!p.early_plan) grid_dependency_wait();
@@ -437,8 +409,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int active = sm.active, split = sm.split;
   if ((int)(PAIR ? blockIdx.x >> 1 : blockIdx.x) >= active) return;
   if (warp == kWarpS) {
-    tmem_alloc(&sm.tmem_base, kTmemCols);
-    tmem_relinquish();
+    if (PAIR) {
+      tmem_alloc_pair(&sm.tmem_base, kTmemCols);
+    } else {
+      tmem_alloc(&sm.tmem_base, kTmemCols);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -446,100 +422,70 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = uniform(sm.tmem_base);
   if (PAIR) cluster_barrier();  // both CTAs' barriers are ready
 
+  // Arrive on a barrier -- both CTAs', in a pair -- once the MMAs so far are done.
+  auto commit = [](uint64_t* bar) { PAIR ? commit_pair(bar) : tc_commit(bar); };
+
   if (warp == kWarpK || warp == kWarpV) {
     // =========================== copies ===================================
     const bool vside = warp == kWarpV;
-    uint64_t* const full = vside ? sm.v_full : sm.k_full;
-    uint64_t* const empty = vside ? sm.v_empty : sm.k_empty;
-    const int ring = vside ? kRingV : kRingK;
     const bool leader = elect_one();
-    int n_item = 0, t = 0;
-    int n_chunk = 0, slot = 0, phase = 1;  // chunks so far; their slot and the parity it waits for
+    int slot = 0, phase = 1, n_chunk = 0;  // the chunk's slot and the parity it waits for; chunks so far
     bool ok = true;
-    // Tile tt of the item's values, key tile j, has landed: what not every row may
-    // see is taken out.  The arrival, beside the softmax warps', lets the tile's
-    // product begin.
-    auto finish = [&](const Item& it, int j, int tt) {
-      const int first = (tt & 1) * kVChunks;
-      for (int c = first; c < first + kVChunks; ++c)
-        if (!all_of(wait_for(&sm.v_full[c], (tt >> 1) & 1, p.err, ctl))) return false;
-      if ((j + 1) * kTile > it.pos0 + 1)
-        clean_values(sm.v + first, j * kTile, it.pos0, it.nt, sm.bad[n_item % kItems], lane);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.p_full[tt & 1]);
-      return true;
-    };
-    auto stream = [&](const Item& it) {
-      if (vside && lane < 2) sm.bad[n_item % kItems][lane] = 0;
-      __syncwarp();
-      const int head = uniform(it.head), t1 = uniform(it.t1);
-      int y = uniform(it.k0 + it.t0 * kTile);
-      #pragma unroll 1
-      for (int j = uniform(it.t0); j < t1; ++j, ++t, y += kTile) {
-        const int chunks = vside ? kVChunks : kKChunks;
-        #pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-          if (!all_of(wait_for(&empty[slot], phase, p.err, ctl))) return false;
-          if (leader) {
-            mbar_arrive_expect_tx(&full[slot], kChunkBytes);
-            // A pair's CTAs take turns at the chunks.
-            if (!PAIR || (n_chunk & 1) == rank) {
-              const bool rope = !vside && c == kKChunks - 1;
-              const CUtensorMap* map = rope ? &rmap : &kvmap;
-              const int x = rope ? 0 : (vside ? kNope : 0) + c * 64;
-              const int a = rope ? y : head, b = rope ? 0 : y;
-              void* dst = vside ? sm.v[slot] : sm.k[slot];
-              PAIR ? tma_load_3d_pair(dst, map, x, a, b, &full[slot]) : tma_load_3d(dst, map, x, a, b, &full[slot]);
-            }
-          }
-          __syncwarp();
-          ++n_chunk;
-          if (++slot == ring) slot = 0, phase ^= 1;
-        }
-        if (j == it.t0 && !vside) {
-          // The item's queries, once the MMAs of the item before are done with
-          // theirs (its first keys are on their way).
-          if (n_item > 0 && !all_of(wait_for(&sm.q_empty, (n_item - 1) & 1, p.err, ctl))) return false;
-          if (leader) {
-            sm.items[n_item % kItems] = it;
-            mbar_arrive(&sm.item_full[n_item % kItems]);
-            mbar_arrive_expect_tx(&sm.q_full, kKChunks * kChunkBytes);
-            for (int c = 0; c < kKChunks; ++c)
-              tma_load_3d(sm.q[c], &qmap, c * 64, head, it.row0, &sm.q_full);
-          }
-          ++n_item;
-          __syncwarp();
-        }
-        if (vside && j > it.t0 && !finish(it, j - 1, t - 1)) return false;
-      }
-      return !vside || finish(it, t1 - 1, t - 1);
-    };
     if (vside) {
-      for (;; ++n_item) {
-        const int b = n_item % kItems;
-        ok = wait_for(&sm.vitem_full[b], (n_item / kItems) & 1, p.err, ctl);
-        if (!ok) break;
-        const Item it = sm.vitems[b];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.vitem_empty[b]);
-        if (it.end) break;
-        ok = stream(it);
-        if (!ok) break;
-      }
-    } else {
-      int handed = 0;
-      auto hand_over = [&](const Item& it) {
-        const int b = handed % kItems;
-        if (handed >= kItems && !wait_for(&sm.vitem_empty[b], ((handed / kItems) - 1) & 1, p.err, ctl))
-          return false;
-        if (lane == 0) {
-          sm.vitems[b] = it;
-          mbar_arrive(&sm.vitem_full[b]);
+      // ---- values: this CTA's chunks, on its own barriers
+      int t = 0, f_slot = 0, f_phase = 0;
+      // A tile's values have landed: what not every row may see is taken out.  The
+      // arrival, beside the softmax warps', lets the tile's product begin.
+      auto finish = [&](const Item& it, int n_item, int j, int tt) {
+        const int first = f_slot;
+        #pragma unroll
+        for (int c = 0; c < kVCount; ++c) {
+          if (!all_of(wait_for(&sm.v_full[f_slot], f_phase, p.err, ctl))) return false;
+          if (++f_slot == kRingV) f_slot = 0, f_phase ^= 1;
         }
-        ++handed;
+        if ((j + 1) * kTile > it.gpos0 + 1)
+          clean_values<kVCount, PAIR>(sm.v + first, j * kTile, it.gpos0, it.gnt, sm.bad[n_item % kBadItems], rank, lane);
+        fence_proxy_async_smem();
+        // (the barrier's phase before, tile tt - 2's, must be over)
+        if (tt >= 2 && !all_of(wait_for(&sm.p_free[tt & 1], ((tt >> 1) - 1) & 1, p.err, ctl))) return false;
         __syncwarp();
+        if (lane == 0) PAIR ? arrive_at(first_cta(&sm.p_full[tt & 1])) : mbar_arrive(&sm.p_full[tt & 1]);
         return true;
       };
+      for (int n_item = 0; ok; ++n_item) {
+        ok = all_of(wait_for(&sm.item_full[n_item % kItems], (n_item / kItems) & 1, p.err, ctl));
+        if (!ok) break;
+        const Item it = sm.items[n_item % kItems];
+        if (it.end) break;
+        const int head = uniform(it.head), t0 = uniform(it.t0), t1 = uniform(it.t1);
+        int y = uniform(it.k0 + it.t0 * kTile);
+        #pragma unroll 1
+        for (int j = t0; j < t1 && ok; ++j, ++t, y += kTile) {
+          #pragma unroll
+          for (int c = 0; c < kVCount; ++c) {
+            ok = ok && all_of(wait_for(&sm.v_empty[slot], phase, p.err, ctl));
+            if (!ok) break;
+            if (leader) {
+              mbar_arrive_expect_tx(&sm.v_full[slot], kChunkBytes);
+              tma_load_3d(sm.v[slot], &kvmap, kNope + (PAIR ? rank : c) * 64, head, y, &sm.v_full[slot]);
+            }
+            __syncwarp();
+            ++n_chunk;
+            if (++slot == kRingV) slot = 0, phase ^= 1;
+          }
+          // (one tile behind, so that the next one's copies are under way)
+          if (ok && j > t0) ok = finish(it, n_item, j - 1, t - 1);
+        }
+        ok = ok && finish(it, n_item, t1 - 1, t - 1);
+      }
+      if (!ok) {
+        // Aborted: the copies in flight must land before the CTA ends.
+        for (int i = max(0, n_chunk - kRingV); i < n_chunk; ++i)
+          mbar_wait_drain(&sm.v_full[i % kRingV], (i / kRingV) & 1, p.err, ctl);
+      }
+    } else {
+      // ---- items, queries and keys; a pair's on the first CTA's barriers
+      int n_item = 0;
       Finder<GROUP> f;
       f.start(p, split);
       for (int n = 0; ok; ++n) {
@@ -548,10 +494,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!PAIR || rank == 0) {
           if (lane == 0) v = atomicAdd(p.sched, 1ull);
           v = __shfl_sync(0xffffffffu, v, 0);
-          if (PAIR && lane == 0) send(&sm.next[n % kItems], &sm.next_full[n % kItems], v);
+          if (PAIR && lane == 0) send_second(&sm.next[n % kItems], &sm.next_full[n % kItems], v);
         } else {
           ok = wait_for(&sm.next_full[n % kItems], (n / kItems) & 1, p.err, ctl);
-          if (!ok) break;
+          if (!all_of(ok)) break;
           asm volatile("fence.acq_rel.cluster;" ::: "memory");
           v = *(volatile unsigned long long*)&sm.next[n % kItems];
         }
@@ -562,30 +508,67 @@ __global__ void __launch_bounds__(kThreads, 1)
         // takes it.
         if (split != INT_MAX && lane == 0)
           *reinterpret_cast<int4*>(p.piece + 4 * v) = make_int4(of, it.row0, it.nt, it.head);
-        ok = hand_over(it) && stream(it);
+        const int head = uniform(it.head), row0 = uniform(it.row0), t0 = uniform(it.t0), t1 = uniform(it.t1);
+        int y = uniform(it.k0 + it.t0 * kTile) + rank * kKeyRows;
+        #pragma unroll 1
+        for (int j = t0; j < t1 && ok; ++j, y += kTile) {
+          #pragma unroll
+          for (int c = 0; c < kKChunks; ++c) {
+            ok = ok && all_of(wait_for(&sm.k_empty[slot], phase, p.err, ctl));
+            if (!ok) break;
+            if (leader) {
+              uint8_t* const dst = sm.k + slot * kKBytes;
+              uint64_t* const bar = &sm.k_full[slot];
+              if (rank == 0) mbar_arrive_expect_tx(bar, kChunkBytes);  // (both CTAs' halves)
+              const bool rope = c == kKChunks - 1;
+              if (PAIR) tma_load_3d_pair(dst, rope ? &rmap : &kmap, rope ? 0 : c * 64, rope ? y : head, rope ? 0 : y, first_cta(bar));
+              else tma_load_3d(dst, rope ? &rmap : &kmap, rope ? 0 : c * 64, rope ? y : head, rope ? 0 : y, bar);
+            }
+            __syncwarp();
+            ++n_chunk;
+            if (++slot == kRingK) slot = 0, phase ^= 1;
+          }
+          if (ok && j == t0) {
+            // The item's queries, once the MMAs of the item before are done with
+            // theirs (its first keys are on their way).
+            if (n_item > 0) ok = all_of(wait_for(&sm.q_empty, (n_item - 1) & 1, p.err, ctl));
+            if (!ok) break;
+            if (leader) {
+              sm.items[n_item % kItems] = it;
+              mbar_arrive(&sm.item_full[n_item % kItems]);
+              if (rank == 0) mbar_arrive_expect_tx(&sm.q_full, kCtas * kKChunks * kChunkBytes);
+              #pragma unroll
+              for (int c = 0; c < kKChunks; ++c) {
+                if (PAIR) tma_load_3d_pair(sm.q[c], &qmap, c * 64, head, row0, first_cta(&sm.q_full));
+                else tma_load_3d(sm.q[c], &qmap, c * 64, head, row0, &sm.q_full);
+              }
+            }
+            ++n_item;
+            __syncwarp();
+          }
+        }
       }
-      Item fin = {};
-      fin.end = 1;
-      if (ok) ok = hand_over(fin);
-      if (ok && n_item > 0) ok = wait_for(&sm.q_empty, (n_item - 1) & 1, p.err, ctl);
+      if (ok && n_item > 0) ok = all_of(wait_for(&sm.q_empty, (n_item - 1) & 1, p.err, ctl));
       if (ok && lane == 0) {
         sm.items[n_item % kItems].end = 1;
         mbar_arrive(&sm.item_full[n_item % kItems]);
-        mbar_arrive(&sm.q_full);
+        if (rank == 0) mbar_arrive(&sm.q_full);
       }
       __syncwarp();
-      if (!ok && n_item > 0) mbar_wait_drain(&sm.q_full, (n_item - 1) & 1, p.err, ctl);
+      if (!ok && rank == 0) {
+        // Aborted: the copies in flight must land before the CTA ends (the barrier at
+        // the end keeps a pair's other CTA until then).
+        if (n_item > 0) mbar_wait_drain(&sm.q_full, (n_item - 1) & 1, p.err, ctl);
+        for (int i = max(0, n_chunk - kRingK); i < n_chunk; ++i)
+          mbar_wait_drain(&sm.k_full[i % kRingK], (i / kRingK) & 1, p.err, ctl);
+      }
     }
-    // Aborted: the copies in flight must land before the CTA ends.
-    if (!ok)
-      for (int i = max(0, n_chunk - ring); i < n_chunk; ++i)
-        mbar_wait_drain(&full[i % ring], (i / ring) & 1, p.err, ctl);
-  } else if (warp == kWarpS) {
+  } else if (warp == kWarpS && rank == 0) {
     // ========================= MMAs of the scores =========================
-    constexpr uint32_t kIdesc = idesc_bf16_f32(kRows, kTile, 0, 0);
+    constexpr uint32_t kIdesc = idesc_bf16_f32(kCtas * kRows, kTile, 0, 0);
     constexpr int kStep = kChunkBytes >> 4;
     const uint64_t desc_q = smem_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
-    const uint64_t desc_k = smem_desc_sw128(smem_u32(sm.k[0]), 16, 1024);
+    const uint64_t desc_k = smem_desc_sw128(smem_u32(sm.k), 16, 1024);
     const bool leader = elect_one();
     bool ok = true;
     int slot = 0, phase = 0;
@@ -605,19 +588,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           if (leader) {
-            const uint64_t db = desc_k + (uint64_t)(slot * kStep);
+            const uint64_t db = desc_k + (uint64_t)(slot * (kKBytes >> 4));
             #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc_mma_f16_ss(tmem + b * kTile, desc_q + (c * kStep + 2 * kk), db + 2 * kk, kIdesc, c > 0 || kk > 0);
-            PAIR ? tc_commit_pair(&sm.k_empty[slot]) : tc_commit(&sm.k_empty[slot]);
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t da = desc_q + (c * kStep + 2 * kk);
+              if (PAIR) mma_pair(tmem + b * kTile, da, db + 2 * kk, kIdesc, c > 0 || kk > 0);
+              else tc_mma_f16_ss(tmem + b * kTile, da, db + 2 * kk, kIdesc, c > 0 || kk > 0);
+            }
+            commit(&sm.k_empty[slot]);
           }
           __syncwarp();
           if (++slot == kRingK) slot = 0, phase ^= 1;
         }
         if (!ok) break;
         if (leader) {
-          tc_commit(&sm.s_full[b]);
-          if (left == 1) tc_commit(&sm.q_empty);
+          commit(&sm.s_full[b]);
+          if (left == 1) commit(&sm.q_empty);
         }
         __syncwarp();
       }
@@ -625,19 +611,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok) {
       // Aborted: the issued MMAs must end before TMEM is freed.
-      if (leader) tc_commit(&sm.drained[0]);
+      if (leader) commit(&sm.drained[0]);
       __syncwarp();
       mbar_wait_drain(&sm.drained[0], 0, p.err, ctl);
     }
-  } else if (warp == kWarpO) {
+  } else if (warp == kWarpO && rank == 0) {
     // ========================= MMAs of the outputs ========================
-    constexpr uint32_t kIdesc = idesc_bf16_f32(kRows, 64, 0, 1);
+    // V is MN-major: atoms of 64 dims x 8 keys.  Alone, a chunk's 64 dims at a time (A
+    // comes from TMEM: no slower than all 128).
+    constexpr uint32_t kIdesc = idesc_bf16_f32(kCtas * kRows, PAIR ? kValDim : 64, 0, 1);
     constexpr int kStep = kChunkBytes >> 4;
-    // V is MN-major: atoms of 64 dims x 8 keys.  A chunk's 64 dims at a time (A comes
-    // from TMEM: no slower than all 128).
     const uint64_t desc_v = smem_desc_sw128(smem_u32(sm.v[0]), kChunkBytes, 1024);
     const bool leader = elect_one();
     bool ok = true;
+    int slot = 0;
     for (int n_item = 0, t = 0;; ++n_item) {
       ok = all_of(wait_for(&sm.item_full[n_item % kItems], (n_item / kItems) & 1, p.err, ctl));
       if (!ok) break;
@@ -646,27 +633,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = uniform(it.t1 - it.t0);
       #pragma unroll 1
       for (int j = 0; j < n; ++j, ++t) {
-        const int b = t & 1, first = b * kVChunks;
-        // (the tile's values landed: the warp that copies them arrived on p_full too)
-        #pragma unroll
-        for (int c = 0; c < kVChunks; ++c) ok = ok && wait_for(&sm.v_full[first + c], (t >> 1) & 1, p.err, ctl);
-        if (j == 0 && n_item > 0) ok = ok && wait_for(&sm.o_empty, (n_item - 1) & 1, p.err, ctl);
+        const int b = t & 1;
+        // (the values have landed: the warps that copy them arrive on p_full too)
+        if (j == 0 && n_item > 0) ok = wait_for(&sm.o_empty, (n_item - 1) & 1, p.err, ctl);
         ok = all_of(ok && wait_for(&sm.p_full[b], (t >> 1) & 1, p.err, ctl));
         if (!ok) break;
         tc_fence_after();
-        if (leader) {
-          #pragma unroll
-          for (int c = 0; c < kVChunks; ++c) {
-            const uint64_t db = desc_v + (uint64_t)((first + c) * kStep);
+        #pragma unroll
+        for (int c = 0; c < kVCount; ++c) {
+          if (leader) {
+            const uint64_t db = desc_v + (uint64_t)(slot * kStep);
             #pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
+            for (int kk = 0; kk < kTile / 16; ++kk) {
               // P: two keys a column, in the first 64 columns of its S buffer.
-              tc_mma_f16_ts(tmem + 2 * kTile + c * 64, tmem + b * kTile + kk * 8, db + kk * (2048 >> 4), kIdesc,
-                            j > 0 || kk > 0);
-            PAIR ? tc_commit_pair(&sm.v_empty[first + c]) : tc_commit(&sm.v_empty[first + c]);
+              const uint32_t ta = tmem + b * kTile + kk * 8;
+              if (PAIR) mma_pair_ts(tmem + 2 * kTile, ta, db + kk * (2048 >> 4), kIdesc, j > 0 || kk > 0);
+              else tc_mma_f16_ts(tmem + 2 * kTile + c * 64, ta, db + kk * (2048 >> 4), kIdesc, j > 0 || kk > 0);
+            }
+            commit(&sm.v_empty[slot]);
           }
-          tc_commit(&sm.p_free[b]);
-          if (j == n - 1) tc_commit(&sm.o_full);
+          __syncwarp();
+          if (++slot == kRingV) slot = 0;
+        }
+        if (leader) {
+          commit(&sm.p_free[b]);
+          if (j == n - 1) commit(&sm.o_full);
         }
         __syncwarp();
       }
@@ -674,11 +665,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok) {
       // Aborted: the issued MMAs must end before TMEM is freed.
-      if (leader) tc_commit(&sm.drained[1]);
+      if (leader) commit(&sm.drained[1]);
       __syncwarp();
       mbar_wait_drain(&sm.drained[1], 0, p.err, ctl);
     }
-  } else {
+  } else if (warp < kSoftWarps) {
     // ==================== softmax and epilogue (warps 0-15) ==================
     // Warps 4 c .. 4 c + 3 take keys 32 c .. 32 c + 31 of a tile and output dims
     // 32 c ..; warp w reaches TMEM lanes 32 (w % 4) ..
@@ -694,7 +685,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Agree before any other barrier: a wait that gave up stops everyone.  (Also:
       // sm.xrow is free again.)
       if (barrier_or(kBarSoft, kSoftThreads, !have || !ok || it.end)) break;
-      const unsigned long long* bad = sm.bad[n_item % kItems];
+      const unsigned long long* bad = sm.bad[n_item % kBadItems];
+      // The item before is done with: its notes are empty again, long before items
+      // that have theirs in the same place.
+      if (tid < 4 && n_item > 0) sm.bad[(n_item - 1) % kBadItems][tid] = 0;
       const bool valid = row < it.nt;
       const int prow = valid ? it.pos0 + row : -1;  // the last key that the row sees
       float m = -INFINITY, l = 0.f;
@@ -773,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += (sum_lo[0] + sum_hi[0]) + (sum_lo[1] + sum_hi[1]);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_full[sb]);
+        if (lane == 0) PAIR ? arrive_at(first_cta(&sm.p_full[sb])) : mbar_arrive(&sm.p_full[sb]);
       }
       // ---- epilogue ---------------------------------------------------------
       sm.xrow[part][row] = l;
@@ -781,16 +775,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float lrow = (sm.xrow[0][row] + sm.xrow[1][row]) + (sm.xrow[2][row] + sm.xrow[3][row]);
       ok = ok && wait_for(&sm.o_full, n_item & 1, p.err, ctl);
       tc_fence_after();
-      const unsigned long long gone0 = bad[0], gone1 = bad[1];
+      const bool gone = (bad[0] | bad[1] | bad[2] | bad[3]) != 0;
       {
         float o[32];
         tmem_ld32(tO, o);
         tc_wait_ld();
-        if (gone0 | gone1) {
+        if (gone) {
           float x[32];  // (a copy, so that o itself stays in registers)
           #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = o[i];
-          add_bad(p, it, gone0, gone1, valid ? row : 0, part * kPartKeys, x);
+          add_bad(p, it, bad, valid ? rank * kRows + row : 0, part * kPartKeys, x);
           #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = x[i];
         }
@@ -814,16 +808,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.o_empty);
+      if (lane == 0) PAIR ? arrive_at(first_cta(&sm.o_empty)) : mbar_arrive(&sm.o_empty);
     }
   }
   // (an abort only shortens the loops: every warp gets here)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kWarpS) tmem_dealloc(tmem, kTmemCols);
-  // A CTA's memory and barriers outlive the copies and commits of the other.
-  if (PAIR) cluster_barrier();
+  if (PAIR) {
+    cluster_barrier();  // nothing of either CTA is under way in the other
+    if (warp == kWarpS) tmem_dealloc_pair(tmem, kTmemCols);
+    cluster_barrier();
+  } else if (warp == kWarpS) {
+    tmem_dealloc(tmem, kTmemCols);
+  }
   // The last CTA to finish empties the queue for the next launch.
   if (tid == 0 && rank == 0) {
     __threadfence();
@@ -895,7 +893,7 @@ cudaError_t launch_prefill(const LatentPrefillLaunch& L, cudaStream_t stream) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = PAIR ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, latent_prefill_kernel<PAIR>, L.qmap, L.kvmap, L.rmap, L.p);
+  return cudaLaunchKernelEx(&cfg, latent_prefill_kernel<PAIR>, L.qmap, L.kvmap, L.kmap, L.rmap, L.p);
 }
 
 }  // namespace

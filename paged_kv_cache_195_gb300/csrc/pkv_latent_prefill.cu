@@ -9,8 +9,10 @@
 // Bound: tensor core (640 flops a (row, key, head)).
 //
 // Tiling.  A work item is (request, head, 128 query tokens); a key tile is 128
-// keys.  S = Q K^T (12 MMAs of K = 16) has two TMEM buffers, P (bf16) replaces its
-// S there and O += P V (8 MMAs, A from TMEM) accumulates in 128 columns.  Four
+// keys.  S = Q K^T (12 MMAs of K = 16) and P (bf16) have two TMEM buffers each, so
+// that scores run two tiles ahead of the products (over its S, P held that back for
+// the product: 1.1 us a tile), and O += P V (8 MMAs, A from TMEM) accumulates in 128
+// columns.  Four
 // threads a row run the softmax, 32 keys each; the row maximum moves, and O is
 // rescaled, only when a score exceeds it by 2^8, on a vote of the four warps that
 // hold the same rows.  Keys and values have rings of their own, of 64-dim chunks,
@@ -65,7 +67,9 @@ constexpr int kBytesK = 7 * kChunkBytes;
 constexpr int kRingV = 4;
 constexpr int kItems = 4;
 constexpr int kBadItems = 8;
-constexpr uint32_t kTmemCols = 512;      // S: columns 0 .. 255, O: 256 .. 383
+constexpr uint32_t kTmemCols = 512;      // S: columns 0 .. 255, O: 256 .. 383, P: 384 .. 511
+constexpr int kColO = 2 * kTile;
+constexpr int kColP = kColO + kValDim;
 constexpr float kRescaleLog2 = 8.0f;
 constexpr int kMinPieceTiles = 4;
 
@@ -88,7 +92,7 @@ struct __align__(1024) Smem {
   uint8_t v[kRingV][kChunkBytes];
   uint64_t q_full, q_empty;
   uint64_t k_full[14], k_empty[14], v_full[kRingV], v_empty[kRingV];
-  uint64_t s_full[2], p_full[2], p_free[2];
+  uint64_t s_full[2], s_free[2], p_full[2], p_free[2];
   uint64_t o_full, o_empty;
   uint64_t item_full[kItems], next_full[kItems];
   uint64_t drained[2];
@@ -370,6 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.s_full[b], 1);
       mbar_init(&sm.p_full[b], kCtas * (kSoftWarps + 1));
       mbar_init(&sm.p_free[b], 1);
+      mbar_init(&sm.s_free[b], kCtas * kSoftWarps);
     }
     mbar_init(&sm.o_full, 1);
     mbar_init(&sm.o_empty, kCtas * kSoftWarps);
@@ -580,8 +585,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       #pragma unroll 1
       for (int left = uniform(it.t1 - it.t0); left > 0; --left, ++t) {
         const int b = t & 1;
-        // S buffer b holds P(t - 2) until its product is done.
-        if (t >= 2) ok = all_of(wait_for(&sm.p_free[b], ((t >> 1) - 1) & 1, p.err, ctl));
+        // (the softmax has taken the scores of tile t - 2)
+        if (t >= 2) ok = all_of(wait_for(&sm.s_free[b], ((t >> 1) - 1) & 1, p.err, ctl));
         #pragma unroll
         for (int c = 0; c < kKChunks; ++c) {
           ok = ok && all_of(wait_for(&sm.k_full[slot], phase, p.err, ctl));
@@ -645,10 +650,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t db = desc_v + (uint64_t)(slot * kStep);
             #pragma unroll
             for (int kk = 0; kk < kTile / 16; ++kk) {
-              // P: two keys a column, in the first 64 columns of its S buffer.
-              const uint32_t ta = tmem + b * kTile + kk * 8;
-              if (PAIR) mma_pair_ts(tmem + 2 * kTile, ta, db + kk * (2048 >> 4), kIdesc, j > 0 || kk > 0);
-              else tc_mma_f16_ts(tmem + 2 * kTile + c * 64, ta, db + kk * (2048 >> 4), kIdesc, j > 0 || kk > 0);
+              // P: two keys a column.
+              const uint32_t ta = tmem + kColP + b * (kTile / 2) + kk * 8;
+              if (PAIR) mma_pair_ts(tmem + kColO, ta, db + kk * (2048 >> 4), kIdesc, j > 0 || kk > 0);
+              else tc_mma_f16_ts(tmem + kColO + c * 64, ta, db + kk * (2048 >> 4), kIdesc, j > 0 || kk > 0);
             }
             commit(&sm.v_empty[slot]);
           }
@@ -676,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quad = warp & 3, part = warp >> 2;
     const int row = quad * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const uint32_t tO = tmem + lane_off + 2 * kTile + part * kPartKeys;
+    const uint32_t tO = tmem + lane_off + kColO + part * kPartKeys;
     int t = 0;
     bool ok = true;
     for (int n_item = 0;; ++n_item) {
@@ -701,6 +706,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         float v[kPartKeys];
         tmem_ld32(tS + part * kPartKeys, v);
         tc_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) PAIR ? arrive_at(first_cta(&sm.s_free[sb])) : mbar_arrive(&sm.s_free[sb]);
         if (kbase + kPartKeys - 1 > prow) {
           #pragma unroll
           for (int i = 0; i < kPartKeys; ++i)
@@ -721,10 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (kbase + i <= prow) mxp[i & 3] = fmaxf(mxp[i & 3], v[i] * p.scale_log2);
         }
         const float mxh = fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3]));
-        // The vote also orders the four warps' reads of S before any P write.
-        tc_fence_before();
         const bool exchange = barrier_or(kBarQuad + quad, 128, j == it.t0 || mxh > m + kRescaleLog2);
-        tc_fence_after();
         if (exchange) {
           sm.xrow[part][row] = mxh;
           named_barrier(kBarQuad + quad, 128);
@@ -743,8 +748,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           m = m_new;
         }
-        // P = exp2(s scale - m), two keys a column over the row's S; the sum adds
-        // the rounded values that the product uses.  (A row that saw no key yet
+        // P = exp2(s scale - m), two keys a column; the sum adds the rounded values
+        // that the product uses.  (A row that saw no key yet
         // has m = -inf.)
         const float ref = m == -INFINITY ? 0.f : m;
         const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
@@ -762,7 +767,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           w[e] = pack_bf16(fast_exp2(x.x), fast_exp2(x.y));
           add_bf16x2(sum_lo[e & 1], sum_hi[e & 1], w[e]);
         }
-        tmem_st16(tS + part * (kPartKeys / 2), w);
+        // (P's buffer is free once the product of tile t - 2 is done)
+        if (t >= 2) ok = ok && wait_for(&sm.p_free[sb], ((t >> 1) - 1) & 1, p.err, ctl);
+        tc_fence_after();
+        tmem_st16(tmem + lane_off + kColP + sb * (kTile / 2) + part * (kPartKeys / 2), w);
         tc_wait_st();
         l += (sum_lo[0] + sum_hi[0]) + (sum_lo[1] + sum_hi[1]);
         tc_fence_before();

@@ -1215,8 +1215,8 @@ int pkv_attention_latent(const void* q, const void* pool, const int32_t* block_t
     return fail(PKV_ERR_INVALID, "NULL pointer argument");
   if (!aligned16(q) || !aligned16(pool) || !aligned16(out))
     return fail(PKV_ERR_INVALID, "q, out and the pool must be 16-byte aligned");
-  if (!(scale - scale == 0.f) || scale == 0.f)
-    return fail(PKV_ERR_INVALID, "scale must be finite, non-zero");
+  if (!(scale > 0.f) || !(scale - scale == 0.f))
+    return fail(PKV_ERR_INVALID, "scale must be finite and positive");
   DeviceState* st = device_state();
   if (!st) return PKV_ERR_CUDA;
   const LatentLayout w = latent_layout(st->sm_count);
@@ -1330,8 +1330,8 @@ int pkv_attention_expanded(const void* q, const void* kv, const void* k_rope, co
     return fail(PKV_ERR_INVALID, "NULL pointer argument");
   if (!aligned16(q) || !aligned16(kv) || !aligned16(k_rope) || !aligned16(out))
     return fail(PKV_ERR_INVALID, "q, kv, k_rope and out must be 16-byte aligned");
-  if (!(scale - scale == 0.f) || scale == 0.f)
-    return fail(PKV_ERR_INVALID, "scale must be finite, non-zero");
+  if (!(scale > 0.f) || !(scale - scale == 0.f))
+    return fail(PKV_ERR_INVALID, "scale must be finite and positive");
   DeviceState* st = device_state();
   if (!st) return PKV_ERR_CUDA;
   const LatentLayout w = latent_layout(st->sm_count);

@@ -110,6 +110,12 @@ static_assert(sizeof(Smem) <= 227 * 1024, "latent prefill shared memory");
 
 __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
 
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -714,21 +720,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < kPartKeys; ++i)
             if (kbase + i > prow) v[i] = -INFINITY;
         }
-        // The largest of the scaled scores (a negative scale turns the order).
         float mxp[4];
         #pragma unroll
         for (int i = 0; i < 4; ++i) mxp[i] = -INFINITY;
-        if (p.scale_log2 > 0.f) {
-          #pragma unroll
-          for (int i = 0; i < kPartKeys / 2; ++i) mxp[i & 3] = fmax3(mxp[i & 3], v[2 * i], v[2 * i + 1]);
-          #pragma unroll
-          for (int i = 0; i < 4; ++i) mxp[i] *= p.scale_log2;
-        } else {
-          #pragma unroll
-          for (int i = 0; i < kPartKeys; ++i)
-            if (kbase + i <= prow) mxp[i & 3] = fmaxf(mxp[i & 3], v[i] * p.scale_log2);
-        }
-        const float mxh = fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3]));
+        #pragma unroll
+        for (int i = 0; i < kPartKeys / 2; ++i) mxp[i & 3] = fmax3(mxp[i & 3], v[2 * i], v[2 * i + 1]);
+        const float mxh = fmaxf(fmaxf(mxp[0], mxp[1]), fmaxf(mxp[2], mxp[3])) * p.scale_log2;
         const bool exchange = barrier_or(kBarQuad + quad, 128, j == it.t0 || mxh > m + kRescaleLog2);
         if (exchange) {
           sm.xrow[part][row] = mxh;
@@ -756,11 +753,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 nm2 = make_float2(-ref, -ref);
         float sum_lo[2] = {0.f, 0.f}, sum_hi[2] = {0.f, 0.f};
         uint32_t w[kPartKeys / 2];
-        if (p.scale_log2 < 0.f && kbase + kPartKeys - 1 > prow) {
-          #pragma unroll
-          for (int i = 0; i < kPartKeys; ++i)
-            if (kbase + i > prow) v[i] = INFINITY;  // times a negative scale
-        }
         #pragma unroll
         for (int e = 0; e < kPartKeys / 2; ++e) {
           const float2 x = ffma2(make_float2(v[2 * e], v[2 * e + 1]), sc2, nm2);
@@ -796,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = x[i];
         }
-        if (valid && ok && it.slot >= 0) {
+        if (!PAIR && valid && ok && it.slot >= 0) {
           if (part == 0)
             *reinterpret_cast<float2*>(p.piece_ml + ((long long)it.slot * kRows + row) * 2) = make_float2(m, lrow);
           float* dst = p.piece_o + ((long long)it.slot * kRows + row) * kValDim + part * kPartKeys;
@@ -804,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32; i += 4)
             *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
         } else if (valid && ok) {
-          const float inv = 1.f / lrow;
+          const float inv = reciprocal(lrow);
           __nv_bfloat16* dst =
               p.out + ((long long)(it.row0 + row) * p.num_heads + it.head) * kValDim + part * kPartKeys;
           #pragma unroll

@@ -121,7 +121,7 @@ struct __align__(1024) SmemT {
   uint8_t p[COLS * 128];  // P^T: [column][64 keys] bf16, 128-byte swizzle
   uint64_t kv_full[STAGES][kParts], kv_empty[STAGES][kParts];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full, p_free, o_full, o_empty;
+  uint64_t s_full[2], s_free[2], p_full, p_free, o_full, o_empty;
   uint64_t item_full[kItems];
   uint64_t drained[2];
   Item items[kItems];
@@ -260,13 +260,29 @@ static __device__ __noinline__ void plan_range(const LatentDecodeParams& p, Plan
     if (3ll * all_items <= 2 * units) {
       // ceil(keys / piece) summed over the items is at most their keys / piece + all_items.
       const long long all_keys = total - (long long)all_items * p.item_cost, room = units - all_items;
-      const long long least = (div_ll(all_keys + room - 1, room) + tile - 1) / tile * tile;
-      piece = (int)min(max(least, (long long)p.min_keys), 1ll << 30);
-      mine = 0;
-      each([&](const Req& a, int) {
-        mine += groups_units(p, a, a.ng, piece);
-        return true;
-      });
+      auto whole_tiles = [&](long long k) {
+        return (int)min(max((k + tile - 1) / tile * tile, (long long)p.min_keys), 1ll << 30);
+      };
+      auto count = [&]() {
+        mine = 0;
+        each([&](const Req& a, int) {
+          mine += groups_units(p, a, a.ng, piece);
+          return true;
+        });
+      };
+      const int most = whole_tiles(div_ll(all_keys + room - 1, room));
+      piece = most;
+      if (PER > 0) {
+        // Often a shorter one does: the shortest of eight steps that leaves no CTA two.
+        const int least = whole_tiles(div_ll(all_keys + units - 1, units));
+        const int step = max(tile, ((most - least) / 8 + tile - 1) / tile * tile);
+        for (piece = least; piece < most; piece += step) {
+          count();
+          if (__reduce_add_sync(0xffffffffu, (int)mine) <= units) break;
+        }
+        piece = min(piece, most);
+      }
+      count();
       if (THREADS > 32) __syncthreads();  // pl.part is free again
     }
   }
@@ -481,6 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.q_empty, 1);
     mbar_init(&sm.s_full[0], 1);
     mbar_init(&sm.s_full[1], 1);
+    mbar_init(&sm.s_free[0], kSoftWarps);
+    mbar_init(&sm.s_free[1], kSoftWarps);
     mbar_init(&sm.p_full, kSoftWarps);
     mbar_init(&sm.p_free, 1);
     mbar_init(&sm.o_full, 1);
@@ -684,14 +702,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kWarpS) {
     // ========================= MMAs of the scores =========================
-    // As soon as a tile's chunks land.  The buffer of S(t) was read by the softmax
-    // before the PV of tile t - 2, whose end tile t's latents waited for.
+    // As soon as a tile's chunks land and the softmax has read the scores of the tile
+    // two before, whose buffer this one's go to.
     const uint32_t idesc = idesc_bf16_f32(kMmaKeys, n_cols, 0, 0);
     const uint64_t desc_k = smem_desc_sw128(smem_u32(sm.kv[0][0]), 16, 1024);
     const uint64_t desc_q = smem_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
     const bool leader = elect_one();
     bool ok = true;
-    int st = 0, phase = 0, b = 0;
+    int st = 0, phase = 0, b = 0, s_phase = 1;  // (the first two tiles' buffers are free)
     for (int n_item = 0;; ++n_item) {
       ok = all_of(wait_for(&sm.q_full, n_item & 1, p.err, ctl));
       if (!ok) break;
@@ -700,6 +718,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       #pragma unroll 1
       for (int left = uniform(it.t1 - it.t0); left > 0; --left) {
         const uint64_t da = desc_k + (uint64_t)(st * (kChunks * kKvStep));
+        ok = all_of(wait_for(&sm.s_free[b], s_phase, p.err, ctl));
+        if (!ok) break;
         #pragma unroll
         for (int part = 0; part < kParts; ++part) {
           ok = all_of(wait_for(&sm.kv_full[st][part], phase, p.err, ctl));
@@ -722,6 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (left == 1) tc_commit(&sm.q_empty);
         }
         __syncwarp();
+        s_phase ^= b;
         b ^= 1;
         if (++st == STAGES) st = 0, phase ^= 1;
       }
@@ -829,6 +850,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           float v[8];
           tmem_ld_16x16(tmem + lane_off + (t & 1) * kLatMaxRows + wg * 16, v);
           tc_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.s_free[t & 1]);
           float mx[4];
           #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -906,6 +930,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int part = 0; part < kParts - 1; ++part)
             ok = ok && wait_for(&sm.kv_full[t % STAGES][part], (t / STAGES) & 1, p.err, ctl);
           clean_tile<TILE>(sm.kv[t % STAGES], key0, it.pos0, it.vis, bad, warp, lane);
+        }
+        if (!mine) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.s_free[t & 1]);
         }
         // P's buffer is free once the product before has read it.
         if (t > 0) ok = ok && wait_for(&sm.p_free, (t - 1) & 1, p.err, ctl);

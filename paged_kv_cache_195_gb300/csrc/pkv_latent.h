@@ -18,6 +18,27 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, int* er
   return mbar_try_wait(bar, parity) || wait_spin(bar, parity, err, ctl);
 }
 
+// Ways out of an aborted call.  Copies in flight must land before a CTA ends; those
+// whose barrier will not tell (the other CTA of a pair did not issue its part, or it
+// counts on the other's barrier) are given a time by which any copy has landed.
+constexpr unsigned long long kSettleNs = 10000000ull;
+
+static __device__ __noinline__ void settle() {
+  const unsigned long long t0 = global_timer_ns();
+  while (global_timer_ns() - t0 < kSettleNs) __nanosleep(1000);
+}
+
+static __device__ __noinline__ void drain(uint64_t* bar, uint32_t parity, int* err, WaitCtl* ctl) {
+  const unsigned long long t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    const unsigned long long waited = global_timer_ns() - t0;
+    if (waited > ctl->limit_ns && waited > kSettleNs) {
+      record_error(err, kErrTimeout);
+      return;
+    }
+  }
+}
+
 // The same value in all lanes, in a uniform register; and a vote.  Warps that issue
 // MMAs or copies keep their control flow uniform with these and guard nothing but
 // the instructions with one thread, so that descriptors and coordinates are in

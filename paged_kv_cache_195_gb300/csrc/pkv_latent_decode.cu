@@ -696,9 +696,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int part = 0; part < kParts; ++part) {
         const int n = t + (part < parts ? 1 : 0);  // tiles whose part was issued
         for (int i = max(0, n - STAGES); i < n; ++i)
-          mbar_wait_drain(&sm.kv_full[i % STAGES][part], (i / STAGES) & 1, p.err, ctl);
+          drain(&sm.kv_full[i % STAGES][part], (i / STAGES) & 1, p.err, ctl);
       }
-      if (n_item > 0) mbar_wait_drain(&sm.q_full, (n_item - 1) & 1, p.err, ctl);
+      if (n_item > 0) drain(&sm.q_full, (n_item - 1) & 1, p.err, ctl);
     }
   } else if (warp == kWarpS) {
     // ========================= MMAs of the scores =========================
@@ -752,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Aborted: the issued MMAs must end before TMEM is freed.
       if (leader) tc_commit(&sm.drained[0]);
       __syncwarp();
-      mbar_wait_drain(&sm.drained[0], 0, p.err, ctl);
+      drain(&sm.drained[0], 0, p.err, ctl);
     }
   } else if (warp == kWarpO) {
     // ========================= MMAs of the outputs ========================
@@ -802,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Aborted: the issued MMAs must end before TMEM is freed.
       if (leader) tc_commit(&sm.drained[1]);
       __syncwarp();
-      mbar_wait_drain(&sm.drained[1], 0, p.err, ctl);
+      drain(&sm.drained[1], 0, p.err, ctl);
     }
   } else {
     // ==================== softmax and epilogue (warps 0-15) ==================

@@ -258,11 +258,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Aborted: the copies in flight must land before the pair ends (the barrier
       // at the end keeps the other CTA's memory until then).
       for (int i = max(0, n_b - kStages); i < n_b; ++i)
-        mbar_wait_drain(&sm.b_full[i % kStages], (i / kStages) & 1, p.err, ctl);
+        drain(&sm.b_full[i % kStages], (i / kStages) & 1, p.err, ctl);
       for (int c = 0; c < kChunks; ++c) {
         const int n = n_tile + (c < chunks ? 1 : 0);
-        if (n > 0) mbar_wait_drain(&sm.a_full[c], (n - 1) & 1, p.err, ctl);
+        if (n > 0) drain(&sm.a_full[c], (n - 1) & 1, p.err, ctl);
       }
+    } else if (!ok) {
+      settle();
     }
   } else if (warp == kWarpMma && rank == 0) {
     // ============================ MMAs ====================================
@@ -304,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Aborted: the issued MMAs must end before TMEM is freed.
       if (leader) commit_pair(&sm.drained);
       __syncwarp();
-      mbar_wait_drain(&sm.drained, 0, p.err, ctl);
+      drain(&sm.drained, 0, p.err, ctl);
     }
   } else if (warp < kEpiWarps) {
     // ====================== rounding and stores (warps 0-3) ==================

@@ -288,10 +288,17 @@ __device__ __forceinline__ bool non_finite(uint32_t w) {
   return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
+// Two bf16 numbers, zeros for those that are not finite.
+__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  return (w & 0x7f800000u) == 0x7f800000u ? w & 0xffffu : w;
+}
+
 // Values of the tile's keys from pos0 + 1 on, the item's first token's position:
-// where any is not finite, those that no row of the item sees (from its last
-// token's position on) become zeros, and those of its own tokens that are not finite
-// too, noted in bad (a pair's: in both CTAs').  One warp; v: CHUNKS chunks of 64 dims.
+// where any is not finite, such rows that no row of the item sees (from its last
+// token's position on) become zeros; in those of its own tokens the numbers that are
+// not finite do, and the token is noted in bad (a pair's: in both CTAs').  One warp;
+// v: CHUNKS chunks of 64 dims.
 template <int CHUNKS, bool PAIR>
 static __device__ __noinline__ void clean_values(uint8_t (*v)[kChunkBytes], int key0, int pos0, int nt,
                                                  unsigned long long* bad, int rank, int lane) {
@@ -317,14 +324,19 @@ static __device__ __noinline__ void clean_values(uint8_t (*v)[kChunkBytes], int 
   #pragma unroll 1
   for (int row = first; row < kTile; ++row) {
     const int b = key0 + row - pos0 - 1;  // the item's token b + 1
-    const uint4 x = *at(row);
+    uint4 x = *at(row);
     if (!__any_sync(0xffffffffu, non_finite(x.x) || non_finite(x.y) || non_finite(x.z) || non_finite(x.w))) continue;
-    if (b < nt - 1 && lane == 0) {
-      atomicOr(bad + (b >> 6), 1ull << (b & 63));
-      if (PAIR) or_other(bad + (b >> 6), rank, 1ull << (b & 63));
+    if (b < nt - 1) {
+      if (lane == 0) {
+        atomicOr(bad + (b >> 6), 1ull << (b & 63));
+        if (PAIR) or_other(bad + (b >> 6), rank, 1ull << (b & 63));
+      }
+      x = make_uint4(finite_only(x.x), finite_only(x.y), finite_only(x.z), finite_only(x.w));
+    } else {
+      x = make_uint4(0, 0, 0, 0);
     }
     __syncwarp();
-    if (lane < kPieces) *at(row) = make_uint4(0, 0, 0, 0);
+    if (lane < kPieces) *at(row) = x;
   }
 }
 
@@ -492,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) {
         // Aborted: the copies in flight must land before the CTA ends.
         for (int i = max(0, n_chunk - kRingV); i < n_chunk; ++i)
-          mbar_wait_drain(&sm.v_full[i % kRingV], (i / kRingV) & 1, p.err, ctl);
+          drain(&sm.v_full[i % kRingV], (i / kRingV) & 1, p.err, ctl);
       }
     } else {
       // ---- items, queries and keys; a pair's on the first CTA's barriers
@@ -569,9 +581,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok && rank == 0) {
         // Aborted: the copies in flight must land before the CTA ends (the barrier at
         // the end keeps a pair's other CTA until then).
-        if (n_item > 0) mbar_wait_drain(&sm.q_full, (n_item - 1) & 1, p.err, ctl);
+        if (n_item > 0) drain(&sm.q_full, (n_item - 1) & 1, p.err, ctl);
         for (int i = max(0, n_chunk - kRingK); i < n_chunk; ++i)
-          mbar_wait_drain(&sm.k_full[i % kRingK], (i / kRingK) & 1, p.err, ctl);
+          drain(&sm.k_full[i % kRingK], (i / kRingK) & 1, p.err, ctl);
+      } else if (!ok) {
+        settle();
       }
     }
   } else if (warp == kWarpS && rank == 0) {
@@ -624,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Aborted: the issued MMAs must end before TMEM is freed.
       if (leader) commit(&sm.drained[0]);
       __syncwarp();
-      mbar_wait_drain(&sm.drained[0], 0, p.err, ctl);
+      drain(&sm.drained[0], 0, p.err, ctl);
     }
   } else if (warp == kWarpO && rank == 0) {
     // ========================= MMAs of the outputs ========================
@@ -678,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Aborted: the issued MMAs must end before TMEM is freed.
       if (leader) commit(&sm.drained[1]);
       __syncwarp();
-      mbar_wait_drain(&sm.drained[1], 0, p.err, ctl);
+      drain(&sm.drained[1], 0, p.err, ctl);
     }
   } else if (warp < kSoftWarps) {
     // ==================== softmax and epilogue (warps 0-15) ==================

@@ -327,8 +327,251 @@ def test_expanded_split_items(heads, lens, qs):
     exp_check(c, exp_run(c))
 
 
+@pytest.mark.parametrize("heads,lens,qs", [(16, [512] * 8, [512] * 8), (80, [700, 9, 0, 300], [514, 9, 0, 257]),
+                                           (33, [2000], [1200]), (128, [321, 321], [193, 320]),
+                                           (20, [256, 257, 384, 385, 511, 513, 600], [256, 257, 384, 129, 511, 513, 1])])
+def test_expanded_in_pairs(heads, lens, qs):
+    """Steps that take the form of two CTAs an item: whole pairs of query tiles, ones
+    whose second has few tokens or none, lengths at tile edges, empty requests."""
+    n, sms = sum(qs), torch.cuda.get_device_properties(0).multi_processor_count
+    assert n >= 192 * len(lens) and n * heads >= 256 * sms  # the host's rule
+    c = exp_case(lens, qs, heads, seed=heads)
+    exp_check(c, exp_run(c))
+
+
 def test_expanded_many_requests():
     rng = np.random.default_rng(6)
     lens = rng.integers(0, 150, 500).tolist()
     c = exp_case(lens, [min(n, int(q)) for n, q in zip(lens, rng.integers(0, 140, 500))], 1, seed=3)
     exp_check(c, exp_run(c))
+
+
+# ------------------------------------------------------------ special values
+def test_absorbed_special_values_reach_their_rows_only():
+    """A NaN or an infinity in one token's latent or rotated key, as the last but
+    one, a middle and an early token of a chunk: later tokens see it, earlier ones
+    must not (with several tokens to a work item they share its tiles)."""
+    for heads, m, at in ((4, 12, 5), (16, 3, 1), (1, 64, 40), (20, 3, 2), (2, 40, 0)):
+        for what in ("nan", "inf", "-inf"):
+            for part in ("latent", "rope"):
+                c = lat_case([100, 70], [m, min(m, 60)], heads, seed=m)
+                # -inf scores need a query that makes them: every query 1 in that dim
+                dim = 17 if part == "latent" else 530
+                c["q"][:, :, dim] = 1
+                pos = 100 - m + at
+                c["pool"][c["tab"][0, pos // 16], pos % 16, dim] = float(what)
+                lat_check(c, lat_run(c))
+
+
+def test_absorbed_row_that_sees_only_minus_infinity():
+    c = lat_case([3], [3], 2)
+    c["q"][:, :, 5] = 1
+    for j in range(3):
+        c["pool"][c["tab"][0, 0], j, 5] = float("-inf")
+    out = f64(lat_run(c))
+    assert np.isnan(out).all()  # exp(-inf - -inf): no weights at all
+
+
+def test_absorbed_extremes():
+    """Scores from far apart, equal keys, zero queries, a growing maximum."""
+    c = lat_case([700, 300], [2, 1], 24, seed=9)
+    c["q"][0] *= 30
+    c["q"][1] = 0
+    p = c["pool"]
+    ids = torch.from_numpy(c["tab"][0, :44].astype(np.int64)).cuda()
+    p[ids] = p[ids] * (torch.arange(44, device="cuda")[:, None, None] / 8 + 0.1).to(BF)
+    p[torch.from_numpy(c["tab"][1, :19].astype(np.int64)).cuda()] = 0.5
+    p[c["tab"][0, 43], 12:] = float("nan")
+    p[c["tab"][1, 18], 12:] = float("nan")
+    lat_check(c, lat_run(c))
+
+
+@pytest.mark.parametrize("heads,lens,qs", [(1, [200], [150]), (3, [400, 130], [256, 130]), (8, [700] * 8, [512] * 8),
+                                           (20, [700] * 4, [520] * 4)])
+def test_expanded_special_values_reach_their_rows_only(heads, lens, qs):
+    """Values and keys that are not finite at several of a chunk's own tokens (the last
+    set runs in pairs of CTAs)."""
+    for where, what in (("v", "nan"), ("v", "inf"), ("v", "-inf"), ("k", "nan"), ("r", "nan"), ("v2", "inf")):
+        c = exp_case(lens, qs, heads, seed=4)
+        m, n = qs[0], lens[0]
+        for i, at in enumerate((0, 1, m // 2, 127 % m, m - 2)):
+            pos = n - m + at
+            if where == "k":
+                c["kv"][pos, i % heads, 7] = float(what)
+            elif where == "r":
+                c["kr"][pos, 3] = float(what)
+            else:
+                c["kv"][pos, i % heads, 128 + 9 * i + (60 if where == "v2" else 0)] = float(what)
+        exp_check(c, exp_run(c))
+
+
+def test_expanded_ignores_what_follows_a_request():
+    """The rows of kv behind a request's end, another's or none's, hold NaN."""
+    c = exp_case([100, 60, 33], [100, 60, 33], 2, seed=5)
+    c["kv"][100:160] = float("nan")
+    c["kr"][100:160] = float("nan")
+    pad = torch.full((77, 2, 256), float("nan"), dtype=BF, device="cuda")
+    c["kv"], c["kr"] = torch.cat([c["kv"], pad]), torch.cat([c["kr"], pad[:, 0, :64].contiguous()])
+    out = f64(exp_run(c))
+    want, bound = ref.expanded(f64(c["q"]), np.nan_to_num(f64(c["kv"])), np.nan_to_num(f64(c["kr"])), c["lens"], c["qsl"],
+                               c["scale"])
+    live = np.r_[0:100, 160:193]
+    close(out[live], want[live], bound[live])
+    assert np.isnan(out[100:160]).all()
+
+
+def test_expand_special_values_stay_in_their_rows():
+    c = lat_case([70, 300], [1, 1], 1, seed=6)
+    w = torch.randn(3, 256, 512, device="cuda").to(BF)
+    for r, j, v in ((0, 3, "nan"), (0, 69, "inf"), (1, 128, "-inf")):
+        c["pool"][c["tab"][r, j // 16], j % 16, 40] = float(v)
+    kv, kr = torch.empty(370, 3, 256, dtype=BF, device="cuda"), torch.empty(370, 64, dtype=BF, device="cuda")
+    pkv.pkv_expand_latent(c["pool"], w, dev(c["tab"], torch.int32), dev(c["lens"], torch.int32),
+                          dev([0, 70, 370], torch.int32), kv, kr)
+    bad = [3, 69, 70 + 128]
+    assert (~torch.isfinite(kv[bad])).all()
+    keep = np.delete(np.arange(370), bad)
+    pool = torch.nan_to_num(c["pool"].float(), nan=0, posinf=0, neginf=0)
+    want, rope, bound = ref.expand(f64(pool), f64(w), c["tab"], c["lens"])
+    close(f64(kv)[keep], want[keep], bound[keep])
+
+
+# ------------------------------------------------------------ padding, errors, order of calls
+def test_padded_steps_leave_other_rows():
+    c = lat_case([40, 0, 300, 0], [1, 0, 3, 0], 16, pad=6)
+    out = torch.full((10, 16, 512), 7.0, dtype=BF, device="cuda")
+    lat_run(c, out=out)
+    lat_check(c, out)
+    assert (out[4:] == 7).all()
+    e = exp_case([40, 0, 300, 0], [1, 0, 3, 0], 4, pad=6)
+    out = torch.full((10, 4, 128), 7.0, dtype=BF, device="cuda")
+    exp_run(e, out=out)
+    exp_check(e, out)
+    assert (out[4:] == 7).all()
+
+
+BOUNDS = pkv._binding.PKV_ERR_DEVICE_BOUNDS
+
+
+def test_bad_lengths_and_blocks_are_reported():
+    """What the checks turn into an error: the request is skipped, the others are served."""
+    c = lat_case([40, 50, 60, 70], [1, 1, 1, 1], 8)
+    good = lat_run(c)
+    for r, n in ((1, 0), (1, -5), (2, 10 ** 6)):
+        bad = dict(c, lens=c["lens"].copy())
+        bad["lens"][r] = n
+        out = torch.full((4, 8, 512), 7.0, dtype=BF, device="cuda")
+        lat_run(bad, out=out)
+        assert pkv.pkv_get_device_error() == BOUNDS
+        rest = [i for i in range(4) if i != r]
+        assert (out[r] == 7).all() and torch.equal(out[rest], good[rest])
+    bad = dict(c, tab=c["tab"].copy())
+    bad["tab"][3, 2] = c["pool"].shape[0]
+    out = lat_run(bad)
+    assert pkv.pkv_get_device_error() == BOUNDS and torch.equal(out[:3], good[:3])
+    bad["tab"][3, 2] = -1
+    lat_run(bad)
+    assert pkv.pkv_get_device_error() == BOUNDS
+
+    n, w = 220, torch.randn(2, 256, 512, device="cuda").to(BF)
+    kv, kr = (torch.full(s, 7.0, dtype=BF, device="cuda") for s in ((n, 2, 256), (n, 64)))
+    args = (dev(c["tab"], torch.int32), dev(c["lens"], torch.int32))
+    ksl = [0, 40, 90, 150, 220]
+    pkv.pkv_expand_latent(c["pool"], w, *args, dev(ksl, torch.int32), kv, kr)
+    want_kv, want_kr = kv.clone(), kr.clone()
+    for starts, lost in (([0, 40, 89, 150, 220], (40, 150)), ([-1, 40, 90, 150, 220], (0, 40)), ([0, 40, 90, 150, 221], (150, 220))):
+        kv.fill_(7), kr.fill_(7)
+        pkv.pkv_expand_latent(c["pool"], w, *args, dev(starts, torch.int32), kv, kr)
+        assert pkv.pkv_get_device_error() == BOUNDS
+        live = np.r_[0:lost[0], lost[1]:220]
+        assert (kv[lost[0]:lost[1]] == 7).all() and torch.equal(kv[live], want_kv[live]) and torch.equal(kr[live], want_kr[live])
+
+    e = exp_case([40, 50, 60], [2, 50, 7], 2)
+    good = exp_run(e)
+    for key, i, v in (("lens", 1, 51), ("ksl", 3, 151), ("qsl", 3, 60), ("ksl", 0, -1)):
+        bad = dict(e, **{key: e[key].copy()})
+        bad[key][i] = v
+        out = torch.full_like(good, 7)
+        exp_run(bad, out=out)
+        assert pkv.pkv_get_device_error() == BOUNDS
+        r = i if key == "lens" else 2 if i == 3 else 0
+        assert (out[e["qsl"][r]:e["qsl"][r + 1]] == 7).all()
+        for o in range(3):
+            if o != r:
+                assert torch.equal(out[e["qsl"][o]:e["qsl"][o + 1]], good[e["qsl"][o]:e["qsl"][o + 1]])
+
+
+def test_repeated_calls_agree():
+    """The same call again and again, from a cache that is in L2 by then: the same
+    bits every time (no order of arrival changes a sum)."""
+    for c, run in ((lat_case([512] * 64, [1] * 64, 16), lat_run), (lat_case([700] * 100, [1] * 100, 128), lat_run),
+                   (lat_case([64] * 200, [1] * 200, 33), lat_run), (lat_case([900, 5000], [5, 1], 16), lat_run),
+                   (exp_case([600] * 8, [512] * 8, 16), exp_run), (exp_case([3000], [100], 2), exp_run)):
+        ws = pkv.LatentWorkspace()
+        first = run(c, workspace=ws).clone()
+        for _ in range(60):
+            assert torch.equal(run(c, workspace=ws), first)
+        assert pkv.pkv_get_device_error() == 0
+
+
+def test_one_workspace_serves_all_calls():
+    """Calls of different sizes and kinds, one after the other on one workspace, on a
+    stream that is not the current one."""
+    ws, s = pkv.LatentWorkspace(), torch.cuda.Stream()
+    cases = [(lat_case([3000, 20], [1, 3], 16), lat_run, lat_check), (exp_case([2000], [50], 2), exp_run, exp_check),
+             (lat_case([5], [1], 128), lat_run, lat_check), (exp_case([300] * 3, [256] * 3, 3), exp_run, exp_check),
+             (lat_case([900] * 20, [1] * 20, 64), lat_run, lat_check)]
+    torch.cuda.synchronize()
+    tensors = [[dev(c[k], torch.int32) for k in (("tab", "lens", "qsl") if "tab" in c else ("lens", "qsl", "ksl"))]
+               for c, _, _ in cases]
+    results = [torch.empty(*c["q"].shape[:2], 512 if "tab" in c else 128, dtype=BF, device="cuda") for c, _, _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(2):
+        for (c, _, _), t, out in zip(cases, tensors, results):
+            if "tab" in c:
+                pkv.pkv_attention_latent(c["q"], c["pool"], *t, c["scale"], out=out, workspace=ws, stream=s)
+            else:
+                pkv.pkv_attention_expanded(c["q"], c["kv"], c["kr"], *t, c["scale"], out=out, workspace=ws, stream=s)
+    s.synchronize()
+    for (c, _, check), out in zip(cases, results):
+        check(c, out)
+
+
+def test_without_a_workspace_on_another_stream():
+    c, s = lat_case([3000, 20], [1, 3], 16), torch.cuda.Stream()
+    t = [dev(c[k], torch.int32) for k in ("tab", "lens", "qsl")]
+    out = torch.empty(4, 16, 512, dtype=BF, device="cuda")
+    torch.cuda.synchronize()
+    pkv.pkv_attention_latent(c["q"], c["pool"], *t, c["scale"], out=out, stream=s)
+    s.synchronize()
+    lat_check(c, out)
+
+
+@pytest.mark.parametrize("option", [dict(pdl=0), dict(early_plan=0)])
+def test_launch_options(pkv_opts, option):
+    pkv_opts(**option)
+    c = lat_case([3000, 20, 77], [1, 3, 1], 16)
+    lat_check(c, lat_run(c))
+    c = lat_case([900] * 30, [1] * 30, 100)
+    lat_check(c, lat_run(c))
+    e = exp_case([2000, 5], [50, 5], 2)
+    exp_check(e, exp_run(e))
+
+
+def test_timeout_ends_the_call(pkv_opts):
+    """With a limit of a microsecond waits run out: the calls return, report it, and the
+    next ones (the workspace's head zeroed again) are right."""
+    c, e = lat_case([5000] * 4, [1] * 4, 128), exp_case([3000], [300], 4)
+    p = exp_case([600] * 8, [512] * 8, 16)
+    ws = pkv.LatentWorkspace()
+    saved = pkv.get_options()["wait_limit_us"]
+    for run, case in ((lat_run, c), (exp_run, e), (exp_run, p)):
+        pkv.set_options(wait_limit_us=1)
+        for _ in range(3):
+            run(case, workspace=ws)
+        assert pkv.pkv_get_device_error() in (0, pkv._binding.PKV_ERR_TIMEOUT)
+        pkv.set_options(wait_limit_us=saved)
+        ws = pkv.LatentWorkspace()
+    lat_check(c, lat_run(c, workspace=ws))
+    exp_check(e, exp_run(e, workspace=ws))
+    exp_check(p, exp_run(p, workspace=ws))

@@ -1247,8 +1247,8 @@ int pkv_attention_latent(const void* q, const void* pool, const int32_t* block_t
   p.head_groups = g.head_groups;
   p.group_heads = g.group_heads;
   p.group_tokens = g.group_tokens;
-  p.item_cost = 128;
-  p.min_keys = 256;
+  p.item_cost = 192;
+  p.min_keys = 128;
   // Without cuts, a step whose items have a CTA each and few keys needs no second
   // kernel.
   const long long units = st->sm_count / g.head_groups;

@@ -10,18 +10,20 @@
 // The values are the first 512 dims of the keys: a tile that came in for the
 // scores is there for the products too, and a key costs 1152 bytes of HBM and
 // 2176 flops a head.  Up to 64 heads that is bound by HBM; 128 heads bring the
-// tensor core near its own bound.
+// tensor core near its own bound.  Measured: 8 rows of 32768 keys, 16 heads, 66 us
+// (4.6 TB/s); 64 rows of 4096 keys, 128 heads, 103 us (711 TFLOP/s, 2.9 TB/s).
 //
 // Tiling.  A work item is a request's `group_tokens` query tokens times
 // `group_heads` heads: its (token, head) pairs are the N <= 64 columns of the
-// MMAs, so that few heads cost little.  A tile is 64 keys = 4 pool blocks, nine
-// 64-dim chunks of [64 keys][128 bytes], fetched block by block with 2-D TMA
+// MMAs, so that few heads cost little.  A tile is 64 keys = 4 pool blocks (or 48, see
+// below), nine 64-dim chunks of [keys][128 bytes], fetched block by block with 2-D TMA
 // copies (128-byte swizzle).  S^T[64 keys x N] = K Q^T accumulates over the
 // chunks; O^T[512 dims x N] += C^T P is four M = 128 tiles whose A operand is
 // the same chunks read MN-major.  O^T takes 256 TMEM columns, S^T two buffers
 // of 64.  The other way round (rows as M) O would need all 512 columns.
 // Shared memory holds Q (72 KB), two tiles (144 KB) and P (8 KB), all there
-// is; a tile is therefore loaded and released in five parts (the rotated keys,
+// is; items of up to 48 columns leave room for three tiles of 48 keys (8 x 32768 keys,
+// 16 heads: 66 us, and 83 in two of 64).  A tile is therefore loaded and released in five parts (the rotated keys,
 // four pairs of latent chunks), each going back as soon as its last MMA is
 // done, so that copies stay in flight while the other tile is worked on.
 //
@@ -34,7 +36,7 @@
 // the copies, warp 17 the MMAs of S^T, warp 18 those of O^T: neither waits for
 // the other, so that a tile goes back to the copies as soon as its own P is
 // there (one warp that issued S(t + 1) before PV(t) held every slot until the
-// next tile had landed: 106 us for ...).
+// next tile had landed: 106 us where two warps took 83, 8 x 32768 keys, 16 heads).
 //
 // Work split.  The items' keys (plus a fixed cost an item) form one sequence
 // that is cut in equal ranges, one a CTA -- or, with more than 64 heads, one a
@@ -468,6 +470,12 @@ __device__ __forceinline__ void tc_commit_both(uint64_t* bar) {
       : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+
 template <int COLS, int TILE, int STAGES, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
@@ -644,6 +652,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             cur = row_of(nxt);
             if (j + kWindow < j1) nxt = ids(j + kWindow);
           }
+          // Pairs wait for half of a tile's copies each, with one tile in flight while the
+          // other is worked on: the tile after next comes into L2 meanwhile (64 rows of
+          // 4096 keys, 128 heads: 103 us for 112; three or four tiles ahead 104 and 105).
+          int ahead[kTileBlocks];
+          if (PAIR) {
+            const int far = row_of(nxt);
+            #pragma unroll
+            for (int b = 0; b < kTileBlocks; ++b) {
+              const int l = k + 2 * kTileBlocks + b;
+              const int here = __shfl_sync(0xffffffffu, cur, l), there = __shfl_sync(0xffffffffu, far, l - kWindow * kTileBlocks);
+              ahead[b] = uniform(l < kWindow * kTileBlocks ? here : there);
+            }
+          }
           int rows[kTileBlocks];
           #pragma unroll
           for (int b = 0; b < kTileBlocks; ++b) rows[b] = uniform(__shfl_sync(0xffffffffu, cur, k + b));
@@ -672,6 +693,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             parts = part + 1;
           }
           if (!ok) break;
+          if (PAIR && leader && j + 2 < j1) {
+            #pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+              #pragma unroll
+              for (int b = 0; b < kTileBlocks; ++b)
+                if (((c * kTileBlocks + b) & 1) == hg) tma_prefetch_2d(&kmap, c * 64, ahead[b]);
+            }
+          }
+          __syncwarp();
           parts = 0;
           ++t;
           if (++st == STAGES) st = 0, phase ^= 1;

@@ -15,15 +15,15 @@
 //
 // Tiling.  A work item is a request's `group_tokens` query tokens times
 // `group_heads` heads: its (token, head) pairs are the N <= 64 columns of the
-// MMAs, so that few heads cost little.  A tile is 64 keys = 4 pool blocks (or 48, see
-// below), nine 64-dim chunks of [keys][128 bytes], fetched block by block with 2-D TMA
+// MMAs, so that few heads cost little.  A tile is 64 keys = 4 pool blocks, nine
+// 64-dim chunks of [64 keys][128 bytes], fetched block by block with 2-D TMA
 // copies (128-byte swizzle).  S^T[64 keys x N] = K Q^T accumulates over the
 // chunks; O^T[512 dims x N] += C^T P is four M = 128 tiles whose A operand is
 // the same chunks read MN-major.  O^T takes 256 TMEM columns, S^T two buffers
 // of 64.  The other way round (rows as M) O would need all 512 columns.
 // Shared memory holds Q (72 KB), two tiles (144 KB) and P (8 KB), all there
-// is; items of up to 48 columns leave room for three tiles of 48 keys (8 x 32768 keys,
-// 16 heads: 66 us, and 83 in two of 64).  A tile is therefore loaded and released in five parts (the rotated keys,
+// is (three tiles of 48 keys, which up to 48 columns leave room for, were no faster
+// anywhere: 8 x 32768 keys, 16 heads 66.6 us for 65.1).  A tile is therefore loaded and released in five parts (the rotated keys,
 // four pairs of latent chunks), each going back as soon as its last MMA is
 // done, so that copies stay in flight while the other tile is worked on.
 //
@@ -63,7 +63,12 @@ constexpr int kBarGroup = 2;  // + warpgroup
 constexpr int kChunks = kLatRow / 64;     // 64-dim chunks of a row
 constexpr int kParts = 5;                 // release units of a tile: four latent pairs, rotated keys
 constexpr int kItems = 4;
-constexpr int kMmaKeys = 64;              // M of the scores' MMAs
+constexpr int kTile = 64;                 // keys of a tile
+constexpr int kTileBlocks = kTile / kBlockSize;
+constexpr int kWindow = 32 / kTileBlocks; // tiles of a load of block ids
+constexpr int kStages = 2;
+constexpr int kChunkBytes = kTile * 128;  // 64 dims of a tile's keys, or of 64 columns' queries
+static_assert(kTile == kLatMaxRows, "chunks of keys and of queries are alike");
 constexpr uint32_t kTmemCols = 512;
 constexpr int kColO = 2 * kLatMaxRows;    // TMEM: S^T buffers, then O^T
 constexpr float kRescaleLog2 = 8.0f;
@@ -115,15 +120,13 @@ struct Plan {
   int start_req, piece;
 };
 
-// COLS: columns that there is room for; TILE keys in each of STAGES tiles.
-template <int COLS, int TILE, int STAGES>
-struct __align__(1024) SmemT {
-  uint8_t q[kChunks][COLS * 128];
-  uint8_t kv[STAGES][kChunks][TILE * 128];
-  uint8_t p[COLS * 128];  // P^T: [column][64 keys] bf16, 128-byte swizzle
-  uint64_t kv_full[STAGES][kParts], kv_empty[STAGES][kParts];
+struct __align__(1024) Smem {
+  uint8_t q[kChunks][kChunkBytes];
+  uint8_t kv[kStages][kChunks][kChunkBytes];
+  uint8_t p[kLatMaxRows * 128];  // P^T: [column][64 keys] bf16, 128-byte swizzle
+  uint64_t kv_full[kStages][kParts], kv_empty[kStages][kParts];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], s_free[2], p_full, p_free, o_full, o_empty;
+  uint64_t s_full[2], p_full, p_free, o_full, o_empty;
   uint64_t item_full[kItems];
   uint64_t drained[2];
   Item items[kItems];
@@ -138,6 +141,7 @@ struct __align__(1024) SmemT {
   uint32_t tmem_base;
   WaitCtl wait;
 };
+static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "latent decode shared memory");
 
 // Part i's chunks: 2 i and 2 i + 1, of the last part the one with the rotated keys.
 __host__ __device__ constexpr int part_chunks(int part) { return part == kParts - 1 ? 1 : 2; }
@@ -356,8 +360,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // Address of 16-byte piece `piece` (0 .. 63) of key row `row`'s latent in a tile.
-template <int TILE>
-__device__ __forceinline__ uint4* latent_piece(uint8_t (*tile)[TILE * 128], int row, int piece) {
+__device__ __forceinline__ uint4* latent_piece(uint8_t (*tile)[kChunkBytes], int row, int piece) {
   return reinterpret_cast<uint4*>(tile[piece >> 3] + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
 }
 
@@ -371,23 +374,22 @@ __device__ __forceinline__ bool non_finite(uint32_t w) {
 // that the others must not get: those are taken out too and noted, and the
 // epilogue gives them to the rows that see them.  Rare or at a range's last
 // tiles; one warp a row, out of line.
-template <int TILE>
-static __device__ __noinline__ void clean_tile(uint8_t (*tile)[TILE * 128], int key0, int pos0, int vis,
+static __device__ __noinline__ void clean_tile(uint8_t (*tile)[kChunkBytes], int key0, int pos0, int vis,
                                                unsigned long long* bad, int warp, int lane) {
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int row = max(pos0 + 1 - key0, 0) + warp; row < TILE; row += kSoftWarps) {
+  for (int row = max(pos0 + 1 - key0, 0) + warp; row < kTile; row += kSoftWarps) {
     const int key = key0 + row;
     bool out = key >= vis;
     if (!out) {
-      const uint4 a = *latent_piece<TILE>(tile, row, lane), b = *latent_piece<TILE>(tile, row, lane + 32);
+      const uint4 a = *latent_piece(tile, row, lane), b = *latent_piece(tile, row, lane + 32);
       out = __any_sync(0xffffffffu, non_finite(a.x) || non_finite(a.y) || non_finite(a.z) ||
                                         non_finite(a.w) || non_finite(b.x) || non_finite(b.y) ||
                                         non_finite(b.z) || non_finite(b.w));
       if (out && lane == 0) atomicOr(bad, 1ull << (key - pos0 - 1));
     }
     if (out) {
-      *latent_piece<TILE>(tile, row, lane) = zero;
-      *latent_piece<TILE>(tile, row, lane + 32) = zero;
+      *latent_piece(tile, row, lane) = zero;
+      *latent_piece(tile, row, lane + 32) = zero;
     }
   }
   fence_proxy_async_smem();
@@ -476,17 +478,13 @@ __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, i
                : "memory");
 }
 
-template <int COLS, int TILE, int STAGES, bool PAIR>
+template <bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
                          const __grid_constant__ CUtensorMap kmap, const LatentDecodeParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
-  using Smem = SmemT<COLS, TILE, STAGES>;
-  constexpr int kTileBlocks = TILE / kBlockSize;
-  constexpr int kWindow = 32 / kTileBlocks;         // tiles of a load of block ids
-  constexpr int kKvStep = TILE * 128 >> 4;          // a chunk in the unit of the MMA's descriptors
-  constexpr int kQStep = COLS * 128 >> 4;
+  constexpr int kStep = kChunkBytes >> 4;  // a chunk in the unit of the MMA's descriptors
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw + (((raw + 1023u) & ~1023u) - raw));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   WaitCtl* ctl = &sm.wait;
@@ -496,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int heads = min(p.group_heads, p.num_q_heads - head0);
 
   if (tid == 0) {
-    for (int s = 0; s < STAGES; ++s)
+    for (int s = 0; s < kStages; ++s)
       for (int i = 0; i < kParts; ++i) {
         mbar_init(&sm.kv_full[s][i], 1);
         mbar_init(&sm.kv_empty[s][i], PAIR ? 2 : 1);
@@ -505,8 +503,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.q_empty, 1);
     mbar_init(&sm.s_full[0], 1);
     mbar_init(&sm.s_full[1], 1);
-    mbar_init(&sm.s_free[0], kSoftWarps);
-    mbar_init(&sm.s_free[1], kSoftWarps);
     mbar_init(&sm.p_full, kSoftWarps);
     mbar_init(&sm.p_free, 1);
     mbar_init(&sm.o_full, 1);
@@ -531,11 +527,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (p.num_reqs <= kWarpReqs) {
     if (warp == kWarpLoad) {
       if (!p.early_plan) grid_dependency_wait();
-      plan_range<32, kWarpPer>(p, sm.plan, unit, units, TILE);
+      plan_range<32, kWarpPer>(p, sm.plan, unit, units, kTile);
     }
   } else {
     if (!p.early_plan) grid_dependency_wait();
-    plan_range<kThreads, 0>(p, sm.plan, unit, units, TILE);
+    plan_range<kThreads, 0>(p, sm.plan, unit, units, kTile);
   }
   tc_fence_before();
   __syncthreads();
@@ -600,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         it.nt = min(p.group_tokens, a.qr - g * p.group_tokens);
         it.pos0 = a.L - a.qr + g * p.group_tokens;
         it.vis = it.pos0 + it.nt;
-        const int tiles = cdiv(it.vis, TILE);
+        const int tiles = cdiv(it.vis, kTile);
         it.t0 = 0;
         it.t1 = tiles;
         if (piece > 0) {
@@ -611,9 +607,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             it.t1 = (int)((long long)tiles * (x + 1) / n);
           }
         } else {
-          // Tile j belongs to the range that holds unit gbase + TILE j.
-          if (gbase < lo) it.t0 = (int)((lo - gbase + TILE - 1) / TILE);
-          if (hi - gbase < it.vis) it.t1 = (int)((hi - gbase + TILE - 1) / TILE);
+          // Tile j belongs to the range that holds unit gbase + kTile j.
+          if (gbase < lo) it.t0 = (int)((lo - gbase + kTile - 1) / kTile);
+          if (hi - gbase < it.vis) it.t1 = (int)((hi - gbase + kTile - 1) / kTile);
         }
         it.end = 0;
         if (it.t0 >= it.t1) continue;
@@ -676,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             if (leader) {
               uint64_t* const bar = &sm.kv_full[st][part];
-              mbar_arrive_expect_tx(bar, (uint32_t)part_chunks(part) * TILE * 128);
+              mbar_arrive_expect_tx(bar, (uint32_t)part_chunks(part) * kTile * 128);
               #pragma unroll
               for (int i = 0; i < part_chunks(part); ++i) {
                 const int c = 2 * part + i;
@@ -704,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           parts = 0;
           ++t;
-          if (++st == STAGES) st = 0, phase ^= 1;
+          if (++st == kStages) st = 0, phase ^= 1;
         }
       }
       base += w;
@@ -725,21 +721,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       #pragma unroll 1
       for (int part = 0; part < kParts; ++part) {
         const int n = t + (part < parts ? 1 : 0);  // tiles whose part was issued
-        for (int i = max(0, n - STAGES); i < n; ++i)
-          drain(&sm.kv_full[i % STAGES][part], (i / STAGES) & 1, p.err, ctl);
+        for (int i = max(0, n - kStages); i < n; ++i)
+          drain(&sm.kv_full[i % kStages][part], (i / kStages) & 1, p.err, ctl);
       }
       if (n_item > 0) drain(&sm.q_full, (n_item - 1) & 1, p.err, ctl);
     }
   } else if (warp == kWarpS) {
     // ========================= MMAs of the scores =========================
-    // As soon as a tile's chunks land and the softmax has read the scores of the tile
-    // two before, whose buffer this one's go to.
-    const uint32_t idesc = idesc_bf16_f32(kMmaKeys, n_cols, 0, 0);
+    // As soon as a tile's chunks land.  Its scores go to the buffer of the tile two
+    // before, which had the same place in shared memory: its latents went back behind its
+    // P, for which the softmax had read the scores.
+    const uint32_t idesc = idesc_bf16_f32(kTile, n_cols, 0, 0);
     const uint64_t desc_k = smem_desc_sw128(smem_u32(sm.kv[0][0]), 16, 1024);
     const uint64_t desc_q = smem_desc_sw128(smem_u32(sm.q[0]), 16, 1024);
     const bool leader = elect_one();
     bool ok = true;
-    int st = 0, phase = 0, b = 0, s_phase = 1;  // (the first two tiles' buffers are free)
+    int st = 0, phase = 0;
     for (int n_item = 0;; ++n_item) {
       ok = all_of(wait_for(&sm.q_full, n_item & 1, p.err, ctl));
       if (!ok) break;
@@ -747,9 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (uniform(it.end)) break;
       #pragma unroll 1
       for (int left = uniform(it.t1 - it.t0); left > 0; --left) {
-        const uint64_t da = desc_k + (uint64_t)(st * (kChunks * kKvStep));
-        ok = all_of(wait_for(&sm.s_free[b], s_phase, p.err, ctl));
-        if (!ok) break;
+        const uint64_t da = desc_k + (uint64_t)(st * (kChunks * kStep));
         #pragma unroll
         for (int part = 0; part < kParts; ++part) {
           ok = all_of(wait_for(&sm.kv_full[st][part], phase, p.err, ctl));
@@ -759,22 +754,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             #pragma unroll
             for (int kk = 0; kk < (part == kParts - 1 ? 4 : 8); ++kk) {
               const int c = 2 * part + (kk >> 2);
-              tc_mma_f16_ss(tmem + b * kLatMaxRows, da + (c * kKvStep + 2 * (kk & 3)),
-                            desc_q + (c * kQStep + 2 * (kk & 3)), idesc, part > 0 || kk > 0);
+              tc_mma_f16_ss(tmem + st * kLatMaxRows, da + (c * kStep + 2 * (kk & 3)),
+                            desc_q + (c * kStep + 2 * (kk & 3)), idesc, part > 0 || kk > 0);
             }
           }
           __syncwarp();
         }
         if (!ok) break;
         if (leader) {
-          tc_commit(&sm.s_full[b]);
+          tc_commit(&sm.s_full[st]);
           PAIR ? tc_commit_both(&sm.kv_empty[st][kParts - 1]) : tc_commit(&sm.kv_empty[st][kParts - 1]);
           if (left == 1) tc_commit(&sm.q_empty);
         }
         __syncwarp();
-        s_phase ^= b;
-        b ^= 1;
-        if (++st == STAGES) st = 0, phase ^= 1;
+        if (++st == kStages) st = 0, phase ^= 1;
       }
       if (!ok) break;
     }
@@ -787,8 +780,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kWarpO) {
     // ========================= MMAs of the outputs ========================
     const uint32_t idesc = idesc_bf16_f32(128, n_cols, 1, 0);
-    // C^T: MN-major atoms of 64 dims x 8 keys, the chunks TILE * 128 bytes apart.
-    const uint64_t desc_v = smem_desc_sw128(smem_u32(sm.kv[0][0]), TILE * 128, 1024);
+    // C^T: MN-major atoms of 64 dims x 8 keys, the chunks kTile * 128 bytes apart.
+    const uint64_t desc_v = smem_desc_sw128(smem_u32(sm.kv[0][0]), kTile * 128, 1024);
     const uint64_t desc_p = smem_desc_sw128(smem_u32(sm.p), 16, 1024);
     const bool leader = elect_one();
     bool ok = true;
@@ -810,12 +803,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         if (leader) {
-          const uint64_t da = desc_v + (uint64_t)(st * (kChunks * kKvStep));
+          const uint64_t da = desc_v + (uint64_t)(st * (kChunks * kStep));
           #pragma unroll
           for (int m = 0; m < 4; ++m) {
             #pragma unroll
-            for (int kk = 0; kk < TILE / 16; ++kk)
-              tc_mma_f16_ss(tmem + kColO + m * kLatMaxRows, da + (2 * m * kKvStep + kk * (2048 >> 4)),
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              tc_mma_f16_ss(tmem + kColO + m * kLatMaxRows, da + (2 * m * kStep + kk * (2048 >> 4)),
                             desc_p + 2 * kk, idesc, j > 0 || kk > 0);
             PAIR ? tc_commit_both(&sm.kv_empty[st][m]) : tc_commit(&sm.kv_empty[st][m]);
           }
@@ -824,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         p_phase ^= 1;
-        if (++st == STAGES) st = 0, phase ^= 1;
+        if (++st == kStages) st = 0, phase ^= 1;
       }
       if (!ok) break;
     }
@@ -844,8 +837,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // 16 quad + lane / 4 + 8 h.
     const int col0 = wg * 16 + 2 * (lane & 3);
     const int key_lo = quad * 16 + (lane >> 2);
-    // (rows of the MMA past the tile's keys are scores of nothing)
-    const bool in_tile = quad * 16 < TILE;
     int tok[4];  // query token of each column; -1: none
     #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -872,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       #pragma unroll
       for (int i = 0; i < 4; ++i) m[i] = -INFINITY, l[i] = 0.f;
       for (int j = it.t0; j < it.t1; ++j, ++t) {
-        const int key0 = j * TILE;
+        const int key0 = j * kTile;
         ok = ok && wait_for(&sm.s_full[t & 1], (t >> 1) & 1, p.err, ctl);
         tc_fence_after();
         uint32_t w[4];
@@ -880,9 +871,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           float v[8];
           tmem_ld_16x16(tmem + lane_off + (t & 1) * kLatMaxRows + wg * 16, v);
           tc_wait_ld();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.s_free[t & 1]);
           float mx[4];
           #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -891,8 +879,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             float& b = v[4 * (i >> 1) + 2 + (i & 1)];
             a *= p.scale_log2;
             b *= p.scale_log2;
-            if (!in_tile || key0 + key_lo > limit[i]) a = -INFINITY;
-            if (!in_tile || key0 + key_lo + 8 > limit[i]) b = -INFINITY;
+            if (key0 + key_lo > limit[i]) a = -INFINITY;
+            if (key0 + key_lo + 8 > limit[i]) b = -INFINITY;
             mx[i] = fmaxf(a, b);
           }
           bool grow = j == it.t0;
@@ -954,16 +942,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             add_bf16x2(l[2 * c], l[2 * c + 1], w[2 * c + 1]);
           }
         }
-        if (key0 + TILE > it.pos0 + 1) {
+        if (key0 + kTile > it.pos0 + 1) {
           // (landed long since: the scores came from them)
           #pragma unroll 1
           for (int part = 0; part < kParts - 1; ++part)
-            ok = ok && wait_for(&sm.kv_full[t % STAGES][part], (t / STAGES) & 1, p.err, ctl);
-          clean_tile<TILE>(sm.kv[t % STAGES], key0, it.pos0, it.vis, bad, warp, lane);
-        }
-        if (!mine) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.s_free[t & 1]);
+            ok = ok && wait_for(&sm.kv_full[t % kStages][part], (t / kStages) & 1, p.err, ctl);
+          clean_tile(sm.kv[t % kStages], key0, it.pos0, it.vis, bad, warp, lane);
         }
         // P's buffer is free once the product before has read it.
         if (t > 0) ok = ok && wait_for(&sm.p_free, (t - 1) & 1, p.err, ctl);
@@ -976,7 +960,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&sm.p_full);
       }
       // ---- epilogue ---------------------------------------------------------
-      const int n_tiles = cdiv(it.vis, TILE);
+      const int n_tiles = cdiv(it.vis, kTile);
       const bool whole = it.t0 == 0 && it.t1 == n_tiles;
       const int slot = 2 * blockIdx.x + (it.t0 == 0 ? 1 : 0);
       // Columns in use: rows (token, head) of out from the first on, in order
@@ -1147,18 +1131,16 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const La
   }
 }
 
-template <int COLS, int TILE, int STAGES, bool PAIR>
+template <bool PAIR>
 cudaError_t launch_decode(const LatentDecodeLaunch& L, cudaStream_t stream) {
-  using Smem = SmemT<COLS, TILE, STAGES>;
   constexpr size_t smem = sizeof(Smem) + 1024;
-  static_assert(smem <= 227 * 1024, "latent decode shared memory");
   static unsigned long long configured = 0;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & bit)) {
-    e = cudaFuncSetAttribute(latent_decode_kernel<COLS, TILE, STAGES, PAIR>,
+    e = cudaFuncSetAttribute(latent_decode_kernel<PAIR>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     __atomic_fetch_or(&configured, bit, __ATOMIC_RELEASE);
@@ -1176,17 +1158,14 @@ cudaError_t launch_decode(const LatentDecodeLaunch& L, cudaStream_t stream) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = PAIR ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, latent_decode_kernel<COLS, TILE, STAGES, PAIR>, L.qmap, L.kmap, L.p);
+  return cudaLaunchKernelEx(&cfg, latent_decode_kernel<PAIR>, L.qmap, L.kmap, L.p);
 }
 
 }  // namespace
 
 cudaError_t launch_latent_decode(const LatentDecodeLaunch& L, cudaStream_t stream) {
-  // Up to 48 columns leave room for three tiles of 48 keys.
   const int rows = L.p.group_heads * L.p.group_tokens;
-  const bool pair = L.p.head_groups == 2;
-  cudaError_t e = rows <= 48 ? (pair ? launch_decode<48, 48, 3, true>(L, stream) : launch_decode<48, 48, 3, false>(L, stream))
-                             : (pair ? launch_decode<64, 64, 2, true>(L, stream) : launch_decode<64, 64, 2, false>(L, stream));
+  cudaError_t e = L.p.head_groups == 2 ? launch_decode<true>(L, stream) : launch_decode<false>(L, stream);
   if (e == cudaSuccess && L.p.merge) {
     cudaLaunchConfig_t cfg = {};
     const int split = rows <= 16 ? 4 : 1;

@@ -1053,19 +1053,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the pieces of rows that were cut.  Block (b, y): eight columns of the item
 // whose first piece is in CTA b's last slot, if any; its later pieces are in the
-// first slots of the next CTAs of the same head group.  SPLIT warps a column, 16 /
-// SPLIT dims a lane (few columns have many pieces, and few warps else); flags and
+// first slots of the next CTAs of the same head group.  A warp a column; flags and
 // statistics of up to 32 pieces are read at once, a lane each, and the loads of the
 // outputs depend on nothing but them.
 constexpr int kMergeWarps = 8;
 
-template <int SPLIT>
 __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const LatentDecodeParams p, int grid) {
   grid_dependency_wait();
   allow_dependent_launch();
   const int cta = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int kVecs = 4 / SPLIT;  // of four dims, a lane
-  const int row = (blockIdx.y * kMergeWarps + warp) / SPLIT, at = warp % SPLIT * kVecs * 32 + lane;
+  constexpr int kVecs = 4;  // of four dims, a lane
+  const int row = blockIdx.y * kMergeWarps + warp;
   const int4 rec = *reinterpret_cast<const int4*>(p.piece + (2 * cta + 1) * kPieceWords);
   float m = -INFINITY, l = 0.f;
   float4 o[kVecs];
@@ -1104,14 +1102,14 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const La
     #pragma unroll
     for (int k = 0; k < kVecs; ++k) o[k] = make_float4(o[k].x * keep, o[k].y * keep, o[k].z * keep, o[k].w * keep);
     m = top;
-    #pragma unroll SPLIT == 1 ? 4 : 8
+    #pragma unroll 4
     for (int i = 0; i < n; ++i) {
       const float wi = __shfl_sync(0xffffffffu, w, i);
       const int si = __shfl_sync(0xffffffffu, slot, i);
       const float4* src = reinterpret_cast<const float4*>(p.piece_o + ((long long)si * p.piece_rows + row) * kLatent);
       #pragma unroll
       for (int k = 0; k < kVecs; ++k) {
-        const float4 v = src[k * 32 + at];
+        const float4 v = src[k * 32 + lane];
         o[k].x += v.x * wi;
         o[k].y += v.y * wi;
         o[k].z += v.z * wi;
@@ -1127,7 +1125,125 @@ __global__ void __launch_bounds__(32 * kMergeWarps) latent_merge_kernel(const La
     uint2 v;
     v.x = pack_bf16(o[k].x * inv, o[k].y * inv);
     v.y = pack_bf16(o[k].z * inv, o[k].w * inv);
-    reinterpret_cast<uint2*>(p.out + out_row * kLatent)[k * 32 + at] = v;
+    reinterpret_cast<uint2*>(p.out + out_row * kLatent)[k * 32 + lane] = v;
+  }
+}
+
+// The same for few items of many pieces, which the warps of an item's own blocks alone
+// took long to read (with the attention, a row of 32768 keys, 128 heads: 57 us, 33
+// here; 16 rows of 2000 to 8000 keys, 32 heads 34.0 and 32.5, 8 rows of 32768 keys, 16
+// heads 64.8 and 65.8).  A unit is 128 dims of a column;
+// every block counts the items from the records and takes its share of the units.
+// With units for less than half of the warps, two, four or eight of a block share one:
+// its pieces in turn, the sums joined through shared memory.
+constexpr int kFewSplit = 4;
+constexpr int kFewBlocks = 4;    // an SM
+constexpr int kCtaGroups = 8;    // of 32 CTAs' records
+
+__global__ void __launch_bounds__(32 * kMergeWarps, kFewBlocks)
+    latent_merge_few_kernel(const LatentDecodeParams p, int grid) {
+  __shared__ float4 part[kMergeWarps][32];
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned starts[kCtaGroups];
+  int items = 0;
+  #pragma unroll
+  for (int g = 0; g < kCtaGroups; ++g)
+    starts[g] = g * 32 + lane < grid ? p.piece[(2 * (g * 32 + lane) + 1) * kPieceWords] : 0;
+  #pragma unroll
+  for (int g = 0; g < kCtaGroups; ++g) {
+    starts[g] = __ballot_sync(0xffffffffu, starts[g] != 0);
+    items += __popc(starts[g]);
+  }
+  const int per_item = p.piece_rows * kFewSplit, units = items * per_item, warps = gridDim.x * kMergeWarps;
+  if (items == 0) return;
+  int share = 1;  // warps a unit
+  while (share < kMergeWarps && units * share * 2 <= warps) share *= 2;
+  for (int u = (blockIdx.x * kMergeWarps + warp) / share; u < units || share > 1; u += warps / share) {
+    // (with more than one warp a unit there is one round for all)
+    const int nth = u / per_item, row = u % per_item / kFewSplit, at = u % kFewSplit * 32 + lane;
+    int cta = -1;
+    #pragma unroll
+    for (int g = 0, before = 0; g < kCtaGroups; ++g) {
+      const bool here = ((starts[g] >> lane) & 1) && before + __popc(starts[g] & ((1u << lane) - 1)) == nth;
+      const unsigned who = __ballot_sync(0xffffffffu, here);
+      if (who) cta = g * 32 + __ffs(who) - 1;
+      before += __popc(starts[g]);
+    }
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    int4 rec = make_int4(0, 0, 0, 0);
+    if (cta >= 0) rec = *reinterpret_cast<const int4*>(p.piece + (2 * cta + 1) * kPieceWords);
+    // Lane i: piece first + i.
+    int flags = 0, slot = 0;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    auto load = [&](int first) {
+      const int c = cta + (first + lane) * p.head_groups;
+      slot = first + lane == 0 ? 2 * cta + 1 : 2 * c;
+      flags = 0;
+      if (c < grid) {
+        flags = p.piece[slot * kPieceWords];
+        ml = *reinterpret_cast<const float2*>(p.piece_ml + ((long long)slot * p.piece_rows + row) * 2);
+      }
+    };
+    if (cta >= 0) load(0);
+    const bool have = row < rec.z;
+    bool last = !have;
+    for (int first = 0; !last; first += 32) {
+      const unsigned ends = __ballot_sync(0xffffffffu, (flags & kPieceLast) != 0);
+      // (a record that is missing, of an aborted CTA, ends the item as well)
+      const unsigned holes = __ballot_sync(0xffffffffu, flags == 0);
+      int n = 32;
+      if (ends) n = min(n, __ffs(ends));
+      if (holes) n = min(n, __ffs(holes) - 1);
+      last = n < 32 || ends != 0;
+      float top = lane < n ? ml.x : -INFINITY;
+      #pragma unroll
+      for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+      top = fmaxf(top, m);
+      const float keep = m == -INFINITY ? 0.f : fast_exp2(m - top);
+      // (a piece of which the row saw no key weighs nothing)
+      const float w = lane < n && !(ml.x == -INFINITY && ml.y == 0.f) ? fast_exp2(ml.x - top) : 0.f;
+      float sum = lane < n ? ml.y * w : 0.f;
+      #pragma unroll
+      for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+      l = l * keep + sum;
+      o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
+      m = top;
+      const int from = slot;
+      if (!last) load(first + 32);
+      #pragma unroll 4
+      for (int i = warp & (share - 1); i < n; i += share) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+        const int si = __shfl_sync(0xffffffffu, from, i);
+        const float4* src = reinterpret_cast<const float4*>(p.piece_o + ((long long)si * p.piece_rows + row) * kLatent);
+        const float4 v = src[at];
+        o.x += v.x * wi;
+        o.y += v.y * wi;
+        o.z += v.z * wi;
+        o.w += v.w * wi;
+      }
+    }
+    if (share > 1) {
+      part[warp][lane] = o;
+      __syncthreads();
+      if ((warp & (share - 1)) != 0) return;
+      for (int i = 1; i < share; ++i) {
+        const float4 v = part[warp + i][lane];
+        o = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
+      }
+    }
+    if (have) {
+      // (the item's columns are rows of out, in order)
+      const long long out_row = (long long)rec.y * p.num_q_heads + (cta % p.head_groups) * p.group_heads + row;
+      const float inv = 1.f / l;
+      uint2 v;
+      v.x = pack_bf16(o.x * inv, o.y * inv);
+      v.y = pack_bf16(o.z * inv, o.w * inv);
+      reinterpret_cast<uint2*>(p.out + out_row * kLatent)[at] = v;
+    }
+    if (share > 1) return;
   }
 }
 
@@ -1168,8 +1284,9 @@ cudaError_t launch_latent_decode(const LatentDecodeLaunch& L, cudaStream_t strea
   cudaError_t e = L.p.head_groups == 2 ? launch_decode<true>(L, stream) : launch_decode<false>(L, stream);
   if (e == cudaSuccess && L.p.merge) {
     cudaLaunchConfig_t cfg = {};
-    const int split = rows <= 16 ? 4 : 1;
-    cfg.gridDim = dim3(L.grid, (rows * split + kMergeWarps - 1) / kMergeWarps);
+    // An item has at least one token: few have eight CTAs and more each.
+    const bool few = 8ll * L.p.num_q_tokens * L.p.head_groups <= L.grid;
+    cfg.gridDim = few ? dim3(kFewBlocks * L.grid) : dim3(L.grid, (rows + kMergeWarps - 1) / kMergeWarps);
     cfg.blockDim = dim3(32 * kMergeWarps);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -1177,8 +1294,8 @@ cudaError_t launch_latent_decode(const LatentDecodeLaunch& L, cudaStream_t strea
     attr[0].val.programmaticStreamSerializationAllowed = L.p.pdl ? 1 : 0;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = split == 4 ? cudaLaunchKernelEx(&cfg, latent_merge_kernel<4>, L.p, L.grid)
-                   : cudaLaunchKernelEx(&cfg, latent_merge_kernel<1>, L.p, L.grid);
+    e = few ? cudaLaunchKernelEx(&cfg, latent_merge_few_kernel, L.p, L.grid)
+            : cudaLaunchKernelEx(&cfg, latent_merge_kernel, L.p, L.grid);
   }
   if (e != cudaSuccess) return e;
   return cudaGetLastError();

@@ -437,6 +437,16 @@ def test_expand_special_values_stay_in_their_rows():
 
 
 # ------------------------------------------------------------ padding, errors, order of calls
+@pytest.mark.parametrize("heads", [1, 16, 24, 64, 100, 128])
+@pytest.mark.parametrize("lens,qs", [([9000], [1]), ([20000, 513], [1, 1]), ([6000, 7, 0, 5000], [2, 1, 0, 1]),
+                                     ([3000] * 9, [1] * 9), ([2500] * 19, [1] * 19), ([2500] * 20, [1] * 20),
+                                     ([40000], [17]), ([12000], [20])])
+def test_absorbed_joins(heads, lens, qs):
+    """Few long items in many pieces, on both sides of the choice of the joining kernel."""
+    c = lat_case(lens, qs, heads, seed=heads)
+    lat_check(c, lat_run(c))
+
+
 def test_padded_steps_leave_other_rows():
     c = lat_case([40, 0, 300, 0], [1, 0, 3, 0], 16, pad=6)
     out = torch.full((10, 16, 512), 7.0, dtype=BF, device="cuda")

@@ -308,9 +308,10 @@ int check_latent_dims(const pkv_dims* d, bool attention) {
   // (tensor-map rows are addressed with 32-bit coordinates)
   if ((long long)d->num_blocks * pkv::kBlockSize > 0x7fffffffll)
     return fail(PKV_ERR_UNSUPPORTED, "pool beyond 2^31 - 1 rows");
-  if (d->num_q_heads < 0 || d->num_q_heads > (attention ? pkv::kMaxLatentHeads : kMaxRopeHeads) ||
-      (attention && d->num_q_heads == 0))
-    return fail(PKV_ERR_UNSUPPORTED, "num_q_heads %d unsupported", d->num_q_heads);
+  if (d->num_q_heads < (attention ? 1 : 0)) return fail(PKV_ERR_INVALID, "num_q_heads is %d", d->num_q_heads);
+  const int most = attention ? pkv::kMaxLatentHeads : kMaxRopeHeads;
+  if (d->num_q_heads > most)
+    return fail(PKV_ERR_UNSUPPORTED, "num_q_heads %d unsupported (up to %d)", d->num_q_heads, most);
   return PKV_OK;
 }
 

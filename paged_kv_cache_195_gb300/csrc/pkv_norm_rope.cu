@@ -9,8 +9,9 @@
 // once, in fp32.  Everything is fp32 from the load to the one rounding to bf16
 // at the store.
 //
-// Bound: HBM for chunks, latency for decodes (slot and position, then the
-// table's row, then the store).  Sixteen lanes hold a 128-dim head, eight lanes
+// Bound: HBM for chunks (8 of 512 tokens: 32 + 8 heads of 128 dims 22.0 us, 4.7 TB/s;
+// a latent and 128 heads' 64 dims 26.8 us, 5.4 TB/s), latency for decodes (64 tokens:
+// 1.7 and 2.0 us; slot and position, then the table's row, then the store).  Sixteen lanes hold a 128-dim head, eight lanes
 // the 64 rotated dims of a latent's head, each lane two runs of four dims that
 // make four whole pairs -- dims i .. i + 3 and i + rot/2 .. of a half-split
 // rotation -- so that a rotation needs no shuffles and a lane keeps four cos and
@@ -21,7 +22,11 @@
 namespace pkv {
 namespace {
 
-constexpr int kRopeThreads = 256;
+// Small blocks: a token's chain (position, cos and sin, stores) leaves no more of an SM
+// idle than its own (256 threads: 8 chunks of 512, 32 + 8 heads 24.1 us for 22.0, 128
+// latent heads 29.7 for 26.8; 64 threads: 21.7, but 256 decodes 3.4 us for 2.9).
+constexpr int kRopeThreads = 128;
+constexpr int kLatentThreads = 128;
 
 // Eight bf16 of a lane, as two runs of four.
 struct Raw {
@@ -74,18 +79,19 @@ __device__ __forceinline__ float lane_sum(float v) {
   return v;
 }
 
-// x to x / sqrt(mean of squares + eps) over the N float2 of each of WIDTH lanes.
+// x to x / sqrt(mean of squares + eps) over the N float2 of each of WIDTH lanes;
+// where `on` is not set (the same for the WIDTH lanes), x stays.
 // rsqrt is off by 2^-22, and the result is rounded to bf16's 2^-8.  Where the
 // squares of finite elements leave fp32's range, they are summed again, scaled
 // down: x * 2^-70 has squares below 2^116, and eps no weight beside them.
 template <int N, int WIDTH>
-__device__ __forceinline__ void norm(float2 (&x)[N], float eps) {
+__device__ __forceinline__ void norm(float2 (&x)[N], float eps, bool on) {
   constexpr float kMean = 1.f / (2 * N * WIDTH);
   float2 s2 = make_float2(0.f, 0.f);
   #pragma unroll
   for (int i = 0; i < N; ++i) s2 = ffma2(x[i], x[i], s2);
   float s = lane_sum<WIDTH>(s2.x + s2.y);
-  const bool over = s == INFINITY;
+  const bool over = on && s == INFINITY;
   if (__any_sync(0xffffffffu, over)) {
     const float k = over ? 0x1p-70f : 1.f;
     s2 = make_float2(0.f, 0.f);
@@ -97,7 +103,7 @@ __device__ __forceinline__ void norm(float2 (&x)[N], float eps) {
     s = lane_sum<WIDTH>(s2.x + s2.y);
     if (over) eps = 0.f;
   }
-  const float r = rsqrtf(fmaf(s, kMean, eps));
+  const float r = on ? rsqrtf(fmaf(s, kMean, eps)) : 1.f;
   #pragma unroll
   for (int i = 0; i < N; ++i) x[i] = fmul2(x[i], make_float2(r, r));
 }
@@ -128,10 +134,14 @@ __device__ __forceinline__ void turn(float2 (&x)[4], const Turn& t, bool inter) 
     turn_pair(x[2].x, x[2].y, t.c.z, t.s.z);
     turn_pair(x[3].x, x[3].y, t.c.w, t.s.w);
   } else {
-    turn_pair(x[0].x, x[2].x, t.c.x, t.s.x);
-    turn_pair(x[0].y, x[2].y, t.c.y, t.s.y);
-    turn_pair(x[1].x, x[3].x, t.c.z, t.s.z);
-    turn_pair(x[1].y, x[3].y, t.c.w, t.s.w);
+    const float2 c[2] = {make_float2(t.c.x, t.c.y), make_float2(t.c.z, t.c.w)};
+    const float2 s[2] = {make_float2(t.s.x, t.s.y), make_float2(t.s.z, t.s.w)};
+    #pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 a = x[i], b = x[i + 2];
+      x[i] = ffma2(b, make_float2(-s[i].x, -s[i].y), fmul2(a, c[i]));
+      x[i + 2] = ffma2(a, s[i], fmul2(b, c[i]));
+    }
   }
 }
 
@@ -148,27 +158,28 @@ __device__ __forceinline__ bool token_ok(long long slot, long long pos, int num_
 
 // Block (t, y): vectors 16 U y .. of token t; its heads in the order q, k, v.
 template <int U>
-__global__ void __launch_bounds__(kRopeThreads, 5) norm_rope_append_kernel(const NormRopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 9) norm_rope_append_kernel(const NormRopeParams p) {
   grid_dependency_wait();  // inputs and pools may belong to the previous kernel
   allow_dependent_launch();
-  const int sub = threadIdx.x >> 4, l = threadIdx.x & 15;
-  const int hq = p.num_q_heads, hkv = p.num_kv_heads;
-  const int total = hq + 2 * hkv;
-  const int first = blockIdx.y * (U * kRopeThreads / 16) + sub;
+  constexpr int kVecs = kRopeThreads / 16;
+  const int l = threadIdx.x & 15;
+  const int hq = p.num_q_heads, hk = hq + p.num_kv_heads, total = hk + p.num_kv_heads;
+  const int first = blockIdx.y * (U * kVecs) + (threadIdx.x >> 4);
   const bool inter = p.interleaved != 0;
   const Place at = place(l, p.rot, inter);
   const int t = blockIdx.x;
   const long long slot = __ldg(p.slot_mapping + t), pos = __ldg(p.positions + t);
   Raw raw[U];
-  #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int vec = first + u * (kRopeThreads / 16);
-    raw[u] = Raw{make_uint2(0, 0), make_uint2(0, 0)};
-    if (vec < total) {
-      const __nv_bfloat16* src = vec < hq         ? p.q + t * p.q_stride + vec * kHeadDim
-                                 : vec < hq + hkv ? p.k + t * p.k_stride + (vec - hq) * kHeadDim
-                                                  : p.v + t * p.v_stride + (vec - hq - hkv) * kHeadDim;
-      raw[u] = load8(src, at);
+  {
+    // (each as if its heads were numbered from the token's first vector on)
+    const __nv_bfloat16* const q = p.q + t * p.q_stride;
+    const __nv_bfloat16* const k = p.k + t * p.k_stride - hq * kHeadDim;
+    const __nv_bfloat16* const v = p.v + t * p.v_stride - hk * kHeadDim;
+    #pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int vec = first + u * kVecs;
+      raw[u] = Raw{make_uint2(0, 0), make_uint2(0, 0)};
+      if (vec < total) raw[u] = load8((vec < hq ? q : vec < hk ? k : v) + vec * kHeadDim, at);
     }
   }
   Raw wq{make_uint2(0, 0), make_uint2(0, 0)}, wk = wq;
@@ -177,36 +188,34 @@ __global__ void __launch_bounds__(kRopeThreads, 5) norm_rope_append_kernel(const
   if (!token_ok(slot, pos, p.num_blocks, p.max_position, p.err)) return;
   Turn tr{};
   if (at.turned) tr = load_turn(p.cos_sin + pos * p.rot, p.rot, l);
-  const long long row = (slot / kBlockSize * hkv * kBlockSize + slot % kBlockSize) * kHeadDim;
+  constexpr int kBlockHead = kBlockSize * kHeadDim;
+  const long long row = (slot / kBlockSize * p.num_kv_heads * kBlockSize + slot % kBlockSize) * kHeadDim;
+  __nv_bfloat16* const q = p.q_out + t * p.out_stride;
+  __nv_bfloat16* const k = p.k_pool + row - hq * kBlockHead;
+  __nv_bfloat16* const v = p.v_pool + row - hk * kBlockHead;
+  const bool by_q = p.q_weight != nullptr, by_k = p.k_weight != nullptr;
   #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int vec = first + u * (kRopeThreads / 16);
-    const bool is_q = vec < hq, is_v = vec >= hq + hkv;
+    const int vec = first + u * kVecs;
+    const bool is_q = vec < hq, is_v = vec >= hk;
     // (a warp's two vectors, both values or past the end: nothing to compute)
     if (!__all_sync(0xffffffffu, is_v)) {
       float2 x[4];
       unpack8(raw[u], x);
-      const bool by_q = p.q_weight != nullptr, by_k = p.k_weight != nullptr;
       if (by_q || by_k) {
-        float2 y[4], w[4];
-        #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = x[i];
-        norm<4, 16>(y, p.eps);
-        unpack8(is_q ? wq : wk, w);
-        if (is_q ? by_q : by_k) {
+        const bool on = is_q ? by_q : by_k && !is_v;
+        norm<4, 16>(x, p.eps, on);
+        if (on) {
+          float2 w[4];
+          unpack8(is_q ? wq : wk, w);
           #pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = fmul2(y[i], w[i]);
+          for (int i = 0; i < 4; ++i) x[i] = fmul2(x[i], w[i]);
         }
       }
       if (at.turned) turn(x, tr, inter);
       if (!is_v) raw[u] = pack8(x);
     }
-    if (vec < total) {
-      __nv_bfloat16* dst = is_q ? p.q_out + t * p.out_stride + vec * kHeadDim
-                           : is_v ? p.v_pool + row + (vec - hq - hkv) * (kBlockSize * kHeadDim)
-                                  : p.k_pool + row + (vec - hq) * (kBlockSize * kHeadDim);
-      store8(dst, at, raw[u]);
-    }
+    if (vec < total) store8((is_q ? q : is_v ? v : k) + vec * (is_q ? kHeadDim : kBlockHead), at, raw[u]);
   }
 }
 
@@ -214,13 +223,13 @@ __global__ void __launch_bounds__(kRopeThreads, 5) norm_rope_append_kernel(const
 // latent as 16 elements a lane; the rotated key on eight lanes); all warps turn
 // the queries' vectors, eight lanes each, the first vectors by the last warps.
 template <int U>
-__global__ void __launch_bounds__(kRopeThreads, 4) append_latent_kernel(const AppendLatentParams p) {
+__global__ void __launch_bounds__(kLatentThreads, 8) append_latent_kernel(const AppendLatentParams p) {
   grid_dependency_wait();  // inputs and pool may belong to the previous kernel
   allow_dependent_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int l = lane & 7;
-  constexpr int kVecs = kRopeThreads / 8;
-  const int first = blockIdx.y * (U * kVecs) + (kRopeThreads / 32 - 1 - warp) * 4 + (lane >> 3);
+  constexpr int kVecs = kLatentThreads / 8;
+  const int first = blockIdx.y * (U * kVecs) + (kLatentThreads / 32 - 1 - warp) * 4 + (lane >> 3);
   const bool inter = p.interleaved != 0;
   const Place at = place(l, kRopeDim, inter);
   const int t = blockIdx.x;
@@ -254,7 +263,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) append_latent_kernel(const Ap
         x[4 * h + 2] = bf16x2_to_float2(lat[h].z);
         x[4 * h + 3] = bf16x2_to_float2(lat[h].w);
       }
-      norm<8, 32>(x, p.eps);
+      norm<8, 32>(x, p.eps, true);
       #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint4 w = __ldg(wp + lane + 32 * h);
@@ -284,10 +293,10 @@ __global__ void __launch_bounds__(kRopeThreads, 4) append_latent_kernel(const Ap
 }
 
 template <class P>
-cudaError_t launch(void (*kernel)(P), const P& p, dim3 grid, cudaStream_t stream) {
+cudaError_t launch(void (*kernel)(P), const P& p, dim3 grid, int threads, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kRopeThreads);
+  cfg.blockDim = dim3(threads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -303,7 +312,7 @@ cudaError_t launch(void (*kernel)(P), const P& p, dim3 grid, cudaStream_t stream
 // the blocks are few (latency), up to four, as evenly as it goes, when they would
 // fill the GPU several times over (loads in flight, cos and sin used again).
 int vectors(long long tokens, int passes, int sm_count) {
-  if (tokens * passes <= 8ll * sm_count) return 1;
+  if (tokens * passes <= 16ll * sm_count) return 1;
   const int blocks = (passes + 3) / 4;
   return (passes + blocks - 1) / blocks;
 }
@@ -316,23 +325,23 @@ cudaError_t launch_norm_rope_append(const NormRopeParams& p, int sm_count, cudaS
   const int u = vectors(p.num_tokens, passes, sm_count);
   const dim3 grid(p.num_tokens, (passes + u - 1) / u);
   switch (u) {
-    case 1: return launch(norm_rope_append_kernel<1>, p, grid, stream);
-    case 2: return launch(norm_rope_append_kernel<2>, p, grid, stream);
-    case 3: return launch(norm_rope_append_kernel<3>, p, grid, stream);
-    default: return launch(norm_rope_append_kernel<4>, p, grid, stream);
+    case 1: return launch(norm_rope_append_kernel<1>, p, grid, kRopeThreads, stream);
+    case 2: return launch(norm_rope_append_kernel<2>, p, grid, kRopeThreads, stream);
+    case 3: return launch(norm_rope_append_kernel<3>, p, grid, kRopeThreads, stream);
+    default: return launch(norm_rope_append_kernel<4>, p, grid, kRopeThreads, stream);
   }
 }
 
 cudaError_t launch_append_latent(const AppendLatentParams& p, int sm_count, cudaStream_t stream) {
-  constexpr int kVecs = kRopeThreads / 8;
+  constexpr int kVecs = kLatentThreads / 8;
   const int passes = p.num_q_heads > 0 ? (p.num_q_heads + kVecs - 1) / kVecs : 1;
   const int u = vectors(p.num_tokens, passes, sm_count);
   const dim3 grid(p.num_tokens, (passes + u - 1) / u);
   switch (u) {
-    case 1: return launch(append_latent_kernel<1>, p, grid, stream);
-    case 2: return launch(append_latent_kernel<2>, p, grid, stream);
-    case 3: return launch(append_latent_kernel<3>, p, grid, stream);
-    default: return launch(append_latent_kernel<4>, p, grid, stream);
+    case 1: return launch(append_latent_kernel<1>, p, grid, kLatentThreads, stream);
+    case 2: return launch(append_latent_kernel<2>, p, grid, kLatentThreads, stream);
+    case 3: return launch(append_latent_kernel<3>, p, grid, kLatentThreads, stream);
+    default: return launch(append_latent_kernel<4>, p, grid, kLatentThreads, stream);
   }
 }
 

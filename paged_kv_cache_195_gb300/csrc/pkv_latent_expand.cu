@@ -4,7 +4,8 @@
 //   kv[j, h, :] = W_h c_j,   W_h [256 x 512], c_j the latent of position j
 //
 // a matrix product whose left operand is gathered through the block table.
-// Bound: tensor core (512 flops a byte written, the largest stream).
+// Bound: tensor core (512 flops a byte written, the largest stream).  Measured: 8
+// contexts of 512 to 4608 keys, 32 heads 83 us (1510 TFLOP/s); 701 keys, 16 heads 8.4.
 //
 // Tiling.  Two CTAs work as one (cta_group::2): a unit is (256 keys of one request,
 // head), D[256 x 256] = C[256 x 512] W_h^T, each CTA holding 128 of the keys, 128
@@ -14,14 +15,15 @@
 // The units form one sequence, heads fastest, cut in equal ranges, one a pair: a
 // tile's latents (128 KB a CTA, eight 64-dim chunks gathered by 2-D TMA copies of
 // pool blocks) stay in shared memory for all of its heads, and the weights stream
-// by from L2, a 64-dim chunk at a time.  D has two TMEM buffers of 256 columns, so
+// by from L2, a 64-dim chunk at a time, five in flight (four: 92 us for 83).  D has two TMEM buffers of 256 columns, so
 // that a unit's rows are rounded and stored while the next is multiplied.  Keys
 // behind the request's end are rows of D that nobody stores.
 //
-// Roles (192 threads): warps 0-3 take D's rows, one a thread, round them once,
+// Roles (224 threads): warps 0-3 take D's rows, one a thread, round them once,
 // and turn them through shared memory into stores of whole 128-byte lines (a bulk
-// copy a row took longer to issue than the products); warp 4 copies, warp 5 of the pair's first CTA
-// issues the MMAs of both.  Copies of both CTAs count on the first one's barriers,
+// copy a row took longer to issue than the products); warp 4 copies weights, warp 6
+// latents, each as its own room comes free; warp 5 of the pair's first CTA issues the
+// MMAs of both.  Copies of both CTAs count on the first one's barriers,
 // commits arrive on both's.
 #include <climits>
 
@@ -34,14 +36,15 @@ namespace {
 constexpr int kEpiWarps = 4;
 constexpr int kWarpLoad = kEpiWarps;
 constexpr int kWarpMma = kEpiWarps + 1;
-constexpr int kThreads = 32 * (kEpiWarps + 2);
+constexpr int kWarpKeys = kEpiWarps + 2;
+constexpr int kThreads = 32 * (kEpiWarps + 3);
 constexpr int kKeys = 128;                 // keys of a CTA: half of the MMA's M
 constexpr int kPairKeys = 2 * kKeys;
 constexpr int kOut = kNope + kValDim;      // outputs of a unit: MMA N
 constexpr int kHalf = 128;                 // weight rows of a CTA
 constexpr int kChunks = kLatent / 64;
 constexpr int kChunkBytes = 128 * 128;     // 128 rows of 64 bf16
-constexpr int kStages = 4;                 // weight pieces in flight
+constexpr int kStages = 5;                 // weight pieces in flight
 constexpr int kRowCols = 64;               // columns that a row stores at a time
 constexpr int kRowBytes = kRowCols * 2 + 16;  // (16 bytes apart from a bank-aligned stride)
 
@@ -59,7 +62,8 @@ struct __align__(1024) Smem {
   long long range_lo, range_hi, start_base;
   int start_req;
 };
-static_assert(sizeof(Smem) + 1024 <= 227 * 1024, "latent expand shared memory");
+// (no room to align it in: a block without static shared memory has it on a KiB)
+static_assert(sizeof(Smem) <= 227 * 1024, "latent expand shared memory");
 
 __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
 
@@ -166,8 +170,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     latent_expand_kernel(const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap wmap, const LatentExpandParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  Smem& sm = *reinterpret_cast<Smem*>(smem_raw + (((raw + 1023u) & ~1023u) - raw));
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+  if ((smem_u32(smem_raw) & 1023u) != 0) {
+    if (threadIdx.x == 0) record_error(p.err, kErrCapacity);
+    return;
+  }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blockIdx.x & 1;  // in the pair
   WaitCtl* ctl = &sm.wait;
@@ -209,12 +216,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   Walk w;
   w.start(sm);
 
-  if (warp == kWarpLoad) {
-    // =========================== copies ===================================
+  if (warp == kWarpKeys) {
+    // =========================== latents ==================================
     const bool leader = elect_one();
     const int oob_row = p.num_blocks * kBlockSize;
     int n_tile = 0, chunks = 0;  // runs so far; chunks of run n_tile
-    int n_b = 0, st = 0, phase = 1;  // weight pieces; their stage and the parity it waits for
     bool ok = true;
     while (ok && w.next(p, sm)) {
       // Lane b < 8 holds the row of block b; blocks past the end are read at a row
@@ -226,20 +232,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         if ((unsigned)id < (unsigned)p.num_blocks) row = id * kBlockSize;
         else record_error(p.err, kErrBounds);
       }
-      chunks = 0;
+      // (one thread issues all copies, from uniform registers)
+      int rows[kKeys / kBlockSize];
+      #pragma unroll
+      for (int b = 0; b < kKeys / kBlockSize; ++b) rows[b] = uniform(__shfl_sync(0xffffffffu, row, b));
       #pragma unroll 1
-      for (int h = w.h0; h < w.h1; ++h) {
+      for (chunks = 0; chunks < kChunks; ++chunks) {
+        if (n_tile > 0) ok = all_of(wait_for(&sm.a_empty[chunks], (n_tile - 1) & 1, p.err, ctl));
+        if (!ok) break;
+        if (leader) {
+          if (rank == 0) mbar_arrive_expect_tx(&sm.a_full[chunks], 2 * kChunkBytes);
+          const uint32_t bar = first_cta(&sm.a_full[chunks]);
+          #pragma unroll
+          for (int b = 0; b < kKeys / kBlockSize; ++b)
+            tma_load_2d_pair(sm.a[chunks] + b * 2048, &kmap, chunks * 64, rows[b], bar);
+        }
+        __syncwarp();
+      }
+      if (ok) ++n_tile;
+    }
+    if (!ok && rank == 0) {
+      // Aborted: the copies in flight must land before the pair ends (the barrier
+      // at the end keeps the other CTA's memory until then).
+      for (int c = 0; c < kChunks; ++c) {
+        const int n = n_tile + (c < chunks ? 1 : 0);
+        if (n > 0) drain(&sm.a_full[c], (n - 1) & 1, p.err, ctl);
+      }
+    } else if (!ok) {
+      settle();
+    }
+  } else if (warp == kWarpLoad) {
+    // =========================== weights ==================================
+    const bool leader = elect_one();
+    int n_b = 0, st = 0, phase = 1;  // pieces so far; their stage and the parity it waits for
+    bool ok = true;
+    while (ok && w.next(p, sm)) {
+      #pragma unroll 1
+      for (int h = w.h0; h < w.h1 && ok; ++h) {
         #pragma unroll 1
         for (int c = 0; c < kChunks; ++c) {
-          if (h == w.h0) {
-            if (n_tile > 0) ok = all_of(wait_for(&sm.a_empty[c], (n_tile - 1) & 1, p.err, ctl));
-            if (!ok) break;
-            if (leader && rank == 0) mbar_arrive_expect_tx(&sm.a_full[c], 2 * kChunkBytes);
-            __syncwarp();
-            if (lane < 8) tma_load_2d_pair(sm.a[c] + lane * 2048, &kmap, c * 64, row, first_cta(&sm.a_full[c]));
-            __syncwarp();
-            ++chunks;
-          }
           ok = all_of(wait_for(&sm.b_empty[st], phase, p.err, ctl));
           if (!ok) break;
           if (leader) {
@@ -250,19 +281,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++n_b;
           if (++st == kStages) st = 0, phase ^= 1;
         }
-        if (!ok) break;
       }
-      if (ok) ++n_tile, chunks = 0;
     }
     if (!ok && rank == 0) {
-      // Aborted: the copies in flight must land before the pair ends (the barrier
-      // at the end keeps the other CTA's memory until then).
       for (int i = max(0, n_b - kStages); i < n_b; ++i)
         drain(&sm.b_full[i % kStages], (i / kStages) & 1, p.err, ctl);
-      for (int c = 0; c < kChunks; ++c) {
-        const int n = n_tile + (c < chunks ? 1 : 0);
-        if (n > 0) drain(&sm.a_full[c], (n - 1) & 1, p.err, ctl);
-      }
     } else if (!ok) {
       settle();
     }
@@ -380,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace
 
 cudaError_t launch_latent_expand(const LatentExpandLaunch& L, cudaStream_t stream) {
-  const size_t smem = sizeof(Smem) + 1024;
+  const size_t smem = sizeof(Smem);
   static unsigned long long configured = 0;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

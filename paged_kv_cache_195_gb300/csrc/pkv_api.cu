@@ -1356,6 +1356,7 @@ int pkv_attention_expanded(const void* q, const void* kv, const void* k_rope, co
   p.piece_o = p.piece_ml + 4 * (size_t)st->sm_count * 128;
   p.sched = reinterpret_cast<unsigned long long*>(ws);
   p.err = st->err;
+  p.wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
   p.num_reqs = dims->num_reqs;
   p.num_q_tokens = dims->num_q_tokens;
   p.num_rows = num_rows;

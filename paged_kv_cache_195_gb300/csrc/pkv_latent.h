@@ -177,8 +177,11 @@ struct LatentPrefillParams {
   int* num_pieces;
   float* piece_ml;             // [max_pieces][128][2]
   float* piece_o;              // [max_pieces][128][128]
-  unsigned long long* sched;   // [0] next piece, [1] CTAs done; zero between launches
+  // [0] pieces handed out beyond each CTA's (pair's) first, [1] CTAs done; zero
+  // between launches.
+  unsigned long long* sched;
   int* err;
+  int wide;                    // out is aligned to 32 bytes
   int num_reqs, num_q_tokens, num_rows, num_heads;
   int max_pieces;              // 0: items are not split
   float scale_log2;

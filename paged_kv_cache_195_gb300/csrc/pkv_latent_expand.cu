@@ -15,8 +15,8 @@
 // The units form one sequence, heads fastest, cut in equal ranges, one a pair: a
 // tile's latents (128 KB a CTA, eight 64-dim chunks gathered by 2-D TMA copies of
 // pool blocks) stay in shared memory for all of its heads, and the weights stream
-// by from L2, a 64-dim chunk at a time, five in flight (four: 92 us for 83).  D has two TMEM buffers of 256 columns, so
-// that a unit's rows are rounded and stored while the next is multiplied.  Keys
+// by from L2, a 64-dim chunk at a time, five in flight (four: 92 us for 83).  D has two
+// TMEM buffers of 256 columns, so that a unit's rows are rounded and stored while the next is multiplied.  Keys
 // behind the request's end are rows of D that nobody stores.
 //
 // Roles (224 threads): warps 0-3 take D's rows, one a thread, round them once,

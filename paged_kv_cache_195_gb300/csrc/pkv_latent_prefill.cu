@@ -6,16 +6,17 @@
 // with keys and values of each head side by side in kv [rows, H, 256] and the
 // rotated keys r, shared by the heads, in a tensor of their own: a key tile takes
 // its three 64-dim chunks from both, and no head's copy of r is ever made.
-// Bound: tensor core (640 flops a (row, key, head)).
+// Bound: tensor core (640 flops a (row, key, head)).  Measured: 8 chunks of 512 on up
+// to 4608 keys, 32 heads 113 us (1186 TFLOP/s; a tile's softmax, 0.85 us a pair's 256
+// rows, is longer than its products' 0.67); three odd chunks, 16 heads 11 us.
 //
 // Tiling.  A work item is (request, head, 128 query tokens); a key tile is 128
 // keys.  S = Q K^T (12 MMAs of K = 16) and P (bf16) have two TMEM buffers each, so
 // that scores run two tiles ahead of the products (over its S, P held that back for
 // the product: 1.1 us a tile), and O += P V (8 MMAs, A from TMEM) accumulates in 128
-// columns.  Four
-// threads a row run the softmax, 32 keys each; the row maximum moves, and O is
-// rescaled, only when a score exceeds it by 2^8, on a vote of the four warps that
-// hold the same rows.  Keys and values have rings of their own, of 64-dim chunks,
+// columns.  Four threads a row run the softmax, 32 keys each; the row maximum moves,
+// and O is rescaled, only when a score exceeds it by 2^8, on a vote of the four warps
+// that hold the same rows.  Keys and values have rings of their own, of 64-dim chunks,
 // each of which goes back as soon as its MMAs are done.
 // Steps of long chunks run in pairs of CTAs (cta_group::2): the pair takes two query
 // tiles of one head, 256 MMA rows, and each CTA holds half of the keys and half of
@@ -24,14 +25,14 @@
 // MMAs' own reads is more than shared memory and the copies give (1.04-1.09 us a
 // tile, with the keys multicast or not).
 //
-// Order.  Items come from a queue, longest requests first, a head's query tiles
-// one after the other (the CTAs that run them at one time read the same keys:
-// L2), later tiles first, as they see more keys.  With too few items for the
+// Order.  A CTA's first item is its own by its number, the others come from a queue,
+// longest requests first, a head's query tiles one after the other (the CTAs that run
+// them at one time read the same keys: L2), later tiles first, as they see more keys.  With too few items for the
 // GPU each is cut over its keys into pieces, numbered like items, whose
 // unnormalised states a second kernel joins.
 //
 // A value that only some rows of an item see must not reach the others, whatever
-// it holds (0 * NaN): rows of V with a NaN or infinity among the item's own
+// it holds (0 * NaN): the NaN and infinities among the values of the item's own
 // tokens are taken out, by the warp that copies them, and added to the rows that
 // see them at the end.
 #include <climits>
@@ -273,6 +274,15 @@ struct Finder {
   }
 };
 
+// Thirty-two bytes, a whole sector.  (A thread has a row: each store of a warp goes to
+// 32 lines, and in sixteens there are twice as many: 8 chunks of 512, 32 heads 113.1 us
+// for 117.0, 16 of 256, 40 heads 94.7 for 104.3.)
+__device__ __forceinline__ void store32(void* p, const uint32_t (&r)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // O (32 columns at TMEM address tO) times alpha.
 static __device__ __noinline__ void rescale_o32(uint32_t tO, float alpha) {
   float o[32];
@@ -415,9 +425,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (!p.early_plan) grid_dependency_wait();
   int first_pieces = 0;
+  Finder<GROUP> f;  // (of warp kWarpK)
   if (warp == kWarpK) {
     long long pieces;
     const int split = plan_split<GROUP>(p, gridDim.x, &pieces);
+    f.start(p, split);
     if (lane == 0) {
       if (blockIdx.x == 0) first_pieces = split != INT_MAX ? (int)pieces : 0;
       sm.split = split;
@@ -509,20 +521,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       // ---- items, queries and keys; a pair's on the first CTA's barriers
       int n_item = 0;
-      Finder<GROUP> f;
-      f.start(p, split);
       for (int n = 0; ok; ++n) {
-        // A pair's first CTA takes the number for both.
-        unsigned long long v = 0;
-        if (!PAIR || rank == 0) {
-          if (lane == 0) v = atomicAdd(p.sched, 1ull);
+        // The first piece is the CTA's own, by its number; the others come from the
+        // queue.  A pair's first CTA takes the number for both.
+        unsigned long long v = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+        const int at = (n - 1) % kItems;
+        if (n > 0 && (!PAIR || rank == 0)) {
+          if (lane == 0) v = active + atomicAdd(p.sched, 1ull);
           v = __shfl_sync(0xffffffffu, v, 0);
-          if (PAIR && lane == 0) send_second(&sm.next[n % kItems], &sm.next_full[n % kItems], v);
-        } else {
-          ok = wait_for(&sm.next_full[n % kItems], (n / kItems) & 1, p.err, ctl);
+          if (PAIR && lane == 0) send_second(&sm.next[at], &sm.next_full[at], v);
+        } else if (n > 0) {
+          ok = wait_for(&sm.next_full[at], ((n - 1) / kItems) & 1, p.err, ctl);
           if (!all_of(ok)) break;
           asm volatile("fence.acq_rel.cluster;" ::: "memory");
-          v = *(volatile unsigned long long*)&sm.next[n % kItems];
+          v = *(volatile unsigned long long*)&sm.next[at];
         }
         Item it;
         int of;
@@ -794,6 +806,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float o[32];
         tmem_ld32(tO, o);
         tc_wait_ld();
+        // (ahead of the stores, for which the arrival would wait)
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) PAIR ? arrive_at(first_cta(&sm.o_empty)) : mbar_arrive(&sm.o_empty);
         if (gone) {
           float x[32];  // (a copy, so that o itself stays in registers)
           #pragma unroll
@@ -807,22 +823,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<float2*>(p.piece_ml + ((long long)it.slot * kRows + row) * 2) = make_float2(m, lrow);
           float* dst = p.piece_o + ((long long)it.slot * kRows + row) * kValDim + part * kPartKeys;
           #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          for (int i = 0; i < 32; i += 8) {
+            uint32_t r[8];
+            #pragma unroll
+            for (int k = 0; k < 8; ++k) r[k] = __float_as_uint(o[i + k]);
+            store32(dst + i, r);
+          }
         } else if (valid && ok) {
           const float inv = reciprocal(lrow);
           __nv_bfloat16* dst =
               p.out + ((long long)(it.row0 + row) * p.num_heads + it.head) * kValDim + part * kPartKeys;
           #pragma unroll
-          for (int i = 0; i < 32; i += 8)
-            *reinterpret_cast<uint4*>(dst + i) =
-                make_uint4(pack_bf16(o[i] * inv, o[i + 1] * inv), pack_bf16(o[i + 2] * inv, o[i + 3] * inv),
-                           pack_bf16(o[i + 4] * inv, o[i + 5] * inv), pack_bf16(o[i + 6] * inv, o[i + 7] * inv));
+          for (int i = 0; i < 32; i += 16) {
+            uint32_t r[8];
+            #pragma unroll
+            for (int k = 0; k < 8; ++k) r[k] = pack_bf16(o[i + 2 * k] * inv, o[i + 2 * k + 1] * inv);
+            if (p.wide) {
+              store32(dst + i, r);
+            } else {
+              *reinterpret_cast<uint4*>(dst + i) = make_uint4(r[0], r[1], r[2], r[3]);
+              *reinterpret_cast<uint4*>(dst + i + 8) = make_uint4(r[4], r[5], r[6], r[7]);
+            }
+          }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) PAIR ? arrive_at(first_cta(&sm.o_empty)) : mbar_arrive(&sm.o_empty);
     }
   }
   // (an abort only shortens the loops: every warp gets here)

@@ -302,6 +302,33 @@ def test_requests_may_share_blocks():
     assert torch.equal(kv[:64], kv[64:128]) and np.array_equal(f64(kr), rope)
 
 
+def _offset(t):
+    """The same tensor 16 bytes behind a 32-byte boundary."""
+    b = torch.empty(t.numel() + 8, dtype=t.dtype, device=t.device)[8:].view(t.shape)
+    return b.copy_(t)
+
+
+def test_buffers_need_16_bytes_of_alignment_only():
+    for c in (exp_case([130, 40], [130, 7], 3), exp_case([2000], [50], 2), exp_case([600] * 8, [512] * 8, 10)):
+        want = exp_run(c)
+        for k in ("q", "kv", "kr"):
+            c[k] = _offset(c[k])
+        out = _offset(torch.zeros_like(want))
+        assert out.data_ptr() % 32 == 16
+        assert torch.equal(exp_run(c, out=out), want)
+    for c in (lat_case([3000, 20], [1, 3], 16), lat_case([700] * 4, [1] * 4, 128)):
+        want = lat_run(c)
+        c["q"], c["pool"] = _offset(c["q"]), _offset(torch.nan_to_num(c["pool"]))
+        assert torch.equal(lat_run(c, out=_offset(torch.zeros_like(want))), want)
+    c, w = lat_case([300], [1], 1), (torch.randn(3, 256, 512, device="cuda") / 20).to(BF)
+    outs = []
+    for f in (lambda t: t, _offset):
+        kv, kr = f(torch.zeros(300, 3, 256, dtype=BF, device="cuda")), f(torch.zeros(300, 64, dtype=BF, device="cuda"))
+        pkv.pkv_expand_latent(f(c["pool"]), f(w), dev(c["tab"], I32), dev(c["lens"], I32), dev([0, 300], I32), kv, kr)
+        outs.append((kv, kr))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
 def test_empty_calls():
     none = torch.empty(0, 16, 576, dtype=BF, device="cuda")
     pool = torch.zeros(3, 16, 576, dtype=BF, device="cuda")

@@ -742,7 +742,7 @@ def pkv_norm_rope_append(q, k, v, positions, cos_sin, slot_mapping, k_pool, v_po
     kp, ks = _heads(k, "k", dev, T, Hkv)
     vp, vs = _heads(v, "v", dev, T, Hkv)
     op, os_ = _heads(q_out, "q_out", dev, T, Hq)
-    if positions.shape[0] != T or slot_mapping.shape[0] != T:
+    if positions.numel() != T or slot_mapping.numel() != T:
         raise ValueError("positions and slot_mapping need one entry per token")
     nb, h, bs, D = pool = k_pool.shape
     if v_pool.shape != pool or h != Hkv:
@@ -766,11 +766,17 @@ def pkv_norm_rope_append(q, k, v, positions, cos_sin, slot_mapping, k_pool, v_po
 
 _LATENT_FIXED = _spec(("positions", _I64, 1), ("cos_sin", _F32, 2), ("slot_mapping", _I64, 1),
                       ("pool", _BF16, 3))
+_LATENT_NORMED = _spec(("positions", _I64, 1), ("cos_sin", _F32, 2), ("slot_mapping", _I64, 1),
+                       ("pool", _BF16, 3), ("weight", _BF16, 1))
 
 
-def _rope_part(t, name: str, dev: int, shape: tuple):
+def _rope_part(t, name: str, dev: int, shape):
     """(pointer, strides of tokens and heads) of a bf16 [tokens, heads, 64] tensor."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.get_device() != dev or t.shape != shape:
+    try:
+        good = t.dtype is _BF16 and t.get_device() == dev and t.shape == shape
+    except AttributeError:
+        good = False
+    if not good:
         raise ValueError(f"{name} must be a bf16 [tokens, heads, {ROPE}] tensor like q_rope on kv's device")
     a, b, c = t.stride()
     if c != 1:
@@ -789,7 +795,14 @@ def pkv_append_latent(kv, positions, cos_sin, slot_mapping, pool, weight=None, e
     meets the rotated keys (any strides between tokens and heads), is rotated
     too, into q_rope_out (default: in place).  A token with a negative slot is
     padding: nothing of it is written."""
-    dev, (pos, table, slots, pp) = _fast_need((positions, cos_sin, slot_mapping, pool), _LATENT_FIXED)
+    if weight is None:
+        dev, (pos, table, slots, pp) = _fast_need((positions, cos_sin, slot_mapping, pool), _LATENT_FIXED)
+        w = None
+    else:
+        dev, (pos, table, slots, pp, w) = _fast_need((positions, cos_sin, slot_mapping, pool, weight),
+                                                     _LATENT_NORMED)
+        if weight.numel() != LATENT:
+            raise ValueError(f"weight must have {LATENT} elements")
     try:
         T, width = kv.shape
         stride, one = kv.stride()
@@ -800,35 +813,31 @@ def pkv_append_latent(kv, positions, cos_sin, slot_mapping, pool, weight=None, e
         _rows(kv, "kv", dev, (LATENT + ROPE,))
     if T < 2:
         stride = LATENT + ROPE
-    if positions.shape[0] != T or slot_mapping.shape[0] != T:
+    if positions.numel() != T or slot_mapping.numel() != T:
         raise ValueError("positions and slot_mapping need one entry per token")
     n, rot = cos_sin.shape
     if rot != ROPE:
         raise ValueError(f"cos_sin must have {ROPE} columns")
-    w = None if weight is None else _weight(weight, "weight", LATENT, dev)
-    heads, q, out = 0, (None, 0, 0), (None, 0, 0)
+    heads, q, qa, qb, out, oa, ob = 0, None, 0, 0, None, 0, 0
     if q_rope is not None:
-        if not isinstance(q_rope, torch.Tensor) or q_rope.dim() != 3 or q_rope.shape[0] != T \
-                or q_rope.shape[2] != ROPE:
+        if not isinstance(q_rope, torch.Tensor) or q_rope.dim() != 3:
             raise ValueError(f"q_rope must be a [tokens, heads, {ROPE}] tensor")
         shape = q_rope.shape
-        heads = shape[1]
-        q = out = _rope_part(q_rope, "q_rope", dev, shape)
-        if q_rope_out is not None and q_rope_out is not q_rope:
-            out = _rope_part(q_rope_out, "q_rope_out", dev, shape)
-        if T and heads:
-            if 0 < out[1] < ROPE or 0 < out[2] < ROPE or (T > 1 and out[1] == 0) or (heads > 1 and out[2] == 0):
-                raise ValueError("q_rope_out's rows overlap")
-            # (one thread's rows may be another's: only ranges apart, or the same rows)
-            size = [2 * ((T - 1) * a + (heads - 1) * b + ROPE) for _, a, b in (q, out)]
-            if out != q and q[0] < out[0] + size[1] and out[0] < q[0] + size[0]:
-                raise ValueError("q_rope_out may be q_rope, but not overlap it otherwise")
+        tokens, heads, width = shape
+        if tokens != T or width != ROPE:
+            raise ValueError(f"q_rope must be a [tokens, heads, {ROPE}] tensor")
+        q, qa, qb = _rope_part(q_rope, "q_rope", dev, shape)
+        if q_rope_out is None or q_rope_out is q_rope:
+            out, oa, ob = q, qa, qb
+        else:
+            out, oa, ob = _rope_part(q_rope_out, "q_rope_out", dev, shape)
     elif q_rope_out is not None:
         raise ValueError("q_rope_out without q_rope")
     nb, bs, D = pool.shape
     dims = Dims(0, T, heads, 1, D, bs, nb, 0)
     _call((_lib or load_library()).pkv_append_latent, dev, kv.data_ptr(), stride, pos, table, n,
-          1 if interleaved else 0, w, eps, slots, pp, *q, *out, ctypes.byref(dims), _raw_stream(stream, dev))
+          1 if interleaved else 0, w, eps, slots, pp, q, qa, qb, out, oa, ob, ctypes.byref(dims),
+          _raw_stream(stream, dev))
 
 
 class LatentWorkspace:

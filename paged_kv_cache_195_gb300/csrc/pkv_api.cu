@@ -297,6 +297,29 @@ bool stride_ok(int64_t stride, int row, int tokens) {
   return stride >= 0 && stride % 8 == 0 && (stride >= row || tokens <= 1);
 }
 
+// Rows of 64 bf16 of every (token, head).
+struct Rows {
+  const void* base;
+  int64_t token, head;  // elements between tokens, and heads
+  static constexpr int kDims = pkv::kRopeDim;
+
+  __int128 last(int tokens, int heads) const {  // elements from the first row's start to the end
+    return (__int128)(tokens - 1) * token + (__int128)(heads - 1) * head + kDims;
+  }
+  // Heads side by side within tokens that lie apart, or the other way round.
+  bool apart(int tokens, int heads) const {
+    const bool h = heads == 1 || head >= kDims, t = tokens == 1 || token >= kDims;
+    return (h && (tokens == 1 || token >= last(1, heads))) || (t && (heads == 1 || head >= last(tokens, 1)));
+  }
+  bool same(const Rows& o, int tokens, int heads) const {
+    return base == o.base && (tokens == 1 || token == o.token) && (heads == 1 || head == o.head);
+  }
+  bool meets(const Rows& o, int tokens, int heads) const {
+    const __int128 a = (__int128)reinterpret_cast<uintptr_t>(base), b = (__int128)reinterpret_cast<uintptr_t>(o.base);
+    return a < b + 2 * o.last(tokens, heads) && b < a + 2 * last(tokens, heads);
+  }
+};
+
 int check_latent_dims(const pkv_dims* d, bool attention) {
   if (d == nullptr) return fail(PKV_ERR_INVALID, "dims is NULL");
   if (d->head_dim != pkv::kLatRow)
@@ -1166,6 +1189,14 @@ int pkv_append_latent(const void* kv, int64_t kv_stride, const int64_t* position
   if (turn && (q_stride % 8 || q_head_stride % 8 || q_out_stride % 8 || q_out_head_stride % 8 ||
                q_stride < 0 || q_head_stride < 0 || q_out_stride < 0 || q_out_head_stride < 0))
     return fail(PKV_ERR_INVALID, "query strides must be multiples of 8 elements");
+  if (turn) {
+    const Rows in{q_rope, q_stride, q_head_stride}, to{q_rope_out, q_out_stride, q_out_head_stride};
+    const int T = dims->num_q_tokens, H = dims->num_q_heads;
+    if (!to.apart(T, H)) return fail(PKV_ERR_INVALID, "q_rope_out's rows overlap");
+    // (one thread's rows may be another's: only ranges apart, or the same rows)
+    if (!in.same(to, T, H) && in.meets(to, T, H))
+      return fail(PKV_ERR_INVALID, "q_rope_out may be q_rope, but not overlap it otherwise");
+  }
   DeviceState* st = device_state();
   if (!st) return PKV_ERR_CUDA;
   pkv::AppendLatentParams p{};

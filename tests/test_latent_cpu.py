@@ -147,7 +147,12 @@ LATENT_DIMS = [(dict(head_dim=128), b.PKV_ERR_UNSUPPORTED), (dict(num_kv_heads=2
     *[({name: ODD}, b.PKV_ERR_INVALID) for name in ("kv", "cs", "pool", "w")],
     (dict(q=ODD, out=FAKE), b.PKV_ERR_INVALID), (dict(q=FAKE, out=ODD), b.PKV_ERR_INVALID),
     (dict(q=FAKE, out=None), b.PKV_ERR_INVALID), (dict(q=FAKE, out=FAKE, qs=1028), b.PKV_ERR_INVALID),
-    (dict(q=FAKE, out=FAKE, oh=-64), b.PKV_ERR_INVALID), (dict(stride=568), b.PKV_ERR_INVALID),
+    (dict(q=FAKE, out=FAKE, oh=-64), b.PKV_ERR_INVALID), (dict(q=FAKE, out=FAKE, oh=32), b.PKV_ERR_INVALID),
+    (dict(q=FAKE, out=FAKE, os_=64), b.PKV_ERR_INVALID), (dict(q=FAKE, out=FAKE, os_=0), b.PKV_ERR_INVALID),
+    (dict(q=FAKE, out=FAKE, os_=1016), b.PKV_ERR_INVALID), (dict(q=FAKE, out=FAKE, oh=0), b.PKV_ERR_INVALID),
+    (dict(q=FAKE, out=FAKE, qs=2048), b.PKV_ERR_INVALID), (dict(q=FAKE, out=FAKE + 128), b.PKV_ERR_INVALID),
+    (dict(q=FAKE + 4080, out=FAKE), b.PKV_ERR_INVALID), (dict(q=FAKE, out=FAKE, os_=1 << 62, qs=1 << 62, oh=72), b.PKV_ERR_INVALID),
+    (dict(stride=568), b.PKV_ERR_INVALID),
     (dict(stride=580), b.PKV_ERR_INVALID)])
 def test_append_latent_refuses(lib, kw, code):
     assert _append(lib, **kw) == code and lib.pkv_last_error()

@@ -9,14 +9,15 @@
 // once, in fp32.  Everything is fp32 from the load to the one rounding to bf16
 // at the store.
 //
-// Bound: HBM for chunks (8 of 512 tokens: 32 + 8 heads of 128 dims 22.0 us, 4.7 TB/s;
-// a latent and 128 heads' 64 dims 26.8 us, 5.4 TB/s), latency for decodes (64 tokens:
-// 1.7 and 2.0 us; slot and position, then the table's row, then the store).  Sixteen lanes hold a 128-dim head, eight lanes
-// the 64 rotated dims of a latent's head, each lane two runs of four dims that
-// make four whole pairs -- dims i .. i + 3 and i + rot/2 .. of a half-split
-// rotation -- so that a rotation needs no shuffles and a lane keeps four cos and
-// four sin over all the heads that it turns.  A thread issues the loads of up to
-// four heads before it uses the first.
+// Bound: HBM for chunks (8 of 512 tokens: 32 + 8 heads of 128 dims 22 us, 4.7 TB/s;
+// a latent and 128 heads' 64 dims 27 us, 5.4 TB/s), latency for decodes (64 tokens:
+// 1.7 and 2.0 us; slot and position, then the table's row, then the store).
+// Sixteen lanes hold a 128-dim head, eight lanes the 64 rotated dims of a latent's
+// head, each lane two runs of four dims that make four whole pairs -- dims i .. i + 3
+// and i + rot/2 .. of a half-split rotation -- so that a rotation needs no shuffles and
+// a lane keeps four cos and four sin over all the heads that it turns.  (Eight lanes
+// and sixteen dims each: 24 us for 22.)  A thread issues the loads of up to four heads
+// before it uses the first.
 #include "pkv_latent.h"
 
 namespace pkv {

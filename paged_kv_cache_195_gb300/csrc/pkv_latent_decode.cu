@@ -1285,7 +1285,7 @@ cudaError_t launch_latent_decode(const LatentDecodeLaunch& L, cudaStream_t strea
   if (e == cudaSuccess && L.p.merge) {
     cudaLaunchConfig_t cfg = {};
     // An item has at least one token: few have eight CTAs and more each.
-    const bool few = 8ll * L.p.num_q_tokens * L.p.head_groups <= L.grid;
+    const bool few = 8ll * L.p.num_q_tokens * L.p.head_groups <= L.grid && L.grid <= 32 * kCtaGroups;
     cfg.gridDim = few ? dim3(kFewBlocks * L.grid) : dim3(L.grid, (rows + kMergeWarps - 1) / kMergeWarps);
     cfg.blockDim = dim3(32 * kMergeWarps);
     cfg.stream = stream;

@@ -302,6 +302,79 @@ def test_requests_may_share_blocks():
     assert torch.equal(kv[:64], kv[64:128]) and np.array_equal(f64(kr), rope)
 
 
+@pytest.mark.parametrize("what", ["nan", "inf", "-inf"])
+def test_queries_that_are_not_finite_spoil_their_rows_only(what):
+    for c, run, check in ((lat_case([200, 3000], [3, 1], 16), lat_run, lat_check), (lat_case([900] * 3, [1] * 3, 128), lat_run, lat_check),
+                          (exp_case([130, 300], [130, 70], 3), exp_run, exp_check), (exp_case([2000], [50], 2), exp_run, exp_check),
+                          (exp_case([600] * 8, [512] * 8, 10), exp_run, exp_check)):
+        good = run(c).clone()
+        T, H = c["q"].shape[:2]
+        for t, h in ((0, 0), (T // 2, H // 2), (T - 1, H - 1)):
+            c["q"][t, h, 3] = float(what)
+        out = run(c)
+        rows = torch.ones(T, H, dtype=torch.bool, device="cuda")
+        for t, h in ((0, 0), (T // 2, H // 2), (T - 1, H - 1)):
+            rows[t, h] = False
+        assert torch.equal(out[rows], good[rows])
+        check(c, out)
+
+
+def test_requests_of_a_step_mostly_idle():
+    """Far more requests than rows, most without query tokens, some without keys."""
+    rng = np.random.default_rng(4)
+    lens = rng.integers(0, 200, 700).tolist()
+    qs = [0] * 700
+    for r, m in ((3, 1), (350, 5), (699, 2)):
+        lens[r], qs[r] = 150 + r, m
+    c = lat_case(lens, qs, 16)
+    lat_check(c, lat_run(c))
+    e = exp_case(lens, qs, 2)
+    exp_check(e, exp_run(e))
+
+
+def test_pairs_ignore_what_others_hold():
+    """Whole pairs of query tiles over keys between rows of NaN, requests of odd lengths."""
+    lens, qs = [333, 700, 129, 512], [333, 600, 129, 512]
+    c = exp_case(lens, qs, 26)
+    assert sum(qs) >= 192 * 4
+    assert sum(qs) * 26 >= 256 * torch.cuda.get_device_properties(0).multi_processor_count
+    want = exp_run(c).clone()
+    exp_check(c, want)
+    a, b = 333, 333 + 700  # the second request's rows
+    c["kv"][a:b], c["kr"][a:b] = float("nan"), float("nan")
+    pad = torch.full((300, 26, 256), float("nan"), dtype=BF, device="cuda")
+    c["kv"], c["kr"] = torch.cat([c["kv"], pad]), torch.cat([c["kr"], pad[:, 0, :64].contiguous()])
+    out = exp_run(c)
+    assert torch.equal(out[:333], want[:333]) and torch.equal(out[933:], want[933:])
+    assert torch.isnan(out[333:933]).all()
+
+
+def test_workspaces_that_are_too_small_are_refused():
+    c, e = _buffers(lat_case([40], [1], 16)), _buffers(exp_case([40], [3], 2))
+    ws = pkv.LatentWorkspace()
+    ws.nbytes -= 1
+    for x in (c, e):
+        with pytest.raises(pkv.PagedKVError) as err:
+            _call(x, workspace=ws)
+        assert err.value.code == pkv._binding.PKV_ERR_WORKSPACE
+        assert (x["out"] == 7).all()
+
+
+def test_capture_without_a_workspace():
+    """The call's own workspace is captured with it."""
+    for c, check in ((_buffers(lat_case([3000, 20], [1, 1], 16)), lat_check), (_buffers(exp_case([2000], [50], 2)), exp_check)):
+        _call(c)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            _call(c)
+            _call(c)
+        for _ in range(3):
+            c["out"].fill_(7.0)
+            g.replay()
+            check(c, c["out"])
+
+
 def _offset(t):
     """The same tensor 16 bytes behind a 32-byte boundary."""
     b = torch.empty(t.numel() + 8, dtype=t.dtype, device=t.device)[8:].view(t.shape)

@@ -384,7 +384,8 @@ int pkv_attention_fp8_block(const void *q, const void *k_pool, const void *v_poo
  * first half of a row, the sin in the second.  The leading rotary_dim dims (16,
  * 32, .. 128) are rotated; pair i is dims i and i + rotary_dim / 2, or with
  * interleaved != 0 dims 2i and 2i + 1.  Computed in fp32 and rounded once.
- * Queries go to q_out (token stride q_out_stride; may be q with its stride),
+ * Queries go to q_out (token stride q_out_stride; may be q with its stride, and
+ * must not share elements with q, k or v otherwise),
  * keys and values to the pools at slot_mapping [num_q_tokens].  A token whose
  * slot is negative is padding: nothing of it is written, its position not
  * looked at.  A slot or position out of range: the token is skipped and

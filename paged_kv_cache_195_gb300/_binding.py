@@ -680,28 +680,6 @@ def _heads(t, name: str, dev: int, T: int, H: int):
     return t.data_ptr(), t.stride(0) if T > 1 else 128 * H
 
 
-def _overlap(a, b) -> bool:
-    """Whether the address ranges of two tensors meet."""
-    def span(t):
-        n = sum((k - 1) * s for k, s in zip(t.shape, t.stride())) + 1 if t.numel() else 0
-        return t.data_ptr(), t.data_ptr() + n * t.element_size()
-    (a0, a1), (b0, b1) = span(a), span(b)
-    return a0 < b1 and b0 < a1
-
-
-def _shares(a, b) -> bool:
-    """Whether two [tokens, heads, 128] tensors (see _rows) share elements, rather
-    than lie side by side in the rows of one tensor."""
-    if not _overlap(a, b):
-        return False
-    if a.stride(0) != b.stride(0) or a.shape[0] < 2:
-        return True
-    row = a.stride(0) * a.element_size()
-    wa, wb = (t[0].numel() * t.element_size() for t in (a, b))
-    gap = (b.data_ptr() - a.data_ptr()) % row
-    return gap < wa or gap + wb > row
-
-
 def _weight(t, name: str, n: int, dev: int):
     if t is None:
         return None
@@ -713,6 +691,9 @@ def _weight(t, name: str, n: int, dev: int):
 
 _ROPE_FIXED = _spec(("positions", _I64, 1), ("cos_sin", _F32, 2), ("slot_mapping", _I64, 1),
                     ("k_pool", _BF16, 4), ("v_pool", _BF16, 4))
+_ROPE_NORMED = _spec(("positions", _I64, 1), ("cos_sin", _F32, 2), ("slot_mapping", _I64, 1),
+                     ("k_pool", _BF16, 4), ("v_pool", _BF16, 4), ("q_weight", _BF16, 1),
+                     ("k_weight", _BF16, 1))
 
 
 def pkv_norm_rope_append(q, k, v, positions, cos_sin, slot_mapping, k_pool, v_pool,
@@ -729,8 +710,16 @@ def pkv_norm_rope_append(q, k, v, positions, cos_sin, slot_mapping, k_pool, v_po
     in place), keys and v [T, Hkv, 128] into the pools at slot_mapping [T]
     int64.  A token with a negative slot is padding: nothing of it is written.
     Returns q_out."""
-    dev, (pos, table, slots, kpool, vpool) = _fast_need((positions, cos_sin, slot_mapping, k_pool, v_pool),
-                                                        _ROPE_FIXED)
+    if q_weight is not None and k_weight is not None:
+        dev, (pos, table, slots, kpool, vpool, wq, wk) = _fast_need(
+            (positions, cos_sin, slot_mapping, k_pool, v_pool, q_weight, k_weight), _ROPE_NORMED)
+        if q_weight.numel() != 128 or k_weight.numel() != 128:
+            raise ValueError("q_weight and k_weight must have 128 elements")
+    else:
+        dev, (pos, table, slots, kpool, vpool) = _fast_need(
+            (positions, cos_sin, slot_mapping, k_pool, v_pool), _ROPE_FIXED)
+        wq = _weight(q_weight, "q_weight", 128, dev)
+        wk = _weight(k_weight, "k_weight", 128, dev)
     try:
         T, Hq, _ = q.shape
         Hkv = k.shape[1]
@@ -747,15 +736,6 @@ def pkv_norm_rope_append(q, k, v, positions, cos_sin, slot_mapping, k_pool, v_po
     nb, h, bs, D = pool = k_pool.shape
     if v_pool.shape != pool or h != Hkv:
         raise ValueError("pool shape does not match the new rows")
-    wq = None if q_weight is None else _weight(q_weight, "q_weight", 128, dev)
-    wk = None if k_weight is None else _weight(k_weight, "k_weight", 128, dev)
-    if T and Hq:
-        # Ranges that meet: side by side in the rows of one tensor, or overlapping?
-        end = op + 2 * ((T - 1) * os_ + 128 * Hq)
-        for t, ptr, stride, H in ((q, qp, qs, Hq), (k, kp, ks, Hkv), (v, vp, vs, Hkv)):
-            if ptr < end and op < ptr + 2 * ((T - 1) * stride + 128 * H):
-                if not (t is q and ptr == op and stride == os_) and _shares(q_out, t):
-                    raise ValueError("q_out may be q, but not overlap the inputs otherwise")
     n, rot = cos_sin.shape
     dims = Dims(0, T, Hq, Hkv, D, bs, nb, 0)
     _call((_lib or load_library()).pkv_norm_rope_append, dev, qp, kp, vp, qs, ks, vs, pos, table, n, rot,

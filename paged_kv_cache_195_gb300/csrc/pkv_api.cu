@@ -293,6 +293,22 @@ constexpr int kMaxRopeHeads = 4096;
 bool eps_ok(float eps) { return eps >= 0x1p-64f && eps <= 1.f; }
 
 // A token stride in elements: rows 16-byte aligned, a token inside one (any for a single token).
+// Whether tokens of `row` elements, `stride` apart, share elements with others: their
+// ranges may meet and they still lie side by side, in the rows of one tensor.
+bool tokens_meet(const void* a, int64_t a_stride, int64_t a_row, const void* b, int64_t b_stride, int64_t b_row,
+                 int tokens) {
+  if (a_row == 0 || b_row == 0) return false;
+  const __int128 x = (__int128)reinterpret_cast<uintptr_t>(a), y = (__int128)reinterpret_cast<uintptr_t>(b);
+  const __int128 x1 = x + 2 * ((__int128)(tokens - 1) * a_stride + a_row);
+  const __int128 y1 = y + 2 * ((__int128)(tokens - 1) * b_stride + b_row);
+  if (x1 <= y || y1 <= x) return false;
+  if (a_stride != b_stride || tokens < 2) return true;
+  const __int128 pitch = 2 * (__int128)a_stride;
+  __int128 gap = (y - x) % pitch;
+  if (gap < 0) gap += pitch;
+  return gap < 2 * a_row || gap + 2 * b_row > pitch;
+}
+
 bool stride_ok(int64_t stride, int row, int tokens) {
   return stride >= 0 && stride % 8 == 0 && (stride >= row || tokens <= 1);
 }
@@ -1132,6 +1148,13 @@ int pkv_norm_rope_append(const void* q, const void* k, const void* v, int64_t q_
       !stride_ok(k_stride, dims->num_kv_heads * pkv::kHeadDim, dims->num_q_tokens) ||
       !stride_ok(v_stride, dims->num_kv_heads * pkv::kHeadDim, dims->num_q_tokens))
     return fail(PKV_ERR_INVALID, "token strides must be multiples of 8 elements and hold a token");
+  const int tokens = dims->num_q_tokens;
+  const int64_t q_row = (int64_t)dims->num_q_heads * pkv::kHeadDim, kv_row = (int64_t)dims->num_kv_heads * pkv::kHeadDim;
+  if ((!(q == q_out && (q_stride == q_out_stride || tokens < 2)) &&
+       tokens_meet(q_out, q_out_stride, q_row, q, q_stride, q_row, tokens)) ||
+      tokens_meet(q_out, q_out_stride, q_row, k, k_stride, kv_row, tokens) ||
+      tokens_meet(q_out, q_out_stride, q_row, v, v_stride, kv_row, tokens))
+    return fail(PKV_ERR_INVALID, "q_out may be q, but not overlap the inputs otherwise");
   DeviceState* st = device_state();
   if (!st) return PKV_ERR_CUDA;
   pkv::NormRopeParams p{};

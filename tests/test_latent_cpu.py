@@ -107,7 +107,7 @@ def _dims(**kw):
     return b.Dims(*[d[f] for f, _ in b.Dims._fields_])
 
 
-def _rope(lib, q=FAKE, k=FAKE, v=FAKE, qs=2048, ks=256, vs=256, pos=FAKE, cs=FAKE, n=100, rot=128, wq=None, wk=None,
+def _rope(lib, q=FAKE, k=FAKE << 8, v=FAKE << 8, qs=2048, ks=256, vs=256, pos=FAKE, cs=FAKE, n=100, rot=128, wq=None, wk=None,
           eps=1e-6, slots=FAKE, out=FAKE, os_=2048, kp=FAKE, vp=FAKE, **kw):
     d = _dims(**{"num_kv_heads": 2, "head_dim": 128, **kw})
     return lib.pkv_norm_rope_append(q, k, v, qs, ks, vs, pos, cs, n, rot, 0, wq, wk, eps, slots, out, os_, kp, vp,
@@ -124,7 +124,11 @@ def _rope(lib, q=FAKE, k=FAKE, v=FAKE, qs=2048, ks=256, vs=256, pos=FAKE, cs=FAK
     *[({name: None}, b.PKV_ERR_INVALID) for name in ("q", "k", "v", "pos", "cs", "slots", "out", "kp", "vp")],
     *[({name: ODD}, b.PKV_ERR_INVALID) for name in ("q", "k", "v", "cs", "out", "kp", "vp", "wq", "wk")],
     (dict(qs=2040), b.PKV_ERR_INVALID), (dict(qs=2052), b.PKV_ERR_INVALID), (dict(ks=255), b.PKV_ERR_INVALID),
-    (dict(vs=0), b.PKV_ERR_INVALID), (dict(os_=-2048), b.PKV_ERR_INVALID)])
+    (dict(vs=0), b.PKV_ERR_INVALID), (dict(os_=-2048), b.PKV_ERR_INVALID),
+    # q_out over the inputs: another stride, k's and v's rows, parts of one tensor that overlap
+    (dict(os_=4096), b.PKV_ERR_INVALID), (dict(out=FAKE + 16), b.PKV_ERR_INVALID), (dict(out=FAKE << 8), b.PKV_ERR_INVALID),
+    (dict(qs=2560, ks=2560, os_=2560, k=FAKE + 4080), b.PKV_ERR_INVALID),
+    (dict(qs=2560, vs=2560, os_=2560, v=FAKE + 5120 - 496), b.PKV_ERR_INVALID)])
 def test_norm_rope_append_refuses(lib, kw, code):
     assert _rope(lib, **kw) == code and lib.pkv_last_error()
 

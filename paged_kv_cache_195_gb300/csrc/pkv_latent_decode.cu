@@ -377,7 +377,9 @@ __device__ __forceinline__ bool non_finite(uint32_t w) {
 static __device__ __noinline__ void clean_tile(uint8_t (*tile)[kChunkBytes], int key0, int pos0, int vis,
                                                unsigned long long* bad, int warp, int lane) {
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int row = max(pos0 + 1 - key0, 0) + warp; row < kTile; row += kSoftWarps) {
+  // (blocks behind the last are zeros already)
+  const int end = min(kTile, (vis + kBlockSize - 1) / kBlockSize * kBlockSize - key0);
+  for (int row = max(pos0 + 1 - key0, 0) + warp; row < end; row += kSoftWarps) {
     const int key = key0 + row;
     bool out = key >= vis;
     if (!out) {
@@ -541,14 +543,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long lo = pl.range_lo, hi = pl.range_hi, start_base = pl.start_base;
   const int piece = pl.piece, start_req = pl.start_req;
   const Req start = pl.start;
-  grid_dependency_wait();
-  allow_dependent_launch();
-  // This CTA's piece records, written again by the pieces that it cuts.
-  if (p.merge && tid < 2) p.piece[(2 * blockIdx.x + tid) * kPieceWords] = 0;
   // The plan's room is the softmax warps' from here on; and the pair's barriers are
   // ready before either CTA's copies or commits arrive on them.
   __syncthreads();
   if (PAIR) cluster_barrier();
+  // (the warp that copies works out its first item before it waits)
+  if (warp != kWarpLoad || lo >= hi) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+  }
+  // This CTA's piece records, written again by the pieces that it cuts.
+  if (p.merge && tid == 0) {
+    p.piece[2 * blockIdx.x * kPieceWords] = 0;
+    p.piece[(2 * blockIdx.x + 1) * kPieceWords] = 0;
+  }
 
   // Columns of the MMAs.
   const int n_cols = ((p.group_heads * p.group_tokens + 15) / 16) * 16;
@@ -626,6 +634,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (id != INT_MIN) record_error(p.err, kErrBounds);
           return oob_row;
         };
+        if (n_item == 0) {
+          grid_dependency_wait();
+          allow_dependent_launch();
+        }
         int nxt = ids(it.t0), cur = 0;
         // The item and its queries, ahead of its first keys.
         if (n_item > 0) ok = all_of(wait_for(&sm.q_empty, (n_item - 1) & 1, p.err, ctl));
@@ -1006,6 +1018,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __nv_bfloat16* dst = p.out + ((long long)it.row0 * p.num_q_heads + head0) * kLatent;
         float* part = p.piece_o + (long long)slot * p.piece_rows * kLatent;
         const uint32_t ta = tmem + lane_off + kColO + wg * 16;
+        float scale[16];
+        #pragma unroll
+        for (int i = 0; i < 16; ++i) scale[i] = __shfl_sync(0xffffffffu, inv, i);
         #pragma unroll 1
         for (int mt = 0; mt < 4; ++mt) {
           const int d = mt * 128 + quad * 32 + lane;
@@ -1018,7 +1033,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __nv_bfloat16* at = dst + (long long)(wg * 16 + (lane & 1)) * kLatent + (d & ~1);
             #pragma unroll
             for (int i = 0; i < 16; i += 2) {
-              const float a = o[i] * __shfl_sync(0xffffffffu, inv, i), b = o[i + 1] * __shfl_sync(0xffffffffu, inv, i + 1);
+              const float a = o[i] * scale[i], b = o[i + 1] * scale[i + 1];
               const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
               if (i + (lane & 1) < n)
                 *reinterpret_cast<uint32_t*>(at + i * kLatent) = lane & 1 ? pack_bf16(other, b) : pack_bf16(a, other);

@@ -202,9 +202,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (!p.early_plan) grid_dependency_wait();
   plan_range(p, sm);
-  if (p.early_plan) grid_dependency_wait();
-  allow_dependent_launch();
-  if (sm.range_lo >= sm.range_hi) return;  // (so does the pair's other CTA)
+  // What the kernel ahead may have written is not looked at, and nothing written, before.
+  // (A CTA without work waits too: the next kernel relies on all before this one.)
+  auto begin = [&] {
+    if (p.early_plan) grid_dependency_wait();
+    allow_dependent_launch();
+  };
+  if (sm.range_lo >= sm.range_hi) {  // (so has the pair's other CTA)
+    begin();
+    return;
+  }
   if (warp == kWarpMma) {
     tmem_alloc_pair(&sm.tmem_base, 512);
   }
@@ -213,6 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_barrier();  // both CTAs' barriers are ready
   tc_fence_after();
   const uint32_t tmem = uniform(sm.tmem_base);
+  begin();
   Walk w;
   w.start(sm);
 

@@ -437,12 +437,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   __syncthreads();
-  if (p.early_plan) grid_dependency_wait();
-  allow_dependent_launch();
-  // How many pieces the joining kernel has to look at.
-  if (p.max_pieces > 0 && blockIdx.x == 0 && tid == 32 * kWarpK) *p.num_pieces = first_pieces;
   const int active = sm.active, split = sm.split;
-  if ((int)(PAIR ? blockIdx.x >> 1 : blockIdx.x) >= active) return;
+  // What the kernel ahead may have written is not looked at, and nothing written, before.
+  // (A CTA without work waits too: the next kernel relies on all before this one.)
+  auto begin = [&] {
+    if (p.early_plan) grid_dependency_wait();
+    allow_dependent_launch();
+    // How many pieces the joining kernel has to look at.
+    if (p.max_pieces > 0 && blockIdx.x == 0 && tid == 32 * kWarpK) *p.num_pieces = first_pieces;
+  };
+  if ((int)(PAIR ? blockIdx.x >> 1 : blockIdx.x) >= active) {
+    begin();
+    return;
+  }
   if (warp == kWarpS) {
     if (PAIR) {
       tmem_alloc_pair(&sm.tmem_base, kTmemCols);
@@ -456,6 +463,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = uniform(sm.tmem_base);
   if (PAIR) cluster_barrier();  // both CTAs' barriers are ready
+  // (the warp of the items works out its first before it waits)
+  if (warp != kWarpK) begin();
 
   // Arrive on a barrier -- both CTAs', in a pair -- once the MMAs so far are done.
   auto commit = [](uint64_t* bar) { PAIR ? commit_pair(bar) : tc_commit(bar); };
@@ -539,6 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Item it;
         int of;
         if (!f.find(p, split, (long long)v, rank, &it, &of)) break;
+        if (n == 0) begin();
         // For the joining kernel: every piece's record is written anew by whoever
         // takes it.
         if (split != INT_MAX && lane == 0)

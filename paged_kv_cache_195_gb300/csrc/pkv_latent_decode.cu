@@ -10,8 +10,9 @@
 // The values are the first 512 dims of the keys: a tile that came in for the
 // scores is there for the products too, and a key costs 1152 bytes of HBM and
 // 2176 flops a head.  Up to 64 heads that is bound by HBM; 128 heads bring the
-// tensor core near its own bound.  Measured: 8 rows of 32768 keys, 16 heads, 66 us
-// (4.6 TB/s); 64 rows of 4096 keys, 128 heads, 103 us (711 TFLOP/s, 2.9 TB/s).
+// tensor core near its own bound.  Measured: 8 rows of 32768 keys, 16 heads, 65 us
+// (4.6 TB/s); 64 rows of 4096 keys, 128 heads, 102 us (714 TFLOP/s, 3.1 TB/s); four
+// rows of up to 128 keys, 16 heads, 7.9 us.
 //
 // Tiling.  A work item is a request's `group_tokens` query tokens times
 // `group_heads` heads: its (token, head) pairs are the N <= 64 columns of the

@@ -22,11 +22,12 @@
 // chunks; O^T[512 dims x N] += C^T P is four M = 128 tiles whose A operand is
 // the same chunks read MN-major.  O^T takes 256 TMEM columns, S^T two buffers
 // of 64.  The other way round (rows as M) O would need all 512 columns.
-// Shared memory holds Q (72 KB), two tiles (144 KB) and P (8 KB), all there
-// is (three tiles of 48 keys, which up to 48 columns leave room for, were no faster
-// anywhere: 8 x 32768 keys, 16 heads 66.6 us for 65.1).  A tile is therefore loaded and released in five parts (the rotated keys,
-// four pairs of latent chunks), each going back as soon as its last MMA is
-// done, so that copies stay in flight while the other tile is worked on.
+// Shared memory holds Q (72 KB), two tiles (144 KB) and P (8 KB), all there is (three
+// tiles of 48 keys, which up to 48 columns leave room for, were no faster anywhere: 8 x
+// 32768 keys, 16 heads 66.6 us for 65.1).  A tile is therefore loaded and released in
+// five parts (the rotated keys, four pairs of latent chunks), each going back as soon
+// as its last MMA is done, so that copies stay in flight while the other tile is
+// worked on.
 //
 // Roles (608 threads).  Sixteen softmax warps: warpgroup g has columns 16 g ..
 // 16 g + 15, its four warps 16 keys each (an M = 64 accumulator lies in 16 of
@@ -670,7 +671,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             #pragma unroll
             for (int b = 0; b < kTileBlocks; ++b) {
               const int l = k + 2 * kTileBlocks + b;
-              const int here = __shfl_sync(0xffffffffu, cur, l), there = __shfl_sync(0xffffffffu, far, l - kWindow * kTileBlocks);
+              const int here = __shfl_sync(0xffffffffu, cur, l);
+              const int there = __shfl_sync(0xffffffffu, far, l - kWindow * kTileBlocks);
               ahead[b] = uniform(l < kWindow * kTileBlocks ? here : there);
             }
           }

@@ -566,8 +566,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint64_t* const bar = &sm.k_full[slot];
               if (rank == 0) mbar_arrive_expect_tx(bar, kChunkBytes);  // (both CTAs' halves)
               const bool rope = c == kKChunks - 1;
-              if (PAIR) tma_load_3d_pair(dst, rope ? &rmap : &kmap, rope ? 0 : c * 64, rope ? y : head, rope ? 0 : y, first_cta(bar));
-              else tma_load_3d(dst, rope ? &rmap : &kmap, rope ? 0 : c * 64, rope ? y : head, rope ? 0 : y, bar);
+              const CUtensorMap* const map = rope ? &rmap : &kmap;
+              const int c0 = rope ? 0 : c * 64, c1 = rope ? y : head, c2 = rope ? 0 : y;
+              if (PAIR) tma_load_3d_pair(dst, map, c0, c1, c2, first_cta(bar));
+              else tma_load_3d(dst, map, c0, c1, c2, bar);
             }
             __syncwarp();
             ++n_chunk;

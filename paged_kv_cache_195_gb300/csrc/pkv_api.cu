@@ -1426,6 +1426,7 @@ int pkv_attention_expanded(const void* q, const void* kv, const void* k_rope, co
   p.scale_log2 = scale * 1.4426950408889634f;
   p.pdl = opt.pdl != 0;
   p.early_plan = p.pdl && opt.early_plan != 0;
+  p.debug_withhold_q = opt.debug_withhold_q != 0;
   p.wait_limit_ns = (unsigned long long)opt.wait_limit_us * 1000ull;
   // In pairs where chunks are long enough for two query tiles on average, and enough.
   L.pairs = dims->num_q_tokens >= 192ll * dims->num_reqs &&

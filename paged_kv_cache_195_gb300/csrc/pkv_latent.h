@@ -174,11 +174,11 @@ struct LatentPrefillParams {
   __nv_bfloat16* out;          // [num_q_tokens, H, 128]
   // Partial states of items split over their keys, by piece number.
   int* piece;                  // [max_pieces][4]: pieces of the item (first pieces only), its rows, head
-  int* num_pieces;
+  int* num_pieces;             // pieces to be joined
   float* piece_ml;             // [max_pieces][128][2]
   float* piece_o;              // [max_pieces][128][128]
-  // [0] pieces handed out beyond each CTA's (pair's) first, [1] CTAs done; zero
-  // between launches.
+  // [0] pieces handed out beyond each CTA's (pair's) first, [1] CTAs done, from bit 32 on
+  // those of them that gave up on a wait; zero between launches.
   unsigned long long* sched;
   int* err;
   int wide;                    // out is aligned to 32 bytes
@@ -187,6 +187,7 @@ struct LatentPrefillParams {
   float scale_log2;
   int early_plan;
   int pdl;
+  int debug_withhold_q;
   unsigned long long wait_limit_ns;
 };
 

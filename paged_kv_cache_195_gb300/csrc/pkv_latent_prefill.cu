@@ -104,6 +104,7 @@ struct __align__(1024) Smem {
   uint32_t tmem_base;
   int active;  // CTAs that take pieces
   int split;   // key tiles of a piece (INT_MAX: items are whole)
+  int pieces;  // of a step whose items are split, else 0
   WaitCtl wait;
 };
 // (no room to align it in: a block without static shared memory has it on a KiB)
@@ -431,15 +432,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&rmap);
   }
   if (!p.early_plan) grid_dependency_wait();
-  int first_pieces = 0;
   Finder<GROUP> f;  // (of warp kWarpK)
   if (warp == kWarpK) {
     long long pieces;
     const int split = plan_split<GROUP>(p, gridDim.x, &pieces);
     f.start(p, split);
     if (lane == 0) {
-      if (blockIdx.x == 0) first_pieces = split != INT_MAX ? (int)pieces : 0;
       sm.split = split;
+      sm.pieces = split != INT_MAX ? (int)pieces : 0;
       sm.active = (int)min(pieces, (long long)(PAIR ? gridDim.x >> 1 : gridDim.x));  // CTAs, or pairs
     }
   }
@@ -450,8 +450,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto begin = [&] {
     if (p.early_plan) grid_dependency_wait();
     allow_dependent_launch();
-    // How many pieces the joining kernel has to look at.
-    if (p.max_pieces > 0 && blockIdx.x == 0 && tid == 32 * kWarpK) *p.num_pieces = first_pieces;
+    // Nothing to join, unless the last CTA to finish says otherwise.
+    if (p.max_pieces > 0 && blockIdx.x == 0 && tid == 32 * kWarpK) *p.num_pieces = 0;
   };
   if ((int)(PAIR ? blockIdx.x >> 1 : blockIdx.x) >= active) {
     begin();
@@ -593,6 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (rank == 0) mbar_arrive_expect_tx(&sm.q_full, kCtas * kKChunks * kChunkBytes);
               #pragma unroll
               for (int c = 0; c < kKChunks; ++c) {
+                if (p.debug_withhold_q) break;
                 if (PAIR) tma_load_3d_pair(sm.q[c], &qmap, c * 64, head, row0, first_cta(&sm.q_full));
                 else tma_load_3d(sm.q[c], &qmap, c * 64, head, row0, &sm.q_full);
               }
@@ -879,10 +880,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kWarpS) {
     tmem_dealloc(tmem, kTmemCols);
   }
-  // The last CTA to finish empties the queue for the next launch.
+  // The last CTA to finish empties the queue for the next launch, and says how many
+  // pieces the joining kernel has to look at: all, or none once a CTA gave up on a wait
+  // (counted from bit 32 on), for then pieces may be left whose records and states are
+  // not of this call.
   if (tid == 0 && rank == 0) {
     __threadfence();
-    if (atomicAdd(p.sched + 1, 1ull) == (unsigned long long)(active - 1)) {
+    const unsigned long long mine = 1ull + (sm.wait.abort ? 1ull << 32 : 0);
+    const unsigned long long all = atomicAdd(p.sched + 1, mine) + mine;
+    if ((unsigned)all == (unsigned)active) {
+      if (p.max_pieces > 0 && all >> 32 == 0) *p.num_pieces = sm.pieces;
       p.sched[0] = 0;
       p.sched[1] = 0;
       __threadfence();

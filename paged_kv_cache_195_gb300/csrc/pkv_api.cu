@@ -1314,6 +1314,7 @@ int pkv_attention_latent(const void* q, const void* pool, const int32_t* block_t
   p.scale_log2 = scale * 1.4426950408889634f;
   p.pdl = opt.pdl != 0;
   p.early_plan = p.pdl && opt.early_plan != 0;
+  p.debug_withhold_q = opt.debug_withhold_q != 0;
   p.wait_limit_ns = (unsigned long long)opt.wait_limit_us * 1000ull;
   const cuuint32_t qbox[3] = {64, (cuuint32_t)g.group_heads, (cuuint32_t)g.group_tokens};
   rc = encode_bf16_3d(&L.qmap, q, pkv::kLatRow, dims->num_q_heads, dims->num_q_tokens, pkv::kLatRow,

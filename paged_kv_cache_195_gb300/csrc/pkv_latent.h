@@ -127,6 +127,7 @@ struct LatentDecodeParams {
   float scale_log2;
   int early_plan;
   int pdl;
+  int debug_withhold_q;
   unsigned long long wait_limit_ns;
 };
 

@@ -649,7 +649,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&sm.item_full[n_item % kItems]);
           mbar_arrive_expect_tx(&sm.q_full, q_bytes);
           #pragma unroll 1
-          for (int c = 0; c < kChunks; ++c) tma_load_3d(sm.q[c], &qmap, c * 64, head0, it.row0, &sm.q_full);
+          for (int c = p.debug_withhold_q ? kChunks : 0; c < kChunks; ++c)
+            tma_load_3d(sm.q[c], &qmap, c * 64, head0, it.row0, &sm.q_full);
         }
         __syncwarp();
         ++n_item;
@@ -1005,13 +1006,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<float2*>(p.piece_ml + ((long long)slot * p.piece_rows + col) * 2) =
               make_float2(sm.top[col], sum);
       }
-      if (!whole && ok && tid == 0) {
-        int* rec = p.piece + slot * kPieceWords;
-        rec[1] = it.row0;
-        rec[2] = cols;
-        rec[0] = 4 | (it.t0 == 0 ? kPieceFirst : 0) | (it.t1 == n_tiles ? kPieceLast : 0);
-      }
-      ok = ok && wait_for(&sm.o_full, n_item & 1, p.err, ctl);
+      // (one answer for the warp: what follows takes all of its lanes)
+      ok = all_of(ok && wait_for(&sm.o_full, n_item & 1, p.err, ctl));
       tc_fence_after();
       // Boundary keys that were taken out, by any warp.
       if (it.nt > 1) named_barrier(kBarSoft, kSoftThreads);
@@ -1058,7 +1054,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.o_empty);
       if (barrier_or(kBarSoft, kSoftThreads, !ok)) break;
-      if (tid == 0) *bad = 0;
+      if (tid == 0) {
+        *bad = 0;
+        // The piece is there, every warp's part of it.
+        if (!whole) {
+          int* rec = p.piece + slot * kPieceWords;
+          rec[1] = it.row0;
+          rec[2] = cols;
+          rec[0] = 4 | (it.t0 == 0 ? kPieceFirst : 0) | (it.t1 == n_tiles ? kPieceLast : 0);
+        }
+      }
     }
   }
   tc_fence_before();

@@ -547,8 +547,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           v = __shfl_sync(0xffffffffu, v, 0);
           if (PAIR && lane == 0) send_second(&sm.next[at], &sm.next_full[at], v);
         } else if (n > 0) {
-          ok = wait_for(&sm.next_full[at], ((n - 1) / kItems) & 1, p.err, ctl);
-          if (!all_of(ok)) break;
+          ok = all_of(wait_for(&sm.next_full[at], ((n - 1) / kItems) & 1, p.err, ctl));
+          if (!ok) break;
           asm volatile("fence.acq_rel.cluster;" ::: "memory");
           v = *(volatile unsigned long long*)&sm.next[at];
         }

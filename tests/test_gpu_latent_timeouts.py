@@ -12,7 +12,7 @@ import torch
 import paged_kv_cache_195_gb300 as pkv
 from paged_kv_cache_195_gb300 import build as pkv_build
 
-from test_gpu_latent import exp_case, exp_check, exp_run
+from test_gpu_latent import exp_case, exp_check, exp_run, lat_case, lat_check, lat_run
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
@@ -90,4 +90,21 @@ def test_expanded_form_without_its_queries(pkv_opts, lens, qs, heads):
     ws.buf[:ws.ptr - ws.buf.data_ptr() + 128].zero_()
     for _ in range(2):  # TMEM and the aborted CTAs' state are gone
         exp_check(c, exp_run(c, out=out[:T], workspace=ws))
+        assert (out[T:] == 7).all()
+
+
+@pytest.mark.parametrize("lens,qs,heads", [
+    ([5000] * 4, [1] * 4, 128), ([32768], [1], 16),  # few rows, in pieces
+    ([900] * 200, [1] * 200, 100),                   # ranges that cut rows
+    ([17, 64, 100, 128], [1] * 4, 16),               # whole
+    ([300, 70, 0, 9], [60, 5, 0, 1], 16)])
+def test_absorbed_form_without_its_queries(pkv_opts, lens, qs, heads):
+    c = lat_case(lens, qs, heads)
+    T = sum(qs)
+    ws = stale_workspace(T)
+    out = torch.full((T + GUARD, heads, 512), 7.0, dtype=BF, device="cuda")
+    withheld(pkv_opts, lambda: lat_run(c, out=out[:T], workspace=ws))
+    assert (out == 7).all(), "an aborted call wrote output"
+    for _ in range(2):
+        lat_check(c, lat_run(c, out=out[:T], workspace=ws))
         assert (out[T:] == 7).all()

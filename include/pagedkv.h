@@ -610,7 +610,8 @@ typedef struct pkv_options {
                                PKV_ERR_TIMEOUT (>= 1) */
     int32_t debug_withhold_q; /* testing only (0): the tensor-core decode,
                                pkv_attention_latent and pkv_attention_expanded
-                               never load q, so their waits run out after wait_limit_us; exercises
+                               never load q, and pkv_expand_latent no weights, so
+                               their waits run out after wait_limit_us; exercises
                                the timeout path.  Results are not computed. */
     int32_t rowgroup_cost;  /* PKV_ROWGROUP_COST (16): when the decode plan cuts the
                                step into equal per-CTA ranges, every (query row, KV

@@ -1360,6 +1360,7 @@ int pkv_expand_latent(const void* pool, const void* weight, const int32_t* block
   p.max_blocks = dims->max_blocks_per_req;
   p.pdl = opt.pdl != 0;
   p.early_plan = p.pdl && opt.early_plan != 0;
+  p.debug_withhold_q = opt.debug_withhold_q != 0;
   p.wait_limit_ns = (unsigned long long)opt.wait_limit_us * 1000ull;
   const cuuint32_t wbox[3] = {64, 128, 1};
   rc = encode_latent_map(&L.kmap, pool, dims);

@@ -154,6 +154,7 @@ struct LatentExpandParams {
   int num_reqs, num_rows, num_heads, num_blocks, max_blocks;
   int early_plan;
   int pdl;
+  int debug_withhold_q;
   unsigned long long wait_limit_ns;
 };
 

@@ -283,7 +283,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           if (leader) {
             if (rank == 0) mbar_arrive_expect_tx(&sm.b_full[st], 2 * kChunkBytes);
-            tma_load_3d_pair(sm.b[st], &wmap, c * 64, h * kOut + rank * kHalf, 0, first_cta(&sm.b_full[st]));
+            if (!p.debug_withhold_q)
+              tma_load_3d_pair(sm.b[st], &wmap, c * 64, h * kOut + rank * kHalf, 0, first_cta(&sm.b_full[st]));
           }
           __syncwarp();
           ++n_b;

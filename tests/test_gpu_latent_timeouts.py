@@ -12,7 +12,8 @@ import torch
 import paged_kv_cache_195_gb300 as pkv
 from paged_kv_cache_195_gb300 import build as pkv_build
 
-from test_gpu_latent import exp_case, exp_check, exp_run, lat_case, lat_check, lat_run
+import lat_reference as ref
+from test_gpu_latent import close, dev, exp_case, exp_check, exp_run, f64, lat_case, lat_check, lat_run
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
@@ -108,3 +109,18 @@ def test_absorbed_form_without_its_queries(pkv_opts, lens, qs, heads):
     for _ in range(2):
         lat_check(c, lat_run(c, out=out[:T], workspace=ws))
         assert (out[T:] == 7).all()
+
+
+@pytest.mark.parametrize("lens,heads", [([701], 16), ([17, 64, 0, 300], 1), ([3000] * 4, 32)])
+def test_expansion_without_its_weights(pkv_opts, lens, heads):
+    c, n = lat_case(lens, [0] * len(lens), 1), sum(lens)
+    w = (torch.randn(heads, 256, 512, generator=torch.Generator().manual_seed(1)) / 20).to(BF).cuda()
+    kv = torch.full((n + GUARD, heads, 256), 7.0, dtype=BF, device="cuda")
+    kr = torch.full((n + GUARD, 64), 7.0, dtype=BF, device="cuda")
+    args = [dev(x, torch.int32) for x in (c["tab"], c["lens"], np.concatenate([[0], np.cumsum(lens)]))]
+    withheld(pkv_opts, lambda: pkv.pkv_expand_latent(c["pool"], w, *args, kv, kr))
+    assert (kv == 7).all() and (kr[n:] == 7).all()  # (the rotated keys need no weights)
+    pkv.pkv_expand_latent(c["pool"], w, *args, kv, kr)
+    want, rope, bound = ref.expand(f64(c["pool"]), f64(w), c["tab"], lens)
+    close(f64(kv)[:n], want, bound)
+    assert np.array_equal(f64(kr)[:n], rope) and (kv[n:] == 7).all() and (kr[n:] == 7).all()

@@ -74,7 +74,8 @@ struct Req {
 
 __device__ __forceinline__ Req load_req(const LatentExpandParams& p, int r, bool* bad) {
   const int n = __ldg(p.seq_lens + r), a = __ldg(p.kv_start + r), b = __ldg(p.kv_start + r + 1);
-  *bad = !(n >= 0 && n <= p.max_blocks * kBlockSize && a >= 0 && b <= p.num_rows && b - a == n);
+  // (b >= a: the difference of wild entries may wrap)
+  *bad = !(n >= 0 && n <= p.max_blocks * kBlockSize && a >= 0 && b >= a && b <= p.num_rows && b - a == n);
   return Req{*bad ? 0 : n, a};
 }
 

@@ -138,7 +138,8 @@ __device__ __forceinline__ Req load_req(const LatentPrefillParams& p, int r, boo
   a.k0 = __ldg(p.kv_start + r);
   const int k1 = __ldg(p.kv_start + r + 1);
   a.qr = q1 - a.q0;
-  *bad = !(a.q0 >= 0 && a.qr >= 0 && q1 <= p.num_q_tokens && a.qr <= a.L && a.k0 >= 0 &&
+  // (ends not before starts: the difference of wild entries may wrap)
+  *bad = !(a.q0 >= 0 && q1 >= a.q0 && q1 <= p.num_q_tokens && a.qr <= a.L && a.k0 >= 0 && k1 >= a.k0 &&
            k1 <= p.num_rows && k1 - a.k0 == a.L);
   a.nq = *bad ? 0 : cdiv(a.qr, GROUP);
   return a;

@@ -57,7 +57,8 @@ __device__ __forceinline__ ReqInfo make_request(const DecodeParams& p, int q0, i
   ri.q0 = q0;
   ri.L = L;
   ri.qr = q1 - q0;
-  const bool ok = ri.q0 >= 0 && ri.qr >= 0 && q1 <= p.num_q_tokens && ri.qr <= ri.L &&
+  // (q1 >= q0, not qr >= 0: the difference of wild entries may wrap)
+  const bool ok = ri.q0 >= 0 && q1 >= q0 && q1 <= p.num_q_tokens && ri.qr <= ri.L &&
                   ri.L <= p.max_blocks * kBlockSize;
   ri.decode = ok && ri.qr > 0 && ri.qr < p.prefill_min_q;
   // A shared prefix (cascade) must end before the request's first query.

@@ -143,7 +143,8 @@ __device__ __forceinline__ PfReq load_pf_request(const PrefillParams& p, int u, 
     const int q1 = idx_ok ? __ldg(p.qsl + first + n) : 0;
     a.qr = q1 - a.q0;
     a.L = nb * kBlockSize;
-    a.ok = idx_ok && a.q0 >= 0 && a.qr >= 1 && q1 <= p.num_q_tokens && nb >= 1 &&
+    // (q1 >= q0 as well: the difference of wild entries may wrap)
+    a.ok = idx_ok && a.q0 >= 0 && q1 >= a.q0 && a.qr >= 1 && q1 <= p.num_q_tokens && nb >= 1 &&
            nb <= p.max_blocks;
   } else {
     a.tab = u;
@@ -151,7 +152,7 @@ __device__ __forceinline__ PfReq load_pf_request(const PrefillParams& p, int u, 
     const int q1 = __ldg(p.qsl + u + 1);
     a.L = __ldg(p.seq_lens + u);
     a.qr = q1 - a.q0;
-    a.ok = a.q0 >= 0 && a.qr >= p.prefill_min_q && q1 <= p.num_q_tokens && a.qr <= a.L &&
+    a.ok = a.q0 >= 0 && q1 >= a.q0 && a.qr >= p.prefill_min_q && q1 <= p.num_q_tokens && a.qr <= a.L &&
            a.L <= p.max_blocks * kBlockSize;
   }
   a.nchunk = p.prefix_mode ? prefix_chunks(a.L) : 1;

@@ -175,7 +175,8 @@ __device__ __forceinline__ Req load_req(const PrefillParams& p, int r, int tq) {
   const int q1 = __ldg(p.qsl + r + 1);
   a.L = __ldg(p.seq_lens + r);
   a.qr = q1 - a.q0;
-  const bool ok = a.q0 >= 0 && a.qr >= p.prefill_min_q && q1 <= p.num_q_tokens && a.qr <= a.L &&
+  // (q1 >= q0 as well: the difference of wild entries may wrap)
+  const bool ok = a.q0 >= 0 && q1 >= a.q0 && a.qr >= p.prefill_min_q && q1 <= p.num_q_tokens && a.qr <= a.L &&
                   a.L <= p.max_blocks * kBlockSize;
   if (!ok && a.qr >= p.prefill_min_q && blockIdx.x == 0) record_error(p.err, kErrBounds);
   a.ntiles = ok ? ceil_div(a.qr, tq) : 0;

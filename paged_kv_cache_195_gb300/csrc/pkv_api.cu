@@ -1359,7 +1359,6 @@ int pkv_expand_latent(const void* pool, const void* weight, const int32_t* block
   p.num_blocks = dims->num_blocks;
   p.max_blocks = dims->max_blocks_per_req;
   p.pdl = opt.pdl != 0;
-  p.early_plan = p.pdl && opt.early_plan != 0;
   p.debug_withhold_q = opt.debug_withhold_q != 0;
   p.wait_limit_ns = (unsigned long long)opt.wait_limit_us * 1000ull;
   const cuuint32_t wbox[3] = {64, 128, 1};
@@ -1427,7 +1426,6 @@ int pkv_attention_expanded(const void* q, const void* kv, const void* k_rope, co
   p.max_pieces = items < st->sm_count && num_rows > 1024 ? 2 * st->sm_count : 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.pdl = opt.pdl != 0;
-  p.early_plan = p.pdl && opt.early_plan != 0;
   p.debug_withhold_q = opt.debug_withhold_q != 0;
   p.wait_limit_ns = (unsigned long long)opt.wait_limit_us * 1000ull;
   // In pairs where chunks are long enough for two query tiles on average, and enough.

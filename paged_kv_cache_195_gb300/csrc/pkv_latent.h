@@ -152,7 +152,6 @@ struct LatentExpandParams {
   __nv_bfloat16* k_rope;       // [num_rows, 64]
   int* err;
   int num_reqs, num_rows, num_heads, num_blocks, max_blocks;
-  int early_plan;
   int pdl;
   int debug_withhold_q;
   unsigned long long wait_limit_ns;
@@ -187,7 +186,6 @@ struct LatentPrefillParams {
   int num_reqs, num_q_tokens, num_rows, num_heads;
   int max_pieces;              // 0: items are not split
   float scale_log2;
-  int early_plan;
   int pdl;
   int debug_withhold_q;
   unsigned long long wait_limit_ns;

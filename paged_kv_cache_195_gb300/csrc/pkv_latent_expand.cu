@@ -148,9 +148,11 @@ struct Walk {
     if (pos >= sm.range_hi) return false;
     bool bad;
     if (a.keys < 0) a = load_req(p, req, &bad);
-    while (pos >= base + units(p, a)) {  // (pos < range_hi: there is a later request)
+    while (pos >= base + units(p, a)) {
       base += units(p, a);
-      a = load_req(p, ++req, &bad);
+      // (pos < range_hi: there is a later request, unless someone writes the lengths meanwhile)
+      if (++req >= p.num_reqs) return false;
+      a = load_req(p, req, &bad);
     }
     const long long local = pos - base;
     tile = (int)(local / p.num_heads);
@@ -201,18 +203,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&kmap);
     prefetch_tensormap(&wmap);
   }
-  if (!p.early_plan) grid_dependency_wait();
+  // The plan is made after the wait: the running sum of the lengths is as a rule the work
+  // of the kernel ahead.  (A CTA without work waits too: the next kernel relies on all
+  // before this one.)
+  grid_dependency_wait();
+  allow_dependent_launch();
   plan_range(p, sm);
-  // What the kernel ahead may have written is not looked at, and nothing written, before.
-  // (A CTA without work waits too: the next kernel relies on all before this one.)
-  auto begin = [&] {
-    if (p.early_plan) grid_dependency_wait();
-    allow_dependent_launch();
-  };
-  if (sm.range_lo >= sm.range_hi) {  // (so has the pair's other CTA)
-    begin();
-    return;
-  }
+  if (sm.range_lo >= sm.range_hi) return;  // (so has the pair's other CTA)
   if (warp == kWarpMma) {
     tmem_alloc_pair(&sm.tmem_base, 512);
   }
@@ -221,7 +218,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_barrier();  // both CTAs' barriers are ready
   tc_fence_after();
   const uint32_t tmem = uniform(sm.tmem_base);
-  begin();
   Walk w;
   w.start(sm);
 

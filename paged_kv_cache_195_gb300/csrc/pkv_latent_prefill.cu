@@ -432,7 +432,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&kmap);
     prefetch_tensormap(&rmap);
   }
-  if (!p.early_plan) grid_dependency_wait();
+  // The plan is made after the wait: the running sum of the lengths is as a rule the work
+  // of a kernel just ahead.  (A CTA without work waits too: the next kernel relies on all
+  // before this one.)
+  grid_dependency_wait();
+  allow_dependent_launch();
+  // Nothing to join, unless the last CTA to finish says otherwise.
+  if (p.max_pieces > 0 && blockIdx.x == 0 && tid == 0) *p.num_pieces = 0;
   Finder<GROUP> f;  // (of warp kWarpK)
   if (warp == kWarpK) {
     long long pieces;
@@ -446,18 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   const int active = sm.active, split = sm.split;
-  // What the kernel ahead may have written is not looked at, and nothing written, before.
-  // (A CTA without work waits too: the next kernel relies on all before this one.)
-  auto begin = [&] {
-    if (p.early_plan) grid_dependency_wait();
-    allow_dependent_launch();
-    // Nothing to join, unless the last CTA to finish says otherwise.
-    if (p.max_pieces > 0 && blockIdx.x == 0 && tid == 32 * kWarpK) *p.num_pieces = 0;
-  };
-  if ((int)(PAIR ? blockIdx.x >> 1 : blockIdx.x) >= active) {
-    begin();
-    return;
-  }
+  if ((int)(PAIR ? blockIdx.x >> 1 : blockIdx.x) >= active) return;
   if (warp == kWarpS) {
     if (PAIR) {
       tmem_alloc_pair(&sm.tmem_base, kTmemCols);
@@ -471,8 +466,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = uniform(sm.tmem_base);
   if (PAIR) cluster_barrier();  // both CTAs' barriers are ready
-  // (the warp of the items works out its first before it waits)
-  if (warp != kWarpK) begin();
 
   // Arrive on a barrier -- both CTAs', in a pair -- once the MMAs so far are done.
   auto commit = [](uint64_t* bar) { PAIR ? commit_pair(bar) : tc_commit(bar); };
@@ -556,7 +549,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         Item it;
         int of;
         if (!f.find(p, split, (long long)v, rank, &it, &of)) break;
-        if (n == 0) begin();
         // For the joining kernel: every piece's record is written anew by whoever
         // takes it.
         if (split != INT_MAX && lane == 0)

@@ -11,7 +11,7 @@
 // scores is there for the products too, and a key costs 1152 bytes of HBM and
 // 2176 flops a head.  Up to 64 heads that is bound by HBM; 128 heads bring the
 // tensor core near its own bound.  Measured: 8 rows of 32768 keys, 16 heads, 65 us
-// (4.6 TB/s); 64 rows of 4096 keys, 128 heads, 102 us (714 TFLOP/s, 3.1 TB/s); four
+// (4.7 TB/s); 64 rows of 4096 keys, 128 heads, 100 us (730 TFLOP/s, 3.2 TB/s); four
 // rows of up to 128 keys, 16 heads, 7.9 us.
 //
 // Tiling.  A work item is a request's `group_tokens` query tokens times
@@ -41,14 +41,14 @@
 // next tile had landed: 106 us where two warps took 83, 8 x 32768 keys, 16 heads).
 //
 // Work split.  The items' keys (plus a fixed cost an item) form one sequence
-// that is cut in equal ranges, one a CTA -- or, with more than 64 heads, one a
-// pair of CTAs that read the same keys for half of the heads each.  Rows cut
+// that is cut in equal ranges, one a CTA -- or, with more than 64 heads, one for
+// two neighbours that read the same keys for half of the heads each.  Rows cut
 // by a range end leave unnormalised partial states, which latent_merge_kernel
 // joins; it needs no counters, so the workspace holds no state between calls.
 #include <climits>
 
 #include "pkv_latent.h"
-#include "pkv_pair.cuh"
+#include "pkv_tc.cuh"
 
 namespace pkv {
 namespace {
@@ -217,10 +217,11 @@ __device__ __forceinline__ long long div_ll(long long a, long long b) {
   return a / b;
 }
 
-// Unit `unit` of `units` CTAs' (or pairs') share.  THREADS threads with up to PER
-// requests each in registers: one warp for steps of up to kWarpReqs requests, beside
-// which the rest of the CTA is set up, else the block (which then needs a
-// __syncthreads before it reads the result), PER = 0: any number, read again.
+// Unit `unit` of `units` CTAs' (or, with two head groups, neighbours') share.
+// THREADS threads with up to PER requests each in registers: one warp for steps of up
+// to kWarpReqs requests, beside which the rest of the CTA is set up, else the block
+// (which then needs a __syncthreads before it reads the result), PER = 0: any number,
+// read again.
 constexpr int kWarpPer = 4;
 constexpr int kWarpReqs = 32 * kWarpPer;
 
@@ -457,32 +458,14 @@ static __device__ __noinline__ void spread_bad(const LatentDecodeParams& p, cons
   }
 }
 
-// The pair's side of the copies and of their release: a copy lands in both CTAs of
-// the cluster, at the same place, and counts on both barriers; a commit arrives on
-// both.
-__device__ __forceinline__ void tma_load_2d_both(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      ".multicast::cluster [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar)), "h"((uint16_t)3)
-      : "memory");
-}
-
-__device__ __forceinline__ void tc_commit_both(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-      "[%0], %1;" ::"r"(smem_u32(bar)),
-      "h"((uint16_t)3)
-      : "memory");
-}
-
 __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
                "r"(x), "r"(y)
                : "memory");
 }
 
-template <bool PAIR>
+// TWO: two groups of heads.
+template <bool TWO>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_decode_kernel(const __grid_constant__ CUtensorMap qmap,
                          const __grid_constant__ CUtensorMap kmap, const LatentDecodeParams p) {
@@ -492,8 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw + (((raw + 1023u) & ~1023u) - raw));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   WaitCtl* ctl = &sm.wait;
-  // CTA b of a pair: head group b % 2 of range b / 2.
-  const int hg = PAIR ? blockIdx.x & 1 : 0;
+  // CTA b of two: head group b % 2 of range b / 2.
+  const int hg = TWO ? blockIdx.x & 1 : 0;
   const int head0 = hg * p.group_heads;
   const int heads = min(p.group_heads, p.num_q_heads - head0);
 
@@ -501,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kStages; ++s)
       for (int i = 0; i < kParts; ++i) {
         mbar_init(&sm.kv_full[s][i], 1);
-        mbar_init(&sm.kv_empty[s][i], PAIR ? 2 : 1);
+        mbar_init(&sm.kv_empty[s][i], 1);
       }
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, 1);
@@ -527,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&sm.tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  const int unit = PAIR ? blockIdx.x >> 1 : blockIdx.x, units = PAIR ? gridDim.x >> 1 : gridDim.x;
+  const int unit = TWO ? blockIdx.x >> 1 : blockIdx.x, units = TWO ? gridDim.x >> 1 : gridDim.x;
   if (p.num_reqs <= kWarpReqs) {
     if (warp == kWarpLoad) {
       if (!p.early_plan) grid_dependency_wait();
@@ -545,10 +528,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long lo = pl.range_lo, hi = pl.range_hi, start_base = pl.start_base;
   const int piece = pl.piece, start_req = pl.start_req;
   const Req start = pl.start;
-  // The plan's room is the softmax warps' from here on; and the pair's barriers are
-  // ready before either CTA's copies or commits arrive on them.
+  // The plan's room is the softmax warps' from here on.
   __syncthreads();
-  if (PAIR) cluster_barrier();
   // (the warp that copies works out its first item before it waits)
   if (warp != kWarpLoad || lo >= hi) {
     grid_dependency_wait();
@@ -563,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Columns of the MMAs.
   const int n_cols = ((p.group_heads * p.group_tokens + 15) / 16) * 16;
   if (lo >= hi) {
-    // no work (nor for the pair's other CTA)
+    // no work
   } else if (warp == kWarpLoad) {
     // =========================== copies ===================================
     // One thread issues all copies, from uniform registers (a thread a copy, eight
@@ -663,11 +644,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             cur = row_of(nxt);
             if (j + kWindow < j1) nxt = ids(j + kWindow);
           }
-          // Pairs wait for half of a tile's copies each, with one tile in flight while the
-          // other is worked on: the tile after next comes into L2 meanwhile (64 rows of
-          // 4096 keys, 128 heads: 103 us for 112; three or four tiles ahead 104 and 105).
+          // Of two neighbours each brings half of the tile after next into L2, while one
+          // tile is in flight and the other worked on (64 rows of 4096 keys, 128 heads: 100
+          // us for 108 without; 64 of 2048, 96 heads 57 for 61; one group alone, 8 of 32768,
+          // 16 heads, gains nothing: 66.8 for 65.1).
           int ahead[kTileBlocks];
-          if (PAIR) {
+          if (TWO) {
             const int far = row_of(nxt);
             #pragma unroll
             for (int b = 0; b < kTileBlocks; ++b) {
@@ -693,19 +675,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 0; i < part_chunks(part); ++i) {
                 const int c = 2 * part + i;
                 #pragma unroll
-                for (int b = 0; b < kTileBlocks; ++b) {
-                  if (!PAIR) tma_load_2d(sm.kv[st][c] + b * 2048, &kmap, c * 64, rows[b], bar);
-                  // (every other copy is the other CTA's)
-                  else if (((c * kTileBlocks + b) & 1) == hg)
-                    tma_load_2d_both(sm.kv[st][c] + b * 2048, &kmap, c * 64, rows[b], bar);
-                }
+                for (int b = 0; b < kTileBlocks; ++b)
+                  tma_load_2d(sm.kv[st][c] + b * 2048, &kmap, c * 64, rows[b], bar);
               }
             }
             __syncwarp();
             parts = part + 1;
           }
           if (!ok) break;
-          if (PAIR && leader && j + 2 < j1) {
+          if (TWO && leader && j + 2 < j1) {
             #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
               #pragma unroll
@@ -779,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         if (leader) {
           tc_commit(&sm.s_full[st]);
-          PAIR ? tc_commit_both(&sm.kv_empty[st][kParts - 1]) : tc_commit(&sm.kv_empty[st][kParts - 1]);
+          tc_commit(&sm.kv_empty[st][kParts - 1]);
           if (left == 1) tc_commit(&sm.q_empty);
         }
         __syncwarp();
@@ -826,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int kk = 0; kk < kTile / 16; ++kk)
               tc_mma_f16_ss(tmem + kColO + m * kLatMaxRows, da + (2 * m * kStep + kk * (2048 >> 4)),
                             desc_p + 2 * kk, idesc, j > 0 || kk > 0);
-            PAIR ? tc_commit_both(&sm.kv_empty[st][m]) : tc_commit(&sm.kv_empty[st][m]);
+            tc_commit(&sm.kv_empty[st][m]);
           }
           tc_commit(&sm.p_free);
           if (j == n - 1) tc_commit(&sm.o_full);
@@ -1070,8 +1048,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == kWarpS) tmem_dealloc(tmem, kTmemCols);
-  // A CTA's memory and barriers outlive the copies and commits of the other.
-  if (PAIR) cluster_barrier();
 }
 
 // Joins the pieces of rows that were cut.  Block (b, y): eight columns of the item
@@ -1270,7 +1246,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps, kFewBlocks)
   }
 }
 
-template <bool PAIR>
+template <bool TWO>
 cudaError_t launch_decode(const LatentDecodeLaunch& L, cudaStream_t stream) {
   constexpr size_t smem = sizeof(Smem) + 1024;
   static unsigned long long configured = 0;
@@ -1279,7 +1255,7 @@ cudaError_t launch_decode(const LatentDecodeLaunch& L, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(__atomic_load_n(&configured, __ATOMIC_ACQUIRE) & bit)) {
-    e = cudaFuncSetAttribute(latent_decode_kernel<PAIR>,
+    e = cudaFuncSetAttribute(latent_decode_kernel<TWO>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     __atomic_fetch_or(&configured, bit, __ATOMIC_RELEASE);
@@ -1289,15 +1265,12 @@ cudaError_t launch_decode(const LatentDecodeLaunch& L, cudaStream_t stream) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = L.p.pdl ? 1 : 0;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = PAIR ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, latent_decode_kernel<PAIR>, L.qmap, L.kmap, L.p);
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, latent_decode_kernel<TWO>, L.qmap, L.kmap, L.p);
 }
 
 }  // namespace

@@ -23,7 +23,7 @@
 // the value dims of a tile: half the copies, half the operand reads, and room for
 // four tiles in flight.  A CTA alone holds all 80 KB of a tile, which with the
 // MMAs' own reads is more than shared memory and the copies give (1.04-1.09 us a
-// tile, with the keys multicast or not).
+// tile).
 //
 // Order.  A CTA's first item is its own by its number, the others come from a queue,
 // longest requests first, a head's query tiles one after the other (the CTAs that run

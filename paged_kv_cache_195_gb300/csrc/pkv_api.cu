@@ -1407,6 +1407,7 @@ int pkv_attention_expanded(const void* q, const void* kv, const void* k_rope, co
   p.qsl = query_start_loc;
   p.kv_start = kv_start_loc;
   p.kv = static_cast<const __nv_bfloat16*>(kv);
+  p.k_rope = static_cast<const __nv_bfloat16*>(k_rope);
   p.out = static_cast<__nv_bfloat16*>(out);
   p.piece = reinterpret_cast<int*>(ws + w.piece);
   p.num_pieces = reinterpret_cast<int*>(ws + 128);

@@ -172,6 +172,7 @@ struct LatentPrefillParams {
   const int32_t* qsl;
   const int32_t* kv_start;
   const __nv_bfloat16* kv;     // [num_rows, H, 256]: key | value
+  const __nv_bfloat16* k_rope; // [num_rows, 64]
   __nv_bfloat16* out;          // [num_q_tokens, H, 128]
   // Partial states of items split over their keys, by piece number.
   int* piece;                  // [max_pieces][4]: pieces of the item (first pieces only), its rows, head

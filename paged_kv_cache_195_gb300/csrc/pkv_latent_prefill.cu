@@ -359,18 +359,31 @@ static __device__ __noinline__ void clean_values(uint8_t (*v)[kChunkBytes], int 
   }
 }
 
+// Whether the key of row `row` of kv, its part in k_rope with it, is finite.
+__device__ __forceinline__ bool finite_key(const LatentPrefillParams& p, long long row, int head) {
+  const uint32_t* k = reinterpret_cast<const uint32_t*>(p.kv + (row * p.num_heads + head) * (kNope + kValDim));
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(p.k_rope + row * kRopeDim);
+  bool out = false;
+  for (int i = 0; i < kNope / 2; ++i) out = out || non_finite(k[i]);
+  for (int i = 0; i < kRopeDim / 2; ++i) out = out || non_finite(r[i]);
+  return !out;
+}
+
 // What the values taken out add to a row that sees the first `seen` of them: its
-// weight is positive, so a NaN stays one and an infinity keeps its sign.
+// weight is positive, so a NaN stays one and an infinity keeps its sign.  But where
+// the key is not finite either, the row scored it -inf (or is all NaN already), and a
+// weight of 0 makes a NaN of an infinity.
 static __device__ __noinline__ void add_bad(const LatentPrefillParams& p, const Item& it,
                                             const unsigned long long* bad, int seen, int d0, float (&o)[32]) {
   for (int b = 0; b < seen; ++b) {
     if (!((bad[b >> 6] >> (b & 63)) & 1)) continue;
-    const __nv_bfloat16* v =
-        p.kv + ((long long)(it.k0 + it.gpos0 + 1 + b) * p.num_heads + it.head) * (kNope + kValDim) + kNope + d0;
+    const long long row = (long long)it.k0 + it.gpos0 + 1 + b;
+    const __nv_bfloat16* v = p.kv + (row * p.num_heads + it.head) * (kNope + kValDim) + kNope + d0;
+    const bool weighs = finite_key(p, row, it.head);
     #pragma unroll
     for (int i = 0; i < 32; ++i) {
       const float x = __bfloat162float(v[i]);
-      if (!(x - x == 0.f)) o[i] += x;
+      if (!(x - x == 0.f)) o[i] += weighs ? x : NAN;
     }
   }
 }

@@ -466,8 +466,9 @@ int pkv_attention_latent(const void *q, const void *pool, const int32_t *block_t
  * 512], all bf16; products summed in fp32 and rounded once.  kv_start_loc
  * [num_reqs + 1] int32 is the running sum of seq_lens; a request for which it is
  * not, or whose rows or table do not hold it, is skipped and recorded as
- * PKV_ERR_DEVICE_BOUNDS.  Rows of no request are not written.  num_q_heads up to
- * 4096; num_q_tokens is not read.  Nothing is read or written before the kernel
+ * PKV_ERR_DEVICE_BOUNDS.  A block id outside [0, num_blocks) is recorded too; its
+ * keys' rows of kv and k_rope become zeros.  Rows of no request are not written.
+ * num_q_heads up to 4096; num_q_tokens is not read.  Nothing is read or written before the kernel
  * issued ahead of this call has ended (so in pkv_attention_expanded): that may
  * well be the one that sums the lengths.
  */

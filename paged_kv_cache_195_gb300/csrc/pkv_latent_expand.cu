@@ -351,10 +351,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int k = key0 + (i >> 3);
           if (k >= w.a.keys) break;
           const int id = __ldg(p.block_tables + (long long)w.req * p.max_blocks + k / kBlockSize);
-          if ((unsigned)id >= (unsigned)p.num_blocks) continue;
-          const uint4* src = reinterpret_cast<const uint4*>(
-              p.pool + ((long long)id * kBlockSize + k % kBlockSize) * kLatRow + kLatent);
-          reinterpret_cast<uint4*>(p.k_rope + ((long long)w.a.row0 + k) * kRopeDim)[i & 7] = src[i & 7];
+          // (zeros for a block outside the pool, as its rows of kv)
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if ((unsigned)id < (unsigned)p.num_blocks)
+            x = reinterpret_cast<const uint4*>(p.pool + ((long long)id * kBlockSize + k % kBlockSize) * kLatRow +
+                                               kLatent)[i & 7];
+          reinterpret_cast<uint4*>(p.k_rope + ((long long)w.a.row0 + k) * kRopeDim)[i & 7] = x;
         }
       }
       for (int h = w.h0; h < w.h1 && ok; ++h, ++n_d) {

@@ -1,5 +1,6 @@
-"""Start offsets on the device so far out that their differences wrap: the requests are
-skipped, and nothing is written for them."""
+"""Numbers on the device that are out of range.  Start offsets so far out that their
+differences wrap: the requests are skipped, and nothing is written for them.  Blocks
+outside the pool: keys of zeros."""
 import pytest
 import torch
 
@@ -78,3 +79,23 @@ def test_latent_cache(start, heads):
     for qsl, ksl in ((i32(*start), rows), (i32(0, 1, 2, 3), i32(*start)), (i32(*start), i32(*start))):
         pkv.pkv_attention_expanded(zeros(64, heads, 192), kv, kr, lens, qsl, ksl, 0.1, out=out)
         untouched(out)
+
+
+@pytest.mark.parametrize("block", [-1, 9, MOST, LEAST])
+def test_expansion_of_blocks_outside_the_pool(block):
+    """Rows of zeros in kv and in k_rope, whatever they held."""
+    g = torch.Generator().manual_seed(0)
+    pool, w = (torch.randn(*s, generator=g).to(BF).cuda() for s in ((9, 16, 576), (3, 256, 512)))
+    table = i32(*range(9)).reshape(1, 9).contiguous()
+    kv = torch.full((150, 3, 256), 7.0, dtype=BF, device="cuda")
+    kr = torch.full((150, 64), 7.0, dtype=BF, device="cuda")
+    pkv.pkv_expand_latent(pool, w, table, i32(141), i32(0, 141), kv, kr)
+    assert pkv.pkv_get_device_error() == 0
+    want = kv.clone(), kr.clone()
+    table[0, 1] = table[0, 8] = block
+    kv.fill_(7), kr.fill_(7)
+    pkv.pkv_expand_latent(pool, w, table, i32(141), i32(0, 141), kv, kr)
+    assert pkv.pkv_get_device_error() == pkv._binding.PKV_ERR_DEVICE_BOUNDS
+    for t, x in zip((kv, kr), want):
+        x[16:32] = x[128:141] = 0
+        assert torch.equal(t, x)

@@ -420,8 +420,8 @@ int pkv_norm_rope_append(const void *q, const void *k, const void *v, int64_t q_
  * rotated (cos_sin [max_position, 64]), and both written to the pool at
  * slot_mapping.  q_rope [num_q_tokens, num_q_heads, 64], if not NULL and
  * num_q_heads > 0 (up to 4096), is the queries' part that meets the rotated keys: it is
- * rotated into q_rope_out (which may be q_rope with its strides, and must not
- * overlap it otherwise); tokens and heads lie any multiples of 8 elements apart, the
+ * rotated into q_rope_out (which may be q_rope with its strides, must not
+ * overlap it otherwise, and must not share elements with kv); tokens and heads lie any multiples of 8 elements apart, the
  * rows of q_rope_out without overlap, heads within tokens or tokens within heads.  Padding and errors as in
  * pkv_norm_rope_append.
  */

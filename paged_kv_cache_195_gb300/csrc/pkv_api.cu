@@ -295,7 +295,7 @@ bool eps_ok(float eps) { return eps >= 0x1p-64f && eps <= 1.f; }
 // A token stride in elements: rows 16-byte aligned, a token inside one (any for a single token).
 // Whether tokens of `row` elements, `stride` apart, share elements with others: their
 // ranges may meet and they still lie side by side, in the rows of one tensor.
-bool tokens_meet(const void* a, int64_t a_stride, int64_t a_row, const void* b, int64_t b_stride, int64_t b_row,
+bool tokens_meet(const void* a, int64_t a_stride, __int128 a_row, const void* b, int64_t b_stride, __int128 b_row,
                  int tokens) {
   if (a_row == 0 || b_row == 0) return false;
   const __int128 x = (__int128)reinterpret_cast<uintptr_t>(a), y = (__int128)reinterpret_cast<uintptr_t>(b);
@@ -333,6 +333,13 @@ struct Rows {
   bool meets(const Rows& o, int tokens, int heads) const {
     const __int128 a = (__int128)reinterpret_cast<uintptr_t>(base), b = (__int128)reinterpret_cast<uintptr_t>(o.base);
     return a < b + 2 * o.last(tokens, heads) && b < a + 2 * last(tokens, heads);
+  }
+  // Whether they share elements with rows of `row` elements, one a token: with heads
+  // within tokens the two may lie side by side, else only ranges that do not meet do.
+  bool meets_tokens(const void* o, int64_t stride, int row, int tokens, int heads) const {
+    const __int128 span = last(1, heads);
+    if (tokens == 1 || token >= span) return tokens_meet(base, token, span, o, stride, row, tokens);
+    return tokens_meet(base, 0, last(tokens, heads), o, 0, (__int128)(tokens - 1) * stride + row, 1);
   }
 };
 
@@ -1219,6 +1226,8 @@ int pkv_append_latent(const void* kv, int64_t kv_stride, const int64_t* position
     // (one thread's rows may be another's: only ranges apart, or the same rows)
     if (!in.same(to, T, H) && in.meets(to, T, H))
       return fail(PKV_ERR_INVALID, "q_rope_out may be q_rope, but not overlap it otherwise");
+    if (to.meets_tokens(kv, kv_stride, pkv::kLatRow, T, H))
+      return fail(PKV_ERR_INVALID, "q_rope_out and kv overlap");
   }
   DeviceState* st = device_state();
   if (!st) return PKV_ERR_CUDA;

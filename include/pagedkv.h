@@ -446,7 +446,7 @@ size_t pkv_latent_workspace_size(const pkv_dims *dims);
  * Absorbed attention over a latent cache: for row (token, head) with query q
  * [num_q_tokens, num_q_heads, 576] and the rows x_j = (c_j, r_j) of its request,
  *   s_j = scale <q, x_j>, out [num_q_tokens, num_q_heads, 512] = sum_j softmax(s)_j c_j
- * over the keys j that the token sees.  num_q_heads 1..128; scale finite and > 0
+ * over the keys j that the token sees.  num_q_heads 1..128; scale in (0, 2^127]
  * (so in pkv_attention_expanded).  Lengths, tables, causal order, padded steps, errors and launch overlap as in pkv_attention.
  * Softmax and sums in fp32, weights bf16 in the product (their sum adds the
  * rounded values).  A NaN or infinity in a cached row reaches the tokens that

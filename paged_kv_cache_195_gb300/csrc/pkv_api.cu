@@ -361,6 +361,9 @@ int check_latent_dims(const pkv_dims* d, bool attention) {
   return PKV_OK;
 }
 
+// (times log2(e) it must still be a number)
+bool latent_scale_ok(float scale) { return scale > 0.f && scale <= 0x1p127f; }
+
 // How a step's (token, head) rows are grouped into work items of at most 64.
 // With no more rows than requests nearly every request has one; then an item is
 // one token's heads.
@@ -1279,8 +1282,7 @@ int pkv_attention_latent(const void* q, const void* pool, const int32_t* block_t
     return fail(PKV_ERR_INVALID, "NULL pointer argument");
   if (!aligned16(q) || !aligned16(pool) || !aligned16(out))
     return fail(PKV_ERR_INVALID, "q, out and the pool must be 16-byte aligned");
-  if (!(scale > 0.f) || !(scale - scale == 0.f))
-    return fail(PKV_ERR_INVALID, "scale must be finite and positive");
+  if (!latent_scale_ok(scale)) return fail(PKV_ERR_INVALID, "scale must be in (0, 2^127]");
   DeviceState* st = device_state();
   if (!st) return PKV_ERR_CUDA;
   const LatentLayout w = latent_layout(st->sm_count);
@@ -1398,8 +1400,7 @@ int pkv_attention_expanded(const void* q, const void* kv, const void* k_rope, co
     return fail(PKV_ERR_INVALID, "NULL pointer argument");
   if (!aligned16(q) || !aligned16(kv) || !aligned16(k_rope) || !aligned16(out))
     return fail(PKV_ERR_INVALID, "q, kv, k_rope and out must be 16-byte aligned");
-  if (!(scale > 0.f) || !(scale - scale == 0.f))
-    return fail(PKV_ERR_INVALID, "scale must be finite and positive");
+  if (!latent_scale_ok(scale)) return fail(PKV_ERR_INVALID, "scale must be in (0, 2^127]");
   DeviceState* st = device_state();
   if (!st) return PKV_ERR_CUDA;
   const LatentLayout w = latent_layout(st->sm_count);

@@ -412,7 +412,11 @@ int pkv_norm_rope_append(const void *q, const void *k, const void *v, int64_t q_
  * the outputs through W_h[128:256] by the caller, which reads 1152 bytes a key
  * for all heads and suits decodes; and expanded (pkv_expand_latent, then
  * pkv_attention_expanded), which needs less than a third of the products a (row, key) and
- * suits chunks.  In these calls dims->head_dim is 576 and num_kv_heads 1.
+ * suits chunks.  A mixed step orders its decodes first and splits: with D decodes,
+ * the absorbed call takes num_reqs = D and the step's arrays as they are; expansion and
+ * expanded call take the tables and lengths from request D on, the query_start_loc of
+ * these requests less that of request D, q from that row on, and the running sum of
+ * their lengths.  In these calls dims->head_dim is 576 and num_kv_heads 1.
  *
  * pkv_append_latent: of each row of kv [num_q_tokens][512 latent | 64 key] bf16,
  * rows kv_stride elements apart (a multiple of 8), the latent is normed as in

@@ -823,7 +823,9 @@ def pkv_append_latent(kv, positions, cos_sin, slot_mapping, pool, weight=None, e
 class LatentWorkspace:
     """A device workspace for pkv_attention_latent and pkv_attention_expanded,
     ready for use on the current stream.  One serves calls of any size on its
-    device, one after the other."""
+    device, one after the other: its size depends on none of the counts, which
+    are only checked.  After a call that ended with PKV_ERR_TIMEOUT make a new
+    one."""
 
     def __init__(self, num_q_tokens=1, num_q_heads=1, num_reqs=1, device="cuda"):
         dims = Dims(num_reqs, num_q_tokens, num_q_heads, 1, LATENT + ROPE, 16, 1, 1)
@@ -862,7 +864,8 @@ def pkv_attention_latent(q, pool, block_tables, seq_lens, query_start_loc, scale
     """Attention over a paged latent cache, absorbed form: q [Tq, Hq, 576] bf16
     (up to 128 heads: the part that meets the latents, then the rotated part)
     against the rows of pool [blocks, 16, 576]; the values are the rows' first
-    512 dims.  Returns out [Tq, Hq, 512] bf16."""
+    512 dims.  As in pkv_attention, the kernel issued immediately before must not
+    write seq_lens or query_start_loc.  Returns out [Tq, Hq, 512] bf16."""
     if out is None and isinstance(q, torch.Tensor) and q.dim() == 3:
         out = torch.empty((*q.shape[:2], LATENT), dtype=_BF16, device=q.device)
     dev, ptrs = _fast_need((q, pool, block_tables, seq_lens, query_start_loc, out), _ATTENTION_LATENT)

@@ -292,7 +292,6 @@ constexpr int kMaxRopeHeads = 4096;
 
 bool eps_ok(float eps) { return eps >= 0x1p-64f && eps <= 1.f; }
 
-// A token stride in elements: rows 16-byte aligned, a token inside one (any for a single token).
 // Whether tokens of `row` elements, `stride` apart, share elements with others: their
 // ranges may meet and they still lie side by side, in the rows of one tensor.
 bool tokens_meet(const void* a, int64_t a_stride, __int128 a_row, const void* b, int64_t b_stride, __int128 b_row,
@@ -309,6 +308,7 @@ bool tokens_meet(const void* a, int64_t a_stride, __int128 a_row, const void* b,
   return gap < 2 * a_row || gap + 2 * b_row > pitch;
 }
 
+// A token stride in elements: rows 16-byte aligned, a token inside one (any for a single token).
 bool stride_ok(int64_t stride, int row, int tokens) {
   return stride >= 0 && stride % 8 == 0 && (stride >= row || tokens <= 1);
 }
@@ -364,9 +364,13 @@ int check_latent_dims(const pkv_dims* d, bool attention) {
 // (times log2(e) it must still be a number)
 bool latent_scale_ok(float scale) { return scale > 0.f && scale <= 0x1p127f; }
 
-// How a step's (token, head) rows are grouped into work items of at most 64.
-// With no more rows than requests nearly every request has one; then an item is
-// one token's heads.
+// How a step's (token, head) rows are grouped into work items of at most 64.  With no
+// more rows than request slots an item is one token's heads: as a rule every request
+// has one row then, and items of more would have columns that nobody uses.  Beyond
+// that, an item has no more tokens than a request can have if each has one.  (Slots that
+// sit the step out are not known here, and count as if they had a row: four drafts of 4
+// on 2000 keys, 16 heads 20 us in 64 slots for 19 in 4; a chunk of 60 on 2000 keys,
+// which reads its keys token by token then, 66 for 28.)
 struct LatentGroups {
   int head_groups, group_heads, group_tokens;
 };
@@ -375,7 +379,7 @@ LatentGroups latent_groups(const pkv_dims* d) {
   LatentGroups l;
   l.head_groups = d->num_q_heads > pkv::kLatMaxRows ? 2 : 1;
   l.group_heads = (d->num_q_heads + l.head_groups - 1) / l.head_groups;
-  const int most = d->num_q_tokens - d->num_reqs + 1;  // tokens that a request can have beside one each
+  const int most = d->num_q_tokens - d->num_reqs + 1;
   l.group_tokens = pkv::kLatMaxRows / l.group_heads;
   if (l.group_tokens > most) l.group_tokens = most < 1 ? 1 : most;
   return l;
@@ -1319,7 +1323,9 @@ int pkv_attention_latent(const void* q, const void* pool, const int32_t* block_t
   p.item_cost = 192;
   p.min_keys = 128;
   // Without cuts, a step whose items have a CTA each and few keys needs no second
-  // kernel.
+  // kernel (four rows, 16 heads: of 480 keys 14.2 us whole, 14.7 cut and joined; of 640
+  // 15.9 and 14.6, of 2000 40 and 15; 100 rows of 500 20 and 28).  The table's width
+  // stands for the longest row.
   const long long units = st->sm_count / g.head_groups;
   p.merge = dims->num_q_tokens > units || (long long)dims->max_blocks_per_req * pkv::kBlockSize > 512;
   p.scale_log2 = scale * 1.4426950408889634f;
@@ -1430,16 +1436,21 @@ int pkv_attention_expanded(const void* q, const void* kv, const void* k_rope, co
   p.num_q_tokens = dims->num_q_tokens;
   p.num_rows = num_rows;
   p.num_heads = heads;
-  // Items are split, and the joining kernel follows, only where the step's rows,
-  // were they all in use, are fewer items than CTAs, and an item can see more keys
-  // than are worth two pieces.
+  // Items are split, and the joining kernel follows, only where the step's rows, were
+  // they one request's, are fewer items than CTAs, and the step has keys for an item
+  // that is worth it (a chunk of 64, 4 heads: on 700 keys 14.8 us whole, 17.3 split and
+  // joined; on 1000 16.5 and 17.3, on 1500 20.5 and 17.4, on 2500 28.8 and 17.4).  The
+  // longest request is not known here: many short ones pay 5 us for a join that has
+  // nothing to do (30 chunks of 20 on 100 keys 15.2 for 9.5).
   const long long items = ((long long)dims->num_q_tokens + 127) / 128 * heads;
   p.max_pieces = items < st->sm_count && num_rows > 1024 ? 2 * st->sm_count : 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.pdl = opt.pdl != 0;
   p.debug_withhold_q = opt.debug_withhold_q != 0;
   p.wait_limit_ns = (unsigned long long)opt.wait_limit_us * 1000ull;
-  // In pairs where chunks are long enough for two query tiles on average, and enough.
+  // In pairs where chunks are long enough for two query tiles on average, and enough (8
+  // of 512 on 512-4608 keys, 32 heads 129 us for 138 alone).  Slots that sit the step out
+  // count as chunks: four of 1024 on 2000 keys among 60 such run alone, 114 us for 109.
   L.pairs = dims->num_q_tokens >= 192ll * dims->num_reqs &&
             (long long)dims->num_q_tokens * heads >= 256ll * st->sm_count;
   const cuuint32_t keys = L.pairs ? 64 : 128;

@@ -194,8 +194,8 @@ struct LatentPrefillParams {
 
 struct LatentPrefillLaunch {
   CUtensorMap qmap;   // q as [tokens][H][192], box (64, 1, 128), 128-byte swizzle
-  CUtensorMap kvmap;  // keys and values: kv as [rows][H][256], same box
-  CUtensorMap kmap;   // a pair's keys: the same, box (64, 1, 64)
+  CUtensorMap kvmap;  // values: kv as [rows][H][256], same box
+  CUtensorMap kmap;   // keys: the same; a pair's box (64, 1, 64)
   CUtensorMap rmap;   // k_rope as [1][rows][64], box (64, 128, 1); a pair's (64, 64, 1)
   LatentPrefillParams p;
   int pairs;          // two query tiles of a head by two CTAs

@@ -12,7 +12,7 @@
 // 2176 flops a head.  Up to 64 heads that is bound by HBM; 128 heads bring the
 // tensor core near its own bound.  Measured: 8 rows of 32768 keys, 16 heads, 65 us
 // (4.7 TB/s); 64 rows of 4096 keys, 128 heads, 100 us (730 TFLOP/s, 3.2 TB/s); four
-// rows of up to 128 keys, 16 heads, 7.9 us.
+// rows of up to 128 keys, 16 heads, 7.7 us.
 //
 // Tiling.  A work item is a request's `group_tokens` query tokens times
 // `group_heads` heads: its (token, head) pairs are the N <= 64 columns of the

@@ -5,7 +5,7 @@
 //
 // a matrix product whose left operand is gathered through the block table.
 // Bound: tensor core (512 flops a byte written, the largest stream).  Measured: 8
-// contexts of 512 to 4608 keys, 32 heads 81 us (1536 TFLOP/s); 701 keys, 16 heads 7.9.
+// contexts of 512 to 4608 keys, 32 heads 83 us (1500 TFLOP/s); 701 keys, 16 heads 8.7.
 //
 // Tiling.  Two CTAs work as one (cta_group::2): a unit is (256 keys of one request,
 // head), D[256 x 256] = C[256 x 512] W_h^T, each CTA holding 128 of the keys, 128

@@ -7,8 +7,8 @@
 // rotated keys r, shared by the heads, in a tensor of their own: a key tile takes
 // its three 64-dim chunks from both, and no head's copy of r is ever made.
 // Bound: tensor core (640 flops a (row, key, head)).  Measured: 8 chunks of 512 on up
-// to 4608 keys, 32 heads 110 us (1225 TFLOP/s; a tile's softmax, 0.85 us a pair's 256
-// rows, is longer than its products' 0.67); three odd chunks, 16 heads 10.4 us.
+// to 4608 keys, 32 heads 112 us (1199 TFLOP/s; a tile's softmax, 0.85 us a pair's 256
+// rows, is longer than its products' 0.67); three odd chunks, 16 heads 12.9 us.
 //
 // Tiling.  A work item is (request, head, 128 query tokens); a key tile is 128
 // keys.  S = Q K^T (12 MMAs of K = 16) and P (bf16) have two TMEM buffers each, so
